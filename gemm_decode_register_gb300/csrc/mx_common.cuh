@@ -37,7 +37,7 @@ static inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 blo
 namespace mx {
 
 enum : int { FMT_MXFP4 = 0, FMT_MXFP8 = 1, FMT_NVFP4 = 2 };
-enum : int { DEVERR_BAD_EXPERT = 0x1, DEVERR_TIMEOUT = 0x2 };
+enum : int { DEVERR_BAD_EXPERT = 0x1, DEVERR_TIMEOUT = 0x2, DEVERR_BAD_PAGE = 0x4, DEVERR_BAD_POSITION = 0x8 };
 
 // ------------------------------------------------------------- conversions
 
@@ -145,6 +145,27 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi)
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out) : "f"(hi), "f"(lo));
     return out;
 }
+
+// Four fp32 values to four E4M3 codes, v[0] in the lowest byte.
+__device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float v0, float v1, float v2, float v3)
+{
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v1), "f"(v0));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v3), "f"(v2));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// -0 codes (the sign bit alone) of four E4M3 bytes become +0.
+__device__ __forceinline__ uint32_t e4m3x4_plus_zero(uint32_t w)
+{
+    const uint32_t t = w & 0x7F7F7F7Fu;
+    const uint32_t nonzero = (t + 0x7F7F7F7Fu) & 0x80808080u;  // bit 7 of byte i: magnitude i non-zero
+    return w & (nonzero | 0x7F7F7F7Fu);
+}
+
+// The two elements of a bf16 pair as fp32, exact.
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // Exact 2^e as fp32 for e in [-149, 127]; 0 below, +inf above.
 __device__ __forceinline__ float pow2f(int e)

@@ -43,32 +43,13 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&v)[8])
     return d;
 }
 
-// Four fp32 values to four E4M3 codes, v[0] in the lowest byte.
-__device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float v0, float v1, float v2, float v3)
-{
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v1), "f"(v0));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v3), "f"(v2));
-    return (uint32_t)lo | ((uint32_t)hi << 16);
-}
-
-// -0 codes (the sign bit alone) become +0: eight E2M1 nibbles, four E4M3 bytes.
+// -0 codes (the sign bit alone) of eight E2M1 nibbles become +0.
 __device__ __forceinline__ uint32_t e2m1x8_plus_zero(uint32_t w)
 {
     const uint32_t t = w & 0x77777777u;
     const uint32_t zero = ~(t | (t >> 1) | (t >> 2)) & 0x11111111u;  // bit 4i: nibble i has magnitude 0
     return w & ~(zero << 3);
 }
-
-__device__ __forceinline__ uint32_t e4m3x4_plus_zero(uint32_t w)
-{
-    const uint32_t t = w & 0x7F7F7F7Fu;
-    const uint32_t nonzero = (t + 0x7F7F7F7Fu) & 0x80808080u;  // bit 7 of byte i: magnitude i non-zero
-    return w & (nonzero | 0x7F7F7F7Fu);
-}
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // Largest |bits| of the bf16 pairs in w[0..n) (bf16 magnitudes compare as
 // integers) and whether any of them is an infinity or a NaN.  One packed

@@ -8,6 +8,7 @@ is no fallback path: if the library is missing, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 import threading
@@ -44,7 +45,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                "(run __graft_entry__.build() or python -m "
                                "gemm_decode_register_gb300.build)")
         lib = ctypes.CDLL(p)
-        P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        P, I, Z, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
         sig = {
             "mx_qmv": [I, P, P, P, P, I, I, I],
             "mx_qmv_noalloc": [I, P, P, P, P, I, I, I],
@@ -63,13 +64,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
             "mx_moe_qmm": [I, P, P, P, P, P, I, I, I, I, I, P, Z],
             "mx_quantize": [I, P, P, P, I, I],
             "mx_moe_ffn_prefill": [I, P, P, P, P, P, P, P, P, I, I, I, I, I, P, Z],
+            "mx_rope_table": [P, ctypes.c_double, P, L, I, I],
+            "mx_rope": [P, P, I, P, P, I, I, I, I, I, L, L, L, L, I],
+            "mx_kv_append": [P, P, I, L, P, P, P, I, I, P, I, I, I, I],
+            "mx_paged_attn": [P, P, L, L, P, P, ctypes.c_float, I, I, P, P, P, I, I, I, P, Z],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = I
         for name, args in {"mx_moe_qmm_workspace_size": [I, I, I, I],
-                           "mx_moe_ffn_prefill_workspace_size": [I, I, I, I, I]}.items():
+                           "mx_moe_ffn_prefill_workspace_size": [I, I, I, I, I],
+                           "mx_paged_attn_workspace_size": [I, I, I, I, I]}.items():
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = Z
@@ -302,6 +308,238 @@ def moe_combine(yd: torch.Tensor, r: torch.Tensor, out: torch.Tensor | None = No
     _stream()
     _check("mx_moe_combine", load().mx_moe_combine(_ptr(yd), _ptr(r), _ptr(out), T, topk, N))
     return out
+
+
+# ---- rotary positions, paged key/value cache, attention
+
+KV_BF16, KV_MXFP8 = 0, 1
+ROPE_INTERLEAVED, ROPE_INVERSE = 0x1, 0x2
+ATTN_CAUSAL = 0x1
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _cuda(name: str, t: torch.Tensor, dtype, dim: int | None = None) -> int:
+    """Device pointer of a tensor of the type(s), its last dimension contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if dim is not None and t.dim() != dim:
+        raise ValueError(f"{name}: expected {dim} dimensions, got {t.dim()}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _whole(name: str, t: torch.Tensor, dtype, *shape: int) -> int:
+    """Device pointer of a contiguous tensor of the type and shape."""
+    p = _cuda(name, t, dtype)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {shape}, got {tuple(t.shape)}")
+    return p
+
+
+class _PagedKV(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "v_scales", "block_table")]
+    _fields_ += [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride", "scale_page_stride",
+                                               "scale_head_stride", "scale_token_stride")]
+    _fields_ += [(n, ctypes.c_int32) for n in ("kv_fmt", "num_pages", "page_size", "Hkv", "D", "table_stride")]
+
+
+class PagedKV:
+    """A paged key/value cache and a batch's block table, as mx_kv_append and
+    mx_paged_attn take them (mx_paged_kv).
+
+    k, v         [num_pages][Hkv][page_size][D], any strides with the last
+                 dimension contiguous (a transposed view of tokens-major pages
+                 works), the same for both: bf16, or uint8 E4M3 codes with
+    k_scales, v_scales  uint8 E8M0 [num_pages][Hkv][page_size][D/32]
+    block_table  int32 [B][pages], the last dimension contiguous
+
+    The object keeps the tensors alive and may be kept and reused while the
+    table's contents change."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
+                 k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None):
+        if (k_scales is None) != (v_scales is None):
+            raise ValueError("k_scales and v_scales come together")
+        mx8 = k_scales is not None
+        dtype = torch.uint8 if mx8 else torch.bfloat16
+        c = _PagedKV()
+        c.k, c.v = _cuda("k", k, dtype, 4), _cuda("v", v, dtype, 4)
+        if k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v: expected the same shape and strides")
+        c.num_pages, c.Hkv, c.page_size, c.D = k.shape
+        c.page_stride, c.head_stride, c.token_stride, _ = k.stride()
+        if mx8:
+            c.k_scales, c.v_scales = (_cuda("scales", t, torch.uint8, 4) for t in (k_scales, v_scales))
+            want = (*k.shape[:3], k.shape[3] // 32)
+            if k_scales.shape != want or v_scales.shape != want or k_scales.stride() != v_scales.stride():
+                raise ValueError(f"scales: expected shape {want} and the same strides")
+            c.scale_page_stride, c.scale_head_stride, c.scale_token_stride, _ = k_scales.stride()
+        c.kv_fmt = KV_MXFP8 if mx8 else KV_BF16
+        c.block_table = _cuda("block_table", block_table, torch.int32, 2)
+        # one row may have any stride; several are as far apart as the table says
+        self.B = block_table.shape[0]
+        c.table_stride = block_table.shape[1] if self.B == 1 else block_table.stride(0)
+        if self.B > 1 and block_table.stride(0) != block_table.shape[1]:
+            raise ValueError("block_table: expected contiguous rows")
+        self.k, self.v, self.k_scales, self.v_scales, self.block_table = k, v, k_scales, v_scales, block_table
+        self.Hkv, self.D = c.Hkv, c.D
+        self._c = c
+        self._ref = ctypes.byref(c)
+
+    @classmethod
+    def empty(cls, num_pages: int, Hkv: int, page_size: int, D: int, block_table: torch.Tensor,
+              kv_fmt: int = KV_BF16) -> "PagedKV":
+        """A new cache of heads-major pages (contents undefined)."""
+        mx8 = kv_fmt == KV_MXFP8
+        kv = [torch.empty((num_pages, Hkv, page_size, D), dtype=torch.uint8 if mx8 else torch.bfloat16,
+                          device=block_table.device) for _ in "kv"]
+        sc = [torch.empty((num_pages, Hkv, page_size, D // 32), dtype=torch.uint8, device=block_table.device)
+              for _ in "kv"] if mx8 else [None, None]
+        return cls(*kv, block_table, *sc)
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_len: int = 8192, low: float = 1.0, high: float = 4.0) -> tuple[torch.Tensor, float]:
+    """Radians per position of the rot/2 pairs (fp64) and the factor on the
+    cosines and sines, base^(-2i/rot) and 1 unless a scaling for contexts
+    longer than the trained `original_len` changes them:
+
+    "linear"  every frequency over `factor`;
+    "base"    the base times factor^(rot/(rot-2)): the slowest pair turns
+              `factor` times slower, the fastest as before;
+    "banded"  by the turns a pair makes over original_len: above `high`
+              unchanged, below `low` over `factor`, blended between;
+    "yarn"    the blend runs over the pair's number, between those that turn
+              `high` and `low` times (32 and 1 as published), and cosines and
+              sines grow by 0.1 ln(factor) + 1.
+    """
+    if rot <= 0 or rot % 2 or base <= 1.0 or factor < 1.0:
+        raise ValueError("rope_frequencies: rot even and positive, base > 1, factor >= 1")
+    i = torch.arange(0, rot, 2, dtype=torch.float64)
+    f = base ** (-i / rot)
+    if scaling == "none":
+        return f, 1.0
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling == "base":
+        return (base * factor ** (rot / (rot - 2.0))) ** (-i / rot) if rot > 2 else f, 1.0
+    if scaling == "banded":
+        turns = original_len * f / (2.0 * math.pi)
+        keep = ((turns - low) / (high - low)).clamp(0.0, 1.0)
+        return f * keep + f / factor * (1.0 - keep), 1.0
+    if scaling == "yarn":
+        def dim(turns: float) -> float:
+            return rot * math.log(original_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        first, last = max(math.floor(dim(high)), 0), min(math.ceil(dim(low)), rot - 1)
+        slow = ((i / 2 - first) / max(last - first, 1e-3)).clamp(0.0, 1.0)
+        return f * (1.0 - slow) + f / factor * slow, 0.1 * math.log(factor) + 1.0
+    raise ValueError(f"rope_frequencies: unknown scaling {scaling!r}")
+
+
+def rope_table(inv_freq: torch.Tensor, n: int, factor: float = 1.0, pos0: int = 0, device="cuda") -> torch.Tensor:
+    """fp32 [n][half][2] cosines and sines (times factor) of positions pos0 .. pos0 + n - 1."""
+    f = inv_freq.to(device=device, dtype=torch.float64).contiguous()
+    table = torch.empty((n, f.numel(), 2), dtype=torch.float32, device=f.device)
+    _stream()
+    _check("mx_rope_table", load().mx_rope_table(_ptr(f), factor, _ptr(table), pos0, n, f.numel()))
+    return table
+
+
+def _table_arg(table: torch.Tensor | None) -> tuple[int | None, int, int]:
+    """Pointer, positions and rotating dimensions of a rotation table."""
+    if table is None:
+        return None, 0, 0
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError("table: expected [positions][rot / 2][2]")
+    return _whole("table", table, torch.float32, *table.shape), table.shape[0], 2 * table.shape[1]
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False,
+         inverse: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotate the first 2 * table.shape[1] dimensions of each head of x [T][H][D]
+    (bf16 or fp32, the last dimension contiguous) by the angles of its token's position
+    (positions int32 [T]); inverse: rotate back (the gradient).  out may be x."""
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"x: expected bf16 or fp32, got {x.dtype}")
+    xp = _cuda("x", x, x.dtype, 3)
+    T, H, D = x.shape
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape:
+        raise ValueError("out: expected the shape of x")
+    op = _cuda("out", out, x.dtype, 3)
+    tp, n, rot = _table_arg(table)
+    pp = _whole("positions", positions, torch.int32, T)
+    if T == 0:
+        return out
+    _stream()
+    _check("mx_rope", load().mx_rope(xp, op, _DTYPES[x.dtype], pp, tp, n, T, H, D, rot, x.stride(0), x.stride(1),
+                                     out.stride(0), out.stride(1),
+                                     (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)))
+    return out
+
+
+def kv_append(kv: PagedKV, rows: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, Hq: int,
+              table: torch.Tensor | None, interleaved: bool = False, q: torch.Tensor | None = None) -> torch.Tensor:
+    """Split the fused QKV rows [T][(Hq + 2 Hkv) D] (bf16 or fp32): rotate queries
+    and keys at their places in the contexts, write keys and values to the
+    cache and return the queries, bf16 [T][Hq][D].  q_start int32 [B+1], kv_len int32 [B] (new
+    tokens included); table None: no rotation."""
+    if rows.dtype not in _DTYPES:
+        raise ValueError(f"rows: expected bf16 or fp32, got {rows.dtype}")
+    rp = _cuda("rows", rows, rows.dtype, 2)
+    T, D = rows.shape[0], kv.D
+    if rows.shape[1] != (Hq + 2 * kv.Hkv) * D:
+        raise ValueError(f"rows: expected (Hq + 2 Hkv) D = {(Hq + 2 * kv.Hkv) * D} elements per token")
+    if q is None:
+        q = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=rows.device)
+    qp = _whole("q", q, torch.bfloat16, T, Hq, D)
+    tp, n, rot = _table_arg(table)
+    sp, lp = _whole("q_start", q_start, torch.int32, kv.B + 1), _whole("kv_len", kv_len, torch.int32, kv.B)
+    if T == 0:
+        return q
+    _stream()
+    _check("mx_kv_append", load().mx_kv_append(kv._ref, rp, _DTYPES[rows.dtype], rows.stride(0), sp, lp, tp, n, rot,
+                                               qp, T, kv.B, Hq, ROPE_INTERLEAVED if interleaved else 0))
+    return q
+
+
+def paged_attn_workspace(T: int, B: int, Hq: int, Hkv: int, D: int, device="cuda") -> torch.Tensor:
+    return _workspace(load().mx_paged_attn_workspace_size(T, B, Hq, Hkv, D), None, device)
+
+
+def paged_attn(kv: PagedKV, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+               scale: float | None = None, causal: bool = True, window: int = 0, sinks: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, return_lse: bool = False, lse: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None):
+    """Attention of the new tokens' queries q [T][Hq][D] (bf16, the last dimension
+    contiguous) over their contexts in the cache; out bf16 [T][Hq][D], and with
+    return_lse (out, lse) with lse fp32 [T][Hq].  scale: 1/sqrt(D) by default; window > 0: each token sees
+    itself and the window - 1 tokens before it; sinks fp32 [Hq]."""
+    qp = _cuda("q", q, torch.bfloat16, 3)
+    T, Hq, D = q.shape
+    if D != kv.D:
+        raise ValueError(f"q: heads of {D}, the cache's have {kv.D}")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    op = _whole("out", out, torch.bfloat16, T, Hq, D)
+    ep = None if lse is None else _whole("lse", lse, torch.float32, T, Hq)
+    kp = None if sinks is None else _whole("sinks", sinks, torch.float32, Hq)
+    sp, lp = _whole("q_start", q_start, torch.int32, kv.B + 1), _whole("kv_len", kv_len, torch.int32, kv.B)
+    if T > 0:
+        lib = load()
+        ws = _workspace(lib.mx_paged_attn_workspace_size(T, kv.B, Hq, kv.Hkv, D), workspace, q.device)
+        _stream()
+        _check("mx_paged_attn", lib.mx_paged_attn(
+            kv._ref, qp, q.stride(0), q.stride(1), sp, lp, 1.0 / math.sqrt(D) if scale is None else scale,
+            ATTN_CAUSAL if causal else 0, window, kp, op, ep, T, kv.B, Hq, _ptr(ws), ws.numel()))
+    return (out, lse) if return_lse else out
 
 
 def debug_qmm_stall(stall: bool, wait_ns: int = 0) -> None:

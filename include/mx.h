@@ -79,6 +79,8 @@ enum mx_status {
 /* Device error word bits, as returned by mx_device_error(). */
 #define MX_DEVERR_BAD_EXPERT 0x1 /* an expert id outside [0, E); that slot's y rows are NaN */
 #define MX_DEVERR_TIMEOUT 0x2    /* a bounded pipeline wait gave up; that tile of Y is NaN */
+#define MX_DEVERR_BAD_PAGE 0x4   /* a context reaches past its block-table row, or a page id outside [0, num_pages) */
+#define MX_DEVERR_BAD_POSITION 0x8 /* a position outside the rotation table, or more new tokens than context */
 
 /* Decode GEMV for a few tokens (the memory-bound decode step; "MLxcel 0.8
  * release", section "Profiling set the porting order": the qmv kernel is 95%
@@ -260,6 +262,114 @@ int mx_moe_ffn_prefill(int fmt, const void *gate_up_codes, const void *gate_up_s
  *   zero codes; a zero result is stored as +0.
  * K a multiple of the block (else MX_EINVAL); x and codes 16-byte aligned. */
 int mx_quantize(int fmt, const void *x, void *codes, void *scales, int M, int K);
+
+/* ---- attention: rotary positions, paged key/value cache, attention over it
+ *
+ * What stands between a layer's fused QKV projection (mx_qmv / mx_qmm) and
+ * its output projection when a model decodes or reads a prompt.
+ *
+ * A batch holds B sequences.  Sequence b's new tokens are rows q_start[b] ..
+ * q_start[b+1]-1 of the token-major tensors (q_start int32 [B+1], from 0,
+ * not decreasing, at most T; rows of no sequence are left alone), and
+ * kv_len[b] (int32) is the length of its context with those tokens
+ * included: new token i of n sits at position kv_len[b] - n + i.  A context
+ * lives in pages of page_size tokens; block_table[b*table_stride + j] is the
+ * page that holds positions j*page_size .. (entries past the context are
+ * not read).  q_start, kv_len and the block table are read as soon as a
+ * kernel starts, like the expert ids of mx_moe_qmv: they must be complete
+ * when the call is issued, i.e. not written by a kernel that lets its
+ * dependents start early (no kernel of this library writes them). */
+
+enum mx_dtype { MX_BF16 = 0, MX_F32 = 1 };
+
+/* Cache formats: bf16, or MXFP8 as above (E4M3 codes, one E8M0 scale per 32
+ * elements along the head, so each cached token can be written by itself). */
+enum mx_kv_fmt { MX_KV_BF16 = 0, MX_KV_MXFP8 = 1 };
+
+/* A paged cache and a batch's block table.  Element (page, head, token, d)
+ * of k and of v is at page*page_stride + head*head_stride +
+ * token*token_stride + d, in elements (bf16) or bytes (codes); the strides
+ * hold for both halves, so heads-major pages, tokens-major pages and views of
+ * one tensor that holds both halves all work.  MXFP8: the scale of elements
+ * 32 i .. 32 i + 31 is at page*scale_page_stride + head*scale_head_stride +
+ * token*scale_token_stride + i of k_scales / v_scales.  All strides positive;
+ * k, v and their strides multiples of 16 bytes.  D: a multiple of 8 (bf16) or 32
+ * (MXFP8), at most 256; page_size >= 1. */
+typedef struct mx_paged_kv {
+    void *k, *v;
+    void *k_scales, *v_scales; /* MXFP8 only */
+    const int32_t *block_table;
+    int64_t page_stride, head_stride, token_stride;
+    int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+    int32_t kv_fmt, num_pages, page_size, Hkv, D, table_stride;
+} mx_paged_kv;
+
+/* Rotation table: table[p - pos0][i] = (cos a, sin a) * factor with
+ * a = p * inv_freq[i], p = pos0 .. pos0 + n - 1, i < half, evaluated in fp64 and
+ * rounded once to fp32.  inv_freq fp64 [half] (device), table fp32
+ * [n][half][2].  The scalings for long contexts are a choice of inv_freq and
+ * factor. */
+int mx_rope_table(const double *inv_freq, double factor, float *table, int64_t pos0, int n, int half);
+
+#define MX_ROPE_INTERLEAVED 0x1 /* pairs (2i, 2i + 1) instead of (i, i + rot/2) */
+#define MX_ROPE_INVERSE 0x2     /* rotate back: the gradient of the rotation */
+
+/* Rotary positions: in each head of x[T][H][D] the pairs of the first `rot`
+ * dimensions turn by the angles of the token's position, the others are copied:
+ *   (a, b) -> (a c - b s, b c + a s),  (c, s) = table[positions[t]][i],
+ * each product and sum rounded to fp32, then to dtype (mx_dtype) once.
+ * positions int32 [T]; table fp32 [table_len][rot/2][2] (mx_rope_table from
+ * position 0); strides in elements, the last dimension contiguous; y may be x
+ * with the same strides.  MX_ROPE_INVERSE (s -> -s) maps the gradient of y to
+ * the gradient of x.  Any H, D >= 1, rot even, 0 <= rot <= D.  x, y and the
+ * strides need only be multiples of the element size (multiples of 16 bytes
+ * take the vector path); positions 4-byte, table 16-byte aligned.  A position outside [0, table_len)
+ * sets MX_DEVERR_BAD_POSITION and makes that token's outputs NaN. */
+int mx_rope(const void *x, void *y, int dtype, const int32_t *positions, const float *table, int table_len, int T,
+            int H, int D, int rot, int64_t x_token_stride, int64_t x_head_stride, int64_t y_token_stride,
+            int64_t y_head_stride, int flags);
+
+/* Append to the cache: rows[t] holds Hq query heads, then Hkv key heads, then
+ * Hkv value heads, each of D elements (the fused QKV projection's output:
+ * fp32 from mx_qmv, bf16 from mx_qmm; row_stride elements apart).  Queries and keys are rotated
+ * as by mx_rope at the token's position in its context; q (bf16
+ * [T][Hq][D], contiguous) receives the queries, the cache the keys and the
+ * values, rounded to bf16 once or quantised from fp32 as mx_quantize does.
+ * The queries' rounding and the cache's are the only ones.  flags: MX_ROPE_INTERLEAVED;
+ * rot = 0: no rotation (table may be null).  Hq = 0: no queries (q may be
+ * null).  rows and row_stride multiples of 16 bytes, q and table 16-byte aligned.  A token whose position is
+ * negative or beyond the table sets MX_DEVERR_BAD_POSITION, one whose page is
+ * missing MX_DEVERR_BAD_PAGE; its queries become NaN and nothing of it is
+ * cached.  Two tokens must not share a place in the cache. */
+int mx_kv_append(const mx_paged_kv *kv, const void *rows, int dtype, int64_t row_stride, const int32_t *q_start,
+                 const int32_t *kv_len, const float *table, int table_len, int rot, void *q, int T, int B, int Hq,
+                 int flags);
+
+#define MX_ATTN_CAUSAL 0x1
+
+/* Attention of the new tokens over their contexts:
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k[j]) v[j]
+ * over the keys j of the sequence that token t (at position p) may see:
+ * 0 <= j < kv_len, with MX_ATTN_CAUSAL j <= p, and with window > 0 j > p - window.
+ * Head h reads cache head h / (Hq / Hkv).  sinks (fp32 [Hq] or null): a
+ * logit per head that joins the softmax's sum without a value.
+ * lse (fp32 [T][Hq] or null): the natural logarithm of that sum.  A row that
+ * sees no key gets zeros (and lse = its sink, or -infinity).  Cache places
+ * that a row may not see have no influence on it, whatever they hold.
+ * q bf16, strides in elements, last dimension contiguous; out bf16
+ * [T][Hq][D].  Scores, statistics and sums are fp32; the weights are rounded to
+ * bf16 for the product with v.
+ * workspace: caller-owned device memory of at least
+ * mx_paged_attn_workspace_size(T, B, Hq, kv->Hkv, kv->D) bytes, 256-byte
+ * aligned; overwritten, so calls sharing one must not overlap.
+ * Hq a multiple of Hkv, at most 128 query heads per cache head.  q and its
+ * strides multiples of 16 bytes, out 16-byte aligned.  A missing page sets
+ * MX_DEVERR_BAD_PAGE and makes the outputs that need it NaN. */
+size_t mx_paged_attn_workspace_size(int T, int B, int Hq, int Hkv, int D);
+int mx_paged_attn(const mx_paged_kv *kv, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                  const int32_t *q_start, const int32_t *kv_len, float scale, int flags, int window,
+                  const float *sinks, void *out, float *lse, int T, int B, int Hq, void *workspace,
+                  size_t workspace_bytes);
 
 /* ---- support calls (not on the pages; part of this library's contract) */
 
