@@ -11,122 +11,6 @@
 namespace mx {
 
 constexpr int DIRECT_WARPS = 4;
-constexpr int MAX_D = 256;
-
-// Running softmax of one row: the sums belong to the maximum m (log2 units);
-// lane l holds dimensions 2 l + 64 i and the one after.
-struct RowState {
-    float m = -INFINITY, l = 0.0f;
-    float o[MAX_D / 32] = {};
-};
-
-// One key's product with the row q (fp32, shared memory).
-template <int KVF>
-__device__ __forceinline__ float key_dot(const mx_paged_kv &kv, const float *q, long long at, long long sat)
-{
-    float acc = 0.0f;
-    if constexpr (KVF == KV_BF16) {
-        const uint16_t *p = static_cast<const uint16_t *>(kv.k) + at;
-        for (int d = 0; d < kv.D; d += 8) {
-            const uint4 r = *reinterpret_cast<const uint4 *>(p + d);
-            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc = fmaf(q[d + 2 * i], bf16_lo(w[i]), acc);
-                acc = fmaf(q[d + 2 * i + 1], bf16_hi(w[i]), acc);
-            }
-        }
-    } else {
-        const uint8_t *p = static_cast<const uint8_t *>(kv.k) + at;
-        const uint8_t *sc = static_cast<const uint8_t *>(kv.k_scales) + sat;
-        for (int d = 0; d < kv.D; d += 32) {
-            float part = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; j += 16) {
-                const uint4 r = *reinterpret_cast<const uint4 *>(p + d + j);
-                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t h0, h1;
-                    e4m3x4_to_f16x2(w[i], h0, h1);
-                    const float *qq = q + d + j + 4 * i;
-                    part = fmaf(qq[0], f16_lo_to_f32(h0), part);
-                    part = fmaf(qq[1], f16_hi_to_f32(h0), part);
-                    part = fmaf(qq[2], f16_lo_to_f32(h1), part);
-                    part = fmaf(qq[3], f16_hi_to_f32(h1), part);
-                }
-            }
-            acc = fmaf(part, e8m0_to_f32(sc[d / 32]), acc);
-        }
-    }
-    return acc;
-}
-
-// Adds keys first, first + 32 step, ... (32 at a time) below hi to the row;
-// keys below lo are skipped.  false if a page is missing.
-template <int KVF>
-__device__ bool row_keys(const mx_paged_kv &kv, const int32_t *table, int kvh, const float *q, float scale_log2,
-                         int lo, int hi, int first, int step, RowState &r)
-{
-    const int lane = threadIdx.x & 31;
-    bool all = true;
-    for (long long k0 = first; k0 < hi; k0 += 32ll * step) {
-        const long long key = k0 + lane;
-        bool seen = key >= lo && key < hi;
-        long long at = 0, sat = 0;
-        float s = -INFINITY;
-        if (seen) {
-            const int pi = (int)key / kv.page_size, slot = (int)key - pi * kv.page_size;
-            const int page = page_of(kv, table, pi);
-            if (page < 0) {
-                seen = all = false;
-            } else {
-                at = page * kv.page_stride + kvh * kv.head_stride + slot * kv.token_stride;
-                sat = page * kv.scale_page_stride + kvh * kv.scale_head_stride + slot * kv.scale_token_stride;
-                s = key_dot<KVF>(kv, q, at, sat) * scale_log2;
-            }
-        }
-        const unsigned mask = __ballot_sync(0xFFFFFFFFu, seen);
-        float top = s;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const float m = fmaxf(r.m, top);
-        // nothing seen yet, or only scores of -infinity: their weights are zero, unless one is NaN
-        const float base = m == -INFINITY ? 0.0f : m;
-        const float p = seen ? exp2f(s - base) : 0.0f;
-        const float shrink = exp2f(r.m - base);
-        r.m = m;
-        float sum = p;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        r.l = fmaf(r.l, shrink, sum);
-#pragma unroll
-        for (int i = 0; i < MAX_D / 32; ++i) r.o[i] *= shrink;
-        for (unsigned left = mask; left != 0; left &= left - 1) {
-            const int src = __ffs(left) - 1;
-            const float pj = __shfl_sync(0xFFFFFFFFu, p, src);
-            const long long vat = __shfl_sync(0xFFFFFFFFu, at, src);
-            const long long vsat = __shfl_sync(0xFFFFFFFFu, sat, src);
-#pragma unroll
-            for (int i = 0; i < MAX_D / 64; ++i) {
-                const int d = 2 * lane + 64 * i;
-                if (d >= kv.D) break;
-                if constexpr (KVF == KV_BF16) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(kv.v) + vat + d);
-                    r.o[2 * i] = fmaf(pj, bf16_lo(w), r.o[2 * i]);
-                    r.o[2 * i + 1] = fmaf(pj, bf16_hi(w), r.o[2 * i + 1]);
-                } else {
-                    const uint32_t w = *reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(kv.v) + vat + d);
-                    const float sc = e8m0_to_f32(static_cast<const uint8_t *>(kv.v_scales)[vsat + d / 32]);
-                    const uint32_t h2 = e4m3x2_to_f16x2(w);
-                    r.o[2 * i] = fmaf(pj, f16_lo_to_f32(h2) * sc, r.o[2 * i]);
-                    r.o[2 * i + 1] = fmaf(pj, f16_hi_to_f32(h2) * sc, r.o[2 * i + 1]);
-                }
-            }
-        }
-    }
-    return all;
-}
 
 template <int KVF>
 __global__ void __launch_bounds__(DIRECT_WARPS * 32) attn_direct_kernel(AttnArgs a)
@@ -185,10 +69,11 @@ __global__ void __launch_bounds__(DIRECT_WARPS * 32) attn_direct_kernel(AttnArgs
         a.lse[row] = bad ? __uint_as_float(0x7FC00000u) : (base + log2f(l)) * 0.6931471805599453f;
 }
 
-size_t attn_workspace_bytes(int, int, int, int, int) { return 256; }
+size_t attn_workspace_bytes(int T, int, int Hq, int Hkv, int D) { return attn_tc_workspace_bytes(T, Hq, Hkv, D); }
 
 cudaError_t launch_paged_attn(const DeviceState &ds, cudaStream_t st, const AttnArgs &a)
 {
+    if (attn_tc_ok(a)) return launch_attn_tc(ds, st, a);
     const long long blocks = (long long)a.T * a.Hq;
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks), block(DIRECT_WARPS * 32);

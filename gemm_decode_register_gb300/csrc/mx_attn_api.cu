@@ -144,5 +144,7 @@ extern "C" int mx_paged_attn(const mx_paged_kv *kv, const void *q, int64_t q_tok
     a.g = Hq / kv->Hkv;
     a.workspace = workspace;
     a.err = ds->err;
-    return finish(launch_paged_attn(*ds, current_stream(), a));
+    DeviceState v = *ds;  // the slot's counters: items cut across CTAs
+    if (!attach_stream_workspace(v, current_stream())) return MX_ECUDA;
+    return finish(launch_paged_attn(v, current_stream(), a));
 }

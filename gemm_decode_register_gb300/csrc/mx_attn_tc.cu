@@ -1,0 +1,1137 @@
+// mx_attn_tc.cu -- attention over the paged cache on the tensor cores
+// (tcgen05), heads of 64 or 128, sm_103a.
+//
+//   S = Q K^T,  P = 2^(scale log2(e) S - m),  O = P V,  out = O / sum P
+//
+// One persistent CTA per SM.  A row tile is 128 rows of (token, query head)
+// that share a cache head, a key tile 128 keys.  Two groups of four warps each
+// own one accumulator pair (S, O) in tensor memory; a thread owns a row, so
+// the softmax needs no shuffles.  What the two groups work on goes by the
+// item at hand:
+//   rows  (more than one row tile of new tokens): two row tiles over the same
+//         keys, each key tile read once for 256 rows;
+//   keys  (few tokens, e.g. one per sequence): the same row tile over
+//         alternate key tiles, merged at the end; the context streams through
+//         shared memory once.
+// While one group computes its softmax the tensor cores work for the other.
+// P is written over its S in tensor memory as bf16 and is operand A of the
+// second product from there; V is its operand B as it lies in the cache
+// (keys x dimensions, i.e. N-major).
+//
+// The maximum that P is taken against is only raised when a row's scores
+// outgrow it by 2^8 (the sums stay far inside fp32 and are exact ratios
+// either way): O then is rescaled in tensor memory by the row's own threads.
+//
+// Work is cut by cost, not by item: the (sequence, cache head, row tiles)
+// items laid end to end, each as long as the keys it sees, are divided into
+// equal stretches, one per CTA, so that any mix of prompts and single tokens
+// loads every SM the same.  An item cut across CTAs leaves partial (m, l, O)
+// rows in the workspace and the last CTA to arrive adds them in order.
+//
+//   warps 0-3, 4-7  softmax groups and epilogue
+//   warp 8          TMA producer (queries, keys, values)
+//   warp 9          MMA issuer
+//
+// Every wait is bounded as in the GEMMs; a CTA whose wait gives up makes its
+// outputs NaN and sets MX_DEVERR_TIMEOUT.
+#include "mx_attn.cuh"
+#include "mx_tc.cuh"
+
+namespace mx {
+
+constexpr int AT_ROWS = 128;  // rows of a tile
+constexpr int AT_KEYS = 128;  // keys of a tile
+constexpr int AT_THREADS = 320;
+constexpr int AT_SPLIT_KEYS = 2 * AT_KEYS;  // what an item costs beside its keys, and more than its tiles' rounding
+constexpr int AT_Q_COPIES = 4;              // up to so many tokens are loaded one by one
+constexpr float AT_RAISE = 8.0f;            // log2 by which scores may outgrow the maximum before it is raised
+constexpr unsigned long long AT_WAIT_NS = 2000000000ull;
+
+template <int D>
+struct AtGeo {
+    static constexpr int SLABS = D / 64;                    // 128-byte swizzled slabs of 64 dimensions
+    static constexpr int SLAB = 128 * 128;                  // bytes of a slab: 128 rows x 128 bytes
+    static constexpr int TILE = SLABS * SLAB;               // bytes of a row tile or a key tile
+    static constexpr int SLOTS = D == 128 ? 5 : 11;         // key/value tiles in flight
+    static constexpr int OFF_KV = 2 * TILE;                 // after two row tiles
+    static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
+    static constexpr int CTRL = 3072;                       // control block
+    static constexpr int SMEM = OFF_BAR + CTRL;
+    // tensor memory columns
+    static constexpr int S_COL = 0, O_COL = 256;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct AtParams {
+    AttnArgs a;
+    int *counters;      // 2 per CTA, zero between calls
+    float *partials;    // see partial_base
+    int part_rows;      // rows a partial has room for
+    int page_rows;      // rows of a TMA copy: min(page_size, 128)
+    unsigned long long wait_ns;
+    int stall;          // test hook: load no queries
+};
+
+// ------------------------------------------------------------ work
+
+// What a sequence's items cost: an item is (cache head, pair of row tiles).
+struct Seq {
+    int q0, n, len;   // first token row, new tokens, context
+    int pairs;        // items per cache head
+    int w;            // cost per key
+};
+
+__device__ __forceinline__ long long sum_range(long long a, long long s, long long lo, long long hi)
+{
+    // sum of a + i s for lo <= i < hi
+    const long long n = hi - lo;
+    return n <= 0 ? 0 : n * a + s * ((lo + hi - 1) * n / 2);
+}
+
+// Sum over i < p of max(a + i s, 0).
+__device__ __forceinline__ long long sum_pos(long long a, long long s, long long p)
+{
+    const long long z = a >= 0 ? 0 : (-a + s - 1) / s;
+    return sum_range(a, s, z, p);
+}
+
+struct Cost {
+    int s2;             // tokens of a pair of row tiles
+    int causal, window;
+    int heads;          // cache heads
+
+    // Keys before which items p, p + 1, ... of a head start (each item's own
+    // keys and AT_SPLIT_KEYS): items see [lo(p), hi(p)).
+    __device__ __forceinline__ long long before(const Seq &q, int p) const
+    {
+        const long long base = (long long)q.len - q.n;
+        long long h = (long long)p * q.len, l = 0;
+        if (causal) {
+            h = sum_pos(base + s2, s2, p);
+            if (p == q.pairs) h -= max(0ll, base + (long long)p * s2 - q.len);
+        }
+        if (window > 0) l = sum_pos(base - window + 1, s2, p);
+        return h - l + (long long)p * AT_SPLIT_KEYS;
+    }
+    __device__ __forceinline__ void range(const Seq &q, int p, int &lo, int &hi) const
+    {
+        const long long base = (long long)q.len - q.n;
+        hi = causal ? (int)max(0ll, min((long long)q.len, base + (p + 1ll) * s2)) : q.len;
+        lo = window > 0 ? (int)max(0ll, base + (long long)p * s2 - window + 1) : 0;
+        if (lo > hi) lo = hi;
+    }
+    __device__ __forceinline__ long long total(const Seq &q) const
+    {
+        return q.pairs > 0 ? before(q, q.pairs) * heads * q.w : 0;
+    }
+};
+
+__device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b, int s1)
+{
+    Seq q;
+    const int e0 = min(max(__ldg(a.q_start + b), 0), a.T), e1 = min(max(__ldg(a.q_start + b + 1), e0), a.T);
+    q.q0 = e0;
+    q.n = e1 - e0;
+    q.len = max(__ldg(a.kv_len + b), 0);
+    q.pairs = (q.n + 2 * s1 - 1) / (2 * s1);
+    q.w = q.n > s1 ? 3 : 2;
+    return q;
+}
+
+// A CTA's stretch of the work, found once per launch.
+struct Stretch {
+    long long total, start, end;  // cost
+    long long first_cost;         // cost before sequence `first`
+    int first, ctas;
+};
+
+// One piece: key tiles [k0, k1) of an item.
+struct Piece {
+    int b, kvh;
+    int q0, ntok;       // first token row of the item and its tokens
+    int first;          // position in the context of its first token
+    int len;            // context
+    int lo, hi;         // keys any of its rows may see
+    int tile0;          // key tile lo lies in
+    int k0, k1, tiles;  // this piece's tiles, relative to tile0, and the item's
+    bool rows;          // two row tiles (else alternate key tiles)
+    int c0, c1;         // CTAs the item is cut across
+};
+
+// Walks a CTA's pieces; every role runs its own.
+struct Walk {
+    const AttnArgs &a;
+    const Stretch &st;
+    Cost cost;
+    int s1;  // tokens of a row tile
+    Seq q;
+    int b, kvh, p;
+    long long at;  // cost before the item
+    bool found;
+
+    __device__ __forceinline__ Walk(const AttnArgs &args, const Stretch &stretch, const Cost &c)
+        : a(args), st(stretch), cost(c), s1(c.s2 / 2), b(stretch.first), kvh(0), p(0), at(stretch.first_cost), found(false)
+    {
+        if (st.start >= st.end) b = a.B;
+        if (b < a.B) q = load_seq(a, b, s1);
+    }
+    __device__ __forceinline__ int cta_of(long long x) const
+    {
+        return (int)(((x + 1) * st.ctas - 1) / st.total);
+    }
+    __device__ __forceinline__ bool next(Piece &o)
+    {
+        if (!found) {
+            // the first item that ends after the stretch's start
+            found = true;
+            while (b < a.B && at + cost.total(q) <= st.start) skip_seq();
+            if (b >= a.B) return false;
+            const long long head = cost.before(q, q.pairs) * q.w;
+            const long long off = max(st.start - at, 0ll);
+            kvh = (int)(off / head);
+            at += kvh * head;
+            int x = 0, y = q.pairs - 1;  // the last p with before(p) w <= offset
+            const long long rest = max(st.start - at, 0ll);
+            while (x < y) {
+                const int m = (x + y + 1) / 2;
+                if (cost.before(q, m) * q.w <= rest) x = m;
+                else y = m - 1;
+            }
+            p = x;
+            at += cost.before(q, p) * q.w;
+        }
+        for (;;) {
+            while (b < a.B && kvh >= cost.heads) {  // the sequence is done
+                ++b;
+                kvh = p = 0;
+                if (b < a.B) q = load_seq(a, b, s1);
+                if (b < a.B && q.pairs == 0) kvh = cost.heads;
+            }
+            if (b >= a.B || at >= st.end) return false;
+            cost.range(q, p, o.lo, o.hi);
+            o.tile0 = o.lo / AT_KEYS;
+            o.tiles = o.hi > o.lo ? (o.hi + AT_KEYS - 1) / AT_KEYS - o.tile0 : 0;
+            const long long w = (long long)AT_KEYS * q.w;
+            const long long x = (st.start - at + w - 1), y = (st.end - at + w - 1);
+            o.k0 = st.start <= at ? 0 : (int)min(x / w, (long long)o.tiles);
+            o.k1 = (int)min(y / w, (long long)o.tiles);
+            o.b = b;
+            o.kvh = kvh;
+            o.q0 = q.q0 + p * cost.s2;
+            o.ntok = min(q.n - p * cost.s2, cost.s2);
+            o.first = q.len - q.n + p * cost.s2;
+            o.len = q.len;
+            o.rows = o.ntok > s1;
+            o.c0 = cta_of(at);
+            o.c1 = o.tiles > 0 ? cta_of(at + (o.tiles - 1) * w) : o.c0;
+            const bool mine = o.tiles > 0 ? o.k0 < o.k1 : st.start <= at;
+            at += ((long long)(o.hi - o.lo) + AT_SPLIT_KEYS) * q.w;
+            if (++p >= q.pairs) {
+                p = 0;
+                ++kvh;
+            }
+            if (mine) return true;
+        }
+    }
+    __device__ __forceinline__ void skip_seq()
+    {
+        at += cost.total(q);
+        ++b;
+        if (b < a.B) q = load_seq(a, b, s1);
+    }
+};
+
+// The whole block: costs of all sequences, this CTA's stretch of them.
+// scratch: 2 words of 8 bytes per warp, and 4 more.
+__device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, long long *scratch, Stretch *out)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int SCAN = 256;
+    const int per = (a.B + SCAN - 1) / SCAN;
+    long long sum = 0;
+    if (tid < SCAN)
+        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) sum += cost.total(load_seq(a, b, cost.s2 / 2));
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    long long pre = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < SCAN / 32; ++w) {
+        if (w < warp) pre += scratch[w];
+        total += scratch[w];
+    }
+    const long long before = pre + inc - sum;
+    // a CTA's stretch is no shorter than two tiles of the costlier kind, so
+    // no CTA between an item's first and last is left without a tile
+    const long long most = max(1ll, total / (2 * AT_KEYS * 3));
+    const int ctas = (int)min((long long)gridDim.x, most);
+    const int c = blockIdx.x;
+    const long long start = c < ctas ? total * c / ctas : total;
+    const long long end = c < ctas ? total * (c + 1) / ctas : total;
+    if (tid == 0) {
+        out->total = total;
+        out->start = start;
+        out->end = end;
+        out->ctas = ctas;
+        out->first = a.B;
+        out->first_cost = total;
+    }
+    __syncthreads();
+    if (tid < SCAN && sum > 0 && before <= start && start < before + sum) {
+        out->first = tid * per;
+        out->first_cost = before;
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------ tensor ops
+
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+// Operand A in tensor memory.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t at, uint64_t bd, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(at), "l"(bd), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void umma_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+// bf16 operands, fp32 accumulator, M = 128; B K-major or N-major.
+template <int N>
+__device__ __forceinline__ constexpr uint32_t at_idesc(bool b_n_major)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+           ((128u >> 4) << 24);
+}
+
+// V as operand B, N-major with 128-byte swizzle: rows of 64 dimensions (128
+// bytes), 8 keys every 1024 bytes, the next 64 dimensions a slab further.
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr, uint32_t slab_bytes)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(slab_bytes >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+#define MX_R32(r, o)                                                                                                  \
+    "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]),  \
+        "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]),            \
+        "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15]), "=r"(r[o + 16]), "=r"(r[o + 17]), "=r"(r[o + 18]),         \
+        "=r"(r[o + 19]), "=r"(r[o + 20]), "=r"(r[o + 21]), "=r"(r[o + 22]), "=r"(r[o + 23]), "=r"(r[o + 24]),         \
+        "=r"(r[o + 25]), "=r"(r[o + 26]), "=r"(r[o + 27]), "=r"(r[o + 28]), "=r"(r[o + 29]), "=r"(r[o + 30]),         \
+        "=r"(r[o + 31])
+
+// 32 columns of the thread's lane into r[o..], without waiting.
+template <int NR>
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[NR], const int o)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : MX_R32(r, o)
+                 : "r"(taddr));
+}
+#undef MX_R32
+
+// Keeps uses of r[o..o+31] behind the wait that precedes it.
+template <int NR>
+__device__ __forceinline__ void pin32(uint32_t (&r)[NR], const int o)
+{
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+r"(r[o + i]), "+r"(r[o + i + 1]), "+r"(r[o + i + 2]), "+r"(r[o + i + 3]),
+                          "+r"(r[o + i + 4]), "+r"(r[o + i + 5]), "+r"(r[o + i + 6]), "+r"(r[o + i + 7]));
+}
+
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+                 "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+                 "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// Two fp32 in one 64-bit register.
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ void group_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                            uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// ------------------------------------------------------------ kernel
+
+// Shared control block, after the tiles.
+struct AtCtrl {
+    uint64_t full[12], empty[12];    // key/value slots
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t done;
+    long long scratch[16];
+    Stretch stretch;
+    uint32_t tmem;
+    int abort_flag;
+    int missing[8];                  // by piece number: a page of it is missing
+    int last[2];
+    float m[2][AT_ROWS], l[2][AT_ROWS];
+};
+static_assert(sizeof(AtCtrl) <= AtGeo<128>::CTRL, "control block");
+
+// Load numbers within a piece of n key tiles: K tile t, V tile t.  The keys
+// run `ahead` tiles ahead: K 0 .. ahead-1, then V t, K t + ahead in turn.
+__device__ __forceinline__ int k_load(int t, int ahead) { return t < ahead ? t : 2 * t - ahead + 1; }
+__device__ __forceinline__ int v_load(int t, int n, int ahead) { return t + min(n, ahead + t); }
+
+// Where the partial of (CTA, which of its two, group) lies: m and l of the
+// rows, then O in units of four dimensions, rows fastest.
+template <int D>
+__device__ __forceinline__ float *partial_base(const AtParams &p, int cta, int which, int group)
+{
+    return p.partials + (size_t)((cta * 2 + which) * 2 + group) * p.part_rows * (D + 2);
+}
+
+// A row whose sum over the tiles came out NaN or infinite, computed again from
+// its own keys alone: a product with a weight of zero is not zero when the
+// value is NaN or infinite, and such a value may lie where the row may not
+// see it.  By the whole warp; q_row: MAX_D floats of shared memory per warp.
+template <int KVF>
+__device__ __noinline__ void row_again(const AttnArgs &a, int b, int t, int h, int lo, int hi, int d0, int d1,
+                                       float inv_total, float m_used)
+{
+    const int lane = threadIdx.x & 31;
+    const mx_paged_kv &kv = a.kv;
+    const int32_t *table = kv.block_table + (size_t)b * kv.table_stride;
+    const uint16_t *q = a.q + (long long)t * a.q_token_stride + (long long)h * a.q_head_stride;
+    const int kvh = h / a.g;
+    float o[MAX_D / 32] = {};
+    for (int k0 = lo; k0 < hi; k0 += 32) {
+        const int key = k0 + lane;
+        long long at = 0, sat = 0;
+        float p = 0.0f;
+        if (key < hi) {
+            const int pi = key / kv.page_size, slot = key - pi * kv.page_size;
+            const int page = max(page_of(kv, table, pi), 0);
+            at = page * kv.page_stride + kvh * kv.head_stride + slot * kv.token_stride;
+            sat = page * kv.scale_page_stride + kvh * kv.scale_head_stride + slot * kv.scale_token_stride;
+            p = exp2f(key_dot<KVF>(kv, q, at, sat) * a.scale_log2 - m_used) * inv_total;
+        }
+        for (int j = 0; j < min(32, hi - k0); ++j) {
+            const float pj = __shfl_sync(0xFFFFFFFFu, p, j);
+            add_value<KVF>(kv, __shfl_sync(0xFFFFFFFFu, at, j), __shfl_sync(0xFFFFFFFFu, sat, j), pj, o);
+        }
+    }
+    uint16_t *out = a.out + ((size_t)t * a.Hq + h) * kv.D;
+#pragma unroll
+    for (int i = 0; i < MAX_D / 64; ++i) {
+        const int d = 2 * lane + 64 * i;
+        if (d >= d0 && d < d1) *reinterpret_cast<uint32_t *>(out + d) = f32x2_to_bf16x2(o[2 * i], o[2 * i + 1]);
+    }
+}
+
+template <int D, int KVF>
+__global__ void __launch_bounds__(AT_THREADS, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_q1,
+                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                   const __grid_constant__ AtParams prm)
+{
+    using G = AtGeo<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];  // 1024: the swizzle's period
+    AtCtrl &c = *reinterpret_cast<AtCtrl *>(smem + G::OFF_BAR);
+    const AttnArgs &a = prm.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int *abort_flag = &c.abort_flag;
+    Cost cost;
+    const int s1 = AT_ROWS / a.g;
+    cost.s2 = 2 * s1;
+    cost.causal = a.causal;
+    cost.window = a.window;
+    cost.heads = a.kv.Hkv;
+
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::SLOTS; ++s) {
+            mbar_init(&c.full[s], 1);
+            mbar_init(&c.empty[s], 1);
+        }
+        mbar_init(&c.q_full, 1);
+        mbar_init(&c.q_empty, 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&c.s_full[w], 1);
+            mbar_init(&c.p_full[w], 4);
+            mbar_init(&c.o_full[w], 1);
+        }
+        mbar_init(&c.done, 1);
+        c.abort_flag = 0;
+        for (int i = 0; i < 8; ++i) c.missing[i] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
+    }
+    plan(a, cost, c.scratch, &c.stretch);  // its barriers also publish the set-up above
+    tc_fence_after();
+    const uint32_t tmem = c.tmem;
+    const Stretch st = c.stretch;
+    pdl_wait();
+    Walk walk(a, st, cost);
+    Piece pc;
+
+    if (warp == 8) {
+        // ---------------- producer
+        const int ppt = AT_KEYS / prm.page_rows;  // TMA copies per tile and slab
+        int load = 0, piece = 0;
+        bool go = true;
+        while (go && walk.next(pc)) {
+            if (pc.k0 >= pc.k1) continue;
+            const int32_t *table = a.kv.block_table + (size_t)pc.b * a.kv.table_stride;
+            const int ahead = pc.rows ? 1 : 2, n = pc.k1 - pc.k0;
+            if (lane == 0) c.missing[piece & 7] = 0;
+            // queries
+            int ok = 1;
+            if (lane == 0 && piece > 0) ok = mbar_wait(&c.q_empty, (piece - 1) & 1, abort_flag, prm.wait_ns);
+            if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+            if (lane == 0 && !prm.stall) {
+                const uint32_t dst = smem_u32(smem);
+                if (pc.rows) {
+                    mbar_arrive_expect_tx(&c.q_full, 2 * G::SLABS * (uint32_t)(s1 * a.g) * 128u);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int s = 0; s < G::SLABS; ++s)
+                            tma_load_3d(dst + r * G::TILE + s * G::SLAB, &map_q, 64 * s, pc.kvh * a.g,
+                                        pc.q0 + r * s1, &c.q_full);
+                } else if (pc.ntok > AT_Q_COPIES) {
+                    // whole row tile: the rows past the item's tokens are not used
+                    mbar_arrive_expect_tx(&c.q_full, G::SLABS * (uint32_t)(s1 * a.g) * 128u);
+#pragma unroll
+                    for (int s = 0; s < G::SLABS; ++s)
+                        tma_load_3d(dst + s * G::SLAB, &map_q, 64 * s, pc.kvh * a.g, pc.q0, &c.q_full);
+                } else {
+                    mbar_arrive_expect_tx(&c.q_full, G::SLABS * (uint32_t)(pc.ntok * a.g) * 128u);
+                    for (int t = 0; t < pc.ntok; ++t)
+#pragma unroll
+                        for (int s = 0; s < G::SLABS; ++s)
+                            tma_load_3d(dst + s * G::SLAB + (uint32_t)(t * a.g) * 128u, &map_q1, 64 * s,
+                                        pc.kvh * a.g, pc.q0 + t, &c.q_full);
+                }
+            }
+            // page ids: lane i holds copy i of a window of 32 copies; the keys'
+            // window, the one before it (the values lag by up to two tiles)
+            // and the one after it (on its way)
+            const int per_win = 32 / ppt;  // tiles per window
+            auto load_ids = [&](int wn) {
+                const long long key = (long long)(pc.tile0 + wn * per_win) * AT_KEYS + lane * prm.page_rows;
+                if (key >= pc.hi || key + prm.page_rows <= pc.lo) return -1;  // not seen: no copy
+                const int id = page_of(a.kv, table, (int)key / a.kv.page_size);
+                return id < 0 ? -2 : id;  // -2: missing
+            };
+            int win = pc.k0 / per_win, id_before = -1, id_here = load_ids(win), id_after = load_ids(win + 1);
+            for (int i = 0; i < 2 * n; ++i) {
+                // the i-th load: K or V, of tile t
+                int t;
+                bool is_k;
+                if (i < min(ahead, n)) {
+                    t = i;
+                    is_k = true;
+                } else {
+                    const int r = i - min(ahead, n);
+                    // V 0, K ahead, V 1, K ahead + 1, ... then the last Vs
+                    if (r < 2 * (n - ahead)) {
+                        is_k = r & 1;
+                        t = is_k ? ahead + r / 2 : r / 2;
+                    } else {
+                        is_k = false;
+                        t = r - max(n - ahead, 0);
+                    }
+                }
+                const int tile = pc.tile0 + pc.k0 + t;
+                const int wn = (pc.k0 + t) / per_win;
+                if (wn > win) {
+                    win = wn;
+                    id_before = id_here;
+                    id_here = id_after;
+                    id_after = load_ids(win + 1);
+                }
+                const int copy = ((pc.k0 + t) % per_win) * ppt + lane / G::SLABS;
+                const int page = __shfl_sync(0xFFFFFFFFu, wn == win ? id_here : id_before, copy & 31);
+                const bool mine = lane < ppt * G::SLABS;
+                const unsigned valid = __ballot_sync(0xFFFFFFFFu, mine && page >= 0);
+                if (__any_sync(0xFFFFFFFFu, mine && page == -2) && lane == 0) c.missing[piece & 7] = 1;
+                const int s = load % G::SLOTS;
+                ok = 1;
+                if (lane == 0) {
+                    if (load >= G::SLOTS) ok = mbar_wait(&c.empty[s], ((load / G::SLOTS) - 1) & 1, abort_flag, prm.wait_ns);
+                    if (ok) mbar_arrive_expect_tx(&c.full[s], (uint32_t)__popc(valid) * prm.page_rows * 128u);
+                }
+                if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
+                    go = false;
+                    break;
+                }
+                if (mine && page >= 0) {
+                    const int j = lane / G::SLABS, sl = lane % G::SLABS;
+                    const int key = tile * AT_KEYS + j * prm.page_rows;
+                    tma_load_4d(smem_u32(smem + G::OFF_KV + s * G::TILE + sl * G::SLAB) + (uint32_t)(j * prm.page_rows) * 128u,
+                                is_k ? &map_k : &map_v, 64 * sl, key % a.kv.page_size, pc.kvh, page, &c.full[s]);
+                }
+                ++load;
+            }
+            ++piece;
+        }
+        if (*abort_flag) {
+            // copies in flight must land before the CTA may exit
+            __syncwarp();
+            if (lane == 0) {
+                for (int i = max(load - G::SLOTS, 0); i < load; ++i)
+                    mbar_wait(&c.full[i % G::SLOTS], (i / G::SLOTS) & 1, abort_flag, AT_WAIT_NS, false);
+                if (!prm.stall && piece > 0) mbar_wait(&c.q_full, (piece - 1) & 1, abort_flag, AT_WAIT_NS, false);
+                if (!prm.stall) mbar_wait(&c.q_full, piece & 1, abort_flag, 1000000ull, false);
+            }
+        }
+    } else if (warp == 9) {
+        // ---------------- MMA issuer
+        if (lane == 0) {
+            const uint32_t qs = smem_u32(smem), kvs = smem_u32(smem + G::OFF_KV);
+            constexpr uint32_t idesc_s = at_idesc<AT_KEYS>(false), idesc_o = at_idesc<D>(true);
+            int base = 0, piece = 0;
+            int np[2] = {0, 0};  // softmax steps issued by each group
+            bool go = true;
+            auto wait_slot = [&](int i) {
+                return mbar_wait(&c.full[i % G::SLOTS], (i / G::SLOTS) & 1, abort_flag, prm.wait_ns);
+            };
+            auto s_mma = [&](int w, int qtile, int i) {
+                const uint32_t kb = kvs + (uint32_t)(i % G::SLOTS) * G::TILE, qb = qs + (uint32_t)qtile * G::TILE;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (uint32_t)(kk / 4) * G::SLAB + (kk % 4) * 32;
+                    umma_ss(tmem + G::S_COL + 128 * w, sw128_desc(qb + off), sw128_desc(kb + off), idesc_s, kk > 0);
+                }
+                umma_commit(&c.s_full[w]);
+            };
+            auto o_mma = [&](int w, int i, bool first) {
+                const uint32_t vb = kvs + (uint32_t)(i % G::SLOTS) * G::TILE;
+#pragma unroll
+                for (int kk = 0; kk < AT_KEYS / 16; ++kk)
+                    umma_ts(tmem + G::O_COL + 128 * w, tmem + G::S_COL + 128 * w + 8 * kk,
+                            v_desc(vb + kk * 2048, G::SLAB), idesc_o, !(first && kk == 0));
+                umma_commit(&c.o_full[w]);
+            };
+            while (go && walk.next(pc)) {
+                if (pc.k0 >= pc.k1) continue;
+                const int n = pc.k1 - pc.k0, ahead = pc.rows ? 1 : 2;
+                if (!mbar_wait(&c.q_full, piece & 1, abort_flag, prm.wait_ns)) break;
+                tc_fence_after();
+                // the first scores of each group
+                go = wait_slot(base);
+                if (!go) break;
+                tc_fence_after();
+                s_mma(0, 0, base);
+                if (pc.rows) {
+                    s_mma(1, 1, base);
+                    umma_commit(&c.empty[base % G::SLOTS]);
+                } else {
+                    umma_commit(&c.empty[base % G::SLOTS]);
+                    if (n > 1) {
+                        go = wait_slot(base + 1);
+                        if (!go) break;
+                        tc_fence_after();
+                        s_mma(1, 0, base + 1);
+                        umma_commit(&c.empty[(base + 1) % G::SLOTS]);
+                    }
+                }
+                if (n <= ahead) umma_commit(&c.q_empty);
+                for (int t = 0; t < n && go; ++t) {
+                    const int vi = base + v_load(t, n, ahead), ki = base + k_load(t + ahead, ahead);
+                    const bool more = t + ahead < n;
+                    for (int w = pc.rows ? 0 : (t & 1); w < (pc.rows ? 2 : (t & 1) + 1); ++w) {
+                        go = mbar_wait(&c.p_full[w], np[w] & 1, abort_flag, prm.wait_ns) && wait_slot(vi);
+                        if (!go) break;
+                        ++np[w];
+                        tc_fence_after();
+                        o_mma(w, vi, pc.rows ? t == 0 : t < 2);
+                        if (!pc.rows || w == 1) umma_commit(&c.empty[vi % G::SLOTS]);
+                        if (more) {
+                            go = wait_slot(ki);
+                            if (!go) break;
+                            tc_fence_after();
+                            s_mma(w, pc.rows ? w : 0, ki);
+                            if (!pc.rows || w == 1) umma_commit(&c.empty[ki % G::SLOTS]);
+                        }
+                    }
+                    if (go && t + ahead == n - 1) umma_commit(&c.q_empty);  // the last scores are on their way
+                }
+                base += 2 * n;
+                ++piece;
+            }
+            umma_commit(&c.done);
+        }
+    } else if (warp < 8) {
+        // ---------------- softmax groups
+        const int w = warp >> 2;            // group
+        const int row = threadIdx.x & 127;  // row of the tile; also the tensor-memory lane
+        const uint32_t lane_base = tmem + ((uint32_t)(row & ~31) << 16);
+        const uint32_t s_addr = lane_base + G::S_COL + 128 * w;
+        const float sl2 = a.scale_log2;
+        int base = 0, piece = 0, steps = 0;  // steps: softmax steps of this group so far
+        bool alive = true;
+        // warp-uniform, as the tensor-memory instructions that follow a wait must be
+        auto wait = [&](uint64_t *bar, int phase) {
+            return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1, abort_flag, prm.wait_ns)) != 0;
+        };
+        while (walk.next(pc)) {
+            const int n = pc.k1 - pc.k0, ahead = pc.rows ? 1 : 2;
+            const int tok = (pc.rows ? w * s1 : 0) + row / a.g, head = pc.kvh * a.g + row % a.g;
+            const bool valid = row < s1 * a.g && tok < pc.ntok;
+            const int pos = pc.first + tok;
+            int rlo = 0, rhi = 0x7FFFFFFF;  // (a lane without a row needs no mask)
+            if (valid) {
+                rhi = a.causal ? min(pos + 1, pc.len) : pc.len;
+                rlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+                if (rhi < rlo) rhi = rlo;
+            }
+            const bool warp_on = __any_sync(0xFFFFFFFFu, valid);
+            float m = -INFINITY, l = 0.0f;  // m: log2 units, what P was taken against
+            int mine = 0;                   // steps of this piece
+            for (int t = pc.rows ? 0 : w; t < n && alive; t += ahead) {
+                alive = wait(&c.s_full[w], steps);
+                if (!alive) break;
+                const int key0 = (pc.tile0 + pc.k0 + t) * AT_KEYS;
+                // rows of V that no row sees, or that were not loaded: their
+                // weights are zero, their values must be finite
+                if ((key0 < pc.lo || key0 + AT_KEYS > pc.hi) && (w == 0 || !pc.rows)) {
+                    const int vi = base + v_load(t, n, ahead);
+                    alive = wait(&c.full[vi % G::SLOTS], vi / G::SLOTS);
+                    if (!alive) break;
+                    uint8_t *v = smem + G::OFF_KV + (vi % G::SLOTS) * G::TILE;
+                    const int key = key0 + row;
+                    if (key < pc.lo || key >= pc.hi)
+                        for (int i = 0; i < G::SLABS * 8; ++i)
+                            *reinterpret_cast<uint4 *>(v + (i / 8) * G::SLAB + row * 128 + (i % 8) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                }
+                if (warp_on) {
+                    tc_fence_after();
+                    uint32_t s[128];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld32_async(s_addr + 32 * i, s, 32 * i);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) pin32(s, 32 * i);
+                    if (__any_sync(0xFFFFFFFFu, key0 < rlo || key0 + AT_KEYS > rhi)) {
+                        const int klo = rlo - key0, khi = rhi - key0;
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (i < klo || i >= khi) s[i] = 0xFF800000u;
+                    }
+                    float x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(s[i]);
+#pragma unroll
+                    for (int i = 4; i < 128; i += 8)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            x[j] = i + 4 + j < 128 ? max3(x[j], __uint_as_float(s[i + j]), __uint_as_float(s[i + 4 + j]))
+                                                   : fmaxf(x[j], __uint_as_float(s[i + j]));
+                    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl2;
+                    // raise the maximum: at the first tile that has one, and when it is outgrown
+                    const bool raise = valid && (top > m + AT_RAISE || (m == -INFINITY && top > -INFINITY));
+                    if (__any_sync(0xFFFFFFFFu, raise)) {
+                        const float m_new = raise ? top : m;
+                        const float f = m == -INFINITY ? 0.0f : exp2_approx(m - m_new);
+                        m = m_new;
+                        l *= f;
+                        if (mine > 0) {
+                            // the O so far belongs to the old maximum
+                            alive = wait(&c.o_full[w], steps - 1);
+                            if (!alive) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int i = 0; i < D; i += 32) {
+                                uint32_t o[32];
+                                tmem_ld32_async(lane_base + G::O_COL + 128 * w + i, o, 0);
+                                tmem_wait_ld();
+                                pin32(o, 0);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st32(lane_base + G::O_COL + 128 * w + i, o);
+                            }
+                        }
+                    }
+                    const float neg = m == -INFINITY ? 0.0f : -m;
+                    const uint64_t sl22 = pack2(sl2, sl2), neg2 = pack2(neg, neg);
+                    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const uint64_t e2 = fma2(pack2(__uint_as_float(s[64 * h + 2 * i]),
+                                                           __uint_as_float(s[64 * h + 2 * i + 1])), sl22, neg2);
+                            float e0, e1;
+                            unpack2(e2, e0, e1);
+                            e0 = exp2_approx(e0);
+                            e1 = exp2_approx(e1);
+                            sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
+                            pk[i] = f32x2_to_bf16x2(e0, e1);
+                        }
+                        tmem_st32(s_addr + 32 * h, pk);
+                    }
+                    float s0, s1_, s2, s3;
+                    unpack2(sum[0], s0, s1_);
+                    unpack2(sum[1], s2, s3);
+                    l += (s0 + s1_) + (s2 + s3);
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.p_full[w]);
+                ++steps;
+                ++mine;
+            }
+            // the last product must be in before O is read
+            if (mine > 0 && alive) alive = wait(&c.o_full[w], steps - 1);
+            tc_fence_after();
+            const bool bad = !alive || (n > 0 && c.missing[piece & 7] != 0);
+            if (bad && row == 0) set_device_error(a.err, alive ? DEVERR_BAD_PAGE : DEVERR_TIMEOUT);
+            // rows: the group's own rows, all dimensions.  keys: both groups'
+            // sums of the same rows; group w takes half of the dimensions.
+            int d0 = 0, d1 = D;
+            float f_own = 1.0f, f_other = 0.0f;
+            if (!pc.rows) {
+                c.m[w][row] = m;
+                c.l[w][row] = alive ? l : __uint_as_float(0x7FC00000u);
+                tc_fence_before();
+                group_sync(1, 256);
+                tc_fence_after();
+                const float m2 = c.m[w ^ 1][row], l2 = c.l[w ^ 1][row];
+                const float top = fmaxf(m, m2);
+                if (top > -INFINITY) {
+                    f_own = m == -INFINITY ? 0.0f : exp2_approx(m - top);
+                    f_other = m2 == -INFINITY ? 0.0f : exp2_approx(m2 - top);
+                }
+                // in the same order in both groups
+                l = w == 0 ? fmaf(l, f_own, l2 * f_other) : fmaf(l2, f_other, l * f_own);
+                m = top;
+                d0 = w * (D / 2);
+                d1 = d0 + D / 2;
+            }
+            const bool own = pc.rows ? mine > 0 : (w == 0 ? n > 0 : n > 1);
+            const bool oth = pc.rows ? false : (w == 0 ? n > 1 : n > 0);
+            // 32 dimensions of the row's sums against m
+            auto read_o = [&](int d, float (&o)[32]) {
+                uint32_t u[32] = {}, v[32] = {};
+                if (own) tmem_ld32_async(lane_base + G::O_COL + 128 * w + d, u, 0);
+                if (oth) tmem_ld32_async(lane_base + G::O_COL + 128 * (w ^ 1) + d, v, 0);
+                tmem_wait_ld();
+                pin32(u, 0);
+                pin32(v, 0);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float x = own ? __uint_as_float(u[j]) * f_own : 0.0f;
+                    const float y = oth ? __uint_as_float(v[j]) * f_other : 0.0f;
+                    o[j] = x + y;
+                }
+            };
+            const bool cut = pc.c0 != pc.c1;
+            int npieces = 1;
+            bool finish_here = true;
+            float *part = nullptr;
+            if (cut) {
+                npieces = pc.c1 - pc.c0 + 1;
+                const int cta = blockIdx.x;
+                part = partial_base<D>(prm, cta, cta == pc.c0 ? 1 : 0, w);
+                if (valid) {
+                    part[2 * row] = bad ? __uint_as_float(0x7FC00000u) : m;
+                    part[2 * row + 1] = bad ? __uint_as_float(0x7FC00000u) : l;
+                }
+                float4 *po = reinterpret_cast<float4 *>(part + 2 * prm.part_rows);
+                if (warp_on && !bad)
+#pragma unroll 1
+                    for (int d = d0; d < d1; d += 32) {
+                        float o[32];
+                        read_o(d, o);
+                        if (valid)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                po[(size_t)((d - d0) / 4 + j) * prm.part_rows + row] =
+                                    make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                __threadfence();
+                group_sync(2 + w, 128);
+                if (row == 0) {
+                    int *count = prm.counters + 2 * pc.c0 + w;
+                    const int arrived = atomicAdd(count, 1) + 1;
+                    if (arrived == npieces) *count = 0;
+                    c.last[w] = arrived == npieces;
+                    __threadfence();
+                }
+                group_sync(2 + w, 128);
+                finish_here = c.last[w] != 0;
+            }
+            if (finish_here && warp_on) {
+                // the sums' maximum and total over all pieces
+                float top = m, total = l;
+                bool nan = bad;
+                if (cut) {
+                    __threadfence();
+                    top = -INFINITY;
+                    total = 0.0f;
+                    if (valid) {
+                        for (int i = 0; i < npieces; ++i) {
+                            const float mi = __ldcg(partial_base<D>(prm, pc.c0 + i, i == 0 ? 1 : 0, w) + 2 * row);
+                            if (mi != mi) nan = true;
+                            top = fmaxf(top, mi);
+                        }
+                        for (int i = 0; i < npieces; ++i) {
+                            const float *pi = partial_base<D>(prm, pc.c0 + i, i == 0 ? 1 : 0, w) + 2 * row;
+                            const float mi = __ldcg(pi);
+                            if (mi > -INFINITY) total = fmaf(__ldcg(pi + 1), exp2_approx(mi - top), total);
+                        }
+                    }
+                }
+                const float m_all = top;
+                float sink = -INFINITY;
+                if (a.sinks && valid) sink = __ldg(a.sinks + head) * 1.4426950408889634f;
+                const float ref = fmaxf(top, sink);
+                const float base2 = ref == -INFINITY ? 0.0f : ref;
+                float f = m_all == -INFINITY ? 0.0f : exp2_approx(m_all - base2);
+                float den = total * f;
+                if (a.sinks) den += exp2_approx(sink - base2);
+                const float inv = den == 0.0f ? 0.0f : f / den;
+                const size_t out_row = (size_t)(pc.q0 + tok) * a.Hq + head;
+                if (valid && a.lse && (pc.rows || w == 0))
+                    a.lse[out_row] = nan ? __uint_as_float(0x7FC00000u) : (base2 + log2f(den)) * 0.6931471805599453f;
+                float check = 0.0f;
+#pragma unroll 1
+                for (int d = d0; d < d1; d += 32) {
+                    float o[32];
+                    if (nan) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(0x7FC00000u);
+                    } else if (!cut) {
+                        read_o(d, o);  // (nan is the same for the whole group here)
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+                    }
+                    if (cut && valid && !nan)
+                        for (int i = 0; i < npieces; ++i) {
+                            const float *pi = partial_base<D>(prm, pc.c0 + i, i == 0 ? 1 : 0, w);
+                            const float mi = __ldcg(pi + 2 * row);
+                            const float fi = mi == -INFINITY ? 0.0f : exp2_approx(mi - m_all);
+                            const float4 *po = reinterpret_cast<const float4 *>(pi + 2 * prm.part_rows);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 r = __ldcg(po + (size_t)((d - d0) / 4 + j) * prm.part_rows + row);
+                                o[4 * j] = fmaf(r.x, fi, o[4 * j]);
+                                o[4 * j + 1] = fmaf(r.y, fi, o[4 * j + 1]);
+                                o[4 * j + 2] = fmaf(r.z, fi, o[4 * j + 2]);
+                                o[4 * j + 3] = fmaf(r.w, fi, o[4 * j + 3]);
+                            }
+                        }
+                    if (valid) {
+                        uint32_t r[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float x = o[2 * j] * inv, y = o[2 * j + 1] * inv;
+                            check = fmaf(x, 0.0f, check);
+                            check = fmaf(y, 0.0f, check);
+                            r[j] = f32x2_to_bf16x2(x, y);
+                        }
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * D + d);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) dst[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                    }
+                }
+                // rows that saw a NaN or an infinity, or only multiplied one by zero
+                unsigned again = __ballot_sync(0xFFFFFFFFu, valid && !nan && check != 0.0f);
+                for (; again != 0; again &= again - 1) {
+                    const int src = __ffs(again) - 1;
+                    row_again<KVF>(a, pc.b, __shfl_sync(0xFFFFFFFFu, pc.q0 + tok, src),
+                                   __shfl_sync(0xFFFFFFFFu, head, src), __shfl_sync(0xFFFFFFFFu, rlo, src),
+                                   __shfl_sync(0xFFFFFFFFu, rhi, src), d0, d1,
+                                   1.0f / __shfl_sync(0xFFFFFFFFu, den, src), __shfl_sync(0xFFFFFFFFu, base2, src));
+                }
+            }
+            if (!pc.rows) {
+                // the other group's O is read; it may be overwritten after this
+                tc_fence_before();
+                group_sync(1, 256);
+            }
+            tc_fence_before();
+            base += 2 * max(n, 0);
+            if (n > 0) ++piece;
+        }
+    }
+    __syncthreads();
+    if (warp == 9) {
+        if (lane == 0) mbar_wait(&c.done, 0, abort_flag, AT_WAIT_NS, false);
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// ------------------------------------------------------------ host
+
+constexpr int AT_MAX_CTAS = 160;
+
+static int part_rows(int T, int g)
+{
+    const int s1 = AT_ROWS / g;
+    return ((T < s1 ? T : s1) * g + 7) / 8 * 8;
+}
+
+size_t attn_tc_workspace_bytes(int T, int Hq, int Hkv, int D)
+{
+    return ((size_t)AT_MAX_CTAS * 4 * part_rows(T, Hq / Hkv) * (D + 2) * sizeof(float) + 255) / 256 * 256;
+}
+
+bool attn_tc_ok(const AttnArgs &a)
+{
+    const int ps = a.kv.page_size;
+    // whole copies of at least 16 rows per key tile; a maximum that is raised needs a positive scale
+    return a.kv.kv_fmt == KV_BF16 && (a.kv.D == 64 || a.kv.D == 128) &&
+           (ps % AT_KEYS == 0 || (ps >= 16 && AT_KEYS % ps == 0)) && a.scale_log2 > 0.0f &&
+           a.scale_log2 < INFINITY;
+}
+
+template <int D>
+static cudaError_t run_attn_tc(const DeviceState &ds, cudaStream_t st, const AttnArgs &a)
+{
+    using G = AtGeo<D>;
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    if (G::SMEM > ds.max_smem_optin || ds.ws_counters < 2 * AT_MAX_CTAS) return cudaErrorInvalidValue;
+    AtParams p;
+    p.a = a;
+    p.counters = ds.ws_count;
+    p.partials = static_cast<float *>(a.workspace);
+    p.part_rows = part_rows(a.T, a.g);
+    p.page_rows = a.kv.page_size < AT_KEYS ? a.kv.page_size : AT_KEYS;
+    p.stall = qmm_stall(&p.wait_ns);
+    const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
+    const int s1 = AT_ROWS / a.g;
+    CUtensorMap maps[4];
+    for (int i = 0; i < 2; ++i) {
+        const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+        const cuuint64_t strides[2] = {(cuuint64_t)a.q_head_stride * 2, (cuuint64_t)a.q_token_stride * 2};
+        const cuuint32_t box[3] = {64u, (cuuint32_t)a.g, i == 0 ? (cuuint32_t)s1 : 1u};
+        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(a.q), dims, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    for (int i = 0; i < 2; ++i) {
+        const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.kv.page_size, (cuuint64_t)a.kv.Hkv,
+                                    (cuuint64_t)a.kv.num_pages};
+        const cuuint64_t strides[3] = {(cuuint64_t)a.kv.token_stride * 2, (cuuint64_t)a.kv.head_stride * 2,
+                                       (cuuint64_t)a.kv.page_stride * 2};
+        const cuuint32_t box[4] = {64u, (cuuint32_t)p.page_rows, 1u, 1u};
+        if (enc(&maps[2 + i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, i == 0 ? a.kv.k : a.kv.v, dims, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    static int configured_dev[64] = {0};
+    if (ds.device < 64 && !configured_dev[ds.device]) {
+        cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, KV_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             G::SMEM);
+        if (e != cudaSuccess) return e;
+        configured_dev[ds.device] = 1;
+    }
+    const int ctas = ds.num_sms < AT_MAX_CTAS ? ds.num_sms : AT_MAX_CTAS;
+    return launch_k(attn_tc_kernel<D, KV_BF16>, dim3(ctas), dim3(AT_THREADS), G::SMEM, st, maps[0], maps[1], maps[2],
+                    maps[3], p);
+}
+
+cudaError_t launch_attn_tc(const DeviceState &ds, cudaStream_t st, const AttnArgs &a)
+{
+    return a.kv.D == 128 ? run_attn_tc<128>(ds, st, a) : run_attn_tc<64>(ds, st, a);
+}
+
+}  // namespace mx

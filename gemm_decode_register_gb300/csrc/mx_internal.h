@@ -93,6 +93,7 @@ cudaError_t launch_moe_ffn_prefill(const DeviceState &ds, cudaStream_t st, int f
 
 // Test hook of the tensor-core kernels' bounded waits (mx_debug_qmm_stall).
 void set_qmm_stall(int stall_x, unsigned long long wait_ns);
+int qmm_stall(unsigned long long *wait_ns);  // its state: whether to stall, and the limit of a wait
 
 // Limits checked on the host.
 constexpr int QMV_MAX_K = 1 << 20;

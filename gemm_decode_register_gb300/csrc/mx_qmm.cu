@@ -744,12 +744,17 @@ void set_qmm_stall(int stall_x, unsigned long long wait_ns)
     g_wait_ns.store(wait_ns);
 }
 
-static void qmm_wait_args(QmmArgs &a)
+int qmm_stall(unsigned long long *wait_ns)
 {
     const unsigned long long w = g_wait_ns.load();
-    a.wait_ns = w ? w : QMM_WAIT_NS;
+    *wait_ns = w ? w : QMM_WAIT_NS;
+    return g_stall_x.load();
+}
+
+static void qmm_wait_args(QmmArgs &a)
+{
+    a.stall_x = qmm_stall(&a.wait_ns);
     a.drain_ns = QMM_WAIT_NS;
-    a.stall_x = g_stall_x.load();
 }
 
 template <int FMT, int NACC, int MODE>

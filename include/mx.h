@@ -439,7 +439,7 @@ int mx_qmv_noalloc(int fmt, const void *codes, const void *scales, const void *x
 int mx_mma_peak(int kind, int iters, float *ms);
 
 /* Test hook for the bounded waits of the tensor-core kernels (mx_qmm,
- * mx_moe_qmm, mx_moe_ffn_prefill); the pages' fault handling (talk slide 10
+ * mx_moe_qmm, mx_moe_ffn_prefill, mx_paged_attn); the pages' fault handling (talk slide 10
  * "70 Fixes to the ROCm Fork", GPU fault handling: waits that used to block
  * forever after a fault now give up and report it).  With stall != 0, every
  * later launch of those kernels from this process issues none of its

@@ -342,3 +342,24 @@ def test_refusals():
     with pytest.raises(ValueError):
         ops.rope(torch.zeros((2, 3, 64), device="cuda", dtype=torch.float16), b.kv_len, torch.zeros((4, 32, 2)))
     assert ops.device_error() == 0
+
+
+@pytest.mark.parametrize("n,m", [([1, 1], [20000, 300]), ([300, 1], [900, 5])])
+def test_timeout_then_recovers(n, m):
+    """Queries that never come (the test hook withholds their loads): the waits give up, the outputs are NaN, and the next
+    calls (whose cut items count arrivals in the same words) are right."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    b = Batch(n, m, 8, 1, 128, 64)
+    good = b.check()[0]
+    ops.debug_qmm_stall(True, 1_000_000)
+    try:
+        out, lse = ops.paged_attn(b.kv, b.q, b.q_start, b.kv_len, return_lse=True)
+        assert ops.device_error() & 0x2
+    finally:
+        ops.debug_qmm_stall(False, 0)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+    for _ in range(2):
+        assert torch.equal(ops.paged_attn(b.kv, b.q, b.q_start, b.kv_len), good)
+    assert ops.device_error() == 0
