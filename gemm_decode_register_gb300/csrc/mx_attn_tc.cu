@@ -31,30 +31,48 @@
 //   warps 0-3, 4-7  softmax groups and epilogue
 //   warp 8          TMA producer (queries, keys, values)
 //   warp 9          MMA issuer
+//   warps 10-15     MXFP8 cache only: decoders.  The codes and scales of a tile
+//                   land in a ring of their own and are decoded exactly to the
+//                   bf16 tiles that the MMAs read, as in the prefill GEMM.
+//                   (bf16 cache: warps 10 and 11 only fill up the warpgroup.)
 //
 // Every wait is bounded as in the GEMMs; a CTA whose wait gives up makes its
 // outputs NaN and sets MX_DEVERR_TIMEOUT.
 #include "mx_attn.cuh"
+#include "mx_decode_bf16.cuh"
 #include "mx_tc.cuh"
 
 namespace mx {
 
 constexpr int AT_ROWS = 128;  // rows of a tile
 constexpr int AT_KEYS = 128;  // keys of a tile
-constexpr int AT_THREADS = 320;
 constexpr int AT_SPLIT_KEYS = 2 * AT_KEYS;  // what an item costs beside its keys, and more than its tiles' rounding
 constexpr int AT_Q_COPIES = 4;              // up to so many tokens are loaded one by one
+constexpr int AT_RING = 4;                  // pieces the producer may run ahead by
 constexpr float AT_RAISE = 8.0f;            // log2 by which scores may outgrow the maximum before it is raised
 constexpr unsigned long long AT_WAIT_NS = 2000000000ull;
 
-template <int D>
+template <int D, int KVF>
 struct AtGeo {
+    static constexpr bool MX8 = KVF == KV_MXFP8;
+    static constexpr int THREADS = MX8 ? 512 : 384;
+    // registers: what the launch gives each thread, shared out again between
+    // the softmax warps and the others (2 x 4 and 1 or 2 x 4 warps)
+    static constexpr int R_SOFTMAX = MX8 ? 184 : 208, R_OTHER = MX8 ? 72 : 88;
+    static_assert(2 * R_SOFTMAX + (MX8 ? 2 : 1) * R_OTHER <= (MX8 ? 4 * 128 : 3 * 168), "register split");
     static constexpr int SLABS = D / 64;                    // 128-byte swizzled slabs of 64 dimensions
     static constexpr int SLAB = 128 * 128;                  // bytes of a slab: 128 rows x 128 bytes
-    static constexpr int TILE = SLABS * SLAB;               // bytes of a row tile or a key tile
-    static constexpr int SLOTS = D == 128 ? 5 : 11;         // key/value tiles in flight
+    static constexpr int TILE = SLABS * SLAB;               // bytes of a row tile or a bf16 key tile
+    static constexpr int SLOTS = MX8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 11);  // bf16 key/value tiles
+    // MXFP8: ring of packed tiles, codes [128][D] then scales [128][D / 32]
+    static constexpr int CODES = 128 * D, SCALES = 128 * (D / 32);
+    static constexpr int C_SLOTS = MX8 ? (D == 128 ? 3 : 8) : 1;
+    static constexpr int DECODERS = 6;                      // warps
+    static constexpr int UNITS = 4 * D / 32;                // warp-sized parts of a tile's decode
     static constexpr int OFF_KV = 2 * TILE;                 // after two row tiles
-    static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
+    static constexpr int OFF_C = OFF_KV + SLOTS * TILE;
+    static constexpr int OFF_SC = OFF_C + (MX8 ? C_SLOTS * CODES : 0);
+    static constexpr int OFF_BAR = OFF_SC + (MX8 ? C_SLOTS * SCALES : 0);
     static constexpr int CTRL = 3072;                       // control block
     static constexpr int SMEM = OFF_BAR + CTRL;
     // tensor memory columns
@@ -154,11 +172,12 @@ struct Piece {
     int lo, hi;         // keys any of its rows may see
     int tile0;          // key tile lo lies in
     int k0, k1, tiles;  // this piece's tiles, relative to tile0, and the item's
-    bool rows;          // two row tiles (else alternate key tiles)
+    int rows;           // two row tiles (else alternate key tiles)
     int c0, c1;         // CTAs the item is cut across
+    int end;            // no piece: the stretch is done
 };
 
-// Walks a CTA's pieces; every role runs its own.
+// Walks a CTA's pieces.
 struct Walk {
     const AttnArgs &a;
     const Stretch &st;
@@ -290,6 +309,28 @@ __device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, long l
 }
 
 // ------------------------------------------------------------ tensor ops
+
+// mbar_wait without a call: ptxas (13.0) cannot allocate the softmax warps'
+// registers past the launch's count across the call of its slow path.
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                        unsigned long long limit_ns, bool respect_abort = true)
+{
+    unsigned long long t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 63u) == 0u) {
+            if (respect_abort && *abort_flag) return false;
+            const unsigned long long t = globaltimer();
+            if (t0 == 0) {
+                t0 = t;
+            } else if (t - t0 > limit_ns) {
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+    return true;
+}
 
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc)
 {
@@ -423,6 +464,20 @@ __device__ __forceinline__ void group_sync(int id, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// A barrier of the threads that also tells whether all came with `ok`.
+__device__ __forceinline__ bool vote(int id, int threads, bool ok)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.b32 p, %1, 0;\n\t"
+                 "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)ok), "r"(id), "r"(threads)
+                 : "memory");
+    return r != 0;
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar)
 {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
@@ -440,14 +495,24 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
                  : "memory");
 }
 
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 // ------------------------------------------------------------ kernel
 
 // Shared control block, after the tiles.
 struct AtCtrl {
-    uint64_t full[12], empty[12];    // key/value slots
+    uint64_t full[12], empty[12];    // bf16 key/value slots
+    uint64_t c_full[8], c_empty[8];  // packed slots (MXFP8)
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t done;
+    uint64_t r_full[AT_RING], r_free[AT_RING];
+    Piece ring[AT_RING];             // pieces, from the producer to the other roles
     long long scratch[16];
     Stretch stretch;
     uint32_t tmem;
@@ -456,7 +521,7 @@ struct AtCtrl {
     int last[2];
     float m[2][AT_ROWS], l[2][AT_ROWS];
 };
-static_assert(sizeof(AtCtrl) <= AtGeo<128>::CTRL, "control block");
+static_assert(sizeof(AtCtrl) <= AtGeo<128, KV_BF16>::CTRL, "control block");
 
 // Load numbers within a piece of n key tiles: K tile t, V tile t.  The keys
 // run `ahead` tiles ahead: K 0 .. ahead-1, then V t, K t + ahead in turn.
@@ -509,13 +574,57 @@ __device__ __noinline__ void row_again(const AttnArgs &a, int b, int t, int h, i
     }
 }
 
+// A group's part of a cut item is written: is it the last to arrive?
+__device__ __forceinline__ bool last_of(const AtParams &p, const Piece &pc, int w, int row, volatile int *last)
+{
+    __threadfence();
+    group_sync(2 + w, 128);
+    if (row == 0) {
+        int *count = p.counters + 2 * pc.c0 + w;
+        const int pieces = pc.c1 - pc.c0 + 1, arrived = atomicAdd(count, 1) + 1;
+        if (arrived == pieces) *count = 0;  // ready for the next call
+        last[w] = arrived == pieces;
+        __threadfence();
+    }
+    group_sync(2 + w, 128);
+    return last[w] != 0;
+}
+
+// A CTA whose wait gave up: the outputs of its pieces from number `done` on
+// become NaN, its parts of cut items too.
+template <int D>
+__device__ __noinline__ void poison(const AtParams &p, const Stretch &st, const Cost &cost, int done, int w, int row,
+                                    volatile int *last)
+{
+    const AttnArgs &a = p.a;
+    const float nan = __uint_as_float(0x7FC00000u);
+    const int s1 = cost.s2 / 2;
+    if (row == 0) set_device_error(a.err, DEVERR_TIMEOUT);
+    Walk walk(a, st, cost);
+    Piece pc;
+    for (int i = 0; walk.next(pc); ++i) {
+        if (i < done) continue;
+        const int tok = (pc.rows ? w * s1 : 0) + row / a.g, head = pc.kvh * a.g + row % a.g;
+        const bool valid = row < s1 * a.g && tok < pc.ntok;
+        if (pc.c0 != pc.c1) {
+            float *part = partial_base<D>(p, blockIdx.x, (int)blockIdx.x == pc.c0 ? 1 : 0, w);
+            if (valid) part[2 * row] = part[2 * row + 1] = nan;
+            if (!last_of(p, pc, w, row, last)) continue;
+        }
+        if (!valid) continue;
+        const size_t r = (size_t)(pc.q0 + tok) * a.Hq + head;
+        if (a.lse) a.lse[r] = nan;
+        for (int d = pc.rows ? 0 : w * (D / 2); d < (pc.rows ? D : (w + 1) * (D / 2)); ++d) a.out[r * D + d] = 0x7FC0u;
+    }
+}
+
 template <int D, int KVF>
-__global__ void __launch_bounds__(AT_THREADS, 1)
+__global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_q1,
                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ AtParams prm)
 {
-    using G = AtGeo<D>;
+    using G = AtGeo<D, KVF>;
     extern __shared__ __align__(1024) uint8_t smem[];  // 1024: the swizzle's period
     AtCtrl &c = *reinterpret_cast<AtCtrl *>(smem + G::OFF_BAR);
     const AttnArgs &a = prm.a;
@@ -531,9 +640,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     pdl_trigger();
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::SLOTS; ++s) {
-            mbar_init(&c.full[s], 1);
+            mbar_init(&c.full[s], G::MX8 ? G::UNITS : 1);
             mbar_init(&c.empty[s], 1);
         }
+        if (G::MX8)
+            for (int s = 0; s < G::C_SLOTS; ++s) {
+                mbar_init(&c.c_full[s], 1);
+                mbar_init(&c.c_empty[s], G::UNITS);
+            }
         mbar_init(&c.q_full, 1);
         mbar_init(&c.q_empty, 1);
         for (int w = 0; w < 2; ++w) {
@@ -542,6 +656,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             mbar_init(&c.o_full[w], 1);
         }
         mbar_init(&c.done, 1);
+        for (int i = 0; i < AT_RING; ++i) {
+            mbar_init(&c.r_full[i], 1);
+            mbar_init(&c.r_free[i], 1 + 8 + (G::MX8 ? G::DECODERS : 0));  // MMA issuer, softmax and decoder warps
+        }
         c.abort_flag = 0;
         for (int i = 0; i < 8; ++i) c.missing[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -557,198 +675,20 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     const uint32_t tmem = c.tmem;
     const Stretch st = c.stretch;
     pdl_wait();
-    Walk walk(a, st, cost);
     Piece pc;
+    // the i-th piece from the ring, by a whole warp or (lanes = false) one thread
+    auto take = [&](int i, bool lanes) {
+        const bool ok = at_wait(&c.r_full[i % AT_RING], (i / AT_RING) & 1, abort_flag, prm.wait_ns);
+        if (ok) pc = c.ring[i % AT_RING];
+        if (lanes) __syncwarp();
+        if (ok && (!lanes || lane == 0)) mbar_arrive(&c.r_free[i % AT_RING]);
+        return ok;
+    };
 
-    if (warp == 8) {
-        // ---------------- producer
-        const int ppt = AT_KEYS / prm.page_rows;  // TMA copies per tile and slab
-        int load = 0, piece = 0;
-        bool go = true;
-        while (go && walk.next(pc)) {
-            if (pc.k0 >= pc.k1) continue;
-            const int32_t *table = a.kv.block_table + (size_t)pc.b * a.kv.table_stride;
-            const int ahead = pc.rows ? 1 : 2, n = pc.k1 - pc.k0;
-            if (lane == 0) c.missing[piece & 7] = 0;
-            // queries
-            int ok = 1;
-            if (lane == 0 && piece > 0) ok = mbar_wait(&c.q_empty, (piece - 1) & 1, abort_flag, prm.wait_ns);
-            if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
-            if (lane == 0 && !prm.stall) {
-                const uint32_t dst = smem_u32(smem);
-                if (pc.rows) {
-                    mbar_arrive_expect_tx(&c.q_full, 2 * G::SLABS * (uint32_t)(s1 * a.g) * 128u);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int s = 0; s < G::SLABS; ++s)
-                            tma_load_3d(dst + r * G::TILE + s * G::SLAB, &map_q, 64 * s, pc.kvh * a.g,
-                                        pc.q0 + r * s1, &c.q_full);
-                } else if (pc.ntok > AT_Q_COPIES) {
-                    // whole row tile: the rows past the item's tokens are not used
-                    mbar_arrive_expect_tx(&c.q_full, G::SLABS * (uint32_t)(s1 * a.g) * 128u);
-#pragma unroll
-                    for (int s = 0; s < G::SLABS; ++s)
-                        tma_load_3d(dst + s * G::SLAB, &map_q, 64 * s, pc.kvh * a.g, pc.q0, &c.q_full);
-                } else {
-                    mbar_arrive_expect_tx(&c.q_full, G::SLABS * (uint32_t)(pc.ntok * a.g) * 128u);
-                    for (int t = 0; t < pc.ntok; ++t)
-#pragma unroll
-                        for (int s = 0; s < G::SLABS; ++s)
-                            tma_load_3d(dst + s * G::SLAB + (uint32_t)(t * a.g) * 128u, &map_q1, 64 * s,
-                                        pc.kvh * a.g, pc.q0 + t, &c.q_full);
-                }
-            }
-            // page ids: lane i holds copy i of a window of 32 copies; the keys'
-            // window, the one before it (the values lag by up to two tiles)
-            // and the one after it (on its way)
-            const int per_win = 32 / ppt;  // tiles per window
-            auto load_ids = [&](int wn) {
-                const long long key = (long long)(pc.tile0 + wn * per_win) * AT_KEYS + lane * prm.page_rows;
-                if (key >= pc.hi || key + prm.page_rows <= pc.lo) return -1;  // not seen: no copy
-                const int id = page_of(a.kv, table, (int)key / a.kv.page_size);
-                return id < 0 ? -2 : id;  // -2: missing
-            };
-            int win = pc.k0 / per_win, id_before = -1, id_here = load_ids(win), id_after = load_ids(win + 1);
-            for (int i = 0; i < 2 * n; ++i) {
-                // the i-th load: K or V, of tile t
-                int t;
-                bool is_k;
-                if (i < min(ahead, n)) {
-                    t = i;
-                    is_k = true;
-                } else {
-                    const int r = i - min(ahead, n);
-                    // V 0, K ahead, V 1, K ahead + 1, ... then the last Vs
-                    if (r < 2 * (n - ahead)) {
-                        is_k = r & 1;
-                        t = is_k ? ahead + r / 2 : r / 2;
-                    } else {
-                        is_k = false;
-                        t = r - max(n - ahead, 0);
-                    }
-                }
-                const int tile = pc.tile0 + pc.k0 + t;
-                const int wn = (pc.k0 + t) / per_win;
-                if (wn > win) {
-                    win = wn;
-                    id_before = id_here;
-                    id_here = id_after;
-                    id_after = load_ids(win + 1);
-                }
-                const int copy = ((pc.k0 + t) % per_win) * ppt + lane / G::SLABS;
-                const int page = __shfl_sync(0xFFFFFFFFu, wn == win ? id_here : id_before, copy & 31);
-                const bool mine = lane < ppt * G::SLABS;
-                const unsigned valid = __ballot_sync(0xFFFFFFFFu, mine && page >= 0);
-                if (__any_sync(0xFFFFFFFFu, mine && page == -2) && lane == 0) c.missing[piece & 7] = 1;
-                const int s = load % G::SLOTS;
-                ok = 1;
-                if (lane == 0) {
-                    if (load >= G::SLOTS) ok = mbar_wait(&c.empty[s], ((load / G::SLOTS) - 1) & 1, abort_flag, prm.wait_ns);
-                    if (ok) mbar_arrive_expect_tx(&c.full[s], (uint32_t)__popc(valid) * prm.page_rows * 128u);
-                }
-                if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
-                    go = false;
-                    break;
-                }
-                if (mine && page >= 0) {
-                    const int j = lane / G::SLABS, sl = lane % G::SLABS;
-                    const int key = tile * AT_KEYS + j * prm.page_rows;
-                    tma_load_4d(smem_u32(smem + G::OFF_KV + s * G::TILE + sl * G::SLAB) + (uint32_t)(j * prm.page_rows) * 128u,
-                                is_k ? &map_k : &map_v, 64 * sl, key % a.kv.page_size, pc.kvh, page, &c.full[s]);
-                }
-                ++load;
-            }
-            ++piece;
-        }
-        if (*abort_flag) {
-            // copies in flight must land before the CTA may exit
-            __syncwarp();
-            if (lane == 0) {
-                for (int i = max(load - G::SLOTS, 0); i < load; ++i)
-                    mbar_wait(&c.full[i % G::SLOTS], (i / G::SLOTS) & 1, abort_flag, AT_WAIT_NS, false);
-                if (!prm.stall && piece > 0) mbar_wait(&c.q_full, (piece - 1) & 1, abort_flag, AT_WAIT_NS, false);
-                if (!prm.stall) mbar_wait(&c.q_full, piece & 1, abort_flag, 1000000ull, false);
-            }
-        }
-    } else if (warp == 9) {
-        // ---------------- MMA issuer
-        if (lane == 0) {
-            const uint32_t qs = smem_u32(smem), kvs = smem_u32(smem + G::OFF_KV);
-            constexpr uint32_t idesc_s = at_idesc<AT_KEYS>(false), idesc_o = at_idesc<D>(true);
-            int base = 0, piece = 0;
-            int np[2] = {0, 0};  // softmax steps issued by each group
-            bool go = true;
-            auto wait_slot = [&](int i) {
-                return mbar_wait(&c.full[i % G::SLOTS], (i / G::SLOTS) & 1, abort_flag, prm.wait_ns);
-            };
-            auto s_mma = [&](int w, int qtile, int i) {
-                const uint32_t kb = kvs + (uint32_t)(i % G::SLOTS) * G::TILE, qb = qs + (uint32_t)qtile * G::TILE;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (uint32_t)(kk / 4) * G::SLAB + (kk % 4) * 32;
-                    umma_ss(tmem + G::S_COL + 128 * w, sw128_desc(qb + off), sw128_desc(kb + off), idesc_s, kk > 0);
-                }
-                umma_commit(&c.s_full[w]);
-            };
-            auto o_mma = [&](int w, int i, bool first) {
-                const uint32_t vb = kvs + (uint32_t)(i % G::SLOTS) * G::TILE;
-#pragma unroll
-                for (int kk = 0; kk < AT_KEYS / 16; ++kk)
-                    umma_ts(tmem + G::O_COL + 128 * w, tmem + G::S_COL + 128 * w + 8 * kk,
-                            v_desc(vb + kk * 2048, G::SLAB), idesc_o, !(first && kk == 0));
-                umma_commit(&c.o_full[w]);
-            };
-            while (go && walk.next(pc)) {
-                if (pc.k0 >= pc.k1) continue;
-                const int n = pc.k1 - pc.k0, ahead = pc.rows ? 1 : 2;
-                if (!mbar_wait(&c.q_full, piece & 1, abort_flag, prm.wait_ns)) break;
-                tc_fence_after();
-                // the first scores of each group
-                go = wait_slot(base);
-                if (!go) break;
-                tc_fence_after();
-                s_mma(0, 0, base);
-                if (pc.rows) {
-                    s_mma(1, 1, base);
-                    umma_commit(&c.empty[base % G::SLOTS]);
-                } else {
-                    umma_commit(&c.empty[base % G::SLOTS]);
-                    if (n > 1) {
-                        go = wait_slot(base + 1);
-                        if (!go) break;
-                        tc_fence_after();
-                        s_mma(1, 0, base + 1);
-                        umma_commit(&c.empty[(base + 1) % G::SLOTS]);
-                    }
-                }
-                if (n <= ahead) umma_commit(&c.q_empty);
-                for (int t = 0; t < n && go; ++t) {
-                    const int vi = base + v_load(t, n, ahead), ki = base + k_load(t + ahead, ahead);
-                    const bool more = t + ahead < n;
-                    for (int w = pc.rows ? 0 : (t & 1); w < (pc.rows ? 2 : (t & 1) + 1); ++w) {
-                        go = mbar_wait(&c.p_full[w], np[w] & 1, abort_flag, prm.wait_ns) && wait_slot(vi);
-                        if (!go) break;
-                        ++np[w];
-                        tc_fence_after();
-                        o_mma(w, vi, pc.rows ? t == 0 : t < 2);
-                        if (!pc.rows || w == 1) umma_commit(&c.empty[vi % G::SLOTS]);
-                        if (more) {
-                            go = wait_slot(ki);
-                            if (!go) break;
-                            tc_fence_after();
-                            s_mma(w, pc.rows ? w : 0, ki);
-                            if (!pc.rows || w == 1) umma_commit(&c.empty[ki % G::SLOTS]);
-                        }
-                    }
-                    if (go && t + ahead == n - 1) umma_commit(&c.q_empty);  // the last scores are on their way
-                }
-                base += 2 * n;
-                ++piece;
-            }
-            umma_commit(&c.done);
-        }
-    } else if (warp < 8) {
+    // (setmaxnreg stands inside the roles' branches: the register allocation
+    // goes by what reaches a point)
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::R_SOFTMAX));
         // ---------------- softmax groups
         const int w = warp >> 2;            // group
         const int row = threadIdx.x & 127;  // row of the tile; also the tensor-memory lane
@@ -759,9 +699,15 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
         bool alive = true;
         // warp-uniform, as the tensor-memory instructions that follow a wait must be
         auto wait = [&](uint64_t *bar, int phase) {
-            return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1, abort_flag, prm.wait_ns)) != 0;
+            return __all_sync(0xFFFFFFFFu, at_wait(bar, phase & 1, abort_flag, prm.wait_ns)) != 0;
         };
-        while (walk.next(pc)) {
+        for (int np = 0;; ++np) {
+            alive = __all_sync(0xFFFFFFFFu, take(np, true));
+            if (!alive || pc.end) {  // an empty piece, to the vote below
+                pc.k0 = pc.k1 = pc.ntok = 0;
+                pc.rows = 1;
+                pc.c0 = pc.c1 = 0;
+            }
             const int n = pc.k1 - pc.k0, ahead = pc.rows ? 1 : 2;
             const int tok = (pc.rows ? w * s1 : 0) + row / a.g, head = pc.kvh * a.g + row % a.g;
             const bool valid = row < s1 * a.g && tok < pc.ntok;
@@ -874,19 +820,25 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             }
             // the last product must be in before O is read
             if (mine > 0 && alive) alive = wait(&c.o_full[w], steps - 1);
+            if (!pc.rows) {
+                c.m[w][row] = m;
+                c.l[w][row] = l;
+            }
+            tc_fence_before();
+            // both groups go on only together: one that gave up does not come to their barriers any more
+            if (!vote(1, 256, alive)) {
+                poison<D>(prm, st, cost, np, w, row, c.last);
+                break;
+            }
+            if (pc.end) break;
             tc_fence_after();
-            const bool bad = !alive || (n > 0 && c.missing[piece & 7] != 0);
-            if (bad && row == 0) set_device_error(a.err, alive ? DEVERR_BAD_PAGE : DEVERR_TIMEOUT);
+            const bool bad = n > 0 && c.missing[piece & 7] != 0;
+            if (bad && row == 0) set_device_error(a.err, DEVERR_BAD_PAGE);
             // rows: the group's own rows, all dimensions.  keys: both groups'
             // sums of the same rows; group w takes half of the dimensions.
             int d0 = 0, d1 = D;
             float f_own = 1.0f, f_other = 0.0f;
             if (!pc.rows) {
-                c.m[w][row] = m;
-                c.l[w][row] = alive ? l : __uint_as_float(0x7FC00000u);
-                tc_fence_before();
-                group_sync(1, 256);
-                tc_fence_after();
                 const float m2 = c.m[w ^ 1][row], l2 = c.l[w ^ 1][row];
                 const float top = fmaxf(m, m2);
                 if (top > -INFINITY) {
@@ -940,17 +892,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                                 po[(size_t)((d - d0) / 4 + j) * prm.part_rows + row] =
                                     make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     }
-                __threadfence();
-                group_sync(2 + w, 128);
-                if (row == 0) {
-                    int *count = prm.counters + 2 * pc.c0 + w;
-                    const int arrived = atomicAdd(count, 1) + 1;
-                    if (arrived == npieces) *count = 0;
-                    c.last[w] = arrived == npieces;
-                    __threadfence();
-                }
-                group_sync(2 + w, 128);
-                finish_here = c.last[w] != 0;
+                finish_here = last_of(prm, pc, w, row, c.last);
             }
             if (finish_here && warp_on) {
                 // the sums' maximum and total over all pieces
@@ -1046,10 +988,280 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
             base += 2 * max(n, 0);
             if (n > 0) ++piece;
         }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::R_OTHER));
+        if (warp == 8) {
+            // ---------------- producer: walks the stretch for everybody
+            Walk walk(a, st, cost);
+            const int ppt = AT_KEYS / prm.page_rows;  // TMA copies per tile and slab
+            int load = 0, piece = 0;
+            bool go = true;
+            for (int np = 0; go; ++np) {
+                const bool some = walk.next(pc);
+                pc.end = !some;
+                int ok = 1;
+                if (lane == 0) {
+                    if (np >= AT_RING) ok = at_wait(&c.r_free[np % AT_RING], ((np / AT_RING) - 1) & 1, abort_flag, prm.wait_ns);
+                    if (ok) {
+                        c.ring[np % AT_RING] = pc;
+                        mbar_arrive(&c.r_full[np % AT_RING]);
+                    }
+                }
+                if (!some || !__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+                if (pc.k0 >= pc.k1) continue;
+                const int32_t *table = a.kv.block_table + (size_t)pc.b * a.kv.table_stride;
+                const int ahead = pc.rows ? 1 : 2, n = pc.k1 - pc.k0;
+                if (lane == 0) c.missing[piece & 7] = 0;
+                // queries
+                if (lane == 0 && piece > 0) ok = at_wait(&c.q_empty, (piece - 1) & 1, abort_flag, prm.wait_ns);
+                if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+                if (lane == 0 && !prm.stall) {
+                    const uint32_t dst = smem_u32(smem);
+                    if (pc.rows) {
+                        mbar_arrive_expect_tx(&c.q_full, 2 * G::SLABS * (uint32_t)(s1 * a.g) * 128u);
+    #pragma unroll
+                        for (int r = 0; r < 2; ++r)
+    #pragma unroll
+                            for (int s = 0; s < G::SLABS; ++s)
+                                tma_load_3d(dst + r * G::TILE + s * G::SLAB, &map_q, 64 * s, pc.kvh * a.g,
+                                            pc.q0 + r * s1, &c.q_full);
+                    } else if (pc.ntok > AT_Q_COPIES) {
+                        // whole row tile: the rows past the item's tokens are not used
+                        mbar_arrive_expect_tx(&c.q_full, G::SLABS * (uint32_t)(s1 * a.g) * 128u);
+    #pragma unroll
+                        for (int s = 0; s < G::SLABS; ++s)
+                            tma_load_3d(dst + s * G::SLAB, &map_q, 64 * s, pc.kvh * a.g, pc.q0, &c.q_full);
+                    } else {
+                        mbar_arrive_expect_tx(&c.q_full, G::SLABS * (uint32_t)(pc.ntok * a.g) * 128u);
+                        for (int t = 0; t < pc.ntok; ++t)
+    #pragma unroll
+                            for (int s = 0; s < G::SLABS; ++s)
+                                tma_load_3d(dst + s * G::SLAB + (uint32_t)(t * a.g) * 128u, &map_q1, 64 * s,
+                                            pc.kvh * a.g, pc.q0 + t, &c.q_full);
+                    }
+                }
+                // page ids: lane i holds copy i of a window of 32 copies; the keys'
+                // window, the one before it (the values lag by up to two tiles)
+                // and the one after it (on its way)
+                const int per_win = 32 / ppt;  // tiles per window
+                auto load_ids = [&](int wn) {
+                    const long long key = (long long)(pc.tile0 + wn * per_win) * AT_KEYS + lane * prm.page_rows;
+                    if (key >= pc.hi || key + prm.page_rows <= pc.lo) return -1;  // not seen: no copy
+                    const int id = page_of(a.kv, table, (int)key / a.kv.page_size);
+                    return id < 0 ? -2 : id;  // -2: missing
+                };
+                int win = pc.k0 / per_win, id_before = -1, id_here = load_ids(win), id_after = load_ids(win + 1);
+                for (int i = 0; i < 2 * n; ++i) {
+                    // the i-th load: K or V, of tile t
+                    int t;
+                    bool is_k;
+                    if (i < min(ahead, n)) {
+                        t = i;
+                        is_k = true;
+                    } else {
+                        const int r = i - min(ahead, n);
+                        // V 0, K ahead, V 1, K ahead + 1, ... then the last Vs
+                        if (r < 2 * (n - ahead)) {
+                            is_k = r & 1;
+                            t = is_k ? ahead + r / 2 : r / 2;
+                        } else {
+                            is_k = false;
+                            t = r - max(n - ahead, 0);
+                        }
+                    }
+                    const int tile = pc.tile0 + pc.k0 + t;
+                    const int wn = (pc.k0 + t) / per_win;
+                    if (wn > win) {
+                        win = wn;
+                        id_before = id_here;
+                        id_here = id_after;
+                        id_after = load_ids(win + 1);
+                    }
+                    const int copy = ((pc.k0 + t) % per_win) * ppt + lane / (G::MX8 ? 1 : G::SLABS);
+                    const int page = __shfl_sync(0xFFFFFFFFu, wn == win ? id_here : id_before, copy & 31);
+                    // bf16: a lane per page and slab; MXFP8: a lane per page
+                    const bool mine = lane < ppt * (G::MX8 ? 1 : G::SLABS);
+                    const unsigned valid = __ballot_sync(0xFFFFFFFFu, mine && page >= 0);
+                    if (__any_sync(0xFFFFFFFFu, mine && page == -2) && lane == 0) c.missing[piece & 7] = 1;
+                    constexpr int RING = G::MX8 ? G::C_SLOTS : G::SLOTS;
+                    uint64_t *fulls = G::MX8 ? c.c_full : c.full, *empties = G::MX8 ? c.c_empty : c.empty;
+                    const int s = load % RING;
+                    ok = 1;
+                    if (lane == 0) {
+                        if (load >= RING) ok = at_wait(&empties[s], ((load / RING) - 1) & 1, abort_flag, prm.wait_ns);
+                        if (ok)
+                            mbar_arrive_expect_tx(&fulls[s], (uint32_t)__popc(valid) * prm.page_rows *
+                                                                 (G::MX8 ? (uint32_t)(D + D / 32) : 128u));
+                    }
+                    if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
+                        go = false;
+                        break;
+                    }
+                    if (mine && page >= 0) {
+                        const int j = G::MX8 ? lane : lane / G::SLABS, sl = G::MX8 ? 0 : lane % G::SLABS;
+                        const int slot = (tile * AT_KEYS + j * prm.page_rows) % a.kv.page_size;
+                        const uint32_t r0 = (uint32_t)(j * prm.page_rows);
+                        const CUtensorMap *map = is_k ? &map_k : &map_v;
+                        if constexpr (G::MX8) {
+                            tma_load_4d(smem_u32(smem + G::OFF_C + s * G::CODES) + r0 * D, map, 0, slot, pc.kvh, page, &fulls[s]);
+                            const uint8_t *sc = static_cast<const uint8_t *>(is_k ? a.kv.k_scales : a.kv.v_scales) +
+                                                page * a.kv.scale_page_stride + pc.kvh * a.kv.scale_head_stride +
+                                                (long long)slot * (D / 32);
+                            bulk_load(smem_u32(smem + G::OFF_SC + s * G::SCALES) + r0 * (D / 32), sc,
+                                      (uint32_t)prm.page_rows * (D / 32), &fulls[s]);
+                        } else {
+                            tma_load_4d(smem_u32(smem + G::OFF_KV + s * G::TILE + sl * G::SLAB) + r0 * 128u, map, 64 * sl, slot,
+                                        pc.kvh, page, &fulls[s]);
+                        }
+                    }
+                    ++load;
+                }
+                ++piece;
+            }
+            if (*abort_flag) {
+                // copies in flight must land before the CTA may exit
+                __syncwarp();
+                if (lane == 0) {
+                    constexpr int RING = G::MX8 ? G::C_SLOTS : G::SLOTS;
+                    for (int i = max(load - RING, 0); i < load; ++i)
+                        at_wait(G::MX8 ? &c.c_full[i % RING] : &c.full[i % RING], (i / RING) & 1, abort_flag, AT_WAIT_NS,
+                                  false);
+                    if (!prm.stall && piece > 0) at_wait(&c.q_full, (piece - 1) & 1, abort_flag, AT_WAIT_NS, false);
+                    if (!prm.stall) at_wait(&c.q_full, piece & 1, abort_flag, 1000000ull, false);
+                }
+            }
+        } else if (warp == 9) {
+            // ---------------- MMA issuer
+            if (lane == 0) {
+                const uint32_t qs = smem_u32(smem), kvs = smem_u32(smem + G::OFF_KV);
+                constexpr uint32_t idesc_s = at_idesc<AT_KEYS>(false), idesc_o = at_idesc<D>(true);
+                int base = 0, piece = 0;
+                int np[2] = {0, 0};  // softmax steps issued by each group
+                bool go = true;
+                auto wait_slot = [&](int i) {
+                    return at_wait(&c.full[i % G::SLOTS], (i / G::SLOTS) & 1, abort_flag, prm.wait_ns);
+                };
+                auto s_mma = [&](int w, int qtile, int i) {
+                    const uint32_t kb = kvs + (uint32_t)(i % G::SLOTS) * G::TILE, qb = qs + (uint32_t)qtile * G::TILE;
+    #pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (uint32_t)(kk / 4) * G::SLAB + (kk % 4) * 32;
+                        umma_ss(tmem + G::S_COL + 128 * w, sw128_desc(qb + off), sw128_desc(kb + off), idesc_s, kk > 0);
+                    }
+                    umma_commit(&c.s_full[w]);
+                };
+                auto o_mma = [&](int w, int i, bool first) {
+                    const uint32_t vb = kvs + (uint32_t)(i % G::SLOTS) * G::TILE;
+    #pragma unroll
+                    for (int kk = 0; kk < AT_KEYS / 16; ++kk)
+                        umma_ts(tmem + G::O_COL + 128 * w, tmem + G::S_COL + 128 * w + 8 * kk,
+                                v_desc(vb + kk * 2048, G::SLAB), idesc_o, !(first && kk == 0));
+                    umma_commit(&c.o_full[w]);
+                };
+                for (int i = 0; go && take(i, false) && !pc.end; ++i) {
+                    if (pc.k0 >= pc.k1) continue;
+                    const int n = pc.k1 - pc.k0, ahead = pc.rows ? 1 : 2;
+                    if (!at_wait(&c.q_full, piece & 1, abort_flag, prm.wait_ns)) break;
+                    tc_fence_after();
+                    // the first scores of each group
+                    go = wait_slot(base);
+                    if (!go) break;
+                    tc_fence_after();
+                    s_mma(0, 0, base);
+                    if (pc.rows) {
+                        s_mma(1, 1, base);
+                        umma_commit(&c.empty[base % G::SLOTS]);
+                    } else {
+                        umma_commit(&c.empty[base % G::SLOTS]);
+                        if (n > 1) {
+                            go = wait_slot(base + 1);
+                            if (!go) break;
+                            tc_fence_after();
+                            s_mma(1, 0, base + 1);
+                            umma_commit(&c.empty[(base + 1) % G::SLOTS]);
+                        }
+                    }
+                    if (n <= ahead) umma_commit(&c.q_empty);
+                    for (int t = 0; t < n && go; ++t) {
+                        const int vi = base + v_load(t, n, ahead), ki = base + k_load(t + ahead, ahead);
+                        const bool more = t + ahead < n;
+                        for (int w = pc.rows ? 0 : (t & 1); w < (pc.rows ? 2 : (t & 1) + 1); ++w) {
+                            go = at_wait(&c.p_full[w], np[w] & 1, abort_flag, prm.wait_ns) && wait_slot(vi);
+                            if (!go) break;
+                            ++np[w];
+                            tc_fence_after();
+                            o_mma(w, vi, pc.rows ? t == 0 : t < 2);
+                            if (!pc.rows || w == 1) umma_commit(&c.empty[vi % G::SLOTS]);
+                            if (more) {
+                                go = wait_slot(ki);
+                                if (!go) break;
+                                tc_fence_after();
+                                s_mma(w, pc.rows ? w : 0, ki);
+                                if (!pc.rows || w == 1) umma_commit(&c.empty[ki % G::SLOTS]);
+                            }
+                        }
+                        if (go && t + ahead == n - 1) umma_commit(&c.q_empty);  // the last scores are on their way
+                    }
+                    base += 2 * n;
+                    ++piece;
+                }
+                umma_commit(&c.done);
+            }
+        } else if (warp >= 10) {
+            if constexpr (G::MX8) {
+                // ---------------- decoders: unit j of tile `load` goes to warp
+                // (load * UNITS + j) % DECODERS.  A unit is 8 (D = 128) or 16 rows:
+                // a lane decodes 32 elements of one row, neighbouring lanes the two
+                // halves of a slab's row, so that the 16-byte stores of each 8
+                // lanes cover all banks.
+                const int dw = warp - 10;
+                int base = 0;
+                bool go = true;
+                for (int np = 0; go && __all_sync(0xFFFFFFFFu, take(np, true)) && !pc.end; ++np) {
+                    const int loads = 2 * (pc.k1 - pc.k0);
+                    for (int i = base; i < base + loads && go; ++i) {
+                        const int sc = i % G::C_SLOTS, sd = i % G::SLOTS;
+                        const uint8_t *codes = smem + G::OFF_C + sc * G::CODES;
+                        const uint8_t *scales = smem + G::OFF_SC + sc * G::SCALES;
+                        uint8_t *tile = smem + G::OFF_KV + sd * G::TILE;
+                        for (int j = (G::DECODERS + dw - (i * G::UNITS) % G::DECODERS) % G::DECODERS; j < G::UNITS;
+                             j += G::DECODERS) {
+                            const int half = lane & 1;
+                            const int row = D == 128 ? 8 * j + ((lane >> 1) & 7) : 16 * j + (lane >> 1);
+                            const int slab = D == 128 ? lane >> 4 : 0;
+                            const int block = 2 * slab + half;
+                            go = __all_sync(0xFFFFFFFFu, at_wait(&c.c_full[sc], (i / G::C_SLOTS) & 1, abort_flag, prm.wait_ns));
+                            if (!go) break;
+                            // the two 16-byte reads in a row-dependent order, for the banks
+                            const int f = D == 128 ? row & 1 : (row >> 1) & 1;
+                            const uint8_t *cp = codes + row * D + block * 32;
+                            const uint4 v0 = *reinterpret_cast<const uint4 *>(cp + 16 * f);
+                            const uint4 v1 = *reinterpret_cast<const uint4 *>(cp + 16 * (f ^ 1));
+                            const uint32_t e = scales[row * (D / 32) + block];
+                            const uint4 lo = f ? v1 : v0, hi = f ? v0 : v1;
+                            const uint32_t wds[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                            fence_proxy_async_smem();  // the slot may be refilled by TMA
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&c.c_empty[sc]);
+                            if (i >= G::SLOTS) {
+                                go = __all_sync(0xFFFFFFFFu, at_wait(&c.empty[sd], ((i / G::SLOTS) - 1) & 1, abort_flag,
+                                                                       prm.wait_ns));
+                                if (!go) break;
+                            }
+                            qhalf_store<FMT_MXFP8>(wds, e, tile + slab * G::SLAB + row * 128, half, row & 7);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&c.full[sd]);
+                        }
+                    }
+                    base += loads;
+                }
+            }
+        }
     }
     __syncthreads();
     if (warp == 9) {
-        if (lane == 0) mbar_wait(&c.done, 0, abort_flag, AT_WAIT_NS, false);
+        if (lane == 0) at_wait(&c.done, 0, abort_flag, AT_WAIT_NS, false);
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -1074,16 +1286,21 @@ size_t attn_tc_workspace_bytes(int T, int Hq, int Hkv, int D)
 bool attn_tc_ok(const AttnArgs &a)
 {
     const int ps = a.kv.page_size;
+    if (a.kv.D != 64 && a.kv.D != 128) return false;
     // whole copies of at least 16 rows per key tile; a maximum that is raised needs a positive scale
-    return a.kv.kv_fmt == KV_BF16 && (a.kv.D == 64 || a.kv.D == 128) &&
-           (ps % AT_KEYS == 0 || (ps >= 16 && AT_KEYS % ps == 0)) && a.scale_log2 > 0.0f &&
-           a.scale_log2 < INFINITY;
+    if (ps % AT_KEYS != 0 && (ps < 16 || AT_KEYS % ps != 0)) return false;
+    if (!(a.scale_log2 > 0.0f && a.scale_log2 < INFINITY)) return false;
+    if (a.kv.kv_fmt == KV_BF16) return true;
+    // a page's scales of one head come in one bulk copy
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.kv.k_scales) | reinterpret_cast<uintptr_t>(a.kv.v_scales);
+    return a.kv.scale_token_stride == a.kv.D / 32 && a.kv.scale_head_stride % 16 == 0 &&
+           a.kv.scale_page_stride % 16 == 0 && at % 16 == 0;
 }
 
-template <int D>
+template <int D, int KVF>
 static cudaError_t run_attn_tc(const DeviceState &ds, cudaStream_t st, const AttnArgs &a)
 {
-    using G = AtGeo<D>;
+    using G = AtGeo<D, KVF>;
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
     if (G::SMEM > ds.max_smem_optin || ds.ws_counters < 2 * AT_MAX_CTAS) return cudaErrorInvalidValue;
@@ -1109,29 +1326,33 @@ static cudaError_t run_attn_tc(const DeviceState &ds, cudaStream_t st, const Att
     for (int i = 0; i < 2; ++i) {
         const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.kv.page_size, (cuuint64_t)a.kv.Hkv,
                                     (cuuint64_t)a.kv.num_pages};
-        const cuuint64_t strides[3] = {(cuuint64_t)a.kv.token_stride * 2, (cuuint64_t)a.kv.head_stride * 2,
-                                       (cuuint64_t)a.kv.page_stride * 2};
-        const cuuint32_t box[4] = {64u, (cuuint32_t)p.page_rows, 1u, 1u};
-        if (enc(&maps[2 + i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, i == 0 ? a.kv.k : a.kv.v, dims, strides, box, one,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        const cuuint64_t e = G::MX8 ? 1 : 2;  // bytes of an element
+        const cuuint64_t strides[3] = {(cuuint64_t)a.kv.token_stride * e, (cuuint64_t)a.kv.head_stride * e,
+                                       (cuuint64_t)a.kv.page_stride * e};
+        const cuuint32_t box[4] = {G::MX8 ? (cuuint32_t)D : 64u, (cuuint32_t)p.page_rows, 1u, 1u};
+        if (enc(&maps[2 + i], G::MX8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                i == 0 ? a.kv.k : a.kv.v, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                G::MX8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
     static int configured_dev[64] = {0};
     if (ds.device < 64 && !configured_dev[ds.device]) {
-        cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, KV_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D, KVF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              G::SMEM);
         if (e != cudaSuccess) return e;
         configured_dev[ds.device] = 1;
     }
     const int ctas = ds.num_sms < AT_MAX_CTAS ? ds.num_sms : AT_MAX_CTAS;
-    return launch_k(attn_tc_kernel<D, KV_BF16>, dim3(ctas), dim3(AT_THREADS), G::SMEM, st, maps[0], maps[1], maps[2],
+    return launch_k(attn_tc_kernel<D, KVF>, dim3(ctas), dim3(G::THREADS), G::SMEM, st, maps[0], maps[1], maps[2],
                     maps[3], p);
 }
 
 cudaError_t launch_attn_tc(const DeviceState &ds, cudaStream_t st, const AttnArgs &a)
 {
-    return a.kv.D == 128 ? run_attn_tc<128>(ds, st, a) : run_attn_tc<64>(ds, st, a);
+    if (a.kv.kv_fmt == KV_MXFP8)
+        return a.kv.D == 128 ? run_attn_tc<128, KV_MXFP8>(ds, st, a) : run_attn_tc<64, KV_MXFP8>(ds, st, a);
+    return a.kv.D == 128 ? run_attn_tc<128, KV_BF16>(ds, st, a) : run_attn_tc<64, KV_BF16>(ds, st, a);
 }
 
 }  // namespace mx
