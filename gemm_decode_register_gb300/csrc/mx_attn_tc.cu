@@ -365,17 +365,31 @@ __device__ __forceinline__ constexpr uint32_t at_idesc(bool b_n_major)
            ((128u >> 4) << 24);
 }
 
-// V as operand B, N-major with 128-byte swizzle: rows of 64 dimensions (128
-// bytes), 8 keys every 1024 bytes, the next 64 dimensions a slab further.
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr, uint32_t slab_bytes)
+// Shared-memory matrix descriptors, 128-byte swizzle, the 8-row groups 1024
+// bytes apart.  Q and K are K-major (sw128_desc); V is operand B as it lies,
+// N-major: rows of 64 dimensions (128 bytes), 8 keys every 1024 bytes, the
+// next 64 dimensions `lead` bytes further.  The low word holds the address and
+// the leading offset, so that a step through a tile is an addition to it.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead)
 {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(slab_bytes >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+    return ((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
+}
+
+__device__ __forceinline__ uint64_t desc64(uint32_t lo)
+{
+    constexpr uint32_t hi = (1024 >> 4) | (1u << 14) | (2u << 29);  // stride, descriptor version, 128-byte swizzle
+    return ((uint64_t)hi << 32) | lo;
+}
+
+// One lane of the warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xFFFFFFFF;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
 }
 
 #define MX_R32(r, o)                                                                                                  \
@@ -676,12 +690,12 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     const Stretch st = c.stretch;
     pdl_wait();
     Piece pc;
-    // the i-th piece from the ring, by a whole warp or (lanes = false) one thread
-    auto take = [&](int i, bool lanes) {
+    // the i-th piece from the ring, by a whole warp
+    auto take = [&](int i) {
         const bool ok = at_wait(&c.r_full[i % AT_RING], (i / AT_RING) & 1, abort_flag, prm.wait_ns);
         if (ok) pc = c.ring[i % AT_RING];
-        if (lanes) __syncwarp();
-        if (ok && (!lanes || lane == 0)) mbar_arrive(&c.r_free[i % AT_RING]);
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&c.r_free[i % AT_RING]);
         return ok;
     };
 
@@ -702,7 +716,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             return __all_sync(0xFFFFFFFFu, at_wait(bar, phase & 1, abort_flag, prm.wait_ns)) != 0;
         };
         for (int np = 0;; ++np) {
-            alive = __all_sync(0xFFFFFFFFu, take(np, true));
+            alive = __all_sync(0xFFFFFFFFu, take(np));
             if (!alive || pc.end) {  // an empty piece, to the vote below
                 pc.k0 = pc.k1 = pc.ntok = 0;
                 pc.rows = 1;
@@ -1131,82 +1145,92 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 }
             }
         } else if (warp == 9) {
-            // ---------------- MMA issuer
-            if (lane == 0) {
-                const uint32_t qs = smem_u32(smem), kvs = smem_u32(smem + G::OFF_KV);
-                constexpr uint32_t idesc_s = at_idesc<AT_KEYS>(false), idesc_o = at_idesc<D>(true);
-                int base = 0, piece = 0;
-                int np[2] = {0, 0};  // softmax steps issued by each group
-                bool go = true;
-                auto wait_slot = [&](int i) {
-                    return at_wait(&c.full[i % G::SLOTS], (i / G::SLOTS) & 1, abort_flag, prm.wait_ns);
-                };
-                auto s_mma = [&](int w, int qtile, int i) {
-                    const uint32_t kb = kvs + (uint32_t)(i % G::SLOTS) * G::TILE, qb = qs + (uint32_t)qtile * G::TILE;
-    #pragma unroll
+            // ---------------- MMA issuer: the whole warp waits, so that what the
+            // instructions take is warp-uniform, and one elected lane issues.
+            // (One lane in a branch of its own took about 100 cycles per MMA
+            // to bring the descriptors into uniform registers, more than the
+            // 32 to 64 cycles that an MMA of this size runs.)
+            const uint32_t qs = smem_u32(smem), kvs = smem_u32(smem + G::OFF_KV);
+            const bool elected = elect_one();
+            constexpr uint32_t idesc_s = at_idesc<AT_KEYS>(false), idesc_o = at_idesc<D>(true);
+            int base = 0, piece = 0;
+            int np[2] = {0, 0};  // softmax steps issued by each group
+            bool go = true;
+            auto wait = [&](uint64_t *bar, int phase) {
+                const bool ok = __all_sync(0xFFFFFFFFu, at_wait(bar, phase & 1, abort_flag, prm.wait_ns));
+                tc_fence_after();
+                return ok;
+            };
+            auto wait_slot = [&](int i) { return wait(&c.full[i % G::SLOTS], i / G::SLOTS); };
+            auto commit = [&](uint64_t *bar) {
+                if (elected) umma_commit(bar);
+            };
+            auto s_mma = [&](int w, int qtile, int i) {
+                const uint32_t kb = desc_lo(kvs + (uint32_t)(i % G::SLOTS) * G::TILE, 16);
+                const uint32_t qb = desc_lo(qs + (uint32_t)qtile * G::TILE, 16);
+                const uint32_t d = tmem + G::S_COL + 128 * w;
+                if (elected) {
+#pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (uint32_t)(kk / 4) * G::SLAB + (kk % 4) * 32;
-                        umma_ss(tmem + G::S_COL + 128 * w, sw128_desc(qb + off), sw128_desc(kb + off), idesc_s, kk > 0);
+                        const uint32_t off = ((uint32_t)(kk / 4) * G::SLAB + (kk % 4) * 32) >> 4;
+                        umma_ss(d, desc64(qb + off), desc64(kb + off), idesc_s, kk > 0);
                     }
                     umma_commit(&c.s_full[w]);
-                };
-                auto o_mma = [&](int w, int i, bool first) {
-                    const uint32_t vb = kvs + (uint32_t)(i % G::SLOTS) * G::TILE;
-    #pragma unroll
-                    for (int kk = 0; kk < AT_KEYS / 16; ++kk)
-                        umma_ts(tmem + G::O_COL + 128 * w, tmem + G::S_COL + 128 * w + 8 * kk,
-                                v_desc(vb + kk * 2048, G::SLAB), idesc_o, !(first && kk == 0));
-                    umma_commit(&c.o_full[w]);
-                };
-                for (int i = 0; go && take(i, false) && !pc.end; ++i) {
-                    if (pc.k0 >= pc.k1) continue;
-                    const int n = pc.k1 - pc.k0, ahead = pc.rows ? 1 : 2;
-                    if (!at_wait(&c.q_full, piece & 1, abort_flag, prm.wait_ns)) break;
-                    tc_fence_after();
-                    // the first scores of each group
-                    go = wait_slot(base);
-                    if (!go) break;
-                    tc_fence_after();
-                    s_mma(0, 0, base);
-                    if (pc.rows) {
-                        s_mma(1, 1, base);
-                        umma_commit(&c.empty[base % G::SLOTS]);
-                    } else {
-                        umma_commit(&c.empty[base % G::SLOTS]);
-                        if (n > 1) {
-                            go = wait_slot(base + 1);
-                            if (!go) break;
-                            tc_fence_after();
-                            s_mma(1, 0, base + 1);
-                            umma_commit(&c.empty[(base + 1) % G::SLOTS]);
-                        }
-                    }
-                    if (n <= ahead) umma_commit(&c.q_empty);
-                    for (int t = 0; t < n && go; ++t) {
-                        const int vi = base + v_load(t, n, ahead), ki = base + k_load(t + ahead, ahead);
-                        const bool more = t + ahead < n;
-                        for (int w = pc.rows ? 0 : (t & 1); w < (pc.rows ? 2 : (t & 1) + 1); ++w) {
-                            go = at_wait(&c.p_full[w], np[w] & 1, abort_flag, prm.wait_ns) && wait_slot(vi);
-                            if (!go) break;
-                            ++np[w];
-                            tc_fence_after();
-                            o_mma(w, vi, pc.rows ? t == 0 : t < 2);
-                            if (!pc.rows || w == 1) umma_commit(&c.empty[vi % G::SLOTS]);
-                            if (more) {
-                                go = wait_slot(ki);
-                                if (!go) break;
-                                tc_fence_after();
-                                s_mma(w, pc.rows ? w : 0, ki);
-                                if (!pc.rows || w == 1) umma_commit(&c.empty[ki % G::SLOTS]);
-                            }
-                        }
-                        if (go && t + ahead == n - 1) umma_commit(&c.q_empty);  // the last scores are on their way
-                    }
-                    base += 2 * n;
-                    ++piece;
                 }
-                umma_commit(&c.done);
+            };
+            auto o_mma = [&](int w, int i, bool first) {
+                const uint32_t vb = desc_lo(kvs + (uint32_t)(i % G::SLOTS) * G::TILE, G::SLAB);
+                const uint32_t d = tmem + G::O_COL + 128 * w, at = tmem + G::S_COL + 128 * w;
+                if (elected) {
+#pragma unroll
+                    for (int kk = 0; kk < AT_KEYS / 16; ++kk)
+                        umma_ts(d, at + 8 * kk, desc64(vb + kk * (2048 >> 4)), idesc_o, !(first && kk == 0));
+                    umma_commit(&c.o_full[w]);
+                }
+            };
+            for (int i = 0; go && __all_sync(0xFFFFFFFFu, take(i)) && !pc.end; ++i) {
+                if (pc.k0 >= pc.k1) continue;
+                const int n = pc.k1 - pc.k0, ahead = pc.rows ? 1 : 2;
+                if (!wait(&c.q_full, piece)) break;
+                // the first scores of each group
+                go = wait_slot(base);
+                if (!go) break;
+                s_mma(0, 0, base);
+                if (pc.rows) {
+                    s_mma(1, 1, base);
+                    commit(&c.empty[base % G::SLOTS]);
+                } else {
+                    commit(&c.empty[base % G::SLOTS]);
+                    if (n > 1) {
+                        go = wait_slot(base + 1);
+                        if (!go) break;
+                        s_mma(1, 0, base + 1);
+                        commit(&c.empty[(base + 1) % G::SLOTS]);
+                    }
+                }
+                if (n <= ahead) commit(&c.q_empty);
+                for (int t = 0; t < n && go; ++t) {
+                    const int vi = base + v_load(t, n, ahead), ki = base + k_load(t + ahead, ahead);
+                    const bool more = t + ahead < n;
+                    for (int w = pc.rows ? 0 : (t & 1); w < (pc.rows ? 2 : (t & 1) + 1); ++w) {
+                        go = wait_slot(vi) && wait(&c.p_full[w], np[w]);
+                        if (!go) break;
+                        ++np[w];
+                        o_mma(w, vi, pc.rows ? t == 0 : t < 2);
+                        if (!pc.rows || w == 1) commit(&c.empty[vi % G::SLOTS]);
+                        if (more) {
+                            go = wait_slot(ki);
+                            if (!go) break;
+                            s_mma(w, pc.rows ? w : 0, ki);
+                            if (!pc.rows || w == 1) commit(&c.empty[ki % G::SLOTS]);
+                        }
+                    }
+                    if (go && t + ahead == n - 1) commit(&c.q_empty);  // the last scores are on their way
+                }
+                base += 2 * n;
+                ++piece;
             }
+            commit(&c.done);
         } else if (warp >= 10) {
             if constexpr (G::MX8) {
                 // ---------------- decoders: unit j of tile `load` goes to warp
@@ -1217,7 +1241,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 const int dw = warp - 10;
                 int base = 0;
                 bool go = true;
-                for (int np = 0; go && __all_sync(0xFFFFFFFFu, take(np, true)) && !pc.end; ++np) {
+                for (int np = 0; go && __all_sync(0xFFFFFFFFu, take(np)) && !pc.end; ++np) {
                     const int loads = 2 * (pc.k1 - pc.k0);
                     for (int i = base; i < base + loads && go; ++i) {
                         const int sc = i % G::C_SLOTS, sd = i % G::SLOTS;
