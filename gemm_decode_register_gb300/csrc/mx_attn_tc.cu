@@ -444,7 +444,12 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // Two fp32 in one 64-bit register.
 __device__ __forceinline__ uint64_t pack2(float a, float b)
@@ -523,7 +528,8 @@ struct AtCtrl {
     uint64_t full[12], empty[12];    // bf16 key/value slots
     uint64_t c_full[8], c_empty[8];  // packed slots (MXFP8)
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], o_full[2];
+    uint64_t p_full[2][2];           // by group, and half of the key tile
     uint64_t done;
     uint64_t r_full[AT_RING], r_free[AT_RING];
     Piece ring[AT_RING];             // pieces, from the producer to the other roles
@@ -537,7 +543,21 @@ struct AtCtrl {
 };
 static_assert(sizeof(AtCtrl) <= AtGeo<128, KV_BF16>::CTRL, "control block");
 
-// Load numbers within a piece of n key tiles: K tile t, V tile t.  The keys
+// A position in a ring of N slots and the phase of its barriers there.
+template <int N>
+struct Slot {
+    int i = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++i == N) {
+            i = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// Load number of V tile t within a piece of n key tiles.  The keys' tiles
 // run `ahead` tiles ahead: K 0 .. ahead-1, then V t, K t + ahead in turn.
 __device__ __forceinline__ int k_load(int t, int ahead) { return t < ahead ? t : 2 * t - ahead + 1; }
 __device__ __forceinline__ int v_load(int t, int n, int ahead) { return t + min(n, ahead + t); }
@@ -666,7 +686,8 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
         mbar_init(&c.q_empty, 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(&c.s_full[w], 1);
-            mbar_init(&c.p_full[w], 4);
+            mbar_init(&c.p_full[w][0], 4);
+            mbar_init(&c.p_full[w][1], 4);
             mbar_init(&c.o_full[w], 1);
         }
         mbar_init(&c.done, 1);
@@ -769,13 +790,15 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     }
                     float x[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(s[i]);
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = max3(__uint_as_float(s[3 * j]), __uint_as_float(s[3 * j + 1]), __uint_as_float(s[3 * j + 2]));
 #pragma unroll
-                    for (int i = 4; i < 128; i += 8)
+                    for (int i = 12; i < 124; i += 8)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            x[j] = i + 4 + j < 128 ? max3(x[j], __uint_as_float(s[i + j]), __uint_as_float(s[i + 4 + j]))
-                                                   : fmaxf(x[j], __uint_as_float(s[i + j]));
+                            x[j] = max3(x[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
+                    x[0] = max3(x[0], __uint_as_float(s[124]), __uint_as_float(s[125]));
+                    x[1] = max3(x[1], __uint_as_float(s[126]), __uint_as_float(s[127]));
                     const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl2;
                     // raise the maximum: at the first tile that has one, and when it is outgrown
                     const bool raise = valid && (top > m + AT_RAISE || (m == -INFINITY && top > -INFINITY));
@@ -819,6 +842,13 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                             pk[i] = f32x2_to_bf16x2(e0, e1);
                         }
                         tmem_st32(s_addr + 32 * h, pk);
+                        if (h == 0) {
+                            // the product with the first half of V starts here
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&c.p_full[w][0]);
+                        }
                     }
                     float s0, s1_, s2, s3;
                     unpack2(sum[0], s0, s1_);
@@ -826,9 +856,11 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     l += (s0 + s1_) + (s2 + s3);
                     tmem_wait_st();
                     tc_fence_before();
+                } else if (lane == 0) {
+                    mbar_arrive(&c.p_full[w][0]);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&c.p_full[w]);
+                if (lane == 0) mbar_arrive(&c.p_full[w][1]);
                 ++steps;
                 ++mine;
             }
@@ -1150,84 +1182,103 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             // (One lane in a branch of its own took about 100 cycles per MMA
             // to bring the descriptors into uniform registers, more than the
             // 32 to 64 cycles that an MMA of this size runs.)
-            const uint32_t qs = smem_u32(smem), kvs = smem_u32(smem + G::OFF_KV);
+            // What this warp does between two MMAs is on the critical path of
+            // both groups: positions in the ring are counted, not divided, and
+            // everything that is ready together is issued together.
+            const uint32_t q_lo = desc_lo(smem_u32(smem), 16);
+            const uint32_t kv_addr = smem_u32(smem + G::OFF_KV);
             const bool elected = elect_one();
             constexpr uint32_t idesc_s = at_idesc<AT_KEYS>(false), idesc_o = at_idesc<D>(true);
-            int base = 0, piece = 0;
-            int np[2] = {0, 0};  // softmax steps issued by each group
+            Slot<G::SLOTS> cur;          // next tile of the ring, in the order of the loads
+            int piece = 0;
+            uint32_t p_phase[2] = {0, 0};  // of each group's p_full
             bool go = true;
-            auto wait = [&](uint64_t *bar, int phase) {
-                const bool ok = __all_sync(0xFFFFFFFFu, at_wait(bar, phase & 1, abort_flag, prm.wait_ns));
-                tc_fence_after();
-                return ok;
+            auto wait = [&](uint64_t *bar, uint32_t phase) {
+                if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, phase))) return true;
+                return __all_sync(0xFFFFFFFFu, at_wait(bar, phase, abort_flag, prm.wait_ns)) != 0;
             };
-            auto wait_slot = [&](int i) { return wait(&c.full[i % G::SLOTS], i / G::SLOTS); };
             auto commit = [&](uint64_t *bar) {
                 if (elected) umma_commit(bar);
             };
+            // (elected lane) S of group w from row tile `qtile` and the keys in slot i
             auto s_mma = [&](int w, int qtile, int i) {
-                const uint32_t kb = desc_lo(kvs + (uint32_t)(i % G::SLOTS) * G::TILE, 16);
-                const uint32_t qb = desc_lo(qs + (uint32_t)qtile * G::TILE, 16);
+                const uint32_t kb = desc_lo(kv_addr + (uint32_t)i * G::TILE, 16);
+                const uint32_t qb = q_lo + (uint32_t)qtile * (G::TILE >> 4);
                 const uint32_t d = tmem + G::S_COL + 128 * w;
-                if (elected) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((uint32_t)(kk / 4) * G::SLAB + (kk % 4) * 32) >> 4;
-                        umma_ss(d, desc64(qb + off), desc64(kb + off), idesc_s, kk > 0);
-                    }
-                    umma_commit(&c.s_full[w]);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((uint32_t)(kk / 4) * G::SLAB + (kk % 4) * 32) >> 4;
+                    umma_ss(d, desc64(qb + off), desc64(kb + off), idesc_s, kk > 0);
                 }
+                umma_commit(&c.s_full[w]);
             };
-            auto o_mma = [&](int w, int i, bool first) {
-                const uint32_t vb = desc_lo(kvs + (uint32_t)(i % G::SLOTS) * G::TILE, G::SLAB);
+            // (elected lane) half of O of group w from its weights and the values in slot i
+            auto o_mma = [&](int w, int i, int half, bool first) {
+                const uint32_t vb = desc_lo(kv_addr + (uint32_t)i * G::TILE, G::SLAB);
                 const uint32_t d = tmem + G::O_COL + 128 * w, at = tmem + G::S_COL + 128 * w;
-                if (elected) {
 #pragma unroll
-                    for (int kk = 0; kk < AT_KEYS / 16; ++kk)
-                        umma_ts(d, at + 8 * kk, desc64(vb + kk * (2048 >> 4)), idesc_o, !(first && kk == 0));
-                    umma_commit(&c.o_full[w]);
+                for (int kk = 0; kk < AT_KEYS / 32; ++kk) {
+                    const int k = kk + half * (AT_KEYS / 32);
+                    umma_ts(d, at + 8 * k, desc64(vb + k * (2048 >> 4)), idesc_o, !(first && half == 0 && kk == 0));
                 }
             };
             for (int i = 0; go && __all_sync(0xFFFFFFFFu, take(i)) && !pc.end; ++i) {
                 if (pc.k0 >= pc.k1) continue;
                 const int n = pc.k1 - pc.k0, ahead = pc.rows ? 1 : 2;
-                if (!wait(&c.q_full, piece)) break;
                 // the first scores of each group
-                go = wait_slot(base);
+                go = wait(&c.q_full, piece & 1) && wait(&c.full[cur.i], cur.phase);
                 if (!go) break;
-                s_mma(0, 0, base);
-                if (pc.rows) {
-                    s_mma(1, 1, base);
-                    commit(&c.empty[base % G::SLOTS]);
-                } else {
-                    commit(&c.empty[base % G::SLOTS]);
-                    if (n > 1) {
-                        go = wait_slot(base + 1);
-                        if (!go) break;
-                        s_mma(1, 0, base + 1);
-                        commit(&c.empty[(base + 1) % G::SLOTS]);
+                if (elected) {
+                    s_mma(0, 0, cur.i);
+                    if (pc.rows) s_mma(1, 1, cur.i);
+                    umma_commit(&c.empty[cur.i]);
+                }
+                cur.next();
+                if (!pc.rows && n > 1) {
+                    go = wait(&c.full[cur.i], cur.phase);
+                    if (!go) break;
+                    if (elected) {
+                        s_mma(1, 0, cur.i);
+                        umma_commit(&c.empty[cur.i]);
                     }
+                    cur.next();
                 }
                 if (n <= ahead) commit(&c.q_empty);
                 for (int t = 0; t < n && go; ++t) {
-                    const int vi = base + v_load(t, n, ahead), ki = base + k_load(t + ahead, ahead);
-                    const bool more = t + ahead < n;
-                    for (int w = pc.rows ? 0 : (t & 1); w < (pc.rows ? 2 : (t & 1) + 1); ++w) {
-                        go = wait_slot(vi) && wait(&c.p_full[w], np[w]);
+                    const bool more = t + ahead < n, last = t + ahead == n - 1;
+                    const Slot<G::SLOTS> v = cur;  // V t
+                    cur.next();
+                    const Slot<G::SLOTS> k = cur;  // K t + ahead
+                    if (more) cur.next();
+                    // both tiles first, so that nothing is waited for between the
+                    // weights and the next scores
+                    go = wait(&c.full[v.i], v.phase) && (!more || wait(&c.full[k.i], k.phase));
+                    if (!go) break;
+                    const int w_end = pc.rows ? 2 : (t & 1) + 1;
+                    for (int w = pc.rows ? 0 : (t & 1); w < w_end; ++w) {
+                        go = wait(&c.p_full[w][0], p_phase[w]);
                         if (!go) break;
-                        ++np[w];
-                        o_mma(w, vi, pc.rows ? t == 0 : t < 2);
-                        if (!pc.rows || w == 1) commit(&c.empty[vi % G::SLOTS]);
-                        if (more) {
-                            go = wait_slot(ki);
-                            if (!go) break;
-                            s_mma(w, pc.rows ? w : 0, ki);
-                            if (!pc.rows || w == 1) commit(&c.empty[ki % G::SLOTS]);
+                        tc_fence_after();
+                        if (elected) o_mma(w, v.i, 0, pc.rows ? t == 0 : t < 2);
+                        go = wait(&c.p_full[w][1], p_phase[w]);
+                        if (!go) break;
+                        p_phase[w] ^= 1;
+                        tc_fence_after();
+                        if (elected) {
+                            o_mma(w, v.i, 1, false);
+                            umma_commit(&c.o_full[w]);
+                            const bool rel = w == w_end - 1;
+                            if (rel) umma_commit(&c.empty[v.i]);
+                            if (more) {
+                                s_mma(w, pc.rows ? w : 0, k.i);
+                                if (rel) {
+                                    umma_commit(&c.empty[k.i]);
+                                    if (last) umma_commit(&c.q_empty);  // the last scores are on their way
+                                }
+                            }
                         }
                     }
-                    if (go && t + ahead == n - 1) commit(&c.q_empty);  // the last scores are on their way
                 }
-                base += 2 * n;
                 ++piece;
             }
             commit(&c.done);
