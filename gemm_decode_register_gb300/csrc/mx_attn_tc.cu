@@ -48,7 +48,8 @@ constexpr int AT_ROWS = 128;  // rows of a tile
 constexpr int AT_KEYS = 128;  // keys of a tile
 constexpr int AT_SPLIT_KEYS = 2 * AT_KEYS;  // what an item costs beside its keys, and more than its tiles' rounding
 constexpr int AT_Q_COPIES = 4;              // up to so many tokens are loaded one by one
-constexpr int AT_RING = 4;                  // pieces the producer may run ahead by
+constexpr int AT_MIN_KEYS = 3 * AT_KEYS;      // shortest stretch of a CTA
+constexpr int AT_RING = 3;                  // pieces the producer may run ahead by
 constexpr float AT_RAISE = 8.0f;            // log2 by which scores may outgrow the maximum before it is raised
 constexpr unsigned long long AT_WAIT_NS = 2000000000ull;
 
@@ -75,6 +76,7 @@ struct AtGeo {
     static constexpr int OFF_BAR = OFF_SC + (MX8 ? C_SLOTS * SCALES : 0);
     static constexpr int CTRL = 3072;                       // control block
     static constexpr int SMEM = OFF_BAR + CTRL;
+    static_assert(2 * SLOTS + (MX8 ? 2 * C_SLOTS : 0) <= 28, "barriers");
     // tensor memory columns
     static constexpr int S_COL = 0, O_COL = 256;
     static_assert(SMEM <= 232448, "shared memory");
@@ -87,6 +89,7 @@ struct AtParams {
     int part_rows;      // rows a partial has room for
     int page_rows;      // rows of a TMA copy: min(page_size, 128)
     unsigned long long wait_ns;
+    int out32;          // out is 32-byte aligned
     int stall;          // test hook: load no queries
 };
 
@@ -96,7 +99,6 @@ struct AtParams {
 struct Seq {
     int q0, n, len;   // first token row, new tokens, context
     int pairs;        // items per cache head
-    int w;            // cost per key
 };
 
 __device__ __forceinline__ long long sum_range(long long a, long long s, long long lo, long long hi)
@@ -140,7 +142,7 @@ struct Cost {
     }
     __device__ __forceinline__ long long total(const Seq &q) const
     {
-        return q.pairs > 0 ? before(q, q.pairs) * heads * q.w : 0;
+        return q.pairs > 0 ? before(q, q.pairs) * heads : 0;
     }
 };
 
@@ -152,15 +154,15 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b, int s1)
     q.n = e1 - e0;
     q.len = max(__ldg(a.kv_len + b), 0);
     q.pairs = (q.n + 2 * s1 - 1) / (2 * s1);
-    q.w = q.n > s1 ? 3 : 2;
     return q;
 }
 
 // A CTA's stretch of the work, found once per launch.
 struct Stretch {
     long long total, start, end;  // cost
-    long long first_cost;         // cost before sequence `first`
-    int first, ctas;
+    long long at;                 // cost before the first item
+    int b, kvh, p;                // the first item (b = B: none)
+    int ctas;
 };
 
 // One piece: key tiles [k0, k1) of an item.
@@ -186,54 +188,37 @@ struct Walk {
     Seq q;
     int b, kvh, p;
     long long at;  // cost before the item
-    bool found;
 
     __device__ __forceinline__ Walk(const AttnArgs &args, const Stretch &stretch, const Cost &c)
-        : a(args), st(stretch), cost(c), s1(c.s2 / 2), b(stretch.first), kvh(0), p(0), at(stretch.first_cost), found(false)
+        : a(args), st(stretch), cost(c), s1(c.s2 / 2), b(stretch.b), kvh(stretch.kvh), p(stretch.p), at(stretch.at)
     {
-        if (st.start >= st.end) b = a.B;
         if (b < a.B) q = load_seq(a, b, s1);
     }
+    // The CTA whose stretch holds cost x: the last c with total c / ctas <= x,
+    // guessed in fp32 and set right exactly.
     __device__ __forceinline__ int cta_of(long long x) const
     {
-        return (int)(((x + 1) * st.ctas - 1) / st.total);
+        const long long lim = (x + 1) * st.ctas - 1;
+        int c = (int)((float)x * (float)st.ctas / (float)st.total);
+        while (st.total * c > lim) --c;
+        while (st.total * (c + 1) <= lim) ++c;
+        return c;
     }
     __device__ __forceinline__ bool next(Piece &o)
     {
-        if (!found) {
-            // the first item that ends after the stretch's start
-            found = true;
-            while (b < a.B && at + cost.total(q) <= st.start) skip_seq();
-            if (b >= a.B) return false;
-            const long long head = cost.before(q, q.pairs) * q.w;
-            const long long off = max(st.start - at, 0ll);
-            kvh = (int)(off / head);
-            at += kvh * head;
-            int x = 0, y = q.pairs - 1;  // the last p with before(p) w <= offset
-            const long long rest = max(st.start - at, 0ll);
-            while (x < y) {
-                const int m = (x + y + 1) / 2;
-                if (cost.before(q, m) * q.w <= rest) x = m;
-                else y = m - 1;
-            }
-            p = x;
-            at += cost.before(q, p) * q.w;
-        }
         for (;;) {
-            while (b < a.B && kvh >= cost.heads) {  // the sequence is done
+            while (b < a.B && (kvh >= cost.heads || q.pairs == 0)) {  // the sequence is done
                 ++b;
                 kvh = p = 0;
                 if (b < a.B) q = load_seq(a, b, s1);
-                if (b < a.B && q.pairs == 0) kvh = cost.heads;
             }
             if (b >= a.B || at >= st.end) return false;
             cost.range(q, p, o.lo, o.hi);
             o.tile0 = o.lo / AT_KEYS;
             o.tiles = o.hi > o.lo ? (o.hi + AT_KEYS - 1) / AT_KEYS - o.tile0 : 0;
-            const long long w = (long long)AT_KEYS * q.w;
-            const long long x = (st.start - at + w - 1), y = (st.end - at + w - 1);
-            o.k0 = st.start <= at ? 0 : (int)min(x / w, (long long)o.tiles);
-            o.k1 = (int)min(y / w, (long long)o.tiles);
+            // tile k begins at cost at + 128 k and is its CTA's whose stretch holds that
+            o.k0 = st.start <= at ? 0 : (int)min((st.start - at + AT_KEYS - 1) / AT_KEYS, (long long)o.tiles);
+            o.k1 = (int)min((st.end - at + AT_KEYS - 1) / AT_KEYS, (long long)o.tiles);
             o.b = b;
             o.kvh = kvh;
             o.q0 = q.q0 + p * cost.s2;
@@ -241,10 +226,13 @@ struct Walk {
             o.first = q.len - q.n + p * cost.s2;
             o.len = q.len;
             o.rows = o.ntok > s1;
-            o.c0 = cta_of(at);
-            o.c1 = o.tiles > 0 ? cta_of(at + (o.tiles - 1) * w) : o.c0;
+            o.c0 = o.c1 = 0;
+            if (o.k1 - o.k0 != o.tiles) {
+                o.c0 = cta_of(at);
+                o.c1 = cta_of(at + (o.tiles - 1ll) * AT_KEYS);
+            }
             const bool mine = o.tiles > 0 ? o.k0 < o.k1 : st.start <= at;
-            at += ((long long)(o.hi - o.lo) + AT_SPLIT_KEYS) * q.w;
+            at += (long long)(o.hi - o.lo) + AT_SPLIT_KEYS;
             if (++p >= q.pairs) {
                 p = 0;
                 ++kvh;
@@ -252,24 +240,19 @@ struct Walk {
             if (mine) return true;
         }
     }
-    __device__ __forceinline__ void skip_seq()
-    {
-        at += cost.total(q);
-        ++b;
-        if (b < a.B) q = load_seq(a, b, s1);
-    }
 };
 
-// The whole block: costs of all sequences, this CTA's stretch of them.
-// scratch: 2 words of 8 bytes per warp, and 4 more.
+// The whole block: costs of all sequences, this CTA's stretch of them and its
+// first item.  scratch: a word of 8 bytes per warp.
 __device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, long long *scratch, Stretch *out)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int SCAN = 256;
+    const int s1 = cost.s2 / 2;
     const int per = (a.B + SCAN - 1) / SCAN;
     long long sum = 0;
     if (tid < SCAN)
-        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) sum += cost.total(load_seq(a, b, cost.s2 / 2));
+        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) sum += cost.total(load_seq(a, b, s1));
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -285,25 +268,56 @@ __device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, long l
         total += scratch[w];
     }
     const long long before = pre + inc - sum;
-    // a CTA's stretch is no shorter than two tiles of the costlier kind, so
+    // a CTA's stretch is no shorter than AT_MIN_KEYS, more than a tile, so that
     // no CTA between an item's first and last is left without a tile
-    const long long most = max(1ll, total / (2 * AT_KEYS * 3));
-    const int ctas = (int)min((long long)gridDim.x, most);
+    const int ctas = (int)min((long long)gridDim.x, max(1ll, total / AT_MIN_KEYS));
     const int c = blockIdx.x;
-    const long long start = c < ctas ? total * c / ctas : total;
-    const long long end = c < ctas ? total * (c + 1) / ctas : total;
+    long long start = total, end = total;
+    if (c < ctas) {
+        if (total < (1ll << 23)) {  // the usual case: 32-bit division
+            start = (uint32_t)total * (uint32_t)c / (uint32_t)ctas;
+            end = (uint32_t)total * (uint32_t)(c + 1) / (uint32_t)ctas;
+        } else {
+            start = total * c / ctas;
+            end = total * (c + 1) / ctas;
+        }
+    }
     if (tid == 0) {
         out->total = total;
         out->start = start;
         out->end = end;
         out->ctas = ctas;
-        out->first = a.B;
-        out->first_cost = total;
+        out->b = a.B;
+    }
+    // the sequence that holds the start (its finder skips to it among its own)
+    if (start < end && tid < SCAN && sum > 0 && before <= start && start < before + sum) {
+        long long at = before;
+        int b = tid * per;
+        for (;; ++b) {
+            const long long t = cost.total(load_seq(a, b, s1));
+            if (at + t > start) break;
+            at += t;
+        }
+        scratch[12] = at;
+        scratch[13] = b;
     }
     __syncthreads();
-    if (tid < SCAN && sum > 0 && before <= start && start < before + sum) {
-        out->first = tid * per;
-        out->first_cost = before;
+    if (start >= end) return;
+    // its item that holds the start: each thread looks at some
+    const int b = (int)scratch[13];
+    const Seq q = load_seq(a, b, s1);
+    const long long head = cost.before(q, q.pairs);
+    const int items = cost.heads * q.pairs;
+    for (int i = tid; i < items; i += blockDim.x) {
+        const int kvh = i / q.pairs, p = i - kvh * q.pairs;
+        const long long at = scratch[12] + kvh * head + cost.before(q, p);
+        const long long next = scratch[12] + kvh * head + cost.before(q, p + 1);
+        if (at <= start && start < next) {
+            out->at = at;
+            out->b = b;
+            out->kvh = kvh;
+            out->p = p;
+        }
     }
     __syncthreads();
 }
@@ -525,8 +539,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 // Shared control block, after the tiles.
 struct AtCtrl {
-    uint64_t full[12], empty[12];    // bf16 key/value slots
-    uint64_t c_full[8], c_empty[8];  // packed slots (MXFP8)
+    uint64_t slot_bars[28];          // full and empty barriers of the bf16 slots, then of the packed ones (MXFP8)
     uint64_t q_full, q_empty;
     uint64_t s_full[2], o_full[2];
     uint64_t p_full[2][2];           // by group, and half of the key tile
@@ -538,7 +551,9 @@ struct AtCtrl {
     uint32_t tmem;
     int abort_flag;
     int missing[8];                  // by piece number: a page of it is missing
-    int last[2];
+    int last[2];                     // by group: its part of a cut item was the last to come
+    Piece pending[2];                // by group: a part that is written but not counted yet
+    unsigned again[2][4];            // by group: rows to compute again
     float m[2][AT_ROWS], l[2][AT_ROWS];
 };
 static_assert(sizeof(AtCtrl) <= AtGeo<128, KV_BF16>::CTRL, "control block");
@@ -608,7 +623,39 @@ __device__ __noinline__ void row_again(const AttnArgs &a, int b, int t, int h, i
     }
 }
 
-// A group's part of a cut item is written: is it the last to arrive?
+// Two sums against maxima m0 and m1 become one against the larger: the first
+// times f0 plus the second times f1.
+struct Merge {
+    float m, f0, f1;
+    __device__ __forceinline__ Merge(float m0, float m1)
+    {
+        m = fmaxf(m0, m1);
+        const bool none = m == -INFINITY;
+        f0 = none ? 0.0f : exp2_approx(m0 - m);
+        f1 = none ? 0.0f : exp2_approx(m1 - m);
+    }
+    __device__ __forceinline__ float add(float x0, float x1) const { return fmaf(x1, f1, x0 * f0); }
+};
+
+// Are all parts of a cut item but this group's in?  Then its count is ready
+// for the next call again.
+__device__ __forceinline__ bool all_others_in(const AtParams &p, const Piece &pc, int w, int row, volatile int *last)
+{
+    if (row == 0) {
+        int *count = p.counters + 2 * pc.c0 + w;
+        int v;
+        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+        last[w] = v == pc.c1 - pc.c0;
+        if (last[w]) *count = 0;
+        __threadfence();
+    }
+    group_sync(2 + w, 128);
+    const bool in = last[w] != 0;
+    group_sync(2 + w, 128);
+    return in;
+}
+
+// A group's part of a cut item is written: counts it; true if it was the last.
 __device__ __forceinline__ bool last_of(const AtParams &p, const Piece &pc, int w, int row, volatile int *last)
 {
     __threadfence();
@@ -624,11 +671,82 @@ __device__ __forceinline__ bool last_of(const AtParams &p, const Piece &pc, int 
     return last[w] != 0;
 }
 
+// Counts a group's part of a cut item; the last to come adds all parts up, in
+// their order, and writes the outputs: a thread takes four dimensions of a row,
+// neighbouring threads neighbouring rows.
+template <int D, int KVF>
+__device__ __noinline__ void arrive_cut(const AtParams &p, const Piece &piece, int w, int tid, volatile int *last,
+                                        unsigned *again)
+{
+    const Piece pc = piece;
+    if (tid < 4) again[tid] = 0u;
+    if (!last_of(p, pc, w, tid, last)) return;
+    const AttnArgs &a = p.a;
+    const int s1 = AT_ROWS / a.g;
+    const int t0 = pc.rows ? w * s1 : 0, R = min(pc.ntok - t0, s1) * a.g;
+    const int d0 = pc.rows ? 0 : w * (D / 2), W = pc.rows ? D : D / 2, parts = pc.c1 - pc.c0 + 1;
+    __threadfence();
+    for (int e = tid; e < R * (W / 4); e += 128) {
+        const int quad = e / R, row = e - quad * R;
+        const int t = pc.q0 + t0 + row / a.g, head = pc.kvh * a.g + row % a.g;
+        float m = -INFINITY, total = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) {
+            const float *pi = partial_base<D>(p, pc.c0 + i, i == 0 ? 1 : 0, w);
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pi) + row);
+            const float4 r = __ldcg(reinterpret_cast<const float4 *>(pi + 2 * p.part_rows) + (size_t)quad * p.part_rows + row);
+            if (i == 0) {
+                m = ml.x;
+                total = ml.y;
+                o = r;
+            } else {
+                const Merge mg(m, ml.x);
+                m = mg.m;
+                total = mg.add(total, ml.y);
+                o = make_float4(mg.add(o.x, r.x), mg.add(o.y, r.y), mg.add(o.z, r.z), mg.add(o.w, r.w));
+            }
+        }
+        const float sink = a.sinks ? __ldg(a.sinks + head) * 1.4426950408889634f : -INFINITY;
+        const float ref = fmaxf(m, sink), base2 = ref == -INFINITY ? 0.0f : ref;
+        const float f = m == -INFINITY ? 0.0f : exp2_approx(m - base2);
+        float den = total * f;
+        if (a.sinks) den += exp2_approx(sink - base2);
+        const float inv = den == 0.0f ? 0.0f : f / den;
+        const size_t out_row = (size_t)t * a.Hq + head;
+        if (a.lse && quad == 0 && (pc.rows || w == 0)) a.lse[out_row] = (base2 + log2f(den)) * 0.6931471805599453f;
+        const float x = fmaf(o.x, inv, 0.0f), y = fmaf(o.y, inv, 0.0f), z = fmaf(o.z, inv, 0.0f), u = fmaf(o.w, inv, 0.0f);
+        *reinterpret_cast<uint2 *>(a.out + out_row * D + d0 + 4 * quad) =
+            make_uint2(f32x2_to_bf16x2(x, y), f32x2_to_bf16x2(z, u));
+        if (x * 0.0f + y * 0.0f + z * 0.0f + u * 0.0f != 0.0f && inv == inv) atomicOr(again + row / 32, 1u << (row % 32));
+    }
+    group_sync(2 + w, 128);
+    // rows that saw a NaN or an infinity, or only multiplied one by zero
+    for (unsigned left = again[tid / 32]; left != 0; left &= left - 1) {
+        const int row = (tid & ~31) + __ffs(left) - 1;
+        const int tok = t0 + row / a.g, head = pc.kvh * a.g + row % a.g, pos = pc.first + tok;
+        const int hi = a.causal ? min(pos + 1, pc.len) : pc.len;
+        const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+        float m = -INFINITY, total = 0.0f;
+        for (int i = 0; i < parts; ++i) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(partial_base<D>(p, pc.c0 + i, i == 0 ? 1 : 0, w)) + row);
+            const Merge mg(m, ml.x);
+            m = mg.m;
+            total = mg.add(total, ml.y);
+        }
+        const float sink = a.sinks ? __ldg(a.sinks + head) * 1.4426950408889634f : -INFINITY;
+        const float ref = fmaxf(m, sink), base2 = ref == -INFINITY ? 0.0f : ref;
+        float den = m == -INFINITY ? 0.0f : total * exp2_approx(m - base2);
+        if (a.sinks) den += exp2_approx(sink - base2);
+        row_again<KVF>(a, pc.b, pc.q0 + tok, head, lo, hi, d0, d0 + W, 1.0f / den, base2);
+    }
+}
+
 // A CTA whose wait gave up: the outputs of its pieces from number `done` on
 // become NaN, its parts of cut items too.
-template <int D>
+template <int D, int KVF>
 __device__ __noinline__ void poison(const AtParams &p, const Stretch &st, const Cost &cost, int done, int w, int row,
-                                    volatile int *last)
+                                    AtCtrl &c)
 {
     const AttnArgs &a = p.a;
     const float nan = __uint_as_float(0x7FC00000u);
@@ -643,12 +761,13 @@ __device__ __noinline__ void poison(const AtParams &p, const Stretch &st, const 
         if (pc.c0 != pc.c1) {
             float *part = partial_base<D>(p, blockIdx.x, (int)blockIdx.x == pc.c0 ? 1 : 0, w);
             if (valid) part[2 * row] = part[2 * row + 1] = nan;
-            if (!last_of(p, pc, w, row, last)) continue;
+            arrive_cut<D, KVF>(p, pc, w, row, c.last, c.again[w]);
+        } else if (valid) {
+            const size_t r = (size_t)(pc.q0 + tok) * a.Hq + head;
+            if (a.lse) a.lse[r] = nan;
+            for (int d = pc.rows ? 0 : w * (D / 2); d < (pc.rows ? D : (w + 1) * (D / 2)); ++d)
+                a.out[r * D + d] = 0x7FC0u;
         }
-        if (!valid) continue;
-        const size_t r = (size_t)(pc.q0 + tok) * a.Hq + head;
-        if (a.lse) a.lse[r] = nan;
-        for (int d = pc.rows ? 0 : w * (D / 2); d < (pc.rows ? D : (w + 1) * (D / 2)); ++d) a.out[r * D + d] = 0x7FC0u;
     }
 }
 
@@ -664,6 +783,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     const AttnArgs &a = prm.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort_flag = &c.abort_flag;
+    uint64_t *full = c.slot_bars, *empty = full + G::SLOTS, *c_full = empty + G::SLOTS, *c_empty = c_full + G::C_SLOTS;
     Cost cost;
     const int s1 = AT_ROWS / a.g;
     cost.s2 = 2 * s1;
@@ -674,13 +794,13 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     pdl_trigger();
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::SLOTS; ++s) {
-            mbar_init(&c.full[s], G::MX8 ? G::UNITS : 1);
-            mbar_init(&c.empty[s], 1);
+            mbar_init(&full[s], G::MX8 ? G::UNITS : 1);
+            mbar_init(&empty[s], 1);
         }
         if (G::MX8)
             for (int s = 0; s < G::C_SLOTS; ++s) {
-                mbar_init(&c.c_full[s], 1);
-                mbar_init(&c.c_empty[s], G::UNITS);
+                mbar_init(&c_full[s], 1);
+                mbar_init(&c_empty[s], G::UNITS);
             }
         mbar_init(&c.q_full, 1);
         mbar_init(&c.q_empty, 1);
@@ -730,6 +850,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
         const uint32_t lane_base = tmem + ((uint32_t)(row & ~31) << 16);
         const uint32_t s_addr = lane_base + G::S_COL + 128 * w;
         const float sl2 = a.scale_log2;
+        bool pending = false;  // c.pending[w] waits to be counted
         int base = 0, piece = 0, steps = 0;  // steps: softmax steps of this group so far
         bool alive = true;
         // warp-uniform, as the tensor-memory instructions that follow a wait must be
@@ -764,7 +885,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 // weights are zero, their values must be finite
                 if ((key0 < pc.lo || key0 + AT_KEYS > pc.hi) && (w == 0 || !pc.rows)) {
                     const int vi = base + v_load(t, n, ahead);
-                    alive = wait(&c.full[vi % G::SLOTS], vi / G::SLOTS);
+                    alive = wait(&full[vi % G::SLOTS], vi / G::SLOTS);
                     if (!alive) break;
                     uint8_t *v = smem + G::OFF_KV + (vi % G::SLOTS) * G::TILE;
                     const int key = key0 + row;
@@ -872,11 +993,10 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             }
             tc_fence_before();
             // both groups go on only together: one that gave up does not come to their barriers any more
-            if (!vote(1, 256, alive)) {
-                poison<D>(prm, st, cost, np, w, row, c.last);
-                break;
-            }
-            if (pc.end) break;
+            const bool go_on = vote(1, 256, alive);
+            if ((!go_on || pc.end) && pending) arrive_cut<D, KVF>(prm, c.pending[w], w, row, c.last, c.again[w]);
+            if (!go_on) poison<D, KVF>(prm, st, cost, np, w, row, c);
+            if (!go_on || pc.end) break;
             tc_fence_after();
             const bool bad = n > 0 && c.missing[piece & 7] != 0;
             if (bad && row == 0) set_device_error(a.err, DEVERR_BAD_PAGE);
@@ -897,132 +1017,149 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 d0 = w * (D / 2);
                 d1 = d0 + D / 2;
             }
-            const bool own = pc.rows ? mine > 0 : (w == 0 ? n > 0 : n > 1);
-            const bool oth = pc.rows ? false : (w == 0 ? n > 1 : n > 0);
-            // 32 dimensions of the row's sums against m
-            auto read_o = [&](int d, float (&o)[32]) {
-                uint32_t u[32] = {}, v[32] = {};
-                if (own) tmem_ld32_async(lane_base + G::O_COL + 128 * w + d, u, 0);
-                if (oth) tmem_ld32_async(lane_base + G::O_COL + 128 * (w ^ 1) + d, v, 0);
+            // o: the row's sums against m, dimensions d0 .. (rows: D of them, keys: D / 2)
+            float o[D];
+            if (warp_on && n > 0) {
+                uint32_t(&u)[D] = reinterpret_cast<uint32_t(&)[D]>(o);
+                const uint32_t mine_at = lane_base + G::O_COL + 128 * w, other_at = lane_base + G::O_COL + 128 * (w ^ 1);
+                if (pc.rows) {
+#pragma unroll
+                    for (int i = 0; i < D; i += 32) tmem_ld32_async(mine_at + i, u, i);
+                } else {
+                    // (group 1 has no sums where there is one tile: its factor is zero, its O anything)
+#pragma unroll
+                    for (int i = 0; i < D / 2; i += 32) {
+                        tmem_ld32_async(mine_at + d0 + i, u, i);
+                        tmem_ld32_async(other_at + d0 + i, u, D / 2 + i);
+                    }
+                }
                 tmem_wait_ld();
-                pin32(u, 0);
-                pin32(v, 0);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float x = own ? __uint_as_float(u[j]) * f_own : 0.0f;
-                    const float y = oth ? __uint_as_float(v[j]) * f_other : 0.0f;
-                    o[j] = x + y;
-                }
-            };
-            const bool cut = pc.c0 != pc.c1;
-            int npieces = 1;
-            bool finish_here = true;
-            float *part = nullptr;
-            if (cut) {
-                npieces = pc.c1 - pc.c0 + 1;
-                const int cta = blockIdx.x;
-                part = partial_base<D>(prm, cta, cta == pc.c0 ? 1 : 0, w);
-                if (valid) {
-                    part[2 * row] = bad ? __uint_as_float(0x7FC00000u) : m;
-                    part[2 * row + 1] = bad ? __uint_as_float(0x7FC00000u) : l;
-                }
-                float4 *po = reinterpret_cast<float4 *>(part + 2 * prm.part_rows);
-                if (warp_on && !bad)
-#pragma unroll 1
-                    for (int d = d0; d < d1; d += 32) {
-                        float o[32];
-                        read_o(d, o);
-                        if (valid)
+                for (int i = 0; i < D; i += 32) pin32(u, i);
+                if (!pc.rows) {
+                    const bool one = n == 1;  // group 0 alone
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                po[(size_t)((d - d0) / 4 + j) * prm.part_rows + row] =
-                                    make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    for (int i = 0; i < D / 2; ++i) {
+                        const float x = one && w == 1 ? 0.0f : o[i] * f_own, y = one && w == 0 ? 0.0f : o[D / 2 + i] * f_other;
+                        o[i] = x + y;
                     }
-                finish_here = last_of(prm, pc, w, row, c.last);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < D; ++i) o[i] = 0.0f;
             }
-            if (finish_here && warp_on) {
-                // the sums' maximum and total over all pieces
-                float top = m, total = l;
-                bool nan = bad;
-                if (cut) {
-                    __threadfence();
-                    top = -INFINITY;
-                    total = 0.0f;
+            const bool cut = pc.c0 != pc.c1;
+            bool finish_here = !cut;
+            float m_all = m, total = l;  // over all of the item's pieces
+            if (cut) {
+                // The first CTA of an item reaches its part last, as the end of
+                // its stretch; the others' is the start of theirs.  Where the
+                // one other part is in, the first CTA adds it to its own from
+                // registers; otherwise parts go through memory, and a part that
+                // begins a stretch is counted only after the next piece, so that
+                // the wait for its stores costs nothing.
+                const bool first = (int)blockIdx.x == pc.c0;
+                const bool two = first && pc.c1 == pc.c0 + 1 && all_others_in(prm, pc, w, row, c.last);
+                if (two) {
+                    finish_here = true;
+                    const float *pi = partial_base<D>(prm, pc.c1, 0, w);
                     if (valid) {
-                        for (int i = 0; i < npieces; ++i) {
-                            const float mi = __ldcg(partial_base<D>(prm, pc.c0 + i, i == 0 ? 1 : 0, w) + 2 * row);
-                            if (mi != mi) nan = true;
-                            top = fmaxf(top, mi);
-                        }
-                        for (int i = 0; i < npieces; ++i) {
-                            const float *pi = partial_base<D>(prm, pc.c0 + i, i == 0 ? 1 : 0, w) + 2 * row;
-                            const float mi = __ldcg(pi);
-                            if (mi > -INFINITY) total = fmaf(__ldcg(pi + 1), exp2_approx(mi - top), total);
-                        }
-                    }
-                }
-                const float m_all = top;
-                float sink = -INFINITY;
-                if (a.sinks && valid) sink = __ldg(a.sinks + head) * 1.4426950408889634f;
-                const float ref = fmaxf(top, sink);
-                const float base2 = ref == -INFINITY ? 0.0f : ref;
-                float f = m_all == -INFINITY ? 0.0f : exp2_approx(m_all - base2);
-                float den = total * f;
-                if (a.sinks) den += exp2_approx(sink - base2);
-                const float inv = den == 0.0f ? 0.0f : f / den;
-                const size_t out_row = (size_t)(pc.q0 + tok) * a.Hq + head;
-                if (valid && a.lse && (pc.rows || w == 0))
-                    a.lse[out_row] = nan ? __uint_as_float(0x7FC00000u) : (base2 + log2f(den)) * 0.6931471805599453f;
-                float check = 0.0f;
-#pragma unroll 1
-                for (int d = d0; d < d1; d += 32) {
-                    float o[32];
-                    if (nan) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pi) + row);
+                        const float4 *po = reinterpret_cast<const float4 *>(pi + 2 * prm.part_rows) + row;
+                        Merge mg(m_all, ml.x);
+                        total = mg.add(total, ml.y);
+                        m_all = mg.m;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(0x7FC00000u);
-                    } else if (!cut) {
-                        read_o(d, o);  // (nan is the same for the whole group here)
-                    } else {
+                        for (int h = 0; h < 2; ++h) {
+                            if (h == 1 && !pc.rows) break;
+                            float4 r[D / 8];  // in flight together
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-                    }
-                    if (cut && valid && !nan)
-                        for (int i = 0; i < npieces; ++i) {
-                            const float *pi = partial_base<D>(prm, pc.c0 + i, i == 0 ? 1 : 0, w);
-                            const float mi = __ldcg(pi + 2 * row);
-                            const float fi = mi == -INFINITY ? 0.0f : exp2_approx(mi - m_all);
-                            const float4 *po = reinterpret_cast<const float4 *>(pi + 2 * prm.part_rows);
+                            for (int j = 0; j < D / 8; ++j) r[j] = __ldcg(po + (size_t)(h * (D / 8) + j) * prm.part_rows);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float4 r = __ldcg(po + (size_t)((d - d0) / 4 + j) * prm.part_rows + row);
-                                o[4 * j] = fmaf(r.x, fi, o[4 * j]);
-                                o[4 * j + 1] = fmaf(r.y, fi, o[4 * j + 1]);
-                                o[4 * j + 2] = fmaf(r.z, fi, o[4 * j + 2]);
-                                o[4 * j + 3] = fmaf(r.w, fi, o[4 * j + 3]);
+                            for (int j = 0; j < D / 8; ++j) {
+                                float *x = o + h * (D / 2) + 4 * j;
+                                x[0] = mg.add(x[0], r[j].x);
+                                x[1] = mg.add(x[1], r[j].y);
+                                x[2] = mg.add(x[2], r[j].z);
+                                x[3] = mg.add(x[3], r[j].w);
                             }
                         }
+                    }
+                } else {
+                    float *part = partial_base<D>(prm, blockIdx.x, first ? 1 : 0, w);
                     if (valid) {
-                        uint32_t r[16];
+                        part[2 * row] = bad ? __uint_as_float(0x7FC00000u) : m;
+                        part[2 * row + 1] = bad ? __uint_as_float(0x7FC00000u) : l;
+                        float4 *po = reinterpret_cast<float4 *>(part + 2 * prm.part_rows) + row;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float x = o[2 * j] * inv, y = o[2 * j + 1] * inv;
-                            check = fmaf(x, 0.0f, check);
-                            check = fmaf(y, 0.0f, check);
+                        for (int i = 0; i < D / 4; ++i)
+                            if (i < D / 8 || pc.rows)
+                                po[(size_t)i * prm.part_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                }
+            }
+            if (finish_here && warp_on) {
+                float sink = -INFINITY;
+                if (a.sinks && valid) sink = __ldg(a.sinks + head) * 1.4426950408889634f;
+                const float ref = fmaxf(m_all, sink);
+                const float base2 = ref == -INFINITY ? 0.0f : ref;
+                const float f = m_all == -INFINITY ? 0.0f : exp2_approx(m_all - base2);
+                float den = total * f;
+                if (a.sinks) den += exp2_approx(sink - base2);
+                float inv = den == 0.0f ? 0.0f : f / den;
+                if (bad) inv = den = __uint_as_float(0x7FC00000u);
+                const size_t out_row = (size_t)(pc.q0 + tok) * a.Hq + head;
+                uint64_t check = 0ull;
+                if (valid) {
+                    if (a.lse && (pc.rows || w == 0)) a.lse[out_row] = (base2 + log2f(den)) * 0.6931471805599453f;
+                    uint16_t *dst = a.out + out_row * D + d0;
+                    const uint64_t inv2 = pack2(inv, inv);
+#pragma unroll
+                    for (int q = 0; q < D / 16; ++q) {
+                        if (q >= D / 32 && !pc.rows) break;
+                        uint32_t r[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint64_t v = fma2(pack2(o[16 * q + 2 * j], o[16 * q + 2 * j + 1]), inv2, 0ull);
+                            check = fma2(v, 0ull, check);  // NaN once a value is not finite
+                            float x, y;
+                            unpack2(v, x, y);
                             r[j] = f32x2_to_bf16x2(x, y);
                         }
-                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * D + d);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) dst[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                        if (prm.out32) {
+                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 16 * q), "r"(r[0]),
+                                         "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                                         : "memory");
+                        } else {
+                            uint4 *d4 = reinterpret_cast<uint4 *>(dst + 16 * q);
+                            d4[0] = make_uint4(r[0], r[1], r[2], r[3]);
+                            d4[1] = make_uint4(r[4], r[5], r[6], r[7]);
+                        }
                     }
                 }
                 // rows that saw a NaN or an infinity, or only multiplied one by zero
-                unsigned again = __ballot_sync(0xFFFFFFFFu, valid && !nan && check != 0.0f);
+                float c0, c1;
+                unpack2(check, c0, c1);
+                unsigned again = __ballot_sync(0xFFFFFFFFu, valid && inv == inv && c0 + c1 != 0.0f);
                 for (; again != 0; again &= again - 1) {
                     const int src = __ffs(again) - 1;
                     row_again<KVF>(a, pc.b, __shfl_sync(0xFFFFFFFFu, pc.q0 + tok, src),
                                    __shfl_sync(0xFFFFFFFFu, head, src), __shfl_sync(0xFFFFFFFFu, rlo, src),
                                    __shfl_sync(0xFFFFFFFFu, rhi, src), d0, d1,
                                    1.0f / __shfl_sync(0xFFFFFFFFu, den, src), __shfl_sync(0xFFFFFFFFu, base2, src));
+                }
+            }
+            if (pending) {
+                arrive_cut<D, KVF>(prm, c.pending[w], w, row, c.last, c.again[w]);
+                pending = false;
+            }
+            if (cut && !finish_here) {
+                if (row == 0) c.pending[w] = pc;
+                pending = true;  // (read after the group's next barrier)
+                if ((int)blockIdx.x == pc.c0) {
+                    group_sync(2 + w, 128);
+                    arrive_cut<D, KVF>(prm, c.pending[w], w, row, c.last, c.again[w]);
+                    pending = false;
                 }
             }
             if (!pc.rows) {
@@ -1130,7 +1267,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     const unsigned valid = __ballot_sync(0xFFFFFFFFu, mine && page >= 0);
                     if (__any_sync(0xFFFFFFFFu, mine && page == -2) && lane == 0) c.missing[piece & 7] = 1;
                     constexpr int RING = G::MX8 ? G::C_SLOTS : G::SLOTS;
-                    uint64_t *fulls = G::MX8 ? c.c_full : c.full, *empties = G::MX8 ? c.c_empty : c.empty;
+                    uint64_t *fulls = G::MX8 ? c_full : full, *empties = G::MX8 ? c_empty : empty;
                     const int s = load % RING;
                     ok = 1;
                     if (lane == 0) {
@@ -1170,7 +1307,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 if (lane == 0) {
                     constexpr int RING = G::MX8 ? G::C_SLOTS : G::SLOTS;
                     for (int i = max(load - RING, 0); i < load; ++i)
-                        at_wait(G::MX8 ? &c.c_full[i % RING] : &c.full[i % RING], (i / RING) & 1, abort_flag, AT_WAIT_NS,
+                        at_wait(G::MX8 ? &c_full[i % RING] : &full[i % RING], (i / RING) & 1, abort_flag, AT_WAIT_NS,
                                   false);
                     if (!prm.stall && piece > 0) at_wait(&c.q_full, (piece - 1) & 1, abort_flag, AT_WAIT_NS, false);
                     if (!prm.stall) at_wait(&c.q_full, piece & 1, abort_flag, 1000000ull, false);
@@ -1226,20 +1363,20 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 if (pc.k0 >= pc.k1) continue;
                 const int n = pc.k1 - pc.k0, ahead = pc.rows ? 1 : 2;
                 // the first scores of each group
-                go = wait(&c.q_full, piece & 1) && wait(&c.full[cur.i], cur.phase);
+                go = wait(&c.q_full, piece & 1) && wait(&full[cur.i], cur.phase);
                 if (!go) break;
                 if (elected) {
                     s_mma(0, 0, cur.i);
                     if (pc.rows) s_mma(1, 1, cur.i);
-                    umma_commit(&c.empty[cur.i]);
+                    umma_commit(&empty[cur.i]);
                 }
                 cur.next();
                 if (!pc.rows && n > 1) {
-                    go = wait(&c.full[cur.i], cur.phase);
+                    go = wait(&full[cur.i], cur.phase);
                     if (!go) break;
                     if (elected) {
                         s_mma(1, 0, cur.i);
-                        umma_commit(&c.empty[cur.i]);
+                        umma_commit(&empty[cur.i]);
                     }
                     cur.next();
                 }
@@ -1252,7 +1389,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     if (more) cur.next();
                     // both tiles first, so that nothing is waited for between the
                     // weights and the next scores
-                    go = wait(&c.full[v.i], v.phase) && (!more || wait(&c.full[k.i], k.phase));
+                    go = wait(&full[v.i], v.phase) && (!more || wait(&full[k.i], k.phase));
                     if (!go) break;
                     const int w_end = pc.rows ? 2 : (t & 1) + 1;
                     for (int w = pc.rows ? 0 : (t & 1); w < w_end; ++w) {
@@ -1268,11 +1405,11 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                             o_mma(w, v.i, 1, false);
                             umma_commit(&c.o_full[w]);
                             const bool rel = w == w_end - 1;
-                            if (rel) umma_commit(&c.empty[v.i]);
+                            if (rel) umma_commit(&empty[v.i]);
                             if (more) {
                                 s_mma(w, pc.rows ? w : 0, k.i);
                                 if (rel) {
-                                    umma_commit(&c.empty[k.i]);
+                                    umma_commit(&empty[k.i]);
                                     if (last) umma_commit(&c.q_empty);  // the last scores are on their way
                                 }
                             }
@@ -1305,7 +1442,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                             const int row = D == 128 ? 8 * j + ((lane >> 1) & 7) : 16 * j + (lane >> 1);
                             const int slab = D == 128 ? lane >> 4 : 0;
                             const int block = 2 * slab + half;
-                            go = __all_sync(0xFFFFFFFFu, at_wait(&c.c_full[sc], (i / G::C_SLOTS) & 1, abort_flag, prm.wait_ns));
+                            go = __all_sync(0xFFFFFFFFu, at_wait(&c_full[sc], (i / G::C_SLOTS) & 1, abort_flag, prm.wait_ns));
                             if (!go) break;
                             // the two 16-byte reads in a row-dependent order, for the banks
                             const int f = D == 128 ? row & 1 : (row >> 1) & 1;
@@ -1317,16 +1454,16 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                             const uint32_t wds[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                             fence_proxy_async_smem();  // the slot may be refilled by TMA
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(&c.c_empty[sc]);
+                            if (lane == 0) mbar_arrive(&c_empty[sc]);
                             if (i >= G::SLOTS) {
-                                go = __all_sync(0xFFFFFFFFu, at_wait(&c.empty[sd], ((i / G::SLOTS) - 1) & 1, abort_flag,
+                                go = __all_sync(0xFFFFFFFFu, at_wait(&empty[sd], ((i / G::SLOTS) - 1) & 1, abort_flag,
                                                                        prm.wait_ns));
                                 if (!go) break;
                             }
                             qhalf_store<FMT_MXFP8>(wds, e, tile + slab * G::SLAB + row * 128, half, row & 7);
                             fence_proxy_async_smem();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(&c.full[sd]);
+                            if (lane == 0) mbar_arrive(&full[sd]);
                         }
                     }
                     base += loads;
@@ -1385,6 +1522,7 @@ static cudaError_t run_attn_tc(const DeviceState &ds, cudaStream_t st, const Att
     p.partials = static_cast<float *>(a.workspace);
     p.part_rows = part_rows(a.T, a.g);
     p.page_rows = a.kv.page_size < AT_KEYS ? a.kv.page_size : AT_KEYS;
+    p.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     p.stall = qmm_stall(&p.wait_ns);
     const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
     const int s1 = AT_ROWS / a.g;
