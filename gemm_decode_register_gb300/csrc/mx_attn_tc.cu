@@ -49,6 +49,7 @@ constexpr int AT_KEYS = 128;  // keys of a tile
 constexpr int AT_SPLIT_KEYS = 2 * AT_KEYS;  // what an item costs beside its keys, and more than its tiles' rounding
 constexpr int AT_Q_COPIES = 4;              // up to so many tokens are loaded one by one
 constexpr int AT_MIN_KEYS = 3 * AT_KEYS;      // shortest stretch of a CTA
+constexpr unsigned NAP_R = 50, NAP_S = 0, NAP_M = 0, NAP_P = 100, NAP_D = 50;
 constexpr int AT_RING = 3;                  // pieces the producer may run ahead by
 constexpr float AT_RAISE = 8.0f;            // log2 by which scores may outgrow the maximum before it is raised
 constexpr unsigned long long AT_WAIT_NS = 2000000000ull;
@@ -59,7 +60,7 @@ struct AtGeo {
     static constexpr int THREADS = MX8 ? 512 : 384;
     // registers: what the launch gives each thread, shared out again between
     // the softmax warps and the others (2 x 4 and 1 or 2 x 4 warps)
-    static constexpr int R_SOFTMAX = MX8 ? 184 : 208, R_OTHER = MX8 ? 72 : 88;
+    static constexpr int R_SOFTMAX = MX8 ? 168 : 208, R_OTHER = 88;
     static_assert(2 * R_SOFTMAX + (MX8 ? 2 : 1) * R_OTHER <= (MX8 ? 4 * 128 : 3 * 168), "register split");
     static constexpr int SLABS = D / 64;                    // 128-byte swizzled slabs of 64 dimensions
     static constexpr int SLAB = 128 * 128;                  // bytes of a slab: 128 rows x 128 bytes
@@ -77,6 +78,7 @@ struct AtGeo {
     static constexpr int CTRL = 3072;                       // control block
     static constexpr int SMEM = OFF_BAR + CTRL;
     static_assert(2 * SLOTS + (MX8 ? 2 * C_SLOTS : 0) <= 28, "barriers");
+    static constexpr int H0 = MX8 ? 1 : 0;                  // the half of a key tile whose weights come first
     // tensor memory columns
     static constexpr int S_COL = 0, O_COL = 256;
     static_assert(SMEM <= 232448, "shared memory");
@@ -325,14 +327,18 @@ __device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, long l
 // ------------------------------------------------------------ tensor ops
 
 // mbar_wait without a call: ptxas (13.0) cannot allocate the softmax warps'
-// registers past the launch's count across the call of its slow path.
+// registers past the launch's count across the call of its slow path.  Between
+// two polls the warp sleeps for about `nap` ns: every poll is a shared-memory
+// operation of each lane, and the polls of a dozen waiting warps slowed the
+// working ones (prompt 628 -> 582 us with naps in the producer alone).
 __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                        unsigned long long limit_ns, bool respect_abort = true)
+                                        unsigned long long limit_ns, unsigned nap, bool respect_abort = true)
 {
     unsigned long long t0 = 0;
 #pragma unroll 1
     for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-        if ((i & 63u) == 0u) {
+        if (nap) __nanosleep(nap);
+        if (__builtin_expect((i & 63u) == 0u, 0)) {
             if (respect_abort && *abort_flag) return false;
             const unsigned long long t = globaltimer();
             if (t0 == 0) {
@@ -344,6 +350,14 @@ __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, volatile
         }
     }
     return true;
+}
+
+// A wait of the whole warp, polled by all of it: a poll by one lane in a branch
+// of its own was slower still (prompt 585 -> 764 us).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                          unsigned long long limit_ns, unsigned nap)
+{
+    return __all_sync(0xFFFFFFFFu, at_wait(bar, parity, abort_flag, limit_ns, nap)) != 0;
 }
 
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc)
@@ -535,6 +549,42 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+// 32 MXFP8 elements (codes w, block scale e) to bf16: chunks 4 half .. of the
+// row's 128 bytes in a slab (chunk c at c ^ sw).  An E4M3 code's seven magnitude
+// bits, moved to the top of a bf16's mantissa and the bottom of its exponent,
+// are its value times 2^-120 (subnormal codes included); a bf16 product with
+// 2^(e - 127 + 120) then gives code * scale exactly, as long as that power and
+// the products are normal.  Scales out of that range and NaN codes take the
+// conversions through fp32.
+__device__ __noinline__ void decode32_any(const uint32_t *w, uint32_t e, uint8_t *row, int half, int sw)
+{
+    qhalf_store<FMT_MXFP8>(w, e, row, half, sw);
+}
+
+__device__ __forceinline__ void decode32(const uint32_t (&w)[8], uint32_t e, uint8_t *row, int half, int sw)
+{
+    uint32_t top = 0u;  // the largest magnitudes, two to a word: a NaN code is 0x07F0
+    uint32_t o[16];
+    const uint32_t p = (e + 120u) << 7, m = p | (p << 16);  // 2^(e - 127 + 120), exponent field e + 120
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t t = __byte_perm(w[i], 0u, j == 0 ? 0x1404 : 0x3424);  // two codes, each in the top byte of a half
+            const uint32_t mag = (t >> 4) & 0x07F007F0u;
+            top = __vmaxu2(top, mag);
+            o[2 * i + j] = bf16x2_mul(mag | (t & 0x80008000u), m);
+        }
+    }
+    // exponent field at most 254; products at least 2^-9 * 2^(e - 127) >= 2^-126
+    if (__builtin_expect(e - 10u > 124u || __vcmpgeu2(top, 0x07F007F0u) != 0u, 0)) {
+        decode32_any(w, e, row, half, sw);
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) store_chunk(row, 4 * half + c, sw, o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+}
+
 // ------------------------------------------------------------ kernel
 
 // Shared control block, after the tiles.
@@ -542,7 +592,7 @@ struct AtCtrl {
     uint64_t slot_bars[28];          // full and empty barriers of the bf16 slots, then of the packed ones (MXFP8)
     uint64_t q_full, q_empty;
     uint64_t s_full[2], o_full[2];
-    uint64_t p_full[2][2];           // by group, and half of the key tile
+    uint64_t p_full[2][2];           // by group: the first half's weights (G::H0), the second's
     uint64_t done;
     uint64_t r_full[AT_RING], r_free[AT_RING];
     Piece ring[AT_RING];             // pieces, from the producer to the other roles
@@ -794,13 +844,13 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     pdl_trigger();
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::SLOTS; ++s) {
-            mbar_init(&full[s], G::MX8 ? G::UNITS : 1);
+            mbar_init(&full[s], G::MX8 ? G::DECODERS : 1);
             mbar_init(&empty[s], 1);
         }
         if (G::MX8)
             for (int s = 0; s < G::C_SLOTS; ++s) {
                 mbar_init(&c_full[s], 1);
-                mbar_init(&c_empty[s], G::UNITS);
+                mbar_init(&c_empty[s], G::DECODERS);
             }
         mbar_init(&c.q_full, 1);
         mbar_init(&c.q_empty, 1);
@@ -833,7 +883,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     Piece pc;
     // the i-th piece from the ring, by a whole warp
     auto take = [&](int i) {
-        const bool ok = at_wait(&c.r_full[i % AT_RING], (i / AT_RING) & 1, abort_flag, prm.wait_ns);
+        const bool ok = warp_wait(&c.r_full[i % AT_RING], (i / AT_RING) & 1, abort_flag, prm.wait_ns, NAP_R);
         if (ok) pc = c.ring[i % AT_RING];
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&c.r_free[i % AT_RING]);
@@ -855,10 +905,17 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
         bool alive = true;
         // warp-uniform, as the tensor-memory instructions that follow a wait must be
         auto wait = [&](uint64_t *bar, int phase) {
-            return __all_sync(0xFFFFFFFFu, at_wait(bar, phase & 1, abort_flag, prm.wait_ns)) != 0;
+            return warp_wait(bar, phase & 1, abort_flag, prm.wait_ns, NAP_S);
         };
         for (int np = 0;; ++np) {
-            alive = __all_sync(0xFFFFFFFFu, take(np));
+            alive = take(np);
+            if (pending) {
+                // the last piece's part: its stores are on their way while the next
+                // piece's queries and first scores are
+                group_sync(2 + w, 128);
+                arrive_cut<D, KVF>(prm, c.pending[w], w, row, c.last, c.again[w]);
+                pending = false;
+            }
             if (!alive || pc.end) {  // an empty piece, to the vote below
                 pc.k0 = pc.k1 = pc.ntok = 0;
                 pc.rows = 1;
@@ -897,33 +954,61 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 }
                 if (warp_on) {
                     tc_fence_after();
-                    uint32_t s[128];
+                    const bool edge = __any_sync(0xFFFFFFFFu, key0 < rlo || key0 + AT_KEYS > rhi);
+                    // half h of the scores (32 pairs): from tensor memory, masked
+                    auto load_half = [&](int h, uint32_t(&s)[64]) {
+                        tmem_ld32_async(s_addr + 64 * h, s, 0);
+                        tmem_ld32_async(s_addr + 64 * h + 32, s, 32);
+                    };
+                    auto mask_half = [&](int h, uint32_t(&s)[64]) {
+                        pin32(s, 0);
+                        pin32(s, 32);
+                        if (__builtin_expect(edge, 0)) {
+                            const int klo = rlo - key0 - 64 * h, khi = rhi - key0 - 64 * h;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld32_async(s_addr + 32 * i, s, 32 * i);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) pin32(s, 32 * i);
-                    if (__any_sync(0xFFFFFFFFu, key0 < rlo || key0 + AT_KEYS > rhi)) {
-                        const int klo = rlo - key0, khi = rhi - key0;
-#pragma unroll
-                        for (int i = 0; i < 128; ++i)
-                            if (i < klo || i >= khi) s[i] = 0xFF800000u;
-                    }
-                    float x[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[j] = max3(__uint_as_float(s[3 * j]), __uint_as_float(s[3 * j + 1]), __uint_as_float(s[3 * j + 2]));
-#pragma unroll
-                    for (int i = 12; i < 124; i += 8)
+                            for (int i = 0; i < 64; ++i)
+                                if (i < klo || i >= khi) s[i] = 0xFF800000u;
+                        }
+                    };
+                    auto max_half = [&](const uint32_t(&s)[64]) {
+                        float x[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            x[j] = max3(x[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
-                    x[0] = max3(x[0], __uint_as_float(s[124]), __uint_as_float(s[125]));
-                    x[1] = max3(x[1], __uint_as_float(s[126]), __uint_as_float(s[127]));
-                    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl2;
-                    // raise the maximum: at the first tile that has one, and when it is outgrown
-                    const bool raise = valid && (top > m + AT_RAISE || (m == -INFINITY && top > -INFINITY));
-                    if (__any_sync(0xFFFFFFFFu, raise)) {
+                            x[j] = max3(__uint_as_float(s[3 * j]), __uint_as_float(s[3 * j + 1]), __uint_as_float(s[3 * j + 2]));
+#pragma unroll
+                        for (int i = 12; i < 60; i += 8)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                x[j] = max3(x[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
+                        return fmaxf(max3(x[0], x[1], __uint_as_float(s[60])),
+                                     max3(max3(x[2], x[3], __uint_as_float(s[61])), __uint_as_float(s[62]), __uint_as_float(s[63])));
+                    };
+                    // weights 2^(s scale - m) as bf16 pairs, and their sum
+                    const uint64_t sl22 = pack2(sl2, sl2);
+                    auto weights = [&](const uint32_t(&s)[64], uint32_t(&pk)[32]) {
+                        const float neg = m == -INFINITY ? 0.0f : -m;
+                        const uint64_t neg2 = pack2(neg, neg);
+                        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const uint64_t e2 = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sl22, neg2);
+                            float e0, e1;
+                            unpack2(e2, e0, e1);
+                            e0 = exp2_approx(e0);
+                            e1 = exp2_approx(e1);
+                            sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
+                            pk[i] = f32x2_to_bf16x2(e0, e1);
+                        }
+                        float s0, s1_, s2, s3;
+                        unpack2(sum[0], s0, s1_);
+                        unpack2(sum[1], s2, s3);
+                        return (s0 + s1_) + (s2 + s3);
+                    };
+                    // raise the maximum: at the first tile that has one, and when it is
+                    // outgrown; true if any of the warp's rows did
+                    auto raise_to = [&](float top) {
+                        const bool raise = valid && (top > m + AT_RAISE || (m == -INFINITY && top > -INFINITY));
+                        if (__builtin_expect(!__any_sync(0xFFFFFFFFu, raise), 1)) return false;
                         const float m_new = raise ? top : m;
                         const float f = m == -INFINITY ? 0.0f : exp2_approx(m - m_new);
                         m = m_new;
@@ -931,10 +1016,9 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                         if (mine > 0) {
                             // the O so far belongs to the old maximum
                             alive = wait(&c.o_full[w], steps - 1);
-                            if (!alive) break;
                             tc_fence_after();
 #pragma unroll 1
-                            for (int i = 0; i < D; i += 32) {
+                            for (int i = 0; i < D && alive; i += 32) {
                                 uint32_t o[32];
                                 tmem_ld32_async(lane_base + G::O_COL + 128 * w + i, o, 0);
                                 tmem_wait_ld();
@@ -944,39 +1028,61 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                                 tmem_st32(lane_base + G::O_COL + 128 * w + i, o);
                             }
                         }
-                    }
-                    const float neg = m == -INFINITY ? 0.0f : -m;
-                    const uint64_t sl22 = pack2(sl2, sl2), neg2 = pack2(neg, neg);
-                    uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const uint64_t e2 = fma2(pack2(__uint_as_float(s[64 * h + 2 * i]),
-                                                           __uint_as_float(s[64 * h + 2 * i + 1])), sl22, neg2);
-                            float e0, e1;
-                            unpack2(e2, e0, e1);
-                            e0 = exp2_approx(e0);
-                            e1 = exp2_approx(e1);
-                            sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
-                            pk[i] = f32x2_to_bf16x2(e0, e1);
+                        return true;
+                    };
+                    // a half's weights over its own scores; the product with that half of V starts here
+                    auto publish = [&](int h, const uint32_t(&pk)[32]) {
+                        tmem_st32(s_addr + 64 * h, pk);
+                        tmem_wait_st();
+                        tc_fence_before();
+                    };
+                    uint32_t s0[64], s1[64], pk[32];
+                    float sum;
+                    load_half(0, s0);
+                    if constexpr (G::MX8) {
+                        // registers for one half: the second half's weights come first, the
+                        // first half's scores are read twice
+                        tmem_wait_ld();
+                        mask_half(0, s0);
+                        float top = max_half(s0);
+                        load_half(1, s0);
+                        tmem_wait_ld();
+                        mask_half(1, s0);
+                        top = fmaxf(top, max_half(s0)) * sl2;
+                        raise_to(top);
+                        if (!alive) break;
+                        sum = weights(s0, pk);
+                        publish(1, pk);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c.p_full[w][0]);
+                        load_half(0, s0);
+                        tmem_wait_ld();
+                        mask_half(0, s0);
+                        sum += weights(s0, pk);
+                        publish(0, pk);
+                    } else {
+                        // the first half's weights against the maximum so far, while the
+                        // tile's maximum is found; again in the rare case that it is raised
+                        load_half(1, s1);
+                        tmem_wait_ld();
+                        mask_half(0, s0);
+                        mask_half(1, s1);
+                        const float top = fmaxf(max_half(s0), max_half(s1)) * sl2;
+                        sum = weights(s0, pk);
+                        if (__builtin_expect(raise_to(top), 0)) {
+                            if (!alive) break;
+                            load_half(0, s0);
+                            tmem_wait_ld();
+                            mask_half(0, s0);
+                            sum = weights(s0, pk);
                         }
-                        tmem_st32(s_addr + 32 * h, pk);
-                        if (h == 0) {
-                            // the product with the first half of V starts here
-                            tmem_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&c.p_full[w][0]);
-                        }
+                        publish(0, pk);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c.p_full[w][0]);
+                        sum += weights(s1, pk);
+                        publish(1, pk);
                     }
-                    float s0, s1_, s2, s3;
-                    unpack2(sum[0], s0, s1_);
-                    unpack2(sum[1], s2, s3);
-                    l += (s0 + s1_) + (s2 + s3);
-                    tmem_wait_st();
-                    tc_fence_before();
+                    l += sum;
                 } else if (lane == 0) {
                     mbar_arrive(&c.p_full[w][0]);
                 }
@@ -994,7 +1100,6 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             tc_fence_before();
             // both groups go on only together: one that gave up does not come to their barriers any more
             const bool go_on = vote(1, 256, alive);
-            if ((!go_on || pc.end) && pending) arrive_cut<D, KVF>(prm, c.pending[w], w, row, c.last, c.again[w]);
             if (!go_on) poison<D, KVF>(prm, st, cost, np, w, row, c);
             if (!go_on || pc.end) break;
             tc_fence_after();
@@ -1017,113 +1122,99 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 d0 = w * (D / 2);
                 d1 = d0 + D / 2;
             }
-            // o: the row's sums against m, dimensions d0 .. (rows: D of them, keys: D / 2)
-            float o[D];
-            if (warp_on && n > 0) {
-                uint32_t(&u)[D] = reinterpret_cast<uint32_t(&)[D]>(o);
-                const uint32_t mine_at = lane_base + G::O_COL + 128 * w, other_at = lane_base + G::O_COL + 128 * (w ^ 1);
-                if (pc.rows) {
-#pragma unroll
-                    for (int i = 0; i < D; i += 32) tmem_ld32_async(mine_at + i, u, i);
-                } else {
-                    // (group 1 has no sums where there is one tile: its factor is zero, its O anything)
-#pragma unroll
-                    for (int i = 0; i < D / 2; i += 32) {
-                        tmem_ld32_async(mine_at + d0 + i, u, i);
-                        tmem_ld32_async(other_at + d0 + i, u, D / 2 + i);
-                    }
-                }
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < D; i += 32) pin32(u, i);
-                if (!pc.rows) {
-                    const bool one = n == 1;  // group 0 alone
-#pragma unroll
-                    for (int i = 0; i < D / 2; ++i) {
-                        const float x = one && w == 1 ? 0.0f : o[i] * f_own, y = one && w == 0 ? 0.0f : o[D / 2 + i] * f_other;
-                        o[i] = x + y;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < D; ++i) o[i] = 0.0f;
-            }
             const bool cut = pc.c0 != pc.c1;
-            bool finish_here = !cut;
+            // The first CTA of a cut item reaches its part last, as the end of its
+            // stretch; the others' is the start of theirs.  Where the one other
+            // part is in, the first CTA adds it to its own from registers;
+            // otherwise parts go through memory and are counted before the next piece.
+            const bool first = (int)blockIdx.x == pc.c0;
+            const bool two = cut && first && pc.c1 == pc.c0 + 1 && all_others_in(prm, pc, w, row, c.last);
+            const bool finish_here = !cut || two;
+            float *part = nullptr;  // this group's part, or the one to add
+            if (cut) part = partial_base<D>(prm, two ? pc.c1 : (int)blockIdx.x, first && !two ? 1 : 0, w);
+            float4 *part_o = reinterpret_cast<float4 *>(part + 2 * prm.part_rows) + row;
             float m_all = m, total = l;  // over all of the item's pieces
-            if (cut) {
-                // The first CTA of an item reaches its part last, as the end of
-                // its stretch; the others' is the start of theirs.  Where the
-                // one other part is in, the first CTA adds it to its own from
-                // registers; otherwise parts go through memory, and a part that
-                // begins a stretch is counted only after the next piece, so that
-                // the wait for its stores costs nothing.
-                const bool first = (int)blockIdx.x == pc.c0;
-                const bool two = first && pc.c1 == pc.c0 + 1 && all_others_in(prm, pc, w, row, c.last);
-                if (two) {
-                    finish_here = true;
-                    const float *pi = partial_base<D>(prm, pc.c1, 0, w);
-                    if (valid) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pi) + row);
-                        const float4 *po = reinterpret_cast<const float4 *>(pi + 2 * prm.part_rows) + row;
-                        Merge mg(m_all, ml.x);
-                        total = mg.add(total, ml.y);
-                        m_all = mg.m;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (h == 1 && !pc.rows) break;
-                            float4 r[D / 8];  // in flight together
-#pragma unroll
-                            for (int j = 0; j < D / 8; ++j) r[j] = __ldcg(po + (size_t)(h * (D / 8) + j) * prm.part_rows);
-#pragma unroll
-                            for (int j = 0; j < D / 8; ++j) {
-                                float *x = o + h * (D / 2) + 4 * j;
-                                x[0] = mg.add(x[0], r[j].x);
-                                x[1] = mg.add(x[1], r[j].y);
-                                x[2] = mg.add(x[2], r[j].z);
-                                x[3] = mg.add(x[3], r[j].w);
-                            }
-                        }
-                    }
-                } else {
-                    float *part = partial_base<D>(prm, blockIdx.x, first ? 1 : 0, w);
-                    if (valid) {
-                        part[2 * row] = bad ? __uint_as_float(0x7FC00000u) : m;
-                        part[2 * row + 1] = bad ? __uint_as_float(0x7FC00000u) : l;
-                        float4 *po = reinterpret_cast<float4 *>(part + 2 * prm.part_rows) + row;
-#pragma unroll
-                        for (int i = 0; i < D / 4; ++i)
-                            if (i < D / 8 || pc.rows)
-                                po[(size_t)i * prm.part_rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    }
-                }
+            Merge mg(m, -INFINITY);
+            if (two && valid) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part) + row);
+                mg = Merge(m, ml.x);
+                total = mg.add(l, ml.y);
+                m_all = mg.m;
+            } else if (cut && valid) {
+                part[2 * row] = bad ? __uint_as_float(0x7FC00000u) : m;
+                part[2 * row + 1] = bad ? __uint_as_float(0x7FC00000u) : l;
             }
-            if (finish_here && warp_on) {
-                float sink = -INFINITY;
-                if (a.sinks && valid) sink = __ldg(a.sinks + head) * 1.4426950408889634f;
-                const float ref = fmaxf(m_all, sink);
-                const float base2 = ref == -INFINITY ? 0.0f : ref;
-                const float f = m_all == -INFINITY ? 0.0f : exp2_approx(m_all - base2);
-                float den = total * f;
-                if (a.sinks) den += exp2_approx(sink - base2);
-                float inv = den == 0.0f ? 0.0f : f / den;
-                if (bad) inv = den = __uint_as_float(0x7FC00000u);
-                const size_t out_row = (size_t)(pc.q0 + tok) * a.Hq + head;
-                uint64_t check = 0ull;
-                if (valid) {
-                    if (a.lse && (pc.rows || w == 0)) a.lse[out_row] = (base2 + log2f(den)) * 0.6931471805599453f;
-                    uint16_t *dst = a.out + out_row * D + d0;
+            float sink = -INFINITY;
+            if (a.sinks && valid) sink = __ldg(a.sinks + head) * 1.4426950408889634f;
+            const float ref = fmaxf(m_all, sink);
+            const float base2 = ref == -INFINITY ? 0.0f : ref;
+            const float f = m_all == -INFINITY ? 0.0f : exp2_approx(m_all - base2);
+            float den = total * f;
+            if (a.sinks) den += exp2_approx(sink - base2);
+            float inv = den == 0.0f ? 0.0f : f / den;
+            if (bad) inv = den = __uint_as_float(0x7FC00000u);
+            const size_t out_row = (size_t)(pc.q0 + tok) * a.Hq + head;
+            if (finish_here && valid && a.lse && (pc.rows || w == 0))
+                a.lse[out_row] = (base2 + log2f(den)) * 0.6931471805599453f;
+            uint64_t check = 0ull;
+            if (warp_on) {
+                constexpr int EC = G::MX8 ? 32 : D / 2;  // dimensions at a time, for the registers
+#pragma unroll 1
+                for (int d = d0; d < d1; d += EC) {
+                    uint32_t u[EC], v[EC];
+#pragma unroll
+                    for (int i = 0; i < EC; i += 32) tmem_ld32_async(lane_base + G::O_COL + 128 * w + d + i, u, i);
+                    if (!pc.rows) {
+#pragma unroll
+                        for (int i = 0; i < EC; i += 32) tmem_ld32_async(lane_base + G::O_COL + 128 * (w ^ 1) + d + i, v, i);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < EC; ++i) v[i] = 0u;
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < EC; i += 32) {
+                        pin32(u, i);
+                        pin32(v, i);
+                    }
+                    float o[EC];  // the row's sums against m
+                    const bool own = n > 1 || (n == 1 && (pc.rows || w == 0)), oth = !pc.rows && (n > 1 || (n == 1 && w == 1));
+#pragma unroll
+                    for (int i = 0; i < EC; ++i) {
+                        // (a group that had no tile of this piece has anything in its O)
+                        o[i] = own ? __uint_as_float(u[i]) * f_own : 0.0f;
+                        if (oth) o[i] += __uint_as_float(v[i]) * f_other;
+                    }
+                    if (!valid) continue;
+                    float4 *po = part_o + (size_t)((d - d0) / 4) * prm.part_rows;
+                    if (two) {
+                        float4 r[EC / 4];  // in flight together
+#pragma unroll
+                        for (int j = 0; j < EC / 4; ++j) r[j] = __ldcg(po + (size_t)j * prm.part_rows);
+#pragma unroll
+                        for (int j = 0; j < EC / 4; ++j) {
+                            o[4 * j] = mg.add(o[4 * j], r[j].x);
+                            o[4 * j + 1] = mg.add(o[4 * j + 1], r[j].y);
+                            o[4 * j + 2] = mg.add(o[4 * j + 2], r[j].z);
+                            o[4 * j + 3] = mg.add(o[4 * j + 3], r[j].w);
+                        }
+                    } else if (cut) {
+#pragma unroll
+                        for (int j = 0; j < EC / 4; ++j)
+                            po[(size_t)j * prm.part_rows] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        continue;
+                    }
+                    uint16_t *dst = a.out + out_row * D + d;
                     const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
-                    for (int q = 0; q < D / 16; ++q) {
-                        if (q >= D / 32 && !pc.rows) break;
+                    for (int q = 0; q < EC / 16; ++q) {
                         uint32_t r[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const uint64_t v = fma2(pack2(o[16 * q + 2 * j], o[16 * q + 2 * j + 1]), inv2, 0ull);
-                            check = fma2(v, 0ull, check);  // NaN once a value is not finite
+                            const uint64_t x2 = fma2(pack2(o[16 * q + 2 * j], o[16 * q + 2 * j + 1]), inv2, 0ull);
+                            check = fma2(x2, 0ull, check);  // NaN once a value is not finite
                             float x, y;
-                            unpack2(v, x, y);
+                            unpack2(x2, x, y);
                             r[j] = f32x2_to_bf16x2(x, y);
                         }
                         if (prm.out32) {
@@ -1137,6 +1228,8 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                         }
                     }
                 }
+            }
+            if (finish_here && warp_on) {
                 // rows that saw a NaN or an infinity, or only multiplied one by zero
                 float c0, c1;
                 unpack2(check, c0, c1);
@@ -1149,18 +1242,9 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                                    1.0f / __shfl_sync(0xFFFFFFFFu, den, src), __shfl_sync(0xFFFFFFFFu, base2, src));
                 }
             }
-            if (pending) {
-                arrive_cut<D, KVF>(prm, c.pending[w], w, row, c.last, c.again[w]);
-                pending = false;
-            }
             if (cut && !finish_here) {
                 if (row == 0) c.pending[w] = pc;
-                pending = true;  // (read after the group's next barrier)
-                if ((int)blockIdx.x == pc.c0) {
-                    group_sync(2 + w, 128);
-                    arrive_cut<D, KVF>(prm, c.pending[w], w, row, c.last, c.again[w]);
-                    pending = false;
-                }
+                pending = true;
             }
             if (!pc.rows) {
                 // the other group's O is read; it may be overwritten after this
@@ -1178,13 +1262,16 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             Walk walk(a, st, cost);
             const int ppt = AT_KEYS / prm.page_rows;  // TMA copies per tile and slab
             int load = 0, piece = 0;
+            Slot<G::MX8 ? G::C_SLOTS : G::SLOTS> slot;
+            bool fresh = true;  // the ring's first round: nothing to wait for
+            const bool elected = elect_one();
             bool go = true;
             for (int np = 0; go; ++np) {
                 const bool some = walk.next(pc);
                 pc.end = !some;
                 int ok = 1;
                 if (lane == 0) {
-                    if (np >= AT_RING) ok = at_wait(&c.r_free[np % AT_RING], ((np / AT_RING) - 1) & 1, abort_flag, prm.wait_ns);
+                    if (np >= AT_RING) ok = at_wait(&c.r_free[np % AT_RING], ((np / AT_RING) - 1) & 1, abort_flag, prm.wait_ns, NAP_P);
                     if (ok) {
                         c.ring[np % AT_RING] = pc;
                         mbar_arrive(&c.r_full[np % AT_RING]);
@@ -1196,7 +1283,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 const int ahead = pc.rows ? 1 : 2, n = pc.k1 - pc.k0;
                 if (lane == 0) c.missing[piece & 7] = 0;
                 // queries
-                if (lane == 0 && piece > 0) ok = at_wait(&c.q_empty, (piece - 1) & 1, abort_flag, prm.wait_ns);
+                if (lane == 0 && piece > 0) ok = at_wait(&c.q_empty, (piece - 1) & 1, abort_flag, prm.wait_ns, NAP_P);
                 if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
                 if (lane == 0 && !prm.stall) {
                     const uint32_t dst = smem_u32(smem);
@@ -1234,70 +1321,58 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     return id < 0 ? -2 : id;  // -2: missing
                 };
                 int win = pc.k0 / per_win, id_before = -1, id_here = load_ids(win), id_after = load_ids(win + 1);
-                for (int i = 0; i < 2 * n; ++i) {
-                    // the i-th load: K or V, of tile t
-                    int t;
-                    bool is_k;
-                    if (i < min(ahead, n)) {
-                        t = i;
-                        is_k = true;
-                    } else {
-                        const int r = i - min(ahead, n);
-                        // V 0, K ahead, V 1, K ahead + 1, ... then the last Vs
-                        if (r < 2 * (n - ahead)) {
-                            is_k = r & 1;
-                            t = is_k ? ahead + r / 2 : r / 2;
-                        } else {
-                            is_k = false;
-                            t = r - max(n - ahead, 0);
-                        }
-                    }
-                    const int tile = pc.tile0 + pc.k0 + t;
-                    const int wn = (pc.k0 + t) / per_win;
+                // One tile into the ring.  The copies are issued by one elected lane
+                // from warp-uniform values (a lane per copy took about 150 cycles
+                // for each: pages of 16 tokens ran at 3.9 TB/s instead of 6).
+                auto load_tile = [&](bool is_k, int t) {
+                    const int kt = pc.k0 + t, wn = kt / per_win;
                     if (wn > win) {
                         win = wn;
                         id_before = id_here;
                         id_here = id_after;
                         id_after = load_ids(win + 1);
                     }
-                    const int copy = ((pc.k0 + t) % per_win) * ppt + lane / (G::MX8 ? 1 : G::SLABS);
-                    const int page = __shfl_sync(0xFFFFFFFFu, wn == win ? id_here : id_before, copy & 31);
-                    // bf16: a lane per page and slab; MXFP8: a lane per page
-                    const bool mine = lane < ppt * (G::MX8 ? 1 : G::SLABS);
-                    const unsigned valid = __ballot_sync(0xFFFFFFFFu, mine && page >= 0);
-                    if (__any_sync(0xFFFFFFFFu, mine && page == -2) && lane == 0) c.missing[piece & 7] = 1;
-                    constexpr int RING = G::MX8 ? G::C_SLOTS : G::SLOTS;
-                    uint64_t *fulls = G::MX8 ? c_full : full, *empties = G::MX8 ? c_empty : empty;
-                    const int s = load % RING;
-                    ok = 1;
-                    if (lane == 0) {
-                        if (load >= RING) ok = at_wait(&empties[s], ((load / RING) - 1) & 1, abort_flag, prm.wait_ns);
-                        if (ok)
-                            mbar_arrive_expect_tx(&fulls[s], (uint32_t)__popc(valid) * prm.page_rows *
-                                                                 (G::MX8 ? (uint32_t)(D + D / 32) : 128u));
-                    }
-                    if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
-                        go = false;
-                        break;
-                    }
-                    if (mine && page >= 0) {
-                        const int j = G::MX8 ? lane : lane / G::SLABS, sl = G::MX8 ? 0 : lane % G::SLABS;
-                        const int slot = (tile * AT_KEYS + j * prm.page_rows) % a.kv.page_size;
+                    const int ids = wn == win ? id_here : id_before, first = (kt - wn * per_win) * ppt;
+                    const bool here = lane >= first && lane < first + ppt;
+                    const int copies = __popc(__ballot_sync(0xFFFFFFFFu, here && ids >= 0));
+                    if (__any_sync(0xFFFFFFFFu, here && ids == -2) && lane == 0) c.missing[piece & 7] = 1;
+                    uint64_t *bar = (G::MX8 ? c_full : full) + slot.i;
+                    if (!fresh && !warp_wait((G::MX8 ? c_empty : empty) + slot.i, slot.phase ^ 1, abort_flag, prm.wait_ns, NAP_P))
+                        return false;
+                    if (elected)
+                        mbar_arrive_expect_tx(bar, (uint32_t)(copies * prm.page_rows) *
+                                                       (G::MX8 ? (uint32_t)(D + D / 32) : 128u * G::SLABS));
+                    const CUtensorMap *map = is_k ? &map_k : &map_v;
+                    int row = (int)((unsigned)((pc.tile0 + kt) * AT_KEYS) % (unsigned)a.kv.page_size);  // 0 in pages of up to a tile
+                    for (int j = 0; j < ppt; ++j) {
+                        const int page = __shfl_sync(0xFFFFFFFFu, ids, first + j);
+                        if (page < 0 || !elected) continue;
                         const uint32_t r0 = (uint32_t)(j * prm.page_rows);
-                        const CUtensorMap *map = is_k ? &map_k : &map_v;
                         if constexpr (G::MX8) {
-                            tma_load_4d(smem_u32(smem + G::OFF_C + s * G::CODES) + r0 * D, map, 0, slot, pc.kvh, page, &fulls[s]);
+                            tma_load_4d(smem_u32(smem + G::OFF_C + slot.i * G::CODES) + r0 * D, map, 0, row, pc.kvh, page, bar);
                             const uint8_t *sc = static_cast<const uint8_t *>(is_k ? a.kv.k_scales : a.kv.v_scales) +
                                                 page * a.kv.scale_page_stride + pc.kvh * a.kv.scale_head_stride +
-                                                (long long)slot * (D / 32);
-                            bulk_load(smem_u32(smem + G::OFF_SC + s * G::SCALES) + r0 * (D / 32), sc,
-                                      (uint32_t)prm.page_rows * (D / 32), &fulls[s]);
+                                                (long long)row * (D / 32);
+                            bulk_load(smem_u32(smem + G::OFF_SC + slot.i * G::SCALES) + r0 * (D / 32), sc,
+                                      (uint32_t)prm.page_rows * (D / 32), bar);
                         } else {
-                            tma_load_4d(smem_u32(smem + G::OFF_KV + s * G::TILE + sl * G::SLAB) + r0 * 128u, map, 64 * sl, slot,
-                                        pc.kvh, page, &fulls[s]);
+#pragma unroll
+                            for (int sl = 0; sl < G::SLABS; ++sl)
+                                tma_load_4d(smem_u32(smem + G::OFF_KV + slot.i * G::TILE + sl * G::SLAB) + r0 * 128u, map,
+                                            64 * sl, row, pc.kvh, page, bar);
                         }
                     }
                     ++load;
+                    slot.next();
+                    if (slot.i == 0) fresh = false;
+                    return true;
+                };
+                // (one call: the roles' loops share an instruction cache)
+                for (int kt = 0, vt = 0; vt < n && go;) {
+                    const bool is_k = kt < min(n, vt + ahead);
+                    go = load_tile(is_k, is_k ? kt : vt);
+                    if (is_k) ++kt;
+                    else ++vt;
                 }
                 ++piece;
             }
@@ -1307,10 +1382,9 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 if (lane == 0) {
                     constexpr int RING = G::MX8 ? G::C_SLOTS : G::SLOTS;
                     for (int i = max(load - RING, 0); i < load; ++i)
-                        at_wait(G::MX8 ? &c_full[i % RING] : &full[i % RING], (i / RING) & 1, abort_flag, AT_WAIT_NS,
-                                  false);
-                    if (!prm.stall && piece > 0) at_wait(&c.q_full, (piece - 1) & 1, abort_flag, AT_WAIT_NS, false);
-                    if (!prm.stall) at_wait(&c.q_full, piece & 1, abort_flag, 1000000ull, false);
+                        at_wait(G::MX8 ? &c_full[i % RING] : &full[i % RING], (i / RING) & 1, abort_flag, AT_WAIT_NS, NAP_P, false);
+                    if (!prm.stall && piece > 0) at_wait(&c.q_full, (piece - 1) & 1, abort_flag, AT_WAIT_NS, NAP_P, false);
+                    if (!prm.stall) at_wait(&c.q_full, piece & 1, abort_flag, 1000000ull, NAP_P, false);
                 }
             }
         } else if (warp == 9) {
@@ -1331,8 +1405,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             uint32_t p_phase[2] = {0, 0};  // of each group's p_full
             bool go = true;
             auto wait = [&](uint64_t *bar, uint32_t phase) {
-                if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, phase))) return true;
-                return __all_sync(0xFFFFFFFFu, at_wait(bar, phase, abort_flag, prm.wait_ns)) != 0;
+                return warp_wait(bar, phase, abort_flag, prm.wait_ns, NAP_M);
             };
             auto commit = [&](uint64_t *bar) {
                 if (elected) umma_commit(bar);
@@ -1349,17 +1422,15 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 }
                 umma_commit(&c.s_full[w]);
             };
-            // (elected lane) half of O of group w from its weights and the values in slot i
+            // (elected lane) group w's O plus its weights of half a tile times the values in slot i
             auto o_mma = [&](int w, int i, int half, bool first) {
                 const uint32_t vb = desc_lo(kv_addr + (uint32_t)i * G::TILE, G::SLAB);
-                const uint32_t d = tmem + G::O_COL + 128 * w, at = tmem + G::S_COL + 128 * w;
+                const uint32_t d = tmem + G::O_COL + 128 * w, at = tmem + G::S_COL + 128 * w + 64 * half;
 #pragma unroll
-                for (int kk = 0; kk < AT_KEYS / 32; ++kk) {
-                    const int k = kk + half * (AT_KEYS / 32);
-                    umma_ts(d, at + 8 * k, desc64(vb + k * (2048 >> 4)), idesc_o, !(first && half == 0 && kk == 0));
-                }
+                for (int kk = 0; kk < AT_KEYS / 32; ++kk)
+                    umma_ts(d, at + 8 * kk, desc64(vb + (kk + half * (AT_KEYS / 32)) * (2048 >> 4)), idesc_o, !(first && kk == 0));
             };
-            for (int i = 0; go && __all_sync(0xFFFFFFFFu, take(i)) && !pc.end; ++i) {
+            for (int i = 0; go && take(i) && !pc.end; ++i) {
                 if (pc.k0 >= pc.k1) continue;
                 const int n = pc.k1 - pc.k0, ahead = pc.rows ? 1 : 2;
                 // the first scores of each group
@@ -1396,13 +1467,13 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                         go = wait(&c.p_full[w][0], p_phase[w]);
                         if (!go) break;
                         tc_fence_after();
-                        if (elected) o_mma(w, v.i, 0, pc.rows ? t == 0 : t < 2);
+                        if (elected) o_mma(w, v.i, G::H0, pc.rows ? t == 0 : t < 2);
                         go = wait(&c.p_full[w][1], p_phase[w]);
                         if (!go) break;
                         p_phase[w] ^= 1;
                         tc_fence_after();
                         if (elected) {
-                            o_mma(w, v.i, 1, false);
+                            o_mma(w, v.i, 1 - G::H0, false);
                             umma_commit(&c.o_full[w]);
                             const bool rel = w == w_end - 1;
                             if (rel) umma_commit(&empty[v.i]);
@@ -1421,59 +1492,61 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             commit(&c.done);
         } else if (warp >= 10) {
             if constexpr (G::MX8) {
-                // ---------------- decoders: unit j of tile `load` goes to warp
-                // (load * UNITS + j) % DECODERS.  A unit is 8 (D = 128) or 16 rows:
-                // a lane decodes 32 elements of one row, neighbouring lanes the two
-                // halves of a slab's row, so that the 16-byte stores of each 8
-                // lanes cover all banks.
-                const int dw = warp - 10;
-                int base = 0;
+                // ---------------- decoders: a tile's units go round the warps,
+                // two or three to each; which warps get three moves on from tile to
+                // tile.  A unit is 8 (D = 128) or 16 rows: a lane decodes 32
+                // elements of one row, neighbouring lanes the two halves of a slab's
+                // row, so that the 16-byte stores of each 8 lanes cover all banks.
+                constexpr int ND = G::DECODERS;
+                const int half = lane & 1, slab = D == 128 ? lane >> 4 : 0;
+                const int row0 = D == 128 ? (lane >> 1) & 7 : lane >> 1, rows = D == 128 ? 8 : 16;  // of a unit
+                const int block = 2 * slab + half;
+                // the two 16-byte reads in a row-dependent order, for the banks
+                const int f = D == 128 ? row0 & 1 : (row0 >> 1) & 1;
+                int first = warp - 10;  // this warp's first unit of the tile
+                Slot<G::C_SLOTS> sc;
+                Slot<G::SLOTS> sd;
+                bool fresh = true;  // the decoded ring's first round: nothing to wait for
                 bool go = true;
-                for (int np = 0; go && __all_sync(0xFFFFFFFFu, take(np)) && !pc.end; ++np) {
-                    const int loads = 2 * (pc.k1 - pc.k0);
-                    for (int i = base; i < base + loads && go; ++i) {
-                        const int sc = i % G::C_SLOTS, sd = i % G::SLOTS;
-                        const uint8_t *codes = smem + G::OFF_C + sc * G::CODES;
-                        const uint8_t *scales = smem + G::OFF_SC + sc * G::SCALES;
-                        uint8_t *tile = smem + G::OFF_KV + sd * G::TILE;
-                        for (int j = (G::DECODERS + dw - (i * G::UNITS) % G::DECODERS) % G::DECODERS; j < G::UNITS;
-                             j += G::DECODERS) {
-                            const int half = lane & 1;
-                            const int row = D == 128 ? 8 * j + ((lane >> 1) & 7) : 16 * j + (lane >> 1);
-                            const int slab = D == 128 ? lane >> 4 : 0;
-                            const int block = 2 * slab + half;
-                            go = __all_sync(0xFFFFFFFFu, at_wait(&c_full[sc], (i / G::C_SLOTS) & 1, abort_flag, prm.wait_ns));
+                for (int np = 0; go && take(np) && !pc.end; ++np) {
+                    for (int left = 2 * (pc.k1 - pc.k0); left > 0; --left) {
+                        go = warp_wait(&c_full[sc.i], sc.phase, abort_flag, prm.wait_ns, NAP_D);
+                        if (!go) break;
+                        const uint8_t *codes = smem + G::OFF_C + sc.i * G::CODES + block * 32;
+                        const uint8_t *scales = smem + G::OFF_SC + sc.i * G::SCALES + block;
+                        uint8_t *tile = smem + G::OFF_KV + sd.i * G::TILE + slab * G::SLAB;
+                        if (!fresh) {
+                            go = warp_wait(&empty[sd.i], sd.phase ^ 1, abort_flag, prm.wait_ns, NAP_D);
                             if (!go) break;
-                            // the two 16-byte reads in a row-dependent order, for the banks
-                            const int f = D == 128 ? row & 1 : (row >> 1) & 1;
-                            const uint8_t *cp = codes + row * D + block * 32;
-                            const uint4 v0 = *reinterpret_cast<const uint4 *>(cp + 16 * f);
-                            const uint4 v1 = *reinterpret_cast<const uint4 *>(cp + 16 * (f ^ 1));
-                            const uint32_t e = scales[row * (D / 32) + block];
-                            const uint4 lo = f ? v1 : v0, hi = f ? v0 : v1;
-                            const uint32_t wds[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                            fence_proxy_async_smem();  // the slot may be refilled by TMA
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&c_empty[sc]);
-                            if (i >= G::SLOTS) {
-                                go = __all_sync(0xFFFFFFFFu, at_wait(&empty[sd], ((i / G::SLOTS) - 1) & 1, abort_flag,
-                                                                       prm.wait_ns));
-                                if (!go) break;
-                            }
-                            qhalf_store<FMT_MXFP8>(wds, e, tile + slab * G::SLAB + row * 128, half, row & 7);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&full[sd]);
                         }
+#pragma unroll 1
+                        for (int u = first; u < G::UNITS; u += ND) {
+                            const int row = u * rows + row0;
+                            const uint4 x = *reinterpret_cast<const uint4 *>(codes + row * D + 16 * f);
+                            const uint4 y = *reinterpret_cast<const uint4 *>(codes + row * D + 16 * (f ^ 1));
+                            const uint32_t e = scales[row * (D / 32)];
+                            const uint4 a0 = f ? y : x, a1 = f ? x : y;
+                            const uint32_t wds[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+                            decode32(wds, e, tile + row * 128, half, row & 7);
+                        }
+                        fence_proxy_async_smem();  // the tile is read by MMAs, the packed slot refilled by TMA
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&full[sd.i]);
+                            mbar_arrive(&c_empty[sc.i]);
+                        }
+                        sc.next();
+                        sd.next();
+                        if (sd.i == 0) fresh = false;
+                        first = (first + ND - G::UNITS % ND) % ND;
                     }
-                    base += loads;
                 }
             }
         }
     }
     __syncthreads();
     if (warp == 9) {
-        if (lane == 0) at_wait(&c.done, 0, abort_flag, AT_WAIT_NS, false);
+        if (lane == 0) at_wait(&c.done, 0, abort_flag, AT_WAIT_NS, NAP_P, false);
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

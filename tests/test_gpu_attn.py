@@ -363,3 +363,35 @@ def test_timeout_then_recovers(n, m):
     for _ in range(2):
         assert torch.equal(ops.paged_attn(b.kv, b.q, b.q_start, b.kv_len), good)
     assert ops.device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_mxfp8_values_are_exact(D):
+    """A context of one token gives its value back: every E4M3 code under every E8M0 scale, decoded exactly (rounded to bf16 only
+    where the product has no bf16), NaN codes and the NaN scale included."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    scales = torch.arange(256, dtype=torch.uint8, device="cuda")
+    B = 256 * 256 // D  # sequence b: codes (b D + d) % 256 under the scale b D // 256
+    codes = (torch.arange(B * D, device="cuda") % 256).to(torch.uint8).view(B, 1, 1, D)
+    sc = scales[(torch.arange(B, device="cuda") * D // 256)].view(B, 1, 1, 1).expand(B, 1, 1, D // 32).contiguous()
+    page = 16
+    k = torch.zeros((B, 1, page, D), dtype=torch.uint8, device="cuda")
+    v = torch.full_like(k, 0x7F)
+    ks = torch.full((B, 1, page, D // 32), 127, dtype=torch.uint8, device="cuda")
+    vs = torch.full_like(ks, 255)
+    v[:, :, :1], vs[:, :, :1] = codes, sc
+    table = torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1)
+    q_start = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    one = torch.ones(B, dtype=torch.int32, device="cuda")
+    q = torch.ones((B, 2, D), dtype=torch.bfloat16, device="cuda")
+    out = ops.paged_attn(ops.PagedKV(k, v, table, ks, vs), q, q_start, one)
+    assert ops.device_error() == 0
+    # MXFP8 values in bf16: at most 4 significant bits, so only the range rounds; fp32 holds what overflows as infinity
+    want = ref.mxfp8_values(v[:, 0, 0], vs[:, 0, 0]).to(torch.float32).to(torch.bfloat16)
+    for h in range(2):
+        got = out[:, h]
+        nan = torch.isnan(want)
+        assert torch.equal(torch.isnan(got), nan)
+        assert torch.equal(got[~nan], want[~nan])
