@@ -439,6 +439,16 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[NR
 }
 #undef MX_R32
 
+// 16 columns.
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+
 // Keeps uses of r[o..o+31] behind the wait that precedes it.
 template <int NR>
 __device__ __forceinline__ void pin32(uint32_t (&r)[NR], const int o)
@@ -447,6 +457,14 @@ __device__ __forceinline__ void pin32(uint32_t (&r)[NR], const int o)
     for (int i = 0; i < 32; i += 8)
         asm volatile("" : "+r"(r[o + i]), "+r"(r[o + i + 1]), "+r"(r[o + i + 2]), "+r"(r[o + i + 3]),
                           "+r"(r[o + i + 4]), "+r"(r[o + i + 5]), "+r"(r[o + i + 6]), "+r"(r[o + i + 7]));
+}
+
+__device__ __forceinline__ void pin16(uint32_t (&r)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                          "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -1163,30 +1181,20 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 a.lse[out_row] = (base2 + log2f(den)) * 0.6931471805599453f;
             uint64_t check = 0ull;
             if (warp_on) {
-                constexpr int EC = G::MX8 ? 32 : D / 2;  // dimensions at a time, for the registers
+                constexpr int EC = 16;  // dimensions at a time: little code, which comes from beyond the instruction cache
+                const bool own = n > 1 || (n == 1 && (pc.rows || w == 0)), oth = !pc.rows && (n > 1 || (n == 1 && w == 1));
 #pragma unroll 1
                 for (int d = d0; d < d1; d += EC) {
                     uint32_t u[EC], v[EC];
-#pragma unroll
-                    for (int i = 0; i < EC; i += 32) tmem_ld32_async(lane_base + G::O_COL + 128 * w + d + i, u, i);
-                    if (!pc.rows) {
-#pragma unroll
-                        for (int i = 0; i < EC; i += 32) tmem_ld32_async(lane_base + G::O_COL + 128 * (w ^ 1) + d + i, v, i);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < EC; ++i) v[i] = 0u;
-                    }
+                    tmem_ld16_async(lane_base + G::O_COL + 128 * w + d, u);
+                    tmem_ld16_async(lane_base + G::O_COL + 128 * (w ^ 1) + d, v);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < EC; i += 32) {
-                        pin32(u, i);
-                        pin32(v, i);
-                    }
+                    pin16(u);
+                    pin16(v);
                     float o[EC];  // the row's sums against m
-                    const bool own = n > 1 || (n == 1 && (pc.rows || w == 0)), oth = !pc.rows && (n > 1 || (n == 1 && w == 1));
 #pragma unroll
                     for (int i = 0; i < EC; ++i) {
-                        // (a group that had no tile of this piece has anything in its O)
+                        // (a group that had no tile of this piece has anything in its O; in rows the other O is not the row's)
                         o[i] = own ? __uint_as_float(u[i]) * f_own : 0.0f;
                         if (oth) o[i] += __uint_as_float(v[i]) * f_other;
                     }
