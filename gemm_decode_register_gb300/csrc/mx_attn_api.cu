@@ -115,11 +115,12 @@ extern "C" int mx_paged_attn(const mx_paged_kv *kv, const void *q, int64_t q_tok
     int s = check_kv(kv);
     if (s == MX_OK) s = check_batch(q_start, kv_len, T, B);
     if (s != MX_OK) return s;
-    if (!q || !out || !workspace || Hq <= 0 || Hq % kv->Hkv != 0 || window < 0 || (flags & ~MX_ATTN_CAUSAL) ||
+    if (!q || !out || Hq <= 0 || Hq % kv->Hkv != 0 || window < 0 || (flags & ~MX_ATTN_CAUSAL) ||
         !(scale == scale) || q_token_stride <= 0 || q_head_stride <= 0)
         return MX_EINVAL;
     if (!attn_sizes_ok(T, B, Hq, kv->Hkv, kv->D)) return MX_EUNSUPPORTED;
-    if (workspace_bytes < attn_workspace_bytes(T, B, Hq, kv->Hkv, kv->D)) return MX_EINVAL;
+    const size_t need = attn_workspace_bytes(T, B, Hq, kv->Hkv, kv->D);
+    if (workspace ? workspace_bytes < need : workspace_bytes != 0 || need > WS_FLOATS * sizeof(float)) return MX_EINVAL;
     if (!aligned(q, 16) || q_token_stride % 8 || q_head_stride % 8 || !aligned(out, 16) || !aligned(workspace, 256) ||
         !aligned(lse, 4) || !aligned(sinks, 4))
         return MX_EALIGN;
@@ -144,7 +145,8 @@ extern "C" int mx_paged_attn(const mx_paged_kv *kv, const void *q, int64_t q_tok
     a.g = Hq / kv->Hkv;
     a.workspace = workspace;
     a.err = ds->err;
-    DeviceState v = *ds;  // the slot's counters: items cut across CTAs
+    DeviceState v = *ds;  // the slot's counters, for items cut across CTAs, and its sums' space
     if (!attach_stream_workspace(v, current_stream())) return MX_ECUDA;
+    if (!workspace) a.workspace = v.ws;
     return finish(launch_paged_attn(v, current_stream(), a));
 }

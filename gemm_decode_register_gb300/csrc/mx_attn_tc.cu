@@ -1613,7 +1613,8 @@ static cudaError_t run_attn_tc(const DeviceState &ds, cudaStream_t st, const Att
     const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
     const int s1 = AT_ROWS / a.g;
     CUtensorMap maps[4];
-    for (int i = 0; i < 2; ++i) {
+    // whole row tiles of queries (not needed by calls of few tokens), single tokens
+    for (int i = a.T > AT_Q_COPIES ? 0 : 1; i < 2; ++i) {
         const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
         const cuuint64_t strides[2] = {(cuuint64_t)a.q_head_stride * 2, (cuuint64_t)a.q_token_stride * 2};
         const cuuint32_t box[3] = {64u, (cuuint32_t)a.g, i == 0 ? (cuuint32_t)s1 : 1u};
@@ -1622,6 +1623,7 @@ static cudaError_t run_attn_tc(const DeviceState &ds, cudaStream_t st, const Att
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
+    if (a.T <= AT_Q_COPIES) maps[0] = maps[1];
     for (int i = 0; i < 2; ++i) {
         const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.kv.page_size, (cuuint64_t)a.kv.Hkv,
                                     (cuuint64_t)a.kv.num_pages};

@@ -107,8 +107,17 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (3 us of a small call's 13): torch's own accessors where
+# they exist.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream() -> None:
-    load().mx_set_stream(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    if _raw_stream is not None and _raw_device is not None:
+        load().mx_set_stream(_raw_stream(_raw_device()))
+    else:
+        load().mx_set_stream(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
 
 
 def qmv(fmt: int, codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, N: int,
@@ -315,28 +324,29 @@ def moe_combine(yd: torch.Tensor, r: torch.Tensor, out: torch.Tensor | None = No
 KV_BF16, KV_MXFP8 = 0, 1
 ROPE_INTERLEAVED, ROPE_INVERSE = 0x1, 0x2
 ATTN_CAUSAL = 0x1
+WORKSPACE_SLOT_BYTES = 16 << 20  # the library's own workspace of a stream
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
-def _cuda(name: str, t: torch.Tensor, dtype, dim: int | None = None) -> int:
-    """Device pointer of a tensor of the type(s), its last dimension contiguous."""
+def _cuda(name: str, t: torch.Tensor, dtype, dim: int) -> int:
+    """Device pointer of a tensor of the type, its last dimension contiguous."""
+    if t.dtype is dtype and t.is_cuda and t.dim() == dim and (t.stride(-1) == 1 or t.shape[-1] <= 1):
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if dim is not None and t.dim() != dim:
+    if t.dim() != dim:
         raise ValueError(f"{name}: expected {dim} dimensions, got {t.dim()}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: the last dimension must be contiguous")
 
 
-def _whole(name: str, t: torch.Tensor, dtype, *shape: int) -> int:
+def _whole(name: str, t: torch.Tensor, dtype, shape: tuple) -> int:
     """Device pointer of a contiguous tensor of the type and shape."""
-    p = _cuda(name, t, dtype)
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor of shape {shape}, got {tuple(t.shape)}")
-    return p
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtype}, shape {tuple(shape)}; got {t.dtype}, "
+                     f"{tuple(t.shape)} on {t.device}")
 
 
 class _PagedKV(ctypes.Structure):
@@ -455,7 +465,8 @@ def _table_arg(table: torch.Tensor | None) -> tuple[int | None, int, int]:
         return None, 0, 0
     if table.dim() != 3 or table.shape[2] != 2:
         raise ValueError("table: expected [positions][rot / 2][2]")
-    return _whole("table", table, torch.float32, *table.shape), table.shape[0], 2 * table.shape[1]
+    n, half, _ = shape = table.shape
+    return _whole("table", table, torch.float32, shape), n, 2 * half
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False,
@@ -467,18 +478,21 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, interlea
         raise ValueError(f"x: expected bf16 or fp32, got {x.dtype}")
     xp = _cuda("x", x, x.dtype, 3)
     T, H, D = x.shape
+    xt, xh, _ = x.stride()
     if out is None:
         out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape:
-        raise ValueError("out: expected the shape of x")
-    op = _cuda("out", out, x.dtype, 3)
+        op, yt, yh = out.data_ptr(), H * D, D
+    else:
+        if out.shape != x.shape:
+            raise ValueError("out: expected the shape of x")
+        op = _cuda("out", out, x.dtype, 3)
+        yt, yh, _ = out.stride()
     tp, n, rot = _table_arg(table)
-    pp = _whole("positions", positions, torch.int32, T)
+    pp = _whole("positions", positions, torch.int32, (T,))
     if T == 0:
         return out
     _stream()
-    _check("mx_rope", load().mx_rope(xp, op, _DTYPES[x.dtype], pp, tp, n, T, H, D, rot, x.stride(0), x.stride(1),
-                                     out.stride(0), out.stride(1),
+    _check("mx_rope", load().mx_rope(xp, op, _DTYPES[x.dtype], pp, tp, n, T, H, D, rot, xt, xh, yt, yh,
                                      (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)))
     return out
 
@@ -497,9 +511,11 @@ def kv_append(kv: PagedKV, rows: torch.Tensor, q_start: torch.Tensor, kv_len: to
         raise ValueError(f"rows: expected (Hq + 2 Hkv) D = {(Hq + 2 * kv.Hkv) * D} elements per token")
     if q is None:
         q = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=rows.device)
-    qp = _whole("q", q, torch.bfloat16, T, Hq, D)
+        qp = q.data_ptr()
+    else:
+        qp = _whole("q", q, torch.bfloat16, (T, Hq, D))
     tp, n, rot = _table_arg(table)
-    sp, lp = _whole("q_start", q_start, torch.int32, kv.B + 1), _whole("kv_len", kv_len, torch.int32, kv.B)
+    sp, lp = _whole("q_start", q_start, torch.int32, (kv.B + 1,)), _whole("kv_len", kv_len, torch.int32, (kv.B,))
     if T == 0:
         return q
     _stream()
@@ -526,19 +542,31 @@ def paged_attn(kv: PagedKV, q: torch.Tensor, q_start: torch.Tensor, kv_len: torc
         raise ValueError(f"q: heads of {D}, the cache's have {kv.D}")
     if out is None:
         out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    if lse is None and return_lse:
+        op = out.data_ptr()
+    else:
+        op = _whole("out", out, torch.bfloat16, (T, Hq, D))
+    if lse is not None:
+        ep = _whole("lse", lse, torch.float32, (T, Hq))
+    elif return_lse:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    op = _whole("out", out, torch.bfloat16, T, Hq, D)
-    ep = None if lse is None else _whole("lse", lse, torch.float32, T, Hq)
-    kp = None if sinks is None else _whole("sinks", sinks, torch.float32, Hq)
-    sp, lp = _whole("q_start", q_start, torch.int32, kv.B + 1), _whole("kv_len", kv_len, torch.int32, kv.B)
+        ep = lse.data_ptr()
+    else:
+        ep = None
+    kp = None if sinks is None else _whole("sinks", sinks, torch.float32, (Hq,))
+    B = kv.B
+    sp, lp = _whole("q_start", q_start, torch.int32, (B + 1,)), _whole("kv_len", kv_len, torch.int32, (B,))
     if T > 0:
         lib = load()
-        ws = _workspace(lib.mx_paged_attn_workspace_size(T, kv.B, Hq, kv.Hkv, D), workspace, q.device)
+        if workspace is None:
+            need = lib.mx_paged_attn_workspace_size(T, B, Hq, kv.Hkv, D)
+            if need == 0 or need > WORKSPACE_SLOT_BYTES:
+                workspace = _workspace(need, None, q.device)
+        wp, wn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
+        qt, qh, _ = q.stride()
         _stream()
-        _check("mx_paged_attn", lib.mx_paged_attn(
-            kv._ref, qp, q.stride(0), q.stride(1), sp, lp, 1.0 / math.sqrt(D) if scale is None else scale,
-            ATTN_CAUSAL if causal else 0, window, kp, op, ep, T, kv.B, Hq, _ptr(ws), ws.numel()))
+        _check("mx_paged_attn", lib.mx_paged_attn(kv._ref, qp, qt, qh, sp, lp,
+                                                  1.0 / math.sqrt(D) if scale is None else scale,
+                                                  ATTN_CAUSAL if causal else 0, window, kp, op, ep, T, B, Hq, wp, wn))
     return (out, lse) if return_lse else out
 
 

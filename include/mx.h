@@ -39,7 +39,8 @@
  * kernels are queued.  The device error word is a variable of the library
  * image.  Calls whose kernels pass partial sums through global memory
  * (mx_qmv when K is split across CTAs, mx_moe_gate_up_swiglu for rows the
- * streaming kernel cannot take, mx_moe_down_combine, NVFP4 mx_quantize) use a 16 MiB workspace slot of the stream they are issued on,
+ * streaming kernel cannot take, mx_moe_down_combine, NVFP4 mx_quantize,
+ * mx_paged_attn) use a 16 MiB workspace slot of the stream they are issued on,
  * so calls on different streams never share one; a stream's slot is
  * allocated and cleared by the first such call on it (cudaMalloc, with the
  * calling thread switched to relaxed capture mode for it, so that first call
@@ -361,7 +362,9 @@ int mx_kv_append(const mx_paged_kv *kv, const void *rows, int dtype, int64_t row
  * bf16 for the product with v.
  * workspace: caller-owned device memory of at least
  * mx_paged_attn_workspace_size(T, B, Hq, kv->Hkv, kv->D) bytes, 256-byte
- * aligned; overwritten, so calls sharing one must not overlap.
+ * aligned; overwritten, so calls sharing one must not overlap.  Null (with
+ * workspace_bytes 0) where that size is at most 16 MiB: the calling stream's
+ * workspace slot.
  * Hq a multiple of Hkv, at most 128 query heads per cache head.  q and its
  * strides multiples of 16 bytes, out 16-byte aligned.  A missing page sets
  * MX_DEVERR_BAD_PAGE and makes the outputs that need it NaN. */

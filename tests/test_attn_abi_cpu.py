@@ -67,6 +67,14 @@ def test_attn_rejects(lib, i, value, want):
     assert lib.mx_paged_attn(*args) == want
 
 
+def test_attn_null_workspace(lib):
+    """Only where the stream's slot (16 MiB) is large enough, and with no size."""
+    c = kv()
+    assert lib.mx_paged_attn_workspace_size(4, 2, 8, 2, 128) <= 16 << 20 < lib.mx_paged_attn_workspace_size(4096, 1, 64, 2, 128)
+    args = [ctypes.byref(c), A, 8192, 128, A, A, 0.1, 1, 0, None, A, None, 4096, 1, 64, None, 0]
+    assert lib.mx_paged_attn(*args) == -1
+
+
 @pytest.mark.parametrize("i,value,want", [
     (0, 0, -1), (1, 0, -1), (2, 2, -2), (3, 0, -1), (4, 0, -1), (6, 0, -1), (7, 0, -1), (8, 0, -1), (9, 63, -1),
     (9, 130, -1), (10, -1, -1), (12, 0, -1), (14, 4, -1), (0, A + 1, -3), (3, A + 2, -3), (4, A + 8, -3)])
