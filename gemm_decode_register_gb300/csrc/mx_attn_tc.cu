@@ -29,12 +29,14 @@
 // rows in the workspace and the last CTA to arrive adds them in order.
 //
 //   warps 0-3, 4-7  softmax groups and epilogue
-//   warp 8          TMA producer (queries, keys, values)
 //   warp 9          MMA issuer
-//   warps 10-15     MXFP8 cache only: decoders.  The codes and scales of a tile
+//   warp 10         TMA producer (queries, keys, values); not on the SM's first
+//                   quarter, whose softmax warps have the rows when there are few
+//                   (verification 122 -> 113 us against warp 8)
+//   warps 11-18     MXFP8 cache only: decoders.  The codes and scales of a tile
 //                   land in a ring of their own and are decoded exactly to the
 //                   bf16 tiles that the MMAs read, as in the prefill GEMM.
-//                   (bf16 cache: warps 10 and 11 only fill up the warpgroup.)
+//                   (The other warps only fill up the warpgroups.)
 //
 // Every wait is bounded as in the GEMMs; a CTA whose wait gives up makes its
 // outputs NaN and sets MX_DEVERR_TIMEOUT.
@@ -57,11 +59,12 @@ constexpr unsigned long long AT_WAIT_NS = 2000000000ull;
 template <int D, int KVF>
 struct AtGeo {
     static constexpr bool MX8 = KVF == KV_MXFP8;
-    static constexpr int THREADS = MX8 ? 512 : 384;
-    // registers: what the launch gives each thread, shared out again between
-    // the softmax warps and the others (2 x 4 and 1 or 2 x 4 warps)
-    static constexpr int R_SOFTMAX = MX8 ? 168 : 208, R_OTHER = 88;
-    static_assert(2 * R_SOFTMAX + (MX8 ? 2 : 1) * R_OTHER <= (MX8 ? 4 * 128 : 3 * 168), "register split");
+    static constexpr int THREADS = MX8 ? 640 : 384;
+    // registers: what the launch gives each thread (168, 96), shared out again
+    // between the softmax warps and the others (on each of the SM's quarters two,
+    // and one or three)
+    static constexpr int R_SOFTMAX = MX8 ? 144 : 208, R_OTHER = MX8 ? 64 : 88;
+    static_assert(2 * R_SOFTMAX + (MX8 ? 3 : 1) * R_OTHER <= (MX8 ? 5 * 96 : 3 * 168), "register split");
     static constexpr int SLABS = D / 64;                    // 128-byte swizzled slabs of 64 dimensions
     static constexpr int SLAB = 128 * 128;                  // bytes of a slab: 128 rows x 128 bytes
     static constexpr int TILE = SLABS * SLAB;               // bytes of a row tile or a bf16 key tile
@@ -69,8 +72,8 @@ struct AtGeo {
     // MXFP8: ring of packed tiles, codes [128][D] then scales [128][D / 32]
     static constexpr int CODES = 128 * D, SCALES = 128 * (D / 32);
     static constexpr int C_SLOTS = MX8 ? (D == 128 ? 3 : 8) : 1;
-    static constexpr int DECODERS = 6;                      // warps
-    static constexpr int UNITS = 4 * D / 32;                // warp-sized parts of a tile's decode
+    static constexpr int DECODERS = 8;                      // warps
+    static constexpr int UNITS = D / 8;                // warp-sized parts of a tile's decode
     static constexpr int OFF_KV = 2 * TILE;                 // after two row tiles
     static constexpr int OFF_C = OFF_KV + SLOTS * TILE;
     static constexpr int OFF_SC = OFF_C + (MX8 ? C_SLOTS * CODES : 0);
@@ -567,39 +570,25 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 }
 
 // 32 MXFP8 elements (codes w, block scale e) to bf16: chunks 4 half .. of the
-// row's 128 bytes in a slab (chunk c at c ^ sw).  An E4M3 code's seven magnitude
-// bits, moved to the top of a bf16's mantissa and the bottom of its exponent,
-// are its value times 2^-120 (subnormal codes included); a bf16 product with
-// 2^(e - 127 + 120) then gives code * scale exactly, as long as that power and
-// the products are normal.  Scales out of that range and NaN codes take the
-// conversions through fp32.
-__device__ __noinline__ void decode32_any(const uint32_t *w, uint32_t e, uint8_t *row, int half, int sw)
-{
-    qhalf_store<FMT_MXFP8>(w, e, row, half, sw);
-}
-
+// row's 128 bytes in a slab (chunk c at c ^ sw).  Through fp32, exactly, for every code
+// and scale: the conversions and products run on the floating-point pipes,
+// which are free here, where moving bits into place keeps the integer pipe busy
+// (a tile of 128 x 128 by eight warps: 673 cycles against 906 to 1064 for three ways of bit placement).
 __device__ __forceinline__ void decode32(const uint32_t (&w)[8], uint32_t e, uint8_t *row, int half, int sw)
 {
-    uint32_t top = 0u;  // the largest magnitudes, two to a word: a NaN code is 0x07F0
-    uint32_t o[16];
-    const uint32_t p = (e + 120u) << 7, m = p | (p << 16);  // 2^(e - 127 + 120), exponent field e + 120
+    const float s = e8m0_to_f32(e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int c = 0; c < 4; ++c) {
+        uint32_t o[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t t = __byte_perm(w[i], 0u, j == 0 ? 0x1404 : 0x3424);  // two codes, each in the top byte of a half
-            const uint32_t mag = (t >> 4) & 0x07F007F0u;
-            top = __vmaxu2(top, mag);
-            o[2 * i + j] = bf16x2_mul(mag | (t & 0x80008000u), m);
+        for (int i = 0; i < 2; ++i) {
+            uint32_t h0, h1;
+            e4m3x4_to_f16x2(w[2 * c + i], h0, h1);
+            o[2 * i] = scaled_bf16x2(h0, s);
+            o[2 * i + 1] = scaled_bf16x2(h1, s);
         }
+        store_chunk(row, 4 * half + c, sw, o[0], o[1], o[2], o[3]);
     }
-    // exponent field at most 254; products at least 2^-9 * 2^(e - 127) >= 2^-126
-    if (__builtin_expect(e - 10u > 124u || __vcmpgeu2(top, 0x07F007F0u) != 0u, 0)) {
-        decode32_any(w, e, row, half, sw);
-        return;
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) store_chunk(row, 4 * half + c, sw, o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
 }
 
 // ------------------------------------------------------------ kernel
@@ -624,6 +613,11 @@ struct AtCtrl {
     float m[2][AT_ROWS], l[2][AT_ROWS];
 };
 static_assert(sizeof(AtCtrl) <= AtGeo<128, KV_BF16>::CTRL, "control block");
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
 
 // A position in a ring of N slots and the phase of its barriers there.
 template <int N>
@@ -948,10 +942,15 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 rlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
                 if (rhi < rlo) rhi = rlo;
             }
-            const bool warp_on = __any_sync(0xFFFFFFFFu, valid);
+            // warps with rows, the first ones of the group; the others go to the
+            // vote, and the first warp arrives for them
+            const int R = min(pc.ntok - (pc.rows ? w * s1 : 0), s1) * a.g, warps_on = (R + 31) / 32;
+            const bool warp_on = (warp & 3) < warps_on;
+            const uint32_t arrivals = (warp & 3) == 0 ? 5 - warps_on : 1;
+            const int n_mine = pc.rows ? n : (n + 1 - w) / 2;  // this group's steps
             float m = -INFINITY, l = 0.0f;  // m: log2 units, what P was taken against
             int mine = 0;                   // steps of this piece
-            for (int t = pc.rows ? 0 : w; t < n && alive; t += ahead) {
+            for (int t = pc.rows ? 0 : w; t < n && alive && warp_on; t += ahead) {
                 alive = wait(&c.s_full[w], steps);
                 if (!alive) break;
                 const int key0 = (pc.tile0 + pc.k0 + t) * AT_KEYS;
@@ -962,14 +961,14 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     alive = wait(&full[vi % G::SLOTS], vi / G::SLOTS);
                     if (!alive) break;
                     uint8_t *v = smem + G::OFF_KV + (vi % G::SLOTS) * G::TILE;
-                    const int key = key0 + row;
-                    if (key < pc.lo || key >= pc.hi)
-                        for (int i = 0; i < G::SLABS * 8; ++i)
-                            *reinterpret_cast<uint4 *>(v + (i / 8) * G::SLAB + row * 128 + (i % 8) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                    for (int r = row; r < AT_KEYS; r += 32 * warps_on)
+                        if (key0 + r < pc.lo || key0 + r >= pc.hi)
+                            for (int i = 0; i < G::SLABS * 8; ++i)
+                                *reinterpret_cast<uint4 *>(v + (i / 8) * G::SLAB + r * 128 + (i % 8) * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
-                if (warp_on) {
+                {
                     tc_fence_after();
                     const bool edge = __any_sync(0xFFFFFFFFu, key0 < rlo || key0 + AT_KEYS > rhi);
                     // half h of the scores (32 pairs): from tensor memory, masked
@@ -1056,7 +1055,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     // the product with the first half of V may start
                     auto half_done = [&]() {
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&c.p_full[w][0]);
+                        if (lane == 0) mbar_arrive_n(&c.p_full[w][0], arrivals);
                     };
                     if constexpr (G::MX8) {
                         // one half at a time, its scores read twice: fewer registers and
@@ -1106,14 +1105,13 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                         publish(1, pk);
                         l += sum;
                     }
-                } else if (lane == 0) {
-                    mbar_arrive(&c.p_full[w][0]);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&c.p_full[w][1]);
+                if (lane == 0) mbar_arrive_n(&c.p_full[w][1], arrivals);
                 ++steps;
                 ++mine;
             }
+            if (!warp_on) steps += n_mine;
             // the last product must be in before O is read
             if (mine > 0 && alive) alive = wait(&c.o_full[w], steps - 1);
             if (!pc.rows) {
@@ -1270,7 +1268,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::R_OTHER));
-        if (warp == 8) {
+        if (warp == 10) {
             // ---------------- producer: walks the stretch for everybody
             Walk walk(a, st, cost);
             const int ppt = AT_KEYS / prm.page_rows;  // TMA copies per tile and slab
@@ -1503,20 +1501,19 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 ++piece;
             }
             commit(&c.done);
-        } else if (warp >= 10) {
+        } else if (G::MX8 && warp >= 11 && warp < 11 + G::DECODERS) {
             if constexpr (G::MX8) {
-                // ---------------- decoders: a tile's units go round the warps,
-                // two or three to each; which warps get three moves on from tile to
-                // tile.  A unit is 8 (D = 128) or 16 rows: a lane decodes 32
-                // elements of one row, neighbouring lanes the two halves of a slab's
-                // row, so that the 16-byte stores of each 8 lanes cover all banks.
+                // ---------------- decoders: each takes UNITS / 8 parts of every tile.  A
+                // unit is 8 (D = 128) or 16 rows: a lane decodes 32 elements of one
+                // row, neighbouring lanes the two halves of a slab's row, so that the
+                // 16-byte stores of each 8 lanes cover all banks.
                 constexpr int ND = G::DECODERS;
                 const int half = lane & 1, slab = D == 128 ? lane >> 4 : 0;
                 const int row0 = D == 128 ? (lane >> 1) & 7 : lane >> 1, rows = D == 128 ? 8 : 16;  // of a unit
                 const int block = 2 * slab + half;
                 // the two 16-byte reads in a row-dependent order, for the banks
                 const int f = D == 128 ? row0 & 1 : (row0 >> 1) & 1;
-                int first = warp - 10;  // this warp's first unit of the tile
+                const int first = warp - 11;  // this warp's first unit of a tile
                 Slot<G::C_SLOTS> sc;
                 Slot<G::SLOTS> sd;
                 bool fresh = true;  // the decoded ring's first round: nothing to wait for
@@ -1551,7 +1548,6 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                         sc.next();
                         sd.next();
                         if (sd.i == 0) fresh = false;
-                        first = (first + ND - G::UNITS % ND) % ND;
                     }
                 }
             }
