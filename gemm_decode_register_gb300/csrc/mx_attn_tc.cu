@@ -246,84 +246,89 @@ struct Walk {
     }
 };
 
-// The whole block: costs of all sequences, this CTA's stretch of them and its
-// first item.  scratch: a word of 8 bytes per warp.
-__device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, long long *scratch, Stretch *out)
+// A CTA's stretch, by one warp (the producer's, which walks it; nobody else waits for
+// more than its first piece): the costs of all sequences, 32 at a time, then
+// the item that holds the stretch's start.
+__device__ __forceinline__ long long warp_sum_before(long long v, long long *total)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int SCAN = 256;
-    const int s1 = cost.s2 / 2;
-    const int per = (a.B + SCAN - 1) / SCAN;
-    long long sum = 0;
-    if (tid < SCAN)
-        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) sum += cost.total(load_seq(a, b, s1));
-    long long inc = sum;
+    const int lane = threadIdx.x & 31;
+    long long inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += v;
+        const long long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += x;
     }
-    if (lane == 31) scratch[warp] = inc;
-    __syncthreads();
-    long long pre = 0, total = 0;
+    *total = __shfl_sync(0xFFFFFFFFu, inc, 31);
+    return inc - v;
+}
+
+__device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, Stretch &st)
+{
+    const int lane = threadIdx.x & 31, s1 = cost.s2 / 2;
+    auto cost_at = [&](int b) { return b < a.B ? cost.total(load_seq(a, b, s1)) : 0ll; };
+    const long long c0 = cost_at(lane);  // of the first 32, kept
+    long long total, first_total;
+    const long long before0 = warp_sum_before(c0, &first_total);
+    total = first_total;
+    if (a.B > 32) {
+        long long rest = 0;
+#pragma unroll 4
+        for (int b = 32 + lane; b < a.B; b += 32) rest += cost_at(b);
 #pragma unroll
-    for (int w = 0; w < SCAN / 32; ++w) {
-        if (w < warp) pre += scratch[w];
-        total += scratch[w];
+        for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
+        total += rest;
     }
-    const long long before = pre + inc - sum;
     // a CTA's stretch is no shorter than AT_MIN_KEYS, more than a tile, so that
     // no CTA between an item's first and last is left without a tile
-    const int ctas = (int)min((long long)gridDim.x, max(1ll, total / AT_MIN_KEYS));
+    const int grid = gridDim.x;
+    const int ctas = total >= (long long)grid * AT_MIN_KEYS ? grid : max(1, (int)((uint32_t)total / AT_MIN_KEYS));
     const int c = blockIdx.x;
-    long long start = total, end = total;
-    if (c < ctas) {
-        if (total < (1ll << 23)) {  // the usual case: 32-bit division
-            start = (uint32_t)total * (uint32_t)c / (uint32_t)ctas;
-            end = (uint32_t)total * (uint32_t)(c + 1) / (uint32_t)ctas;
-        } else {
-            start = total * c / ctas;
-            end = total * (c + 1) / ctas;
-        }
+    st.total = total;
+    st.ctas = ctas;
+    st.start = st.end = total;
+    st.b = a.B;
+    if (c >= ctas) return;
+    if (total < (1ll << 23)) {  // the usual case: 32-bit division
+        st.start = (uint32_t)total * (uint32_t)c / (uint32_t)ctas;
+        st.end = (uint32_t)total * (uint32_t)(c + 1) / (uint32_t)ctas;
+    } else {
+        st.start = total * c / ctas;
+        st.end = total * (c + 1) / ctas;
     }
-    if (tid == 0) {
-        out->total = total;
-        out->start = start;
-        out->end = end;
-        out->ctas = ctas;
-        out->b = a.B;
+    if (st.start >= st.end) return;
+    // the sequence that holds the start
+    long long at = before0, mine = c0, sum = first_total, base = 0;
+    int b0 = 0;
+    while (base + sum <= st.start && b0 < a.B) {
+        base += sum;
+        b0 += 32;
+        mine = cost_at(b0 + lane);
+        at = base + warp_sum_before(mine, &sum);
     }
-    // the sequence that holds the start (its finder skips to it among its own)
-    if (start < end && tid < SCAN && sum > 0 && before <= start && start < before + sum) {
-        long long at = before;
-        int b = tid * per;
-        for (;; ++b) {
-            const long long t = cost.total(load_seq(a, b, s1));
-            if (at + t > start) break;
-            at += t;
-        }
-        scratch[12] = at;
-        scratch[13] = b;
+    const unsigned holds = __ballot_sync(0xFFFFFFFFu, at <= st.start && st.start < at + mine);
+    if (holds == 0) return;  // (only if the lengths change meanwhile)
+    const int src = __ffs(holds) - 1;
+    at = __shfl_sync(0xFFFFFFFFu, at, src);
+    mine = __shfl_sync(0xFFFFFFFFu, mine, src);
+    st.b = b0 + src;
+    // its cache head and item
+    const Seq q = load_seq(a, st.b, s1);
+    const long long head = cost.before(q, q.pairs);  // mine = heads * head
+    int kvh = min((int)((float)(st.start - at) / (float)head), cost.heads - 1);
+    while (kvh * head > st.start - at) --kvh;
+    while ((kvh + 1) * head <= st.start - at) ++kvh;
+    at += kvh * head;
+    int lo = 0, n = q.pairs;  // the last p with at + before(p) <= start, 32 candidates a round
+    while (n > 1) {
+        const int step = (n + 31) >> 5, i = lane * step;
+        const unsigned le = __ballot_sync(0xFFFFFFFFu, i < n && at + cost.before(q, lo + i) <= st.start);
+        const int k = 31 - __clz(le);
+        lo += k * step;
+        n = min(step, n - k * step);
     }
-    __syncthreads();
-    if (start >= end) return;
-    // its item that holds the start: each thread looks at some
-    const int b = (int)scratch[13];
-    const Seq q = load_seq(a, b, s1);
-    const long long head = cost.before(q, q.pairs);
-    const int items = cost.heads * q.pairs;
-    for (int i = tid; i < items; i += blockDim.x) {
-        const int kvh = i / q.pairs, p = i - kvh * q.pairs;
-        const long long at = scratch[12] + kvh * head + cost.before(q, p);
-        const long long next = scratch[12] + kvh * head + cost.before(q, p + 1);
-        if (at <= start && start < next) {
-            out->at = at;
-            out->b = b;
-            out->kvh = kvh;
-            out->p = p;
-        }
-    }
-    __syncthreads();
+    st.kvh = kvh;
+    st.p = lo;
+    st.at = at + cost.before(q, lo);
 }
 
 // ------------------------------------------------------------ tensor ops
@@ -602,7 +607,6 @@ struct AtCtrl {
     uint64_t done;
     uint64_t r_full[AT_RING], r_free[AT_RING];
     Piece ring[AT_RING];             // pieces, from the producer to the other roles
-    long long scratch[16];
     Stretch stretch;
     uint32_t tmem;
     int abort_flag;
@@ -806,14 +810,14 @@ __device__ __noinline__ void arrive_cut(const AtParams &p, const Piece &piece, i
 // A CTA whose wait gave up: the outputs of its pieces from number `done` on
 // become NaN, its parts of cut items too.
 template <int D, int KVF>
-__device__ __noinline__ void poison(const AtParams &p, const Stretch &st, const Cost &cost, int done, int w, int row,
+__device__ __noinline__ void poison(const AtParams &p, const Cost &cost, int done, int w, int row,
                                     AtCtrl &c)
 {
     const AttnArgs &a = p.a;
     const float nan = __uint_as_float(0x7FC00000u);
     const int s1 = cost.s2 / 2;
     if (row == 0) set_device_error(a.err, DEVERR_TIMEOUT);
-    Walk walk(a, st, cost);
+    Walk walk(a, c.stretch, cost);
     Piece pc;
     for (int i = 0; walk.next(pc); ++i) {
         if (i < done) continue;
@@ -886,11 +890,10 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         tc_fence_before();
     }
-    plan(a, cost, c.scratch, &c.stretch);  // its barriers also publish the set-up above
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c.tmem;
-    const Stretch st = c.stretch;
-    pdl_wait();
+    if (warp != 10) pdl_wait();
     Piece pc;
     // the i-th piece from the ring, by a whole warp
     auto take = [&](int i) {
@@ -960,12 +963,13 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     const int vi = base + v_load(t, n, ahead);
                     alive = wait(&full[vi % G::SLOTS], vi / G::SLOTS);
                     if (!alive) break;
-                    uint8_t *v = smem + G::OFF_KV + (vi % G::SLOTS) * G::TILE;
-                    for (int r = row; r < AT_KEYS; r += 32 * warps_on)
+                    // (eight lanes to a 128-byte row, so that a store covers all banks)
+                    uint8_t *v = smem + G::OFF_KV + (vi % G::SLOTS) * G::TILE + (lane & 7) * 16;
+                    for (int r = (row >> 5) * 4 + (lane >> 3); r < AT_KEYS; r += 4 * warps_on)
                         if (key0 + r < pc.lo || key0 + r >= pc.hi)
-                            for (int i = 0; i < G::SLABS * 8; ++i)
-                                *reinterpret_cast<uint4 *>(v + (i / 8) * G::SLAB + r * 128 + (i % 8) * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                            for (int i = 0; i < G::SLABS; ++i)
+                                *reinterpret_cast<uint4 *>(v + i * G::SLAB + r * 128) = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
                 {
@@ -1083,7 +1087,8 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                         }
                     } else {
                         // the first half's weights against the maximum so far, while the
-                        // tile's maximum is found; again in the rare case that it is raised
+                        // tile's maximum is found; again in the rare case that it is raised,
+                        // and only then at the piece's first tile, which sets it
                         uint32_t s0[64], s1[64], pk[32];
                         load_half(0, s0);
                         load_half(1, s1);
@@ -1091,8 +1096,9 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                         mask_half(0, s0);
                         mask_half(1, s1);
                         const float top = fmaxf(max_half(s0), max_half(s1)) * sl2;
-                        float sum = weights(s0, pk);
-                        if (__builtin_expect(raise_to(top), 0)) {
+                        float sum = 0.0f;
+                        if (mine > 0) sum = weights(s0, pk);
+                        if (__builtin_expect(raise_to(top) || mine == 0, 0)) {
                             if (!alive) break;
                             load_half(0, s0);
                             tmem_wait_ld();
@@ -1121,7 +1127,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             tc_fence_before();
             // both groups go on only together: one that gave up does not come to their barriers any more
             const bool go_on = vote(1, 256, alive);
-            if (!go_on) poison<D, KVF>(prm, st, cost, np, w, row, c);
+            if (!go_on) poison<D, KVF>(prm, cost, np, w, row, c);
             if (!go_on || pc.end) break;
             tc_fence_after();
             const bool bad = n > 0 && c.missing[piece & 7] != 0;
@@ -1269,8 +1275,12 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::R_OTHER));
         if (warp == 10) {
-            // ---------------- producer: walks the stretch for everybody
-            Walk walk(a, st, cost);
+            // ---------------- producer: walks the stretch for everybody.  Lengths
+            // and the block table are read before the wait for the preceding kernel.
+            plan(a, cost, c.stretch);
+            __syncwarp();
+            Walk walk(a, c.stretch, cost);
+            bool waited = false;
             const int ppt = AT_KEYS / prm.page_rows;  // TMA copies per tile and slab
             int load = 0, piece = 0;
             Slot<G::MX8 ? G::C_SLOTS : G::SLOTS> slot;
@@ -1293,7 +1303,28 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 const int32_t *table = a.kv.block_table + (size_t)pc.b * a.kv.table_stride;
                 const int ahead = pc.rows ? 1 : 2, n = pc.k1 - pc.k0;
                 if (lane == 0) c.missing[piece & 7] = 0;
+                // page ids: lane i holds copy i of a window of 32 copies; the keys'
+                // window, the one before it (the values lag by up to two tiles)
+                // and the one after it (on its way)
+                const int per_win = 32 / ppt;  // tiles per window
+                auto id_index = [&](int wn) {  // in the table's row; -1: not seen, no copy; -2: past the row
+                    const long long key = (long long)(pc.tile0 + wn * per_win) * AT_KEYS + lane * prm.page_rows;
+                    if (key >= pc.hi || key + prm.page_rows <= pc.lo) return -1;
+                    const int i = (int)key / a.kv.page_size;
+                    return i < a.kv.table_stride ? i : -2;
+                };
+                auto id_of = [&](int index, int entry) {  // -2: missing
+                    return index < 0 ? index : (unsigned)entry < (unsigned)a.kv.num_pages ? entry : -2;
+                };
+                auto entry = [&](int index) { return index >= 0 ? __ldg(table + index) : 0; };
+                int win = pc.k0 / per_win, id_before = -1;
+                const int i0 = id_index(win), i1 = id_index(win + 1);
+                const int e0 = entry(i0), e1 = entry(i1);  // both on their way
                 // queries
+                if (!waited) {
+                    pdl_wait();
+                    waited = true;
+                }
                 if (lane == 0 && piece > 0) ok = at_wait(&c.q_empty, (piece - 1) & 1, abort_flag, prm.wait_ns, NAP_P);
                 if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
                 if (lane == 0 && !prm.stall) {
@@ -1321,17 +1352,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                                             pc.kvh * a.g, pc.q0 + t, &c.q_full);
                     }
                 }
-                // page ids: lane i holds copy i of a window of 32 copies; the keys'
-                // window, the one before it (the values lag by up to two tiles)
-                // and the one after it (on its way)
-                const int per_win = 32 / ppt;  // tiles per window
-                auto load_ids = [&](int wn) {
-                    const long long key = (long long)(pc.tile0 + wn * per_win) * AT_KEYS + lane * prm.page_rows;
-                    if (key >= pc.hi || key + prm.page_rows <= pc.lo) return -1;  // not seen: no copy
-                    const int id = page_of(a.kv, table, (int)key / a.kv.page_size);
-                    return id < 0 ? -2 : id;  // -2: missing
-                };
-                int win = pc.k0 / per_win, id_before = -1, id_here = load_ids(win), id_after = load_ids(win + 1);
+                int id_here = id_of(i0, e0), id_after = id_of(i1, e1);
                 // One tile into the ring.  The copies are issued by one elected lane
                 // from warp-uniform values (a lane per copy took about 150 cycles
                 // for each: pages of 16 tokens ran at 3.9 TB/s instead of 6).
@@ -1341,7 +1362,8 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                         win = wn;
                         id_before = id_here;
                         id_here = id_after;
-                        id_after = load_ids(win + 1);
+                        const int i = id_index(win + 1);
+                        id_after = id_of(i, entry(i));
                     }
                     const int ids = wn == win ? id_here : id_before, first = (kt - wn * per_win) * ppt;
                     const bool here = lane >= first && lane < first + ppt;
