@@ -115,7 +115,8 @@ __device__ __forceinline__ long long sum_range(long long a, long long s, long lo
 // Sum over i < p of max(a + i s, 0).
 __device__ __forceinline__ long long sum_pos(long long a, long long s, long long p)
 {
-    const long long z = a >= 0 ? 0 : (-a + s - 1) / s;
+    if (a >= 0) return sum_range(a, s, 0, p);
+    const uint32_t x = (uint32_t)min(-a, 0xFFFFFFFFll), z = x / (uint32_t)s + (x % (uint32_t)s != 0);
     return sum_range(a, s, z, p);
 }
 
@@ -126,7 +127,7 @@ struct Cost {
 
     // Keys before which items p, p + 1, ... of a head start (each item's own
     // keys and AT_SPLIT_KEYS): items see [lo(p), hi(p)).
-    __device__ __forceinline__ long long before(const Seq &q, int p) const
+    __device__ __noinline__ long long before(const Seq q, int p) const  // (one copy, for the instruction cache)
     {
         const long long base = (long long)q.len - q.n;
         long long h = (long long)p * q.len, l = 0;
@@ -487,6 +488,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
                  "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
                  "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
                  "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
 }
 
@@ -974,21 +984,30 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 }
                 {
                     tc_fence_after();
-                    const bool edge = __any_sync(0xFFFFFFFFu, key0 < rlo || key0 + AT_KEYS > rhi);
-                    // half h of the scores (32 pairs): from tensor memory, masked
+                    if (__builtin_expect(__any_sync(0xFFFFFFFFu, key0 < rlo || key0 + AT_KEYS > rhi), 0)) {
+                        // scores that the row may not see, in place: a small loop, for the instruction cache
+                        const int klo = rlo - key0, khi = rhi - key0;
+#pragma unroll 1
+                        for (int i = 0; i < AT_KEYS; i += 16) {
+                            uint32_t x[16];
+                            tmem_ld16_async(s_addr + i, x);
+                            tmem_wait_ld();
+                            pin16(x);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (i + j < klo || i + j >= khi) x[j] = 0xFF800000u;
+                            tmem_st16(s_addr + i, x);
+                        }
+                        tmem_wait_st();
+                    }
+                    // half h of the scores (32 pairs)
                     auto load_half = [&](int h, uint32_t(&s)[64]) {
                         tmem_ld32_async(s_addr + 64 * h, s, 0);
                         tmem_ld32_async(s_addr + 64 * h + 32, s, 32);
                     };
-                    auto mask_half = [&](int h, uint32_t(&s)[64]) {
+                    auto pin_half = [&](uint32_t(&s)[64]) {
                         pin32(s, 0);
                         pin32(s, 32);
-                        if (__builtin_expect(edge, 0)) {
-                            const int klo = rlo - key0 - 64 * h, khi = rhi - key0 - 64 * h;
-#pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (i < klo || i >= khi) s[i] = 0xFF800000u;
-                        }
                     };
                     auto max_half = [&](const uint32_t(&s)[64]) {
                         float x[4];
@@ -1038,14 +1057,14 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                             alive = wait(&c.o_full[w], steps - 1);
                             tc_fence_after();
 #pragma unroll 1
-                            for (int i = 0; i < D && alive; i += 32) {
-                                uint32_t o[32];
-                                tmem_ld32_async(lane_base + G::O_COL + 128 * w + i, o, 0);
+                            for (int i = 0; i < D && alive; i += 16) {
+                                uint32_t o[16];
+                                tmem_ld16_async(lane_base + G::O_COL + 128 * w + i, o);
                                 tmem_wait_ld();
-                                pin32(o, 0);
+                                pin16(o);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_st32(lane_base + G::O_COL + 128 * w + i, o);
+                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st16(lane_base + G::O_COL + 128 * w + i, o);
                             }
                         }
                         return true;
@@ -1071,7 +1090,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                         for (int h = 0; h < 2; ++h) {
                             load_half(h, s0);
                             tmem_wait_ld();
-                            mask_half(h, s0);
+                            pin_half(s0);
                             top = fmaxf(top, max_half(s0));
                         }
                         raise_to(top * sl2);
@@ -1080,7 +1099,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                         for (int h = 0; h < 2; ++h) {
                             load_half(h, s0);
                             tmem_wait_ld();
-                            mask_half(h, s0);
+                            pin_half(s0);
                             l += weights(s0, pk);
                             publish(h, pk);
                             if (h == 0) half_done();
@@ -1093,8 +1112,8 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                         load_half(0, s0);
                         load_half(1, s1);
                         tmem_wait_ld();
-                        mask_half(0, s0);
-                        mask_half(1, s1);
+                        pin_half(s0);
+                        pin_half(s1);
                         const float top = fmaxf(max_half(s0), max_half(s1)) * sl2;
                         float sum = 0.0f;
                         if (mine > 0) sum = weights(s0, pk);
@@ -1102,7 +1121,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                             if (!alive) break;
                             load_half(0, s0);
                             tmem_wait_ld();
-                            mask_half(0, s0);
+                            pin_half(s0);
                             sum = weights(s0, pk);
                         }
                         publish(0, pk);
