@@ -50,8 +50,7 @@ constexpr int AT_ROWS = 128;  // rows of a tile
 constexpr int AT_KEYS = 128;  // keys of a tile
 constexpr int AT_SPLIT_KEYS = 2 * AT_KEYS;  // what an item costs beside its keys, and more than its tiles' rounding
 constexpr int AT_Q_COPIES = 4;              // up to so many tokens are loaded one by one
-constexpr int AT_MIN_KEYS = 3 * AT_KEYS;      // shortest stretch of a CTA
-constexpr unsigned NAP_R = 50, NAP_S = 0, NAP_M = 0, NAP_P = 100, NAP_D = 50;
+constexpr int AT_MIN_KEYS = 3 * AT_KEYS;      // shortest stretch of a CTA that only divides an item
 constexpr int AT_RING = 3;                  // pieces the producer may run ahead by
 constexpr float AT_RAISE = 8.0f;            // log2 by which scores may outgrow the maximum before it is raised
 constexpr unsigned long long AT_WAIT_NS = 2000000000ull;
@@ -266,7 +265,13 @@ __device__ __forceinline__ long long warp_sum_before(long long v, long long *tot
 __device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, Stretch &st)
 {
     const int lane = threadIdx.x & 31, s1 = cost.s2 / 2;
-    auto cost_at = [&](int b) { return b < a.B ? cost.total(load_seq(a, b, s1)) : 0ll; };
+    int items = 0;  // of this lane's sequences
+    auto cost_at = [&](int b) {
+        if (b >= a.B) return 0ll;
+        const Seq q = load_seq(a, b, s1);
+        items += min(q.pairs * cost.heads, 1024);
+        return cost.total(q);
+    };
     const long long c0 = cost_at(lane);  // of the first 32, kept
     long long total, first_total;
     const long long before0 = warp_sum_before(c0, &first_total);
@@ -279,10 +284,12 @@ __device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, Stretc
         for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
         total += rest;
     }
-    // a CTA's stretch is no shorter than AT_MIN_KEYS, more than a tile, so that
-    // no CTA between an item's first and last is left without a tile
+    // A CTA for every item or every AT_MIN_KEYS keys, whichever are more.  Items
+    // cost at least two tiles, so a stretch is longer than a tile and no CTA
+    // between an item's first and last is left without one.
     const int grid = gridDim.x;
-    const int ctas = total >= (long long)grid * AT_MIN_KEYS ? grid : max(1, (int)((uint32_t)total / AT_MIN_KEYS));
+    items = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)min(items, 1 << 24));
+    const int ctas = total >= (long long)grid * AT_MIN_KEYS ? grid : max(1, min(grid, max(items, (int)total / AT_MIN_KEYS)));
     const int c = blockIdx.x;
     st.total = total;
     st.ctas = ctas;
@@ -335,17 +342,13 @@ __device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, Stretc
 // ------------------------------------------------------------ tensor ops
 
 // mbar_wait without a call: ptxas (13.0) cannot allocate the softmax warps'
-// registers past the launch's count across the call of its slow path.  Between
-// two polls the warp sleeps for about `nap` ns: every poll is a shared-memory
-// operation of each lane, and the polls of a dozen waiting warps slowed the
-// working ones (prompt 628 -> 582 us with naps in the producer alone).
+// registers past the launch's count across the call of its slow path.
 __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                        unsigned long long limit_ns, unsigned nap, bool respect_abort = true)
+                                        unsigned long long limit_ns, bool respect_abort = true)
 {
     unsigned long long t0 = 0;
 #pragma unroll 1
     for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-        if (nap) __nanosleep(nap);
         if (__builtin_expect((i & 63u) == 0u, 0)) {
             if (respect_abort && *abort_flag) return false;
             const unsigned long long t = globaltimer();
@@ -360,12 +363,12 @@ __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, volatile
     return true;
 }
 
-// A wait of the whole warp, polled by all of it: a poll by one lane in a branch
-// of its own was slower still (prompt 585 -> 764 us).
+// A wait of the whole warp, polled by all of it: polled by one lane in a branch
+// of its own a prompt took 764 us instead of 585.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                          unsigned long long limit_ns, unsigned nap)
+                                          unsigned long long limit_ns)
 {
-    return __all_sync(0xFFFFFFFFu, at_wait(bar, parity, abort_flag, limit_ns, nap)) != 0;
+    return __all_sync(0xFFFFFFFFu, at_wait(bar, parity, abort_flag, limit_ns)) != 0;
 }
 
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc)
@@ -907,7 +910,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     Piece pc;
     // the i-th piece from the ring, by a whole warp
     auto take = [&](int i) {
-        const bool ok = warp_wait(&c.r_full[i % AT_RING], (i / AT_RING) & 1, abort_flag, prm.wait_ns, NAP_R);
+        const bool ok = warp_wait(&c.r_full[i % AT_RING], (i / AT_RING) & 1, abort_flag, prm.wait_ns);
         if (ok) pc = c.ring[i % AT_RING];
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&c.r_free[i % AT_RING]);
@@ -929,7 +932,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
         bool alive = true;
         // warp-uniform, as the tensor-memory instructions that follow a wait must be
         auto wait = [&](uint64_t *bar, int phase) {
-            return warp_wait(bar, phase & 1, abort_flag, prm.wait_ns, NAP_S);
+            return warp_wait(bar, phase & 1, abort_flag, prm.wait_ns);
         };
         for (int np = 0;; ++np) {
             alive = take(np);
@@ -982,154 +985,152 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                                 *reinterpret_cast<uint4 *>(v + i * G::SLAB + r * 128) = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
-                {
-                    tc_fence_after();
-                    if (__builtin_expect(__any_sync(0xFFFFFFFFu, key0 < rlo || key0 + AT_KEYS > rhi), 0)) {
-                        // scores that the row may not see, in place: a small loop, for the instruction cache
-                        const int klo = rlo - key0, khi = rhi - key0;
+                tc_fence_after();
+                if (__builtin_expect(__any_sync(0xFFFFFFFFu, key0 < rlo || key0 + AT_KEYS > rhi), 0)) {
+                    // scores that the row may not see, in place: a small loop, for the instruction cache
+                    const int klo = rlo - key0, khi = rhi - key0;
 #pragma unroll 1
-                        for (int i = 0; i < AT_KEYS; i += 16) {
-                            uint32_t x[16];
-                            tmem_ld16_async(s_addr + i, x);
-                            tmem_wait_ld();
-                            pin16(x);
+                    for (int i = 0; i < AT_KEYS; i += 16) {
+                        uint32_t x[16];
+                        tmem_ld16_async(s_addr + i, x);
+                        tmem_wait_ld();
+                        pin16(x);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (i + j < klo || i + j >= khi) x[j] = 0xFF800000u;
-                            tmem_st16(s_addr + i, x);
-                        }
-                        tmem_wait_st();
+                        for (int j = 0; j < 16; ++j)
+                            if (i + j < klo || i + j >= khi) x[j] = 0xFF800000u;
+                        tmem_st16(s_addr + i, x);
                     }
-                    // half h of the scores (32 pairs)
-                    auto load_half = [&](int h, uint32_t(&s)[64]) {
-                        tmem_ld32_async(s_addr + 64 * h, s, 0);
-                        tmem_ld32_async(s_addr + 64 * h + 32, s, 32);
-                    };
-                    auto pin_half = [&](uint32_t(&s)[64]) {
-                        pin32(s, 0);
-                        pin32(s, 32);
-                    };
-                    auto max_half = [&](const uint32_t(&s)[64]) {
-                        float x[4];
+                    tmem_wait_st();
+                }
+                // half h of the scores (32 pairs)
+                auto load_half = [&](int h, uint32_t(&s)[64]) {
+                    tmem_ld32_async(s_addr + 64 * h, s, 0);
+                    tmem_ld32_async(s_addr + 64 * h + 32, s, 32);
+                };
+                auto pin_half = [&](uint32_t(&s)[64]) {
+                    pin32(s, 0);
+                    pin32(s, 32);
+                };
+                auto max_half = [&](const uint32_t(&s)[64]) {
+                    float x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = max3(__uint_as_float(s[3 * j]), __uint_as_float(s[3 * j + 1]), __uint_as_float(s[3 * j + 2]));
+#pragma unroll
+                    for (int i = 12; i < 60; i += 8)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            x[j] = max3(__uint_as_float(s[3 * j]), __uint_as_float(s[3 * j + 1]), __uint_as_float(s[3 * j + 2]));
+                            x[j] = max3(x[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
+                    return fmaxf(max3(x[0], x[1], __uint_as_float(s[60])),
+                                 max3(max3(x[2], x[3], __uint_as_float(s[61])), __uint_as_float(s[62]), __uint_as_float(s[63])));
+                };
+                // weights 2^(s scale - m) as bf16 pairs, and their sum
+                const uint64_t sl22 = pack2(sl2, sl2);
+                auto weights = [&](const uint32_t(&s)[64], uint32_t(&pk)[32]) {
+                    const float neg = m == -INFINITY ? 0.0f : -m;
+                    const uint64_t neg2 = pack2(neg, neg);
+                    uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-                        for (int i = 12; i < 60; i += 8)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                x[j] = max3(x[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
-                        return fmaxf(max3(x[0], x[1], __uint_as_float(s[60])),
-                                     max3(max3(x[2], x[3], __uint_as_float(s[61])), __uint_as_float(s[62]), __uint_as_float(s[63])));
-                    };
-                    // weights 2^(s scale - m) as bf16 pairs, and their sum
-                    const uint64_t sl22 = pack2(sl2, sl2);
-                    auto weights = [&](const uint32_t(&s)[64], uint32_t(&pk)[32]) {
-                        const float neg = m == -INFINITY ? 0.0f : -m;
-                        const uint64_t neg2 = pack2(neg, neg);
-                        uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const uint64_t e2 = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sl22, neg2);
-                            float e0, e1;
-                            unpack2(e2, e0, e1);
-                            e0 = exp2_approx(e0);
-                            e1 = exp2_approx(e1);
-                            sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
-                            pk[i] = f32x2_to_bf16x2(e0, e1);
-                        }
-                        float s0, s1_, s2, s3;
-                        unpack2(sum[0], s0, s1_);
-                        unpack2(sum[1], s2, s3);
-                        return (s0 + s1_) + (s2 + s3);
-                    };
-                    // raise the maximum: at the first tile that has one, and when it is
-                    // outgrown; true if any of the warp's rows did
-                    auto raise_to = [&](float top) {
-                        const bool raise = valid && (top > m + AT_RAISE || (m == -INFINITY && top > -INFINITY));
-                        if (__builtin_expect(!__any_sync(0xFFFFFFFFu, raise), 1)) return false;
-                        const float m_new = raise ? top : m;
-                        const float f = m == -INFINITY ? 0.0f : exp2_approx(m - m_new);
-                        m = m_new;
-                        l *= f;
-                        if (mine > 0) {
-                            // the O so far belongs to the old maximum
-                            alive = wait(&c.o_full[w], steps - 1);
-                            tc_fence_after();
+                    for (int i = 0; i < 32; ++i) {
+                        const uint64_t e2 = fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sl22, neg2);
+                        float e0, e1;
+                        unpack2(e2, e0, e1);
+                        e0 = exp2_approx(e0);
+                        e1 = exp2_approx(e1);
+                        sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
+                        pk[i] = f32x2_to_bf16x2(e0, e1);
+                    }
+                    float s0, s1_, s2, s3;
+                    unpack2(sum[0], s0, s1_);
+                    unpack2(sum[1], s2, s3);
+                    return (s0 + s1_) + (s2 + s3);
+                };
+                // raise the maximum: at the first tile that has one, and when it is
+                // outgrown; true if any of the warp's rows did
+                auto raise_to = [&](float top) {
+                    const bool raise = valid && (top > m + AT_RAISE || (m == -INFINITY && top > -INFINITY));
+                    if (__builtin_expect(!__any_sync(0xFFFFFFFFu, raise), 1)) return false;
+                    const float m_new = raise ? top : m;
+                    const float f = m == -INFINITY ? 0.0f : exp2_approx(m - m_new);
+                    m = m_new;
+                    l *= f;
+                    if (mine > 0) {
+                        // the O so far belongs to the old maximum
+                        alive = wait(&c.o_full[w], steps - 1);
+                        tc_fence_after();
 #pragma unroll 1
-                            for (int i = 0; i < D && alive; i += 16) {
-                                uint32_t o[16];
-                                tmem_ld16_async(lane_base + G::O_COL + 128 * w + i, o);
-                                tmem_wait_ld();
-                                pin16(o);
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_st16(lane_base + G::O_COL + 128 * w + i, o);
-                            }
-                        }
-                        return true;
-                    };
-                    // a half's weights over its own scores
-                    auto publish = [&](int h, const uint32_t(&pk)[32]) {
-                        tmem_st32(s_addr + 64 * h, pk);
-                        tmem_wait_st();
-                        tc_fence_before();
-                    };
-                    // the product with the first half of V may start
-                    auto half_done = [&]() {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_n(&c.p_full[w][0], arrivals);
-                    };
-                    if constexpr (G::MX8) {
-                        // one half at a time, its scores read twice: fewer registers and
-                        // half the code (327 against 367 us for the mixed batch; the bf16
-                        // kernel, with registers for both halves, loses 1-4 %)
-                        uint32_t s0[64], pk[32];
-                        float top = -INFINITY;
-#pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {
-                            load_half(h, s0);
+                        for (int i = 0; i < D && alive; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_async(lane_base + G::O_COL + 128 * w + i, o);
                             tmem_wait_ld();
-                            pin_half(s0);
-                            top = fmaxf(top, max_half(s0));
+                            pin16(o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st16(lane_base + G::O_COL + 128 * w + i, o);
                         }
-                        raise_to(top * sl2);
-                        if (!alive) break;
+                    }
+                    return true;
+                };
+                // a half's weights over its own scores
+                auto publish = [&](int h, const uint32_t(&pk)[32]) {
+                    tmem_st32(s_addr + 64 * h, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                };
+                // the product with the first half of V may start
+                auto half_done = [&]() {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_n(&c.p_full[w][0], arrivals);
+                };
+                if constexpr (G::MX8) {
+                    // one half at a time, its scores read twice: fewer registers and
+                    // half the code (327 against 367 us for the mixed batch; the bf16
+                    // kernel, with registers for both halves, loses 1-4 %)
+                    uint32_t s0[64], pk[32];
+                    float top = -INFINITY;
 #pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {
-                            load_half(h, s0);
-                            tmem_wait_ld();
-                            pin_half(s0);
-                            l += weights(s0, pk);
-                            publish(h, pk);
-                            if (h == 0) half_done();
-                        }
-                    } else {
-                        // the first half's weights against the maximum so far, while the
-                        // tile's maximum is found; again in the rare case that it is raised,
-                        // and only then at the piece's first tile, which sets it
-                        uint32_t s0[64], s1[64], pk[32];
-                        load_half(0, s0);
-                        load_half(1, s1);
+                    for (int h = 0; h < 2; ++h) {
+                        load_half(h, s0);
                         tmem_wait_ld();
                         pin_half(s0);
-                        pin_half(s1);
-                        const float top = fmaxf(max_half(s0), max_half(s1)) * sl2;
-                        float sum = 0.0f;
-                        if (mine > 0) sum = weights(s0, pk);
-                        if (__builtin_expect(raise_to(top) || mine == 0, 0)) {
-                            if (!alive) break;
-                            load_half(0, s0);
-                            tmem_wait_ld();
-                            pin_half(s0);
-                            sum = weights(s0, pk);
-                        }
-                        publish(0, pk);
-                        half_done();
-                        sum += weights(s1, pk);
-                        publish(1, pk);
-                        l += sum;
+                        top = fmaxf(top, max_half(s0));
                     }
+                    raise_to(top * sl2);
+                    if (!alive) break;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        load_half(h, s0);
+                        tmem_wait_ld();
+                        pin_half(s0);
+                        l += weights(s0, pk);
+                        publish(h, pk);
+                        if (h == 0) half_done();
+                    }
+                } else {
+                    // the first half's weights against the maximum so far, while the
+                    // tile's maximum is found; again in the rare case that it is raised,
+                    // and only then at the piece's first tile, which sets it
+                    uint32_t s0[64], s1[64], pk[32];
+                    load_half(0, s0);
+                    load_half(1, s1);
+                    tmem_wait_ld();
+                    pin_half(s0);
+                    pin_half(s1);
+                    const float top = fmaxf(max_half(s0), max_half(s1)) * sl2;
+                    float sum = 0.0f;
+                    if (mine > 0) sum = weights(s0, pk);
+                    if (__builtin_expect(raise_to(top) || mine == 0, 0)) {
+                        if (!alive) break;
+                        load_half(0, s0);
+                        tmem_wait_ld();
+                        pin_half(s0);
+                        sum = weights(s0, pk);
+                    }
+                    publish(0, pk);
+                    half_done();
+                    sum += weights(s1, pk);
+                    publish(1, pk);
+                    l += sum;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive_n(&c.p_full[w][1], arrivals);
@@ -1311,7 +1312,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 pc.end = !some;
                 int ok = 1;
                 if (lane == 0) {
-                    if (np >= AT_RING) ok = at_wait(&c.r_free[np % AT_RING], ((np / AT_RING) - 1) & 1, abort_flag, prm.wait_ns, NAP_P);
+                    if (np >= AT_RING) ok = at_wait(&c.r_free[np % AT_RING], ((np / AT_RING) - 1) & 1, abort_flag, prm.wait_ns);
                     if (ok) {
                         c.ring[np % AT_RING] = pc;
                         mbar_arrive(&c.r_full[np % AT_RING]);
@@ -1344,7 +1345,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     pdl_wait();
                     waited = true;
                 }
-                if (lane == 0 && piece > 0) ok = at_wait(&c.q_empty, (piece - 1) & 1, abort_flag, prm.wait_ns, NAP_P);
+                if (lane == 0 && piece > 0) ok = at_wait(&c.q_empty, (piece - 1) & 1, abort_flag, prm.wait_ns);
                 if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
                 if (lane == 0 && !prm.stall) {
                     const uint32_t dst = smem_u32(smem);
@@ -1389,7 +1390,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     const int copies = __popc(__ballot_sync(0xFFFFFFFFu, here && ids >= 0));
                     if (__any_sync(0xFFFFFFFFu, here && ids == -2) && lane == 0) c.missing[piece & 7] = 1;
                     uint64_t *bar = (G::MX8 ? c_full : full) + slot.i;
-                    if (!fresh && !warp_wait((G::MX8 ? c_empty : empty) + slot.i, slot.phase ^ 1, abort_flag, prm.wait_ns, NAP_P))
+                    if (!fresh && !warp_wait((G::MX8 ? c_empty : empty) + slot.i, slot.phase ^ 1, abort_flag, prm.wait_ns))
                         return false;
                     if (elected)
                         mbar_arrive_expect_tx(bar, (uint32_t)(copies * prm.page_rows) *
@@ -1434,9 +1435,9 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 if (lane == 0) {
                     constexpr int RING = G::MX8 ? G::C_SLOTS : G::SLOTS;
                     for (int i = max(load - RING, 0); i < load; ++i)
-                        at_wait(G::MX8 ? &c_full[i % RING] : &full[i % RING], (i / RING) & 1, abort_flag, AT_WAIT_NS, NAP_P, false);
-                    if (!prm.stall && piece > 0) at_wait(&c.q_full, (piece - 1) & 1, abort_flag, AT_WAIT_NS, NAP_P, false);
-                    if (!prm.stall) at_wait(&c.q_full, piece & 1, abort_flag, 1000000ull, NAP_P, false);
+                        at_wait(G::MX8 ? &c_full[i % RING] : &full[i % RING], (i / RING) & 1, abort_flag, AT_WAIT_NS, false);
+                    if (!prm.stall && piece > 0) at_wait(&c.q_full, (piece - 1) & 1, abort_flag, AT_WAIT_NS, false);
+                    if (!prm.stall) at_wait(&c.q_full, piece & 1, abort_flag, 1000000ull, false);
                 }
             }
         } else if (warp == 9) {
@@ -1457,7 +1458,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             uint32_t p_phase[2] = {0, 0};  // of each group's p_full
             bool go = true;
             auto wait = [&](uint64_t *bar, uint32_t phase) {
-                return warp_wait(bar, phase, abort_flag, prm.wait_ns, NAP_M);
+                return warp_wait(bar, phase, abort_flag, prm.wait_ns);
             };
             auto commit = [&](uint64_t *bar) {
                 if (elected) umma_commit(bar);
@@ -1561,13 +1562,13 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 bool go = true;
                 for (int np = 0; go && take(np) && !pc.end; ++np) {
                     for (int left = 2 * (pc.k1 - pc.k0); left > 0; --left) {
-                        go = warp_wait(&c_full[sc.i], sc.phase, abort_flag, prm.wait_ns, NAP_D);
+                        go = warp_wait(&c_full[sc.i], sc.phase, abort_flag, prm.wait_ns);
                         if (!go) break;
                         const uint8_t *codes = smem + G::OFF_C + sc.i * G::CODES + block * 32;
                         const uint8_t *scales = smem + G::OFF_SC + sc.i * G::SCALES + block;
                         uint8_t *tile = smem + G::OFF_KV + sd.i * G::TILE + slab * G::SLAB;
                         if (!fresh) {
-                            go = warp_wait(&empty[sd.i], sd.phase ^ 1, abort_flag, prm.wait_ns, NAP_D);
+                            go = warp_wait(&empty[sd.i], sd.phase ^ 1, abort_flag, prm.wait_ns);
                             if (!go) break;
                         }
 #pragma unroll 1
@@ -1596,7 +1597,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     }
     __syncthreads();
     if (warp == 9) {
-        if (lane == 0) at_wait(&c.done, 0, abort_flag, AT_WAIT_NS, NAP_P, false);
+        if (lane == 0) at_wait(&c.done, 0, abort_flag, AT_WAIT_NS, false);
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
