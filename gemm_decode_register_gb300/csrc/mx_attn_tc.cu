@@ -664,9 +664,11 @@ __device__ __forceinline__ float *partial_base(const AtParams &p, int cta, int w
 }
 
 // A row whose sum over the tiles came out NaN or infinite, computed again from
-// its own keys alone: a product with a weight of zero is not zero when the
-// value is NaN or infinite, and such a value may lie where the row may not
-// see it.  By the whole warp; q_row: MAX_D floats of shared memory per warp.
+// its own keys alone, by the whole warp: a product with a weight of zero is not
+// zero when the value is NaN or infinite, and such a value may lie where the
+// row may not see it; and values near the type's largest can overflow a sum
+// whose weights are divided only at its end (here each weight is divided
+// first), so rows that see all keys are computed again too.
 template <int KVF>
 __device__ __noinline__ void row_again(const AttnArgs &a, int b, int t, int h, int lo, int hi, int d0, int d1,
                                        float inv_total, float m_used)
@@ -804,7 +806,7 @@ __device__ __noinline__ void arrive_cut(const AtParams &p, const Piece &piece, i
         const int row = (tid & ~31) + __ffs(left) - 1;
         const int tok = t0 + row / a.g, head = pc.kvh * a.g + row % a.g, pos = pc.first + tok;
         const int hi = a.causal ? min(pos + 1, pc.len) : pc.len;
-        const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+        const int lo = a.window > 0 ? (int)max((long long)pos - a.window + 1, 0ll) : 0;
         float m = -INFINITY, total = 0.0f;
         for (int i = 0; i < parts; ++i) {
             const float2 ml = __ldcg(reinterpret_cast<const float2 *>(partial_base<D>(p, pc.c0 + i, i == 0 ? 1 : 0, w)) + row);
@@ -955,7 +957,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             int rlo = 0, rhi = 0x7FFFFFFF;  // (a lane without a row needs no mask)
             if (valid) {
                 rhi = a.causal ? min(pos + 1, pc.len) : pc.len;
-                rlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+                rlo = a.window > 0 ? (int)max((long long)pos - a.window + 1, 0ll) : 0;
                 if (rhi < rlo) rhi = rlo;
             }
             // warps with rows, the first ones of the group; the others go to the

@@ -395,3 +395,15 @@ def test_mxfp8_values_are_exact(D):
         nan = torch.isnan(want)
         assert torch.equal(torch.isnan(got), nan)
         assert torch.equal(got[~nan], want[~nan])
+
+
+def test_large_windows_and_many_sequences():
+    """A window of the largest size is no window; more sequences than a warp looks at in a round, some empty."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    b = Batch([3, 40, 1], [2, 100, 300], 8, 1, 128, 16)
+    assert torch.equal(b.check()[0], b.check(window=(1 << 31) - 1)[0])
+    n = [i % 3 for i in range(75)]
+    Batch(n, [x + 7 * i % 190 for i, x in enumerate(n)], 4, 2, 64, 16, "mxfp8").check()
+    Batch([1] * 1100, [1 + i % 40 for i in range(1100)], 2, 1, 64, 16).check()
