@@ -8,8 +8,9 @@
 // (s -> -s) is the transpose, i.e. the gradient.
 //
 // Both kernels move each element once and are bound by HBM for prompts, by
-// the chain of dependent loads (sequence, length, page, table row) and the
-// launch for single tokens.
+// the launch and the chain of dependent loads (sequence, length, page, table
+// row) for single tokens: 4 tokens x 72 heads x 128 turn in 2.4 us, and are
+// appended in 2.5 us.
 #include "mx_attn.cuh"
 
 namespace mx {
@@ -141,7 +142,9 @@ constexpr int ROPE_HEADS = 4;  // heads a thread takes, with the same cosines an
 // neighbouring ones; the second may be missing.  A thread takes one unit of ROPE_HEADS
 // heads (chunk, chunk + chunks, ...) of a token, so its cosines and sines are
 // loaded once and its loads are all in flight together; consecutive threads
-// take consecutive units, then consecutive heads.
+// take consecutive units, then consecutive heads.  HBM bounds it: 4096 x 64
+// heads x 128 bf16 in 24.6 us, 82 % of a plain copy's rate, 5003 x 64 x 64
+// fp32 in 25.4 us, 97 %.
 template <typename T, int NV, bool INTER>
 __global__ void __launch_bounds__(256) rope_kernel(const T *x, T *y, RopeArgs a)
 {
@@ -245,7 +248,8 @@ static cudaError_t run_rope(cudaStream_t st, const void *x, void *y, RopeArgs a,
 {
     constexpr int N = Vec<T>::N;
     // 16-byte accesses need every vector of every head aligned, and whole vectors on both sides of `rot`
-    // (of rot / 2 where the halves are the pairs)
+    // (of rot / 2 where the halves are the pairs).  4096 x 64 heads x 128 bf16: 23.2 us, and 56.0 us
+    // by single elements (the same call, one element off).
     const uintptr_t addr = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y);
     const bool vec = (addr & 15u) == 0 && (a.xt | a.xh | a.yt | a.yh) % N == 0 && a.D % N == 0 &&
                      (inter ? a.rot : a.rot / 2) % N == 0 && a.rot % N == 0;
@@ -303,7 +307,15 @@ struct AppendArgs {
 
 constexpr int APPEND_THREADS = 256;
 constexpr int APPEND_VECTORS = 2;  // vectors of eight elements a thread of the any-layout kernel takes
-constexpr int APPEND_FEW = 64;     // tokens
+
+// Blocks per SM of kv_append_kernel, by its registers: three for bf16 rows (45
+// -> 37 us at 4096 x 80 heads x 128 into MXFP8), two for fp32 rows, which
+// would spill (49 against 57 us; one token per block).
+template <typename T>
+constexpr int append_resident()
+{
+    return sizeof(T) == 2 ? 3 : 2;
+}
 
 // Eight elements of a row as they lie, and as fp32.
 template <typename T>
@@ -403,20 +415,24 @@ __device__ __forceinline__ void cache8(const AppendArgs &a, const Place &at, boo
 
 constexpr int APPEND_HEADS = 3;  // heads a thread takes at a time
 
-// One block per token (and part of its heads): a thread takes unit u, two
-// vectors of eight elements, of heads slot, slot + slots, ...; in the half layout the
+// A block takes a token (or part of its heads), with MANY one token after the
+// other; a thread takes unit u, two vectors of eight elements, of heads slot, slot + slots, ...; in the half layout the
 // two vectors of a turning unit turn with each other, so nothing is read
 // twice and the cosines and sines are loaded once for all heads.  Needs whole units, and
 // for MXFP8 blocks of 32 that lie in four neighbouring lanes (append_units_ok).
-// The row's loads are issued before the search for the token's place.
-// Three blocks per SM for bf16 rows (45 -> 37 us at 4096 x 80 heads x 128 into
-// MXFP8, against 24 us of HBM time), two for fp32 rows, whose registers would spill
-// (49 against 57 us).
-template <typename T, int KVF, bool INTER>
-__global__ void __launch_bounds__(APPEND_THREADS, sizeof(T) == 2 ? 3 : 2) kv_append_kernel(const T *__restrict__ rows, AppendArgs a)
+// The row's loads are issued before the search for the token's place, a chain of
+// four or five loads; with MANY each warp searches for one of the block's next
+// tokens, so the chain is gone through once for as many.
+// Bound by HBM: 4096 x 80 heads x 128 bf16 into MXFP8 33.2 us (73 % of a plain copy's
+// rate; 37.2 with a block for each token), 8192 tokens 61.5 us (78 %; 68.4),
+// fp32 rows 80.6 us (92.6).  Up to as many tokens as blocks are resident the loop only
+// costs (one token 2.8 us, 3.2 with it).
+template <typename T, int KVF, bool INTER, bool MANY>
+__global__ void __launch_bounds__(APPEND_THREADS, append_resident<T>()) kv_append_kernel(const T *__restrict__ rows, AppendArgs a)
 {
     pdl_trigger();
-    const int t = blockIdx.x, D = a.kv.D, units = D / 16, slots = a.slots;
+    __shared__ Place places[APPEND_THREADS / 32];
+    const int D = a.kv.D, units = D / 16, slots = a.slots, warps = blockDim.x / 32;
     const int slot = threadIdx.x / units, u = threadIdx.x - slot * units;
     const int turning = a.Hq + a.kv.Hkv, half = a.rot / 2, hu = a.rot / 16;
     // the unit's vectors in heads that turn (half layout: partners) and in the others
@@ -425,77 +441,95 @@ __global__ void __launch_bounds__(APPEND_THREADS, sizeof(T) == 2 ? 3 : 2) kv_app
     const int dt1 = INTER ? dt0 + D / 2 : (partners ? dt0 + half : dt0 + (D - a.rot) / 2);
     const int dv0 = 8 * u, dv1 = dv0 + D / 2;
     pdl_wait();
-    const T *row = rows + t * a.row_stride;
-    Place at;
     float c0[8], s0[8], c1[4], s1[4];
     const int step = slots * gridDim.y;  // heads a round of all blocks of the token covers
-    for (int h0 = slot < slots ? blockIdx.y * slots + slot : a.heads, round = 0;; h0 += APPEND_HEADS * step, ++round) {
-        const bool some = h0 < a.heads;
-        Raw8<T> r0[APPEND_HEADS], r1[APPEND_HEADS];
-        if (some)
+    int i = 0;
+    int t = blockIdx.x;
+    do {
+        const T *row = rows + t * a.row_stride;
+        Place at;
+        for (int h0 = slot < slots ? blockIdx.y * slots + slot : a.heads, round = 0;; h0 += APPEND_HEADS * step, ++round) {
+            const bool some = h0 < a.heads;
+            Raw8<T> r0[APPEND_HEADS], r1[APPEND_HEADS];
+            if (some)
+#pragma unroll
+                for (int k = 0; k < APPEND_HEADS; ++k) {
+                    const int h = h0 + k * step;
+                    if (h >= a.heads) break;
+                    r0[k].load(row + (long long)h * D + (h < turning ? dt0 : dv0));
+                    r1[k].load(row + (long long)h * D + (h < turning ? dt1 : dv1));
+                }
+            if (round == 0) {
+                if constexpr (!MANY) {
+                    at = place_of(a, t, threadIdx.x == 0 && blockIdx.y == 0);
+                } else if (i % warps == 0) {  // a warp for each of the block's next tokens
+                    __syncthreads();
+                    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+                    const long long mine = t + (long long)warp * gridDim.x;
+                    if (mine < a.T) {
+                        const Place p = place_of(a, (int)mine, lane == 0 && blockIdx.y == 0);
+                        if (lane == 0) places[warp] = p;
+                    }
+                    __syncthreads();
+                }
+                if constexpr (MANY) at = places[i % warps];
+                if (!at.some) break;
+                const float2 *cs = reinterpret_cast<const float2 *>(a.table) + (at.pos_ok ? at.pos : 0) * half;
+                if (partners) load_angles<8>(cs, dt0, c0, s0);
+                if constexpr (INTER) {
+                    float ca[4], sa[4];
+                    if (dt0 < a.rot) load_angles<4>(cs, dt0 / 2, ca, sa);
+                    if (dt1 < a.rot) load_angles<4>(cs, dt1 / 2, c1, s1);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        c0[j] = ca[j];
+                        s0[j] = sa[j];
+                    }
+                }
+            }
+            if (!some) break;
 #pragma unroll
             for (int k = 0; k < APPEND_HEADS; ++k) {
                 const int h = h0 + k * step;
                 if (h >= a.heads) break;
-                r0[k].load(row + (long long)h * D + (h < turning ? dt0 : dv0));
-                r1[k].load(row + (long long)h * D + (h < turning ? dt1 : dv1));
-            }
-        if (round == 0) {
-            at = place_of(a, t, threadIdx.x == 0 && blockIdx.y == 0);
-            if (!at.some) return;
-            const float2 *cs = reinterpret_cast<const float2 *>(a.table) + (at.pos_ok ? at.pos : 0) * half;
-            if (partners) load_angles<8>(cs, dt0, c0, s0);
-            if constexpr (INTER) {
-                float ca[4], sa[4];
-                if (dt0 < a.rot) load_angles<4>(cs, dt0 / 2, ca, sa);
-                if (dt1 < a.rot) load_angles<4>(cs, dt1 / 2, c1, s1);
+                float v0[8], v1[8];
+                r0[k].get(v0);
+                r1[k].get(v1);
+                if (h < turning) {
+                    if (partners) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    c0[j] = ca[j];
-                    s0[j] = sa[j];
-                }
-            }
-        }
-        if (!some) break;
+                        for (int j = 0; j < 8; ++j) turn(v0[j], v1[j], c0[j], s0[j]);
+                    }
+                    if constexpr (INTER) {
 #pragma unroll
-        for (int k = 0; k < APPEND_HEADS; ++k) {
-            const int h = h0 + k * step;
-            if (h >= a.heads) break;
-            float v0[8], v1[8];
-            r0[k].get(v0);
-            r1[k].get(v1);
-            if (h < turning) {
-                if (partners) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) turn(v0[j], v1[j], c0[j], s0[j]);
-                }
-                if constexpr (INTER) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (dt0 < a.rot) turn(v0[2 * j], v0[2 * j + 1], c0[j], s0[j]);
-                        if (dt1 < a.rot) turn(v1[2 * j], v1[2 * j + 1], c1[j], s1[j]);
+                        for (int j = 0; j < 4; ++j) {
+                            if (dt0 < a.rot) turn(v0[2 * j], v0[2 * j + 1], c0[j], s0[j]);
+                            if (dt1 < a.rot) turn(v1[2 * j], v1[2 * j + 1], c1[j], s1[j]);
+                        }
                     }
                 }
-            }
-            if (h < a.Hq) {
-                if (at.page < 0)
+                if (h < a.Hq) {
+                    if (at.page < 0)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v0[j] = v1[j] = __uint_as_float(0x7FC00000u);
-                uint16_t *q = a.q + ((size_t)t * a.Hq + h) * D;
-                *reinterpret_cast<uint4 *>(q + dt0) = Vec<uint16_t>::put(v0);
-                *reinterpret_cast<uint4 *>(q + dt1) = Vec<uint16_t>::put(v1);
-            } else if (at.page >= 0) {
-                const bool is_v = h >= turning;
-                cache8<KVF>(a, at, is_v, h - (is_v ? turning : a.Hq), is_v ? dv0 : dt0, v0);
-                cache8<KVF>(a, at, is_v, h - (is_v ? turning : a.Hq), is_v ? dv1 : dt1, v1);
+                        for (int j = 0; j < 8; ++j) v0[j] = v1[j] = __uint_as_float(0x7FC00000u);
+                    uint16_t *q = a.q + ((size_t)t * a.Hq + h) * D;
+                    *reinterpret_cast<uint4 *>(q + dt0) = Vec<uint16_t>::put(v0);
+                    *reinterpret_cast<uint4 *>(q + dt1) = Vec<uint16_t>::put(v1);
+                } else if (at.page >= 0) {
+                    const bool is_v = h >= turning;
+                    cache8<KVF>(a, at, is_v, h - (is_v ? turning : a.Hq), is_v ? dv0 : dt0, v0);
+                    cache8<KVF>(a, at, is_v, h - (is_v ? turning : a.Hq), is_v ? dv1 : dt1, v1);
+                }
             }
         }
-    }
+        // (by the distance left: t + gridDim.x could pass 32 bits)
+    } while (MANY && a.T - t > (int)gridDim.x && (t += gridDim.x, ++i, true));
 }
 
 // Whether kv_append_kernel's units fit: whole vectors on both sides of rot (of
 // rot / 2 in the half layout), units that divide a block of threads, and blocks of MXFP8
-// in four neighbouring lanes.
+// in four neighbouring lanes.  4096 x 80 heads x 128 into bf16 29 us, MXFP8 33 us; by
+// kv_append_any_kernel (rot = 120) 95 and 98 us.
 static bool append_units_ok(const AppendArgs &a, bool inter)
 {
     const int D = a.kv.D, unit = a.kv.kv_fmt == KV_MXFP8 ? 64 : 16;
@@ -578,18 +612,26 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_any_kernel(const T *
 }
 
 template <typename T, int KVF>
-static cudaError_t run_append(cudaStream_t st, const void *rows, AppendArgs a, bool inter)
+static cudaError_t run_append(cudaStream_t st, int sms, const void *rows, AppendArgs a, bool inter)
 {
     const T *r = static_cast<const T *>(rows);
     if (append_units_ok(a, inter)) {
-        // a block as large as a token's heads need; few tokens: a block for each
-        // round of heads, so that no load waits for another
+        // a block as large as a token's heads need; a block for each round of heads
+        // where all of them are resident, so that no load waits for another (80 heads
+        // into MXFP8: one token 2.8 us, 3.2 with one block, 128 tokens 3.9 against 4.2;
+        // 512 tokens, not resident, 10.2 against 6.9)
         const int units = a.kv.D / 16, most = APPEND_THREADS / units;
         a.slots = a.heads < most ? a.heads : most;
         const dim3 block((unsigned)(a.slots * units + 31) / 32 * 32);
-        const dim3 grid((unsigned)a.T, a.T < APPEND_FEW ? (unsigned)((a.heads + a.slots - 1) / a.slots) : 1u);
-        if (inter) return launch_k(kv_append_kernel<T, KVF, true>, grid, block, 0, st, r, a);
-        return launch_k(kv_append_kernel<T, KVF, false>, grid, block, 0, st, r, a);
+        const int resident = sms * (append_resident<T>() * APPEND_THREADS / (int)block.x);
+        const int rounds = (a.heads + a.slots - 1) / a.slots;
+        const bool few = (long long)a.T * rounds <= resident;
+        const dim3 grid((unsigned)(a.T < resident ? a.T : resident), few ? (unsigned)rounds : 1u);
+        if (a.T <= resident)
+            return inter ? launch_k(kv_append_kernel<T, KVF, true, false>, grid, block, 0, st, r, a)
+                         : launch_k(kv_append_kernel<T, KVF, false, false>, grid, block, 0, st, r, a);
+        return inter ? launch_k(kv_append_kernel<T, KVF, true, true>, grid, block, 0, st, r, a)
+                     : launch_k(kv_append_kernel<T, KVF, false, true>, grid, block, 0, st, r, a);
     }
     const int total = a.heads * (a.kv.D / 8), per_block = APPEND_THREADS * APPEND_VECTORS;
     const dim3 grid((unsigned)a.T, (unsigned)((total + per_block - 1) / per_block));
@@ -617,10 +659,10 @@ cudaError_t launch_kv_append(const DeviceState &ds, cudaStream_t st, const mx_pa
     a.err = ds.err;
     const bool inter = (flags & MX_ROPE_INTERLEAVED) != 0;
     if (kv.kv_fmt == KV_MXFP8)
-        return dtype == MX_F32 ? run_append<float, KV_MXFP8>(st, rows, a, inter)
-                               : run_append<uint16_t, KV_MXFP8>(st, rows, a, inter);
-    return dtype == MX_F32 ? run_append<float, KV_BF16>(st, rows, a, inter)
-                           : run_append<uint16_t, KV_BF16>(st, rows, a, inter);
+        return dtype == MX_F32 ? run_append<float, KV_MXFP8>(st, ds.num_sms, rows, a, inter)
+                               : run_append<uint16_t, KV_MXFP8>(st, ds.num_sms, rows, a, inter);
+    return dtype == MX_F32 ? run_append<float, KV_BF16>(st, ds.num_sms, rows, a, inter)
+                           : run_append<uint16_t, KV_BF16>(st, ds.num_sms, rows, a, inter);
 }
 
 }  // namespace mx

@@ -233,3 +233,40 @@ def test_append_faults_and_rows_of_no_sequence():
     q, err = call([2, 42])  # beyond the rotation table (and the block table)
     assert err == 0x8 and torch.isnan(q[2:4]).all()
     assert (kv.k[2] == 0).all()
+
+
+THOUSANDS = [3900, 0, 1, 3] + [5 * i % 7 for i in range(230)] + [2099]
+LENS["thousands"] = (THOUSANDS, [n + 13 * n % 50 for n in THOUSANDS])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("D,Hq,Hkv,interleaved", [(64, 1, 1, False), (64, 30, 5, True), (128, 26, 3, False)])
+def test_append_more_tokens_than_blocks(fmt, dtype, D, Hq, Hkv, interleaved):
+    """Blocks that take token after token, sequences of none to many tokens between them."""
+    test_append(fmt, dtype, D, Hq, Hkv, 16, "thousands", D, interleaved, False)
+
+
+def test_append_faults_among_many_tokens():
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    D, page, n = 64, 16, 8000
+    bt = torch.arange(n // page, dtype=torch.int32, device="cuda")[None].clone()
+    bt[0, 300] = -1
+    kv = ops.PagedKV.empty(n // page, 2, page, D, bt)
+    kv.k.zero_()
+    f, factor = ops.rope_frequencies(D)
+    table = ops.rope_table(f, 7000, factor)
+    rows = torch.randn((n + 5, 8 * D), device="cuda")
+    qs, kl = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n], [n]))
+    q = torch.full((n + 5, 4, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    ops.kv_append(kv, rows, qs, kl, 4, table, q=q)
+    assert ops.device_error() == 0x4 | 0x8
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[300 * page:301 * page] = True
+    bad[7000:] = True
+    assert torch.equal(torch.isnan(q[:n]).all(2).all(1), bad) and torch.isfinite(q[:n][~bad]).all()
+    assert (q[n:] == 5).all()
+    stored = (kv.k != 0).any(3).any(1).view(-1)
+    assert torch.equal(stored, ~bad)
