@@ -26,7 +26,19 @@
 // items laid end to end, each as long as the keys it sees, are divided into
 // equal stretches, one per CTA, so that any mix of prompts and single tokens
 // loads every SM the same.  An item cut across CTAs leaves partial (m, l, O)
-// rows in the workspace and the last CTA to arrive adds them in order.
+// rows in the workspace and the last CTA to arrive adds them in order.  Few
+// and short items are not cut (AT_WHOLE_KEYS).
+//
+// P is rounded to bf16 because the tensor cores take their operands so: each
+// weight is off by 2^-9 of itself, as the values of a bf16 cache are already, and
+// the sum that divides them is of the unrounded weights.  64 heads on 8 of 128:
+//   prompt of 4096 on 8192     558 us  1.47 PFLOP/s, 77 % of the measured rate
+//   64 tokens on 0.5-8 K       185 us  6.2 TB/s, 93 % of the measured copy
+//   16 x 2-6 tokens on 1-16 K  104 us  5.9 TB/s
+//   one token on 131 keys        9 us  a chain of latencies
+//   MXFP8, 5 tokens on 24-66 K 204 us  the decode to bf16
+// A prompt is bound by the softmax between two MMAs of a group (tensor cores
+// busy 52 % of the time, as the MMAs' own rate goes), single tokens by HBM.
 //
 //   warps 0-3, 4-7  softmax groups and epilogue
 //   warp 9          MMA issuer
@@ -49,10 +61,24 @@ namespace mx {
 constexpr int AT_ROWS = 128;  // rows of a tile
 constexpr int AT_KEYS = 128;  // keys of a tile
 constexpr int AT_SPLIT_KEYS = 2 * AT_KEYS;  // what an item costs beside its keys, and more than its tiles' rounding
-constexpr int AT_Q_COPIES = 4;              // up to so many tokens are loaded one by one
-constexpr int AT_MIN_KEYS = 3 * AT_KEYS;      // shortest stretch of a CTA that only divides an item
+// Up to so many tokens' queries are copied one by one, of more the whole row tile
+// (8 sequences on 1024: 2 tokens each 21.2 us, 22.0 as a tile; 8 tokens each
+// 28.4 as a tile, 30.5 one by one).
+constexpr int AT_Q_COPIES = 4;
+// Items of up to so many keys are not cut when there is a CTA for each; more when
+// they have two row tiles, whose parts cost more to add up.  Uncut against cut,
+// 64 on 8 heads x 128 bf16, us: one token on 512 keys 9.4, 12.9; on 1024 13.6,
+// 13.3; on 1500 20.0, 13.4; 16 sequences of 50 to 1000 keys 18.0, 23.5; prompts:
+// 512 on 512 17.0, 31.8; 2 x 128 on 1500 28.5, 43.5; 32 on 2000 32.3, 35.2
+// (MXFP8 44.3, 40.3).
+constexpr int AT_WHOLE_KEYS = 8 * AT_KEYS, AT_WHOLE_KEYS_2 = 16 * AT_KEYS;
+// Shortest stretch of a CTA that only divides an item (one token on 2048 keys: 13.1
+// us; 2 tiles 13.4, 6 tiles 15.7).
+constexpr int AT_MIN_KEYS = 3 * AT_KEYS;
 constexpr int AT_RING = 3;                  // pieces the producer may run ahead by
-constexpr float AT_RAISE = 8.0f;            // log2 by which scores may outgrow the maximum before it is raised
+// log2 by which scores may outgrow the maximum before it is raised (0: the
+// prompt of 4096 on 8192 takes 782 us instead of 560)
+constexpr float AT_RAISE = 8.0f;
 constexpr unsigned long long AT_WAIT_NS = 2000000000ull;
 
 template <int D, int KVF>
@@ -123,11 +149,13 @@ struct Cost {
     int s2;             // tokens of a pair of row tiles
     int causal, window;
     int heads;          // cache heads
+    int flat;           // every item costs AT_SPLIT_KEYS: one CTA each
 
     // Keys before which items p, p + 1, ... of a head start (each item's own
     // keys and AT_SPLIT_KEYS): items see [lo(p), hi(p)).
     __device__ __noinline__ long long before(const Seq q, int p) const  // (one copy, for the instruction cache)
     {
+        if (flat) return (long long)p * AT_SPLIT_KEYS;
         const long long base = (long long)q.len - q.n;
         long long h = (long long)p * q.len, l = 0;
         if (causal) {
@@ -167,6 +195,7 @@ struct Stretch {
     long long at;                 // cost before the first item
     int b, kvh, p;                // the first item (b = B: none)
     int ctas;
+    int flat;  // as the cost's
 };
 
 // One piece: key tiles [k0, k1) of an item.
@@ -222,7 +251,7 @@ struct Walk {
             o.tiles = o.hi > o.lo ? (o.hi + AT_KEYS - 1) / AT_KEYS - o.tile0 : 0;
             // tile k begins at cost at + 128 k and is its CTA's whose stretch holds that
             o.k0 = st.start <= at ? 0 : (int)min((st.start - at + AT_KEYS - 1) / AT_KEYS, (long long)o.tiles);
-            o.k1 = (int)min((st.end - at + AT_KEYS - 1) / AT_KEYS, (long long)o.tiles);
+            o.k1 = st.flat ? o.tiles : (int)min((st.end - at + AT_KEYS - 1) / AT_KEYS, (long long)o.tiles);
             o.b = b;
             o.kvh = kvh;
             o.q0 = q.q0 + p * cost.s2;
@@ -236,7 +265,7 @@ struct Walk {
                 o.c1 = cta_of(at + (o.tiles - 1ll) * AT_KEYS);
             }
             const bool mine = o.tiles > 0 ? o.k0 < o.k1 : st.start <= at;
-            at += (long long)(o.hi - o.lo) + AT_SPLIT_KEYS;
+            at += (st.flat ? 0 : (long long)(o.hi - o.lo)) + AT_SPLIT_KEYS;
             if (++p >= q.pairs) {
                 p = 0;
                 ++kvh;
@@ -262,19 +291,22 @@ __device__ __forceinline__ long long warp_sum_before(long long v, long long *tot
     return inc - v;
 }
 
-__device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, Stretch &st)
+__device__ __forceinline__ void plan(const AttnArgs &a, Cost &cost, Stretch &st)
 {
     const int lane = threadIdx.x & 31, s1 = cost.s2 / 2;
-    int items = 0;  // of this lane's sequences
+    int items = 0, over = 0;  // items of this lane's sequences; is one longer than is left whole?
     auto cost_at = [&](int b) {
         if (b >= a.B) return 0ll;
         const Seq q = load_seq(a, b, s1);
         items += min(q.pairs * cost.heads, 1024);
+        const long long most = cost.window > 0 ? min((long long)q.len, (long long)cost.window + cost.s2) : q.len;
+        over |= q.pairs > 0 && most > (q.n > s1 ? AT_WHOLE_KEYS_2 : AT_WHOLE_KEYS);
         return cost.total(q);
     };
-    const long long c0 = cost_at(lane);  // of the first 32, kept
+    cost.flat = 0;
+    long long c0 = cost_at(lane);  // of the first 32, kept
     long long total, first_total;
-    const long long before0 = warp_sum_before(c0, &first_total);
+    long long before0 = warp_sum_before(c0, &first_total);
     total = first_total;
     if (a.B > 32) {
         long long rest = 0;
@@ -284,12 +316,24 @@ __device__ __forceinline__ void plan(const AttnArgs &a, const Cost &cost, Stretc
         for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
         total += rest;
     }
-    // A CTA for every item or every AT_MIN_KEYS keys, whichever are more.  Items
-    // cost at least two tiles, so a stretch is longer than a tile and no CTA
-    // between an item's first and last is left without one.
+    // Few and short items: a CTA for each, uncut.  Else, a CTA for every item or
+    // every AT_MIN_KEYS keys, whichever are more, as many to an item as to the
+    // next if they are alike.  Items cost at least two tiles, so a stretch is longer than
+    // a tile and no CTA between an item's first and last is left without one.
     const int grid = gridDim.x;
     items = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)min(items, 1 << 24));
-    const int ctas = total >= (long long)grid * AT_MIN_KEYS ? grid : max(1, min(grid, max(items, (int)total / AT_MIN_KEYS)));
+    int ctas = grid;
+    if (!__any_sync(0xFFFFFFFFu, over) && items <= grid) {
+        cost.flat = 1;
+        ctas = max(items, 1);
+        total = (long long)items * AT_SPLIT_KEYS;
+        c0 = cost_at(lane);
+        before0 = warp_sum_before(c0, &first_total);
+    } else if (total < (long long)grid * AT_MIN_KEYS) {
+        ctas = max(1, min(grid, max(items, (int)total / AT_MIN_KEYS)));
+        if (items > 0 && items < ctas) ctas -= ctas % items;
+    }
+    st.flat = cost.flat;
     const int c = blockIdx.x;
     st.total = total;
     st.ctas = ctas;
@@ -752,8 +796,9 @@ __device__ __forceinline__ bool last_of(const AtParams &p, const Piece &pc, int 
 }
 
 // Counts a group's part of a cut item; the last to come adds all parts up, in
-// their order, and writes the outputs: a thread takes four dimensions of a row,
-// neighbouring threads neighbouring rows.
+// their order, and writes the outputs: a thread takes sixteen dimensions of a row
+// (loads of four at a time left 512 tokens of prompt waiting 30 us), neighbouring
+// threads neighbouring rows.
 template <int D, int KVF>
 __device__ __noinline__ void arrive_cut(const AtParams &p, const Piece &piece, int w, int tid, volatile int *last,
                                         unsigned *again)
@@ -766,26 +811,29 @@ __device__ __noinline__ void arrive_cut(const AtParams &p, const Piece &piece, i
     const int t0 = pc.rows ? w * s1 : 0, R = min(pc.ntok - t0, s1) * a.g;
     const int d0 = pc.rows ? 0 : w * (D / 2), W = pc.rows ? D : D / 2, parts = pc.c1 - pc.c0 + 1;
     __threadfence();
-    for (int e = tid; e < R * (W / 4); e += 128) {
-        const int quad = e / R, row = e - quad * R;
+    constexpr int U = 4;  // quads a thread takes at once
+    for (int e = tid; e < R * (W / (4 * U)); e += 128) {
+        const int quad = e / R * U, row = e % R;
         const int t = pc.q0 + t0 + row / a.g, head = pc.kvh * a.g + row % a.g;
         float m = -INFINITY, total = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+        float4 o[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
         for (int i = 0; i < parts; ++i) {
             const float *pi = partial_base<D>(p, pc.c0 + i, i == 0 ? 1 : 0, w);
             const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pi) + row);
-            const float4 r = __ldcg(reinterpret_cast<const float4 *>(pi + 2 * p.part_rows) + (size_t)quad * p.part_rows + row);
-            if (i == 0) {
-                m = ml.x;
-                total = ml.y;
-                o = r;
-            } else {
-                const Merge mg(m, ml.x);
-                m = mg.m;
-                total = mg.add(total, ml.y);
-                o = make_float4(mg.add(o.x, r.x), mg.add(o.y, r.y), mg.add(o.z, r.z), mg.add(o.w, r.w));
-            }
+            const float4 *ri = reinterpret_cast<const float4 *>(pi + 2 * p.part_rows) + (size_t)quad * p.part_rows + row;
+            float4 r[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) r[k] = __ldcg(ri + (size_t)k * p.part_rows);
+            const Merge mg(m, ml.x);
+            m = mg.m;
+            total = mg.add(total, ml.y);
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                o[k] = make_float4(mg.add(o[k].x, r[k].x), mg.add(o[k].y, r[k].y), mg.add(o[k].z, r[k].z),
+                                   mg.add(o[k].w, r[k].w));
         }
         const float sink = a.sinks ? __ldg(a.sinks + head) * 1.4426950408889634f : -INFINITY;
         const float ref = fmaxf(m, sink), base2 = ref == -INFINITY ? 0.0f : ref;
@@ -795,10 +843,21 @@ __device__ __noinline__ void arrive_cut(const AtParams &p, const Piece &piece, i
         const float inv = den == 0.0f ? 0.0f : f / den;
         const size_t out_row = (size_t)t * a.Hq + head;
         if (a.lse && quad == 0 && (pc.rows || w == 0)) a.lse[out_row] = (base2 + log2f(den)) * 0.6931471805599453f;
-        const float x = fmaf(o.x, inv, 0.0f), y = fmaf(o.y, inv, 0.0f), z = fmaf(o.z, inv, 0.0f), u = fmaf(o.w, inv, 0.0f);
-        *reinterpret_cast<uint2 *>(a.out + out_row * D + d0 + 4 * quad) =
-            make_uint2(f32x2_to_bf16x2(x, y), f32x2_to_bf16x2(z, u));
-        if (x * 0.0f + y * 0.0f + z * 0.0f + u * 0.0f != 0.0f && inv == inv) atomicOr(again + row / 32, 1u << (row % 32));
+        uint32_t *out = reinterpret_cast<uint32_t *>(a.out + out_row * D + d0 + 4 * quad);
+        float check = 0.0f;
+        uint32_t b[2 * U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const float x = fmaf(o[k].x, inv, 0.0f), y = fmaf(o[k].y, inv, 0.0f), z = fmaf(o[k].z, inv, 0.0f),
+                        u = fmaf(o[k].w, inv, 0.0f);
+            b[2 * k] = f32x2_to_bf16x2(x, y);
+            b[2 * k + 1] = f32x2_to_bf16x2(z, u);
+            check += x * 0.0f + y * 0.0f + z * 0.0f + u * 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < U; k += 2)
+            reinterpret_cast<uint4 *>(out)[k / 2] = make_uint4(b[2 * k], b[2 * k + 1], b[2 * k + 2], b[2 * k + 3]);
+        if (check != 0.0f && inv == inv) atomicOr(again + row / 32, 1u << (row % 32));
     }
     group_sync(2 + w, 128);
     // rows that saw a NaN or an infinity, or only multiplied one by zero
@@ -870,6 +929,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     cost.causal = a.causal;
     cost.window = a.window;
     cost.heads = a.kv.Hkv;
+    cost.flat = 0;
 
     pdl_trigger();
     if (threadIdx.x == 0) {

@@ -407,3 +407,21 @@ def test_large_windows_and_many_sequences():
     n = [i % 3 for i in range(75)]
     Batch(n, [x + 7 * i % 190 for i, x in enumerate(n)], 4, 2, 64, 16, "mxfp8").check()
     Batch([1] * 1100, [1 + i % 40 for i in range(1100)], 2, 1, 64, 16).check()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 16, 2), (64, 9, 3)])
+@pytest.mark.parametrize("n,m", [([1], [1024]), ([1], [1025]), ([70], [2048]), ([70], [2049]),
+                                 ([1, 40, 0, 300, 1], [1025, 2300, 7, 1700, 1]), ([1, 1, 1], [1000, 20, 6000])])
+def test_whole_and_cut_items(fmt, D, Hq, Hkv, n, m):
+    """Both sides of the lengths from which work is divided, and mixes of them."""
+    torch = need_gpu()
+    b = Batch(n, m, Hq, Hkv, D, 64, fmt)
+    b.check()
+    b.check(window=1100, sinks=torch.randn(Hq, device="cuda"))
+
+
+@pytest.mark.parametrize("n,m", [([6], [1500]), ([1, 40], [2500, 2300])])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_values_that_a_row_of_a_cut_item_may_not_see(n, m, value):
+    test_values_that_a_row_may_not_see(n, m, value)
