@@ -11,8 +11,8 @@
 // pages that its copies cannot tile, scales of zero or less).  Bound by its loads:
 // every query head reads the cache again, and by single keys.  64 heads on 8 x
 // 128 bf16, pages of 48 against pages of 64 on the tensor cores: one token on 16
-// keys 10.1 us, 8.8; 16 tokens on 2048 556 us, 32; a prompt of 512 on 1024
-// 3144 us, 60 and less.
+// keys 10.0 us, 8.6; 16 tokens on 2048 567 us, 33; a prompt of 512 on 1024
+// 3138 us, 23.
 #include "mx_attn.cuh"
 
 namespace mx {

@@ -30,11 +30,11 @@
 // and short items are not cut (AT_WHOLE_KEYS).
 //
 // P is rounded to bf16 because the tensor cores take their operands so: each
-// weight is off by 2^-9 of itself, as the values of a bf16 cache are already, and
+// weight is off by up to 2^-8 of itself, as the values of a bf16 cache are already, and
 // the sum that divides them is of the unrounded weights.  64 heads on 8 of 128:
 //   prompt of 4096 on 8192     558 us  1.47 PFLOP/s, 77 % of the measured rate
 //   64 tokens on 0.5-8 K       185 us  6.2 TB/s, 93 % of the measured copy
-//   16 x 2-6 tokens on 1-16 K  104 us  5.9 TB/s
+//   16 x 2-6 tokens on 1-16 K  105 us  5.8 TB/s
 //   one token on 131 keys        9 us  a chain of latencies
 //   MXFP8, 5 tokens on 24-66 K 204 us  the decode to bf16
 // A prompt is bound by the softmax between two MMAs of a group (tensor cores

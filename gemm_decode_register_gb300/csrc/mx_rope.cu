@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, append_resident<T>()) kv_appen
 
 // Whether kv_append_kernel's units fit: whole vectors on both sides of rot (of
 // rot / 2 in the half layout), units that divide a block of threads, and blocks of MXFP8
-// in four neighbouring lanes.  4096 x 80 heads x 128 into bf16 29 us, MXFP8 33 us; by
+// in four neighbouring lanes.  4096 x 80 heads x 128 into bf16 30 us, MXFP8 34 us; by
 // kv_append_any_kernel (rot = 120) 95 and 98 us.
 static bool append_units_ok(const AppendArgs &a, bool inter)
 {
