@@ -33,8 +33,8 @@
 // weight is off by up to 2^-8 of itself, as the values of a bf16 cache are already, and
 // the sum that divides them is of the unrounded weights.  64 heads on 8 of 128:
 //   prompt of 4096 on 8192     558 us  1.47 PFLOP/s, 77 % of the measured rate
-//   64 tokens on 0.5-8 K       185 us  6.2 TB/s, 93 % of the measured copy
-//   16 x 2-6 tokens on 1-16 K  105 us  5.8 TB/s
+//   64 tokens on 0.5-8 K       178 us  6.4 TB/s, 96 % of the measured copy
+//   16 x 2-6 tokens on 1-16 K  103 us  5.9 TB/s
 //   one token on 131 keys        9 us  a chain of latencies
 //   MXFP8, 5 tokens on 24-66 K 204 us  the decode to bf16
 // A prompt is bound by the softmax between two MMAs of a group (tensor cores
@@ -60,7 +60,11 @@ namespace mx {
 
 constexpr int AT_ROWS = 128;  // rows of a tile
 constexpr int AT_KEYS = 128;  // keys of a tile
-constexpr int AT_SPLIT_KEYS = 2 * AT_KEYS;  // what an item costs beside its keys, and more than its tiles' rounding
+// What an item costs beside its keys, and more than its tiles' rounding: its
+// queries, epilogue and the cuts (4, 2, 6 tiles, 64 heads on 8 x 128 bf16, us:
+// 16 x 1-200 tokens on 0.1-4 K 126, 168, 127; 64 tokens on 50-2000 62, 72, 62,
+// in MXFP8 87, 90, 90).
+constexpr int AT_SPLIT_KEYS = 4 * AT_KEYS;
 // Up to so many tokens' queries are copied one by one, of more the whole row tile
 // (8 sequences on 1024: 2 tokens each 21.2 us, 22.0 as a tile; 8 tokens each
 // 28.4 as a tile, 30.5 one by one).
@@ -72,8 +76,8 @@ constexpr int AT_Q_COPIES = 4;
 // 512 on 512 17.0, 31.8; 2 x 128 on 1500 28.5, 43.5; 32 on 2000 32.3, 35.2
 // (MXFP8 44.3, 40.3).
 constexpr int AT_WHOLE_KEYS = 8 * AT_KEYS, AT_WHOLE_KEYS_2 = 16 * AT_KEYS;
-// Shortest stretch of a CTA that only divides an item (one token on 2048 keys: 13.1
-// us; 2 tiles 13.4, 6 tiles 15.7).
+// Shortest stretch of a CTA that only divides an item (one token on 1500 keys
+// 13.8 us; with 4 tiles 15.5, with 6 17.9; on 8192 19.7, 17.8, 19.6).
 constexpr int AT_MIN_KEYS = 3 * AT_KEYS;
 constexpr int AT_RING = 3;                  // pieces the producer may run ahead by
 // log2 by which scores may outgrow the maximum before it is raised (0: the
@@ -318,8 +322,8 @@ __device__ __forceinline__ void plan(const AttnArgs &a, Cost &cost, Stretch &st)
     }
     // Few and short items: a CTA for each, uncut.  Else, a CTA for every item or
     // every AT_MIN_KEYS keys, whichever are more, as many to an item as to the
-    // next if they are alike.  Items cost at least two tiles, so a stretch is longer than
-    // a tile and no CTA between an item's first and last is left without one.
+    // next if they are alike.  A stretch is longer than
+    // a tile, so no CTA between an item's first and last is left without one.
     const int grid = gridDim.x;
     items = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)min(items, 1 << 24));
     int ctas = grid;
