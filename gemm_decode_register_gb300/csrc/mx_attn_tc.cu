@@ -69,6 +69,10 @@ constexpr int AT_SPLIT_KEYS = 4 * AT_KEYS;
 // (8 sequences on 1024: 2 tokens each 21.2 us, 22.0 as a tile; 8 tokens each
 // 28.4 as a tile, 30.5 one by one).
 constexpr int AT_Q_COPIES = 4;
+// Whether an item of n tokens takes whole row tiles of queries, of s1 tokens each:
+// always where it needs two of them, which is from two tokens on in wide groups.  The
+// host encodes the copies by the call's tokens, which no item outnumbers.
+__host__ __device__ constexpr bool at_whole_tiles(int n, int s1) { return n > AT_Q_COPIES || n > s1; }
 // Items of up to so many keys are not cut when there is a CTA for each; more when
 // they have two row tiles, whose parts cost more to add up.  Uncut against cut,
 // 64 on 8 heads x 128 bf16, us: one token on 512 keys 9.4, 12.9; on 1024 13.6,
@@ -1423,7 +1427,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                             for (int s = 0; s < G::SLABS; ++s)
                                 tma_load_3d(dst + r * G::TILE + s * G::SLAB, &map_q, 64 * s, pc.kvh * a.g,
                                             pc.q0 + r * s1, &c.q_full);
-                    } else if (pc.ntok > AT_Q_COPIES) {
+                    } else if (at_whole_tiles(pc.ntok, s1)) {
                         // whole row tile: the rows past the item's tokens are not used
                         mbar_arrive_expect_tx(&c.q_full, G::SLABS * (uint32_t)(s1 * a.g) * 128u);
     #pragma unroll
@@ -1718,7 +1722,8 @@ static cudaError_t run_attn_tc(const DeviceState &ds, cudaStream_t st, const Att
     const int s1 = AT_ROWS / a.g;
     CUtensorMap maps[4];
     // whole row tiles of queries (not needed by calls of few tokens), single tokens
-    for (int i = a.T > AT_Q_COPIES ? 0 : 1; i < 2; ++i) {
+    const bool whole_tiles = at_whole_tiles(a.T, s1);
+    for (int i = whole_tiles ? 0 : 1; i < 2; ++i) {
         const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
         const cuuint64_t strides[2] = {(cuuint64_t)a.q_head_stride * 2, (cuuint64_t)a.q_token_stride * 2};
         const cuuint32_t box[3] = {64u, (cuuint32_t)a.g, i == 0 ? (cuuint32_t)s1 : 1u};
@@ -1727,7 +1732,7 @@ static cudaError_t run_attn_tc(const DeviceState &ds, cudaStream_t st, const Att
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    if (a.T <= AT_Q_COPIES) maps[0] = maps[1];
+    if (!whole_tiles) maps[0] = maps[1];
     for (int i = 0; i < 2; ++i) {
         const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.kv.page_size, (cuuint64_t)a.kv.Hkv,
                                     (cuuint64_t)a.kv.num_pages};
