@@ -29,7 +29,11 @@ __global__ void __launch_bounds__(DIRECT_WARPS * 32) attn_direct_kernel(AttnArgs
     const int t = blockIdx.x / a.Hq, h = blockIdx.x - t * a.Hq;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = sequence_of(a.q_start, a.B, t);
-    if (b < 0) return;
+    if (b < 0) {
+        // all rows may belong to no sequence: the grid must not end before the kernel before it has
+        pdl_wait();
+        return;
+    }
     const int end = __ldg(a.q_start + b + 1), len = __ldg(a.kv_len + b);
     const long long pos = (long long)len - end + t;
     const int hi = a.causal ? (int)(pos + 1 < len ? pos + 1 : len) : len;
