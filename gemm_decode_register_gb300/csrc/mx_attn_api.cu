@@ -62,7 +62,7 @@ extern "C" int mx_rope(const void *x, void *y, int dtype, const int32_t *positio
                        int64_t y_token_stride, int64_t y_head_stride, int flags)
 {
     if (dtype != MX_BF16 && dtype != MX_F32) return MX_EUNSUPPORTED;
-    if (!x || !y || !positions || (rot > 0 && !table)) return MX_EINVAL;
+    if (!x || !y || !positions || (rot > 0 && (!table || table_len == 0))) return MX_EINVAL;
     if (T <= 0 || H <= 0 || D <= 0 || rot < 0 || rot > D || rot % 2 != 0 || table_len < 0) return MX_EINVAL;
     if (flags & ~(MX_ROPE_INTERLEAVED | MX_ROPE_INVERSE)) return MX_EINVAL;
     if (x_token_stride < 0 || x_head_stride < 0 || y_token_stride <= 0 || y_head_stride <= 0) return MX_EINVAL;
@@ -83,7 +83,7 @@ extern "C" int mx_kv_append(const mx_paged_kv *kv, const void *rows, int dtype, 
     if (s != MX_OK) return s;
     if (dtype != MX_BF16 && dtype != MX_F32) return MX_EUNSUPPORTED;
     if (!rows || Hq < 0 || (Hq > 0 && !q) || rot < 0 || rot > kv->D || rot % 2 != 0 || table_len < 0 ||
-        (rot > 0 && !table) || (flags & ~MX_ROPE_INTERLEAVED))
+        (rot > 0 && (!table || table_len == 0)) || (flags & ~MX_ROPE_INTERLEAVED))
         return MX_EINVAL;
     if (Hq > MAX_HEADS) return MX_EUNSUPPORTED;
     if (row_stride < (int64_t)(Hq + 2 * kv->Hkv) * kv->D) return MX_EINVAL;

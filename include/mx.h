@@ -320,7 +320,7 @@ int mx_rope_table(const double *inv_freq, double factor, float *table, int64_t p
  *   (a, b) -> (a c - b s, b c + a s),  (c, s) = table[positions[t]][i],
  * each product and sum rounded to fp32, then to dtype (mx_dtype) once.
  * positions int32 [T]; table fp32 [table_len][rot/2][2] (mx_rope_table from
- * position 0); strides in elements, the last dimension contiguous; y may be x
+ * position 0; not empty); strides in elements, the last dimension contiguous; y may be x
  * with the same strides.  MX_ROPE_INVERSE (s -> -s) maps the gradient of y to
  * the gradient of x.  Any H, D >= 1, rot even, 0 <= rot <= D.  x, y and the
  * strides need only be multiples of the element size (multiples of 16 bytes

@@ -110,3 +110,12 @@ def test_frequencies():
     p, _ = ops.rope_frequencies(128, 10000.0)
     assert y[0] == p[0] and abs(float(p[-1] / y[-1]) - 16) < 1e-9 and abs(my - 1.27725887) < 1e-7
     assert (y[:-1] > y[1:]).all()
+
+
+def test_an_empty_rotation_table_is_refused(lib):
+    """Its row 0 would be read for positions that are out of range; without a rotation there is no table."""
+    c = kv()
+    rope = [A, A, 0, A, A, 0, 4, 8, 128, 128, 1024, 128, 1024, 128, 0]
+    append = [ctypes.byref(c), A, 0, 2048, A, A, A, 0, 128, A, 4, 2, 8, 0]
+    assert lib.mx_rope(*rope) == -1
+    assert lib.mx_kv_append(*append) == -1
