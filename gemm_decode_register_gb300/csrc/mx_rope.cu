@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const T *x, T *y, RopeArgs a)
         }
     }
     const int pos = a.positions[t];
-    const bool ok = (unsigned)pos < (unsigned)a.table_len;
+    const bool ok = a.rot == 0 || (unsigned)pos < (unsigned)a.table_len;  // (no rotation: a copy)
     if (!ok && r == 0) set_device_error(a.err, DEVERR_BAD_POSITION);
     float c[NV], s[NV];  // of the pairs of both vectors
     if (turns) {

@@ -469,11 +469,11 @@ def _table_arg(table: torch.Tensor | None) -> tuple[int | None, int, int]:
     return _whole("table", table, torch.float32, shape), n, 2 * half
 
 
-def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False,
+def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor | None, interleaved: bool = False,
          inverse: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
     """Rotate the first 2 * table.shape[1] dimensions of each head of x [T][H][D]
     (bf16 or fp32, the last dimension contiguous) by the angles of its token's position
-    (positions int32 [T]); inverse: rotate back (the gradient).  out may be x."""
+    (positions int32 [T]); inverse: rotate back (the gradient); table None: a copy.  out may be x."""
     if x.dtype not in _DTYPES:
         raise ValueError(f"x: expected bf16 or fp32, got {x.dtype}")
     xp = _cuda("x", x, x.dtype, 3)

@@ -324,7 +324,8 @@ int mx_rope_table(const double *inv_freq, double factor, float *table, int64_t p
  * with the same strides.  MX_ROPE_INVERSE (s -> -s) maps the gradient of y to
  * the gradient of x.  Any H, D >= 1, rot even, 0 <= rot <= D.  x, y and the
  * strides need only be multiples of the element size (multiples of 16 bytes
- * take the vector path); positions 4-byte, table 16-byte aligned.  A position outside [0, table_len)
+ * take the vector path); positions 4-byte, table 16-byte aligned.  rot = 0: a copy, whatever the
+ * positions (table may be null).  Otherwise a position outside [0, table_len)
  * sets MX_DEVERR_BAD_POSITION and makes that token's outputs NaN. */
 int mx_rope(const void *x, void *y, int dtype, const int32_t *positions, const float *table, int table_len, int T,
             int H, int D, int rot, int64_t x_token_stride, int64_t x_head_stride, int64_t y_token_stride,
