@@ -755,6 +755,17 @@ __device__ __noinline__ void row_again(const AttnArgs &a, int b, int t, int h, i
     }
 }
 
+// Is a page missing that holds any of a sequence's keys [lo, hi)?  (Rare: a loop over
+// the table's entries in each row's own thread.)
+__device__ __noinline__ bool any_missing(const AttnArgs &a, int b, int lo, int hi)
+{
+    const int32_t *table = a.kv.block_table + (size_t)b * a.kv.table_stride;
+    if (lo >= hi) return false;
+    for (int i = lo / a.kv.page_size, end = (hi - 1) / a.kv.page_size; i <= end; ++i)
+        if (page_of(a.kv, table, i) < 0) return true;
+    return false;
+}
+
 // Two sums against maxima m0 and m1 become one against the larger: the first
 // times f0 plus the second times f1.
 struct Merge {
@@ -1220,8 +1231,14 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             if (!go_on) poison<D, KVF>(prm, cost, np, w, row, c);
             if (!go_on || pc.end) break;
             tc_fence_after();
-            const bool bad = n > 0 && c.missing[piece & 7] != 0;
-            if (bad && row == 0) set_device_error(a.err, DEVERR_BAD_PAGE);
+            bool bad = n > 0 && c.missing[piece & 7] != 0;
+            if (bad) {
+                // the row's own keys among this piece's, or the tiles' other rows alone?
+                if (row == 0) set_device_error(a.err, DEVERR_BAD_PAGE);
+                const int k0 = (pc.tile0 + pc.k0) * AT_KEYS, k1 = min((pc.tile0 + pc.k1 - 1) * AT_KEYS, 0x7FFFFFFF - AT_KEYS) + AT_KEYS;
+                bad = valid && any_missing(a, pc.b, max(rlo, k0), min(rhi, k1));
+                __syncwarp();
+            }
             // rows: the group's own rows, all dimensions.  keys: both groups'
             // sums of the same rows; group w takes half of the dimensions.
             int d0 = 0, d1 = D;

@@ -2,6 +2,7 @@
 few tokens of wide groups."""
 import pytest
 
+import attn_ref as ref
 from gpu_util import need_gpu
 from test_gpu_attn import FMTS, Batch
 
@@ -46,3 +47,43 @@ def test_call_without_sequences_keeps_the_order(page):
         ops.rope(rows.view(T, -1, 128), pos, table, out=got)
         assert torch.equal(got, want)
     assert not attn.any() and ops.device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 64), (128, 48), (128, 256)])
+@pytest.mark.parametrize("n,m,window,missing", [
+    ([40, 1], [300, 70], 0, -1),        # the last page: the chunk's first tokens do not need it
+    ([300, 1], [300, 70], 0, 0.5),      # a prompt, a page in the middle
+    ([300, 1], [700, 70], 40, 0.6),     # a window: neither earlier nor later tokens
+    ([200, 1], [9000, 70], 0, -1),      # cut across the GPU
+    ([3, 3], [5000, 2000], 1500, 0.7)])
+def test_a_missing_page_spoils_the_rows_that_need_it(fmt, D, page, n, m, window, missing):
+    """And no others, whichever kernel takes the call."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    b = Batch(n, m, 8, 2, D, page, fmt)
+    good, good_lse = b.check(window=window)
+    pages = -(-m[0] // page)
+    j = pages - 1 if missing == -1 else int(missing * pages)
+    table = b.kv.block_table.clone()
+    table[0, j] = -1
+    kv = ops.PagedKV(b.kv.k, b.kv.v, table, b.kv.k_scales, b.kv.v_scales)
+    out, lse = ops.paged_attn(kv, b.q, b.q_start, b.kv_len, window=window, return_lse=True)
+    assert ops.device_error() == 0x4
+    pos = torch.arange(m[0] - n[0], m[0], device="cuda")
+    first = (pos - window + 1).clamp(min=0) if window else torch.zeros_like(pos)
+    need = torch.zeros(b.T, dtype=torch.bool, device="cuda")
+    need[:n[0]] = (first < (j + 1) * page) & (pos >= j * page)
+    assert need.any()
+    assert torch.isnan(out[need]).all() and torch.isnan(lse[need]).all()
+    # the other rows may be summed again one by one: each within half a bf16 ulp and 2^-8 of the values of the definition
+    first = 0
+    for s in range(2):
+        k, v = b.context(s)
+        rows = slice(first, first + n[s])
+        want, l, tol, ltol = ref.attend(b.q[rows].double(), k, v, D ** -0.5, True, window)
+        keep = ~need[rows]
+        ref.assert_within(out[rows][keep], want[keep], tol[keep], "out")
+        ref.assert_within(lse[rows][keep], l[keep], ltol[keep], "lse")
+        first += n[s]
