@@ -393,21 +393,28 @@ __device__ __forceinline__ void plan(const AttnArgs &a, Cost &cost, Stretch &st)
 
 // ------------------------------------------------------------ tensor ops
 
+// What the waits of a CTA watch beside their barrier.
+struct Watch {
+    int gave_up;  // a wait ran out
+    int busy;     // warps that compute rows again (row_again): over a long context longer than
+                  // the limit, which counts from when they are done
+};
+
 // mbar_wait without a call: ptxas (13.0) cannot allocate the softmax warps'
 // registers past the launch's count across the call of its slow path.
-__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, volatile Watch *watch,
                                         unsigned long long limit_ns, bool respect_abort = true)
 {
     unsigned long long t0 = 0;
 #pragma unroll 1
     for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
         if (__builtin_expect((i & 63u) == 0u, 0)) {
-            if (respect_abort && *abort_flag) return false;
+            if (respect_abort && watch->gave_up) return false;
             const unsigned long long t = globaltimer();
-            if (t0 == 0) {
+            if (t0 == 0 || watch->busy) {
                 t0 = t;
             } else if (t - t0 > limit_ns) {
-                *abort_flag = 1;
+                watch->gave_up = 1;
                 return false;
             }
         }
@@ -417,10 +424,10 @@ __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, volatile
 
 // A wait of the whole warp, polled by all of it: polled by one lane in a branch
 // of its own a prompt took 764 us instead of 585.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile Watch *watch,
                                           unsigned long long limit_ns)
 {
-    return __all_sync(0xFFFFFFFFu, at_wait(bar, parity, abort_flag, limit_ns)) != 0;
+    return __all_sync(0xFFFFFFFFu, at_wait(bar, parity, watch, limit_ns)) != 0;
 }
 
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc)
@@ -674,7 +681,7 @@ struct AtCtrl {
     Piece ring[AT_RING];             // pieces, from the producer to the other roles
     Stretch stretch;
     uint32_t tmem;
-    int abort_flag;
+    Watch watch;
     int missing[8];                  // by piece number: a page of it is missing
     int last[2];                     // by group: its part of a cut item was the last to come
     Piece pending[2];                // by group: a part that is written but not counted yet
@@ -820,7 +827,7 @@ __device__ __forceinline__ bool last_of(const AtParams &p, const Piece &pc, int 
 // threads neighbouring rows.
 template <int D, int KVF>
 __device__ __noinline__ void arrive_cut(const AtParams &p, const Piece &piece, int w, int tid, volatile int *last,
-                                        unsigned *again)
+                                        unsigned *again, Watch *watch)
 {
     const Piece pc = piece;
     if (tid < 4) again[tid] = 0u;
@@ -880,6 +887,8 @@ __device__ __noinline__ void arrive_cut(const AtParams &p, const Piece &piece, i
     }
     group_sync(2 + w, 128);
     // rows that saw a NaN or an infinity, or only multiplied one by zero
+    const bool some = again[tid / 32] != 0;
+    if (some && tid % 32 == 0) atomicAdd(&watch->busy, 1);
     for (unsigned left = again[tid / 32]; left != 0; left &= left - 1) {
         const int row = (tid & ~31) + __ffs(left) - 1;
         const int tok = t0 + row / a.g, head = pc.kvh * a.g + row % a.g, pos = pc.first + tok;
@@ -898,6 +907,7 @@ __device__ __noinline__ void arrive_cut(const AtParams &p, const Piece &piece, i
         if (a.sinks) den += exp2_approx(sink - base2);
         row_again<KVF>(a, pc.b, pc.q0 + tok, head, lo, hi, d0, d0 + W, 1.0f / den, base2);
     }
+    if (some && tid % 32 == 0) atomicSub(&watch->busy, 1);
 }
 
 // A CTA whose wait gave up: the outputs of its pieces from number `done` on
@@ -919,7 +929,7 @@ __device__ __noinline__ void poison(const AtParams &p, const Cost &cost, int don
         if (pc.c0 != pc.c1) {
             float *part = partial_base<D>(p, blockIdx.x, (int)blockIdx.x == pc.c0 ? 1 : 0, w);
             if (valid) part[2 * row] = part[2 * row + 1] = nan;
-            arrive_cut<D, KVF>(p, pc, w, row, c.last, c.again[w]);
+            arrive_cut<D, KVF>(p, pc, w, row, c.last, c.again[w], &c.watch);
         } else if (valid) {
             const size_t r = (size_t)(pc.q0 + tok) * a.Hq + head;
             if (a.lse) a.lse[r] = nan;
@@ -940,7 +950,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     AtCtrl &c = *reinterpret_cast<AtCtrl *>(smem + G::OFF_BAR);
     const AttnArgs &a = prm.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile int *abort_flag = &c.abort_flag;
+    volatile Watch *watch = &c.watch;
     uint64_t *full = c.slot_bars, *empty = full + G::SLOTS, *c_full = empty + G::SLOTS, *c_empty = c_full + G::C_SLOTS;
     Cost cost;
     const int s1 = AT_ROWS / a.g;
@@ -974,7 +984,8 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             mbar_init(&c.r_full[i], 1);
             mbar_init(&c.r_free[i], 1 + 8 + (G::MX8 ? G::DECODERS : 0));  // MMA issuer, softmax and decoder warps
         }
-        c.abort_flag = 0;
+        c.watch.gave_up = 0;
+        c.watch.busy = 0;
         for (int i = 0; i < 8; ++i) c.missing[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -991,7 +1002,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     Piece pc;
     // the i-th piece from the ring, by a whole warp
     auto take = [&](int i) {
-        const bool ok = warp_wait(&c.r_full[i % AT_RING], (i / AT_RING) & 1, abort_flag, prm.wait_ns);
+        const bool ok = warp_wait(&c.r_full[i % AT_RING], (i / AT_RING) & 1, watch, prm.wait_ns);
         if (ok) pc = c.ring[i % AT_RING];
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&c.r_free[i % AT_RING]);
@@ -1013,7 +1024,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
         bool alive = true;
         // warp-uniform, as the tensor-memory instructions that follow a wait must be
         auto wait = [&](uint64_t *bar, int phase) {
-            return warp_wait(bar, phase & 1, abort_flag, prm.wait_ns);
+            return warp_wait(bar, phase & 1, watch, prm.wait_ns);
         };
         for (int np = 0;; ++np) {
             alive = take(np);
@@ -1021,7 +1032,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 // the last piece's part: its stores are on their way while the next
                 // piece's queries and first scores are
                 group_sync(2 + w, 128);
-                arrive_cut<D, KVF>(prm, c.pending[w], w, row, c.last, c.again[w]);
+                arrive_cut<D, KVF>(prm, c.pending[w], w, row, c.last, c.again[w], &c.watch);
                 pending = false;
             }
             if (!alive || pc.end) {  // an empty piece, to the vote below
@@ -1358,6 +1369,8 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 float c0, c1;
                 unpack2(check, c0, c1);
                 unsigned again = __ballot_sync(0xFFFFFFFFu, valid && inv == inv && c0 + c1 != 0.0f);
+                const bool some = again != 0;
+                if (some && lane == 0) atomicAdd(&c.watch.busy, 1);
                 for (; again != 0; again &= again - 1) {
                     const int src = __ffs(again) - 1;
                     row_again<KVF>(a, pc.b, __shfl_sync(0xFFFFFFFFu, pc.q0 + tok, src),
@@ -1365,6 +1378,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                                    __shfl_sync(0xFFFFFFFFu, rhi, src), d0, d1,
                                    1.0f / __shfl_sync(0xFFFFFFFFu, den, src), __shfl_sync(0xFFFFFFFFu, base2, src));
                 }
+                if (some && lane == 0) atomicSub(&c.watch.busy, 1);
             }
             if (cut && !finish_here) {
                 if (row == 0) c.pending[w] = pc;
@@ -1399,7 +1413,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 pc.end = !some;
                 int ok = 1;
                 if (lane == 0) {
-                    if (np >= AT_RING) ok = at_wait(&c.r_free[np % AT_RING], ((np / AT_RING) - 1) & 1, abort_flag, prm.wait_ns);
+                    if (np >= AT_RING) ok = at_wait(&c.r_free[np % AT_RING], ((np / AT_RING) - 1) & 1, watch, prm.wait_ns);
                     if (ok) {
                         c.ring[np % AT_RING] = pc;
                         mbar_arrive(&c.r_full[np % AT_RING]);
@@ -1432,7 +1446,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     pdl_wait();
                     waited = true;
                 }
-                if (lane == 0 && piece > 0) ok = at_wait(&c.q_empty, (piece - 1) & 1, abort_flag, prm.wait_ns);
+                if (lane == 0 && piece > 0) ok = at_wait(&c.q_empty, (piece - 1) & 1, watch, prm.wait_ns);
                 if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
                 if (lane == 0 && !prm.stall) {
                     const uint32_t dst = smem_u32(smem);
@@ -1477,7 +1491,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     const int copies = __popc(__ballot_sync(0xFFFFFFFFu, here && ids >= 0));
                     if (__any_sync(0xFFFFFFFFu, here && ids == -2) && lane == 0) c.missing[piece & 7] = 1;
                     uint64_t *bar = (G::MX8 ? c_full : full) + slot.i;
-                    if (!fresh && !warp_wait((G::MX8 ? c_empty : empty) + slot.i, slot.phase ^ 1, abort_flag, prm.wait_ns))
+                    if (!fresh && !warp_wait((G::MX8 ? c_empty : empty) + slot.i, slot.phase ^ 1, watch, prm.wait_ns))
                         return false;
                     if (elected)
                         mbar_arrive_expect_tx(bar, (uint32_t)(copies * prm.page_rows) *
@@ -1516,15 +1530,15 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 }
                 ++piece;
             }
-            if (*abort_flag) {
+            if (watch->gave_up) {
                 // copies in flight must land before the CTA may exit
                 __syncwarp();
                 if (lane == 0) {
                     constexpr int RING = G::MX8 ? G::C_SLOTS : G::SLOTS;
                     for (int i = max(load - RING, 0); i < load; ++i)
-                        at_wait(G::MX8 ? &c_full[i % RING] : &full[i % RING], (i / RING) & 1, abort_flag, AT_WAIT_NS, false);
-                    if (!prm.stall && piece > 0) at_wait(&c.q_full, (piece - 1) & 1, abort_flag, AT_WAIT_NS, false);
-                    if (!prm.stall) at_wait(&c.q_full, piece & 1, abort_flag, 1000000ull, false);
+                        at_wait(G::MX8 ? &c_full[i % RING] : &full[i % RING], (i / RING) & 1, watch, AT_WAIT_NS, false);
+                    if (!prm.stall && piece > 0) at_wait(&c.q_full, (piece - 1) & 1, watch, AT_WAIT_NS, false);
+                    if (!prm.stall) at_wait(&c.q_full, piece & 1, watch, 1000000ull, false);
                 }
             }
         } else if (warp == 9) {
@@ -1545,7 +1559,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
             uint32_t p_phase[2] = {0, 0};  // of each group's p_full
             bool go = true;
             auto wait = [&](uint64_t *bar, uint32_t phase) {
-                return warp_wait(bar, phase, abort_flag, prm.wait_ns);
+                return warp_wait(bar, phase, watch, prm.wait_ns);
             };
             auto commit = [&](uint64_t *bar) {
                 if (elected) umma_commit(bar);
@@ -1649,13 +1663,13 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 bool go = true;
                 for (int np = 0; go && take(np) && !pc.end; ++np) {
                     for (int left = 2 * (pc.k1 - pc.k0); left > 0; --left) {
-                        go = warp_wait(&c_full[sc.i], sc.phase, abort_flag, prm.wait_ns);
+                        go = warp_wait(&c_full[sc.i], sc.phase, watch, prm.wait_ns);
                         if (!go) break;
                         const uint8_t *codes = smem + G::OFF_C + sc.i * G::CODES + block * 32;
                         const uint8_t *scales = smem + G::OFF_SC + sc.i * G::SCALES + block;
                         uint8_t *tile = smem + G::OFF_KV + sd.i * G::TILE + slab * G::SLAB;
                         if (!fresh) {
-                            go = warp_wait(&empty[sd.i], sd.phase ^ 1, abort_flag, prm.wait_ns);
+                            go = warp_wait(&empty[sd.i], sd.phase ^ 1, watch, prm.wait_ns);
                             if (!go) break;
                         }
 #pragma unroll 1
@@ -1684,7 +1698,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
     }
     __syncthreads();
     if (warp == 9) {
-        if (lane == 0) at_wait(&c.done, 0, abort_flag, AT_WAIT_NS, false);
+        if (lane == 0) at_wait(&c.done, 0, watch, AT_WAIT_NS, false);
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

@@ -1,5 +1,7 @@
 """Attention over the paged cache where shapes, masks and caches are unusual:
 few tokens of wide groups."""
+import math
+
 import pytest
 
 import attn_ref as ref
@@ -87,3 +89,23 @@ def test_a_missing_page_spoils_the_rows_that_need_it(fmt, D, page, n, m, window,
         ref.assert_within(out[rows][keep], want[keep], tol[keep], "out")
         ref.assert_within(lse[rows][keep], l[keep], ltol[keep], "lse")
         first += n[s]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,m", [([20] * 40, [2000] * 40), ([40, 3] * 10, [6000, 3000] * 10)])
+def test_rows_computed_again_outlast_a_wait(fmt, n, m):
+    """Rows that are computed again one by one (a NaN among the values of the last token, which the others may not see) take
+    longer than the other warps' waits may, which stand before a CTA's next items: nobody gives up while they go on."""
+    need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    b = Batch(n, m, 16, 8, 128, 16, fmt)
+    for s in range(len(n)):
+        page, slot = b.place(s, m[s] - 1)
+        b.kv.v[page, :, slot, 5] = math.nan if fmt == "bf16" else 0x7F
+        b.halves[1][page, :, slot, 5] = math.nan
+    ops.debug_qmm_stall(False, 1_000_000)
+    try:
+        b.check()
+    finally:
+        ops.debug_qmm_stall(False, 0)
