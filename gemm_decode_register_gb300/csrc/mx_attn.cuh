@@ -94,6 +94,28 @@ __device__ __forceinline__ float key_dot(const mx_paged_kv &kv, const Q *q, long
     return acc;
 }
 
+// Two neighbouring elements of a value as they lie in the cache, and as fp32.
+template <int KVF>
+struct RawPair {
+    uint32_t w, e;
+    __device__ __forceinline__ void load(const mx_paged_kv &kv, long long at, long long sat, int d)
+    {
+        if constexpr (KVF == KV_BF16) {
+            w = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(kv.v) + at + d);
+        } else {
+            w = *reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(kv.v) + at + d);
+            e = static_cast<const uint8_t *>(kv.v_scales)[sat + d / 32];
+        }
+    }
+    __device__ __forceinline__ float2 get() const
+    {
+        if constexpr (KVF == KV_BF16) return make_float2(bf16_lo(w), bf16_hi(w));
+        const float sc = e8m0_to_f32(e);
+        const uint32_t h2 = e4m3x2_to_f16x2(w);
+        return make_float2(f16_lo_to_f32(h2) * sc, f16_hi_to_f32(h2) * sc);
+    }
+};
+
 // o += p v of one key; lane l holds dimensions 2 l + 64 i and the one after.
 template <int KVF>
 __device__ __forceinline__ void add_value(const mx_paged_kv &kv, long long at, long long sat, float p,
@@ -103,17 +125,11 @@ __device__ __forceinline__ void add_value(const mx_paged_kv &kv, long long at, l
     for (int i = 0; i < MAX_D / 64; ++i) {
         const int d = 2 * (threadIdx.x & 31) + 64 * i;
         if (d >= kv.D) break;
-        if constexpr (KVF == KV_BF16) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(kv.v) + at + d);
-            o[2 * i] = fmaf(p, bf16_lo(w), o[2 * i]);
-            o[2 * i + 1] = fmaf(p, bf16_hi(w), o[2 * i + 1]);
-        } else {
-            const uint32_t w = *reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(kv.v) + at + d);
-            const float sc = e8m0_to_f32(static_cast<const uint8_t *>(kv.v_scales)[sat + d / 32]);
-            const uint32_t h2 = e4m3x2_to_f16x2(w);
-            o[2 * i] = fmaf(p, f16_lo_to_f32(h2) * sc, o[2 * i]);
-            o[2 * i + 1] = fmaf(p, f16_hi_to_f32(h2) * sc, o[2 * i + 1]);
-        }
+        RawPair<KVF> r;
+        r.load(kv, at, sat, d);
+        const float2 v = r.get();
+        o[2 * i] = fmaf(p, v.x, o[2 * i]);
+        o[2 * i + 1] = fmaf(p, v.y, o[2 * i + 1]);
     }
 }
 

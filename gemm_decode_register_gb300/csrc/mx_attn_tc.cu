@@ -396,7 +396,7 @@ __device__ __forceinline__ void plan(const AttnArgs &a, Cost &cost, Stretch &st)
 // What the waits of a CTA watch beside their barrier.
 struct Watch {
     int gave_up;  // a wait ran out
-    int busy;     // warps that compute rows again (row_again): over a long context longer than
+    int busy;     // warps that compute rows again (rows_again): over a long context longer than
                   // the limit, which counts from when they are done
 };
 
@@ -722,44 +722,151 @@ __device__ __forceinline__ float *partial_base(const AtParams &p, int cta, int w
     return p.partials + (size_t)((cta * 2 + which) * 2 + group) * p.part_rows * (D + 2);
 }
 
-// A row whose sum over the tiles came out NaN or infinite, computed again from
-// its own keys alone, by the whole warp: a product with a weight of zero is not
-// zero when the value is NaN or infinite, and such a value may lie where the
-// row may not see it; and values near the type's largest can overflow a sum
-// whose weights are divided only at its end (here each weight is divided
-// first), so rows that see all keys are computed again too.
-template <int KVF>
+// Calls use(key of the 32, offsets of its place) ... for keys [lo, hi) of a cache head,
+// by the whole warp: each lane finds the place of one of 32 keys, then all take
+// them in turn, AHEAD at a time so that their loads are in flight together.
+// first(at, sat): a lane's own key, before.
+template <int AHEAD, typename First, typename Use>
+__device__ __forceinline__ void for_keys(const mx_paged_kv &kv, int b, int kvh, int lo, int hi, First first, Use use)
+{
+    const int lane = threadIdx.x & 31;
+    const int32_t *table = kv.block_table + (size_t)b * kv.table_stride;
+    for (long long k0 = lo; k0 < hi; k0 += 32) {
+        const int key = (int)min(k0 + lane, hi - 1ll), n = (int)min(32ll, hi - k0);
+        const int pi = key / kv.page_size, slot = key - pi * kv.page_size;
+        const int page = max(page_of(kv, table, pi), 0);
+        const long long at = page * kv.page_stride + kvh * kv.head_stride + slot * kv.token_stride;
+        const long long sat = page * kv.scale_page_stride + kvh * kv.scale_head_stride + slot * kv.scale_token_stride;
+        first(lane < n, at, sat);
+#pragma unroll 1
+        for (int j = 0; j < n; j += AHEAD) {
+            long long ats[AHEAD], sats[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                ats[i] = __shfl_sync(0xFFFFFFFFu, at, (j + i) & 31);
+                sats[i] = __shfl_sync(0xFFFFFFFFu, sat, (j + i) & 31);
+            }
+            use(j, n - j, ats, sats);
+        }
+    }
+}
+
+constexpr int AGAIN_AHEAD = 4;  // (8: the softmax warps of the MXFP8 kernel spill)
+
+// What is not finite among the values of keys [lo, hi), in this lane's dimensions
+// 2 lane + 64 i and the one after: for each of them three bits, NaN, +infinity
+// and -infinity.
+template <int D, int KVF>
+__device__ __noinline__ uint32_t kinds_of_values(const mx_paged_kv &kv, int b, int kvh, int lo, int hi)
+{
+    const int d = 2 * (threadIdx.x & 31);
+    uint32_t kinds = 0;
+    for_keys<AGAIN_AHEAD>(
+        kv, b, kvh, lo, hi, [](bool, long long, long long) {},
+        [&](int, int left, const long long(&at)[AGAIN_AHEAD], const long long(&sat)[AGAIN_AHEAD]) {
+            RawPair<KVF> r[AGAIN_AHEAD][D / 64];
+#pragma unroll
+            for (int k = 0; k < AGAIN_AHEAD; ++k)
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                    r[k][i].load(kv, at[k < left ? k : 0], sat[k < left ? k : 0], d + 64 * i);
+#pragma unroll
+            for (int k = 0; k < AGAIN_AHEAD; ++k)
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const float2 v = r[k][i].get();
+                    if (v.x * 0.0f != 0.0f) kinds |= (v.x != v.x ? 1u : v.x > 0.0f ? 2u : 4u) << (6 * i);
+                    if (v.y * 0.0f != 0.0f) kinds |= (v.y != v.y ? 1u : v.y > 0.0f ? 2u : 4u) << (6 * i + 3);
+                }
+        });
+    return kinds;
+}
+
+// One row from its own keys [lo, hi) alone, each weight divided by the sum before it is
+// used, dimensions [d0, d1); by the whole warp.
+template <int D, int KVF>
 __device__ __noinline__ void row_again(const AttnArgs &a, int b, int t, int h, int lo, int hi, int d0, int d1,
                                        float inv_total, float m_used)
 {
-    const int lane = threadIdx.x & 31;
+    const int d = 2 * (threadIdx.x & 31);
     const mx_paged_kv &kv = a.kv;
-    const int32_t *table = kv.block_table + (size_t)b * kv.table_stride;
     const uint16_t *q = a.q + (long long)t * a.q_token_stride + (long long)h * a.q_head_stride;
-    const int kvh = h / a.g;
-    float o[MAX_D / 32] = {};
-    for (int k0 = lo; k0 < hi; k0 += 32) {
-        const int key = k0 + lane;
-        long long at = 0, sat = 0;
-        float p = 0.0f;
-        if (key < hi) {
-            const int pi = key / kv.page_size, slot = key - pi * kv.page_size;
-            const int page = max(page_of(kv, table, pi), 0);
-            at = page * kv.page_stride + kvh * kv.head_stride + slot * kv.token_stride;
-            sat = page * kv.scale_page_stride + kvh * kv.scale_head_stride + slot * kv.scale_token_stride;
-            p = exp2f(key_dot<KVF>(kv, q, at, sat) * a.scale_log2 - m_used) * inv_total;
-        }
-        for (int j = 0; j < min(32, hi - k0); ++j) {
-            const float pj = __shfl_sync(0xFFFFFFFFu, p, j);
-            add_value<KVF>(kv, __shfl_sync(0xFFFFFFFFu, at, j), __shfl_sync(0xFFFFFFFFu, sat, j), pj, o);
-        }
-    }
-    uint16_t *out = a.out + ((size_t)t * a.Hq + h) * kv.D;
+    float o[D / 32] = {}, p = 0.0f;
+    for_keys<AGAIN_AHEAD>(
+        kv, b, h / a.g, lo, hi,
+        [&](bool mine, long long at, long long sat) {
+            p = mine ? exp2f(key_dot<KVF>(kv, q, at, sat) * a.scale_log2 - m_used) * inv_total : 0.0f;
+        },
+        [&](int j, int left, const long long(&at)[AGAIN_AHEAD], const long long(&sat)[AGAIN_AHEAD]) {
+            RawPair<KVF> r[AGAIN_AHEAD][D / 64];
 #pragma unroll
-    for (int i = 0; i < MAX_D / 64; ++i) {
-        const int d = 2 * lane + 64 * i;
-        if (d >= d0 && d < d1) *reinterpret_cast<uint32_t *>(out + d) = f32x2_to_bf16x2(o[2 * i], o[2 * i + 1]);
+            for (int k = 0; k < AGAIN_AHEAD; ++k)
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                    r[k][i].load(kv, at[k < left ? k : 0], sat[k < left ? k : 0], d + 64 * i);
+#pragma unroll
+            for (int k = 0; k < AGAIN_AHEAD; ++k) {
+                const float pk = __shfl_sync(0xFFFFFFFFu, p, (j + k) & 31);
+                if (k < left)
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i) {
+                        const float2 v = r[k][i].get();
+                        o[2 * i] = fmaf(pk, v.x, o[2 * i]);
+                        o[2 * i + 1] = fmaf(pk, v.y, o[2 * i + 1]);
+                    }
+            }
+        });
+    uint16_t *out = a.out + ((size_t)t * a.Hq + h) * D;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+        if (d + 64 * i >= d0 && d + 64 * i < d1)
+            *reinterpret_cast<uint32_t *>(out + d + 64 * i) = f32x2_to_bf16x2(o[2 * i], o[2 * i + 1]);
+}
+
+// Rows (the lanes in the mask, each with its own arguments) whose outputs are not
+// finite: a product with a weight of zero is NaN when the value is NaN or
+// infinite, and such a value may lie where the row may not see it; and values
+// near the type's largest can overflow a sum whose weights are divided only at
+// its end.  What the values that all these rows see account for stands: a NaN
+// where one of them is NaN or both infinities are among them, an infinity where it
+// is among them (with a weight of zero it had become NaN).  Other rows are computed
+// again one by one.
+template <int D, int KVF>
+__device__ __noinline__ void rows_again(const AttnArgs &a, unsigned rows, int b, int t, int h, int lo, int hi, int d0,
+                                        int d1, float inv_total, float m_used, int *busy)
+{
+    const int lane = threadIdx.x & 31;
+    const bool mine = rows >> lane & 1;
+    if (lane == 0) atomicAdd(busy, 1);
+    __syncwarp();
+    const int all_lo = __reduce_max_sync(0xFFFFFFFFu, mine ? lo : 0);
+    const int all_hi = __reduce_min_sync(0xFFFFFFFFu, mine ? hi : 0x7FFFFFFF);
+    const int kvh = __shfl_sync(0xFFFFFFFFu, h, __ffs(rows) - 1) / a.g;
+    const uint32_t kinds = kinds_of_values<D, KVF>(a.kv, b, kvh, all_lo, all_hi);
+    for (; rows != 0; rows &= rows - 1) {
+        const int src = __ffs(rows) - 1;
+        const int row_t = __shfl_sync(0xFFFFFFFFu, t, src), row_h = __shfl_sync(0xFFFFFFFFu, h, src);
+        const volatile uint32_t *out = reinterpret_cast<const uint32_t *>(a.out + ((size_t)row_t * a.Hq + row_h) * D);
+        bool stands = true;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            const int d = 2 * lane + 64 * i;
+            if (d < d0 || d >= d1) continue;
+            const uint32_t w = out[d / 2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float x = e ? bf16_hi(w) : bf16_lo(w);
+                const uint32_t k = kinds >> (6 * i + 3 * e) & 7u;
+                if (x != x) stands = stands && ((k & 1u) || (k & 6u) == 6u);
+                else if (x * 0.0f != 0.0f) stands = stands && (k & (x > 0.0f ? 2u : 4u));
+            }
+        }
+        const int row_lo = __shfl_sync(0xFFFFFFFFu, lo, src), row_hi = __shfl_sync(0xFFFFFFFFu, hi, src);
+        const float row_inv = __shfl_sync(0xFFFFFFFFu, inv_total, src), row_m = __shfl_sync(0xFFFFFFFFu, m_used, src);
+        if (!__all_sync(0xFFFFFFFFu, stands))
+            row_again<D, KVF>(a, b, row_t, row_h, row_lo, row_hi, d0, d1, row_inv, row_m);
     }
+    if (lane == 0) atomicSub(busy, 1);
 }
 
 // Is a page missing that holds any of a sequence's keys [lo, hi)?  (Rare: a loop over
@@ -886,28 +993,28 @@ __device__ __noinline__ void arrive_cut(const AtParams &p, const Piece &piece, i
         if (check != 0.0f && inv == inv) atomicOr(again + row / 32, 1u << (row % 32));
     }
     group_sync(2 + w, 128);
-    // rows that saw a NaN or an infinity, or only multiplied one by zero
-    const bool some = again[tid / 32] != 0;
-    if (some && tid % 32 == 0) atomicAdd(&watch->busy, 1);
-    for (unsigned left = again[tid / 32]; left != 0; left &= left - 1) {
-        const int row = (tid & ~31) + __ffs(left) - 1;
-        const int tok = t0 + row / a.g, head = pc.kvh * a.g + row % a.g, pos = pc.first + tok;
-        const int hi = a.causal ? min(pos + 1, pc.len) : pc.len;
-        const int lo = a.window > 0 ? (int)max((long long)pos - a.window + 1, 0ll) : 0;
+    const unsigned rows = again[tid / 32];
+    if (rows == 0) return;
+    const int tok = t0 + tid / a.g, head = pc.kvh * a.g + tid % a.g, pos = pc.first + tok;
+    const int hi = a.causal ? min(pos + 1, pc.len) : pc.len;
+    const int lo = a.window > 0 ? (int)max((long long)pos - a.window + 1, 0ll) : 0;
+    float den = 0.0f, base2 = 0.0f;
+    if (rows >> tid % 32 & 1) {
         float m = -INFINITY, total = 0.0f;
         for (int i = 0; i < parts; ++i) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(partial_base<D>(p, pc.c0 + i, i == 0 ? 1 : 0, w)) + row);
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(partial_base<D>(p, pc.c0 + i, i == 0 ? 1 : 0, w)) + tid);
             const Merge mg(m, ml.x);
             m = mg.m;
             total = mg.add(total, ml.y);
         }
         const float sink = a.sinks ? __ldg(a.sinks + head) * 1.4426950408889634f : -INFINITY;
-        const float ref = fmaxf(m, sink), base2 = ref == -INFINITY ? 0.0f : ref;
-        float den = m == -INFINITY ? 0.0f : total * exp2_approx(m - base2);
+        const float ref = fmaxf(m, sink);
+        base2 = ref == -INFINITY ? 0.0f : ref;
+        den = m == -INFINITY ? 0.0f : total * exp2_approx(m - base2);
         if (a.sinks) den += exp2_approx(sink - base2);
-        row_again<KVF>(a, pc.b, pc.q0 + tok, head, lo, hi, d0, d0 + W, 1.0f / den, base2);
     }
-    if (some && tid % 32 == 0) atomicSub(&watch->busy, 1);
+    __syncwarp();
+    rows_again<D, KVF>(a, rows, pc.b, pc.q0 + tok, head, lo, hi, d0, d0 + W, 1.0f / den, base2, &watch->busy);
 }
 
 // A CTA whose wait gave up: the outputs of its pieces from number `done` on
@@ -1365,20 +1472,11 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 }
             }
             if (finish_here && warp_on) {
-                // rows that saw a NaN or an infinity, or only multiplied one by zero
                 float c0, c1;
                 unpack2(check, c0, c1);
-                unsigned again = __ballot_sync(0xFFFFFFFFu, valid && inv == inv && c0 + c1 != 0.0f);
-                const bool some = again != 0;
-                if (some && lane == 0) atomicAdd(&c.watch.busy, 1);
-                for (; again != 0; again &= again - 1) {
-                    const int src = __ffs(again) - 1;
-                    row_again<KVF>(a, pc.b, __shfl_sync(0xFFFFFFFFu, pc.q0 + tok, src),
-                                   __shfl_sync(0xFFFFFFFFu, head, src), __shfl_sync(0xFFFFFFFFu, rlo, src),
-                                   __shfl_sync(0xFFFFFFFFu, rhi, src), d0, d1,
-                                   1.0f / __shfl_sync(0xFFFFFFFFu, den, src), __shfl_sync(0xFFFFFFFFu, base2, src));
-                }
-                if (some && lane == 0) atomicSub(&c.watch.busy, 1);
+                const unsigned again = __ballot_sync(0xFFFFFFFFu, valid && inv == inv && c0 + c1 != 0.0f);
+                if (__builtin_expect(again != 0, 0))
+                    rows_again<D, KVF>(a, again, pc.b, pc.q0 + tok, head, rlo, rhi, d0, d1, 1.0f / den, base2, &c.watch.busy);
             }
             if (cut && !finish_here) {
                 if (row == 0) c.pending[w] = pc;

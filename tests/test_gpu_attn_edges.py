@@ -109,3 +109,60 @@ def test_rows_computed_again_outlast_a_wait(fmt, n, m):
         b.check()
     finally:
         ops.debug_qmm_stall(False, 0)
+
+
+def _put(b, half, s, pos, d, value, fmt="bf16"):
+    """A value into the cache and its copy; MXFP8: a NaN only, as its code."""
+    page, slot = b.place(s, pos)
+    (b.kv.v if half else b.kv.k)[page, :, slot, d] = value if fmt == "bf16" else 0x7F
+    b.halves[half][page, :, slot, d] = value
+
+
+@pytest.mark.parametrize("D,n,m", [(128, [6], [150]), (64, [1, 40], [513, 200]), (128, [1], [3000]), (64, [70, 5], [2500, 2600])])
+def test_kinds_of_values(D, n, m):
+    """NaN, infinities of one sign and of both, and sums that overflow, among what all rows see, what some see, and in the same
+    dimensions and others; small items, two row tiles and items cut across the GPU."""
+    need_gpu()
+    nan, inf = math.nan, math.inf
+    for case in ([(3, 5, inf)], [(3, 5, inf), (9, 5, -inf)], [(3, 5, nan), (9, 5, inf), (2, 6, -inf)],
+                 [(3, 5, inf), (-1, 5, nan)], [(3, 5, -inf), (-2, 9, inf), (-1, D - 1, nan)], [(3, 5, inf), (-1, 5, -inf)],
+                 [(3, 0, nan), (-1, 0, inf)]):
+        b = Batch(n, m, 8, 2, D, 16)
+        for pos, d, value in case:
+            _put(b, 1, 0, pos % m[0], d, value)
+        b.check()
+        b.check(window=30)
+    # sums beyond the type in one dimension, an infinity in another, in both signs
+    b = Batch(n, m, 8, 2, D, 16)
+    for x in (b.kv.v, b.halves[1]):
+        x[..., 7] = x[..., 7].abs() * 0 + 3e38
+        x[..., 40] = x[..., 40].abs() * 0 - 3e38
+    b.halves[1] = b.kv.v.double()
+    b.check()
+    _put(b, 1, 0, 3, 5, inf)
+    b.check()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_value_that_all_rows_see_costs_no_second_pass(fmt):
+    """A NaN that every row sees makes the call at most fifty times as long, not a thousand."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    b = Batch([256], [8192], 64, 8, 128, 64, fmt)
+
+    def shortest():
+        times = []
+        for _ in range(4):
+            e = [torch.cuda.Event(enable_timing=True) for _ in "ab"]
+            e[0].record()
+            ops.paged_attn(b.kv, b.q, b.q_start, b.kv_len)
+            e[1].record()
+            torch.cuda.synchronize()
+            times.append(e[0].elapsed_time(e[1]))
+        return min(times[1:])
+
+    clean = shortest()
+    _put(b, 1, 0, 17, 5, math.nan, fmt)
+    assert shortest() <= 50 * clean
+    assert torch.isnan(ops.paged_attn(b.kv, b.q, b.q_start, b.kv_len)[..., 5]).all()
