@@ -1415,6 +1415,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
 #pragma unroll 1
                 for (int d = d0; d < d1; d += EC) {
                     uint32_t u[EC], v[EC];
+                    __syncwarp();  // lanes without a row come back from below
                     tmem_ld16_async(lane_base + G::O_COL + 128 * w + d, u);
                     tmem_ld16_async(lane_base + G::O_COL + 128 * (w ^ 1) + d, v);
                     tmem_wait_ld();
