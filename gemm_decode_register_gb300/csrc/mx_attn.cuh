@@ -34,7 +34,7 @@ __device__ __forceinline__ int sequence_of(const int32_t *q_start, int B, int t)
 // Page of position `pos` (>= 0) of a sequence, -1 if it has none.
 __device__ __forceinline__ int page_of(const mx_paged_kv &kv, const int32_t *row, int page_index)
 {
-    if (page_index >= kv.table_stride) return -1;
+    if (page_index >= kv.table_pages) return -1;
     const int p = __ldg(row + page_index);
     return (unsigned)p < (unsigned)kv.num_pages ? p : -1;
 }

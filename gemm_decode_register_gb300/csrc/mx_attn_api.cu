@@ -19,7 +19,8 @@ int check_kv(const mx_paged_kv *kv)
     if (!kv || !kv->k || !kv->v || !kv->block_table) return MX_EINVAL;
     if (kv->kv_fmt != MX_KV_BF16 && kv->kv_fmt != MX_KV_MXFP8) return MX_EUNSUPPORTED;
     const bool mx8 = kv->kv_fmt == MX_KV_MXFP8;
-    if (kv->num_pages <= 0 || kv->page_size <= 0 || kv->Hkv <= 0 || kv->D <= 0 || kv->table_stride <= 0)
+    if (kv->num_pages <= 0 || kv->page_size <= 0 || kv->Hkv <= 0 || kv->D <= 0 || kv->table_stride <= 0 ||
+        kv->table_pages < 0 || kv->table_pages > kv->table_stride)
         return MX_EINVAL;
     if (kv->page_stride <= 0 || kv->head_stride <= 0 || kv->token_stride <= 0) return MX_EINVAL;
     if (mx8 && (!kv->k_scales || !kv->v_scales || kv->scale_page_stride <= 0 || kv->scale_head_stride <= 0 ||
@@ -31,6 +32,14 @@ int check_kv(const mx_paged_kv *kv)
         kv->token_stride % unit || !aligned(kv->block_table, 4))
         return MX_EALIGN;
     return MX_OK;
+}
+
+// The descriptor as the kernels take it.
+mx_paged_kv filled_in(const mx_paged_kv &kv)
+{
+    mx_paged_kv d = kv;
+    if (d.table_pages == 0) d.table_pages = d.table_stride;
+    return d;
 }
 
 int check_batch(const int32_t *q_start, const int32_t *kv_len, int T, int B)
@@ -92,7 +101,7 @@ extern "C" int mx_kv_append(const mx_paged_kv *kv, const void *rows, int dtype, 
         return MX_EALIGN;
     DeviceState *ds = device_state();
     if (!ds) return MX_ECUDA;
-    return finish(launch_kv_append(*ds, current_stream(), *kv, rows, dtype, row_stride, q_start, kv_len, table,
+    return finish(launch_kv_append(*ds, current_stream(), filled_in(*kv), rows, dtype, row_stride, q_start, kv_len, table,
                                    table_len, rot, static_cast<uint16_t *>(q), T, B, Hq, flags));
 }
 
@@ -127,7 +136,7 @@ extern "C" int mx_paged_attn(const mx_paged_kv *kv, const void *q, int64_t q_tok
     DeviceState *ds = device_state();
     if (!ds) return MX_ECUDA;
     AttnArgs a;
-    a.kv = *kv;
+    a.kv = filled_in(*kv);
     a.q = static_cast<const uint16_t *>(q);
     a.q_token_stride = q_token_stride;
     a.q_head_stride = q_head_stride;

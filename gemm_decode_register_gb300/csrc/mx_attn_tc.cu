@@ -1531,7 +1531,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     const long long key = (long long)(pc.tile0 + wn * per_win) * AT_KEYS + lane * prm.page_rows;
                     if (key >= pc.hi || key + prm.page_rows <= pc.lo) return -1;
                     const int i = (int)key / a.kv.page_size;
-                    return i < a.kv.table_stride ? i : -2;
+                    return i < a.kv.table_pages ? i : -2;
                 };
                 auto id_of = [&](int index, int entry) {  // -2: missing
                     return index < 0 ? index : (unsigned)entry < (unsigned)a.kv.num_pages ? entry : -2;

@@ -353,7 +353,8 @@ class _PagedKV(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "v_scales", "block_table")]
     _fields_ += [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride", "scale_page_stride",
                                                "scale_head_stride", "scale_token_stride")]
-    _fields_ += [(n, ctypes.c_int32) for n in ("kv_fmt", "num_pages", "page_size", "Hkv", "D", "table_stride")]
+    _fields_ += [(n, ctypes.c_int32) for n in ("kv_fmt", "num_pages", "page_size", "Hkv", "D", "table_stride",
+                                               "table_pages")]
 
 
 class PagedKV:
@@ -364,7 +365,8 @@ class PagedKV:
                  dimension contiguous (a transposed view of tokens-major pages
                  works), the same for both: bf16, or uint8 E4M3 codes with
     k_scales, v_scales  uint8 E8M0 [num_pages][Hkv][page_size][D/32]
-    block_table  int32 [B][pages], the last dimension contiguous
+    block_table  int32 [B][pages], the last dimension contiguous (the first
+                 columns of a wider table work; the columns past them are not read)
 
     The object keeps the tensors alive and may be kept and reused while the
     table's contents change."""
@@ -389,11 +391,11 @@ class PagedKV:
             c.scale_page_stride, c.scale_head_stride, c.scale_token_stride, _ = k_scales.stride()
         c.kv_fmt = KV_MXFP8 if mx8 else KV_BF16
         c.block_table = _cuda("block_table", block_table, torch.int32, 2)
-        # one row may have any stride; several are as far apart as the table says
-        self.B = block_table.shape[0]
-        c.table_stride = block_table.shape[1] if self.B == 1 else block_table.stride(0)
-        if self.B > 1 and block_table.stride(0) != block_table.shape[1]:
-            raise ValueError("block_table: expected contiguous rows")
+        self.B, c.table_pages = block_table.shape
+        stride = c.table_pages if self.B == 1 else block_table.stride(0)  # (one row may have any stride)
+        if not c.table_pages <= stride < 1 << 31:
+            raise ValueError("block_table: expected rows that do not overlap")
+        c.table_stride = stride
         self.k, self.v, self.k_scales, self.v_scales, self.block_table = k, v, k_scales, v_scales, block_table
         self.Hkv, self.D = c.Hkv, c.D
         self._c = c

@@ -303,6 +303,7 @@ typedef struct mx_paged_kv {
     int64_t page_stride, head_stride, token_stride;
     int64_t scale_page_stride, scale_head_stride, scale_token_stride;
     int32_t kv_fmt, num_pages, page_size, Hkv, D, table_stride;
+    int32_t table_pages; /* entries of a table row that may be used, at most table_stride; 0: table_stride */
 } mx_paged_kv;
 
 /* Rotation table: table[p - pos0][i] = (cos a, sin a) * factor with

@@ -119,3 +119,10 @@ def test_an_empty_rotation_table_is_refused(lib):
     append = [ctypes.byref(c), A, 0, 2048, A, A, A, 0, 128, A, 4, 2, 8, 0]
     assert lib.mx_rope(*rope) == -1
     assert lib.mx_kv_append(*append) == -1
+
+
+@pytest.mark.parametrize("pages", [-1, 9])
+def test_table_pages_within_a_row(lib, pages):
+    c = ctypes.byref(kv(table_pages=pages))
+    assert lib.mx_kv_append(c, A, 0, 2048, A, A, A, 64, 128, A, 4, 2, 8, 0) == -1
+    assert lib.mx_paged_attn(c, A, 1024, 128, A, A, 0.1, 1, 0, None, A, None, 4, 2, 8, A, 1 << 40) == -1

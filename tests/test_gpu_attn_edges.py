@@ -166,3 +166,43 @@ def test_a_value_that_all_rows_see_costs_no_second_pass(fmt):
     _put(b, 1, 0, 17, 5, math.nan, fmt)
     assert shortest() <= 50 * clean
     assert torch.isnan(ops.paged_attn(b.kv, b.q, b.q_start, b.kv_len)[..., 5]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("page", [16, 48])
+def test_first_columns_of_a_wider_table(fmt, page):
+    """A server keeps one wide table: rows are as far apart as it is wide, and what lies past the view's columns is no page of
+    the context."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    b = Batch([2, 40, 1], [70, 100, 300], 8, 2, 128, page, fmt)
+    want = b.check()[0]
+    table = b.kv.block_table
+    n = table.shape[1]
+    wide = torch.full((3, n + 13), 1, dtype=torch.int32, device="cuda")
+    wide[:, :n] = table
+    halves = (b.kv.k, b.kv.v)
+    scales = (b.kv.k_scales, b.kv.v_scales)
+    kv = ops.PagedKV(*halves, wide[:, :n], *scales)
+    assert torch.equal(ops.paged_attn(kv, b.q, b.q_start, b.kv_len), want)
+    assert torch.equal(ops.paged_attn(ops.PagedKV(*halves, wide, *scales), b.q, b.q_start, b.kv_len), want)
+    one = ops.PagedKV(*halves, wide[2:, :n], *scales)
+    first = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    assert torch.equal(ops.paged_attn(one, b.q[42:], first, b.kv_len[2:]), want[42:])
+    assert ops.device_error() == 0
+    # a page of the last context is past the view: missing for the attention, and for the append
+    short = ops.PagedKV(*halves, wide[:, :299 // page], *scales)
+    out = ops.paged_attn(short, b.q, b.q_start, b.kv_len)
+    assert ops.device_error() == 0x4
+    assert torch.isnan(out[42]).all() and torch.equal(out[:42], want[:42])
+    rows = torch.randn((b.T, 12 * 128), device="cuda")
+    before = b.kv.k.clone()
+    q = ops.kv_append(short, rows, b.q_start, b.kv_len, 8, None)
+    assert ops.device_error() == 0x4
+    assert torch.isnan(q[42]).all() and torch.isfinite(q[:42]).all()
+    at, slot = b.place(2, 299)
+    assert torch.equal(b.kv.k[at, :, slot].view(torch.uint8), before[at, :, slot].view(torch.uint8))
+    for table in (wide[:1].expand(3, n + 13), wide.t()[:3]):
+        with pytest.raises(ValueError):
+            ops.PagedKV(*halves, table, *scales)
