@@ -414,7 +414,7 @@ class PagedKV:
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
-                     original_len: int = 8192, low: float = 1.0, high: float = 4.0) -> tuple[torch.Tensor, float]:
+                     original_len: int = 8192, low: float = 1.0, high: float | None = None) -> tuple[torch.Tensor, float]:
     """Radians per position of the rot/2 pairs (fp64) and the factor on the
     cosines and sines, base^(-2i/rot) and 1 unless a scaling for contexts
     longer than the trained `original_len` changes them:
@@ -422,12 +422,16 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", fac
     "linear"  every frequency over `factor`;
     "base"    the base times factor^(rot/(rot-2)): the slowest pair turns
               `factor` times slower, the fastest as before;
-    "banded"  by the turns a pair makes over original_len: above `high`
-              unchanged, below `low` over `factor`, blended between;
+    "banded"  by the turns a pair makes over original_len: above `high` (4)
+              unchanged, below `low` (1) over `factor`, blended between;
     "yarn"    the blend runs over the pair's number, between those that turn
-              `high` and `low` times (32 and 1 as published), and cosines and
-              sines grow by 0.1 ln(factor) + 1.
+              `high` (32) and `low` (1) times, and cosines and sines grow by
+              0.1 ln(factor) + 1.
+
+    In brackets what `high` and `low` are where they are left out, as published.
     """
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
     if rot <= 0 or rot % 2 or base <= 1.0 or factor < 1.0:
         raise ValueError("rope_frequencies: rot even and positive, base > 1, factor >= 1")
     i = torch.arange(0, rot, 2, dtype=torch.float64)

@@ -126,3 +126,13 @@ def test_table_pages_within_a_row(lib, pages):
     c = ctypes.byref(kv(table_pages=pages))
     assert lib.mx_kv_append(c, A, 0, 2048, A, A, A, 64, 128, A, 4, 2, 8, 0) == -1
     assert lib.mx_paged_attn(c, A, 1024, 128, A, A, 0.1, 1, 0, None, A, None, 4, 2, 8, A, 1 << 40) == -1
+
+
+def test_published_bands_are_the_defaults():
+    """Left out, the band's upper end is each scaling's own: 4 turns (banded), 32 (YaRN)."""
+    for scaling, high in (("yarn", 32.0), ("banded", 4.0)):
+        kw = dict(factor=8.0, original_len=4096)
+        f, m = ops.rope_frequencies(128, 10000.0, scaling, **kw)
+        g, n = ops.rope_frequencies(128, 10000.0, scaling, low=1.0, high=high, **kw)
+        h, _ = ops.rope_frequencies(128, 10000.0, scaling, low=1.0, high=36.0 - high, **kw)
+        assert f.tolist() == g.tolist() and m == n and f.tolist() != h.tolist()
