@@ -206,3 +206,43 @@ def test_first_columns_of_a_wider_table(fmt, page):
     for table in (wide[:1].expand(3, n + 13), wide.t()[:3]):
         with pytest.raises(ValueError):
             ops.PagedKV(*halves, table, *scales)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_unused_slots(fmt):
+    """Batches most of whose sequences have no new tokens: before, between and after the ones that do, whole and cut items."""
+    need_gpu()
+    for B, some in ((100, {0: (3, 40)}), (100, {99: (1, 3000)}), (300, {0: (1, 20), 33: (5, 9), 290: (40, 700)}),
+                    (2000, {1: (1, 5000), 500: (2, 4000), 1800: (1, 100), 1999: (1, 9000)}),
+                    (700, {i: (1, 1500 + i) for i in range(0, 700, 69)})):
+        Batch([some.get(i, (0, 0))[0] for i in range(B)], [some.get(i, (0, 0))[1] for i in range(B)], 8, 2, 64, 16, fmt).check()
+
+
+def test_unused_slots_cost_little():
+    """One token in a batch of 4096 slots takes at most ten times as long as by itself, not fifty."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    def shortest(B):
+        b = Batch([1] + [0] * (B - 1), [300] + [0] * (B - 1), 8, 1, 128, 16)
+        graph = torch.cuda.CUDAGraph()  # the call by itself, without the host's part
+        out, ws = torch.empty_like(b.q), ops.paged_attn_workspace(1, B, 8, 1, 128)
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            ops.paged_attn(b.kv, b.q, b.q_start, b.kv_len, out=out, workspace=ws)
+        s.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            for _ in range(10):
+                ops.paged_attn(b.kv, b.q, b.q_start, b.kv_len, out=out, workspace=ws)
+        times = []
+        for _ in range(4):
+            e = [torch.cuda.Event(enable_timing=True) for _ in "ab"]
+            e[0].record()
+            graph.replay()
+            e[1].record()
+            torch.cuda.synchronize()
+            times.append(e[0].elapsed_time(e[1]))
+        return min(times[1:])
+
+    one, many = shortest(1), shortest(4096)
+    assert many <= 10 * one, (many, one)
