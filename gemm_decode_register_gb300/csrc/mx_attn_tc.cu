@@ -197,7 +197,9 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b, int s1)
     return q;
 }
 
-// The first sequence from b on that has new tokens (B: none), by the whole warp.
+// The first sequence from b on that has new tokens (B: none), by the whole warp, 32 at
+// a time: a batch may have many unused slots (one token in 4096 slots: 797 us one
+// by one, 39 so).
 __device__ __forceinline__ int next_with_tokens(const AttnArgs &a, int b)
 {
     for (; b < a.B; b += 32) {
@@ -260,11 +262,9 @@ struct Walk {
     {
         for (;;) {
             if (at >= st.end) return false;
-            // the sequence is done; of a row of empty ones (a batch's unused slots) 32 are
-            // looked at together (one token in 4096 slots: 797 us one by one, 39 so)
-            while (b < a.B && (kvh >= cost.heads || q.pairs == 0)) {
-                b = q.pairs == 0 ? next_with_tokens(a, b + 1) : b + 1;
-                kvh = p = 0;
+            if (kvh >= cost.heads) {  // the sequence is done
+                b = next_with_tokens(a, b + 1);
+                kvh = 0;
                 if (b < a.B) q = load_seq(a, b, s1);
             }
             if (b >= a.B) return false;
