@@ -65,8 +65,29 @@ __global__ void __launch_bounds__(DIRECT_WARPS * 32) attn_direct_kernel(AttnArgs
         f[w] = exp2f(part_m[w] - base);
         l = fmaf(part_l[w], f[w], l);
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const bool bad = missing != 0;
+    // Values near the type's largest can overflow sums that are divided only at the
+    // end: a second pass with the weights divided first, in the rare case that one is not finite.
+    float check = 0.0f;
+    for (int d = threadIdx.x; d < a.kv.D; d += blockDim.x) {
+        float o = 0.0f;
+#pragma unroll
+        for (int w = 0; w < DIRECT_WARPS; ++w) o = fmaf(part_o[w][d], f[w], o);
+        check += o * 0.0f;
+    }
+    if (__syncthreads_or(!bad && inv == inv && check != 0.0f)) {
+        RowState again;
+        again.m = base;
+        row_keys<KVF, true>(a.kv, a.kv.block_table + (size_t)b * a.kv.table_stride, h / a.g, q, a.scale_log2, lo, hi,
+                            (lo & ~31) + 32 * warp, DIRECT_WARPS, again, inv);
+#pragma unroll
+        for (int i = 0; i < MAX_D / 32; ++i) part_o[warp][2 * lane + 64 * (i / 2) + i % 2] = again.o[i];
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < DIRECT_WARPS; ++w) f[w] = 1.0f;
+        inv = 1.0f;
+    }
     if (bad && threadIdx.x == 0) set_device_error(a.err, DEVERR_BAD_PAGE);
     const size_t row = (size_t)t * a.Hq + h;
     for (int d = threadIdx.x; d < a.kv.D; d += blockDim.x) {

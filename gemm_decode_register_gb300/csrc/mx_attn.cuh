@@ -134,10 +134,11 @@ __device__ __forceinline__ void add_value(const mx_paged_kv &kv, long long at, l
 }
 
 // Adds keys first, first + 32 step, ... (32 at a time) below hi to the row;
-// keys below lo are skipped.  false if a page is missing.
-template <int KVF>
+// keys below lo are skipped.  false if a page is missing.  FIXED: against the
+// row's final maximum r.m, each weight times 1 / sum (`inv`) before it is used; only r.o is added to.
+template <int KVF, bool FIXED = false>
 __device__ bool row_keys(const mx_paged_kv &kv, const int32_t *table, int kvh, const float *q, float scale_log2,
-                         int lo, int hi, int first, int step, RowState &r)
+                         int lo, int hi, int first, int step, RowState &r, float inv = 1.0f)
 {
     const int lane = threadIdx.x & 31;
     bool all = true;
@@ -158,21 +159,26 @@ __device__ bool row_keys(const mx_paged_kv &kv, const int32_t *table, int kvh, c
             }
         }
         const unsigned mask = __ballot_sync(0xFFFFFFFFu, seen);
-        float top = s;
+        float p;
+        if constexpr (FIXED) {
+            p = seen ? exp2f(s - r.m) * inv : 0.0f;
+        } else {
+            float top = s;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const float m = fmaxf(r.m, top);
-        // nothing seen yet, or only scores of -infinity: their weights are zero, unless one is NaN
-        const float base = m == -INFINITY ? 0.0f : m;
-        const float p = seen ? exp2f(s - base) : 0.0f;
-        const float shrink = exp2f(r.m - base);
-        r.m = m;
-        float sum = p;
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const float m = fmaxf(r.m, top);
+            // nothing seen yet, or only scores of -infinity: their weights are zero, unless one is NaN
+            const float base = m == -INFINITY ? 0.0f : m;
+            p = seen ? exp2f(s - base) : 0.0f;
+            const float shrink = exp2f(r.m - base);
+            r.m = m;
+            float sum = p;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        r.l = fmaf(r.l, shrink, sum);
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            r.l = fmaf(r.l, shrink, sum);
 #pragma unroll
-        for (int i = 0; i < MAX_D / 32; ++i) r.o[i] *= shrink;
+            for (int i = 0; i < MAX_D / 32; ++i) r.o[i] *= shrink;
+        }
         for (unsigned left = mask; left != 0; left &= left - 1) {
             const int src = __ffs(left) - 1;
             const float pj = __shfl_sync(0xFFFFFFFFu, p, src);

@@ -246,3 +246,23 @@ def test_unused_slots_cost_little():
 
     one, many = shortest(1), shortest(4096)
     assert many <= 10 * one, (many, one)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 48), (96, 16), (256, 7)])
+def test_sums_near_the_types_largest(fmt, D, page):
+    """Averages of values near the largest number are finite, whichever kernel takes the call: their sum is not formed."""
+    torch = need_gpu()
+    b = Batch([1, 9, 1], [400, 70, 1], 4, 2, D, page, fmt)
+    for sign, d in ((1, 7), (-1, D - 1)):
+        if fmt == "bf16":
+            b.kv.v[..., d] = b.halves[1][..., d] = sign * 3e38
+            b.halves[1] = b.kv.v.double()
+        else:  # 384 * 2^119 in the block of the dimension
+            block = slice(d // 32 * 32, d // 32 * 32 + 32)
+            b.kv.v[..., block] = 0
+            b.kv.v[..., d] = 0x7C if sign > 0 else 0xFC
+            b.kv.v_scales[..., d // 32] = 119 + 127
+            b.halves[1] = ref.mxfp8_values(b.kv.v, b.kv.v_scales)
+    out, _ = b.check()
+    assert torch.isfinite(out).all() and out[0, 0, 7] > 1e38 and out[0, 0, D - 1] < -1e38
