@@ -349,6 +349,17 @@ def _whole(name: str, t: torch.Tensor, dtype, shape: tuple) -> int:
                      f"{tuple(t.shape)} on {t.device}")
 
 
+def _strides(t: torch.Tensor) -> tuple:
+    """Strides; of a dimension of length one, where they may be anything, those of a tensor whose elements lie together."""
+    if 1 not in t.shape:
+        return t.stride()
+    s = list(t.stride())
+    for i in range(t.dim() - 2, -1, -1):
+        if t.shape[i] == 1:
+            s[i] = t.shape[i + 1] * s[i + 1]
+    return tuple(s)
+
+
 class _PagedKV(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "v_scales", "block_table")]
     _fields_ += [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride", "scale_page_stride",
@@ -379,16 +390,16 @@ class PagedKV:
         dtype = torch.uint8 if mx8 else torch.bfloat16
         c = _PagedKV()
         c.k, c.v = _cuda("k", k, dtype, 4), _cuda("v", v, dtype, 4)
-        if k.shape != v.shape or k.stride() != v.stride():
+        if k.shape != v.shape or _strides(k) != _strides(v):
             raise ValueError("k and v: expected the same shape and strides")
         c.num_pages, c.Hkv, c.page_size, c.D = k.shape
-        c.page_stride, c.head_stride, c.token_stride, _ = k.stride()
+        c.page_stride, c.head_stride, c.token_stride, _ = _strides(k)
         if mx8:
             c.k_scales, c.v_scales = (_cuda("scales", t, torch.uint8, 4) for t in (k_scales, v_scales))
             want = (*k.shape[:3], k.shape[3] // 32)
-            if k_scales.shape != want or v_scales.shape != want or k_scales.stride() != v_scales.stride():
+            if k_scales.shape != want or v_scales.shape != want or _strides(k_scales) != _strides(v_scales):
                 raise ValueError(f"scales: expected shape {want} and the same strides")
-            c.scale_page_stride, c.scale_head_stride, c.scale_token_stride, _ = k_scales.stride()
+            c.scale_page_stride, c.scale_head_stride, c.scale_token_stride, _ = _strides(k_scales)
         c.kv_fmt = KV_MXFP8 if mx8 else KV_BF16
         c.block_table = _cuda("block_table", block_table, torch.int32, 2)
         self.B, c.table_pages = block_table.shape
@@ -485,6 +496,10 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor | None, i
     xp = _cuda("x", x, x.dtype, 3)
     T, H, D = x.shape
     xt, xh, _ = x.stride()
+    if H == 1:  # (as _strides)
+        xh = D
+    if T == 1:
+        xt = H * xh
     if out is None:
         out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
         op, yt, yh = out.data_ptr(), H * D, D
@@ -492,7 +507,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor | None, i
         if out.shape != x.shape:
             raise ValueError("out: expected the shape of x")
         op = _cuda("out", out, x.dtype, 3)
-        yt, yh, _ = out.stride()
+        yt, yh, _ = _strides(out)
     tp, n, rot = _table_arg(table)
     pp = _whole("positions", positions, torch.int32, (T,))
     if T == 0:
@@ -525,8 +540,9 @@ def kv_append(kv: PagedKV, rows: torch.Tensor, q_start: torch.Tensor, kv_len: to
     if T == 0:
         return q
     _stream()
-    _check("mx_kv_append", load().mx_kv_append(kv._ref, rp, _DTYPES[rows.dtype], rows.stride(0), sp, lp, tp, n, rot,
-                                               qp, T, kv.B, Hq, ROPE_INTERLEAVED if interleaved else 0))
+    stride = rows.stride(0) if T > 1 else rows.shape[1]
+    _check("mx_kv_append", load().mx_kv_append(kv._ref, rp, _DTYPES[rows.dtype], stride, sp, lp, tp, n, rot, qp, T, kv.B,
+                                               Hq, ROPE_INTERLEAVED if interleaved else 0))
     return q
 
 
@@ -569,6 +585,10 @@ def paged_attn(kv: PagedKV, q: torch.Tensor, q_start: torch.Tensor, kv_len: torc
                 workspace = _workspace(need, None, q.device)
         wp, wn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
         qt, qh, _ = q.stride()
+        if Hq == 1:  # (as _strides)
+            qh = D
+        if T == 1:
+            qt = Hq * qh
         _stream()
         _check("mx_paged_attn", lib.mx_paged_attn(kv._ref, qp, qt, qh, sp, lp,
                                                   1.0 / math.sqrt(D) if scale is None else scale,

@@ -266,3 +266,32 @@ def test_sums_near_the_types_largest(fmt, D, page):
             b.halves[1] = ref.mxfp8_values(b.kv.v, b.kv.v_scales)
     out, _ = b.check()
     assert torch.isfinite(out).all() and out[0, 0, 7] > 1e38 and out[0, 0, D - 1] < -1e38
+
+
+def test_strides_of_dimensions_of_one():
+    """A dimension of length one may have any stride: a single token, page, head or place."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    def odd(t):
+        """The same elements; dimensions of one get a stride that nothing could use."""
+        return torch.as_strided(t, t.shape, [s if n > 1 or i == t.dim() - 1 else 3
+                                             for i, (n, s) in enumerate(zip(t.shape, t.stride()))])
+
+    for fmt in (ops.KV_BF16, ops.KV_MXFP8):
+        for Hq, Hkv, page in ((4, 1, 16), (4, 2, 16), (1, 1, 1)):
+            D, table = 64, torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+            kv = ops.PagedKV.empty(1, Hkv, page, D, table, fmt)
+            view = ops.PagedKV(odd(kv.k), odd(kv.v), odd(table), *(odd(s) for s in (kv.k_scales, kv.v_scales) if s is not None))
+            one = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+            rows = torch.randn((1, (Hq + 2 * Hkv) * D), device="cuda")
+            turn = ops.rope_table(ops.rope_frequencies(D)[0], 4)
+            q = ops.kv_append(kv, rows, one, one[1:], Hq, turn)
+            want = ops.paged_attn(kv, q, one, one[1:])
+            assert torch.equal(ops.kv_append(view, odd(rows), one, one[1:], Hq, turn), q)
+            assert torch.equal(ops.paged_attn(view, odd(q), one, one[1:]), want)
+            x = rows.view(1, -1, D)
+            turned = ops.rope(x, one[:1], turn)
+            out = torch.empty_like(x)
+            assert torch.equal(ops.rope(odd(x), one[:1], turn, out=odd(out)), turned) and torch.equal(out, turned)
+    assert ops.device_error() == 0
