@@ -556,7 +556,7 @@ def paged_attn(kv: PagedKV, q: torch.Tensor, q_start: torch.Tensor, kv_len: torc
                workspace: torch.Tensor | None = None):
     """Attention of the new tokens' queries q [T][Hq][D] (bf16, the last dimension
     contiguous) over their contexts in the cache; out bf16 [T][Hq][D], and with
-    return_lse (out, lse) with lse fp32 [T][Hq].  scale: 1/sqrt(D) by default; window > 0: each token sees
+    return_lse (out, lse) with lse fp32 [T][Hq].  scale: 1/sqrt(D) by default; window > 0 (of any size): each token sees
     itself and the window - 1 tokens before it; sinks fp32 [Hq]."""
     qp = _cuda("q", q, torch.bfloat16, 3)
     T, Hq, D = q.shape
@@ -592,7 +592,8 @@ def paged_attn(kv: PagedKV, q: torch.Tensor, q_start: torch.Tensor, kv_len: torc
         _stream()
         _check("mx_paged_attn", lib.mx_paged_attn(kv._ref, qp, qt, qh, sp, lp,
                                                   1.0 / math.sqrt(D) if scale is None else scale,
-                                                  ATTN_CAUSAL if causal else 0, window, kp, op, ep, T, B, Hq, wp, wn))
+                                                  ATTN_CAUSAL if causal else 0,
+                                                  max(-1, min(window, 0x7FFFFFFF)), kp, op, ep, T, B, Hq, wp, wn))
     return (out, lse) if return_lse else out
 
 

@@ -295,3 +295,17 @@ def test_strides_of_dimensions_of_one():
             out = torch.empty_like(x)
             assert torch.equal(ops.rope(odd(x), one[:1], turn, out=odd(out)), turned) and torch.equal(out, turned)
     assert ops.device_error() == 0
+
+
+def test_windows_beyond_32_bits():
+    """A window past the largest int is no window, not what is left of its bits; a negative one is refused."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    b = Batch([2], [40], 8, 1, 128, 16)
+    want = b.check()[0]
+    for window in ((1 << 31) - 1, 1 << 31, (1 << 32) + 5, (1 << 63) - 1, 1 << 64):
+        assert torch.equal(ops.paged_attn(b.kv, b.q, b.q_start, b.kv_len, window=window), want)
+    for window in (-1, 5 - (1 << 32)):
+        with pytest.raises(ops.MxError):
+            ops.paged_attn(b.kv, b.q, b.q_start, b.kv_len, window=window)
