@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(DIRECT_WARPS * 32) attn_direct_kernel(AttnArgs
     __syncthreads();
     RowState r;
     const bool all = row_keys<KVF>(a.kv, a.kv.block_table + (size_t)b * a.kv.table_stride, h / a.g, q, a.scale_log2,
-                                   lo, hi, (lo & ~31) + 32 * warp, DIRECT_WARPS, r);
+                                   lo, hi, (lo & ~31ll) + 32 * warp, DIRECT_WARPS, r);
     if (!all) missing = 1;
     if (lane == 0) {
         part_m[warp] = r.m;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(DIRECT_WARPS * 32) attn_direct_kernel(AttnArgs
         RowState again;
         again.m = base;
         row_keys<KVF, true>(a.kv, a.kv.block_table + (size_t)b * a.kv.table_stride, h / a.g, q, a.scale_log2, lo, hi,
-                            (lo & ~31) + 32 * warp, DIRECT_WARPS, again, inv);
+                            (lo & ~31ll) + 32 * warp, DIRECT_WARPS, again, inv);
 #pragma unroll
         for (int i = 0; i < MAX_D / 32; ++i) part_o[warp][2 * lane + 64 * (i / 2) + i % 2] = again.o[i];
         __syncthreads();

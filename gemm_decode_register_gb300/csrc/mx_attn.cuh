@@ -138,7 +138,7 @@ __device__ __forceinline__ void add_value(const mx_paged_kv &kv, long long at, l
 // row's final maximum r.m, each weight times 1 / sum (`inv`) before it is used; only r.o is added to.
 template <int KVF, bool FIXED = false>
 __device__ bool row_keys(const mx_paged_kv &kv, const int32_t *table, int kvh, const float *q, float scale_log2,
-                         int lo, int hi, int first, int step, RowState &r, float inv = 1.0f)
+                         int lo, int hi, long long first, int step, RowState &r, float inv = 1.0f)
 {
     const int lane = threadIdx.x & 31;
     bool all = true;

@@ -270,7 +270,7 @@ struct Walk {
             if (b >= a.B) return false;
             cost.range(q, p, o.lo, o.hi);
             o.tile0 = o.lo / AT_KEYS;
-            o.tiles = o.hi > o.lo ? (o.hi + AT_KEYS - 1) / AT_KEYS - o.tile0 : 0;
+            o.tiles = o.hi > o.lo ? (o.hi - 1) / AT_KEYS + 1 - o.tile0 : 0;  // (hi: up to 2^31 - 1)
             // tile k begins at cost at + 128 k and is its CTA's whose stretch holds that
             o.k0 = st.start <= at ? 0 : (int)min((st.start - at + AT_KEYS - 1) / AT_KEYS, (long long)o.tiles);
             o.k1 = st.flat ? o.tiles : (int)min((st.end - at + AT_KEYS - 1) / AT_KEYS, (long long)o.tiles);
@@ -1203,7 +1203,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                 const int key0 = (pc.tile0 + pc.k0 + t) * AT_KEYS;
                 // rows of V that no row sees, or that were not loaded: their
                 // weights are zero, their values must be finite
-                if ((key0 < pc.lo || key0 + AT_KEYS > pc.hi) && (w == 0 || !pc.rows)) {
+                if ((key0 < pc.lo || key0 > pc.hi - AT_KEYS) && (w == 0 || !pc.rows)) {
                     const int vi = base + v_load(t, n, ahead);
                     alive = wait(&full[vi % G::SLOTS], vi / G::SLOTS);
                     if (!alive) break;
@@ -1217,7 +1217,7 @@ __global__ void __launch_bounds__(AtGeo<D, KVF>::THREADS, 1)
                     fence_proxy_async_smem();
                 }
                 tc_fence_after();
-                if (__builtin_expect(__any_sync(0xFFFFFFFFu, key0 < rlo || key0 + AT_KEYS > rhi), 0)) {
+                if (__builtin_expect(__any_sync(0xFFFFFFFFu, key0 < rlo || key0 > rhi - AT_KEYS), 0)) {
                     // scores that the row may not see, in place: a small loop, for the instruction cache
                     const int klo = rlo - key0, khi = rhi - key0;
 #pragma unroll 1

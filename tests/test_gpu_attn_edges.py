@@ -309,3 +309,41 @@ def test_windows_beyond_32_bits():
     for window in (-1, 5 - (1 << 32)):
         with pytest.raises(ops.MxError):
             ops.paged_attn(b.kv, b.q, b.q_start, b.kv_len, window=window)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("page", [1 << 20, (1 << 20) - 48])
+@pytest.mark.parametrize("length", [(1 << 31) - 1, (1 << 31) - 127, (1 << 31) - 128])
+def test_longest_contexts(fmt, page, length):
+    """Contexts up to the largest int (a window over pages of which the last two exist): the end of the last key tile is past
+    it.  Without the pages: NaN and the error, and the next call is right."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    D, n = 64, 3
+    pages = (length - 1) // page + 1
+    table = torch.full((1, pages), -1, dtype=torch.int32, device="cuda")
+    table[0, -2:] = torch.tensor([1, 0], dtype=torch.int32)
+    kv = ops.PagedKV.empty(2, 1, page, D, table, ops.KV_BF16 if fmt == "bf16" else ops.KV_MXFP8)
+    for t in (kv.k, kv.v, kv.k_scales, kv.v_scales):
+        if t is not None:
+            t.fill_(math.nan if fmt == "bf16" else 0xFF)  # (0xFF: a NaN code, and the NaN scale)
+    rows = torch.randn((300, 4 * D), generator=torch.Generator(device="cuda").manual_seed(6), device="cuda")
+    first = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+    kl = torch.tensor([length], dtype=torch.int32, device="cuda")
+    q = ops.kv_append(kv, rows, first, kl, 2, None)[-n:].contiguous()
+    first = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    at = torch.arange(length - 300, length, device="cuda")
+    k, v = (h[table[0, at // page].long(), :, at % page].transpose(0, 1) for h in (
+        (kv.k.double(), kv.v.double()) if fmt == "bf16" else
+        (ref.mxfp8_values(kv.k, kv.k_scales), ref.mxfp8_values(kv.v, kv.v_scales))))
+    for window in (1, 100, 280):
+        out, lse = ops.paged_attn(kv, q, first, kl, window=window, return_lse=True)
+        assert ops.device_error() == 0
+        want, l, tol, ltol = ref.attend(q.double(), k, v, D ** -0.5, True, window)
+        ref.assert_within(out, want, tol, "out")
+        ref.assert_within(lse, l, ltol, "lse")
+    table[0, -1] = -1
+    out = ops.paged_attn(kv, q, first, kl, window=100)
+    assert ops.device_error() == 0x4 and torch.isnan(out).all()
+    Batch([1, 40], [9000, 300], 8, 1, 128, 64, fmt).check()
