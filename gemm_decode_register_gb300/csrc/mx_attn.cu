@@ -11,16 +11,18 @@
 // pages that its copies cannot tile, scales of zero or less).  Bound by its loads:
 // every query head reads the cache again, and by single keys.  64 heads on 8 x
 // 128 bf16, pages of 48 against pages of 64 on the tensor cores: one token on 16
-// keys 10.0 us, 8.6; 16 tokens on 2048 567 us, 33; a prompt of 512 on 1024
-// 3138 us, 23.
+// keys 10.3 us, 8.5; 16 tokens on 2048 559 us, 33; a prompt of 512 on 1024
+// 3168 us, 23.  The weights stay fp32.
 #include "mx_attn.cuh"
 
 namespace mx {
 
 constexpr int DIRECT_WARPS = 4;
 
+// (eight blocks per SM: the second pass's registers would leave seven, 3464 us for the
+// prompt above)
 template <int KVF>
-__global__ void __launch_bounds__(DIRECT_WARPS * 32) attn_direct_kernel(AttnArgs a)
+__global__ void __launch_bounds__(DIRECT_WARPS * 32, 8) attn_direct_kernel(AttnArgs a)
 {
     __shared__ float q[MAX_D];
     __shared__ float part_m[DIRECT_WARPS], part_l[DIRECT_WARPS], part_o[DIRECT_WARPS][MAX_D];
@@ -65,17 +67,21 @@ __global__ void __launch_bounds__(DIRECT_WARPS * 32) attn_direct_kernel(AttnArgs
         f[w] = exp2f(part_m[w] - base);
         l = fmaf(part_l[w], f[w], l);
     }
-    float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const bool bad = missing != 0;
-    // Values near the type's largest can overflow sums that are divided only at the
-    // end: a second pass with the weights divided first, in the rare case that one is not finite.
+    if (bad && threadIdx.x == 0) set_device_error(a.err, DEVERR_BAD_PAGE);
+    const size_t row = (size_t)t * a.Hq + h;
     float check = 0.0f;
     for (int d = threadIdx.x; d < a.kv.D; d += blockDim.x) {
         float o = 0.0f;
 #pragma unroll
         for (int w = 0; w < DIRECT_WARPS; ++w) o = fmaf(part_o[w][d], f[w], o);
         check += o * 0.0f;
+        o = bad ? __uint_as_float(0x7FC00000u) : o * inv;
+        a.out[row * a.kv.D + d] = (uint16_t)(f32x2_to_bf16x2(o, 0.0f) & 0xFFFFu);
     }
+    // Values near the type's largest can overflow sums that are divided only at the
+    // end: a second pass with the weights divided first, in the rare case that one is not finite.
     if (__syncthreads_or(!bad && inv == inv && check != 0.0f)) {
         RowState again;
         again.m = base;
@@ -84,18 +90,12 @@ __global__ void __launch_bounds__(DIRECT_WARPS * 32) attn_direct_kernel(AttnArgs
 #pragma unroll
         for (int i = 0; i < MAX_D / 32; ++i) part_o[warp][2 * lane + 64 * (i / 2) + i % 2] = again.o[i];
         __syncthreads();
+        for (int d = threadIdx.x; d < a.kv.D; d += blockDim.x) {
+            float o = 0.0f;
 #pragma unroll
-        for (int w = 0; w < DIRECT_WARPS; ++w) f[w] = 1.0f;
-        inv = 1.0f;
-    }
-    if (bad && threadIdx.x == 0) set_device_error(a.err, DEVERR_BAD_PAGE);
-    const size_t row = (size_t)t * a.Hq + h;
-    for (int d = threadIdx.x; d < a.kv.D; d += blockDim.x) {
-        float o = 0.0f;
-#pragma unroll
-        for (int w = 0; w < DIRECT_WARPS; ++w) o = fmaf(part_o[w][d], f[w], o);
-        o = bad ? __uint_as_float(0x7FC00000u) : o * inv;
-        a.out[row * a.kv.D + d] = (uint16_t)(f32x2_to_bf16x2(o, 0.0f) & 0xFFFFu);
+            for (int w = 0; w < DIRECT_WARPS; ++w) o += part_o[w][d];
+            a.out[row * a.kv.D + d] = (uint16_t)(f32x2_to_bf16x2(o, 0.0f) & 0xFFFFu);
+        }
     }
     if (a.lse && threadIdx.x == 0)
         a.lse[row] = bad ? __uint_as_float(0x7FC00000u) : (base + log2f(l)) * 0.6931471805599453f;
