@@ -32,13 +32,14 @@
 // P is rounded to bf16 because the tensor cores take their operands so: each
 // weight is off by up to 2^-8 of itself, as the values of a bf16 cache are already, and
 // the sum that divides them is of the unrounded weights.  64 heads on 8 of 128:
-//   prompt of 4096 on 8192     558 us  1.47 PFLOP/s, 77 % of the measured rate
-//   64 tokens on 0.5-8 K       178 us  6.4 TB/s, 96 % of the measured copy
-//   16 x 2-6 tokens on 1-16 K  103 us  5.9 TB/s
+//   prompt of 4096 on 8192     590 us  1.40 PFLOP/s, 73 % of the measured rate
+//                                      (581 to 597; 548 where few calls run)
+//   64 tokens on 0.5-8 K       181 us  6.3 TB/s, 95 % of the measured copy
+//   16 x 2-6 tokens on 1-16 K  105 us  5.8 TB/s
 //   one token on 131 keys        9 us  a chain of latencies
-//   MXFP8, 5 tokens on 24-66 K 204 us  the decode to bf16
+//   MXFP8, 5 tokens on 24-66 K 211 us  the decode to bf16
 // A prompt is bound by the softmax between two MMAs of a group (tensor cores
-// busy 52 % of the time, as the MMAs' own rate goes), single tokens by HBM.
+// busy 54 % of the time, as the MMAs' own rate goes), single tokens by HBM.
 //
 //   warps 0-3, 4-7  softmax groups and epilogue
 //   warp 9          MMA issuer
@@ -63,11 +64,11 @@ constexpr int AT_KEYS = 128;  // keys of a tile
 // What an item costs beside its keys, and more than its tiles' rounding: its
 // queries, epilogue and the cuts (4, 2, 6 tiles, 64 heads on 8 x 128 bf16, us:
 // 16 x 1-200 tokens on 0.1-4 K 126, 168, 127; 64 tokens on 50-2000 62, 72, 62,
-// in MXFP8 87, 90, 90).
+// in MXFP8 87, 90, 90; 124, 62 and 89 now).
 constexpr int AT_SPLIT_KEYS = 4 * AT_KEYS;
 // Up to so many tokens' queries are copied one by one, of more the whole row tile
-// (8 sequences on 1024: 2 tokens each 21.2 us, 22.0 as a tile; 8 tokens each
-// 28.4 as a tile, 30.5 one by one).
+// (32 sequences on 1024: 2 tokens each 35.0 us, 34.9 as a tile, but a call of so few
+// tokens need not encode the tile's copy; 8 tokens each 35.9 as a tile, 36.8 one by one).
 constexpr int AT_Q_COPIES = 4;
 // Whether an item of n tokens takes whole row tiles of queries, of s1 tokens each:
 // always where it needs two of them, which is from two tokens on in wide groups.  The

@@ -10,7 +10,7 @@
 // Both kernels move each element once and are bound by HBM for prompts, by
 // the launch and the chain of dependent loads (sequence, length, page, table
 // row) for single tokens: 4 tokens x 72 heads x 128 turn in 2.4 us, and are
-// appended in 2.5 us.
+// appended in 2.4 us.
 #include "mx_attn.cuh"
 
 namespace mx {
@@ -424,8 +424,8 @@ constexpr int APPEND_HEADS = 3;  // heads a thread takes at a time
 // four or five loads; with MANY each warp searches for one of the block's next
 // tokens, so the chain is gone through once for as many.
 // Bound by HBM: 4096 x 80 heads x 128 bf16 into MXFP8 33.2 us (73 % of a plain copy's
-// rate; 37.2 with a block for each token), 8192 tokens 61.5 us (78 %; 68.4),
-// fp32 rows 80.6 us (92.6).  Up to as many tokens as blocks are resident the loop only
+// rate; 37.2 with a block for each token), 8192 tokens 61.5 us (79 %; 68.4), of
+// fp32 rows 80.7 us (91 %; 92.6).  Up to as many tokens as blocks are resident the loop only
 // costs (one token 2.8 us, 3.2 with it).
 template <typename T, int KVF, bool INTER, bool MANY>
 __global__ void __launch_bounds__(APPEND_THREADS, append_resident<T>()) kv_append_kernel(const T *__restrict__ rows, AppendArgs a)

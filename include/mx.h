@@ -360,8 +360,9 @@ int mx_kv_append(const mx_paged_kv *kv, const void *rows, int dtype, int64_t row
  * sees no key gets zeros (and lse = its sink, or -infinity).  Cache places
  * that a row may not see have no influence on it, whatever they hold.
  * q bf16, strides in elements, last dimension contiguous; out bf16
- * [T][Hq][D].  Scores, statistics and sums are fp32; the weights are rounded to
- * bf16 for the product with v.
+ * [T][Hq][D].  Scores, statistics and sums are fp32.  On the tensor cores (D 64 or
+ * 128, pages of 16, 32, 64 or a multiple of 128 tokens, scale > 0, packed scale rows)
+ * the weights are rounded to bf16 for the product with v; otherwise they stay fp32.
  * workspace: caller-owned device memory of at least
  * mx_paged_attn_workspace_size(T, B, Hq, kv->Hkv, kv->D) bytes, 256-byte
  * aligned; overwritten, so calls sharing one must not overlap.  Null (with
