@@ -1,0 +1,738 @@
+// mx_pages.cu -- a pool of cache pages kept on the device: sequences forked,
+// grown, cut and freed in one step (remap), the pool made dense (compact),
+// and the pages' copies that come of either, sm_103a.
+//
+// Bookkeeping (bound: latency).  Tables of a few thousand to a million
+// entries, a chain of dependent phases (tally the pages' users, decide, hand
+// out pages, collect the freed ones): one launch of one cluster, whose
+// hardware barrier between phases costs a fraction of a launch, instead of a
+// launch per phase.  Everything a phase leaves to the next lies in L2.  The
+// tallies are integer atomics and all orders (pages handed out, pages freed,
+// copies) follow slot and page numbers, so results do not depend on timing.
+// A slot whose pages keep one user needs no tally: only sequences with other
+// than one child touch their pages' counts.
+//
+// These kernels write lengths and tables, which other kernels of the library
+// read before they wait for their predecessor; so they do not let their
+// dependents start early.
+//
+// Copies (bound: HBM): an item is some heads of one page's half in one layer;
+// blocks walk the items, 16-byte vectors, four in flight per thread.
+#include "mx_common.cuh"
+#include "mx_serve.h"
+#include "mx_tc.cuh"
+
+namespace mx {
+
+constexpr int POOL_THREADS = 1024;
+constexpr int POOL_WARPS = POOL_THREADS / 32;
+constexpr int POOL_CLUSTER = 8;  // CTAs of a cluster, the portable most
+constexpr int RUN = 4;           // entries per lane of a warp's task: 128 of one table row
+enum : int { DEVERR_NO_PAGE = MX_DEVERR_NO_PAGE, DEVERR_BAD_SLOT = MX_DEVERR_BAD_SLOT };
+
+// A page's tallies, zero between calls: users gained (or lost) in this step
+// that do not write the page, and the first slot that does, counted from the
+// last (slot s of S: S - s).  Compaction: entries, new place + 1.
+struct __align__(8) PageTally {
+    int users, writer;
+};
+
+// The pool's own memory (mx_page_pool.work).
+struct PoolWork {
+    PageTally *tally;   // [P]
+    uint32_t *freed;    // [P / 32] bits, zero between calls
+    int2 *plan;         // [POOL_MAX_SLOTS] a new slot's first page to be handed out, its copy's number + 1 (0: none)
+    int *word;          // faults of the tally [0] and of the decision [3] (zero between calls), [1] pages handed out, [2] copies
+    int *part;          // [2 * POOL_CLUSTER] counts of each CTA's range of pages
+};
+
+static size_t words_of(int P) { return ((size_t)P + 31) / 32; }
+
+size_t pool_work_bytes(int P)
+{
+    return ((size_t)P * 8 + words_of(P) * 4 + (size_t)POOL_MAX_SLOTS * 8 + 16 + 8 * POOL_CLUSTER + 16 + 255) / 256 * 256;
+}
+
+static PoolWork pool_work(const mx_page_pool &p)
+{
+    PoolWork w;
+    char *m = static_cast<char *>(p.work);
+    w.tally = reinterpret_cast<PageTally *>(m);
+    m += (size_t)p.num_pages * 8;
+    w.plan = reinterpret_cast<int2 *>(m);
+    m += (size_t)POOL_MAX_SLOTS * 8;
+    w.word = reinterpret_cast<int *>(m);
+    w.part = w.word + 4;
+    w.freed = reinterpret_cast<uint32_t *>(w.part + 2 * POOL_CLUSTER);
+    return w;
+}
+
+__device__ __forceinline__ uint32_t cluster_nctarank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// Everything before it is visible to the whole cluster after it.
+__device__ __forceinline__ void cluster_phase()
+{
+    __threadfence();
+    cluster_sync_all();
+}
+
+__device__ __forceinline__ PageTally tally_at(const PageTally *t, int page)
+{
+    const int2 v = __ldcg(reinterpret_cast<const int2 *>(t + page));
+    return PageTally{v.x, v.y};
+}
+
+__device__ __forceinline__ int pages_of(long long tokens, int page_size)
+{
+    return tokens <= 0 ? 0 : (int)((tokens + page_size - 1) / page_size);
+}
+
+// Largest of the block's values.
+__device__ __forceinline__ int block_max(int v, int *scratch)
+{
+    v = __reduce_max_sync(0xFFFFFFFFu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return __reduce_max_sync(0xFFFFFFFFu, scratch[threadIdx.x & 31]);
+}
+
+// Sum of the values of the threads before this one, and of all.
+__device__ __forceinline__ unsigned long long block_prefix(unsigned long long v, unsigned long long *scratch,
+                                                           unsigned long long &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    unsigned long long w = scratch[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+        if (lane >= o) w += y;
+    }
+    total = __shfl_sync(0xFFFFFFFFu, w, 31);
+    const unsigned long long before = __shfl_sync(0xFFFFFFFFu, w, warp > 0 ? warp - 1 : 0);
+    return x - v + (warp > 0 ? before : 0ull);
+}
+
+// ------------------------------------------------------------ remap
+
+struct RemapArgs {
+    RemapCall c;
+    PoolWork w;
+    int *err;
+};
+
+// What becomes of new slot s.
+struct NewSlot {
+    int parent, len, kept;  // parent's length; tokens taken from it
+    long long tokens;       // the slot's length
+    bool bad;
+};
+__device__ __forceinline__ NewSlot new_slot(const RemapCall &c, int s)
+{
+    NewSlot n;
+    n.parent = __ldcg(c.parent + s);
+    n.bad = n.parent >= c.S_in;
+    if (n.bad) n.parent = -1;
+    n.len = n.parent < 0 ? 0 : max(__ldcg(c.kv_len_in + n.parent), 0);
+    n.kept = c.keep ? min(n.len, max(__ldcg(c.keep + s), 0)) : n.len;
+    const int add = c.add ? max(__ldcg(c.add + s), 0) : n.parent < 0 ? 0 : c.add_all;
+    n.tokens = (long long)n.kept + add;
+    return n;
+}
+
+constexpr int CUT_CHILD = 1 << 16;  // children of a sequence: that keep all of it, and (upper half) a part
+
+__global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_constant__ RemapArgs a)
+{
+    const RemapCall &c = a.c;
+    const PoolWork &w = a.w;
+    extern __shared__ int children[];  // [S_in]
+    __shared__ int smax[32];
+    __shared__ unsigned long long scan[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = (int)cluster_ctarank(), ctas = (int)cluster_nctarank();
+    const int gw = warp * ctas + rank, nw = POOL_WARPS * ctas;
+    const int ps = c.page_size, P = c.pool.num_pages;
+    pdl_wait();
+
+    // ---- children of each sequence (every CTA for itself), longest rows
+    for (int p = threadIdx.x; p < c.S_in; p += POOL_THREADS) children[p] = 0;
+    __syncthreads();
+    int fault = 0, rows_in = 0, rows_out = 0;
+    for (int p = threadIdx.x; p < c.S_in; p += POOL_THREADS) {
+        const int n = pages_of(__ldcg(c.kv_len_in + p), ps);
+        if (n > c.in_pages) fault |= DEVERR_BAD_PAGE;
+        rows_in = max(rows_in, min(n, c.in_pages));
+    }
+    for (int s = threadIdx.x; s < c.S_out; s += POOL_THREADS) {
+        const NewSlot n = new_slot(c, s);
+        if (n.bad) fault |= DEVERR_BAD_SLOT;
+        if (n.tokens > (long long)c.out_pages * ps || n.tokens > 0x7FFFFFFFll) fault |= DEVERR_BAD_PAGE;
+        else rows_out = max(rows_out, pages_of(n.tokens, ps));
+        if (n.parent >= 0) atomicAdd(children + n.parent, n.kept == n.len ? 1 : CUT_CHILD);
+    }
+    rows_in = block_max(rows_in, smax);
+    rows_out = block_max(rows_out, smax);
+    const int chunks_in = (rows_in + 32 * RUN - 1) / (32 * RUN), chunks_out = (rows_out + 32 * RUN - 1) / (32 * RUN);
+
+    // f(sequence, its children, entry, page) for the old tables' entries of this warp's tasks
+    auto old_entries = [&](auto f) {
+        for (int t = gw; t < c.S_in * chunks_in; t += nw) {
+            const int p = t % c.S_in, j0 = t / c.S_in * (32 * RUN);
+            const int len = __ldcg(c.kv_len_in + p);
+            const int n = min(pages_of(len, ps), c.in_pages);
+            if (j0 >= n) continue;
+            const int32_t *row = c.table_in + (long long)p * c.in_stride;
+            int page[RUN];
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                const int j = j0 + 32 * i + lane;
+                page[i] = j < n ? __ldcg(row + j) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                const int j = j0 + 32 * i + lane;
+                // users that the step leaves this entry's page through it: the
+                // children that keep the whole sequence, of its full pages (its
+                // partial one is counted by each child)
+                if (j < n) f(p, children[p], page[i], (j < len / ps ? children[p] % CUT_CHILD : 0) - 1);
+            }
+        }
+    };
+
+    // ---- tally
+    old_entries([&](int, int, int page, int d) {
+        if ((unsigned)page >= (unsigned)P) fault |= DEVERR_BAD_PAGE;
+        else if (d != 0) atomicAdd(&w.tally[page].users, d);
+    });
+    for (int t = gw; t < c.S_out * max(chunks_in, 1); t += nw) {
+        const int s = t % c.S_out, j0 = t / c.S_out * (32 * RUN);
+        const NewSlot n = new_slot(c, s);
+        if (n.parent < 0) continue;
+        const int32_t *row = c.table_in + (long long)n.parent * c.in_stride;
+        const int full = min(n.kept / ps, c.in_pages);
+        if (n.kept < n.len)
+            for (int j = j0 + lane; j < min(full, j0 + 32 * RUN); j += 32) {
+                const int page = __ldcg(row + j);
+                if ((unsigned)page < (unsigned)P) atomicAdd(&w.tally[page].users, 1);
+            }
+        if (j0 == 0 && lane == 0 && n.kept % ps != 0 && full < c.in_pages) {
+            const int page = __ldcg(row + full);
+            if ((unsigned)page < (unsigned)P) {
+                if (n.tokens > n.kept) atomicMax(&w.tally[page].writer, c.S_out - s);
+                else atomicAdd(&w.tally[page].users, 1);
+            }
+        }
+    }
+    if (fault) atomicOr(w.word, fault);
+    cluster_phase();
+
+    // ---- pages each slot is handed out, in slot order (CTA 0); pages left
+    // without a user.  Skipped where a fault is known: lengths may not fit
+    // the tables.
+    if (__ldcg(w.word) == 0) {
+        if (rank == 0) {
+            const int per = (c.S_out + POOL_THREADS - 1) / POOL_THREADS;
+            const int s0 = (int)threadIdx.x * per, s1 = min(s0 + per, c.S_out);
+            constexpr unsigned long long COPY = 1ull << 40;  // pages below, copies above
+            unsigned long long mine = 0;
+            auto need = [&](int s) {
+                const NewSlot n = new_slot(c, s);
+                unsigned long long v = (unsigned)(pages_of(n.tokens, ps) - pages_of(n.kept, ps));
+                if (n.kept % ps != 0 && n.tokens > n.kept) {
+                    const int page = __ldcg(c.table_in + (long long)n.parent * c.in_stride + n.kept / ps);
+                    const PageTally t = tally_at(w.tally, page);
+                    // a page that only growing slots use stays with the first
+                    if (!(__ldcg(c.pool.refs + page) + t.users == 0 && t.writer == c.S_out - s)) v += COPY + 1;
+                }
+                return v;
+            };
+            for (int s = s0; s < s1; ++s) mine += need(s);
+            unsigned long long total;
+            unsigned long long at = block_prefix(mine, scan, total);
+            for (int s = s0; s < s1; ++s) {
+                const unsigned long long v = need(s);
+                w.plan[s] = make_int2((int)(at & (COPY - 1)), v >= COPY ? (int)(at / COPY) + 1 : 0);
+                at += v;
+            }
+            if (threadIdx.x == 0) {
+                const int count = __ldcg(c.pool.count);
+                const unsigned long long n = total & (COPY - 1);
+                if (count < 0 || count > P) atomicOr(w.word + 3, (int)DEVERR_BAD_PAGE);
+                else if (n > (unsigned long long)count) atomicOr(w.word + 3, (int)DEVERR_NO_PAGE);
+                w.word[1] = (int)n;
+                w.word[2] = (int)(total / COPY);
+            }
+        }
+        old_entries([&](int, int, int page, int d) {
+            if (d >= 0) return;
+            const PageTally t = tally_at(w.tally, page);
+            const int left = __ldcg(c.pool.refs + page) + t.users;
+            if (left < 0) atomicOr(w.word + 3, (int)DEVERR_BAD_PAGE);  // fewer references than entries
+            if (left == 0 && t.writer == 0) atomicOr(w.freed + (page >> 5), 1u << (page & 31));
+        });
+    }
+    cluster_phase();
+
+    // ---- all or nothing
+    fault = __ldcg(w.word) | __ldcg(w.word + 3);
+    if (fault) {
+        old_entries([&](int, int, int page, int) {
+            if ((unsigned)page >= (unsigned)P) return;
+            w.tally[page] = PageTally{0, 0};
+            w.freed[page >> 5] = 0u;
+        });
+        if (rank == 0) {
+            for (int s = threadIdx.x; s < c.S_out; s += POOL_THREADS) c.kv_len_out[s] = -1;
+            if (threadIdx.x == 0) {
+                reinterpret_cast<int4 *>(c.copies)[0] = make_int4(0, 0, 0, 0);
+                set_device_error(a.err, fault);
+            }
+        }
+        cluster_phase();
+        if (rank == 0 && threadIdx.x == 0) w.word[0] = w.word[3] = 0;
+        return;
+    }
+    const int count = __ldcg(c.pool.count), handed = __ldcg(w.word + 1);
+    old_entries([&](int, int kids, int page, int d) {
+        if (d == 0 && kids < CUT_CHILD) return;
+        // whoever comes first takes the tally
+        const unsigned long long v = atomicExch(reinterpret_cast<unsigned long long *>(w.tally + page), 0ull);
+        if (v == 0ull) return;
+        const int left = __ldcg(c.pool.refs + page) + (int)(uint32_t)v;
+        c.pool.refs[page] = left == 0 && (v >> 32) != 0 ? 1 : left;
+    });
+    for (int t = gw; t < c.S_out * max(chunks_out, 1); t += nw) {
+        const int s = t % c.S_out, j0 = t / c.S_out * (32 * RUN);
+        const NewSlot n = new_slot(c, s);
+        const int2 plan = __ldcg(w.plan + s);
+        const int end = pages_of(n.tokens, ps), start = pages_of(n.kept, ps) - (plan.y != 0);
+        const int32_t *from = c.table_in + (long long)max(n.parent, 0) * c.in_stride;
+        int32_t *to = c.table_out + (long long)s * c.out_stride;
+        if (j0 < end || j0 == 0) {
+            int page[RUN];
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                const int j = j0 + 32 * i + lane;
+                if (j < start) page[i] = __ldcg(from + j);
+                else if (j < end) page[i] = __ldcg(c.pool.free_pages + (count - 1 - plan.x - (j - start)));
+            }
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                const int j = j0 + 32 * i + lane;
+                if (j >= end) continue;
+                to[j] = page[i];
+                if (j < start) continue;
+                if ((unsigned)page[i] < (unsigned)P) c.pool.refs[page[i]] = 1;
+                else set_device_error(a.err, DEVERR_BAD_PAGE);
+                if (j == start && plan.y != 0)
+                    reinterpret_cast<int4 *>(c.copies)[plan.y] = make_int4(__ldcg(from + j), page[i], n.kept % ps, 0);
+            }
+            if (j0 == 0 && lane == 0) c.kv_len_out[s] = (int)n.tokens;
+        }
+    }
+    cluster_phase();
+
+    // ---- the freed pages go on the stack, in page order (CTA 0)
+    if (rank != 0) return;
+    const int words = (P + 31) / 32;
+    int top = count - handed;
+    for (int i0 = 0; i0 < words; i0 += POOL_THREADS) {
+        const int i = i0 + (int)threadIdx.x;
+        uint32_t bits = i < words ? __ldcg(w.freed + i) : 0u;
+        if (__syncthreads_or(bits != 0u) == 0) continue;
+        unsigned long long total;
+        int at = top + (int)block_prefix((unsigned)__popc(bits), scan, total);
+        if (bits) w.freed[i] = 0u;
+        for (; bits; bits &= bits - 1) c.pool.free_pages[at++] = 32 * i + __ffs((int)bits) - 1;
+        top += (int)total;
+    }
+    if (threadIdx.x == 0) {
+        *c.pool.count = top;
+        reinterpret_cast<int4 *>(c.copies)[0] = make_int4(__ldcg(w.word + 2), 0, 0, 0);
+    }
+}
+
+// ------------------------------------------------------------ compact
+
+struct CompactArgs {
+    mx_page_pool pool;
+    PoolWork w;
+    int page_size;
+    int32_t *table;
+    int stride, pages, S;
+    const int32_t *kv_len;
+    int32_t *copies;
+    int *err;
+};
+
+// U pages are in use.  The i-th free page below U takes the place of the i-th
+// page in use from U on whose references are all entries of this table.
+__global__ void __launch_bounds__(POOL_THREADS, 1) kv_compact_kernel(const __grid_constant__ CompactArgs a)
+{
+    const PoolWork &w = a.w;
+    __shared__ int smax[32];
+    __shared__ unsigned long long scan[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = (int)cluster_ctarank(), ctas = (int)cluster_nctarank();
+    const int gw = warp * ctas + rank, nw = POOL_WARPS * ctas;
+    const int ps = a.page_size, P = a.pool.num_pages;
+    // this warp's range of pages
+    const int span = ((P + nw - 1) / nw + 31) / 32 * 32;
+    const int lo = (int)min((long long)(rank * POOL_WARPS + warp) * span, (long long)P);
+    const int hi = (int)min((long long)lo + span, (long long)P);
+    pdl_wait();
+
+    int rows = 0, fault = 0;
+    for (int s = threadIdx.x; s < a.S; s += POOL_THREADS) {
+        const int n = pages_of(__ldcg(a.kv_len + s), ps);
+        if (n > a.pages) fault |= DEVERR_BAD_PAGE;
+        rows = max(rows, min(n, a.pages));
+    }
+    rows = block_max(rows, smax);
+    const int chunks = (rows + 32 * RUN - 1) / (32 * RUN);
+    auto entries = [&](auto f) {
+        for (int t = gw; t < a.S * chunks; t += nw) {
+            const int s = t % a.S, j0 = t / a.S * (32 * RUN);
+            const int n = min(pages_of(__ldcg(a.kv_len + s), ps), a.pages);
+            int32_t *row = a.table + (long long)s * a.stride;
+            int page[RUN];
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                const int j = j0 + 32 * i + lane;
+                page[i] = j < n ? __ldcg(row + j) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < RUN; ++i)
+                if (j0 + 32 * i + lane < n) f(row + j0 + 32 * i + lane, page[i]);
+        }
+    };
+    // Sum over the pages of this CTA before this warp's range and over all the
+    // CTA's, of up to two counts (the second 2^32 up).
+    auto range_sum = [&](unsigned long long mine, unsigned long long &total) {
+        return block_prefix(lane == 0 ? mine : 0ull, scan, total);
+    };
+    // the CTAs' totals: of those before this one, and of all
+    auto totals = [&](int slot, int &all) {
+        int before = 0;
+        all = 0;
+        for (int r = 0; r < ctas; ++r) {
+            const int v = __ldcg(w.part + slot * POOL_CLUSTER + r);
+            if (r < rank) before += v;
+            all += v;
+        }
+        return before;
+    };
+
+    // ---- entries of each page; pages in use
+    entries([&](int32_t *, int page) {
+        if ((unsigned)page >= (unsigned)P) fault |= DEVERR_BAD_PAGE;
+        else atomicAdd(&w.tally[page].users, 1);
+    });
+    unsigned used = 0;
+    for (int p = lo + lane; p < hi; p += 32) used += __ldcg(a.pool.refs + p) > 0;
+    used = __reduce_add_sync(0xFFFFFFFFu, used);
+    unsigned long long total;
+    range_sum(used, total);
+    if (threadIdx.x == 0) w.part[rank] = (int)total;
+    if (fault) atomicOr(w.word, fault);
+    cluster_phase();
+    fault = __ldcg(w.word);
+    if (fault) {
+        for (int p = lo + lane; p < hi; p += 32) w.tally[p] = PageTally{0, 0};
+        if (rank == 0 && threadIdx.x == 0) {
+            reinterpret_cast<int4 *>(a.copies)[0] = make_int4(0, 0, 0, 0);
+            set_device_error(a.err, fault);
+        }
+        cluster_phase();
+        if (rank == 0 && threadIdx.x == 0) w.word[0] = 0;
+        return;
+    }
+    int U;
+    totals(0, U);
+    cluster_phase();  // (the counts' places are used again)
+
+    // ---- free places below U, pages to move from U on
+    auto kind = [&](int p) {  // 1: a free place, 2: a page to move
+        const int r = __ldcg(a.pool.refs + p);
+        if (p < U) return r == 0 ? 1 : 0;
+        return r > 0 && tally_at(w.tally, p).users == r ? 2 : 0;
+    };
+    unsigned holes = 0, movers = 0;
+    for (int p0 = lo; p0 < hi; p0 += 32) {
+        const int k = p0 + lane < hi ? kind(p0 + lane) : 0;
+        holes += __popc(__ballot_sync(0xFFFFFFFFu, k == 1));
+        movers += __popc(__ballot_sync(0xFFFFFFFFu, k == 2));
+    }
+    const unsigned long long at = __shfl_sync(0xFFFFFFFFu, range_sum(holes | ((unsigned long long)movers << 32), total), 0);
+    if (threadIdx.x == 0) {
+        w.part[rank] = (int)(uint32_t)total;
+        w.part[POOL_CLUSTER + rank] = (int)(total >> 32);
+    }
+    cluster_phase();
+    int all_holes, all_movers;
+    int hole = totals(0, all_holes) + (int)(uint32_t)at, mover = totals(1, all_movers) + (int)(at >> 32);
+    const int n = min(all_holes, all_movers);
+    for (int p0 = lo; p0 < hi; p0 += 32) {
+        const int k = p0 + lane < hi ? kind(p0 + lane) : 0;
+        const unsigned h = __ballot_sync(0xFFFFFFFFu, k == 1), m = __ballot_sync(0xFFFFFFFFu, k == 2);
+        const unsigned below = (1u << lane) - 1u;
+        const int i = k == 1 ? hole + __popc(h & below) : mover + __popc(m & below);
+        if (k != 0 && i < n) a.copies[4 * (size_t)(1 + i) + (k == 1 ? 1 : 0)] = p0 + lane;
+        hole += __popc(h);
+        mover += __popc(m);
+    }
+    cluster_phase();
+
+    // ---- the moves
+    for (int i = gw * 32 + lane; i < n; i += nw * 32) {
+        int4 *row = reinterpret_cast<int4 *>(a.copies) + 1 + i;
+        const int2 v = __ldcg(reinterpret_cast<const int2 *>(row));
+        *row = make_int4(v.x, v.y, ps, 0);
+        w.tally[v.x].writer = v.y + 1;
+        a.pool.refs[v.y] = __ldcg(a.pool.refs + v.x);
+        a.pool.refs[v.x] = 0;
+    }
+    cluster_phase();
+    entries([&](int32_t *e, int page) {
+        const int to = tally_at(w.tally, page).writer;
+        if (to > 0) *e = to - 1;
+    });
+    unsigned empty = 0;
+    for (int p = lo + lane; p < hi; p += 32) empty += __ldcg(a.pool.refs + p) == 0;
+    empty = __reduce_add_sync(0xFFFFFFFFu, empty);
+    const int mine = (int)__shfl_sync(0xFFFFFFFFu, range_sum(empty, total), 0);
+    if (threadIdx.x == 0) w.part[rank] = (int)total;
+    cluster_phase();
+
+    // ---- the stack: the lowest page is taken first
+    int all;
+    int below = totals(0, all) + mine;
+    for (int p0 = lo; p0 < hi; p0 += 32) {
+        const int p = p0 + lane;
+        const bool e = p < hi && __ldcg(a.pool.refs + p) == 0;
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, e);
+        if (e) a.pool.free_pages[all - 1 - (below + __popc(m & ((1u << lane) - 1u)))] = p;
+        if (p < hi) w.tally[p] = PageTally{0, 0};
+        below += __popc(m);
+    }
+    if (rank == 0 && threadIdx.x == 0) {
+        *a.pool.count = all;
+        reinterpret_cast<int4 *>(a.copies)[0] = make_int4(n, 0, 0, 0);
+    }
+}
+
+// ------------------------------------------------------------ copies
+
+// What is copied of a page in one half of the cache: rows (head, token) of
+// `row` bytes, moved in units of V's size.
+struct CopyPart {
+    long long page_stride, head_stride, token_stride;  // bytes
+    int row;                                           // bytes
+    int unit;                                          // 16, 8, 4, 2 or 1
+};
+
+template <int LAYERS>
+struct CopyArgs {
+    uint8_t *data[LAYERS][2], *scales[LAYERS][2];
+    CopyPart d, s;  // s.row = 0: no scales
+    const int4 *copies;
+    int max_copies, layers, num_pages, page_size, heads, group;  // group: heads of an item
+    int *err;
+};
+
+template <typename V>
+__device__ __forceinline__ void copy_rows(const uint8_t *src, uint8_t *dst, const CopyPart &p, int heads, int tokens)
+{
+    // tokens that lie together make one row of each head
+    const bool together = p.token_stride == p.row;
+    const unsigned per_row = (unsigned)(p.row / (int)sizeof(V)) * (together ? (unsigned)tokens : 1u);
+    const unsigned rows = together ? 1u : (unsigned)tokens;  // of a head
+    const unsigned n = per_row * rows * (unsigned)heads;
+    constexpr int F = 4;
+    for (unsigned i0 = threadIdx.x; i0 < n; i0 += F * blockDim.x) {
+        V v[F];
+        long long at[F];
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const unsigned i = i0 + f * blockDim.x;
+            if (i >= n) break;
+            const unsigned r = i / per_row, col = i - r * per_row;
+            const unsigned h = r / rows, t = r - h * rows;
+            at[f] = (long long)h * p.head_stride + (long long)t * p.token_stride + (long long)col * (int)sizeof(V);
+            v[f] = __ldcg(reinterpret_cast<const V *>(src + at[f]));
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+            if (i0 + f * blockDim.x < n) *reinterpret_cast<V *>(dst + at[f]) = v[f];
+    }
+}
+
+__device__ __forceinline__ void copy_part(uint8_t *base, const CopyPart &p, int src, int dst, int head, int heads, int tokens)
+{
+    const uint8_t *s = base + src * p.page_stride + head * p.head_stride;
+    uint8_t *d = base + dst * p.page_stride + head * p.head_stride;
+    switch (p.unit) {
+    case 16: copy_rows<uint4>(s, d, p, heads, tokens); break;
+    case 8: copy_rows<uint2>(s, d, p, heads, tokens); break;
+    case 4: copy_rows<uint32_t>(s, d, p, heads, tokens); break;
+    case 2: copy_rows<uint16_t>(s, d, p, heads, tokens); break;
+    default: copy_rows<uint8_t>(s, d, p, heads, tokens); break;
+    }
+}
+
+constexpr int COPY_THREADS = 256;
+
+template <int LAYERS>
+__global__ void __launch_bounds__(COPY_THREADS) kv_copy_kernel(const __grid_constant__ CopyArgs<LAYERS> a)
+{
+    pdl_wait();
+    // (not before: what precedes may have written the tables that the next
+    // kernels read before they wait)
+    pdl_trigger();
+    const int n = min(max(__ldcg(&a.copies->x), 0), a.max_copies);
+    const int groups = (a.heads + a.group - 1) / a.group;
+    const long long items = (long long)n * a.layers * 2 * groups;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const int g = (int)(it % groups);
+        const long long r = it / groups;
+        const int half = (int)(r & 1), layer = (int)((r >> 1) % a.layers), i = (int)((r >> 1) / a.layers);
+        const int4 c = __ldcg(a.copies + 1 + i);
+        const int tokens = min(c.z, a.page_size);
+        if ((unsigned)c.x >= (unsigned)a.num_pages || (unsigned)c.y >= (unsigned)a.num_pages) {
+            if (threadIdx.x == 0) set_device_error(a.err, DEVERR_BAD_PAGE);
+            continue;
+        }
+        if (tokens <= 0 || c.x == c.y) continue;
+        const int head = g * a.group, heads = min(a.group, a.heads - head);
+        copy_part(a.data[layer][half], a.d, c.x, c.y, head, heads, tokens);
+        if (a.s.row > 0) copy_part(a.scales[layer][half], a.s, c.x, c.y, head, heads, tokens);
+    }
+}
+
+// ------------------------------------------------------------ host
+
+// One cluster: a single CTA where it can take every entry in a few tasks per
+// warp, else the portable most.
+template <typename Args>
+static cudaError_t run_cluster(cudaStream_t st, void (*kernel)(const Args), int ctas, size_t smem, const Args &a)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(POOL_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+static int pool_ctas(long long S, long long pages, long long P)
+{
+    return S * ((pages + 32 * RUN - 1) / (32 * RUN)) <= 2 * POOL_WARPS && P <= 64 * 1024 ? 1 : POOL_CLUSTER;
+}
+
+cudaError_t launch_kv_remap(const DeviceState &ds, cudaStream_t st, const RemapCall &c)
+{
+    RemapArgs a;
+    a.c = c;
+    a.w = pool_work(c.pool);
+    a.err = ds.err;
+    const int S = c.S_in > c.S_out ? c.S_in : c.S_out;
+    const int pages = c.in_pages > c.out_pages ? c.in_pages : c.out_pages;
+    return run_cluster(st, kv_remap_kernel, pool_ctas(S, pages, c.pool.num_pages), (size_t)c.S_in * 4, a);
+}
+
+cudaError_t launch_kv_compact(const DeviceState &ds, cudaStream_t st, const mx_page_pool &pool, int page_size,
+                              int32_t *table, int stride, int pages, const int32_t *kv_len, int S, int32_t *copies)
+{
+    CompactArgs a;
+    a.pool = pool;
+    a.w = pool_work(pool);
+    a.page_size = page_size;
+    a.table = table;
+    a.stride = stride;
+    a.pages = pages;
+    a.S = S;
+    a.kv_len = kv_len;
+    a.copies = copies;
+    a.err = ds.err;
+    return run_cluster(st, kv_compact_kernel, pool_ctas(S, pages, pool.num_pages), 0, a);
+}
+
+// Widest unit that every address of a part is a multiple of.
+static int copy_unit(long long bits)
+{
+    return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+}
+
+template <int LAYERS>
+static cudaError_t run_copy(const DeviceState &ds, cudaStream_t st, const mx_paged_kv *kv, int layers,
+                            const int32_t *copies, int max_copies)
+{
+    const bool mx8 = kv->kv_fmt == MX_KV_MXFP8;
+    const long long e = mx8 ? 1 : 2;
+    CopyArgs<LAYERS> a;
+    long long bits = 0;
+    for (int l = 0; l < layers; ++l) {
+        a.data[l][0] = static_cast<uint8_t *>(kv[l].k);
+        a.data[l][1] = static_cast<uint8_t *>(kv[l].v);
+        a.scales[l][0] = static_cast<uint8_t *>(kv[l].k_scales);
+        a.scales[l][1] = static_cast<uint8_t *>(kv[l].v_scales);
+        if (mx8)
+            for (int h = 0; h < 2; ++h) bits |= (long long)reinterpret_cast<uintptr_t>(a.scales[l][h]);
+    }
+    a.d.page_stride = kv->page_stride * e;
+    a.d.head_stride = kv->head_stride * e;
+    a.d.token_stride = kv->token_stride * e;
+    a.d.row = (int)(kv->D * e);
+    a.d.unit = 16;  // (the cache's base and strides are multiples of 16 bytes, a row is)
+    a.s.page_stride = kv->scale_page_stride;
+    a.s.head_stride = kv->scale_head_stride;
+    a.s.token_stride = kv->scale_token_stride;
+    a.s.row = mx8 ? kv->D / 32 : 0;
+    a.s.unit = copy_unit(bits | a.s.page_stride | a.s.head_stride | a.s.token_stride | a.s.row);
+    a.copies = reinterpret_cast<const int4 *>(copies);
+    a.max_copies = max_copies;
+    a.layers = layers;
+    a.num_pages = kv->num_pages;
+    a.page_size = kv->page_size;
+    a.heads = kv->Hkv;
+    // about 32 KB an item: two rounds of a block's loads
+    const long long head = (long long)kv->page_size * a.d.row;
+    a.group = (int)(head >= 32768 ? 1 : 32768 / head < kv->Hkv ? 32768 / head : kv->Hkv);
+    a.err = ds.err;
+    const long long items = (long long)max_copies * layers * 2 * ((kv->Hkv + a.group - 1) / a.group);
+    const long long most = 8ll * ds.num_sms;
+    return launch_k(kv_copy_kernel<LAYERS>, dim3((unsigned)(items < most ? items : most)), dim3(COPY_THREADS), 0, st, a);
+}
+
+cudaError_t launch_kv_copy_pages(const DeviceState &ds, cudaStream_t st, const mx_paged_kv *kv, int layers,
+                                 const int32_t *copies, int max_copies)
+{
+    if (layers <= 8) return run_copy<8>(ds, st, kv, layers, copies, max_copies);
+    return run_copy<COPY_MAX_LAYERS>(ds, st, kv, layers, copies, max_copies);
+}
+
+}  // namespace mx

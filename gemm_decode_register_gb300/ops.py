@@ -12,6 +12,7 @@ import math
 import os
 import re
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -68,6 +69,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
             "mx_rope": [P, P, I, P, P, I, I, I, I, I, L, L, L, L, I],
             "mx_kv_append": [P, P, I, L, P, P, P, I, I, P, I, I, I, I],
             "mx_paged_attn": [P, P, L, L, P, P, ctypes.c_float, I, I, P, P, P, I, I, I, P, Z],
+            "mx_beam_select": [P, I, L, P, P, L, I, I, I, I, I, P, P, P, P, P, P, P, Z],
+            "mx_kv_remap": [P, I, P, I, I, P, I, P, I, I, P, I, P, P, P, I, P],
+            "mx_kv_compact": [P, I, P, I, I, P, I, P],
+            "mx_kv_copy_pages": [P, I, P, I],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -75,7 +80,9 @@ def load(path: str | None = None) -> ctypes.CDLL:
             f.restype = I
         for name, args in {"mx_moe_qmm_workspace_size": [I, I, I, I],
                            "mx_moe_ffn_prefill_workspace_size": [I, I, I, I, I],
-                           "mx_paged_attn_workspace_size": [I, I, I, I, I]}.items():
+                           "mx_paged_attn_workspace_size": [I, I, I, I, I],
+                           "mx_beam_select_workspace_size": [I, I, I, I],
+                           "mx_page_pool_work_size": [I]}.items():
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = Z
@@ -595,6 +602,168 @@ def paged_attn(kv: PagedKV, q: torch.Tensor, q_start: torch.Tensor, kv_len: torc
                                                   ATTN_CAUSAL if causal else 0,
                                                   max(-1, min(window, 0x7FFFFFFF)), kp, op, ep, T, B, Hq, wp, wn))
     return (out, lse) if return_lse else out
+
+
+# ---- decode loops: beams, and the pages of their contexts
+
+
+class Beams(NamedTuple):
+    """beam_select's result: the k best continuations of each batch entry [B][k] (score fp32, parent and token
+    int32), and of those the first W that do not end [B][W]."""
+    score: torch.Tensor
+    parent: torch.Tensor
+    token: torch.Tensor
+    next_score: torch.Tensor
+    next_parent: torch.Tensor
+    next_token: torch.Tensor
+
+
+def beam_select_workspace(B: int, W: int, V: int, k: int, device="cuda") -> torch.Tensor:
+    return _workspace(load().mx_beam_select_workspace_size(B, W, V, k), None, device)
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None, eos: int = -1,
+                mask: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> Beams:
+    """The k (2 W by default) best continuations of each batch entry's beams: logits [B * W][V] (bf16 or fp32, the
+    last dimension contiguous), scores fp32 [B][W] (logarithms of the beams' probabilities; -inf: no beam), key = score
+    + log_softmax(logits).  Ordered by key, then beam, then logit, then the lower token.  parent is the row of
+    `logits`, so it serves kv_remap as it is.  Places without a candidate hold -inf, -1, 0.  eos: the token that ends
+    a beam; beams of that token are left out of next_*.  mask int32 [B * W][ceil(V / 32)]: bit v % 32 of word v // 32
+    allows token v; the probabilities are those among the allowed tokens."""
+    if logits.dtype not in _DTYPES:
+        raise ValueError(f"logits: expected bf16 or fp32, got {logits.dtype}")
+    xp = _cuda("logits", logits, logits.dtype, 2)
+    if scores.dim() != 2 or scores.numel() != logits.shape[0]:
+        raise ValueError("scores: expected [B][W] with a row of logits for each")
+    rows, V = logits.shape
+    B, W = shape = scores.shape
+    sp = _whole("scores", scores, torch.float32, shape)
+    if k is None:
+        k = 2 * W
+    mp, ms = None, 0
+    if mask is not None:
+        mp = _cuda("mask", mask, torch.int32, 2)
+        if mask.shape != (rows, (V + 31) // 32):
+            raise ValueError(f"mask: expected shape {(rows, (V + 31) // 32)}")
+        ms = mask.stride(0) if rows > 1 else mask.shape[1]
+    f = torch.empty((B * (k + W),), dtype=torch.float32, device=logits.device)
+    i = torch.empty((2, B * (k + W)), dtype=torch.int32, device=logits.device)
+    n = B * k
+    out = Beams(f[:n].view(B, k), i[0, :n].view(B, k), i[1, :n].view(B, k),
+                f[n:].view(B, W), i[0, n:].view(B, W), i[1, n:].view(B, W))
+    if rows > 0:
+        lib = load()
+        if workspace is None:
+            need = lib.mx_beam_select_workspace_size(B, W, V, k)
+            if need > WORKSPACE_SLOT_BYTES:
+                workspace = _workspace(need, None, logits.device)
+        wp, wn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
+        fp, ip, jp = f.data_ptr(), i.data_ptr(), i[1].data_ptr()
+        _stream()
+        _check("mx_beam_select", lib.mx_beam_select(
+            xp, _DTYPES[logits.dtype], logits.stride(0) if rows > 1 else V, sp, mp, ms, B, W, V, k, max(eos, -1),
+            fp, ip, jp, fp + 4 * n, ip + 4 * n, jp + 4 * n, wp, wn))
+    return out
+
+
+class _PagePool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("count", "refs", "free_pages", "work")] + [("num_pages", ctypes.c_int32)]
+
+
+class PagePool:
+    """Which of a cache's pages are in use, kept on the device (mx_page_pool): `count` int32 [1] free pages,
+    `refs` int32 [num_pages] references of each page (one for each table entry, and those of other holders),
+    `free_pages` int32 [num_pages] the stack of free pages.  All pages are free at first, page 0 is taken first.  The
+    three are views of `state` int32 [4 + 2 num_pages], which may be given (a pool as it was saved)."""
+
+    def __init__(self, num_pages: int, device="cuda", state: torch.Tensor | None = None):
+        if state is None:
+            state = torch.zeros(4 + 2 * num_pages, dtype=torch.int32, device=device)
+            state[0] = num_pages
+            state[4 + num_pages:] = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        sp = _whole("state", state, torch.int32, (4 + 2 * num_pages,))
+        size = load().mx_page_pool_work_size(num_pages)
+        if size == 0:
+            raise ValueError("sizes outside the library's limits")
+        self.work = torch.zeros(size, dtype=torch.uint8, device=state.device)
+        self.num_pages, self.state = num_pages, state
+        self.count, self.refs, self.free_pages = state[:1], state[4:4 + num_pages], state[4 + num_pages:]
+        c = _PagePool(sp, sp + 16, sp + 16 + 4 * num_pages, self.work.data_ptr(), num_pages)
+        self._c, self._ref = c, ctypes.byref(c)
+
+
+def _table_of(name: str, table: torch.Tensor) -> tuple[int, int, int, int]:
+    """Pointer, row stride, pages of a row and sequences of a block table."""
+    p = _cuda(name, table, torch.int32, 2)
+    S, n = table.shape
+    return p, n if S == 1 else table.stride(0), n, S
+
+
+def kv_remap(pool: PagePool, page_size: int, table: torch.Tensor, kv_len: torch.Tensor, parent: torch.Tensor,
+             table_out: torch.Tensor, add: int | torch.Tensor = 1, keep: torch.Tensor | None = None,
+             kv_len_out: torch.Tensor | None = None,
+             copies: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """One step of the sequences' pages: forks, growth, cuts and releases at once (mx_kv_remap).
+
+    New sequence s takes the first keep[s] tokens (int32 [S_out]; None: all) of sequence parent[s] (int32 [S_out], a
+    row of `table` int32 [S_in][pages] and `kv_len` int32 [S_in]; negative: none) and grows by add (int32 [S_out], or one
+    number for all sequences that have a parent).  `table_out` int32 [S_out][pages] receives its pages; sequences
+    that are no one's parent release theirs.  Pages are shared; a sequence that grows in the middle of a page
+    others hold too gets a page and a copy.  Returns the new lengths int32 [S_out] and the copies that
+    kv_copy_pages has to make before the cache is used.  Where the pool cannot supply the step, or the arguments do
+    not fit, nothing changes, the lengths are -1 and device_error() tells why."""
+    tp, ts, tn, S_in = _table_of("table", table)
+    op, os_, on, S_out = _table_of("table_out", table_out)
+    lp = _whole("kv_len", kv_len, torch.int32, (S_in,))
+    pp = _whole("parent", parent if parent.dim() == 1 else parent.reshape(-1), torch.int32, (S_out,))
+    kp = None if keep is None else _whole("keep", keep, torch.int32, (S_out,))
+    ap, each = (None, add) if isinstance(add, int) else (_whole("add", add, torch.int32, (S_out,)), 0)
+    if kv_len_out is None:
+        kv_len_out = torch.empty((S_out,), dtype=torch.int32, device=table.device)
+    if copies is None:
+        copies = torch.empty((1 + S_out, 4), dtype=torch.int32, device=table.device)
+    np_, cp = _whole("kv_len_out", kv_len_out, torch.int32, (S_out,)), _whole("copies", copies, torch.int32, (1 + S_out, 4))
+    _stream()
+    _check("mx_kv_remap", load().mx_kv_remap(pool._ref, page_size, tp, ts, tn, lp, S_in, op, os_, on, np_, S_out, pp, kp,
+                                             ap, each, cp))
+    return kv_len_out, copies
+
+
+def kv_compact(pool: PagePool, page_size: int, table: torch.Tensor, kv_len: torch.Tensor,
+               copies: torch.Tensor | None = None) -> torch.Tensor:
+    """Make the pool dense in place (mx_kv_compact): pages in use move to the lowest places, `table` follows.
+    Pages with holders besides this table stay.  Returns the copies [1 + num_pages // 2][4] that kv_copy_pages has to
+    make before the cache is used."""
+    tp, ts, tn, S = _table_of("table", table)
+    lp = _whole("kv_len", kv_len, torch.int32, (S,))
+    rows = 1 + pool.num_pages // 2
+    if copies is None:
+        copies = torch.empty((rows, 4), dtype=torch.int32, device=table.device)
+    cp = _whole("copies", copies, torch.int32, (rows, 4))
+    _stream()
+    _check("mx_kv_compact", load().mx_kv_compact(pool._ref, page_size, tp, ts, tn, lp, S, cp))
+    return copies
+
+
+class PagedKVLayers:
+    """The caches of several layers that share a pool (the same format, sizes and strides), as kv_copy_pages takes
+    them.  Keeps them alive."""
+
+    def __init__(self, layers: list[PagedKV]):
+        self.layers = list(layers)
+        self._c = (_PagedKV * len(self.layers))(*(kv._c for kv in self.layers))
+
+
+def kv_copy_pages(layers: PagedKVLayers | PagedKV, copies: torch.Tensor) -> None:
+    """Copy pages in every layer's cache, by a list as kv_remap and kv_compact return it: int32 [1 + most][4], row 0
+    {n, 0, 0, 0}, then n rows {source, destination, tokens, 0}."""
+    c, n = (layers._ref, 1) if isinstance(layers, PagedKV) else (layers._c, len(layers.layers))
+    most = copies.shape[0] - 1
+    cp = _whole("copies", copies, torch.int32, (1 + most, 4))
+    if most == 0:
+        return
+    _stream()
+    _check("mx_kv_copy_pages", load().mx_kv_copy_pages(c, n, cp, most))
 
 
 def debug_qmm_stall(stall: bool, wait_ns: int = 0) -> None:

@@ -40,7 +40,7 @@
  * image.  Calls whose kernels pass partial sums through global memory
  * (mx_qmv when K is split across CTAs, mx_moe_gate_up_swiglu for rows the
  * streaming kernel cannot take, mx_moe_down_combine, NVFP4 mx_quantize,
- * mx_paged_attn) use a 16 MiB workspace slot of the stream they are issued on,
+ * mx_paged_attn, mx_beam_select) use a 16 MiB workspace slot of the stream they are issued on,
  * so calls on different streams never share one; a stream's slot is
  * allocated and cleared by the first such call on it (cudaMalloc, with the
  * calling thread switched to relaxed capture mode for it, so that first call
@@ -82,6 +82,8 @@ enum mx_status {
 #define MX_DEVERR_TIMEOUT 0x2    /* a bounded pipeline wait gave up; that tile of Y is NaN */
 #define MX_DEVERR_BAD_PAGE 0x4   /* a context reaches past its block-table row, or a page id outside [0, num_pages) */
 #define MX_DEVERR_BAD_POSITION 0x8 /* a position outside the rotation table, or more new tokens than context */
+#define MX_DEVERR_NO_PAGE 0x10 /* mx_kv_remap: the pool has fewer free pages than the step needs; nothing was changed */
+#define MX_DEVERR_BAD_SLOT 0x20 /* mx_kv_remap: a parent that is no sequence; nothing was changed */
 
 /* Decode GEMV for a few tokens (the memory-bound decode step; "MLxcel 0.8
  * release", section "Profiling set the porting order": the qmv kernel is 95%
@@ -279,7 +281,8 @@ int mx_quantize(int fmt, const void *x, void *codes, void *scales, int M, int K)
  * not read).  q_start, kv_len and the block table are read as soon as a
  * kernel starts, like the expert ids of mx_moe_qmv: they must be complete
  * when the call is issued, i.e. not written by a kernel that lets its
- * dependents start early (no kernel of this library writes them). */
+ * dependents start early (of this library's, mx_kv_remap and mx_kv_compact
+ * write lengths and tables, and nothing starts before they end). */
 
 enum mx_dtype { MX_BF16 = 0, MX_F32 = 1 };
 
@@ -376,6 +379,106 @@ int mx_paged_attn(const mx_paged_kv *kv, const void *q, int64_t q_token_stride, 
                   const int32_t *q_start, const int32_t *kv_len, float scale, int flags, int window,
                   const float *sinks, void *out, float *lse, int T, int B, int Hq, void *workspace,
                   size_t workspace_bytes);
+
+/* ---- decode loops: beams, and the pages of their contexts
+ *
+ * What a loop with several hypotheses or many requests does between the last
+ * projection of a step and the append of the next, without the host. */
+
+/* The k best continuations of each batch entry's W beams.  Beam r = b*W + w
+ * has score[r] (fp32, the logarithm of its probability so far) and logits
+ * x[r][0..V) (dtype bf16 or fp32, rows row_stride elements apart, any
+ * alignment of an element).  mask (or null): bit v % 32 of word
+ * mask[r*mask_stride + v/32] tells whether beam r may take token v.
+ *   key(r, v) = score[r] + x[r][v] - log sum_{v' allowed} e^x[r][v'].
+ * Candidates are the allowed tokens of logit above -infinity of the beams
+ * whose score and sum are finite; a beam of score -infinity, one that may
+ * take nothing and one with a NaN or +infinity among its allowed logits have
+ * none.  They are ordered by key (exponentials and a chunk's sums fp32, the
+ * rest 64 bits), then beam, then logit, then the lower token.
+ *   cand_score / cand_parent / cand_token [B][k]: the first k of each entry:
+ *     the key as fp32, r, v.  Places without a candidate: -infinity, -1, 0.
+ *   next_score / next_parent / next_token [B][W], or all null: the first W
+ *     of these k whose token is not eos (negative: none is), likewise.  With
+ *     k >= 2 W there are W if there are that many at all.
+ * workspace: caller-owned device memory of at least
+ * mx_beam_select_workspace_size(B, W, V, k) bytes, 256-byte aligned;
+ * overwritten, so calls sharing one must not overlap.  Null (with
+ * workspace_bytes 0) where that size is at most 16 MiB: the calling stream's
+ * workspace slot.  Its counters are used in either case.  W <= 64, k <= 128,
+ * V <= 2^20, B <= 4096, B*W <= 65535; logits aligned to an element, all
+ * else to 4 bytes; row_stride >= V and mask_stride >= ceil(V/32) where there is
+ * more than one row. */
+size_t mx_beam_select_workspace_size(int B, int W, int V, int k);
+int mx_beam_select(const void *logits, int dtype, int64_t row_stride, const float *scores, const uint32_t *mask,
+                   int64_t mask_stride, int B, int W, int V, int k, int eos, float *cand_score, int32_t *cand_parent,
+                   int32_t *cand_token, float *next_score, int32_t *next_parent, int32_t *next_token,
+                   void *workspace, size_t workspace_bytes);
+
+/* A pool of cache pages kept on the device.  refs[p]: the number of table
+ * entries (and other holders, a prefix cache for one) of page p; the first
+ * *count of free_pages are the pages without any, the last of those is taken
+ * first.  work: mx_page_pool_work_size(num_pages) bytes, 256-byte aligned,
+ * zeroed once when the pool is made and left alone.  Calls on one pool must
+ * not overlap.  num_pages <= 2^24. */
+typedef struct mx_page_pool {
+    int32_t *count, *refs, *free_pages;
+    void *work;
+    int32_t num_pages;
+} mx_page_pool;
+size_t mx_page_pool_work_size(int num_pages);
+
+/* One step of the sequences' pages: forks, growth, cuts and releases at once.
+ * table_in [S_in][..] (rows in_stride apart, in_pages of a row may be used) and
+ * kv_len_in describe the sequences before the step, one reference of a page
+ * for each entry; table_out [S_out][..] and kv_len_out those after it.  New
+ * sequence s takes the first kept = min(keep[s], length) tokens (keep null: all)
+ * of sequence parent[s] and grows by add[s] tokens (add null: by add_all,
+ * sequences with a parent only).  A negative parent: nothing is taken.
+ * Sequences that are no one's parent release their pages.  Negative lengths, keeps
+ * and adds count as 0.
+ *   - Pages are shared, except that a sequence that grows in the middle of a
+ *     page has that page to itself: where it has other holders too, the
+ *     lowest-numbered such s keeps it if all its holders are such sequences
+ *     of this step, and each other takes a free page and a copy.
+ *   - Pages are handed out in the order of s, the copy's before those that
+ *     lie behind it.  Pages that lose their last reference join free_pages in
+ *     the order of their numbers; they are handed out from the next call on.
+ *   - copies int32 [1 + S_out][4], 16-byte aligned: row 0 {n, 0, 0, 0}, then n rows
+ *     {source page, destination page, tokens, 0} in the order of s, for
+ *     mx_kv_copy_pages (rows behind them are left alone).
+ * All or nothing: if the free pages do not suffice (MX_DEVERR_NO_PAGE), a
+ * parent is not below S_in (MX_DEVERR_BAD_SLOT), or a length exceeds its
+ * table row, a page number the pool, or a page would lose more references than
+ * it has (MX_DEVERR_BAD_PAGE), the pool and table_out stay as they were, every
+ * kv_len_out is -1 and n is 0.
+ * Entries of table_out past a sequence's pages are left alone.  table_out and
+ * kv_len_out must not overlap table_in and kv_len_in.  S_in, S_out <= 4096.
+ * Reads nothing before the preceding kernel has ended, and lets no kernel
+ * start before it ends. */
+int mx_kv_remap(const mx_page_pool *pool, int page_size, const int32_t *table_in, int in_stride, int in_pages,
+                const int32_t *kv_len_in, int S_in, int32_t *table_out, int out_stride, int out_pages,
+                int32_t *kv_len_out, int S_out, const int32_t *parent, const int32_t *keep, const int32_t *add,
+                int add_all, int32_t *copies);
+
+/* Make the pool dense, in place.  U pages have references; the i-th free page
+ * below U takes the place of the i-th page from U on that has references, all of
+ * them entries of this table (pages with other holders stay where they are).
+ * Tables and references follow; copies int32 [1 + num_pages/2][4] receives the moves
+ * as above (whole pages), which must run before the cache is used.
+ * free_pages becomes all pages without references, the lowest taken
+ * first.  Faults (MX_DEVERR_BAD_PAGE) as for mx_kv_remap: nothing changes, n is 0. */
+int mx_kv_compact(const mx_page_pool *pool, int page_size, int32_t *table, int stride, int pages,
+                  const int32_t *kv_len, int S, int32_t *copies);
+
+/* Copy pages of a cache: the first `tokens` tokens of page `source`, both
+ * halves and their scales, to page `destination`, for the rows of a list as
+ * mx_kv_remap makes it (int32 [1 + max_copies][4], 16-byte aligned), in each
+ * of the `layers` caches kv[0..layers), which have the same format, sizes and
+ * strides (their block tables are not used and may be null).  No destination may be
+ * another row's source or destination.  layers <= 256.  A page outside the cache sets
+ * MX_DEVERR_BAD_PAGE and that row is passed over. */
+int mx_kv_copy_pages(const mx_paged_kv *kv, int layers, const int32_t *copies, int max_copies);
 
 /* ---- support calls (not on the pages; part of this library's contract) */
 
