@@ -37,6 +37,7 @@ static inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 blo
 namespace mx {
 
 enum : int { FMT_MXFP4 = 0, FMT_MXFP8 = 1, FMT_NVFP4 = 2 };
+enum : int { FMT_I8 = 3 };  // (of the prefill GEMM's tiles only) 8-bit integers
 enum : int { DEVERR_BAD_EXPERT = 0x1, DEVERR_TIMEOUT = 0x2, DEVERR_BAD_PAGE = 0x4, DEVERR_BAD_POSITION = 0x8 };
 
 // ------------------------------------------------------------- conversions
@@ -78,6 +79,16 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t &o0, uint32
         "cvt.rn.f16x2.e4m3x2 %1, h1;\n\t}"
         : "=r"(o0), "=r"(o1)
         : "r"(w));
+}
+
+// Four 8-bit integers of a word -> two f16x2 words, exact: each byte, its sign
+// turned into an offset of 128, becomes the low byte of an f16 in [1024, 2048),
+// from which 1024 + 128 is taken.
+__device__ __forceinline__ void i8x4_to_f16x2(uint32_t w, uint32_t &o0, uint32_t &o1)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o0) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o1) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
 }
 
 // Two E4M3 bytes (low byte = first element) -> f16x2 (low half = first).

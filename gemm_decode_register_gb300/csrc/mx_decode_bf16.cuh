@@ -1,4 +1,4 @@
-// mx_decode_bf16.cuh -- exact decode of block-float elements to bf16 in the
+// mx_decode_bf16.cuh -- exact decode of block-float elements to bf16 (8-bit integers to f16) in the
 // 128-byte-swizzled K-major shared-memory layout that TMA produces and
 // tcgen05.mma reads (the prefill GEMM's weights, the attention's MXFP8 cache).
 #pragma once
@@ -55,7 +55,15 @@ __device__ __forceinline__ void store_chunk(uint8_t *row_base, int chunk, int sw
 template <int FMT>
 __device__ __forceinline__ void qhalf_store(const uint32_t *w, uint32_t sbits, uint8_t *row_base, int half, int sw)
 {
-    if constexpr (FMT == FMT_MXFP8) {
+    if constexpr (FMT == FMT_I8) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t h0, h1, h2, h3;
+            i8x4_to_f16x2(w[2 * c], h0, h1);
+            i8x4_to_f16x2(w[2 * c + 1], h2, h3);
+            store_chunk(row_base, 4 * half + c, sw, h0, h1, h2, h3);
+        }
+    } else if constexpr (FMT == FMT_MXFP8) {
         const uint32_t e = sbits & 0xFFu;
         // An E4M3 NaN byte (S.1111.111) converts to an f16 NaN, which the
         // exact move would turn into a finite bf16: a half row holding one

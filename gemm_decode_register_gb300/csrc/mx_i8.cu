@@ -1,0 +1,379 @@
+// mx_i8.cu -- products of 8-bit integers with a scale for each token and each
+// output channel, sm_103a:
+//   y[m][n] = (sum_k xq[m][k] wq[n][k]) * sx[m] * sw[n].
+//
+// Quantisation (bound: HBM): a block per token, its row held in registers
+// between the maximum and the rounding.
+//
+// Few tokens (bound: HBM, the weights once): mma.sync m16n8k32 on 8-bit
+// integers, 32-bit sums, exact.  A warp's 16 weight rows come straight from
+// global memory, 16 bytes per lane; the order of k within 64 elements is the
+// lanes' own (lane t of four holds elements 16t .. 16t+15 of both operands),
+// which a sum does not mind, so nothing is rearranged or decoded.  The warps
+// of a CTA share out a row tile's K between them, the tile's sums meet in
+// shared memory, and the next tile's loads are in flight meanwhile.
+//
+// Many tokens: mx_qmm.cu's tensor-core GEMM.  sm_103a has no 8-bit integer
+// form of tcgen05.mma, and integers up to 2048 are exact in f16: tokens are
+// written as f16 integers by the quantisation, weights decoded to f16 in
+// shared memory, products summed in fp32 (exact while sums stay below 2^24).
+#include <cmath>
+
+#include "mx_common.cuh"
+#include "mx_serve.h"
+
+namespace mx {
+
+// ------------------------------------------------------------ quantisation
+
+constexpr int QI8_THREADS = 256;
+constexpr int QI8_KEEP = 4;  // 8-element groups per thread kept in registers
+
+// Eight elements as fp32.
+__device__ __forceinline__ void load8(const uint16_t *p, float (&v)[8])
+{
+    const uint4 r = __ldcg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+__device__ __forceinline__ void load8(const float *p, float (&v)[8])
+{
+    const float4 a = __ldcg(reinterpret_cast<const float4 *>(p)), b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+__device__ __forceinline__ int code_of(float x, float s) { return __float2int_rn(fminf(fmaxf(__fdiv_rn(x, s), -127.0f), 127.0f)); }
+
+__device__ __forceinline__ void store8(int8_t *p, const int (&c)[8])
+{
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = (uint32_t)(c[4 * i] & 255) | (uint32_t)(c[4 * i + 1] & 255) << 8 | (uint32_t)(c[4 * i + 2] & 255) << 16 |
+               (uint32_t)c[4 * i + 3] << 24;
+    *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+}
+// f16 integers (bits), exact.
+__device__ __forceinline__ void store8(uint16_t *p, const int (&c)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = f32x2_to_f16x2((float)c[2 * i], (float)c[2 * i + 1]);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One token per block: s = max |x| / 127, q = x / s to the nearest even
+// integer.  s = 0 (a row of zeros, or of values that small): q = 0.  A NaN or
+// an infinity in the row: s = NaN, q = 0.
+template <typename In, typename Out>
+__global__ void __launch_bounds__(QI8_THREADS) i8_quantize_kernel(const In *__restrict__ x, Out *__restrict__ q,
+                                                                  float *__restrict__ scales, int K)
+{
+    __shared__ float wmax[QI8_THREADS / 32];
+    pdl_trigger();
+    pdl_wait();
+    const size_t row = blockIdx.x;
+    const In *xr = x + row * K;
+    Out *qr = q + row * K;
+    const int groups = K / 8;
+    float keep[QI8_KEEP][8];
+    float m = 0.0f;
+    bool odd = false;  // a NaN (an infinity shows in the maximum)
+#pragma unroll
+    for (int u = 0; u < QI8_KEEP; ++u) {
+        const int i = u * QI8_THREADS + (int)threadIdx.x;
+        if (i >= groups) break;
+        load8(xr + 8 * i, keep[u]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            m = fmaxf(m, fabsf(keep[u][j]));
+            odd |= keep[u][j] != keep[u][j];
+        }
+    }
+    for (int i = QI8_KEEP * QI8_THREADS + (int)threadIdx.x; i < groups; i += QI8_THREADS) {
+        float v[8];
+        load8(xr + 8 * i, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            m = fmaxf(m, fabsf(v[j]));
+            odd |= v[j] != v[j];
+        }
+    }
+    // (non-negative floats are in the order of their bits; a NaN becomes the largest)
+    uint32_t b = __reduce_max_sync(0xFFFFFFFFu, odd ? 0x7FC00000u : __float_as_uint(m));
+    if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = __uint_as_float(b);
+    __syncthreads();
+    b = 0u;
+#pragma unroll
+    for (int w = 0; w < QI8_THREADS / 32; ++w) b = max(b, __float_as_uint(wmax[w]));
+    const bool bad = b >= 0x7F800000u;
+    const float s = bad ? NAN : __fdiv_rn(__uint_as_float(b), 127.0f);
+    if (threadIdx.x == 0) scales[row] = s;
+    const bool any = s > 0.0f;
+#pragma unroll
+    for (int u = 0; u < QI8_KEEP; ++u) {
+        const int i = u * QI8_THREADS + (int)threadIdx.x;
+        if (i >= groups) break;
+        int c[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = any ? code_of(keep[u][j], s) : 0;
+        store8(qr + 8 * i, c);
+    }
+    for (int i = QI8_KEEP * QI8_THREADS + (int)threadIdx.x; i < groups; i += QI8_THREADS) {
+        float v[8];
+        int c[8];
+        load8(xr + 8 * i, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = any ? code_of(v[j], s) : 0;
+        store8(qr + 8 * i, c);
+    }
+}
+
+// 8-bit integers as f16 integers, 16 at a time.
+__global__ void __launch_bounds__(256) i8_widen_kernel(const int8_t *__restrict__ q, uint16_t *__restrict__ h, size_t n16)
+{
+    pdl_trigger();
+    pdl_wait();
+    for (size_t i = blockIdx.x * (size_t)256 + threadIdx.x; i < n16; i += (size_t)gridDim.x * 256) {
+        const uint4 r = __ldcg(reinterpret_cast<const uint4 *>(q) + i);
+        uint32_t o[8];
+        i8x4_to_f16x2(r.x, o[0], o[1]);
+        i8x4_to_f16x2(r.y, o[2], o[3]);
+        i8x4_to_f16x2(r.z, o[4], o[5]);
+        i8x4_to_f16x2(r.w, o[6], o[7]);
+        uint4 *d = reinterpret_cast<uint4 *>(h) + 2 * i;
+        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
+// ------------------------------------------------------------ few tokens
+
+constexpr int MV_WARPS = 16;
+constexpr int MV_THREADS = 32 * MV_WARPS;
+constexpr int MV_GROUP = 4;  // 64-element steps of K whose loads are in flight together
+
+struct I8MvArgs {
+    const int8_t *x;  // [M][K]
+    const float *sx;
+    const int8_t *w;
+    const float *sw;
+    void *y;
+    int M, N, K;
+    int tokens;  // of this launch: M rows from x on, at most 8 NB
+    int parts;   // warps that share a row tile's K: 1, 2, 4, 8 or 16
+    int xpitch;  // bytes of a staged token, an odd multiple of 64
+};
+
+__device__ __forceinline__ uint4 ld_stream_v4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// D += A(16x32, s8, row) * B(32x8, s8, col), exact in 32 bits.
+__device__ __forceinline__ void mma_s8_16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NB: groups of 8 tokens.  Y: float or uint16_t (bf16).
+template <int NB, typename Y>
+__global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(I8MvArgs a)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t *xs = smem;                                                            // [8 NB][xpitch]
+    int4 *red = reinterpret_cast<int4 *>(smem + (size_t)8 * NB * a.xpitch);        // [2][warps][NB][32]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int steps = (a.K + 63) / 64;             // of a row
+    const int per_cta = MV_WARPS / a.parts;        // row tiles at a time
+    const int part = warp % a.parts, sub = warp / a.parts;
+    const int tiles = (a.N + 15) / 16;
+    const int groups = (steps + a.parts * MV_GROUP - 1) / (a.parts * MV_GROUP);
+    const int rounds = (tiles + per_cta - 1) / per_cta;
+
+    uint4 cur[MV_GROUP][2], nxt[MV_GROUP][2];
+    // step number i of group q: part + parts * (q * MV_GROUP + i)
+    auto load = [&](uint4 (&v)[MV_GROUP][2], int round, int q) {
+        const int tile = round * per_cta + sub;
+        const int n0 = 16 * tile + g, n1 = n0 + 8;
+        const int8_t *w = a.w + 16 * t;
+#pragma unroll
+        for (int i = 0; i < MV_GROUP; ++i) {
+            const int k = 64 * (part + a.parts * (q * MV_GROUP + i));
+            const bool in = round < rounds && k + 16 * t < a.K;
+            v[i][0] = in && n0 < a.N ? ld_stream_v4(w + (size_t)n0 * a.K + k) : make_uint4(0u, 0u, 0u, 0u);
+            v[i][1] = in && n1 < a.N ? ld_stream_v4(w + (size_t)n1 * a.K + k) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    pdl_trigger();
+    load(cur, blockIdx.x, 0);  // weights: before the tokens are there
+    pdl_wait();
+    const int vecs = a.xpitch / 16;
+    for (int i = threadIdx.x; i < 8 * NB * vecs; i += MV_THREADS) {
+        const int m = i / vecs, c = i - m * vecs;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (m < a.tokens && 16 * c < a.K) v = __ldcg(reinterpret_cast<const uint4 *>(a.x + (size_t)m * a.K) + c);
+        *reinterpret_cast<uint4 *>(xs + (size_t)m * a.xpitch + 16 * c) = v;
+    }
+    __syncthreads();
+
+    int flip = 0;
+    for (int round = blockIdx.x; round < rounds; round += gridDim.x) {
+        int acc[NB][4] = {};
+        for (int q = 0; q < groups; ++q) {
+            const bool more = q + 1 < groups;
+            load(nxt, more ? round : round + (int)gridDim.x, more ? q + 1 : 0);
+#pragma unroll
+            for (int i = 0; i < MV_GROUP; ++i) {
+                const int k = min(64 * (part + a.parts * (q * MV_GROUP + i)), 64 * (steps - 1));  // (past the row: weights of zero)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(xs + (size_t)(8 * b + g) * a.xpitch + k + 16 * t);
+                    mma_s8_16832(acc[b], cur[i][0].x, cur[i][1].x, cur[i][0].y, cur[i][1].y, x.x, x.y);
+                    mma_s8_16832(acc[b], cur[i][0].z, cur[i][1].z, cur[i][0].w, cur[i][1].w, x.z, x.w);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MV_GROUP; ++i) cur[i][0] = nxt[i][0], cur[i][1] = nxt[i][1];
+        }
+        // the parts' sums meet; outputs in rows of 16 channels
+        int4 *r = red + (size_t)flip * MV_WARPS * NB * 32;
+        flip ^= 1;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) r[(warp * NB + b) * 32 + lane] = make_int4(acc[b][0], acc[b][1], acc[b][2], acc[b][3]);
+        __syncthreads();
+        const int *ri = reinterpret_cast<const int *>(r);
+        for (int o = threadIdx.x; o < per_cta * NB * 128; o += MV_THREADS) {
+            const int row = o % 16, c = o / 16 % 8, b = o / 128 % NB, s = o / (128 * NB);
+            const int m = 8 * b + c, n = 16 * (round * per_cta + s) + row;
+            if (m >= a.tokens || n >= a.N) continue;
+            const int at = 4 * (4 * (row % 8) + c / 2) + 2 * (row / 8) + c % 2;
+            int sum = 0;
+            for (int p = 0; p < a.parts; ++p) sum += ri[((s * a.parts + p) * NB + b) * 128 + at];
+            const float v = __fmul_rn(__fmul_rn((float)sum, __ldcg(a.sx + m)), __ldg(a.sw + n));
+            if constexpr (sizeof(Y) == 4) static_cast<float *>(a.y)[(size_t)m * a.N + n] = v;
+            else static_cast<uint16_t *>(a.y)[(size_t)m * a.N + n] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
+        }
+    }
+}
+
+// ------------------------------------------------------------ host
+
+template <int NB, typename Y>
+static cudaError_t run_mv(const DeviceState &ds, cudaStream_t st, I8MvArgs a)
+{
+    const int smem = 8 * NB * a.xpitch + 2 * MV_WARPS * NB * 32 * 16;
+    if (smem > ds.max_smem_optin) return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(i8_mv_kernel<NB, Y>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int rounds = ((a.N + 15) / 16 + MV_WARPS / a.parts - 1) / (MV_WARPS / a.parts);
+    return launch_k(i8_mv_kernel<NB, Y>, dim3(rounds < ds.num_sms ? rounds : ds.num_sms), dim3(MV_THREADS), smem, st, a);
+}
+
+static int mv_pitch(int K)
+{
+    const int p = (K + 63) / 64 * 64;
+    return p % 128 == 0 ? p + 64 : p;  // two tokens' 64 bytes then fall into different banks
+}
+
+// Most tokens a pass can stage beside the sums' space.
+static int mv_pass_tokens(const DeviceState &ds, int K)
+{
+    for (int nb = 2; nb >= 1; --nb)
+        if (8 * nb * mv_pitch(K) + 2 * MV_WARPS * nb * 512 <= ds.max_smem_optin) return 8 * nb;
+    return 0;
+}
+
+static cudaError_t launch_i8_mv(const DeviceState &ds, cudaStream_t st, const int8_t *x, const float *sx, const int8_t *w,
+                                const float *sw, void *y, int ydtype, int M, int N, int K)
+{
+    const int most = mv_pass_tokens(ds, K);
+    if (most == 0) return cudaErrorInvalidValue;
+    const size_t ye = ydtype == MX_F32 ? 4 : 2;
+    for (int m = 0; m < M; m += most) {
+        I8MvArgs a;
+        a.x = x + (size_t)m * K;
+        a.sx = sx + m;
+        a.w = w;
+        a.sw = sw;
+        a.y = static_cast<char *>(y) + (size_t)m * N * ye;
+        a.M = M;
+        a.N = N;
+        a.K = K;
+        a.tokens = M - m < most ? M - m : most;
+        a.xpitch = mv_pitch(K);
+        const int steps = (K + 63) / 64;
+        a.parts = 1;
+        while (a.parts < MV_WARPS && steps >= 2 * a.parts * MV_GROUP) a.parts *= 2;
+        cudaError_t e;
+        if (a.tokens <= 8) e = ydtype == MX_F32 ? run_mv<1, float>(ds, st, a) : run_mv<1, uint16_t>(ds, st, a);
+        else e = ydtype == MX_F32 ? run_mv<2, float>(ds, st, a) : run_mv<2, uint16_t>(ds, st, a);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+template <typename In, typename Out>
+static cudaError_t run_quantize(cudaStream_t st, const void *x, void *q, float *scales, int M, int K)
+{
+    return launch_k(i8_quantize_kernel<In, Out>, dim3(M), dim3(QI8_THREADS), 0, st, static_cast<const In *>(x),
+                    static_cast<Out *>(q), scales, K);
+}
+
+cudaError_t launch_i8_quantize(const DeviceState &, cudaStream_t st, const void *x, int dtype, int8_t *q, float *scales,
+                               int M, int K)
+{
+    return dtype == MX_F32 ? run_quantize<float, int8_t>(st, x, q, scales, M, K)
+                           : run_quantize<uint16_t, int8_t>(st, x, q, scales, M, K);
+}
+
+// Up to this many tokens the weights are streamed (again for every pass of
+// tokens), above they are multiplied in the GEMM's tiles.
+constexpr int I8_MV_TOKENS = 16;
+
+size_t i8_mm_workspace_bytes(int M, int K)
+{
+    // codes (8-bit for the streaming kernel, f16 for the GEMM), then scales
+    const size_t codes = ((size_t)M * K * 2 + 255) / 256 * 256;
+    return codes + ((size_t)M * 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_i8_mm(const DeviceState &ds, cudaStream_t st, const I8Call &c, void *workspace)
+{
+    const size_t codes = ((size_t)c.M * c.K * 2 + 255) / 256 * 256;
+    float *own_sx = reinterpret_cast<float *>(static_cast<char *>(workspace) + codes);
+    const float *sx = c.xdtype == MX_I8 ? c.sx : own_sx;
+    cudaError_t e;
+    if (c.M <= I8_MV_TOKENS && mv_pass_tokens(ds, c.K) > 0) {
+        const int8_t *x = static_cast<const int8_t *>(c.x);
+        if (c.xdtype != MX_I8) {
+            e = launch_i8_quantize(ds, st, c.x, c.xdtype, static_cast<int8_t *>(workspace), own_sx, c.M, c.K);
+            if (e != cudaSuccess) return e;
+            x = static_cast<const int8_t *>(workspace);
+        }
+        return launch_i8_mv(ds, st, x, sx, c.w, c.sw, c.y, c.ydtype, c.M, c.N, c.K);
+    }
+    uint16_t *h = static_cast<uint16_t *>(workspace);
+    if (c.xdtype == MX_I8) {
+        const size_t n16 = (size_t)c.M * c.K / 16, blocks = (n16 + 255) / 256, most = 8 * (size_t)ds.num_sms;
+        e = launch_k(i8_widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, st,
+                     static_cast<const int8_t *>(c.x), h, n16);
+    } else {
+        e = c.xdtype == MX_F32 ? run_quantize<float, uint16_t>(st, c.x, h, own_sx, c.M, c.K)
+                               : run_quantize<uint16_t, uint16_t>(st, c.x, h, own_sx, c.M, c.K);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_qmm_i8(ds, st, reinterpret_cast<const uint8_t *>(c.w), c.sw, h, sx, c.y, c.ydtype == MX_F32, c.M, c.N, c.K);
+}
+
+}  // namespace mx

@@ -43,6 +43,7 @@
 
 #include "mx_decode_bf16.cuh"
 #include "mx_internal.h"
+#include "mx_serve.h"
 #include "mx_tc.cuh"
 
 namespace mx {
@@ -67,9 +68,9 @@ constexpr int QMM_CTRL_WORDS = 5 + 16;
 template <int FMT, int NACC, bool GROUPED = false>
 struct QmmGeo {
     static constexpr int BM = 256 * NACC;  // output rows per pair tile
-    static constexpr int CODE_ROW = FMT == FMT_MXFP8 ? QMM_BK : QMM_BK / 2;  // code bytes per row per k-block
+    static constexpr int CODE_ROW = FMT == FMT_MXFP8 || FMT == FMT_I8 ? QMM_BK : QMM_BK / 2;  // code bytes per row per k-block
     static constexpr int C_BYTES = 128 * CODE_ROW;
-    static constexpr int SPK = FMT == FMT_NVFP4 ? 4 : 2;  // scale bytes per row per k-block
+    static constexpr int SPK = FMT == FMT_I8 ? 0 : FMT == FMT_NVFP4 ? 4 : 2;  // scale bytes per row per k-block
     static constexpr int SC_BYTES = 128 * SPK;
     static constexpr int X_STAGE = NACC * QMM_X_BYTES;
     // decoder groups: with 256-row tiles one group of 8 warps decoding a
@@ -102,13 +103,13 @@ struct QmmGeo {
     static_assert(SMEM <= QMM_SMEM_LIMIT, "shared memory");
 };
 
-// Instruction descriptor, kind::f16: bf16 A and B (K-major), fp32 D,
-// M = 256 (the pair), N = 256.
-__host__ __device__ constexpr uint32_t qmm_idesc()
+// Instruction descriptor, kind::f16: A and B (K-major) bf16, or f16 for 8-bit
+// integers; fp32 D, M = 256 (the pair), N = 256.
+__host__ __device__ constexpr uint32_t qmm_idesc(bool f16)
 {
-    return (1u << 4)                // D format fp32
-           | (1u << 7)              // A format bf16
-           | (1u << 10)             // B format bf16
+    return (1u << 4)                      // D format fp32
+           | ((f16 ? 0u : 1u) << 7)       // A format f16 / bf16
+           | ((f16 ? 0u : 1u) << 10)      // B format f16 / bf16
            | ((QMM_BN >> 3) << 17)  // N / 8
            | ((256 >> 4) << 24);    // M / 16
 }
@@ -160,6 +161,9 @@ struct QmmArgs {
     const int *slot_of;  // sorted row -> slot (QMM_GROUPED)
     int E;               // experts
     int ntile;           // column tiles per group tile
+    // 8-bit integers: scales of the X rows and the weight rows; Y is fp32 [M][N]
+    const float *xscale = nullptr, *wscale = nullptr;
+    int yf32 = 0;
 };
 
 // silu(g) * u rounded to bf16 for the prefill SwiGLU epilogue: the same
@@ -203,6 +207,23 @@ __device__ __forceinline__ void store_row32(uint16_t *dst, const uint32_t *o, in
             if (2 * j < valid) dst[2 * j] = (uint16_t)(o[j] & 0xFFFFu);
             if (2 * j + 1 < valid) dst[2 * j + 1] = (uint16_t)(o[j] >> 16);
         }
+    }
+}
+
+// The same for 32 fp32 outputs (v: their bits).
+__device__ __forceinline__ void store_row32_f32(float *dst, const uint32_t *v, int valid, int ystore)
+{
+    if (valid >= 32 && ystore == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st_global_v8(dst + 8 * j, v + 8 * j);
+    } else if (valid >= 32 && ystore == 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            reinterpret_cast<uint4 *>(dst)[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < valid) dst[j] = __uint_as_float(v[j]);
     }
 }
 
@@ -335,21 +356,21 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
         // (whole warp, QG::SPF k-blocks in flight).  The scales come through
         // shared memory so that the decoders hold no global loads in flight.
         const int nsc = a.K / (FMT == FMT_NVFP4 ? 16 : 32);  // scale bytes per weight row
-        const bool wide = nsc % SPK == 0;
+        const bool wide = SPK > 0 && nsc % (SPK > 0 ? SPK : 1) == 0;
         const uint8_t *srow[4];
         bool rok[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = wrow + lane + 32 * i;
             rok[i] = r < a.wrows;
-            srow[i] = a.scales + (size_t)(rok[i] ? r : 0) * nsc;
+            if constexpr (SPK > 0) srow[i] = a.scales + (size_t)(rok[i] ? r : 0) * nsc;
         }
         uint32_t pv[QG::SPF][4];
 #pragma unroll
         for (int j = 0; j < QG::SPF; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (j < KB) pv[j][i] = scale_load_edge<SPK>(srow[i], rok[i], j, nsc, wide);
+                if (SPK > 0 && j < KB) pv[j][i] = scale_load_edge<SPK>(srow[i], rok[i], j, nsc, wide);
         int issued = 0;
         bool go = true;
         for (int kb0 = 0; kb0 < KB && go; kb0 += QG::SPF) {
@@ -370,14 +391,14 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
                 }
                 uint8_t *sc = sring + s * QG::SC_BYTES;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4 && SPK > 0; ++i) {
                     if constexpr (SPK == 4) *reinterpret_cast<uint32_t *>(sc + 4 * (lane + 32 * i)) = pv[j][i];
                     else *reinterpret_cast<uint16_t *>(sc + 2 * (lane + 32 * i)) = (uint16_t)pv[j][i];
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full_c[s]);
                 issued = kb + 1;
-                if (kb + QG::SPF < KB)
+                if (SPK > 0 && kb + QG::SPF < KB)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         pv[j][i] = scale_load_edge<SPK>(srow[i], rok[i], kb + QG::SPF, nsc, wide);
@@ -390,7 +411,7 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
             // ---------------- MMA issuer (CTA 0)
-            constexpr uint32_t idesc = qmm_idesc();
+            constexpr uint32_t idesc = qmm_idesc(FMT == FMT_I8);
             int taken = 0, ptaken = 0;
             for (int kb = 0; kb < KB; ++kb) {
                 const int sx = kb % SX, sd = kb % SD;
@@ -436,8 +457,8 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
             const int sc = kb % SC, sd = kb % SD;
             if (!mbar_wait(&full_c[sc], (kb / SC) & 1, abort_flag, a.wait_ns)) break;
             const uint8_t *cp = cring + sc * QG::C_BYTES + row * QG::CODE_ROW + half * (QG::CODE_ROW / 2);
-            uint32_t w[FMT == FMT_MXFP8 ? 8 : 4];
-            if constexpr (FMT == FMT_MXFP8) {
+            uint32_t w[QG::CODE_ROW / 8];
+            if constexpr (QG::CODE_ROW == QMM_BK) {
                 // the two 16-byte reads in a row-dependent order spread a
                 // warp's reads over all banks
                 const int f = (row >> 1) & 1;
@@ -451,7 +472,7 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
                 w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
             }
             const uint8_t *scp = sring + sc * QG::SC_BYTES + SPK * row + (SPK / 2) * half;
-            const uint32_t sbits = SPK == 4 ? *reinterpret_cast<const uint16_t *>(scp) : *scp;
+            const uint32_t sbits = SPK == 4 ? *reinterpret_cast<const uint16_t *>(scp) : SPK == 2 ? *scp : 0u;
             // the codes slot may be refilled (by TMA) once every warp has read it
             fence_proxy_async_smem();
             __syncwarp();
@@ -572,6 +593,19 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0x7FC00000u;
                 }
+                if constexpr (FMT == FMT_I8) {
+                    const float sx = i < rows ? __ldcg(a.xscale + m0 + i) : 0.0f;
+                    const float sw = n0 + nc + lane < a.N ? __ldg(a.wscale + n0 + nc + lane) : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[j]), sx), __shfl_sync(0xFFFFFFFFu, sw, j)));
+                    if (a.yf32) {
+                        if (i < rows && n0 + nc < a.N)
+                            store_row32_f32(reinterpret_cast<float *>(a.Y) + (size_t)(m0 + i) * a.N + n0 + nc, v,
+                                            a.N - (n0 + nc), a.ystore);
+                        continue;
+                    }
+                }
                 uint32_t o[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -683,7 +717,7 @@ static cudaError_t run_qmm_fmt(const DeviceState &ds, cudaStream_t st, const CUt
     return run_qmm<FMT, 1, QMM_DENSE>(ds, st, xmap, cmap, a, ((a.M + 255) / 256) * n_tiles);
 }
 
-// X: [rows][K] bf16, boxes of 64 x 128 rows, 128-byte swizzle; rows past
+// X: [rows][K] bf16 (or f16: 16 bits are moved either way), boxes of 64 x 128 rows, 128-byte swizzle; rows past
 // `rows` read as zero.  Codes: [wrows][row bytes], boxes of one k-block's
 // bytes x 128 rows.
 static cudaError_t encode_maps(int fmt, const uint16_t *X, long long rows, const uint8_t *codes, long long wrows,
@@ -699,10 +733,11 @@ static cudaError_t encode_maps(int fmt, const uint16_t *X, long long rows, const
                      estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-    const cuuint64_t row_bytes = fmt == FMT_MXFP8 ? (cuuint64_t)K : (cuuint64_t)K / 2;
+    const bool bytes = fmt == FMT_MXFP8 || fmt == FMT_I8;  // a code
+    const cuuint64_t row_bytes = bytes ? (cuuint64_t)K : (cuuint64_t)K / 2;
     const cuuint64_t cdims[2] = {row_bytes, (cuuint64_t)wrows};
     const cuuint64_t cstrides[1] = {row_bytes};
-    const cuuint32_t cbox[2] = {fmt == FMT_MXFP8 ? (cuuint32_t)QMM_BK : (cuuint32_t)QMM_BK / 2, 128u};
+    const cuuint32_t cbox[2] = {bytes ? (cuuint32_t)QMM_BK : (cuuint32_t)QMM_BK / 2, 128u};
     r = enc(&cmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), cdims, cstrides, cbox, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -716,12 +751,12 @@ bool qmm_shape_ok(int fmt, int K) { return K > 0 && K % 32 == 0; }
 
 // Widest epilogue store the output rows allow: 32 bytes when Y and every row
 // (width elements of bf16) are 32-byte aligned, 16 bytes when 16-byte
-// aligned, else 2-byte stores.
-static int y_store_width(const void *Y, int width)
+// aligned, else element by element.  fp32 rows likewise.
+static int y_store_width(const void *Y, int width, int size = 2)
 {
     const uintptr_t y = reinterpret_cast<uintptr_t>(Y);
-    if ((y & 31u) == 0 && width % 16 == 0) return 2;
-    if ((y & 15u) == 0 && width % 8 == 0) return 1;
+    if ((y & 31u) == 0 && width * (long long)size % 32 == 0) return 2;
+    if ((y & 15u) == 0 && width * (long long)size % 16 == 0) return 1;
     return 0;
 }
 
@@ -784,6 +819,33 @@ cudaError_t launch_qmm(const DeviceState &ds, cudaStream_t st, int fmt, const ui
     if (fmt == FMT_MXFP4) return run_qmm_fmt<FMT_MXFP4>(ds, st, xmap, cmap, a);
     if (fmt == FMT_MXFP8) return run_qmm_fmt<FMT_MXFP8>(ds, st, xmap, cmap, a);
     return run_qmm_fmt<FMT_NVFP4>(ds, st, xmap, cmap, a);
+}
+
+cudaError_t launch_qmm_i8(const DeviceState &ds, cudaStream_t st, const uint8_t *w, const float *wscale,
+                          const uint16_t *X, const float *xscale, void *Y, bool yf32, int M, int N, int K)
+{
+    if (K <= 0 || K % 16 != 0) return cudaErrorInvalidValue;
+    CUtensorMap xmap, cmap;
+    cudaError_t e = encode_maps(FMT_I8, X, M, w, N, K, xmap, cmap);
+    if (e != cudaSuccess) return e;
+    QmmArgs a;
+    a.scales = nullptr;
+    a.Y = static_cast<uint16_t *>(Y);
+    a.err = ds.err;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    qmm_wait_args(a);
+    a.wrows = N;
+    a.ystore = y_store_width(Y, N, yf32 ? 4 : 2);
+    a.groups = nullptr;
+    a.slot_of = nullptr;
+    a.E = 1;
+    a.ntile = 0;
+    a.xscale = xscale;
+    a.wscale = wscale;
+    a.yf32 = yf32;
+    return run_qmm_fmt<FMT_I8>(ds, st, xmap, cmap, a);
 }
 
 }  // namespace mx

@@ -50,4 +50,24 @@ cudaError_t launch_kv_compact(const DeviceState &ds, cudaStream_t st, const mx_p
 cudaError_t launch_kv_copy_pages(const DeviceState &ds, cudaStream_t st, const mx_paged_kv *kv, int layers,
                                  const int32_t *copies, int max_copies);
 
+// 8-bit integer products.
+constexpr int I8_MAX_K = 131056;  // 2^14 K stays below 2^31
+
+struct I8Call {
+    const void *x;
+    int xdtype;
+    const float *sx;  // MX_I8 only
+    const int8_t *w;
+    const float *sw;
+    void *y;
+    int ydtype, M, N, K;
+};
+size_t i8_mm_workspace_bytes(int M, int K);
+cudaError_t launch_i8_quantize(const DeviceState &ds, cudaStream_t st, const void *x, int dtype, int8_t *q, float *scales,
+                               int M, int K);
+cudaError_t launch_i8_mm(const DeviceState &ds, cudaStream_t st, const I8Call &c, void *workspace);
+// mx_qmm.cu: X f16 integers, y = (X W^T) xscale wscale
+cudaError_t launch_qmm_i8(const DeviceState &ds, cudaStream_t st, const uint8_t *w, const float *wscale,
+                          const uint16_t *X, const float *xscale, void *Y, bool yf32, int M, int N, int K);
+
 }  // namespace mx

@@ -1,5 +1,5 @@
 // mx_serve_api.cu -- the C ABI of the decode loop's calls (beam selection, page
-// pool, page copies): argument validation.
+// pool, page copies) and of the 8-bit integer products: argument validation.
 #include "mx_serve.h"
 
 using namespace mx;
@@ -190,4 +190,50 @@ extern "C" int mx_kv_copy_pages(const mx_paged_kv *kv, int layers, const int32_t
     DeviceState *ds = device_state();
     if (!ds) return MX_ECUDA;
     return finish(launch_kv_copy_pages(*ds, current_stream(), kv, layers, copies, max_copies));
+}
+
+extern "C" int mx_i8_quantize(const void *x, int dtype, int8_t *q, float *scales, int M, int K)
+{
+    if (dtype != MX_BF16 && dtype != MX_F32) return MX_EUNSUPPORTED;
+    if (!x || !q || !scales || M <= 0 || K <= 0 || K % 16 != 0) return MX_EINVAL;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scales, 4)) return MX_EALIGN;
+    DeviceState *ds = device_state();
+    if (!ds) return MX_ECUDA;
+    return finish(launch_i8_quantize(*ds, current_stream(), x, dtype, q, scales, M, K));
+}
+
+extern "C" size_t mx_i8_mm_workspace_size(int M, int K)
+{
+    return M > 0 && K > 0 && K % 16 == 0 && K <= I8_MAX_K ? i8_mm_workspace_bytes(M, K) : 0;
+}
+
+extern "C" int mx_i8_mm(const void *x, int xdtype, const float *x_scales, const int8_t *w, const float *w_scales, void *y,
+                        int ydtype, int M, int N, int K, void *workspace, size_t workspace_bytes)
+{
+    if ((xdtype != MX_BF16 && xdtype != MX_F32 && xdtype != MX_I8) || (ydtype != MX_BF16 && ydtype != MX_F32))
+        return MX_EUNSUPPORTED;
+    if (!x || !w || !w_scales || !y || (xdtype == MX_I8) != (x_scales != nullptr) || M <= 0 || N <= 0 || K <= 0 || K % 16 != 0)
+        return MX_EINVAL;
+    if (K > I8_MAX_K) return MX_EUNSUPPORTED;
+    const size_t need = i8_mm_workspace_bytes(M, K);
+    if (workspace ? workspace_bytes < need : workspace_bytes != 0 || need > WS_FLOATS * sizeof(float)) return MX_EINVAL;
+    if (!aligned(x, 16) || !aligned(x_scales, 4) || !aligned(w, 16) || !aligned(w_scales, 4) || !aligned(y, 16) ||
+        !aligned(workspace, 256))
+        return MX_EALIGN;
+    DeviceState *ds = device_state();
+    if (!ds) return MX_ECUDA;
+    DeviceState v = *ds;
+    if (!workspace && !attach_stream_workspace(v, current_stream())) return MX_ECUDA;
+    I8Call c;
+    c.x = x;
+    c.xdtype = xdtype;
+    c.sx = x_scales;
+    c.w = w;
+    c.sw = w_scales;
+    c.y = y;
+    c.ydtype = ydtype;
+    c.M = M;
+    c.N = N;
+    c.K = K;
+    return finish(launch_i8_mm(v, current_stream(), c, workspace ? workspace : v.ws));
 }

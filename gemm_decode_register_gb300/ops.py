@@ -73,6 +73,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
             "mx_kv_remap": [P, I, P, I, I, P, I, P, I, I, P, I, P, P, P, I, P],
             "mx_kv_compact": [P, I, P, I, I, P, I, P],
             "mx_kv_copy_pages": [P, I, P, I],
+            "mx_i8_quantize": [P, I, P, P, I, I],
+            "mx_i8_mm": [P, I, P, P, P, P, I, I, I, I, P, Z],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -82,7 +84,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
                            "mx_moe_ffn_prefill_workspace_size": [I, I, I, I, I],
                            "mx_paged_attn_workspace_size": [I, I, I, I, I],
                            "mx_beam_select_workspace_size": [I, I, I, I],
-                           "mx_page_pool_work_size": [I]}.items():
+                           "mx_page_pool_work_size": [I],
+                           "mx_i8_mm_workspace_size": [I, I]}.items():
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = Z
@@ -764,6 +767,76 @@ def kv_copy_pages(layers: PagedKVLayers | PagedKV, copies: torch.Tensor) -> None
         return
     _stream()
     _check("mx_kv_copy_pages", load().mx_kv_copy_pages(c, n, cp, most))
+
+
+# ---- products of 8-bit integers
+
+
+def i8_quantize(x: torch.Tensor, q: torch.Tensor | None = None,
+                scales: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """x [M][K] (bf16 or fp32) -> (codes int8 [M][K], scales fp32 [M]): the scale max |x| / 127 of each token, codes
+    x / scale to the nearest even integer."""
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"x: expected bf16 or fp32, got {x.dtype}")
+    M, K = x.shape
+    xp = _whole("x", x, x.dtype, (M, K))
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    if scales is None:
+        scales = torch.empty((M,), dtype=torch.float32, device=x.device)
+    qp, sp = _whole("q", q, torch.int8, (M, K)), _whole("scales", scales, torch.float32, (M,))
+    if M == 0:
+        return q, scales
+    _stream()
+    _check("mx_i8_quantize", load().mx_i8_quantize(xp, _DTYPES[x.dtype], qp, sp, M, K))
+    return q, scales
+
+
+def i8_mm_workspace(M: int, K: int, device="cuda") -> torch.Tensor:
+    return _workspace(load().mx_i8_mm_workspace_size(M, K), None, device)
+
+
+def i8_mm(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, x_scales: torch.Tensor | None = None,
+          out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+          workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y[M][N] (bf16 or fp32) = (xq . w^T) * x_scales[m] * w_scales[n], w int8 [N][K], w_scales fp32 [N].  x: int8
+    [M][K] with x_scales fp32 [M] (i8_quantize), or bf16 / fp32 [M][K], quantised on the way."""
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError("x and w: expected [M][K] and [N][K]")
+    M, K = x.shape
+    N = w.shape[0]
+    if x.dtype is torch.int8:
+        if x_scales is None:
+            raise ValueError("x_scales: int8 codes come with their scales")
+        xd, sp = 2, _whole("x_scales", x_scales, torch.float32, (M,))
+    elif x.dtype in _DTYPES:
+        if x_scales is not None:
+            raise ValueError("x_scales: only with int8 codes")
+        xd, sp = _DTYPES[x.dtype], None
+    else:
+        raise ValueError(f"x: expected int8, bf16 or fp32, got {x.dtype}")
+    xp, wp = _whole("x", x, x.dtype, (M, K)), _whole("w", w, torch.int8, (N, K))
+    cp = _whole("w_scales", w_scales, torch.float32, (N,))
+    if out is None:
+        if out_dtype not in _DTYPES:
+            raise ValueError(f"out_dtype: expected bf16 or fp32, got {out_dtype}")
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        op = out.data_ptr()
+    else:
+        if out.dtype not in _DTYPES:
+            raise ValueError(f"out: expected bf16 or fp32, got {out.dtype}")
+        op = _whole("out", out, out.dtype, (M, N))
+    if M == 0:
+        return out
+    lib = load()
+    if workspace is None:
+        need = lib.mx_i8_mm_workspace_size(M, K)
+        if need > WORKSPACE_SLOT_BYTES:
+            workspace = _workspace(need, None, x.device)
+    ap, an = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
+    _stream()
+    _check("mx_i8_mm", lib.mx_i8_mm(xp, xd, sp, wp, cp, op, _DTYPES[out.dtype], M, N, K, ap, an))
+    return out
 
 
 def debug_qmm_stall(stall: bool, wait_ns: int = 0) -> None:

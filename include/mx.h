@@ -40,7 +40,7 @@
  * image.  Calls whose kernels pass partial sums through global memory
  * (mx_qmv when K is split across CTAs, mx_moe_gate_up_swiglu for rows the
  * streaming kernel cannot take, mx_moe_down_combine, NVFP4 mx_quantize,
- * mx_paged_attn, mx_beam_select) use a 16 MiB workspace slot of the stream they are issued on,
+ * mx_paged_attn, mx_beam_select, mx_i8_mm) use a 16 MiB workspace slot of the stream they are issued on,
  * so calls on different streams never share one; a stream's slot is
  * allocated and cleared by the first such call on it (cudaMalloc, with the
  * calling thread switched to relaxed capture mode for it, so that first call
@@ -284,7 +284,7 @@ int mx_quantize(int fmt, const void *x, void *codes, void *scales, int M, int K)
  * dependents start early (of this library's, mx_kv_remap and mx_kv_compact
  * write lengths and tables, and nothing starts before they end). */
 
-enum mx_dtype { MX_BF16 = 0, MX_F32 = 1 };
+enum mx_dtype { MX_BF16 = 0, MX_F32 = 1, MX_I8 = 2 /* (x of mx_i8_mm only) */ };
 
 /* Cache formats: bf16, or MXFP8 as above (E4M3 codes, one E8M0 scale per 32
  * elements along the head, so each cached token can be written by itself). */
@@ -479,6 +479,34 @@ int mx_kv_compact(const mx_page_pool *pool, int page_size, int32_t *table, int s
  * another row's source or destination.  layers <= 256.  A page outside the cache sets
  * MX_DEVERR_BAD_PAGE and that row is passed over. */
 int mx_kv_copy_pages(const mx_paged_kv *kv, int layers, const int32_t *copies, int max_copies);
+
+/* ---- products of 8-bit integers, with a scale for each token and channel
+ *
+ * For layers of checkpoints that come in 8-bit integers, the vocabulary
+ * projection for one. */
+
+/* Tokens to 8-bit integers: scales[m] = max_k |x[m][k]| / 127, q[m][k] =
+ * x[m][k] / scales[m] to the nearest integer, ties to even (quotients rounded
+ * to fp32).  x [M][K] bf16 or fp32.  A row whose scale is 0 has codes 0; one
+ * that holds a NaN or an infinity has a NaN scale and codes 0.  K a multiple of
+ * 16; x and q 16-byte aligned. */
+int mx_i8_quantize(const void *x, int dtype, int8_t *q, float *scales, int M, int K);
+
+/* y[m][n] = (sum_k xq[m][k] * w[n][k]) * x_scales[m] * w_scales[n],
+ * w int8 [N][K], w_scales fp32 [N], y [M][N] bf16 or fp32 (ydtype).  x [M][K]:
+ * int8 (xdtype MX_I8) with x_scales fp32 [M], or bf16 / fp32 (x_scales null),
+ * quantised as by mx_i8_quantize on the way.  Up to 16 tokens (of K up
+ * to about 25,000) stream the weights and sum in 32-bit integers; the rest goes to the tensor cores, where sums
+ * are fp32: exact while they stay below 2^24 in magnitude, rounded to 24
+ * bits above.  The scales are applied in fp32, then y is rounded once.
+ * workspace: at least mx_i8_mm_workspace_size(M, K) bytes, 256-byte aligned,
+ * overwritten; null (with workspace_bytes 0) where that is at most 16 MiB: the calling stream's
+ * slot.  w and w_scales are weights: they are read as soon as the kernels start.
+ * Any M, N >= 1; K a multiple of 16, at most 131056.  x, w, y 16-byte aligned.
+ * A pipeline wait that times out sets MX_DEVERR_TIMEOUT and makes that tile of y NaN. */
+size_t mx_i8_mm_workspace_size(int M, int K);
+int mx_i8_mm(const void *x, int xdtype, const float *x_scales, const int8_t *w, const float *w_scales, void *y,
+             int ydtype, int M, int N, int K, void *workspace, size_t workspace_bytes);
 
 /* ---- support calls (not on the pages; part of this library's contract) */
 

@@ -139,6 +139,36 @@ def test_copy_rejects_lists(lib):
     assert lib.mx_kv_copy_pages(c, 1, A + 8, 4) == -3
 
 
+@pytest.mark.parametrize("args,want", [
+    ((A, 2, A, A, 4, 64), -2), ((0, 0, A, A, 4, 64), -1), ((A, 0, 0, A, 4, 64), -1), ((A, 0, A, 0, 4, 64), -1),
+    ((A, 0, A, A, 0, 64), -1), ((A, 0, A, A, 4, 0), -1), ((A, 0, A, A, 4, 72), -1), ((A + 8, 0, A, A, 4, 64), -3),
+    ((A, 0, A + 4, A, 4, 64), -3), ((A, 0, A, A + 2, 4, 64), -3)])
+def test_i8_quantize_rejects(lib, args, want):
+    assert lib.mx_i8_quantize(*args) == want
+
+
+def i8_args(**kw):
+    d = dict(x=A, xdtype=2, sx=A, w=A, sw=A, y=A, ydtype=0, M=4, N=100, K=64, ws=A, ws_bytes=Z)
+    d.update(kw)
+    return list(d.values())
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(xdtype=3), -2), (dict(ydtype=2), -2), (dict(x=0), -1), (dict(w=0), -1), (dict(sw=0), -1), (dict(y=0), -1),
+    (dict(sx=0), -1), (dict(xdtype=0), -1),  # int8 without scales, bf16 with them
+    (dict(M=0), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(K=72), -1), (dict(K=131072), -2), (dict(ws_bytes=255), -1),
+    (dict(ws=None), -1), (dict(ws=None, ws_bytes=0, M=4096, K=8192), -1), (dict(x=A + 8), -3), (dict(w=A + 4), -3),
+    (dict(y=A + 8), -3), (dict(sx=A + 1), -3), (dict(sw=A + 2), -3), (dict(ws=A + 64), -3)])
+def test_i8_mm_rejects(lib, kw, want):
+    assert lib.mx_i8_mm(*i8_args(**kw)) == want
+
+
+def test_i8_workspace_sizes(lib):
+    f = lib.mx_i8_mm_workspace_size
+    assert f(1, 16) > 0 and f(4096, 8192) >= 4096 * 8192 * 2 and f(3, 8192) % 256 == 0
+    assert f(0, 16) == f(1, 0) == f(1, 24) == f(1, 131072) == 0
+
+
 def test_bindings_refuse_host_tensors(lib):
     x, c = torch.zeros((4, 10)), torch.zeros((2, 2))
     with pytest.raises(ValueError):
@@ -147,3 +177,12 @@ def test_bindings_refuse_host_tensors(lib):
         ops.beam_select(x.double(), c)
     with pytest.raises(ValueError):
         ops.PagePool(10, device="cpu")
+    w, s = torch.zeros((4, 32), dtype=torch.int8), torch.zeros(4)
+    with pytest.raises(ValueError):
+        ops.i8_quantize(torch.zeros((2, 32)))
+    with pytest.raises(ValueError):
+        ops.i8_mm(torch.zeros((2, 32)), w, s)
+    with pytest.raises(ValueError):
+        ops.i8_mm(w, w, s)  # codes without scales
+    with pytest.raises(ValueError):
+        ops.i8_mm(torch.zeros((2, 16)), w, s)
