@@ -5,26 +5,30 @@
 // over the tokens v that row r's mask allows; the k largest of a batch
 // entry's W rows (bound: HBM, one pass over the logits).
 //
-// Two launches.  beam_chunk_kernel: a block takes a chunk of one row, up to
-// eight 16-byte vectors per thread, held in registers.  Within a row the
-// order of the keys is that of the logits, so a chunk needs no more of its row
-// than itself:
-//   - the largest element of each vector (packed maxima) and thread; each warp
-//     finds the r-th largest of its lanes' by r warp-wide maxima.  With r warps
-//     times k at least k, the smallest of these is a bound that k elements of
-//     the block reach, and not many more do;
-//   - the vectors that reach it go to a queue in shared memory, a few threads
-//     take their elements apart, and each one that reaches the bound counts
-//     those before it: its rank;
-//   - the sum of exponentials over the block's maximum.
+// Two launches.  beam_chunk_kernel: a block takes a stretch of one row and
+// walks it in steps of four 16-byte vectors per thread, the next step's loads in
+// flight.  Within a row the order of the keys is that of the logits, so a
+// stretch needs no more of its row than itself:
+//   - the largest element of each vector (packed maxima) and thread.  In the
+//     first step each warp finds the r-th largest of its lanes' by r warp-wide
+//     maxima; with r times the warps at least k, the smallest of these is a
+//     bound that k elements reach, and not many more do;
+//   - vectors that reach the bound go to a queue in shared memory.  When it
+//     fills, and after 2, 4, 8, .. steps, a few threads take their elements
+//     apart and the bound rises in the same way by what is found so far: so
+//     each doubling adds about k elements.  (A bisection to the k-th best cost
+//     3 us each time, this 0.3.)  Rows whose later steps keep bringing better
+//     elements get a bound from the step at hand too;
+//   - exponentials are summed over the thread's own reference, a maximum that
+//     is raised only when it falls behind by more than 10.
+// At the end each element found counts those before it: its rank.
 // beam_join_kernel: a block takes a batch entry: the rows' sums, the same
-// bound from the heads of the chunks' lists (in fp32, with what its rounding may
-// be off on either side), and the ranks of those that reach it by keys in 64
+// bound from the heads of the stretches' lists (in fp32, with what its rounding may
+// be off on either side), and the ranks of those that reach it by keys of 48
 // bits: near ties between beams are decided by bits that fp32 scores of -20
-// do not have.  It is launched while the chunks run and waits for them.
+// do not have.  It is launched while the stretches run and waits for them.
 // Where ties let more elements reach a bound than the shared memory holds,
-// both kernels go slower ways to the same result (one that orders equal logits by their
-// places).
+// both kernels go slower ways to the same result.
 #include <cfloat>
 #include <cmath>
 
@@ -36,8 +40,10 @@ namespace mx {
 
 constexpr int BEAM_THREADS = 256;
 constexpr int BEAM_WARPS = BEAM_THREADS / 32;
-constexpr int BEAM_QUEUE = 512;   // vectors that reach a chunk's bound
-constexpr int BEAM_FOUND = 1024;  // elements that do (a chunk's, a batch entry's)
+constexpr int BEAM_U = 4;                      // vectors of a thread and step
+constexpr int BEAM_STEP = BEAM_THREADS * BEAM_U;  // vectors of a step
+constexpr int BEAM_QUEUE = 512;   // vectors that reach a stretch's bound
+constexpr int BEAM_FOUND = 1024;  // elements that do (a stretch's, a batch entry's)
 
 struct BeamArgs {
     const void *logits;
@@ -45,7 +51,8 @@ struct BeamArgs {
     const float *scores;
     const uint32_t *mask;
     long long mask_stride;
-    int B, W, V, k, eos, chunks;
+    int B, W, V, k, eos;
+    int chunks, steps;  // stretches of a row, steps of a stretch
     float *score, *next_score;
     int32_t *parent, *token, *next_parent, *next_token;
     float2 *sums;              // [rows][chunks] maximum and sum
@@ -64,22 +71,21 @@ __device__ __forceinline__ float unordered(uint32_t o)
 {
     return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
-__device__ __forceinline__ unsigned long long ordered64(double d)
-{
-    const long long b = __double_as_longlong(d);
-    return (unsigned long long)b ^ ((unsigned long long)(b >> 63) | 0x8000000000000000ull);
-}
-
 constexpr uint32_t ORD_NEG_INF = 0x007FFFFFu;
 
-// One element type's vectors, and (logit, place in the chunk) as one number:
-// bf16 in 32 bits (a chunk has at most 2^16 places), fp32 in 64.
+// (logit, token) as one whole number: larger logits first, the two zeros
+// alike, then lower tokens.
+__device__ __forceinline__ unsigned long long logit_token(float f, int v)
+{
+    return ((unsigned long long)ordered(f + 0.0f) << 32) | (0xFFFFFFFFu - (uint32_t)v);
+}
+
+// One element type's vectors.
 template <typename E>
 struct Elem;
 template <>
 struct Elem<uint16_t> {
     static constexpr int VEC = 8;
-    using Key = uint32_t;
     static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
     {
         uint32_t d;
@@ -105,21 +111,12 @@ struct Elem<uint16_t> {
     static __device__ __forceinline__ float get(const uint4 &v, int j)
     {
         const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
-        return ((j & 1) ? bf16_hi(w) : bf16_lo(w)) + 0.0f;
+        return (j & 1) ? bf16_hi(w) : bf16_lo(w);
     }
-    static __device__ __forceinline__ Key key(float f, int place)
-    {
-        return (ordered(f) & 0xFFFF0000u) | (0xFFFFu - (uint32_t)place);
-    }
-    static constexpr Key NONE = (ORD_NEG_INF & 0xFFFF0000u) | 0xFFFFu, LAST = 0xFFFFFFFFu;  // keys up to NONE are no candidates
-    // (a negative bf16's ordered number ends in ones)
-    static __device__ __forceinline__ uint32_t value(Key k) { return (k >> 31) ? k & 0xFFFF0000u : k | 0xFFFFu; }
-    static __device__ __forceinline__ int place(Key k) { return (int)(0xFFFFu - (k & 0xFFFFu)); }
 };
 template <>
 struct Elem<float> {
     static constexpr int VEC = 4;
-    using Key = unsigned long long;
     static __device__ __forceinline__ float top(const uint4 &v)
     {
         return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
@@ -133,15 +130,8 @@ struct Elem<float> {
     }
     static __device__ __forceinline__ float get(const uint4 &v, int j)
     {
-        return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w) + 0.0f;
+        return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w);
     }
-    static __device__ __forceinline__ Key key(float f, int place)
-    {
-        return ((Key)ordered(f) << 32) | (0xFFFFFFFFu - (uint32_t)place);
-    }
-    static constexpr Key NONE = ((Key)ORD_NEG_INF << 32) | 0xFFFFFFFFu, LAST = 0xFFFFFFFFFFFFFFFFull;
-    static __device__ __forceinline__ uint32_t value(Key k) { return (uint32_t)(k >> 32); }
-    static __device__ __forceinline__ int place(Key k) { return (int)(0xFFFFFFFFu - (uint32_t)k); }
 };
 
 // The r-th largest of the lanes' values, equal ones counted one by one; `next`
@@ -236,188 +226,291 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t *row, int e, int wo
     return lo >> s;
 }
 
-template <typename E, int U, bool MASK>
-__global__ void __launch_bounds__(BEAM_THREADS, U == 8 && !MASK ? 4 : 3) beam_chunk_kernel(const __grid_constant__ BeamArgs a)
+template <typename E, bool MASK>
+__global__ void __launch_bounds__(BEAM_THREADS, MASK ? 3 : 4) beam_chunk_kernel(const __grid_constant__ BeamArgs a)
 {
     using L = Elem<E>;
-    using Key = typename L::Key;
-    constexpr int VEC = L::VEC;
+    constexpr int VEC = L::VEC, U = BEAM_U;
     __shared__ uint4 queue[BEAM_QUEUE];
-    __shared__ uint16_t queue_at[BEAM_QUEUE];
-    __shared__ Key found[BEAM_FOUND];
-    __shared__ float warp_top[BEAM_WARPS], warp_sum[BEAM_WARPS];
+    __shared__ int queue_at[BEAM_QUEUE];  // the vector's first token
+    __shared__ unsigned long long found[BEAM_FOUND];
+    __shared__ float warp_ref[BEAM_WARPS], warp_sum[BEAM_WARPS];
     __shared__ uint32_t warp_bound[BEAM_WARPS];
     __shared__ int n_queue, n_found, scratch[BEAM_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int chunk = blockIdx.x, row = blockIdx.y;
-
+    if (tid == 0) n_queue = n_found = 0;
     pdl_trigger();
     pdl_wait();
     const E *x = static_cast<const E *>(a.logits) + (size_t)row * a.row_stride;
+    const uint32_t *mask = MASK ? a.mask + (size_t)row * a.mask_stride : nullptr;
     // vectors of the row counted from the 16-byte boundary at or before it;
     // one that the row only partly covers is read element by element
     const int lead = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(E));
-    const int first = chunk * BEAM_THREADS * U;
-    uint4 raw[U];
-    auto load = [&] {
+    const int begin = chunk * a.steps * BEAM_STEP, words = (a.V + 31) >> 5;
+    const int steps = min(a.steps, ((lead + a.V + VEC - 1) / VEC - begin + BEAM_STEP - 1) / BEAM_STEP);
+    auto token = [&](int step, int u) { return (begin + step * BEAM_STEP + u * BEAM_THREADS + tid) * VEC - lead; };
+    auto load = [&](uint4 (&v)[U], int step) {
+        const int e0 = (begin + step * BEAM_STEP) * VEC - lead;
+        if (e0 >= 0 && e0 + BEAM_STEP * VEC <= a.V) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(x + e0) + tid;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int e = (first + u * BEAM_THREADS + tid) * VEC - lead;
-            if (e >= 0 && e + VEC <= a.V) raw[u] = __ldcs(reinterpret_cast<const uint4 *>(x + e));
-            else raw[u] = edge_vector(x + e, e < 0 ? -e : 0, min(VEC, a.V - e));
-        }
-        if constexpr (MASK) {
-            const uint32_t *m = a.mask + (size_t)row * a.mask_stride;
-            const int words = (a.V + 31) >> 5;
-            uint32_t bits[U];
+            for (int u = 0; u < U; ++u) v[u] = __ldcs(p + u * BEAM_THREADS);
+        } else {
 #pragma unroll
-            for (int u = 0; u < U; ++u) bits[u] = mask_bits<VEC>(m, (first + u * BEAM_THREADS + tid) * VEC - lead, words);
-#pragma unroll
-            for (int u = 0; u < U; ++u) L::keep(raw[u], bits[u]);
-        }
-    };
-    load();
-    if (tid == 0) n_queue = n_found = 0;
-
-    // largest elements; the warp's part of the bound: r of its lanes reach it,
-    // and the warps that have elements make r times their number k or more
-    float top[U], m = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        top[u] = L::top(raw[u]);
-        m = fmaxf(m, top[u]);
-    }
-    {
-        const int vecs = min(BEAM_THREADS, (lead + a.V + VEC - 1) / VEC - first);
-        const int warps = max(1, (vecs + 31) / 32), r = (a.k + warps - 1) / warps;
-        const uint32_t mine = ordered(m + 0.0f);
-        const float wm = unordered(__reduce_max_sync(0xFFFFFFFFu, mine));
-        uint32_t bound = r > 32 ? 0u : warp_nth(mine, r, [] { return 0u; });
-        if (warp >= warps) bound = 0xFFFFFFFFu;  // (no elements, no say)
-        if (lane == 0) {
-            warp_top[warp] = wm;
-            warp_bound[warp] = bound;
-        }
-    }
-    __syncthreads();
-    float all = warp_top[0];
-    uint32_t least = warp_bound[0];
-#pragma unroll
-    for (int w = 1; w < BEAM_WARPS; ++w) {
-        all = fmaxf(all, warp_top[w]);
-        least = min(least, warp_bound[w]);
-    }
-    const float bound = least > ORD_NEG_INF ? unordered(least) : -FLT_MAX;  // (-inf is no candidate)
-
-    // the vectors that reach the bound; the sum over the block's maximum
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (top[u] >= bound) {
-            const int i = atomicAdd(&n_queue, 1);
-            if (i < BEAM_QUEUE) {
-                queue[i] = raw[u];
-                queue_at[i] = (uint16_t)(u * BEAM_THREADS + tid);
+            for (int u = 0; u < U; ++u) {
+                const int e = token(step, u);
+                if (e >= 0 && e + VEC <= a.V) v[u] = __ldcs(reinterpret_cast<const uint4 *>(x + e));
+                else v[u] = edge_vector(x + e, e < 0 ? -e : 0, min(VEC, a.V - e));
             }
         }
-    const float over = all > -INFINITY ? all : 0.0f;
-    // (x - maximum before the factor: its rounding stays relative to the difference)
-    const float2 shift = make_float2(-over, -over), log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
-    float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+    };
+    auto load_bits = [&](uint32_t (&bits)[U], int step) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) bits[u] = mask_bits<VEC>(mask, token(step, u), words);
+    };
+
+    float bound = -FLT_MAX;  // (-inf is no candidate)
+    // raises it to what k of the threads' values reach, of which the first
+    // `have` threads have one: r lanes of each of their warps.  Two barriers.
+    auto raise = [&](float v, int have) {
+        const int warps = max(1, min(BEAM_WARPS, (have + 31) / 32)), r = (a.k + warps - 1) / warps;
+        uint32_t n = 0xFFFFFFFFu;  // (no values, no say)
+        if (warp < warps) n = r > 32 ? 0u : warp_nth(ordered(v + 0.0f), r, [] { return 0u; });
+        if (lane == 0) warp_bound[warp] = n;
+        __syncthreads();
+        n = warp_bound[0];
 #pragma unroll
-        for (int j = 0; j < VEC; j += 2) {
-            const float2 d = mul2(add2(make_float2(L::get(raw[u], j), L::get(raw[u], j + 1)), shift), log2e);
-            sum2[(j / 2) & 1] = add2(sum2[(j / 2) & 1], make_float2(exp2_fast(d.x), exp2_fast(d.y)));
-        }
-    float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) warp_sum[warp] = sum;
-    __syncthreads();
-    const size_t list = (size_t)row * a.chunks + chunk;
-    if (tid == 0) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < BEAM_WARPS; ++w) s += warp_sum[w];
-        a.sums[list] = make_float2(all, s);
-    }
-    const int vectors = n_queue;
-    if (vectors <= BEAM_QUEUE)
-        for (int i = tid; i < vectors; i += BEAM_THREADS) {
+        for (int w = 1; w < BEAM_WARPS; ++w) n = min(n, warp_bound[w]);
+        if (n > ORD_NEG_INF) bound = fmaxf(bound, unordered(n));
+        __syncthreads();
+    };
+    // the queue's elements that reach the bound are found; the queue is empty after it
+    auto drain = [&] {
+        const int n = min(n_queue, BEAM_QUEUE);
+        for (int i = tid; i < n; i += BEAM_THREADS) {
             const uint4 v = queue[i];
-            const int place = (int)queue_at[i] * VEC;
+            const int at = queue_at[i];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 const float f = L::get(v, j);
                 if (f >= bound) {
-                    const int at = atomicAdd(&n_found, 1);
-                    if (at < BEAM_FOUND) found[at] = L::key(f + 0.0f, place + j);
+                    const int o = atomicAdd(&n_found, 1);
+                    if (o < BEAM_FOUND) found[o] = logit_token(f, at + j);
                 }
             }
         }
+        __syncthreads();
+        if (tid == 0) n_queue = 0;
+    };
+    // the bound from what is found so far: each thread's largest of up to four
+    auto raise_by_found = [&] {
+        const int n = n_found;
+        uint32_t v = 0u;
+        for (int i = tid; i < n; i += BEAM_THREADS) v = max(v, (uint32_t)(found[i] >> 32));
+        raise(v > ORD_NEG_INF ? unordered(v) : -INFINITY, n);
+    };
+
+    uint4 cur[U], nxt[U];
+    uint32_t bits[U], nbits[U];
+    load(cur, 0);
+    if constexpr (MASK) load_bits(bits, 0);
+    float ref = -INFINITY;
+    float2 sum2 = make_float2(0.0f, 0.0f);
+    bool hot = true, lost = false;
+    for (int step = 0; step < steps; ++step) {
+        if (step + 1 < steps) {
+            load(nxt, step + 1);
+            if constexpr (MASK) load_bits(nbits, step + 1);
+        }
+        if constexpr (MASK) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) L::keep(cur[u], bits[u]);
+        }
+        float top[U], m = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            top[u] = L::top(cur[u]);
+            m = fmaxf(m, top[u]);
+        }
+        if (hot) raise(m, (lead + a.V + VEC - 1) / VEC - begin - step * BEAM_STEP);
+        bool filling = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (top[u] >= bound) {
+                const int i = atomicAdd(&n_queue, 1);
+                filling |= i >= BEAM_QUEUE / 2;
+                if (i < BEAM_QUEUE) {
+                    queue[i] = cur[u];
+                    queue_at[i] = token(step, u);
+                }
+            }
+        if (m > ref + 10.0f) {  // (the first time too)
+            const float s = ref > -INFINITY ? __expf(ref - m) : 1.0f;
+            sum2.x *= s;
+            sum2.y *= s;
+            ref = m;
+        }
+        // (x - reference before the factor: its rounding stays relative to the difference)
+        const float off = ref > -INFINITY ? -ref : 0.0f;
+        const float2 shift = make_float2(off, off), log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < VEC; j += 2) {
+                const float2 d = mul2(add2(make_float2(L::get(cur[u], j), L::get(cur[u], j + 1)), shift), log2e);
+                sum2 = add2(sum2, make_float2(exp2_fast(d.x), exp2_fast(d.y)));
+            }
+        if (step + 1 < steps) {
+            hot = __syncthreads_or(filling);  // (n_queue itself may have grown by another's next step)
+            if (hot || (step > 0 && (step & (step + 1)) == 0)) {
+                __syncthreads();
+                lost |= n_queue > BEAM_QUEUE;
+                __syncthreads();
+                drain();
+                lost |= n_found > BEAM_FOUND;
+                __syncthreads();
+                if (!lost) raise_by_found();
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) cur[u] = nxt[u];
+            if constexpr (MASK) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) bits[u] = nbits[u];
+            }
+        }
+    }
+    // the sums, over the largest reference
+    {
+        float wr = ref, ws = sum2.x + sum2.y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) wr = fmaxf(wr, __shfl_xor_sync(0xFFFFFFFFu, wr, o));
+        ws = ref == wr ? ws : ws * __expf(ref - wr);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) ws += __shfl_xor_sync(0xFFFFFFFFu, ws, o);
+        if (lane == 0) {
+            warp_ref[warp] = wr;
+            warp_sum[warp] = ws;
+        }
+    }
+    __syncthreads();
+    const size_t list = (size_t)row * a.chunks + chunk;
+    if (tid == 0) {
+        float r = -INFINITY, s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < BEAM_WARPS; ++w) r = fmaxf(r, warp_ref[w]);
+#pragma unroll
+        for (int w = 0; w < BEAM_WARPS; ++w) s += warp_ref[w] == r ? warp_sum[w] : warp_sum[w] * __expf(warp_ref[w] - r);
+        a.sums[list] = make_float2(r, s);
+    }
+    lost |= n_queue > BEAM_QUEUE;
+    drain();
+    lost |= n_found > BEAM_FOUND;
     __syncthreads();
     int n = n_found;
-    if (vectors > BEAM_QUEUE || n > BEAM_FOUND) {
-        // too many reach it (ties, most often): the k-th largest key, places
-        // and all, by bisection over every element (loaded again, so that the
-        // registers are free till here)
-        load();
-        Key lo = L::NONE + 1, hi = L::LAST;
+    if (!lost) {
+        raise_by_found();
+        // what no longer reaches the bound is dropped
+        constexpr int F = BEAM_FOUND / BEAM_THREADS;
+        unsigned long long mine[F];
+#pragma unroll
+        for (int i = 0; i < F; ++i) mine[i] = i * BEAM_THREADS + tid < n ? found[i * BEAM_THREADS + tid] : 0ull;
+        if (tid == 0) n_found = 0;
+        __syncthreads();
+        const unsigned long long lo = (unsigned long long)ordered(bound + 0.0f) << 32;
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+            if (mine[i] >= lo) found[atomicAdd(&n_found, 1)] = mine[i];
+        __syncthreads();
+    } else {
+        // too many reach the bound (ties, most often): the k-th largest of
+        // (logit, token) by bisection over the whole stretch, read once per round
+        auto each = [&](auto f) {
+            for (int step = 0; step < steps; ++step) {
+                load(cur, step);
+                if constexpr (MASK) {
+                    load_bits(bits, step);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) L::keep(cur[u], bits[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) f(logit_token(L::get(cur[u], j), token(step, u) + j));
+            }
+        };
+        unsigned long long lo = (unsigned long long)ordered(bound + 0.0f) << 32, hi = 0xFFFFFFFFFFFFFFFFull;
         while (lo < hi) {
-            const Key mid = lo + (hi - lo) / 2 + 1;
+            const unsigned long long mid = lo + (hi - lo) / 2 + 1;
             int c = 0;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) c += L::key(L::get(raw[u], j) + 0.0f, (u * BEAM_THREADS + tid) * VEC + j) >= mid;
+            each([&](unsigned long long v) { c += v >= mid; });
             c = block_sum(c, scratch);
             if (c >= a.k) lo = mid;
             else hi = mid - 1;
             if (c == a.k) break;
         }
+        __syncthreads();
         if (tid == 0) n_found = 0;
         __syncthreads();
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const Key c = L::key(L::get(raw[u], j) + 0.0f, (u * BEAM_THREADS + tid) * VEC + j);
-                if (c >= lo) found[atomicAdd(&n_found, 1)] = c;
-            }
+        each([&](unsigned long long v) {
+            if (v >= lo) found[atomicAdd(&n_found, 1)] = v;
+        });
         __syncthreads();
-        n = n_found;
     }
+    n = n_found;
     unsigned long long *best = a.best + list * a.kpad;
     for (int i = tid; i < n; i += BEAM_THREADS) {
-        const Key c = found[i];
+        const unsigned long long c = found[i];
         int rank = 0;
         for (int j = 0; j < n; ++j) rank += found[j] > c;
-        if (rank < a.k) {
-            const int v = first * VEC + L::place(c) - lead;
-            best[rank] = ((unsigned long long)L::value(c) << 32) | (0xFFFFFFFFu - (uint32_t)v);
-        }
+        if (rank < a.k) best[rank] = c;
     }
     for (int i = min(n, a.k) + tid; i < a.kpad; i += BEAM_THREADS) best[i] = 0ull;
 }
 
 // ---- join of one batch entry's chunks
 
-// The total order: key (64 bits), then beam, then (logit, token).
+// The total order: key, then beam, then (logit, token).
 __device__ __forceinline__ bool before(unsigned long long ka, int ra, unsigned long long la, unsigned long long kb, int rb,
                                        unsigned long long lb)
 {
     return ka != kb ? ka > kb : ra != rb ? ra < rb : la > lb;
 }
 
-__device__ __forceinline__ double key_value(unsigned long long k)
+// A number as the sum of two floats, the second what the first's rounding
+// left: 48 bits at a few additions (fp64 has a sixteenth warp instruction per
+// cycle here: the keys of one batch entry took 11 us).
+struct Pair {
+    float h, l;
+};
+// a + b, exactly.
+__device__ __forceinline__ Pair two_sum(float a, float b)
 {
-    return __longlong_as_double((long long)(k ^ ((k >> 63) ? 0x8000000000000000ull : 0xFFFFFFFFFFFFFFFFull)));
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+
+// m + log t, t > 0.  t is a power of two times a number near 1, whose logarithm
+// is small and so is its rounding; the power's logarithm is a pair.
+__device__ __forceinline__ Pair log_sum(float m, float t)
+{
+    int e = (int)(__float_as_uint(t) >> 23) - 127;  // (t is 1 or more, but for rounding)
+    float f = __uint_as_float((__float_as_uint(t) & 0x007FFFFFu) | 0x3F800000u);
+    if (f > 1.4142135f) {
+        f *= 0.5f;
+        ++e;
+    }
+    // ln 2 in two parts (as Cody and Waite do), the first of 15 bits: its multiples are exact
+    const float eh = (float)e * 0.693145751953125f, el = fmaf((float)e, 1.4286068e-6f, logf(f));
+    const Pair p = two_sum(m, eh);
+    const Pair q = two_sum(p.h, el);
+    return two_sum(q.h, q.l + p.l);
 }
 
 __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_constant__ BeamArgs a)
 {
-    __shared__ double score[BEAM_MAX_W], lse[BEAM_MAX_W];  // lse NaN: the beam has no candidates
+    __shared__ float score[BEAM_MAX_W];
+    __shared__ Pair lse[BEAM_MAX_W];  // NaN: the beam has no candidates
     __shared__ float2 part[BEAM_MAX_W];
     __shared__ unsigned long long key[BEAM_FOUND], lt[BEAM_FOUND];
     __shared__ int beam[BEAM_FOUND];
@@ -430,16 +523,36 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
     pdl_wait();
     const unsigned long long *best = a.best + (size_t)b * lists * a.kpad;
 
-    // heads of the thread's (first) list.  Neighbouring lists go to different
-    // warps, so that each warp sees every beam.
-    const int warps = min(BEAM_WARPS, (lists + 31) / 32);
-    const int mine = lane * warps + warp;
-    ulonglong2 head[2] = {make_ulonglong2(0ull, 0ull), make_ulonglong2(0ull, 0ull)};
-    if (warp < warps && mine < lists) {
-        const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(best + (size_t)mine * a.kpad);
-        head[0] = __ldcg(p);
-        head[1] = __ldcg(p + 1);
+    // Four entries of a list are a group; groups in the order of their depth,
+    // then of the list.  The first R groups of each thread stay in registers.
+    // (lane, warp) -> group: each warp sees all beams and depths.
+    constexpr int R = 4;
+    const int groups = lists * (a.kpad / 4), warps = min(BEAM_WARPS, (groups + 31) / 32);
+    const int mine = warp < warps ? lane * warps + (warp + lane + (lane >> 2)) % warps : groups;
+    struct Group {
+        unsigned long long v[4];
+        int row;
+    };
+    auto fetch = [&](int g) {
+        Group q;
+        const int l = g % lists, d = g / lists;
+        const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(best + (size_t)l * a.kpad + 4 * d);
+        const ulonglong2 x = __ldcg(p), y = __ldcg(p + 1);
+        q.v[0] = x.x;
+        q.v[1] = x.y;
+        q.v[2] = y.x;
+        q.v[3] = y.y;
+        q.row = l / a.chunks;
+        return q;
+    };
+    Group q[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int g = mine + i * 32 * warps;
+        if (g < groups) q[i] = fetch(g);
+        else q[i] = Group{{0ull, 0ull, 0ull, 0ull}, 0};
     }
+    const float own_score = tid < a.W ? __ldcg(a.scores + (size_t)b * a.W + tid) : 0.0f;
     // the rows' sums
     for (int w = warp; w < a.W; w += BEAM_WARPS) {
         const float2 *p = a.sums + ((size_t)b * a.W + w) * a.chunks;
@@ -448,97 +561,98 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
             const float2 v = __ldcg(p + c);
             const float nm = fmaxf(m, v.x);
             // (equal maxima, infinite ones too: no scaling; NaN sums stay)
-            t = (m == nm ? t : t * expf(m - nm)) + (v.x == nm ? v.y : v.y * expf(v.x - nm));
+            t = (m == nm ? t : t * __expf(m - nm)) + (v.x == nm ? v.y : v.y * __expf(v.x - nm));
             m = nm;
         }
+        float top = m;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const float om = __shfl_xor_sync(0xFFFFFFFFu, m, o), ot = __shfl_xor_sync(0xFFFFFFFFu, t, o);
-            const float nm = fmaxf(m, om);
-            t = (m == nm ? t : t * expf(m - nm)) + (om == nm ? ot : ot * expf(om - nm));
-            m = nm;
-        }
-        if (lane == 0) part[w] = make_float2(m, t);
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        t = m == top ? t : t * __expf(m - top);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+        if (lane == 0) part[w] = make_float2(top, t);
     }
     if (tid == 0) n_found = 0;
     __syncthreads();
     if (tid < a.W) {
-        const float c = __ldcg(a.scores + (size_t)b * a.W + tid);
         const float2 p = part[tid];
         // NaN sums: a NaN or +inf among the logits; nothing allowed: no maximum
-        const bool ok = p.y > 0.0f && fabsf(p.x) < INFINITY && fabsf(c) < INFINITY;
-        score[tid] = (double)c;
-        lse[tid] = ok ? (double)p.x + log((double)p.y) : (double)NAN;
+        const bool ok = p.y > 0.0f && fabsf(p.x) < INFINITY && fabsf(own_score) < INFINITY;
+        score[tid] = own_score;
+        lse[tid] = ok ? log_sum(p.x, p.y) : Pair{NAN, NAN};
     }
     __syncthreads();
 
-    // A candidate's key lies within off of fp32 arithmetic: below, above.
+    // Within `off` of a candidate's key, in fp32; NaN: no candidate.
     auto about = [&](int row, unsigned long long l, float &off) {
-        const float c = (float)score[row], s = (float)lse[row], x = unordered((uint32_t)(l >> 32));
+        const float c = score[row], s = lse[row].h, x = unordered((uint32_t)(l >> 32));
         off = (fabsf(c) + fabsf(x) + fabsf(s)) * 2.3841858e-7f;  // three roundings of a quarter of that, and one spare
-        return c + (x - s);
+        return l != 0ull ? c + (x - s) : NAN;
     };
+    // The key as a whole number in its order: both floats of the pair.
     auto exact = [&](int row, unsigned long long l) {
-        return ordered64(score[row] + ((double)unordered((uint32_t)(l >> 32)) - lse[row]));
+        const Pair d = two_sum(unordered((uint32_t)(l >> 32)), -lse[row].h);
+        const Pair k = two_sum(score[row], d.h);
+        const Pair f = two_sum(k.h, k.l + (d.l - lse[row].l));
+        return (unsigned long long)ordered(f.h + 0.0f) << 32 | ordered(f.l + 0.0f);
     };
-    // A bound that k candidates reach, from the first four of a list per lane.
-    uint32_t bound = 0u;
+    // A bound that k candidates reach, from the thread's first group.
+    uint32_t bound = 0xFFFFFFFFu;
     if (warp < warps) {
-        uint32_t low[4] = {0u, 0u, 0u, 0u};
-        const int row = mine / a.chunks;
-        if (mine < lists && lse[row] == lse[row]) {
-            const unsigned long long h[4] = {head[0].x, head[0].y, head[1].x, head[1].y};
+        uint32_t low[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (h[i] != 0ull) {
-                    float off;
-                    const float f = about(row, h[i], off);
-                    low[i] = ordered((f - off) + 0.0f);
-                }
+        for (int i = 0; i < 4; ++i) {
+            float off;
+            const float f = about(q[0].row, q[0].v[i], off);
+            low[i] = f > -INFINITY ? ordered((f - off) + 0.0f) : 0u;
         }
-        // (rounded down in fp32, the heads still descend)
-        const int r = (a.k + warps - 1) / warps;
-        bound = warp_nth(low[0], r, [&] {
+        // (rounded down in fp32, the entries still descend)
+        bound = warp_nth(low[0], (a.k + warps - 1) / warps, [&] {
             low[0] = low[1];
             low[1] = low[2];
             low[2] = low[3];
             low[3] = 0u;
             return low[0];
         });
-        if (lane == 0) warp_bound[warp] = bound;
     }
+    if (lane == 0) warp_bound[warp] = bound;
     __syncthreads();
     bound = warp_bound[0];
-    for (int w = 1; w < warps; ++w) bound = min(bound, warp_bound[w]);
-    const float least = bound == 0u ? -INFINITY : unordered(bound);
-
-    // what may reach it (its key, then)
-    for (int l = mine; warp < warps && l < lists; l += 32 * warps) {
-        const int row = l / a.chunks;
-        if (!(lse[row] == lse[row])) continue;
-        bool more = true;
-        for (int i = 0; more && i < a.kpad; i += 4) {
-            const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(best + (size_t)l * a.kpad + i);
-            const ulonglong2 v0 = l == mine && i == 0 ? head[0] : __ldcg(p), v1 = l == mine && i == 0 ? head[1] : __ldcg(p + 1);
-            const unsigned long long h[4] = {v0.x, v0.y, v1.x, v1.y};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float off = 0.0f;
-                const float f = h[j] != 0ull ? about(row, h[j], off) : 0.0f;
-                more = more && h[j] != 0ull && f + off >= least;
-                if (!more) break;
+    for (int w = 1; w < BEAM_WARPS; ++w) bound = min(bound, warp_bound[w]);
+    const float least = bound == 0u ? -FLT_MAX : unordered(bound);
+
+    // what may reach it
+    auto gather = [&](const Group &p) {
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float off;
+            const float f = about(p.row, p.v[j], off);
+            if (f + off >= least && f > -INFINITY) {
                 const int at = atomicAdd(&n_found, 1);
                 if (at < BEAM_FOUND) {
-                    key[at] = exact(row, h[j]);
-                    lt[at] = h[j];
-                    beam[at] = row;
+                    lt[at] = p.v[j];
+                    beam[at] = p.row;
                 }
+                any = true;
             }
         }
+        return any;
+    };
+#pragma unroll
+    for (int i = 0; i < R; ++i) gather(q[i]);
+    // more groups than registers: until as many in a row as there are lists
+    // have nothing (lists descend)
+    for (int g0 = R * 32 * warps, idle = 0; g0 < groups && idle < lists; g0 += BEAM_THREADS) {
+        const bool any = g0 + tid < groups && gather(fetch(g0 + tid));
+        idle = __syncthreads_or(any) ? 0 : idle + BEAM_THREADS;
     }
     __syncthreads();
     const int n = n_found;
     if (n <= BEAM_FOUND) {
+        for (int i = tid; i < n; i += BEAM_THREADS) key[i] = exact(beam[i], lt[i]);
+        __syncthreads();
         for (int i = tid; i < n; i += BEAM_THREADS) {
             const unsigned long long ki = key[i], li = lt[i];
             const int ri = beam[i];
@@ -548,7 +662,7 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
                 rank += kj > ki || (kj == ki && before(kj, beam[j], lt[j], ki, ri, li));
             }
             if (rank < a.k) {
-                out_score[rank] = (float)key_value(ki);
+                out_score[rank] = unordered((uint32_t)(ki >> 32));
                 out_parent[rank] = b * a.W + ri;
                 out_token[rank] = (int)(0xFFFFFFFFu - (uint32_t)li);
             }
@@ -568,7 +682,7 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
             int mr = 0x7FFFFFFF;
             for (int l = tid; l < lists; l += BEAM_THREADS) {
                 const int row = l / a.chunks;
-                if (!(lse[row] == lse[row])) continue;
+                if (!(lse[row].h == lse[row].h)) continue;
                 for (int e = 0; e < a.k; ++e) {
                     const unsigned long long h = __ldcg(best + (size_t)l * a.kpad + e);
                     if (h == 0ull) break;
@@ -597,7 +711,7 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
             pr = mr;
             pl = ml;
             if (tid == 0) {
-                out_score[i] = (float)key_value(mk);
+                out_score[i] = unordered((uint32_t)(mk >> 32));
                 out_parent[i] = b * a.W + mr;
                 out_token[i] = (int)(0xFFFFFFFFu - (uint32_t)ml);
             }
@@ -637,38 +751,52 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
 
 // ------------------------------------------------------------ host
 
-static int beam_chunks(int V, int vec, int unroll)
+// Stretches of a row and steps of a stretch.  Up to BEAM_RESIDENT blocks run at
+// a time; a block costs its steps and about one and a half more, so the rule
+// takes the count of stretches whose rounds of blocks cost least.
+constexpr long long BEAM_RESIDENT = 4 * 152;
+struct BeamSplit {
+    int chunks, steps;
+};
+static BeamSplit beam_split(int rows, int V, int vec)
 {
-    // a row may begin inside its first vector
-    return (V + vec - 1 + BEAM_THREADS * unroll * vec - 1) / (BEAM_THREADS * unroll * vec);
+    // (a row may begin inside its first vector)
+    const int steps = ((V + vec - 1 + vec - 1) / vec + BEAM_STEP - 1) / BEAM_STEP;
+    BeamSplit best = {1, steps};
+    long long least = -1;
+    for (int c = 1; c <= steps; ++c) {
+        const int s = (steps + c - 1) / c;
+        if ((steps + s - 1) / s != c) continue;  // (the last would be empty)
+        const long long cost = ((long long)rows * c + BEAM_RESIDENT - 1) / BEAM_RESIDENT * (2 * s + 3);
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = {c, s};
+        }
+    }
+    return best;
 }
 
-// Vectors per thread: eight, as long as the chunks still make two blocks per
-// SM; else two, so that a few rows reach more of the GPU.
-constexpr int BEAM_FEW = 304;
-static int beam_unroll(int rows, int V, int vec) { return (long long)rows * beam_chunks(V, vec, 8) >= BEAM_FEW ? 8 : 2; }
-
-static size_t beam_lists(int B, int W, int V, int vec) { return (size_t)B * W * beam_chunks(V, vec, beam_unroll(B * W, V, vec)); }
+static size_t beam_lists(int B, int W, int V, int vec) { return (size_t)B * W * beam_split(B * W, V, vec).chunks; }
 
 size_t beam_workspace_bytes(int B, int W, int V, int k)
 {
     const size_t l4 = beam_lists(B, W, V, 4), l8 = beam_lists(B, W, V, 8);  // fp32, bf16
-    return ((l4 > l8 ? l4 : l8) * (((size_t)k + 3) / 4 * 4 + 2) * 8 + 255) / 256 * 256;
+    return ((l4 > l8 ? l4 : l8) * (((size_t)k + 3) / 4 * 4 + 1) * 8 + 255) / 256 * 256;
 }
 
-template <typename E, int U>
+template <typename E>
 static cudaError_t run_beam(cudaStream_t st, const BeamArgs &a)
 {
     const dim3 grid(a.chunks, a.B * a.W);
-    const cudaError_t e = a.mask ? launch_k(beam_chunk_kernel<E, U, true>, grid, dim3(BEAM_THREADS), 0, st, a)
-                                 : launch_k(beam_chunk_kernel<E, U, false>, grid, dim3(BEAM_THREADS), 0, st, a);
+    const cudaError_t e = a.mask ? launch_k(beam_chunk_kernel<E, true>, grid, dim3(BEAM_THREADS), 0, st, a)
+                                 : launch_k(beam_chunk_kernel<E, false>, grid, dim3(BEAM_THREADS), 0, st, a);
     return e != cudaSuccess ? e : launch_k(beam_join_kernel, dim3(a.B), dim3(BEAM_THREADS), 0, st, a);
 }
 
 cudaError_t launch_beam_select(const DeviceState &, cudaStream_t st, const BeamCall &c, void *workspace)
 {
     const int vec = c.dtype == MX_F32 ? 4 : 8;
-    const int unroll = beam_unroll(c.B * c.W, c.V, vec);
+    const BeamSplit split = beam_split(c.B * c.W, c.V, vec);
     BeamArgs a;
     a.logits = c.logits;
     a.row_stride = c.row_stride;
@@ -680,7 +808,8 @@ cudaError_t launch_beam_select(const DeviceState &, cudaStream_t st, const BeamC
     a.V = c.V;
     a.k = c.k;
     a.eos = c.eos;
-    a.chunks = beam_chunks(c.V, vec, unroll);
+    a.chunks = split.chunks;
+    a.steps = split.steps;
     a.score = c.score;
     a.parent = c.parent;
     a.token = c.token;
@@ -691,8 +820,7 @@ cudaError_t launch_beam_select(const DeviceState &, cudaStream_t st, const BeamC
     a.kpad = (c.k + 3) / 4 * 4;
     a.best = static_cast<unsigned long long *>(workspace);
     a.sums = reinterpret_cast<float2 *>(a.best + lists * a.kpad);
-    if (c.dtype == MX_F32) return unroll == 8 ? run_beam<float, 8>(st, a) : run_beam<float, 2>(st, a);
-    return unroll == 8 ? run_beam<uint16_t, 8>(st, a) : run_beam<uint16_t, 2>(st, a);
+    return c.dtype == MX_F32 ? run_beam<float>(st, a) : run_beam<uint16_t>(st, a);
 }
 
 }  // namespace mx

@@ -394,8 +394,9 @@ int mx_paged_attn(const mx_paged_kv *kv, const void *q, int64_t q_token_stride, 
  * Candidates are the allowed tokens of logit above -infinity of the beams
  * whose score and sum are finite; a beam of score -infinity, one that may
  * take nothing and one with a NaN or +infinity among its allowed logits have
- * none.  They are ordered by key (exponentials and a chunk's sums fp32, the
- * rest 64 bits), then beam, then logit, then the lower token.
+ * none.  (Nor is one a candidate whose key lies beyond fp32's range.)  They are
+ * ordered by key (exponentials and their sums fp32, the rest 48 bits), then
+ * beam, then logit, then the lower token.
  *   cand_score / cand_parent / cand_token [B][k]: the first k of each entry:
  *     the key as fp32, r, v.  Places without a candidate: -infinity, -1, 0.
  *   next_score / next_parent / next_token [B][W], or all null: the first W

@@ -18,9 +18,9 @@ def beam_candidates(logits, scores, W, allowed=None):
             z = logits[r][ok]
             if not math.isfinite(scores[r]) or len(z) == 0 or np.isnan(z).any() or not math.isfinite(z.max()):
                 continue
-            lse = z.max() + math.log(np.exp(z - z.max()).sum())
+            top, log = z.max(), math.log(np.exp(z - z.max()).sum())
             for v in np.nonzero(ok & (logits[r] > -math.inf))[0]:
-                found.append((scores[r] + (logits[r][v] - lse), r, logits[r][v], int(v)))
+                found.append((scores[r] + ((logits[r][v] - top) - log), r, logits[r][v], int(v)))
         found.sort(key=lambda c: (-c[0], c[1], -c[2], c[3]))
         out.append(found)
     return out

@@ -198,19 +198,19 @@ def test_repeats_graphs_streams_and_workspaces():
     assert all(same(o, want[i]) for i, o in outs)
 
 
-def test_larger_than_the_slot():
-    """A selection whose lists do not fit the stream's 16 MiB."""
+@pytest.mark.parametrize("B,W,V,k", [(32, 32, 140000, 128), (1100, 32, 1000, 128)])
+def test_many_rows(B, W, V, k):
+    """Several stretches for each of a thousand rows; lists that do not fit the stream's 16 MiB (the second)."""
     torch = need_gpu()
     from gemm_decode_register_gb300 import ops
 
-    B, W, V, k = 32, 32, 140000, 128
-    assert ops.raw_call("mx_beam_select_workspace_size", B, W, V, k) > 16 << 20
+    assert (ops.raw_call("mx_beam_select_workspace_size", B, W, V, k) > 16 << 20) == (B == 1100)
     g = torch.Generator(device="cuda").manual_seed(9)
     x = torch.randn((B * W, V), generator=g, device="cuda", dtype=torch.bfloat16)
     c = torch.randn((B, W), generator=g, device="cuda")
     got = ops.beam_select(x, c, k)
     lse = torch.logsumexp(x.double(), 1)
-    for b in (0, 13, 31):
+    for b in (0, 13, B - 1):
         key = (c[b].double()[:, None] + x[b * W:(b + 1) * W].double() - lse[b * W:(b + 1) * W, None]).flatten()
         top = key.sort(descending=True, stable=True)
         assert torch.allclose(got.score[b].double(), top.values[:k], rtol=0, atol=OFF + 32 * 2.0 ** -24)
