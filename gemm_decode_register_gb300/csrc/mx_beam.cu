@@ -5,30 +5,33 @@
 // over the tokens v that row r's mask allows; the k largest of a batch
 // entry's W rows (bound: HBM, one pass over the logits).
 //
-// Two launches.  beam_chunk_kernel: a block takes a stretch of one row and
-// walks it in steps of four 16-byte vectors per thread, the next step's loads in
-// flight.  Within a row the order of the keys is that of the logits, so a
-// stretch needs no more of its row than itself:
+// One launch.  The rows, laid end to end in steps of four
+// 16-byte vectors per thread, are cut into equal stretches, one for each
+// block that fits on the GPU; a block walks its own with the next step's loads
+// in flight, over row ends too.  Within a row the order of the keys is that
+// of the logits, so a row's part of a stretch (a piece) needs no more of its row
+// than itself:
 //   - the largest element of each vector (packed maxima) and thread.  In the
 //     first step each warp finds the r-th largest of its lanes' by r warp-wide
 //     maxima; with r times the warps at least k, the smallest of these is a
 //     bound that k elements reach, and not many more do;
 //   - vectors that reach the bound go to a queue in shared memory.  When it
-//     fills, and after 2, 4, 8, .. steps, a few threads take their elements
+//     fills, and after 2, 8, 32, .. steps, a few threads take their elements
 //     apart and the bound rises in the same way by what is found so far: so
-//     each doubling adds about k elements.  (A bisection to the k-th best cost
+//     each such stretch adds a few times k elements.  (A bisection to the k-th best cost
 //     3 us each time, this 0.3.)  Rows whose later steps keep bringing better
 //     elements get a bound from the step at hand too;
 //   - exponentials are summed over the thread's own reference, a maximum that
 //     is raised only when it falls behind by more than 10.
 // At the end each element found counts those before it: its rank.
-// beam_join_kernel: a block takes a batch entry: the rows' sums, the same
-// bound from the heads of the stretches' lists (in fp32, with what its rounding may
-// be off on either side), and the ranks of those that reach it by keys of 48
-// bits: near ties between beams are decided by bits that fp32 scores of -20
-// do not have.  It is launched while the stretches run and waits for them.
+// The last block to finish a piece of a batch entry (a counter) joins its
+// pieces: the rows' sums, the same bound from the heads of the pieces' lists (in fp32,
+// with what its rounding may be off on either side), and the ranks of
+// those that reach it by keys of 48 bits: near ties between beams are decided
+// by bits that fp32 scores of -20 do not have.  Nothing depends on the order in
+// which blocks finish.
 // Where ties let more elements reach a bound than the shared memory holds,
-// both kernels go slower ways to the same result.
+// both go slower ways to the same result.
 #include <cfloat>
 #include <cmath>
 
@@ -42,8 +45,8 @@ constexpr int BEAM_THREADS = 256;
 constexpr int BEAM_WARPS = BEAM_THREADS / 32;
 constexpr int BEAM_U = 4;                      // vectors of a thread and step
 constexpr int BEAM_STEP = BEAM_THREADS * BEAM_U;  // vectors of a step
-constexpr int BEAM_QUEUE = 512;   // vectors that reach a stretch's bound
-constexpr int BEAM_FOUND = 1024;  // elements that do (a stretch's, a batch entry's)
+constexpr int BEAM_QUEUE = 512;   // vectors that reach a piece's bound
+constexpr int BEAM_FOUND = 1024;  // elements that do (a piece's, a batch entry's)
 
 struct BeamArgs {
     const void *logits;
@@ -52,12 +55,13 @@ struct BeamArgs {
     const uint32_t *mask;
     long long mask_stride;
     int B, W, V, k, eos;
-    int chunks, steps;  // stretches of a row, steps of a stretch
+    int steps, span, pieces;  // steps of a row and of a stretch; most pieces of a row
     float *score, *next_score;
     int32_t *parent, *token, *next_parent, *next_token;
-    float2 *sums;              // [rows][chunks] maximum and sum
-    unsigned long long *best;  // [rows][chunks][kpad] (logit, token) in order, 0 past the last
+    float2 *sums;              // [rows][pieces] reference and sum
+    unsigned long long *best;  // [rows][pieces][kpad] (logit, token) in order, 0 past the last
     int kpad;                  // k rounded up to 4
+    int *count;                // [B] pieces that are done, zero between calls
 };
 
 // Whole numbers in the order of the values: -inf is 0x007FFFFF, +inf the
@@ -71,6 +75,13 @@ __device__ __forceinline__ float unordered(uint32_t o)
 {
     return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
+// The first stretch with a step of a row, and how many there are.
+__device__ __forceinline__ int first_stretch(const BeamArgs &a, int row) { return (int)((long long)row * a.steps / a.span); }
+__device__ __forceinline__ int pieces_of(const BeamArgs &a, int row)
+{
+    return (int)(((long long)(row + 1) * a.steps - 1) / a.span) - first_stretch(a, row) + 1;
+}
+
 constexpr uint32_t ORD_NEG_INF = 0x007FFFFFu;
 
 // (logit, token) as one whole number: larger logits first, the two zeros
@@ -208,267 +219,7 @@ __device__ __noinline__ uint4 edge_vector(const float *p, int lo, int hi)
     return v;
 }
 
-// ---- chunks
-
-// Mask bits of the VEC elements from element e on (may be negative or past
-// V: those bits do not count, their elements are -inf already).
-template <int VEC>
-__device__ __forceinline__ uint32_t mask_bits(const uint32_t *row, int e, int words)
-{
-    if (e < 0) return mask_bits<VEC>(row, 0, words) << (-e);
-    const int w = e >> 5;
-    uint32_t lo = w < words ? __ldg(row + w) : 0u;
-    const int s = e & 31;
-    if (s + VEC > 32) {
-        const uint32_t hi = w + 1 < words ? __ldg(row + w + 1) : 0u;
-        return __funnelshift_r(lo, hi, s);
-    }
-    return lo >> s;
-}
-
-template <typename E, bool MASK>
-__global__ void __launch_bounds__(BEAM_THREADS, MASK ? 3 : 4) beam_chunk_kernel(const __grid_constant__ BeamArgs a)
-{
-    using L = Elem<E>;
-    constexpr int VEC = L::VEC, U = BEAM_U;
-    __shared__ uint4 queue[BEAM_QUEUE];
-    __shared__ int queue_at[BEAM_QUEUE];  // the vector's first token
-    __shared__ unsigned long long found[BEAM_FOUND];
-    __shared__ float warp_ref[BEAM_WARPS], warp_sum[BEAM_WARPS];
-    __shared__ uint32_t warp_bound[BEAM_WARPS];
-    __shared__ int n_queue, n_found, scratch[BEAM_WARPS];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-    const int chunk = blockIdx.x, row = blockIdx.y;
-    if (tid == 0) n_queue = n_found = 0;
-    pdl_trigger();
-    pdl_wait();
-    const E *x = static_cast<const E *>(a.logits) + (size_t)row * a.row_stride;
-    const uint32_t *mask = MASK ? a.mask + (size_t)row * a.mask_stride : nullptr;
-    // vectors of the row counted from the 16-byte boundary at or before it;
-    // one that the row only partly covers is read element by element
-    const int lead = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(E));
-    const int begin = chunk * a.steps * BEAM_STEP, words = (a.V + 31) >> 5;
-    const int steps = min(a.steps, ((lead + a.V + VEC - 1) / VEC - begin + BEAM_STEP - 1) / BEAM_STEP);
-    auto token = [&](int step, int u) { return (begin + step * BEAM_STEP + u * BEAM_THREADS + tid) * VEC - lead; };
-    auto load = [&](uint4 (&v)[U], int step) {
-        const int e0 = (begin + step * BEAM_STEP) * VEC - lead;
-        if (e0 >= 0 && e0 + BEAM_STEP * VEC <= a.V) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(x + e0) + tid;
-#pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = __ldcs(p + u * BEAM_THREADS);
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int e = token(step, u);
-                if (e >= 0 && e + VEC <= a.V) v[u] = __ldcs(reinterpret_cast<const uint4 *>(x + e));
-                else v[u] = edge_vector(x + e, e < 0 ? -e : 0, min(VEC, a.V - e));
-            }
-        }
-    };
-    auto load_bits = [&](uint32_t (&bits)[U], int step) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) bits[u] = mask_bits<VEC>(mask, token(step, u), words);
-    };
-
-    float bound = -FLT_MAX;  // (-inf is no candidate)
-    // raises it to what k of the threads' values reach, of which the first
-    // `have` threads have one: r lanes of each of their warps.  Two barriers.
-    auto raise = [&](float v, int have) {
-        const int warps = max(1, min(BEAM_WARPS, (have + 31) / 32)), r = (a.k + warps - 1) / warps;
-        uint32_t n = 0xFFFFFFFFu;  // (no values, no say)
-        if (warp < warps) n = r > 32 ? 0u : warp_nth(ordered(v + 0.0f), r, [] { return 0u; });
-        if (lane == 0) warp_bound[warp] = n;
-        __syncthreads();
-        n = warp_bound[0];
-#pragma unroll
-        for (int w = 1; w < BEAM_WARPS; ++w) n = min(n, warp_bound[w]);
-        if (n > ORD_NEG_INF) bound = fmaxf(bound, unordered(n));
-        __syncthreads();
-    };
-    // the queue's elements that reach the bound are found; the queue is empty after it
-    auto drain = [&] {
-        const int n = min(n_queue, BEAM_QUEUE);
-        for (int i = tid; i < n; i += BEAM_THREADS) {
-            const uint4 v = queue[i];
-            const int at = queue_at[i];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float f = L::get(v, j);
-                if (f >= bound) {
-                    const int o = atomicAdd(&n_found, 1);
-                    if (o < BEAM_FOUND) found[o] = logit_token(f, at + j);
-                }
-            }
-        }
-        __syncthreads();
-        if (tid == 0) n_queue = 0;
-    };
-    // the bound from what is found so far: each thread's largest of up to four
-    auto raise_by_found = [&] {
-        const int n = n_found;
-        uint32_t v = 0u;
-        for (int i = tid; i < n; i += BEAM_THREADS) v = max(v, (uint32_t)(found[i] >> 32));
-        raise(v > ORD_NEG_INF ? unordered(v) : -INFINITY, n);
-    };
-
-    uint4 cur[U], nxt[U];
-    uint32_t bits[U], nbits[U];
-    load(cur, 0);
-    if constexpr (MASK) load_bits(bits, 0);
-    float ref = -INFINITY;
-    float2 sum2 = make_float2(0.0f, 0.0f);
-    bool hot = true, lost = false;
-    for (int step = 0; step < steps; ++step) {
-        if (step + 1 < steps) {
-            load(nxt, step + 1);
-            if constexpr (MASK) load_bits(nbits, step + 1);
-        }
-        if constexpr (MASK) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) L::keep(cur[u], bits[u]);
-        }
-        float top[U], m = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            top[u] = L::top(cur[u]);
-            m = fmaxf(m, top[u]);
-        }
-        if (hot) raise(m, (lead + a.V + VEC - 1) / VEC - begin - step * BEAM_STEP);
-        bool filling = false;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (top[u] >= bound) {
-                const int i = atomicAdd(&n_queue, 1);
-                filling |= i >= BEAM_QUEUE / 2;
-                if (i < BEAM_QUEUE) {
-                    queue[i] = cur[u];
-                    queue_at[i] = token(step, u);
-                }
-            }
-        if (m > ref + 10.0f) {  // (the first time too)
-            const float s = ref > -INFINITY ? __expf(ref - m) : 1.0f;
-            sum2.x *= s;
-            sum2.y *= s;
-            ref = m;
-        }
-        // (x - reference before the factor: its rounding stays relative to the difference)
-        const float off = ref > -INFINITY ? -ref : 0.0f;
-        const float2 shift = make_float2(off, off), log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < VEC; j += 2) {
-                const float2 d = mul2(add2(make_float2(L::get(cur[u], j), L::get(cur[u], j + 1)), shift), log2e);
-                sum2 = add2(sum2, make_float2(exp2_fast(d.x), exp2_fast(d.y)));
-            }
-        if (step + 1 < steps) {
-            hot = __syncthreads_or(filling);  // (n_queue itself may have grown by another's next step)
-            if (hot || (step > 0 && (step & (step + 1)) == 0)) {
-                __syncthreads();
-                lost |= n_queue > BEAM_QUEUE;
-                __syncthreads();
-                drain();
-                lost |= n_found > BEAM_FOUND;
-                __syncthreads();
-                if (!lost) raise_by_found();
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) cur[u] = nxt[u];
-            if constexpr (MASK) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) bits[u] = nbits[u];
-            }
-        }
-    }
-    // the sums, over the largest reference
-    {
-        float wr = ref, ws = sum2.x + sum2.y;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) wr = fmaxf(wr, __shfl_xor_sync(0xFFFFFFFFu, wr, o));
-        ws = ref == wr ? ws : ws * __expf(ref - wr);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) ws += __shfl_xor_sync(0xFFFFFFFFu, ws, o);
-        if (lane == 0) {
-            warp_ref[warp] = wr;
-            warp_sum[warp] = ws;
-        }
-    }
-    __syncthreads();
-    const size_t list = (size_t)row * a.chunks + chunk;
-    if (tid == 0) {
-        float r = -INFINITY, s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < BEAM_WARPS; ++w) r = fmaxf(r, warp_ref[w]);
-#pragma unroll
-        for (int w = 0; w < BEAM_WARPS; ++w) s += warp_ref[w] == r ? warp_sum[w] : warp_sum[w] * __expf(warp_ref[w] - r);
-        a.sums[list] = make_float2(r, s);
-    }
-    lost |= n_queue > BEAM_QUEUE;
-    drain();
-    lost |= n_found > BEAM_FOUND;
-    __syncthreads();
-    int n = n_found;
-    if (!lost) {
-        raise_by_found();
-        // what no longer reaches the bound is dropped
-        constexpr int F = BEAM_FOUND / BEAM_THREADS;
-        unsigned long long mine[F];
-#pragma unroll
-        for (int i = 0; i < F; ++i) mine[i] = i * BEAM_THREADS + tid < n ? found[i * BEAM_THREADS + tid] : 0ull;
-        if (tid == 0) n_found = 0;
-        __syncthreads();
-        const unsigned long long lo = (unsigned long long)ordered(bound + 0.0f) << 32;
-#pragma unroll
-        for (int i = 0; i < F; ++i)
-            if (mine[i] >= lo) found[atomicAdd(&n_found, 1)] = mine[i];
-        __syncthreads();
-    } else {
-        // too many reach the bound (ties, most often): the k-th largest of
-        // (logit, token) by bisection over the whole stretch, read once per round
-        auto each = [&](auto f) {
-            for (int step = 0; step < steps; ++step) {
-                load(cur, step);
-                if constexpr (MASK) {
-                    load_bits(bits, step);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) L::keep(cur[u], bits[u]);
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) f(logit_token(L::get(cur[u], j), token(step, u) + j));
-            }
-        };
-        unsigned long long lo = (unsigned long long)ordered(bound + 0.0f) << 32, hi = 0xFFFFFFFFFFFFFFFFull;
-        while (lo < hi) {
-            const unsigned long long mid = lo + (hi - lo) / 2 + 1;
-            int c = 0;
-            each([&](unsigned long long v) { c += v >= mid; });
-            c = block_sum(c, scratch);
-            if (c >= a.k) lo = mid;
-            else hi = mid - 1;
-            if (c == a.k) break;
-        }
-        __syncthreads();
-        if (tid == 0) n_found = 0;
-        __syncthreads();
-        each([&](unsigned long long v) {
-            if (v >= lo) found[atomicAdd(&n_found, 1)] = v;
-        });
-        __syncthreads();
-    }
-    n = n_found;
-    unsigned long long *best = a.best + list * a.kpad;
-    for (int i = tid; i < n; i += BEAM_THREADS) {
-        const unsigned long long c = found[i];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += found[j] > c;
-        if (rank < a.k) best[rank] = c;
-    }
-    for (int i = min(n, a.k) + tid; i < a.kpad; i += BEAM_THREADS) best[i] = 0ull;
-}
-
-// ---- join of one batch entry's chunks
+// ---- join of one batch entry's pieces
 
 // The total order: key, then beam, then (logit, token).
 __device__ __forceinline__ bool before(unsigned long long ka, int ra, unsigned long long la, unsigned long long kb, int rb,
@@ -507,26 +258,32 @@ __device__ __forceinline__ Pair log_sum(float m, float t)
     return two_sum(q.h, q.l + p.l);
 }
 
-__global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_constant__ BeamArgs a)
+struct JoinSmem {
+    float score[BEAM_MAX_W];
+    Pair lse[BEAM_MAX_W];  // NaN: the beam has no candidates
+    float2 part[BEAM_MAX_W];
+    unsigned long long key[BEAM_FOUND], lt[BEAM_FOUND];
+    uint8_t beam[BEAM_FOUND];
+    uint32_t warp_bound[BEAM_WARPS];
+    float out_score[BEAM_MAX_K];
+    int out_parent[BEAM_MAX_K], out_token[BEAM_MAX_K], n_found;
+};
+
+__device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b)
 {
-    __shared__ float score[BEAM_MAX_W];
-    __shared__ Pair lse[BEAM_MAX_W];  // NaN: the beam has no candidates
-    __shared__ float2 part[BEAM_MAX_W];
-    __shared__ unsigned long long key[BEAM_FOUND], lt[BEAM_FOUND];
-    __shared__ int beam[BEAM_FOUND];
-    __shared__ uint32_t warp_bound[BEAM_WARPS];
-    __shared__ float out_score[BEAM_MAX_K];
-    __shared__ int out_parent[BEAM_MAX_K], out_token[BEAM_MAX_K], n_found;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x, b = blockIdx.x;
-    const int lists = a.W * a.chunks;
-    pdl_trigger();
-    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int lists = a.W * a.pieces;
     const unsigned long long *best = a.best + (size_t)b * lists * a.kpad;
+    float *score = sm.score, *out_score = sm.out_score;
+    Pair *lse = sm.lse;
+    unsigned long long *key = sm.key, *lt = sm.lt;
+    uint8_t *beam = sm.beam;
+    int *out_parent = sm.out_parent, *out_token = sm.out_token;
 
     // Four entries of a list are a group; groups in the order of their depth,
     // then of the list.  The first R groups of each thread stay in registers.
     // (lane, warp) -> group: each warp sees all beams and depths.
-    constexpr int R = 4;
+    constexpr int R = 3;
     const int groups = lists * (a.kpad / 4), warps = min(BEAM_WARPS, (groups + 31) / 32);
     const int mine = warp < warps ? lane * warps + (warp + lane + (lane >> 2)) % warps : groups;
     struct Group {
@@ -536,13 +293,17 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
     auto fetch = [&](int g) {
         Group q;
         const int l = g % lists, d = g / lists;
+        q.row = l / a.pieces;
+        if (l - q.row * a.pieces >= pieces_of(a, b * a.W + q.row)) {
+            q.v[0] = q.v[1] = q.v[2] = q.v[3] = 0ull;
+            return q;
+        }
         const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(best + (size_t)l * a.kpad + 4 * d);
         const ulonglong2 x = __ldcg(p), y = __ldcg(p + 1);
         q.v[0] = x.x;
         q.v[1] = x.y;
         q.v[2] = y.x;
         q.v[3] = y.y;
-        q.row = l / a.chunks;
         return q;
     };
     Group q[R];
@@ -555,9 +316,10 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
     const float own_score = tid < a.W ? __ldcg(a.scores + (size_t)b * a.W + tid) : 0.0f;
     // the rows' sums
     for (int w = warp; w < a.W; w += BEAM_WARPS) {
-        const float2 *p = a.sums + ((size_t)b * a.W + w) * a.chunks;
+        const float2 *p = a.sums + ((size_t)b * a.W + w) * a.pieces;
+        const int pieces = pieces_of(a, b * a.W + w);
         float m = -INFINITY, t = 0.0f;
-        for (int c = lane; c < a.chunks; c += 32) {
+        for (int c = lane; c < pieces; c += 32) {
             const float2 v = __ldcg(p + c);
             const float nm = fmaxf(m, v.x);
             // (equal maxima, infinite ones too: no scaling; NaN sums stay)
@@ -570,12 +332,12 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
         t = m == top ? t : t * __expf(m - top);
 #pragma unroll
         for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-        if (lane == 0) part[w] = make_float2(top, t);
+        if (lane == 0) sm.part[w] = make_float2(top, t);
     }
-    if (tid == 0) n_found = 0;
+    if (tid == 0) sm.n_found = 0;
     __syncthreads();
     if (tid < a.W) {
-        const float2 p = part[tid];
+        const float2 p = sm.part[tid];
         // NaN sums: a NaN or +inf among the logits; nothing allowed: no maximum
         const bool ok = p.y > 0.0f && fabsf(p.x) < INFINITY && fabsf(own_score) < INFINITY;
         score[tid] = own_score;
@@ -615,11 +377,9 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
             return low[0];
         });
     }
-    if (lane == 0) warp_bound[warp] = bound;
+    if (lane == 0) sm.warp_bound[warp] = bound;
     __syncthreads();
-    bound = warp_bound[0];
-#pragma unroll
-    for (int w = 1; w < BEAM_WARPS; ++w) bound = min(bound, warp_bound[w]);
+    bound = __reduce_min_sync(0xFFFFFFFFu, sm.warp_bound[lane % BEAM_WARPS]);
     const float least = bound == 0u ? -FLT_MAX : unordered(bound);
 
     // what may reach it
@@ -630,10 +390,10 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
             float off;
             const float f = about(p.row, p.v[j], off);
             if (f + off >= least && f > -INFINITY) {
-                const int at = atomicAdd(&n_found, 1);
+                const int at = atomicAdd(&sm.n_found, 1);
                 if (at < BEAM_FOUND) {
                     lt[at] = p.v[j];
-                    beam[at] = p.row;
+                    beam[at] = (uint8_t)p.row;
                 }
                 any = true;
             }
@@ -649,7 +409,7 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
         idle = __syncthreads_or(any) ? 0 : idle + BEAM_THREADS;
     }
     __syncthreads();
-    const int n = n_found;
+    const int n = sm.n_found;
     if (n <= BEAM_FOUND) {
         for (int i = tid; i < n; i += BEAM_THREADS) key[i] = exact(beam[i], lt[i]);
         __syncthreads();
@@ -681,8 +441,8 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
             unsigned long long mk = 0ull, ml = 0ull;
             int mr = 0x7FFFFFFF;
             for (int l = tid; l < lists; l += BEAM_THREADS) {
-                const int row = l / a.chunks;
-                if (!(lse[row].h == lse[row].h)) continue;
+                const int row = l / a.pieces;
+                if (!(lse[row].h == lse[row].h) || l - row * a.pieces >= pieces_of(a, b * a.W + row)) continue;
                 for (int e = 0; e < a.k; ++e) {
                     const unsigned long long h = __ldcg(best + (size_t)l * a.kpad + e);
                     if (h == 0ull) break;
@@ -699,7 +459,7 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
             __syncthreads();
             key[tid] = mk;
             lt[tid] = ml;
-            beam[tid] = mr;
+            beam[tid] = (uint8_t)(mr & 255);
             __syncthreads();
             for (int j = 0; j < BEAM_THREADS; ++j)
                 if (before(key[j], beam[j], lt[j], mk, mr, ml)) {
@@ -749,34 +509,344 @@ __global__ void __launch_bounds__(BEAM_THREADS) beam_join_kernel(const __grid_co
     }
 }
 
-// ------------------------------------------------------------ host
+// ---- pieces
 
-// Stretches of a row and steps of a stretch.  Up to BEAM_RESIDENT blocks run at
-// a time; a block costs its steps and about one and a half more, so the rule
-// takes the count of stretches whose rounds of blocks cost least.
-constexpr long long BEAM_RESIDENT = 4 * 152;
-struct BeamSplit {
-    int chunks, steps;
-};
-static BeamSplit beam_split(int rows, int V, int vec)
+// Mask bits of the VEC elements from element e on (may be negative or past
+// V: those bits do not count, their elements are -inf already).
+template <int VEC>
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t *row, int e, int words)
 {
-    // (a row may begin inside its first vector)
-    const int steps = ((V + vec - 1 + vec - 1) / vec + BEAM_STEP - 1) / BEAM_STEP;
-    BeamSplit best = {1, steps};
-    long long least = -1;
-    for (int c = 1; c <= steps; ++c) {
-        const int s = (steps + c - 1) / c;
-        if ((steps + s - 1) / s != c) continue;  // (the last would be empty)
-        const long long cost = ((long long)rows * c + BEAM_RESIDENT - 1) / BEAM_RESIDENT * (2 * s + 3);
-        if (least < 0 || cost < least) {
-            least = cost;
-            best = {c, s};
-        }
+    if (e < 0) return mask_bits<VEC>(row, 0, words) << (-e);
+    const int w = e >> 5;
+    uint32_t lo = w < words ? __ldg(row + w) : 0u;
+    const int s = e & 31;
+    if (s + VEC > 32) {
+        const uint32_t hi = w + 1 < words ? __ldg(row + w + 1) : 0u;
+        return __funnelshift_r(lo, hi, s);
     }
-    return best;
+    return lo >> s;
 }
 
-static size_t beam_lists(int B, int W, int V, int vec) { return (size_t)B * W * beam_split(B * W, V, vec).chunks; }
+struct ChunkSmem {
+    uint4 queue[BEAM_QUEUE];
+    int queue_at[BEAM_QUEUE];  // the vector's first token
+    unsigned long long found[BEAM_FOUND];
+};
+
+template <typename E, bool MASK>
+__global__ void __launch_bounds__(BEAM_THREADS, MASK ? 2 : 4) beam_kernel(const __grid_constant__ BeamArgs a)
+{
+    using L = Elem<E>;
+    constexpr int VEC = L::VEC, U = BEAM_U;
+    __shared__ __align__(16) uint8_t smem[sizeof(ChunkSmem) > sizeof(JoinSmem) ? sizeof(ChunkSmem) : sizeof(JoinSmem)];
+    uint4 *queue = reinterpret_cast<ChunkSmem *>(smem)->queue;
+    int *queue_at = reinterpret_cast<ChunkSmem *>(smem)->queue_at;
+    unsigned long long *found = reinterpret_cast<ChunkSmem *>(smem)->found;
+    __shared__ float warp_ref[BEAM_WARPS], warp_sum[BEAM_WARPS];
+    __shared__ uint32_t warp_bound[BEAM_WARPS];
+    __shared__ int n_queue, n_found, joins, scratch[BEAM_WARPS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    if (tid == 0) n_queue = n_found = 0;
+    pdl_trigger();
+    pdl_wait();
+    const int words = (a.V + 31) >> 5;
+    // a row, and the first token of its step 0: vectors are counted from the
+    // 16-byte boundary at or before the row, and one that the row only partly
+    // covers is read element by element
+    struct Row {
+        const E *x;
+        int token0;
+    };
+    auto row_at = [&](int row) {
+        const E *x = static_cast<const E *>(a.logits) + (size_t)row * a.row_stride;
+        return Row{x, -(int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(E))};
+    };
+    auto load = [&](uint4 (&v)[U], const Row &r, int e0) {  // the step whose first token is e0
+        if (e0 >= 0 && e0 + BEAM_STEP * VEC <= a.V) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(r.x + e0) + tid;
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = __ldcs(p + u * BEAM_THREADS);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int e = e0 + (u * BEAM_THREADS + tid) * VEC;
+                if (e >= 0 && e + VEC <= a.V) v[u] = __ldcs(reinterpret_cast<const uint4 *>(r.x + e));
+                else v[u] = edge_vector(r.x + e, e < 0 ? -e : 0, min(VEC, a.V - e));
+            }
+        }
+    };
+    auto load_bits = [&](uint32_t (&bits)[U], int row, int e0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            bits[u] = mask_bits<VEC>(a.mask + (size_t)row * a.mask_stride, e0 + (u * BEAM_THREADS + tid) * VEC, words);
+    };
+
+    float bound = -FLT_MAX;  // (-inf is no candidate)
+    // raises it to what k of the threads' values reach, of which the first
+    // `have` threads have one: r lanes of each of their warps.  Two barriers.
+    auto raise = [&](float v, int have) {
+        const int warps = max(1, min(BEAM_WARPS, (have + 31) / 32)), r = (a.k + warps - 1) / warps;
+        uint32_t n = 0xFFFFFFFFu;  // (no values, no say)
+        if (warp < warps) n = r > 32 ? 0u : warp_nth(ordered(v + 0.0f), r, [] { return 0u; });
+        if (lane == 0) warp_bound[warp] = n;
+        __syncthreads();
+        n = __reduce_min_sync(0xFFFFFFFFu, warp_bound[lane % BEAM_WARPS]);
+        if (n > ORD_NEG_INF) bound = fmaxf(bound, unordered(n));
+        __syncthreads();
+    };
+    // the queue's elements that reach the bound are found; the queue is empty after it
+    auto drain = [&] {
+        const int n = min(n_queue, BEAM_QUEUE);
+        for (int i = tid; i < n; i += BEAM_THREADS) {
+            const uint4 v = queue[i];
+            const int at = queue_at[i];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float f = L::get(v, j);
+                if (f >= bound) {
+                    const int o = atomicAdd(&n_found, 1);
+                    if (o < BEAM_FOUND) found[o] = logit_token(f, at + j);
+                }
+            }
+        }
+        __syncthreads();
+        if (tid == 0) n_queue = 0;
+    };
+    // the bound from what is found so far: each thread's largest of up to four
+    auto raise_by_found = [&] {
+        const int n = n_found;
+        uint32_t v = 0u;
+        for (int i = tid; i < n; i += BEAM_THREADS) v = max(v, (uint32_t)(found[i] >> 32));
+        raise(v > ORD_NEG_INF ? unordered(v) : -INFINITY, n);
+    };
+
+    const long long end = min((long long)(blockIdx.x + 1) * a.span, (long long)a.B * a.W * a.steps);
+    long long at = (long long)blockIdx.x * a.span;
+    int row = (int)(at / a.steps), step = (int)(at - (long long)row * a.steps), first = step;
+    Row r = row_at(row);
+    int token0 = r.token0 + step * BEAM_STEP * VEC;
+    uint4 cur[U], nxt[U];
+    uint32_t bits[U], nbits[U];
+    load(cur, r, token0);
+    if constexpr (MASK) load_bits(bits, row, token0);
+    float ref = -INFINITY;
+    float2 sum2 = make_float2(0.0f, 0.0f);
+    bool hot = true, lost = false;
+    for (; at < end; ++at) {
+        const bool row_ends = step + 1 == a.steps, last = row_ends || at + 1 == end;  // of the piece
+        const Row here = r;
+        int ntoken0 = token0 + BEAM_STEP * VEC;
+        if (at + 1 < end) {
+            if (row_ends) {
+                r = row_at(row + 1);
+                ntoken0 = r.token0;
+            }
+            load(nxt, r, ntoken0);
+            if constexpr (MASK) load_bits(nbits, row + row_ends, ntoken0);
+        }
+        if constexpr (MASK) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) L::keep(cur[u], bits[u]);
+        }
+        float top[U], m = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            top[u] = L::top(cur[u]);
+            m = fmaxf(m, top[u]);
+        }
+        if (hot) raise(m, (a.V - token0 + VEC - 1) / VEC);
+        bool filling = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (top[u] >= bound) {
+                const int i = atomicAdd(&n_queue, 1);
+                filling |= i >= BEAM_QUEUE / 2;
+                if (i < BEAM_QUEUE) {
+                    queue[i] = cur[u];
+                    queue_at[i] = token0 + (u * BEAM_THREADS + tid) * VEC;
+                }
+            }
+        if (m > ref + 10.0f) {  // (the first time too)
+            const float s = ref > -INFINITY ? __expf(ref - m) : 1.0f;
+            sum2.x *= s;
+            sum2.y *= s;
+            ref = m;
+        }
+        // (x - reference before the factor: its rounding stays relative to the
+        // difference, whatever the size of x)
+        const float off = ref > -INFINITY ? -ref : 0.0f;
+        const float2 shift = make_float2(off, off), log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < VEC; j += 2) {
+                const float2 d = mul2(add2(make_float2(L::get(cur[u], j), L::get(cur[u], j + 1)), shift), log2e);
+                sum2 = add2(sum2, make_float2(exp2_fast(d.x), exp2_fast(d.y)));
+            }
+        if (!last) {
+            hot = __syncthreads_or(filling);  // (n_queue itself may have grown by another's next step)
+            const int done = step - first + 1;
+            // (2, 8, 32, .. steps; for many candidates every power of two)
+            if (hot || ((done & (done - 1)) == 0 && (done & (a.k > 48 ? ~1 : 0x2AAAAAAA)) != 0)) {
+                lost |= n_queue > BEAM_QUEUE;
+                __syncthreads();
+                drain();
+                lost |= n_found > BEAM_FOUND;
+                __syncthreads();
+                if (!lost) raise_by_found();
+            }
+        } else {
+            // ---- the piece ends: its sums, over the largest reference
+            float wr = ref, ws = sum2.x + sum2.y;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) wr = fmaxf(wr, __shfl_xor_sync(0xFFFFFFFFu, wr, o));
+            ws = ref == wr ? ws : ws * __expf(ref - wr);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) ws += __shfl_xor_sync(0xFFFFFFFFu, ws, o);
+            if (lane == 0) {
+                warp_ref[warp] = wr;
+                warp_sum[warp] = ws;
+            }
+            __syncthreads();
+            const size_t list = (size_t)row * a.pieces + (blockIdx.x - first_stretch(a, row));
+            if (warp == 0) {
+                const float wr8 = warp_ref[lane % BEAM_WARPS];
+                float top = wr8, s = lane < BEAM_WARPS ? warp_sum[lane] : 0.0f;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                s = wr8 == top ? s : s * __expf(wr8 - top);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+                if (lane == 0) a.sums[list] = make_float2(top, s);
+            }
+            lost |= n_queue > BEAM_QUEUE;
+            __syncthreads();
+            drain();
+            lost |= n_found > BEAM_FOUND;
+            __syncthreads();
+            if (!lost) {
+                const int n = n_found;
+                raise_by_found();
+                // what no longer reaches the bound is dropped
+                constexpr int F = BEAM_FOUND / BEAM_THREADS;
+                unsigned long long mine[F];
+#pragma unroll
+                for (int i = 0; i < F; ++i) mine[i] = i * BEAM_THREADS + tid < n ? found[i * BEAM_THREADS + tid] : 0ull;
+                if (tid == 0) n_found = 0;
+                __syncthreads();
+                const unsigned long long lo = (unsigned long long)ordered(bound + 0.0f) << 32;
+#pragma unroll
+                for (int i = 0; i < F; ++i)
+                    if (mine[i] >= lo) found[atomicAdd(&n_found, 1)] = mine[i];
+            } else {
+                // too many reach the bound (ties, most often): the k-th largest of
+                // (logit, token) by bisection over the whole piece, read once per round
+                auto each = [&](auto f) {
+                    for (int s = first; s <= step; ++s) {
+                        const int e0 = here.token0 + s * BEAM_STEP * VEC;
+                        load(cur, here, e0);
+                        if constexpr (MASK) {
+                            load_bits(bits, row, e0);
+#pragma unroll
+                            for (int u = 0; u < U; ++u) L::keep(cur[u], bits[u]);
+                        }
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int j = 0; j < VEC; ++j)
+                                f(logit_token(L::get(cur[u], j), e0 + (u * BEAM_THREADS + tid) * VEC + j));
+                    }
+                };
+                unsigned long long lo = (unsigned long long)ordered(bound + 0.0f) << 32, hi = 0xFFFFFFFFFFFFFFFFull;
+                while (lo < hi) {
+                    const unsigned long long mid = lo + (hi - lo) / 2 + 1;
+                    int c = 0;
+                    each([&](unsigned long long v) { c += v >= mid; });
+                    c = block_sum(c, scratch);
+                    if (c >= a.k) lo = mid;
+                    else hi = mid - 1;
+                    if (c == a.k) break;
+                }
+                __syncthreads();
+                if (tid == 0) n_found = 0;
+                __syncthreads();
+                each([&](unsigned long long v) {
+                    if (v >= lo) found[atomicAdd(&n_found, 1)] = v;
+                });
+            }
+            __syncthreads();
+            const int n = n_found;
+            unsigned long long *best = a.best + list * a.kpad;
+            for (int i = tid; i < n; i += BEAM_THREADS) {
+                const unsigned long long c = found[i];
+                int rank = 0;
+                for (int j = 0; j < n; ++j) rank += found[j] > c;
+                if (rank < a.k) best[rank] = c;
+            }
+            for (int i = min(n, a.k) + tid; i < a.kpad; i += BEAM_THREADS) best[i] = 0ull;
+            __syncthreads();
+            if (tid == 0) n_found = 0;  // (the next piece begins with two barriers)
+            first = 0;
+            bound = -FLT_MAX;
+            ref = -INFINITY;
+            sum2 = make_float2(0.0f, 0.0f);
+            hot = true;
+            lost = false;
+        }
+        row += row_ends;
+        step = row_ends ? 0 : step + 1;
+        token0 = ntoken0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) cur[u] = nxt[u];
+        if constexpr (MASK) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) bits[u] = nbits[u];
+        }
+    }
+
+    // ---- this block's pieces are done: batch entries that are complete are joined
+    __threadfence();
+    const int row0 = (int)((long long)blockIdx.x * a.span / a.steps), row1 = (int)((end - 1) / a.steps);
+    for (int b = row0 / a.W; b <= row1 / a.W; ++b) {
+        __syncthreads();
+        if (tid == 0) {
+            const int done = min(row1, (b + 1) * a.W - 1) - max(row0, b * a.W) + 1;
+            int total = 0;
+            for (int w = 0; w < a.W; ++w) total += pieces_of(a, b * a.W + w);
+            joins = atomicAdd(a.count + b, done) + done == total;
+            if (joins) a.count[b] = 0;
+            __threadfence();
+        }
+        __syncthreads();
+        if (joins) beam_join(a, *reinterpret_cast<JoinSmem *>(smem), b);
+    }
+}
+
+// ------------------------------------------------------------ host
+
+// Steps of a row, of a stretch, and the most pieces of a row.  As many
+// stretches as blocks fit on the GPU (those with a mask hold more registers).
+constexpr long long BEAM_SMS = 152;
+struct BeamSplit {
+    int steps, span, pieces, stretches;
+};
+static BeamSplit beam_split(int rows, int V, int vec, bool mask)
+{
+    BeamSplit s;
+    // (a row may begin inside its first vector)
+    s.steps = ((V + vec - 1 + vec - 1) / vec + BEAM_STEP - 1) / BEAM_STEP;
+    const long long total = (long long)rows * s.steps, blocks = BEAM_SMS * (mask ? 2 : 4);
+    s.span = (int)((total + blocks - 1) / blocks);
+    s.pieces = (s.steps + s.span - 1) / s.span + (s.steps % s.span != 0 || s.span == 0 ? 1 : 0);
+    s.stretches = (int)((total + s.span - 1) / s.span);
+    return s;
+}
+
+static size_t beam_lists(int B, int W, int V, int vec)
+{
+    const size_t p = beam_split(B * W, V, vec, false).pieces, m = beam_split(B * W, V, vec, true).pieces;
+    return (size_t)B * W * (p > m ? p : m);
+}
 
 size_t beam_workspace_bytes(int B, int W, int V, int k)
 {
@@ -785,18 +855,17 @@ size_t beam_workspace_bytes(int B, int W, int V, int k)
 }
 
 template <typename E>
-static cudaError_t run_beam(cudaStream_t st, const BeamArgs &a)
+static cudaError_t run_beam(cudaStream_t st, const BeamArgs &a, int stretches)
 {
-    const dim3 grid(a.chunks, a.B * a.W);
-    const cudaError_t e = a.mask ? launch_k(beam_chunk_kernel<E, true>, grid, dim3(BEAM_THREADS), 0, st, a)
-                                 : launch_k(beam_chunk_kernel<E, false>, grid, dim3(BEAM_THREADS), 0, st, a);
-    return e != cudaSuccess ? e : launch_k(beam_join_kernel, dim3(a.B), dim3(BEAM_THREADS), 0, st, a);
+    const dim3 grid((unsigned)stretches);
+    return a.mask ? launch_k(beam_kernel<E, true>, grid, dim3(BEAM_THREADS), 0, st, a)
+                  : launch_k(beam_kernel<E, false>, grid, dim3(BEAM_THREADS), 0, st, a);
 }
 
-cudaError_t launch_beam_select(const DeviceState &, cudaStream_t st, const BeamCall &c, void *workspace)
+cudaError_t launch_beam_select(const DeviceState &ds, cudaStream_t st, const BeamCall &c, void *workspace)
 {
     const int vec = c.dtype == MX_F32 ? 4 : 8;
-    const BeamSplit split = beam_split(c.B * c.W, c.V, vec);
+    const BeamSplit split = beam_split(c.B * c.W, c.V, vec, c.mask != nullptr);
     BeamArgs a;
     a.logits = c.logits;
     a.row_stride = c.row_stride;
@@ -808,19 +877,21 @@ cudaError_t launch_beam_select(const DeviceState &, cudaStream_t st, const BeamC
     a.V = c.V;
     a.k = c.k;
     a.eos = c.eos;
-    a.chunks = split.chunks;
     a.steps = split.steps;
+    a.span = split.span;
+    a.pieces = split.pieces;
     a.score = c.score;
     a.parent = c.parent;
     a.token = c.token;
     a.next_score = c.next_score;
     a.next_parent = c.next_parent;
     a.next_token = c.next_token;
-    const size_t lists = (size_t)c.B * c.W * a.chunks;
+    const size_t lists = (size_t)c.B * c.W * a.pieces;
     a.kpad = (c.k + 3) / 4 * 4;
+    a.count = ds.ws_count;
     a.best = static_cast<unsigned long long *>(workspace);
     a.sums = reinterpret_cast<float2 *>(a.best + lists * a.kpad);
-    return c.dtype == MX_F32 ? run_beam<float>(st, a) : run_beam<uint16_t>(st, a);
+    return c.dtype == MX_F32 ? run_beam<float>(st, a, split.stretches) : run_beam<uint16_t>(st, a, split.stretches);
 }
 
 }  // namespace mx

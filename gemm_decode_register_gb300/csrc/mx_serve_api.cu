@@ -99,8 +99,8 @@ extern "C" int mx_beam_select(const void *logits, int dtype, int64_t row_stride,
         return MX_EALIGN;
     DeviceState *ds = device_state();
     if (!ds) return MX_ECUDA;
-    DeviceState v = *ds;
-    if (!workspace && !attach_stream_workspace(v, current_stream())) return MX_ECUDA;
+    DeviceState v = *ds;  // the slot's counters, and its space for the pieces' lists
+    if (!attach_stream_workspace(v, current_stream())) return MX_ECUDA;
     BeamCall c;
     c.logits = logits;
     c.dtype = dtype;

@@ -649,11 +649,13 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
         if mask.shape != (rows, (V + 31) // 32):
             raise ValueError(f"mask: expected shape {(rows, (V + 31) // 32)}")
         ms = mask.stride(0) if rows > 1 else mask.shape[1]
-    f = torch.empty((B * (k + W),), dtype=torch.float32, device=logits.device)
-    i = torch.empty((2, B * (k + W)), dtype=torch.int32, device=logits.device)
-    n = B * k
-    out = Beams(f[:n].view(B, k), i[0, :n].view(B, k), i[1, :n].view(B, k),
-                f[n:].view(B, W), i[0, n:].view(B, W), i[1, n:].view(B, W))
+    # one allocation, six views of it (a view costs a third of an allocation)
+    n, m = B * k, B * W
+    i = torch.empty(3 * (n + m), dtype=torch.int32, device=logits.device)
+    f = i.view(torch.float32)
+    ks, ws = ((B, k), (k, 1)), ((B, W), (W, 1))
+    out = Beams(f.as_strided(*ks, 0), i.as_strided(*ks, n), i.as_strided(*ks, 2 * n),
+                f.as_strided(*ws, 3 * n), i.as_strided(*ws, 3 * n + m), i.as_strided(*ws, 3 * n + 2 * m))
     if rows > 0:
         lib = load()
         if workspace is None:
@@ -661,11 +663,11 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
             if need > WORKSPACE_SLOT_BYTES:
                 workspace = _workspace(need, None, logits.device)
         wp, wn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
-        fp, ip, jp = f.data_ptr(), i.data_ptr(), i[1].data_ptr()
+        at = i.data_ptr()
         _stream()
         _check("mx_beam_select", lib.mx_beam_select(
             xp, _DTYPES[logits.dtype], logits.stride(0) if rows > 1 else V, sp, mp, ms, B, W, V, k, max(eos, -1),
-            fp, ip, jp, fp + 4 * n, ip + 4 * n, jp + 4 * n, wp, wn))
+            at, at + 4 * n, at + 8 * n, at + 12 * n, at + 12 * n + 4 * m, at + 12 * n + 8 * m, wp, wn))
     return out
 
 

@@ -406,7 +406,7 @@ int mx_paged_attn(const mx_paged_kv *kv, const void *q, int64_t q_token_stride, 
  * mx_beam_select_workspace_size(B, W, V, k) bytes, 256-byte aligned;
  * overwritten, so calls sharing one must not overlap.  Null (with
  * workspace_bytes 0) where that size is at most 16 MiB: the calling stream's
- * workspace slot.  W <= 64, k <= 128,
+ * workspace slot.  Its counters are used in either case.  W <= 64, k <= 128,
  * V <= 2^20, B <= 4096, B*W <= 65535; logits aligned to an element, all
  * else to 4 bytes; row_stride >= V and mask_stride >= ceil(V/32) where there is
  * more than one row. */
