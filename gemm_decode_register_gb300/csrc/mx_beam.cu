@@ -109,6 +109,8 @@ struct Elem<uint16_t> {
         const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
         return fmaxf(bf16_lo(m), bf16_hi(m));
     }
+    // Element number i of a row of vectors.
+    static __device__ __forceinline__ float one(const uint4 *v, int i) { return bf16_to_f32(reinterpret_cast<const uint16_t *>(v)[i]); }
     // Elements whose bit is not set become -inf.
     static __device__ __forceinline__ void keep(uint4 &v, uint32_t bits)
     {
@@ -132,6 +134,7 @@ struct Elem<float> {
     {
         return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
+    static __device__ __forceinline__ float one(const uint4 *v, int i) { return reinterpret_cast<const float *>(v)[i]; }
     static __device__ __forceinline__ void keep(uint4 &v, uint32_t bits)
     {
         uint32_t *w = &v.x;
@@ -594,30 +597,30 @@ __global__ void __launch_bounds__(BEAM_THREADS, MASK ? 2 : 4) beam_kernel(const 
         if (n > ORD_NEG_INF) bound = fmaxf(bound, unordered(n));
         __syncthreads();
     };
-    // the queue's elements that reach the bound are found; the queue is empty after it
+    // the queue's elements that reach the bound are found, a thread for each; the
+    // queue is empty after it
     auto drain = [&] {
-        const int n = min(n_queue, BEAM_QUEUE);
-        for (int i = tid; i < n; i += BEAM_THREADS) {
-            const uint4 v = queue[i];
-            const int at = queue_at[i];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float f = L::get(v, j);
-                if (f >= bound) {
-                    const int o = atomicAdd(&n_found, 1);
-                    if (o < BEAM_FOUND) found[o] = logit_token(f, at + j);
-                }
-            }
+        const int n = min(n_queue, BEAM_QUEUE) * VEC;
+        for (int i0 = 0; i0 < n; i0 += BEAM_THREADS) {
+            const int i = i0 + tid;
+            const float f = i < n ? L::one(queue, i) : -INFINITY;
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, f >= bound);
+            if (hit == 0u) continue;
+            int o = 0;
+            if (lane == 0) o = atomicAdd(&n_found, __popc(hit));
+            o = __shfl_sync(0xFFFFFFFFu, o, 0) + __popc(hit & ((1u << lane) - 1u));
+            if (f >= bound && o < BEAM_FOUND) found[o] = logit_token(f, queue_at[i / VEC] + i % VEC);
         }
         __syncthreads();
         if (tid == 0) n_queue = 0;
     };
-    // the bound from what is found so far: each thread's largest of up to four
+    // the bound from what is found so far, dealt out over the warps: each
+    // thread's largest of up to four
     auto raise_by_found = [&] {
         const int n = n_found;
         uint32_t v = 0u;
-        for (int i = tid; i < n; i += BEAM_THREADS) v = max(v, (uint32_t)(found[i] >> 32));
-        raise(v > ORD_NEG_INF ? unordered(v) : -INFINITY, n);
+        for (int i = lane * BEAM_WARPS + warp; i < n; i += BEAM_THREADS) v = max(v, (uint32_t)(found[i] >> 32));
+        raise(v > ORD_NEG_INF ? unordered(v) : -INFINITY, BEAM_THREADS);
     };
 
     const long long end = min((long long)(blockIdx.x + 1) * a.span, (long long)a.B * a.W * a.steps);
@@ -726,18 +729,20 @@ __global__ void __launch_bounds__(BEAM_THREADS, MASK ? 2 : 4) beam_kernel(const 
             __syncthreads();
             if (!lost) {
                 const int n = n_found;
-                raise_by_found();
-                // what no longer reaches the bound is dropped
-                constexpr int F = BEAM_FOUND / BEAM_THREADS;
-                unsigned long long mine[F];
+                if (n > BEAM_THREADS / 2) {  // (fewer are ranked sooner than sifted)
+                    raise_by_found();
+                    // what no longer reaches the bound is dropped
+                    constexpr int F = BEAM_FOUND / BEAM_THREADS;
+                    unsigned long long mine[F];
 #pragma unroll
-                for (int i = 0; i < F; ++i) mine[i] = i * BEAM_THREADS + tid < n ? found[i * BEAM_THREADS + tid] : 0ull;
-                if (tid == 0) n_found = 0;
-                __syncthreads();
-                const unsigned long long lo = (unsigned long long)ordered(bound + 0.0f) << 32;
+                    for (int i = 0; i < F; ++i) mine[i] = i * BEAM_THREADS + tid < n ? found[i * BEAM_THREADS + tid] : 0ull;
+                    if (tid == 0) n_found = 0;
+                    __syncthreads();
+                    const unsigned long long lo = (unsigned long long)ordered(bound + 0.0f) << 32;
 #pragma unroll
-                for (int i = 0; i < F; ++i)
-                    if (mine[i] >= lo) found[atomicAdd(&n_found, 1)] = mine[i];
+                    for (int i = 0; i < F; ++i)
+                        if (mine[i] >= lo) found[atomicAdd(&n_found, 1)] = mine[i];
+                }
             } else {
                 // too many reach the bound (ties, most often): the k-th largest of
                 // (logit, token) by bisection over the whole piece, read once per round

@@ -17,7 +17,7 @@
 // dependents start early.
 //
 // Copies (bound: HBM): an item is some heads of one page's half in one layer;
-// blocks walk the items, 16-byte vectors, four in flight per thread.
+// blocks walk the items, 16-byte vectors, eight in flight per thread.
 #include "mx_common.cuh"
 #include "mx_serve.h"
 #include "mx_tc.cuh"
@@ -41,8 +41,7 @@ struct __align__(8) PageTally {
 struct PoolWork {
     PageTally *tally;   // [P]
     uint32_t *freed;    // [P / 32] bits, zero between calls
-    int2 *plan;         // [POOL_MAX_SLOTS] a new slot's first page to be handed out, its copy's number + 1 (0: none)
-    int *word;          // faults of the tally [0] and of the decision [3] (zero between calls), [1] pages handed out, [2] copies
+    int *word;          // (compaction) faults, zero between calls
     int *part;          // [2 * POOL_CLUSTER] counts of each CTA's range of pages
 };
 
@@ -50,7 +49,7 @@ static size_t words_of(int P) { return ((size_t)P + 31) / 32; }
 
 size_t pool_work_bytes(int P)
 {
-    return ((size_t)P * 8 + words_of(P) * 4 + (size_t)POOL_MAX_SLOTS * 8 + 16 + 8 * POOL_CLUSTER + 16 + 255) / 256 * 256;
+    return ((size_t)P * 8 + words_of(P) * 4 + 16 + 8 * POOL_CLUSTER + 255) / 256 * 256;
 }
 
 static PoolWork pool_work(const mx_page_pool &p)
@@ -59,8 +58,6 @@ static PoolWork pool_work(const mx_page_pool &p)
     char *m = static_cast<char *>(p.work);
     w.tally = reinterpret_cast<PageTally *>(m);
     m += (size_t)p.num_pages * 8;
-    w.plan = reinterpret_cast<int2 *>(m);
-    m += (size_t)POOL_MAX_SLOTS * 8;
     w.word = reinterpret_cast<int *>(m);
     w.part = w.word + 4;
     w.freed = reinterpret_cast<uint32_t *>(w.part + 2 * POOL_CLUSTER);
@@ -135,235 +132,290 @@ struct RemapArgs {
     int *err;
 };
 
-// What becomes of new slot s.
-struct NewSlot {
-    int parent, len, kept;  // parent's length; tokens taken from it
-    long long tokens;       // the slot's length
-    bool bad;
-};
-__device__ __forceinline__ NewSlot new_slot(const RemapCall &c, int s)
-{
-    NewSlot n;
-    n.parent = __ldcg(c.parent + s);
-    n.bad = n.parent >= c.S_in;
-    if (n.bad) n.parent = -1;
-    n.len = n.parent < 0 ? 0 : max(__ldcg(c.kv_len_in + n.parent), 0);
-    n.kept = c.keep ? min(n.len, max(__ldcg(c.keep + s), 0)) : n.len;
-    const int add = c.add ? max(__ldcg(c.add + s), 0) : n.parent < 0 ? 0 : c.add_all;
-    n.tokens = (long long)n.kept + add;
-    return n;
-}
-
 constexpr int CUT_CHILD = 1 << 16;  // children of a sequence: that keep all of it, and (upper half) a part
 
+// A new sequence: its parent (or -1), tokens taken from it, tokens.
+struct Slot {
+    int parent, kept, tokens;
+};
+
+// What the CTAs of the cluster tell each other, in each one's shared memory.
+struct RemapShared {
+    int fault, late;     // faults of the tally, of the decision (a word of its own: another CTA may be ahead)
+    int handed, copies;  // pages handed out, copies
+    int smax[32];
+    unsigned long long scan[32];
+};
+
+// (a 32-bit word of every CTA's shared memory)
+__device__ __forceinline__ void all_ctas_or(const void *word, int bits)
+{
+    const uint32_t n = cluster_nctarank(), here = smem_u32(word);
+    for (uint32_t r = 0; r < n; ++r)
+        asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(map_to_cta(here, r)), "r"(bits) : "memory");
+}
+
+// (the plan, of two words a slot, on an even word)
+static __host__ __device__ size_t remap_plan_at(int S_in, int S_out) { return (2 * (size_t)S_in + 4 * (size_t)S_out + 1) / 2 * 2; }
+static size_t remap_smem(int S_in, int S_out) { return sizeof(int) * (remap_plan_at(S_in, S_out) + 2 * (size_t)S_out); }
+
+// The first thing a step needs is every sequence's length and every slot's
+// parent: they are read once, into each CTA's shared memory.  A phase is then one
+// round trip to L2 and a barrier.
 __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_constant__ RemapArgs a)
 {
     const RemapCall &c = a.c;
     const PoolWork &w = a.w;
-    extern __shared__ int children[];  // [S_in]
-    __shared__ int smax[32];
-    __shared__ unsigned long long scan[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    extern __shared__ int dyn[];
+    int *children = dyn;                                        // [S_in]
+    int *lens = children + c.S_in;                              // [S_in]
+    Slot *slots = reinterpret_cast<Slot *>(lens + c.S_in);      // [S_out]
+    int2 *plan = reinterpret_cast<int2 *>(dyn + remap_plan_at(c.S_in, c.S_out));  // [S_out] of CTA 0: first page handed out, copy's number + 1
+    int *tails = lens + c.S_in + 3 * c.S_out;                   // [S_out] of CTA 0: page a growing slot writes in, or -1
+    __shared__ RemapShared sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
     const int rank = (int)cluster_ctarank(), ctas = (int)cluster_nctarank();
     const int gw = warp * ctas + rank, nw = POOL_WARPS * ctas;
     const int ps = c.page_size, P = c.pool.num_pages;
+    if (tid == 0) sh.fault = sh.late = 0;
     pdl_wait();
+    cluster_sync_all();  // (before a CTA reports to the others)
 
-    // ---- children of each sequence (every CTA for itself), longest rows
-    for (int p = threadIdx.x; p < c.S_in; p += POOL_THREADS) children[p] = 0;
-    __syncthreads();
+    // ---- lengths and slots, children of each sequence, longest rows
+    const int count = __ldcg(c.pool.count);
     int fault = 0, rows_in = 0, rows_out = 0;
-    for (int p = threadIdx.x; p < c.S_in; p += POOL_THREADS) {
-        const int n = pages_of(__ldcg(c.kv_len_in + p), ps);
+    for (int p = tid; p < c.S_in; p += POOL_THREADS) {
+        const int len = max(__ldcg(c.kv_len_in + p), 0), n = pages_of(len, ps);
         if (n > c.in_pages) fault |= DEVERR_BAD_PAGE;
         rows_in = max(rows_in, min(n, c.in_pages));
+        lens[p] = len;
+        children[p] = 0;
     }
-    for (int s = threadIdx.x; s < c.S_out; s += POOL_THREADS) {
-        const NewSlot n = new_slot(c, s);
-        if (n.bad) fault |= DEVERR_BAD_SLOT;
-        if (n.tokens > (long long)c.out_pages * ps || n.tokens > 0x7FFFFFFFll) fault |= DEVERR_BAD_PAGE;
-        else rows_out = max(rows_out, pages_of(n.tokens, ps));
-        if (n.parent >= 0) atomicAdd(children + n.parent, n.kept == n.len ? 1 : CUT_CHILD);
+    for (int s = tid; s < c.S_out; s += POOL_THREADS) {
+        Slot n;
+        n.parent = __ldcg(c.parent + s);
+        n.kept = c.keep ? max(__ldcg(c.keep + s), 0) : 0x7FFFFFFF;
+        n.tokens = c.add ? max(__ldcg(c.add + s), 0) : n.parent < 0 ? 0 : c.add_all;
+        slots[s] = n;
     }
-    rows_in = block_max(rows_in, smax);
-    rows_out = block_max(rows_out, smax);
+    __syncthreads();
+    for (int s = tid; s < c.S_out; s += POOL_THREADS) {
+        Slot n = slots[s];
+        if (n.parent >= c.S_in) fault |= DEVERR_BAD_SLOT;
+        if (n.parent < 0 || n.parent >= c.S_in) n.parent = -1;
+        const int len = n.parent < 0 ? 0 : lens[n.parent];
+        n.kept = min(n.kept, len);
+        const long long tokens = (long long)n.kept + n.tokens;
+        if (tokens > (long long)c.out_pages * ps || tokens > 0x7FFFFFFFll) fault |= DEVERR_BAD_PAGE;
+        n.tokens = (int)min(tokens, 0x7FFFFFFFll);
+        rows_out = max(rows_out, min(pages_of(n.tokens, ps), c.out_pages));
+        slots[s] = n;
+        if (n.parent >= 0) atomicAdd(children + n.parent, n.kept == len ? 1 : CUT_CHILD);
+    }
+    rows_in = block_max(rows_in, sh.smax);
+    rows_out = block_max(rows_out, sh.smax);
     const int chunks_in = (rows_in + 32 * RUN - 1) / (32 * RUN), chunks_out = (rows_out + 32 * RUN - 1) / (32 * RUN);
 
-    // f(sequence, its children, entry, page) for the old tables' entries of this warp's tasks
+    // f(sequence's children, page, users) for the old tables' entries of this
+    // warp's tasks; users: those that the step leaves this entry's page
+    // through it, the children that keep the whole sequence, of its full pages (its
+    // partial one is counted by each child), less the entry itself.  The first task's entries
+    // stay in registers.
+    int own[RUN];
+    bool have_own = false;
     auto old_entries = [&](auto f) {
         for (int t = gw; t < c.S_in * chunks_in; t += nw) {
             const int p = t % c.S_in, j0 = t / c.S_in * (32 * RUN);
-            const int len = __ldcg(c.kv_len_in + p);
-            const int n = min(pages_of(len, ps), c.in_pages);
+            const int len = lens[p], n = min(pages_of(len, ps), c.in_pages);
             if (j0 >= n) continue;
             const int32_t *row = c.table_in + (long long)p * c.in_stride;
             int page[RUN];
 #pragma unroll
             for (int i = 0; i < RUN; ++i) {
                 const int j = j0 + 32 * i + lane;
-                page[i] = j < n ? __ldcg(row + j) : -1;
+                if (t == gw && have_own) page[i] = own[i];
+                else page[i] = j < n ? __ldcg(row + j) : -1;
+                if (t == gw) own[i] = page[i];
             }
+            const int kids = children[p];
 #pragma unroll
             for (int i = 0; i < RUN; ++i) {
                 const int j = j0 + 32 * i + lane;
-                // users that the step leaves this entry's page through it: the
-                // children that keep the whole sequence, of its full pages (its
-                // partial one is counted by each child)
-                if (j < n) f(p, children[p], page[i], (j < len / ps ? children[p] % CUT_CHILD : 0) - 1);
+                if (j < n) f(kids, page[i], (j < len / ps ? kids % CUT_CHILD : 0) - 1);
             }
         }
+        have_own = true;
     };
 
-    // ---- tally
-    old_entries([&](int, int, int page, int d) {
+    // ---- tally.  The partial page of each slot: CTA 0, a thread for each
+    if (rank == 0)
+        for (int s = tid; s < c.S_out; s += POOL_THREADS) {
+            const Slot n = slots[s];
+            const int full = n.kept / ps;
+            int tail = -1;
+            if (n.kept % ps != 0 && full < c.in_pages) {
+                const int page = __ldcg(c.table_in + (long long)n.parent * c.in_stride + full);
+                if ((unsigned)page < (unsigned)P) {
+                    if (n.tokens > n.kept) atomicMax(&w.tally[tail = page].writer, c.S_out - s);
+                    else atomicAdd(&w.tally[page].users, 1);
+                }
+            }
+            tails[s] = tail;
+        }
+    old_entries([&](int, int page, int d) {
         if ((unsigned)page >= (unsigned)P) fault |= DEVERR_BAD_PAGE;
         else if (d != 0) atomicAdd(&w.tally[page].users, d);
     });
-    for (int t = gw; t < c.S_out * max(chunks_in, 1); t += nw) {
-        const int s = t % c.S_out, j0 = t / c.S_out * (32 * RUN);
-        const NewSlot n = new_slot(c, s);
-        if (n.parent < 0) continue;
-        const int32_t *row = c.table_in + (long long)n.parent * c.in_stride;
-        const int full = min(n.kept / ps, c.in_pages);
-        if (n.kept < n.len)
+    // full pages of those that take a part
+    if (c.keep)
+        for (int t = gw; t < c.S_out * chunks_in; t += nw) {
+            const int s = t % c.S_out, j0 = t / c.S_out * (32 * RUN);
+            const Slot n = slots[s];
+            if (n.parent < 0 || n.kept == lens[n.parent]) continue;
+            const int32_t *row = c.table_in + (long long)n.parent * c.in_stride;
+            const int full = min(n.kept / ps, c.in_pages);
             for (int j = j0 + lane; j < min(full, j0 + 32 * RUN); j += 32) {
                 const int page = __ldcg(row + j);
                 if ((unsigned)page < (unsigned)P) atomicAdd(&w.tally[page].users, 1);
             }
-        if (j0 == 0 && lane == 0 && n.kept % ps != 0 && full < c.in_pages) {
-            const int page = __ldcg(row + full);
-            if ((unsigned)page < (unsigned)P) {
-                if (n.tokens > n.kept) atomicMax(&w.tally[page].writer, c.S_out - s);
-                else atomicAdd(&w.tally[page].users, 1);
-            }
         }
-    }
-    if (fault) atomicOr(w.word, fault);
+    if (fault) all_ctas_or(&sh.fault, fault);
     cluster_phase();
 
     // ---- pages each slot is handed out, in slot order (CTA 0); pages left
-    // without a user.  Skipped where a fault is known: lengths may not fit
-    // the tables.
-    if (__ldcg(w.word) == 0) {
+    // without a user.  Not where a fault is known: lengths may not fit the tables.
+    fault = *(volatile int *)&sh.fault;
+    if (fault == 0) {
+        int bad = 0;
         if (rank == 0) {
-            const int per = (c.S_out + POOL_THREADS - 1) / POOL_THREADS;
-            const int s0 = (int)threadIdx.x * per, s1 = min(s0 + per, c.S_out);
+            constexpr int PER = (POOL_MAX_SLOTS + POOL_THREADS - 1) / POOL_THREADS;
             constexpr unsigned long long COPY = 1ull << 40;  // pages below, copies above
-            unsigned long long mine = 0;
-            auto need = [&](int s) {
-                const NewSlot n = new_slot(c, s);
-                unsigned long long v = (unsigned)(pages_of(n.tokens, ps) - pages_of(n.kept, ps));
-                if (n.kept % ps != 0 && n.tokens > n.kept) {
-                    const int page = __ldcg(c.table_in + (long long)n.parent * c.in_stride + n.kept / ps);
-                    const PageTally t = tally_at(w.tally, page);
-                    // a page that only growing slots use stays with the first
-                    if (!(__ldcg(c.pool.refs + page) + t.users == 0 && t.writer == c.S_out - s)) v += COPY + 1;
+            const int per = (c.S_out + POOL_THREADS - 1) / POOL_THREADS, s0 = tid * per;
+            unsigned long long need[PER], mine = 0;
+            PageTally tally[PER];
+            int refs[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int tail = i < per && s0 + i < c.S_out ? tails[s0 + i] : -1;
+                if (tail >= 0) {
+                    tally[i] = tally_at(w.tally, tail);
+                    refs[i] = __ldcg(c.pool.refs + tail);
                 }
-                return v;
-            };
-            for (int s = s0; s < s1; ++s) mine += need(s);
-            unsigned long long total;
-            unsigned long long at = block_prefix(mine, scan, total);
-            for (int s = s0; s < s1; ++s) {
-                const unsigned long long v = need(s);
-                w.plan[s] = make_int2((int)(at & (COPY - 1)), v >= COPY ? (int)(at / COPY) + 1 : 0);
-                at += v;
             }
-            if (threadIdx.x == 0) {
-                const int count = __ldcg(c.pool.count);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                need[i] = 0;
+                if (i >= per || s0 + i >= c.S_out) continue;
+                const Slot n = slots[s0 + i];
+                need[i] = (unsigned)(pages_of(n.tokens, ps) - pages_of(n.kept, ps));
+                // a page that only growing slots use stays with the first
+                if (tails[s0 + i] >= 0 && !(refs[i] + tally[i].users == 0 && tally[i].writer == c.S_out - s0 - i))
+                    need[i] += COPY + 1;
+                mine += need[i];
+            }
+            unsigned long long total;
+            unsigned long long at = block_prefix(mine, sh.scan, total);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (i >= per || s0 + i >= c.S_out) continue;
+                plan[s0 + i] = make_int2((int)(at & (COPY - 1)), need[i] >= COPY ? (int)(at / COPY) + 1 : 0);
+                at += need[i];
+            }
+            if (tid == 0) {
                 const unsigned long long n = total & (COPY - 1);
-                if (count < 0 || count > P) atomicOr(w.word + 3, (int)DEVERR_BAD_PAGE);
-                else if (n > (unsigned long long)count) atomicOr(w.word + 3, (int)DEVERR_NO_PAGE);
-                w.word[1] = (int)n;
-                w.word[2] = (int)(total / COPY);
+                if (count < 0 || count > P) bad |= DEVERR_BAD_PAGE;
+                else if (n > (unsigned long long)count) bad |= DEVERR_NO_PAGE;
+                sh.handed = (int)n;
+                sh.copies = (int)(total / COPY);
             }
         }
-        old_entries([&](int, int, int page, int d) {
+        old_entries([&](int, int page, int d) {
             if (d >= 0) return;
             const PageTally t = tally_at(w.tally, page);
             const int left = __ldcg(c.pool.refs + page) + t.users;
-            if (left < 0) atomicOr(w.word + 3, (int)DEVERR_BAD_PAGE);  // fewer references than entries
+            if (left < 0) bad |= DEVERR_BAD_PAGE;  // fewer references than entries
             if (left == 0 && t.writer == 0) atomicOr(w.freed + (page >> 5), 1u << (page & 31));
         });
+        if (bad) all_ctas_or(&sh.late, bad);
     }
     cluster_phase();
 
     // ---- all or nothing
-    fault = __ldcg(w.word) | __ldcg(w.word + 3);
+    fault |= *(volatile int *)&sh.late;
     if (fault) {
-        old_entries([&](int, int, int page, int) {
+        old_entries([&](int, int page, int) {
             if ((unsigned)page >= (unsigned)P) return;
             w.tally[page] = PageTally{0, 0};
             w.freed[page >> 5] = 0u;
         });
         if (rank == 0) {
-            for (int s = threadIdx.x; s < c.S_out; s += POOL_THREADS) c.kv_len_out[s] = -1;
-            if (threadIdx.x == 0) {
+            for (int s = tid; s < c.S_out; s += POOL_THREADS) c.kv_len_out[s] = -1;
+            if (tid == 0) {
                 reinterpret_cast<int4 *>(c.copies)[0] = make_int4(0, 0, 0, 0);
                 set_device_error(a.err, fault);
             }
         }
-        cluster_phase();
-        if (rank == 0 && threadIdx.x == 0) w.word[0] = w.word[3] = 0;
+        cluster_sync_all();  // (no CTA leaves while another may report to it)
         return;
     }
-    const int count = __ldcg(c.pool.count), handed = __ldcg(w.word + 1);
-    old_entries([&](int, int kids, int page, int d) {
-        if (d == 0 && kids < CUT_CHILD) return;
-        // whoever comes first takes the tally
-        const unsigned long long v = atomicExch(reinterpret_cast<unsigned long long *>(w.tally + page), 0ull);
-        if (v == 0ull) return;
-        const int left = __ldcg(c.pool.refs + page) + (int)(uint32_t)v;
-        c.pool.refs[page] = left == 0 && (v >> 32) != 0 ? 1 : left;
-    });
+    const uint32_t plan0 = map_to_cta(smem_u32(plan), 0);
     for (int t = gw; t < c.S_out * max(chunks_out, 1); t += nw) {
         const int s = t % c.S_out, j0 = t / c.S_out * (32 * RUN);
-        const NewSlot n = new_slot(c, s);
-        const int2 plan = __ldcg(w.plan + s);
-        const int end = pages_of(n.tokens, ps), start = pages_of(n.kept, ps) - (plan.y != 0);
+        const Slot n = slots[s];
+        const int end = pages_of(n.tokens, ps);
+        if (j0 >= end && j0 > 0) continue;
+        const int first = ld_cluster_s32(plan0 + 8 * s), copy = ld_cluster_s32(plan0 + 8 * s + 4);
+        const int start = pages_of(n.kept, ps) - (copy != 0);
         const int32_t *from = c.table_in + (long long)max(n.parent, 0) * c.in_stride;
         int32_t *to = c.table_out + (long long)s * c.out_stride;
-        if (j0 < end || j0 == 0) {
-            int page[RUN];
+        int page[RUN];
 #pragma unroll
-            for (int i = 0; i < RUN; ++i) {
-                const int j = j0 + 32 * i + lane;
-                if (j < start) page[i] = __ldcg(from + j);
-                else if (j < end) page[i] = __ldcg(c.pool.free_pages + (count - 1 - plan.x - (j - start)));
-            }
-#pragma unroll
-            for (int i = 0; i < RUN; ++i) {
-                const int j = j0 + 32 * i + lane;
-                if (j >= end) continue;
-                to[j] = page[i];
-                if (j < start) continue;
-                if ((unsigned)page[i] < (unsigned)P) c.pool.refs[page[i]] = 1;
-                else set_device_error(a.err, DEVERR_BAD_PAGE);
-                if (j == start && plan.y != 0)
-                    reinterpret_cast<int4 *>(c.copies)[plan.y] = make_int4(__ldcg(from + j), page[i], n.kept % ps, 0);
-            }
-            if (j0 == 0 && lane == 0) c.kv_len_out[s] = (int)n.tokens;
+        for (int i = 0; i < RUN; ++i) {
+            const int j = j0 + 32 * i + lane;
+            if (j < start) page[i] = __ldcg(from + j);
+            else if (j < end) page[i] = __ldcg(c.pool.free_pages + (count - 1 - first - (j - start)));
         }
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+            const int j = j0 + 32 * i + lane;
+            if (j >= end) continue;
+            to[j] = page[i];
+            if (j < start) continue;
+            if ((unsigned)page[i] < (unsigned)P) c.pool.refs[page[i]] = 1;
+            else set_device_error(a.err, DEVERR_BAD_PAGE);
+            if (j == start && copy != 0)
+                reinterpret_cast<int4 *>(c.copies)[copy] = make_int4(__ldcg(from + j), page[i], n.kept % ps, 0);
+        }
+        if (j0 == 0 && lane == 0) c.kv_len_out[s] = n.tokens;
     }
+    old_entries([&](int kids, int page, int d) {
+        if (d == 0 && kids < CUT_CHILD) return;
+        // whoever comes first takes the tally
+        const int refs = __ldcg(c.pool.refs + page);
+        const unsigned long long v = atomicExch(reinterpret_cast<unsigned long long *>(w.tally + page), 0ull);
+        if (v == 0ull) return;
+        const int left = refs + (int)(uint32_t)v;
+        c.pool.refs[page] = left == 0 && (v >> 32) != 0 ? 1 : left;
+    });
     cluster_phase();
 
     // ---- the freed pages go on the stack, in page order (CTA 0)
     if (rank != 0) return;
     const int words = (P + 31) / 32;
-    int top = count - handed;
+    int top = count - sh.handed;
     for (int i0 = 0; i0 < words; i0 += POOL_THREADS) {
-        const int i = i0 + (int)threadIdx.x;
+        const int i = i0 + tid;
         uint32_t bits = i < words ? __ldcg(w.freed + i) : 0u;
         if (__syncthreads_or(bits != 0u) == 0) continue;
         unsigned long long total;
-        int at = top + (int)block_prefix((unsigned)__popc(bits), scan, total);
+        int at = top + (int)block_prefix((unsigned)__popc(bits), sh.scan, total);
         if (bits) w.freed[i] = 0u;
         for (; bits; bits &= bits - 1) c.pool.free_pages[at++] = 32 * i + __ffs((int)bits) - 1;
         top += (int)total;
     }
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         *c.pool.count = top;
-        reinterpret_cast<int4 *>(c.copies)[0] = make_int4(__ldcg(w.word + 2), 0, 0, 0);
+        reinterpret_cast<int4 *>(c.copies)[0] = make_int4(sh.copies, 0, 0, 0);
     }
 }
 
@@ -538,8 +590,10 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_compact_kernel(const __gri
 
 // ------------------------------------------------------------ copies
 
+constexpr int COPY_THREADS = 256;
+
 // What is copied of a page in one half of the cache: rows (head, token) of
-// `row` bytes, moved in units of V's size.
+// `row` bytes.  Data moves in 16-byte units, scales in `unit`s.
 struct CopyPart {
     long long page_stride, head_stride, token_stride;  // bytes
     int row;                                           // bytes
@@ -555,7 +609,7 @@ struct CopyArgs {
     int *err;
 };
 
-template <typename V>
+template <typename V, unsigned F>
 __device__ __forceinline__ void copy_rows(const uint8_t *src, uint8_t *dst, const CopyPart &p, int heads, int tokens)
 {
     // tokens that lie together make one row of each head
@@ -563,42 +617,36 @@ __device__ __forceinline__ void copy_rows(const uint8_t *src, uint8_t *dst, cons
     const unsigned per_row = (unsigned)(p.row / (int)sizeof(V)) * (together ? (unsigned)tokens : 1u);
     const unsigned rows = together ? 1u : (unsigned)tokens;  // of a head
     const unsigned n = per_row * rows * (unsigned)heads;
-    constexpr int F = 4;
-    for (unsigned i0 = threadIdx.x; i0 < n; i0 += F * blockDim.x) {
+    auto place = [&](unsigned i) {
+        const unsigned r = i / per_row, col = i - r * per_row, h = together ? r : r / rows, t = together ? 0u : r - h * rows;
+        return (long long)h * p.head_stride + (long long)t * p.token_stride + (long long)col * (int)sizeof(V);
+    };
+    // (addresses are worked out again for the stores: kept, they would cost
+    // more registers than the data)
+    for (unsigned i0 = threadIdx.x; i0 < n; i0 += F * COPY_THREADS) {
         V v[F];
-        long long at[F];
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-            const unsigned i = i0 + f * blockDim.x;
-            if (i >= n) break;
-            const unsigned r = i / per_row, col = i - r * per_row;
-            const unsigned h = r / rows, t = r - h * rows;
-            at[f] = (long long)h * p.head_stride + (long long)t * p.token_stride + (long long)col * (int)sizeof(V);
-            v[f] = __ldcg(reinterpret_cast<const V *>(src + at[f]));
-        }
+        for (unsigned f = 0; f < F; ++f)
+            if (i0 + f * COPY_THREADS < n) v[f] = __ldcs(reinterpret_cast<const V *>(src + place(i0 + f * COPY_THREADS)));
 #pragma unroll
-        for (int f = 0; f < F; ++f)
-            if (i0 + f * blockDim.x < n) *reinterpret_cast<V *>(dst + at[f]) = v[f];
+        for (unsigned f = 0; f < F; ++f)
+            if (i0 + f * COPY_THREADS < n) *reinterpret_cast<V *>(dst + place(i0 + f * COPY_THREADS)) = v[f];
     }
 }
 
-__device__ __forceinline__ void copy_part(uint8_t *base, const CopyPart &p, int src, int dst, int head, int heads, int tokens)
+__device__ __forceinline__ void copy_scales(const uint8_t *s, uint8_t *d, const CopyPart &p, int heads, int tokens)
 {
-    const uint8_t *s = base + src * p.page_stride + head * p.head_stride;
-    uint8_t *d = base + dst * p.page_stride + head * p.head_stride;
     switch (p.unit) {
-    case 16: copy_rows<uint4>(s, d, p, heads, tokens); break;
-    case 8: copy_rows<uint2>(s, d, p, heads, tokens); break;
-    case 4: copy_rows<uint32_t>(s, d, p, heads, tokens); break;
-    case 2: copy_rows<uint16_t>(s, d, p, heads, tokens); break;
-    default: copy_rows<uint8_t>(s, d, p, heads, tokens); break;
+    case 16: copy_rows<uint4, 1>(s, d, p, heads, tokens); break;
+    case 8: copy_rows<uint2, 1>(s, d, p, heads, tokens); break;
+    case 4: copy_rows<uint32_t, 2>(s, d, p, heads, tokens); break;
+    case 2: copy_rows<uint16_t, 2>(s, d, p, heads, tokens); break;
+    default: copy_rows<uint8_t, 2>(s, d, p, heads, tokens); break;
     }
 }
-
-constexpr int COPY_THREADS = 256;
 
 template <int LAYERS>
-__global__ void __launch_bounds__(COPY_THREADS) kv_copy_kernel(const __grid_constant__ CopyArgs<LAYERS> a)
+__global__ void __launch_bounds__(COPY_THREADS, 4) kv_copy_kernel(const __grid_constant__ CopyArgs<LAYERS> a)
 {
     pdl_wait();
     // (not before: what precedes may have written the tables that the next
@@ -619,8 +667,14 @@ __global__ void __launch_bounds__(COPY_THREADS) kv_copy_kernel(const __grid_cons
         }
         if (tokens <= 0 || c.x == c.y) continue;
         const int head = g * a.group, heads = min(a.group, a.heads - head);
-        copy_part(a.data[layer][half], a.d, c.x, c.y, head, heads, tokens);
-        if (a.s.row > 0) copy_part(a.scales[layer][half], a.s, c.x, c.y, head, heads, tokens);
+        {
+            uint8_t *base = a.data[layer][half] + head * a.d.head_stride;
+            copy_rows<uint4, 8>(base + c.x * a.d.page_stride, base + c.y * a.d.page_stride, a.d, heads, tokens);
+        }
+        if (a.s.row > 0) {
+            uint8_t *base = a.scales[layer][half] + head * a.s.head_stride;
+            copy_scales(base + c.x * a.s.page_stride, base + c.y * a.s.page_stride, a.s, heads, tokens);
+        }
     }
 }
 
@@ -661,7 +715,12 @@ cudaError_t launch_kv_remap(const DeviceState &ds, cudaStream_t st, const RemapC
     a.err = ds.err;
     const int S = c.S_in > c.S_out ? c.S_in : c.S_out;
     const int pages = c.in_pages > c.out_pages ? c.in_pages : c.out_pages;
-    return run_cluster(st, kv_remap_kernel, pool_ctas(S, pages, c.pool.num_pages), (size_t)c.S_in * 4, a);
+    const size_t smem = remap_smem(c.S_in, c.S_out);
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kv_remap_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return run_cluster(st, kv_remap_kernel, pool_ctas(S, pages, c.pool.num_pages), smem, a);
 }
 
 cudaError_t launch_kv_compact(const DeviceState &ds, cudaStream_t st, const mx_page_pool &pool, int page_size,

@@ -633,13 +633,15 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
     `logits`, so it serves kv_remap as it is.  Places without a candidate hold -inf, -1, 0.  eos: the token that ends
     a beam; beams of that token are left out of next_*.  mask int32 [B * W][ceil(V / 32)]: bit v % 32 of word v // 32
     allows token v; the probabilities are those among the allowed tokens."""
-    if logits.dtype not in _DTYPES:
+    dt, dev = _DTYPES.get(logits.dtype), logits.device
+    if dt is None:
         raise ValueError(f"logits: expected bf16 or fp32, got {logits.dtype}")
     xp = _cuda("logits", logits, logits.dtype, 2)
-    if scores.dim() != 2 or scores.numel() != logits.shape[0]:
-        raise ValueError("scores: expected [B][W] with a row of logits for each")
     rows, V = logits.shape
-    B, W = shape = scores.shape
+    shape = scores.shape
+    if len(shape) != 2 or shape[0] * shape[1] != rows:
+        raise ValueError("scores: expected [B][W] with a row of logits for each")
+    B, W = shape
     sp = _whole("scores", scores, torch.float32, shape)
     if k is None:
         k = 2 * W
@@ -649,25 +651,23 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
         if mask.shape != (rows, (V + 31) // 32):
             raise ValueError(f"mask: expected shape {(rows, (V + 31) // 32)}")
         ms = mask.stride(0) if rows > 1 else mask.shape[1]
-    # one allocation, six views of it (a view costs a third of an allocation)
-    n, m = B * k, B * W
-    i = torch.empty(3 * (n + m), dtype=torch.int32, device=logits.device)
-    f = i.view(torch.float32)
-    ks, ws = ((B, k), (k, 1)), ((B, W), (W, 1))
-    out = Beams(f.as_strided(*ks, 0), i.as_strided(*ks, n), i.as_strided(*ks, 2 * n),
-                f.as_strided(*ws, 3 * n), i.as_strided(*ws, 3 * n + m), i.as_strided(*ws, 3 * n + 2 * m))
+    # (six allocations cost less than one and six views)
+    empty, f32, i32, bk, bw = torch.empty, torch.float32, torch.int32, (B, k), (B, W)
+    out = Beams(empty(bk, dtype=f32, device=dev), empty(bk, dtype=i32, device=dev), empty(bk, dtype=i32, device=dev),
+                empty(bw, dtype=f32, device=dev), empty(bw, dtype=i32, device=dev), empty(bw, dtype=i32, device=dev))
     if rows > 0:
         lib = load()
-        if workspace is None:
+        stride = logits.stride(0) if rows > 1 else V
+        op = [t.data_ptr() for t in out]
+        wp, wn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
+        _stream()
+        s = lib.mx_beam_select(xp, dt, stride, sp, mp, ms, B, W, V, k, eos if eos >= 0 else -1, *op, wp, wn)
+        if s == -1 and workspace is None:  # (the stream's own may be too small)
             need = lib.mx_beam_select_workspace_size(B, W, V, k)
             if need > WORKSPACE_SLOT_BYTES:
-                workspace = _workspace(need, None, logits.device)
-        wp, wn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
-        at = i.data_ptr()
-        _stream()
-        _check("mx_beam_select", lib.mx_beam_select(
-            xp, _DTYPES[logits.dtype], logits.stride(0) if rows > 1 else V, sp, mp, ms, B, W, V, k, max(eos, -1),
-            at, at + 4 * n, at + 8 * n, at + 12 * n, at + 12 * n + 4 * m, at + 12 * n + 8 * m, wp, wn))
+                workspace = _workspace(need, None, dev)
+                s = lib.mx_beam_select(xp, dt, stride, sp, mp, ms, B, W, V, k, max(eos, -1), *op, workspace.data_ptr(), need)
+        _check("mx_beam_select", s)
     return out
 
 
@@ -717,17 +717,24 @@ def kv_remap(pool: PagePool, page_size: int, table: torch.Tensor, kv_len: torch.
     others hold too gets a page and a copy.  Returns the new lengths int32 [S_out] and the copies that
     kv_copy_pages has to make before the cache is used.  Where the pool cannot supply the step, or the arguments do
     not fit, nothing changes, the lengths are -1 and device_error() tells why."""
+    i32 = torch.int32
     tp, ts, tn, S_in = _table_of("table", table)
     op, os_, on, S_out = _table_of("table_out", table_out)
-    lp = _whole("kv_len", kv_len, torch.int32, (S_in,))
-    pp = _whole("parent", parent if parent.dim() == 1 else parent.reshape(-1), torch.int32, (S_out,))
-    kp = None if keep is None else _whole("keep", keep, torch.int32, (S_out,))
-    ap, each = (None, add) if isinstance(add, int) else (_whole("add", add, torch.int32, (S_out,)), 0)
+    size = (S_out,)
+    lp = _whole("kv_len", kv_len, i32, (S_in,))
+    pp = _whole("parent", parent if parent.dim() == 1 else parent.reshape(-1), i32, size)
+    kp = None if keep is None else _whole("keep", keep, i32, size)
+    ap, each = (None, add) if isinstance(add, int) else (_whole("add", add, i32, size), 0)
     if kv_len_out is None:
-        kv_len_out = torch.empty((S_out,), dtype=torch.int32, device=table.device)
+        kv_len_out = torch.empty(size, dtype=i32, device=table.device)
+        np_ = kv_len_out.data_ptr()
+    else:
+        np_ = _whole("kv_len_out", kv_len_out, i32, size)
     if copies is None:
-        copies = torch.empty((1 + S_out, 4), dtype=torch.int32, device=table.device)
-    np_, cp = _whole("kv_len_out", kv_len_out, torch.int32, (S_out,)), _whole("copies", copies, torch.int32, (1 + S_out, 4))
+        copies = torch.empty((1 + S_out, 4), dtype=i32, device=table.device)
+        cp = copies.data_ptr()
+    else:
+        cp = _whole("copies", copies, i32, (1 + S_out, 4))
     _stream()
     _check("mx_kv_remap", load().mx_kv_remap(pool._ref, page_size, tp, ts, tn, lp, S_in, op, os_, on, np_, S_out, pp, kp,
                                              ap, each, cp))
@@ -744,7 +751,9 @@ def kv_compact(pool: PagePool, page_size: int, table: torch.Tensor, kv_len: torc
     rows = 1 + pool.num_pages // 2
     if copies is None:
         copies = torch.empty((rows, 4), dtype=torch.int32, device=table.device)
-    cp = _whole("copies", copies, torch.int32, (rows, 4))
+        cp = copies.data_ptr()
+    else:
+        cp = _whole("copies", copies, torch.int32, (rows, 4))
     _stream()
     _check("mx_kv_compact", load().mx_kv_compact(pool._ref, page_size, tp, ts, tn, lp, S, cp))
     return copies
@@ -831,7 +840,7 @@ def i8_mm(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, x_scales: to
     if M == 0:
         return out
     lib = load()
-    if workspace is None:
+    if workspace is None and M * K > WORKSPACE_SLOT_BYTES // 4:  # (2 bytes an element and 4 a row, rounded up)
         need = lib.mx_i8_mm_workspace_size(M, K)
         if need > WORKSPACE_SLOT_BYTES:
             workspace = _workspace(need, None, x.device)

@@ -15,13 +15,9 @@ def _i32(torch, v):
 
 
 def _clean(pool):
-    """The pool's own memory is as it was made, but for the plan of the last step."""
-    n = 8 * pool.num_pages
-    words = -(-pool.num_pages // 32) * 4
-    w = pool.work
-    at = n + 8 * 4096
-    return not bool(w[:n].any()) and not bool(w[at:at + 4].any()) and not bool(w[at + 12:at + 16].any()) and \
-        not bool(w[at + 16 + 64:at + 16 + 64 + words].any())
+    """The pool's own memory is as it was made: tallies, the word of faults, the bits of freed pages."""
+    n, words = 8 * pool.num_pages, -(-pool.num_pages // 32) * 4
+    return not bool(pool.work[:n + 4].any()) and not bool(pool.work[n + 16 + 64:n + 16 + 64 + words].any())
 
 
 class Session:
