@@ -9,8 +9,9 @@
 // launch per phase.  Everything a phase leaves to the next lies in L2.  The
 // tallies are integer atomics and all orders (pages handed out, pages freed,
 // copies) follow slot and page numbers, so results do not depend on timing.
-// A slot whose pages keep one user needs no tally: only sequences with other
-// than one child touch their pages' counts.
+// A page whose users stay as many needs no tally: neighbouring sequences that hold
+// the same page are counted together, so the prompt of a request's beams, or
+// a sequence that only grows, touches no counts.
 //
 // These kernels write lengths and tables, which other kernels of the library
 // read before they wait for their predecessor; so they do not let their
@@ -27,7 +28,9 @@ namespace mx {
 constexpr int POOL_THREADS = 1024;
 constexpr int POOL_WARPS = POOL_THREADS / 32;
 constexpr int POOL_CLUSTER = 8;  // CTAs of a cluster, the portable most
-constexpr int RUN = 4;           // entries per lane of a warp's task: 128 of one table row
+constexpr int RUN = 4;           // entries per lane of a warp's task: 128 of one table row,
+constexpr int GANG = 8;          // or 16 of each of eight neighbouring rows
+constexpr int NO_ENTRY = -0x7FFFFFFF - 1;
 enum : int { DEVERR_NO_PAGE = MX_DEVERR_NO_PAGE, DEVERR_BAD_SLOT = MX_DEVERR_BAD_SLOT };
 
 // A page's tallies, zero between calls: users gained (or lost) in this step
@@ -156,7 +159,7 @@ __device__ __forceinline__ void all_ctas_or(const void *word, int bits)
 }
 
 // (the plan, of two words a slot, on an even word)
-static __host__ __device__ size_t remap_plan_at(int S_in, int S_out) { return (2 * (size_t)S_in + 4 * (size_t)S_out + 1) / 2 * 2; }
+static __host__ __device__ size_t remap_plan_at(int S_in, int S_out) { return (4 * (size_t)S_in + 4 * (size_t)S_out + 1) / 2 * 2; }
 static size_t remap_smem(int S_in, int S_out) { return sizeof(int) * (remap_plan_at(S_in, S_out) + 2 * (size_t)S_out); }
 
 // The first thing a step needs is every sequence's length and every slot's
@@ -168,7 +171,9 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
     const PoolWork &w = a.w;
     extern __shared__ int dyn[];
     int *children = dyn;                                        // [S_in]
-    int *lens = children + c.S_in;                              // [S_in]
+    int *cuts = children + c.S_in;                              // [S_in] what a lone child that keeps a part keeps
+    int *rows = cuts + c.S_in;                                  // [S_in]
+    int *lens = rows + c.S_in;                                  // [S_in]
     Slot *slots = reinterpret_cast<Slot *>(lens + c.S_in);      // [S_out]
     int2 *plan = reinterpret_cast<int2 *>(dyn + remap_plan_at(c.S_in, c.S_out));  // [S_out] of CTA 0: first page handed out, copy's number + 1
     int *tails = lens + c.S_in + 3 * c.S_out;                   // [S_out] of CTA 0: page a growing slot writes in, or -1
@@ -210,38 +215,62 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
         n.tokens = (int)min(tokens, 0x7FFFFFFFll);
         rows_out = max(rows_out, min(pages_of(n.tokens, ps), c.out_pages));
         slots[s] = n;
-        if (n.parent >= 0) atomicAdd(children + n.parent, n.kept == len ? 1 : CUT_CHILD);
+        if (n.parent >= 0) {
+            atomicAdd(children + n.parent, n.kept == len ? 1 : CUT_CHILD);
+            if (n.kept < len) cuts[n.parent] = n.kept;  // (used where there is one)
+        }
     }
     rows_in = block_max(rows_in, sh.smax);
     rows_out = block_max(rows_out, sh.smax);
     const int chunks_in = (rows_in + 32 * RUN - 1) / (32 * RUN), chunks_out = (rows_out + 32 * RUN - 1) / (32 * RUN);
+    // pages and, of what it leaves its child, full pages of each sequence
+    for (int p = tid; p < c.S_in; p += POOL_THREADS) {
+        rows[p] = min(pages_of(lens[p], ps), c.in_pages);
+        cuts[p] = (children[p] == CUT_CHILD ? cuts[p] : lens[p]) / ps;
+    }
+    __syncthreads();
 
-    // f(sequence's children, page, users) for the old tables' entries of this
-    // warp's tasks; users: those that the step leaves this entry's page
-    // through it, the children that keep the whole sequence, of its full pages (its
-    // partial one is counted by each child), less the entry itself.  The first task's entries
-    // stay in registers.
+    // f(page, users, special) for the old tables' entries of this warp's tasks:
+    // a lane takes one of GANG neighbouring sequences and four columns.
+    // Neighbours that hold the same page (beams of one request, a common
+    // prefix) count as one.  users: what the step leaves the page through these entries, the
+    // children that keep the sequence beyond the page (a lone child that keeps a
+    // part of it counts here, others by themselves), less the entries.
+    // special: the page may have been counted by a child itself.  The first
+    // task's entries stay in registers.
+    const int gangs = (c.S_in + GANG - 1) / GANG, columns = (rows_in + 4 * RUN - 1) / (4 * RUN);
     int own[RUN];
     bool have_own = false;
     auto old_entries = [&](auto f) {
-        for (int t = gw; t < c.S_in * chunks_in; t += nw) {
-            const int p = t % c.S_in, j0 = t / c.S_in * (32 * RUN);
-            const int len = lens[p], n = min(pages_of(len, ps), c.in_pages);
-            if (j0 >= n) continue;
+        for (int t = gw; t < gangs * columns; t += nw) {
+            const int p = t % gangs * GANG + lane % GANG, j0 = t / gangs * (4 * RUN) + lane / GANG;
+            const int n = p < c.S_in ? rows[p] : 0, full = p < c.S_in ? cuts[p] : 0, kids = p < c.S_in ? children[p] : 0;
+            const int there = kids == CUT_CHILD ? 1 : kids % CUT_CHILD;
             const int32_t *row = c.table_in + (long long)p * c.in_stride;
             int page[RUN];
 #pragma unroll
             for (int i = 0; i < RUN; ++i) {
-                const int j = j0 + 32 * i + lane;
+                const int j = j0 + 4 * i;
                 if (t == gw && have_own) page[i] = own[i];
-                else page[i] = j < n ? __ldcg(row + j) : -1;
-                if (t == gw) own[i] = page[i];
+                else page[i] = j < n ? max(__ldcg(row + j), -1) : NO_ENTRY;
             }
-            const int kids = children[p];
 #pragma unroll
             for (int i = 0; i < RUN; ++i) {
-                const int j = j0 + 32 * i + lane;
-                if (j < n) f(kids, page[i], (j < len / ps ? kids % CUT_CHILD : 0) - 1);
+                const int j = j0 + 4 * i;
+                if (t == gw) own[i] = page[i];
+                // runs of the same page: from a first lane up to the next's
+                const int left = __shfl_up_sync(0xFFFFFFFFu, page[i], 1);
+                const bool first = lane % GANG == 0 || page[i] != left;
+                const unsigned firsts = __ballot_sync(0xFFFFFFFFu, first) >> lane >> 1;
+                const int run = firsts ? __ffs((int)firsts) : 32 - lane;
+                int users = (j < full ? there : 0) - 1;
+#pragma unroll
+                for (int o = 1; o < GANG; o <<= 1) {
+                    const int more = __shfl_down_sync(0xFFFFFFFFu, users, o);
+                    if (o < run) users += more;
+                }
+                const unsigned special = __ballot_sync(0xFFFFFFFFu, j == full || kids > CUT_CHILD) >> lane;
+                if (first && page[i] != NO_ENTRY) f(page[i], users, (special & ((2u << (run - 1)) - 1u)) != 0u);
             }
         }
         have_own = true;
@@ -262,16 +291,16 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
             }
             tails[s] = tail;
         }
-    old_entries([&](int, int page, int d) {
+    old_entries([&](int page, int d, bool) {
         if ((unsigned)page >= (unsigned)P) fault |= DEVERR_BAD_PAGE;
         else if (d != 0) atomicAdd(&w.tally[page].users, d);
     });
-    // full pages of those that take a part
+    // full pages of those that take a part, with others of the same parent
     if (c.keep)
         for (int t = gw; t < c.S_out * chunks_in; t += nw) {
             const int s = t % c.S_out, j0 = t / c.S_out * (32 * RUN);
             const Slot n = slots[s];
-            if (n.parent < 0 || n.kept == lens[n.parent]) continue;
+            if (n.parent < 0 || n.kept == lens[n.parent] || children[n.parent] == CUT_CHILD) continue;
             const int32_t *row = c.table_in + (long long)n.parent * c.in_stride;
             const int full = min(n.kept / ps, c.in_pages);
             for (int j = j0 + lane; j < min(full, j0 + 32 * RUN); j += 32) {
@@ -329,7 +358,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
                 sh.copies = (int)(total / COPY);
             }
         }
-        old_entries([&](int, int page, int d) {
+        old_entries([&](int page, int d, bool) {
             if (d >= 0) return;
             const PageTally t = tally_at(w.tally, page);
             const int left = __ldcg(c.pool.refs + page) + t.users;
@@ -343,7 +372,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
     // ---- all or nothing
     fault |= *(volatile int *)&sh.late;
     if (fault) {
-        old_entries([&](int, int page, int) {
+        old_entries([&](int page, int, bool) {
             if ((unsigned)page >= (unsigned)P) return;
             w.tally[page] = PageTally{0, 0};
             w.freed[page >> 5] = 0u;
@@ -388,8 +417,8 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
         }
         if (j0 == 0 && lane == 0) c.kv_len_out[s] = n.tokens;
     }
-    old_entries([&](int kids, int page, int d) {
-        if (d == 0 && kids < CUT_CHILD) return;
+    old_entries([&](int page, int d, bool special) {
+        if (d == 0 && !special) return;
         // whoever comes first takes the tally
         const int refs = __ldcg(c.pool.refs + page);
         const unsigned long long v = atomicExch(reinterpret_cast<unsigned long long *>(w.tally + page), 0ull);
