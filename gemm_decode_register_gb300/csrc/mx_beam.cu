@@ -7,8 +7,9 @@
 //
 // One launch.  The rows, laid end to end in steps of four
 // 16-byte vectors per thread, are cut into equal stretches, one for each
-// block that fits on the GPU; a block walks its own with the next step's loads
-// in flight, over row ends too.  Within a row the order of the keys is that
+// block that fits on the GPU; a block walks its own with the next three steps'
+// copies to shared memory in flight (cp.async; each thread reads back its own),
+// over row ends too.  Within a row the order of the keys is that
 // of the logits, so a row's part of a stretch (a piece) needs no more of its row
 // than itself:
 //   - the largest element of each vector (packed maxima) and thread.  In the
@@ -45,8 +46,12 @@ constexpr int BEAM_THREADS = 256;
 constexpr int BEAM_WARPS = BEAM_THREADS / 32;
 constexpr int BEAM_U = 4;                      // vectors of a thread and step
 constexpr int BEAM_STEP = BEAM_THREADS * BEAM_U;  // vectors of a step
-constexpr int BEAM_QUEUE = 512;   // vectors that reach a piece's bound
-constexpr int BEAM_FOUND = 1024;  // elements that do (a piece's, a batch entry's)
+constexpr int BEAM_RING = 4;                      // steps in shared memory
+constexpr int BEAM_BLOCKS = 3;                    // blocks of an SM
+constexpr int BEAM_QUEUE = 256;   // vectors that reach a piece's bound
+constexpr int BEAM_FOUND = 512;   // elements that do
+constexpr int BEAM_JOIN = 1024;   // and a batch entry's
+constexpr int BEAM_ENTRIES = 4096;  // of the lists, in the join's shared memory
 
 struct BeamArgs {
     const void *logits;
@@ -75,11 +80,12 @@ __device__ __forceinline__ float unordered(uint32_t o)
 {
     return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
-// The first stretch with a step of a row, and how many there are.
-__device__ __forceinline__ int first_stretch(const BeamArgs &a, int row) { return (int)((long long)row * a.steps / a.span); }
+// The first stretch with a step of a row, and how many there are.  (All rows'
+// steps are at most 2^24: a row of 2^20 logits has 257, there are 2^16 rows.)
+__device__ __forceinline__ int first_stretch(const BeamArgs &a, int row) { return (int)((unsigned)(row * a.steps) / (unsigned)a.span); }
 __device__ __forceinline__ int pieces_of(const BeamArgs &a, int row)
 {
-    return (int)(((long long)(row + 1) * a.steps - 1) / a.span) - first_stretch(a, row) + 1;
+    return (int)((unsigned)((row + 1) * a.steps - 1) / (unsigned)a.span) - first_stretch(a, row) + 1;
 }
 
 constexpr uint32_t ORD_NEG_INF = 0x007FFFFFu;
@@ -262,68 +268,112 @@ __device__ __forceinline__ Pair log_sum(float m, float t)
 }
 
 struct JoinSmem {
+    unsigned long long entry[BEAM_ENTRIES];  // the lists' first `staged`, list after list
+    unsigned long long key[BEAM_JOIN], lt[BEAM_JOIN];
+    uint8_t beam[BEAM_JOIN], beam_of[BEAM_ENTRIES / 4];  // a candidate's, a list's
     float score[BEAM_MAX_W];
     Pair lse[BEAM_MAX_W];  // NaN: the beam has no candidates
     float2 part[BEAM_MAX_W];
-    unsigned long long key[BEAM_FOUND], lt[BEAM_FOUND];
-    uint8_t beam[BEAM_FOUND];
     uint32_t warp_bound[BEAM_WARPS];
     float out_score[BEAM_MAX_K];
     int out_parent[BEAM_MAX_K], out_token[BEAM_MAX_K], n_found;
 };
 
+// Within `off` of a candidate's key, in fp32; NaN: no candidate.
+__device__ __forceinline__ float key_about(const JoinSmem &sm, int row, unsigned long long l, float &off)
+{
+    const float c = sm.score[row], s = sm.lse[row].h, x = unordered((uint32_t)(l >> 32));
+    off = (fabsf(c) + fabsf(x) + fabsf(s)) * 2.3841858e-7f;  // three roundings of a quarter of that, and one spare
+    return l != 0ull ? c + (x - s) : NAN;
+}
+// The key as a whole number in its order: both floats of the pair.
+__device__ __forceinline__ unsigned long long key_exact(const JoinSmem &sm, int row, unsigned long long l)
+{
+    const Pair d = two_sum(unordered((uint32_t)(l >> 32)), -sm.lse[row].h);
+    const Pair k = two_sum(sm.score[row], d.h);
+    const Pair f = two_sum(k.h, k.l + (d.l - sm.lse[row].l));
+    return (unsigned long long)ordered(f.h + 0.0f) << 32 | ordered(f.l + 0.0f);
+}
+
+// More candidates than fit reach the bound (long ties between beams): one after
+// the other, each the best of what follows the last.
+__device__ __noinline__ void join_one_by_one(const BeamArgs &a, JoinSmem &sm, const unsigned long long *best, int b)
+{
+    const int tid = threadIdx.x, lists = a.W * a.pieces;
+    unsigned long long pk = 0xFFFFFFFFFFFFFFFFull, pl = 0;
+    int pr = -1;
+    for (int i = 0; i < a.k; ++i) {
+        unsigned long long mk = 0ull, ml = 0ull;
+        int mr = 0x7FFFFFFF;
+        for (int l = tid; l < lists; l += BEAM_THREADS) {
+            const int row = l / a.pieces;
+            if (!(sm.lse[row].h == sm.lse[row].h) || l - row * a.pieces >= pieces_of(a, b * a.W + row)) continue;
+            for (int e = 0; e < a.k; ++e) {
+                const unsigned long long h = __ldcg(best + (size_t)l * a.kpad + e);
+                if (h == 0ull) break;
+                const unsigned long long c = key_exact(sm, row, h);
+                if (pr >= 0 && !before(pk, pr, pl, c, row, h)) continue;
+                if (before(c, row, h, mk, mr, ml)) {
+                    mk = c;
+                    mr = row;
+                    ml = h;
+                }
+                break;  // (the list's next are later in the order)
+            }
+        }
+        __syncthreads();
+        sm.key[tid] = mk;
+        sm.lt[tid] = ml;
+        sm.beam[tid] = (uint8_t)(mr & 255);
+        __syncthreads();
+        for (int j = 0; j < BEAM_THREADS; ++j)
+            if (before(sm.key[j], sm.beam[j], sm.lt[j], mk, mr, ml)) {
+                mk = sm.key[j];
+                mr = sm.beam[j];
+                ml = sm.lt[j];
+            }
+        pk = mk;
+        pr = mr;
+        pl = ml;
+        if (tid == 0) {
+            sm.out_score[i] = unordered((uint32_t)(mk >> 32));
+            sm.out_parent[i] = b * a.W + mr;
+            sm.out_token[i] = (int)(0xFFFFFFFFu - (uint32_t)ml);
+        }
+    }
+}
+
+// (Loops are left rolled: this code runs once per block, and what it takes is the
+// fetching of its instructions more than their execution.)
 __device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int lists = a.W * a.pieces;
     const unsigned long long *best = a.best + (size_t)b * lists * a.kpad;
-    float *score = sm.score, *out_score = sm.out_score;
-    Pair *lse = sm.lse;
-    unsigned long long *key = sm.key, *lt = sm.lt;
-    uint8_t *beam = sm.beam;
-    int *out_parent = sm.out_parent, *out_token = sm.out_token;
+    // as many of each list as fit, in groups of four (there are at most some 700 lists)
+    const int depth = min(a.kpad / 4, max(1, BEAM_ENTRIES / 4 / lists)), staged = 4 * depth;
 
-    // Four entries of a list are a group; groups in the order of their depth,
-    // then of the list.  The first R groups of each thread stay in registers.
-    // (lane, warp) -> group: each warp sees all beams and depths.
-    constexpr int R = 3;
-    const int groups = lists * (a.kpad / 4), warps = min(BEAM_WARPS, (groups + 31) / 32);
-    const int mine = warp < warps ? lane * warps + (warp + lane + (lane >> 2)) % warps : groups;
-    struct Group {
-        unsigned long long v[4];
-        int row;
-    };
-    auto fetch = [&](int g) {
-        Group q;
-        const int l = g % lists, d = g / lists;
-        q.row = l / a.pieces;
-        if (l - q.row * a.pieces >= pieces_of(a, b * a.W + q.row)) {
-            q.v[0] = q.v[1] = q.v[2] = q.v[3] = 0ull;
-            return q;
-        }
-        const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(best + (size_t)l * a.kpad + 4 * d);
-        const ulonglong2 x = __ldcg(p), y = __ldcg(p + 1);
-        q.v[0] = x.x;
-        q.v[1] = x.y;
-        q.v[2] = y.x;
-        q.v[3] = y.y;
-        return q;
-    };
-    Group q[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int g = mine + i * 32 * warps;
-        if (g < groups) q[i] = fetch(g);
-        else q[i] = Group{{0ull, 0ull, 0ull, 0ull}, 0};
-    }
     const float own_score = tid < a.W ? __ldcg(a.scores + (size_t)b * a.W + tid) : 0.0f;
-    // the rows' sums
+    // a warp per row: its sums, its lists
+#pragma unroll 1
     for (int w = warp; w < a.W; w += BEAM_WARPS) {
-        const float2 *p = a.sums + ((size_t)b * a.W + w) * a.pieces;
+        const size_t first = ((size_t)b * a.W + w) * a.pieces;
         const int pieces = pieces_of(a, b * a.W + w);
         float m = -INFINITY, t = 0.0f;
-        for (int c = lane; c < pieces; c += 32) {
-            const float2 v = __ldcg(p + c);
+        // (a row has up to 257 pieces)
+#pragma unroll 1
+        for (int c0 = 0; c0 < a.pieces; c0 += 32) {
+            const int c = c0 + lane;
+            const float2 v = c < pieces ? __ldcg(a.sums + first + c) : make_float2(-INFINITY, 0.0f);
+            const int entries = min(32, a.pieces - c0) * depth * 2;  // in pairs
+#pragma unroll 4
+            for (int i = lane; i < entries; i += 32) {
+                const int l = i / (2 * depth), p = i - l * (2 * depth);  // list, pair
+                ulonglong2 e = make_ulonglong2(0ull, 0ull);
+                if (c0 + l < pieces) e = __ldcg(reinterpret_cast<const ulonglong2 *>(a.best + (first + c0 + l) * a.kpad) + p);
+                reinterpret_cast<ulonglong2 *>(sm.entry)[(w * a.pieces + c0 + l) * (2 * depth) + p] = e;
+            }
+            if (c < a.pieces) sm.beam_of[w * a.pieces + c] = (uint8_t)w;
             const float nm = fmaxf(m, v.x);
             // (equal maxima, infinite ones too: no scaling; NaN sums stay)
             t = (m == nm ? t : t * __expf(m - nm)) + (v.x == nm ? v.y : v.y * __expf(v.x - nm));
@@ -343,33 +393,27 @@ __device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b
         const float2 p = sm.part[tid];
         // NaN sums: a NaN or +inf among the logits; nothing allowed: no maximum
         const bool ok = p.y > 0.0f && fabsf(p.x) < INFINITY && fabsf(own_score) < INFINITY;
-        score[tid] = own_score;
-        lse[tid] = ok ? log_sum(p.x, p.y) : Pair{NAN, NAN};
+        sm.score[tid] = own_score;
+        sm.lse[tid] = ok ? log_sum(p.x, p.y) : Pair{NAN, NAN};
     }
     __syncthreads();
 
-    // Within `off` of a candidate's key, in fp32; NaN: no candidate.
-    auto about = [&](int row, unsigned long long l, float &off) {
-        const float c = score[row], s = lse[row].h, x = unordered((uint32_t)(l >> 32));
-        off = (fabsf(c) + fabsf(x) + fabsf(s)) * 2.3841858e-7f;  // three roundings of a quarter of that, and one spare
-        return l != 0ull ? c + (x - s) : NAN;
-    };
-    // The key as a whole number in its order: both floats of the pair.
-    auto exact = [&](int row, unsigned long long l) {
-        const Pair d = two_sum(unordered((uint32_t)(l >> 32)), -lse[row].h);
-        const Pair k = two_sum(score[row], d.h);
-        const Pair f = two_sum(k.h, k.l + (d.l - lse[row].l));
-        return (unsigned long long)ordered(f.h + 0.0f) << 32 | ordered(f.l + 0.0f);
-    };
-    // A bound that k candidates reach, from the thread's first group.
+    // A bound that k candidates reach, from one group of a list for each lane:
+    // groups in the order of their depth, dealt out so that each warp sees all
+    // beams and depths.
+    const int groups = lists * depth, warps = min(BEAM_WARPS, (groups + 31) / 32);
+    const int mine = lane * warps + (warp + lane + (lane >> 2)) % warps;
     uint32_t bound = 0xFFFFFFFFu;
     if (warp < warps) {
-        uint32_t low[4];
+        uint32_t low[4] = {0u, 0u, 0u, 0u};
+        if (mine < groups) {
+            const int l = mine % lists, row = sm.beam_of[l];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float off;
-            const float f = about(q[0].row, q[0].v[i], off);
-            low[i] = f > -INFINITY ? ordered((f - off) + 0.0f) : 0u;
+            for (int i = 0; i < 4; ++i) {
+                float off;
+                const float f = key_about(sm, row, sm.entry[l * staged + 4 * (mine / lists) + i], off);
+                low[i] = f > -INFINITY ? ordered((f - off) + 0.0f) : 0u;
+            }
         }
         // (rounded down in fp32, the entries still descend)
         bound = warp_nth(low[0], (a.k + warps - 1) / warps, [&] {
@@ -385,124 +429,89 @@ __device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b
     bound = __reduce_min_sync(0xFFFFFFFFu, sm.warp_bound[lane % BEAM_WARPS]);
     const float least = bound == 0u ? -FLT_MAX : unordered(bound);
 
-    // what may reach it
-    auto gather = [&](const Group &p) {
-        bool any = false;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
+    // what may reach it, of the staged entries, and of those behind them where a
+    // list's last staged one does (lists descend)
+    auto offer = [&](int row, unsigned long long l) {
+        float off;
+        const float f = key_about(sm, row, l, off);
+        if (!(f + off >= least && f > -INFINITY)) return false;
+        const int at = atomicAdd(&sm.n_found, 1);
+        if (at < BEAM_JOIN) {
+            sm.lt[at] = l;
+            sm.beam[at] = (uint8_t)row;
+        }
+        return true;
+    };
+#pragma unroll 1
+    for (int e = tid; e < lists * staged; e += BEAM_THREADS) offer(sm.beam_of[e / staged], sm.entry[e]);
+    if (staged < a.kpad)
+#pragma unroll 1
+        for (int l = tid; l < lists; l += BEAM_THREADS) {
+            const int row = sm.beam_of[l];
             float off;
-            const float f = about(p.row, p.v[j], off);
-            if (f + off >= least && f > -INFINITY) {
-                const int at = atomicAdd(&sm.n_found, 1);
-                if (at < BEAM_FOUND) {
-                    lt[at] = p.v[j];
-                    beam[at] = (uint8_t)p.row;
-                }
-                any = true;
+            const float f = key_about(sm, row, sm.entry[l * staged + staged - 1], off);
+            if (!(f + off >= least)) continue;
+#pragma unroll 1
+            for (int e = staged; e < a.k && offer(row, __ldcg(best + (size_t)l * a.kpad + e)); ++e) {
             }
         }
-        return any;
-    };
-#pragma unroll
-    for (int i = 0; i < R; ++i) gather(q[i]);
-    // more groups than registers: until as many in a row as there are lists
-    // have nothing (lists descend)
-    for (int g0 = R * 32 * warps, idle = 0; g0 < groups && idle < lists; g0 += BEAM_THREADS) {
-        const bool any = g0 + tid < groups && gather(fetch(g0 + tid));
-        idle = __syncthreads_or(any) ? 0 : idle + BEAM_THREADS;
-    }
     __syncthreads();
     const int n = sm.n_found;
-    if (n <= BEAM_FOUND) {
-        for (int i = tid; i < n; i += BEAM_THREADS) key[i] = exact(beam[i], lt[i]);
+    if (n <= BEAM_JOIN) {
+#pragma unroll 1
+        for (int i = tid; i < n; i += BEAM_THREADS) sm.key[i] = key_exact(sm, sm.beam[i], sm.lt[i]);
         __syncthreads();
+#pragma unroll 1
         for (int i = tid; i < n; i += BEAM_THREADS) {
-            const unsigned long long ki = key[i], li = lt[i];
-            const int ri = beam[i];
+            const unsigned long long ki = sm.key[i], li = sm.lt[i];
+            const int ri = sm.beam[i];
             int rank = 0;
+#pragma unroll 2
             for (int j = 0; j < n; ++j) {
-                const unsigned long long kj = key[j];
-                rank += kj > ki || (kj == ki && before(kj, beam[j], lt[j], ki, ri, li));
+                const unsigned long long kj = sm.key[j];
+                rank += kj > ki;
+                if (kj == ki && j != i) rank += before(kj, sm.beam[j], sm.lt[j], ki, ri, li);
             }
             if (rank < a.k) {
-                out_score[rank] = unordered((uint32_t)(ki >> 32));
-                out_parent[rank] = b * a.W + ri;
-                out_token[rank] = (int)(0xFFFFFFFFu - (uint32_t)li);
+                sm.out_score[rank] = unordered((uint32_t)(ki >> 32));
+                sm.out_parent[rank] = b * a.W + ri;
+                sm.out_token[rank] = (int)(0xFFFFFFFFu - (uint32_t)li);
             }
         }
         for (int i = n + tid; i < a.k; i += BEAM_THREADS) {
-            out_score[i] = -INFINITY;
-            out_parent[i] = -1;
-            out_token[i] = 0;
+            sm.out_score[i] = -INFINITY;
+            sm.out_parent[i] = -1;
+            sm.out_token[i] = 0;
         }
     } else {
-        // more than fit (long ties between beams): one after the other, each
-        // the best of what follows the last
-        unsigned long long pk = 0xFFFFFFFFFFFFFFFFull, pl = 0;
-        int pr = -1;
-        for (int i = 0; i < a.k; ++i) {
-            unsigned long long mk = 0ull, ml = 0ull;
-            int mr = 0x7FFFFFFF;
-            for (int l = tid; l < lists; l += BEAM_THREADS) {
-                const int row = l / a.pieces;
-                if (!(lse[row].h == lse[row].h) || l - row * a.pieces >= pieces_of(a, b * a.W + row)) continue;
-                for (int e = 0; e < a.k; ++e) {
-                    const unsigned long long h = __ldcg(best + (size_t)l * a.kpad + e);
-                    if (h == 0ull) break;
-                    const unsigned long long c = exact(row, h);
-                    if (pr >= 0 && !before(pk, pr, pl, c, row, h)) continue;
-                    if (before(c, row, h, mk, mr, ml)) {
-                        mk = c;
-                        mr = row;
-                        ml = h;
-                    }
-                    break;  // (the list's next are later in the order)
-                }
-            }
-            __syncthreads();
-            key[tid] = mk;
-            lt[tid] = ml;
-            beam[tid] = (uint8_t)(mr & 255);
-            __syncthreads();
-            for (int j = 0; j < BEAM_THREADS; ++j)
-                if (before(key[j], beam[j], lt[j], mk, mr, ml)) {
-                    mk = key[j];
-                    mr = beam[j];
-                    ml = lt[j];
-                }
-            pk = mk;
-            pr = mr;
-            pl = ml;
-            if (tid == 0) {
-                out_score[i] = unordered((uint32_t)(mk >> 32));
-                out_parent[i] = b * a.W + mr;
-                out_token[i] = (int)(0xFFFFFFFFu - (uint32_t)ml);
-            }
-        }
+        join_one_by_one(a, sm, best, b);
     }
     __syncthreads();
+#pragma unroll 1
     for (int i = tid; i < a.k; i += BEAM_THREADS) {
         const size_t at = (size_t)b * a.k + i;
-        a.score[at] = out_score[i];
-        a.parent[at] = out_parent[i];
-        a.token[at] = out_token[i];
+        a.score[at] = sm.out_score[i];
+        a.parent[at] = sm.out_parent[i];
+        a.token[at] = sm.out_token[i];
     }
     // the first W that do not end go on
     if (warp == 0 && a.next_token != nullptr) {
         int at = 0;
+#pragma unroll 1
         for (int i0 = 0; i0 < a.k && at < a.W; i0 += 32) {
             const int i = i0 + lane;
-            const bool on = i < a.k && out_parent[i] >= 0 && out_token[i] != a.eos;
+            const bool on = i < a.k && sm.out_parent[i] >= 0 && sm.out_token[i] != a.eos;
             const unsigned g = __ballot_sync(0xFFFFFFFFu, on);
             const int o = at + __popc(g & ((1u << lane) - 1u));
             if (on && o < a.W) {
                 const size_t q = (size_t)b * a.W + o;
-                a.next_score[q] = out_score[i];
-                a.next_parent[q] = out_parent[i];
-                a.next_token[q] = out_token[i];
+                a.next_score[q] = sm.out_score[i];
+                a.next_parent[q] = sm.out_parent[i];
+                a.next_token[q] = sm.out_token[i];
             }
             at += __popc(g);
         }
+#pragma unroll 1
         for (int o = at + lane; o < a.W; o += 32) {
             const size_t q = (size_t)b * a.W + o;
             a.next_score[q] = -INFINITY;
@@ -531,25 +540,81 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t *row, int e, int wo
 }
 
 struct ChunkSmem {
+    uint4 ring[BEAM_RING][BEAM_STEP];
     uint4 queue[BEAM_QUEUE];
     int queue_at[BEAM_QUEUE];  // the vector's first token
     unsigned long long found[BEAM_FOUND];
 };
+static_assert(sizeof(JoinSmem) <= sizeof(ChunkSmem), "the join's shared memory lies over the stretch's");
+static_assert(BEAM_QUEUE <= BEAM_THREADS, "a thread for each vector");
+static_assert(BEAM_BLOCKS * (sizeof(ChunkSmem) + 1024 + 256) <= 228 * 1024, "blocks of an SM");
+
+// 16 bytes to shared memory.
+__device__ __forceinline__ void copy_async16(uint4 *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Too many elements of a piece reach its bound (ties, most often): the k largest
+// (logit, token) of tokens t0 .. t1 - 1 into found, by bisection over the
+// whole piece, read once per round.  Nothing outside [lo, ..) is among them.
+template <typename E, bool MASK>
+__device__ __noinline__ void piece_exact(const E *x, const uint32_t *mask, int t0, int t1, int V, int k, unsigned long long lo,
+                                         unsigned long long *found, int *n_found, int *scratch)
+{
+    using L = Elem<E>;
+    constexpr int VEC = L::VEC;
+    auto each = [&](auto f) {
+#pragma unroll 1
+        for (int e = t0 + (int)threadIdx.x * VEC; e < t1; e += BEAM_THREADS * VEC) {
+            uint4 v;
+            if (e >= 0 && e + VEC <= V) v = __ldcg(reinterpret_cast<const uint4 *>(x + e));
+            else v = edge_vector(x + e, e < 0 ? -e : 0, min(VEC, V - e));
+            if constexpr (MASK) L::keep(v, mask_bits<VEC>(mask, e, (V + 31) >> 5));
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) f(logit_token(L::get(v, j), e + j));
+        }
+    };
+    unsigned long long hi = 0xFFFFFFFFFFFFFFFFull;
+    while (lo < hi) {
+        const unsigned long long mid = lo + (hi - lo) / 2 + 1;
+        int c = 0;
+        each([&](unsigned long long v) { c += v >= mid; });
+        c = block_sum(c, scratch);
+        if (c >= k) lo = mid;
+        else hi = mid - 1;
+        if (c == k) break;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) *n_found = 0;
+    __syncthreads();
+    each([&](unsigned long long v) {
+        if (v >= lo) found[atomicAdd(n_found, 1)] = v;
+    });
+}
 
 template <typename E, bool MASK>
-__global__ void __launch_bounds__(BEAM_THREADS, MASK ? 2 : 4) beam_kernel(const __grid_constant__ BeamArgs a)
+__global__ void __launch_bounds__(BEAM_THREADS, BEAM_BLOCKS) beam_kernel(const __grid_constant__ BeamArgs a)
 {
     using L = Elem<E>;
     constexpr int VEC = L::VEC, U = BEAM_U;
-    __shared__ __align__(16) uint8_t smem[sizeof(ChunkSmem) > sizeof(JoinSmem) ? sizeof(ChunkSmem) : sizeof(JoinSmem)];
-    uint4 *queue = reinterpret_cast<ChunkSmem *>(smem)->queue;
-    int *queue_at = reinterpret_cast<ChunkSmem *>(smem)->queue_at;
-    unsigned long long *found = reinterpret_cast<ChunkSmem *>(smem)->found;
+    extern __shared__ __align__(16) uint8_t smem[];
+    ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(smem);
+    uint4 *queue = sm.queue;
+    int *queue_at = sm.queue_at;
+    unsigned long long *found = sm.found;
     __shared__ float warp_ref[BEAM_WARPS], warp_sum[BEAM_WARPS];
     __shared__ uint32_t warp_bound[BEAM_WARPS];
-    __shared__ int n_queue, n_found, joins, scratch[BEAM_WARPS];
+    __shared__ int n_queue[2], n_found, joins, scratch[BEAM_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-    if (tid == 0) n_queue = n_found = 0;
+    if (tid == 0) n_queue[0] = n_queue[1] = n_found = 0;
+    int turn = 0;
     pdl_trigger();
     pdl_wait();
     const int words = (a.V + 31) >> 5;
@@ -564,17 +629,30 @@ __global__ void __launch_bounds__(BEAM_THREADS, MASK ? 2 : 4) beam_kernel(const 
         const E *x = static_cast<const E *>(a.logits) + (size_t)row * a.row_stride;
         return Row{x, -(int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(E))};
     };
-    auto load = [&](uint4 (&v)[U], const Row &r, int e0) {  // the step whose first token is e0
+    // the step whose first token is e0: to the ring, and from there (or, of its
+    // vectors that the row covers in part, element by element)
+    auto fetch = [&](int slot, const E *x, int e0) {
+        uint4 *d = &sm.ring[slot][tid];
+        const uint4 *p = reinterpret_cast<const uint4 *>(x + e0) + tid;
         if (e0 >= 0 && e0 + BEAM_STEP * VEC <= a.V) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(r.x + e0) + tid;
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = __ldcs(p + u * BEAM_THREADS);
+            for (int u = 0; u < U; ++u) copy_async16(d + u * BEAM_THREADS, p + u * BEAM_THREADS);
         } else {
+#pragma unroll 1
+            for (int u = 0; u < U; ++u) {
+                const int e = e0 + (u * BEAM_THREADS + tid) * VEC;
+                if (e >= 0 && e + VEC <= a.V) copy_async16(d + u * BEAM_THREADS, p + u * BEAM_THREADS);
+            }
+        }
+    };
+    auto take = [&](uint4 (&v)[U], int slot, const E *x, int e0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = sm.ring[slot][u * BEAM_THREADS + tid];
+        if (e0 < 0 || e0 + BEAM_STEP * VEC > a.V) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int e = e0 + (u * BEAM_THREADS + tid) * VEC;
-                if (e >= 0 && e + VEC <= a.V) v[u] = __ldcs(reinterpret_cast<const uint4 *>(r.x + e));
-                else v[u] = edge_vector(r.x + e, e < 0 ? -e : 0, min(VEC, a.V - e));
+                if (e < 0 || e + VEC > a.V) v[u] = edge_vector(x + e, e < 0 ? -e : 0, min(VEC, a.V - e));
             }
         }
     };
@@ -597,56 +675,93 @@ __global__ void __launch_bounds__(BEAM_THREADS, MASK ? 2 : 4) beam_kernel(const 
         if (n > ORD_NEG_INF) bound = fmaxf(bound, unordered(n));
         __syncthreads();
     };
-    // the queue's elements that reach the bound are found, a thread for each; the
-    // queue is empty after it
+    // the queue's elements that reach the bound are found, a thread for each
+    // vector; later pushes go to the other counter.  One barrier.
     auto drain = [&] {
-        const int n = min(n_queue, BEAM_QUEUE) * VEC;
-        for (int i0 = 0; i0 < n; i0 += BEAM_THREADS) {
-            const int i = i0 + tid;
-            const float f = i < n ? L::one(queue, i) : -INFINITY;
-            const unsigned hit = __ballot_sync(0xFFFFFFFFu, f >= bound);
-            if (hit == 0u) continue;
-            int o = 0;
-            if (lane == 0) o = atomicAdd(&n_found, __popc(hit));
-            o = __shfl_sync(0xFFFFFFFFu, o, 0) + __popc(hit & ((1u << lane) - 1u));
-            if (f >= bound && o < BEAM_FOUND) found[o] = logit_token(f, queue_at[i / VEC] + i % VEC);
+        const int n = min(n_queue[turn], BEAM_QUEUE);
+        if (warp * 32 < n) {
+            unsigned hits = 0u;
+            if (tid < n) {
+                const uint4 v = queue[tid];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) hits |= (L::get(v, j) >= bound ? 1u : 0u) << j;
+            }
+            int o = __popc(hits);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int before = __shfl_up_sync(0xFFFFFFFFu, o, d);
+                if (lane >= d) o += before;
+            }
+            int base = 0;
+            if (lane == 31) base = atomicAdd(&n_found, o);
+            o += __shfl_sync(0xFFFFFFFFu, base, 31) - __popc(hits);
+            for (; hits; hits &= hits - 1, ++o) {
+                const int j = __ffs((int)hits) - 1;
+                if (o < BEAM_FOUND) found[o] = logit_token(L::one(queue, tid * VEC + j), queue_at[tid] + j);
+            }
         }
         __syncthreads();
-        if (tid == 0) n_queue = 0;
+        if (tid == 0) n_queue[turn] = 0;
+        turn ^= 1;
     };
-    // the bound from what is found so far, dealt out over the warps: each
-    // thread's largest of up to four
-    auto raise_by_found = [&] {
+    // the bound from what is found so far, dealt out over the warps (each
+    // thread's larger of two); what no longer reaches it is dropped.  Nothing
+    // where little is found: that is ranked sooner than sifted.
+    auto sift = [&] {
         const int n = n_found;
+        if (n <= BEAM_THREADS / 4) return;
+        constexpr int F = BEAM_FOUND / BEAM_THREADS;
+        unsigned long long mine[F];
         uint32_t v = 0u;
-        for (int i = lane * BEAM_WARPS + warp; i < n; i += BEAM_THREADS) v = max(v, (uint32_t)(found[i] >> 32));
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            const int at = (i * 32 + lane) * BEAM_WARPS + warp;
+            mine[i] = at < n ? found[at] : 0ull;
+            v = max(v, (uint32_t)(mine[i] >> 32));
+        }
         raise(v > ORD_NEG_INF ? unordered(v) : -INFINITY, BEAM_THREADS);
+        if (tid == 0) n_found = 0;
+        __syncthreads();
+        const unsigned long long lo = (unsigned long long)ordered(bound + 0.0f) << 32;
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+            if (mine[i] >= lo) found[atomicAdd(&n_found, 1)] = mine[i];
+        __syncthreads();
     };
 
     const long long end = min((long long)(blockIdx.x + 1) * a.span, (long long)a.B * a.W * a.steps);
     long long at = (long long)blockIdx.x * a.span;
     int row = (int)(at / a.steps), step = (int)(at - (long long)row * a.steps), first = step;
-    Row r = row_at(row);
-    int token0 = r.token0 + step * BEAM_STEP * VEC;
-    uint4 cur[U], nxt[U];
-    uint32_t bits[U], nbits[U];
-    load(cur, r, token0);
-    if constexpr (MASK) load_bits(bits, row, token0);
+    Row here = row_at(row);
+    int token0 = here.token0 + step * BEAM_STEP * VEC;
+    // the step that is fetched next, and its number (of the stretch)
+    Row ahead = here;
+    int arow = row, astep = step, ahead_n = 0;
+    const int steps = (int)(end - at);
+    auto fetch_next = [&] {
+        if (ahead_n < steps) {
+            fetch(ahead_n % BEAM_RING, ahead.x, ahead.token0 + astep * BEAM_STEP * VEC);
+            if (++astep == a.steps && ahead_n + 1 < steps) {
+                astep = 0;
+                ahead = row_at(++arow);
+            }
+        }
+        ++ahead_n;
+        copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < BEAM_RING - 1; ++i) fetch_next();
+    uint4 cur[U];
+    uint32_t bits[U];
     float ref = -INFINITY;
     float2 sum2 = make_float2(0.0f, 0.0f);
     bool hot = true, lost = false;
-    for (; at < end; ++at) {
-        const bool row_ends = step + 1 == a.steps, last = row_ends || at + 1 == end;  // of the piece
-        const Row here = r;
-        int ntoken0 = token0 + BEAM_STEP * VEC;
-        if (at + 1 < end) {
-            if (row_ends) {
-                r = row_at(row + 1);
-                ntoken0 = r.token0;
-            }
-            load(nxt, r, ntoken0);
-            if constexpr (MASK) load_bits(nbits, row + row_ends, ntoken0);
-        }
+    for (int i = 0; i < steps; ++i) {
+        const bool row_ends = step + 1 == a.steps, last = row_ends || i + 1 == steps;  // of the piece
+        fetch_next();
+        if constexpr (MASK) load_bits(bits, row, token0);
+        copy_wait<BEAM_RING - 1>();
+        take(cur, i % BEAM_RING, here.x, token0);
         if constexpr (MASK) {
 #pragma unroll
             for (int u = 0; u < U; ++u) L::keep(cur[u], bits[u]);
@@ -662,7 +777,7 @@ __global__ void __launch_bounds__(BEAM_THREADS, MASK ? 2 : 4) beam_kernel(const 
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (top[u] >= bound) {
-                const int i = atomicAdd(&n_queue, 1);
+                const int i = atomicAdd(&n_queue[turn], 1);
                 filling |= i >= BEAM_QUEUE / 2;
                 if (i < BEAM_QUEUE) {
                     queue[i] = cur[u];
@@ -686,20 +801,8 @@ __global__ void __launch_bounds__(BEAM_THREADS, MASK ? 2 : 4) beam_kernel(const 
                 const float2 d = mul2(add2(make_float2(L::get(cur[u], j), L::get(cur[u], j + 1)), shift), log2e);
                 sum2 = add2(sum2, make_float2(exp2_fast(d.x), exp2_fast(d.y)));
             }
-        if (!last) {
-            hot = __syncthreads_or(filling);  // (n_queue itself may have grown by another's next step)
-            const int done = step - first + 1;
-            // (2, 8, 32, .. steps; for many candidates every power of two)
-            if (hot || ((done & (done - 1)) == 0 && (done & (a.k > 48 ? ~1 : 0x2AAAAAAA)) != 0)) {
-                lost |= n_queue > BEAM_QUEUE;
-                __syncthreads();
-                drain();
-                lost |= n_found > BEAM_FOUND;
-                __syncthreads();
-                if (!lost) raise_by_found();
-            }
-        } else {
-            // ---- the piece ends: its sums, over the largest reference
+        if (last) {
+            // the warp's sum, over its largest reference
             float wr = ref, ws = sum2.x + sum2.y;
 #pragma unroll
             for (int o = 16; o; o >>= 1) wr = fmaxf(wr, __shfl_xor_sync(0xFFFFFFFFu, wr, o));
@@ -710,75 +813,33 @@ __global__ void __launch_bounds__(BEAM_THREADS, MASK ? 2 : 4) beam_kernel(const 
                 warp_ref[warp] = wr;
                 warp_sum[warp] = ws;
             }
-            __syncthreads();
-            const size_t list = (size_t)row * a.pieces + (blockIdx.x - first_stretch(a, row));
-            if (warp == 0) {
-                const float wr8 = warp_ref[lane % BEAM_WARPS];
-                float top = wr8, s = lane < BEAM_WARPS ? warp_sum[lane] : 0.0f;
-#pragma unroll
-                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                s = wr8 == top ? s : s * __expf(wr8 - top);
-#pragma unroll
-                for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-                if (lane == 0) a.sums[list] = make_float2(top, s);
-            }
-            lost |= n_queue > BEAM_QUEUE;
-            __syncthreads();
+        }
+        hot = __syncthreads_or(filling);  // (n_queue itself may have grown by another's next step)
+        const int done = step - first + 1;
+        // (2, 8, 32, .. steps; for many candidates every power of two)
+        if (last || hot || ((done & (done - 1)) == 0 && (done & (a.k > 48 ? ~1 : 0x2AAAAAAA)) != 0)) {
+            lost |= n_queue[turn] > BEAM_QUEUE;
             drain();
             lost |= n_found > BEAM_FOUND;
-            __syncthreads();
-            if (!lost) {
-                const int n = n_found;
-                if (n > BEAM_THREADS / 2) {  // (fewer are ranked sooner than sifted)
-                    raise_by_found();
-                    // what no longer reaches the bound is dropped
-                    constexpr int F = BEAM_FOUND / BEAM_THREADS;
-                    unsigned long long mine[F];
+            if (!lost) sift();
+        }
+        if (last) {
+            // ---- the piece ends
+            const size_t list = (size_t)row * a.pieces + (blockIdx.x - first_stretch(a, row));
+            if (warp == 0) {
+                const float wr = warp_ref[lane % BEAM_WARPS];
+                float top = wr, s = lane < BEAM_WARPS ? warp_sum[lane] : 0.0f;
 #pragma unroll
-                    for (int i = 0; i < F; ++i) mine[i] = i * BEAM_THREADS + tid < n ? found[i * BEAM_THREADS + tid] : 0ull;
-                    if (tid == 0) n_found = 0;
-                    __syncthreads();
-                    const unsigned long long lo = (unsigned long long)ordered(bound + 0.0f) << 32;
+                for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                s = wr == top ? s : s * __expf(wr - top);
 #pragma unroll
-                    for (int i = 0; i < F; ++i)
-                        if (mine[i] >= lo) found[atomicAdd(&n_found, 1)] = mine[i];
-                }
-            } else {
-                // too many reach the bound (ties, most often): the k-th largest of
-                // (logit, token) by bisection over the whole piece, read once per round
-                auto each = [&](auto f) {
-                    for (int s = first; s <= step; ++s) {
-                        const int e0 = here.token0 + s * BEAM_STEP * VEC;
-                        load(cur, here, e0);
-                        if constexpr (MASK) {
-                            load_bits(bits, row, e0);
-#pragma unroll
-                            for (int u = 0; u < U; ++u) L::keep(cur[u], bits[u]);
-                        }
-#pragma unroll
-                        for (int u = 0; u < U; ++u)
-#pragma unroll
-                            for (int j = 0; j < VEC; ++j)
-                                f(logit_token(L::get(cur[u], j), e0 + (u * BEAM_THREADS + tid) * VEC + j));
-                    }
-                };
-                unsigned long long lo = (unsigned long long)ordered(bound + 0.0f) << 32, hi = 0xFFFFFFFFFFFFFFFFull;
-                while (lo < hi) {
-                    const unsigned long long mid = lo + (hi - lo) / 2 + 1;
-                    int c = 0;
-                    each([&](unsigned long long v) { c += v >= mid; });
-                    c = block_sum(c, scratch);
-                    if (c >= a.k) lo = mid;
-                    else hi = mid - 1;
-                    if (c == a.k) break;
-                }
-                __syncthreads();
-                if (tid == 0) n_found = 0;
-                __syncthreads();
-                each([&](unsigned long long v) {
-                    if (v >= lo) found[atomicAdd(&n_found, 1)] = v;
-                });
+                for (int o = 4; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+                if (lane == 0) a.sums[list] = make_float2(top, s);
             }
+            if (lost)
+                piece_exact<E, MASK>(here.x, MASK ? a.mask + (size_t)row * a.mask_stride : nullptr,
+                                     here.token0 + first * BEAM_STEP * VEC, min(a.V, here.token0 + (step + 1) * BEAM_STEP * VEC),
+                                     a.V, a.k, (unsigned long long)ordered(bound + 0.0f) << 32, found, &n_found, scratch);
             __syncthreads();
             const int n = n_found;
             unsigned long long *best = a.best + list * a.kpad;
@@ -798,29 +859,31 @@ __global__ void __launch_bounds__(BEAM_THREADS, MASK ? 2 : 4) beam_kernel(const 
             hot = true;
             lost = false;
         }
-        row += row_ends;
-        step = row_ends ? 0 : step + 1;
-        token0 = ntoken0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) cur[u] = nxt[u];
-        if constexpr (MASK) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) bits[u] = nbits[u];
+        token0 += BEAM_STEP * VEC;
+        ++step;
+        if (row_ends && i + 1 < steps) {
+            here = row_at(++row);
+            token0 = here.token0;
+            step = 0;
         }
     }
+    copy_wait<0>();
 
     // ---- this block's pieces are done: batch entries that are complete are joined
     __threadfence();
     const int row0 = (int)((long long)blockIdx.x * a.span / a.steps), row1 = (int)((end - 1) / a.steps);
     for (int b = row0 / a.W; b <= row1 / a.W; ++b) {
         __syncthreads();
-        if (tid == 0) {
+        if (warp == 0) {
             const int done = min(row1, (b + 1) * a.W - 1) - max(row0, b * a.W) + 1;
             int total = 0;
-            for (int w = 0; w < a.W; ++w) total += pieces_of(a, b * a.W + w);
-            joins = atomicAdd(a.count + b, done) + done == total;
-            if (joins) a.count[b] = 0;
-            __threadfence();
+            for (int w = lane; w < a.W; w += 32) total += pieces_of(a, b * a.W + w);
+            total = __reduce_add_sync(0xFFFFFFFFu, total);
+            if (lane == 0) {
+                joins = atomicAdd(a.count + b, done) + done == total;
+                if (joins) a.count[b] = 0;
+                __threadfence();
+            }
         }
         __syncthreads();
         if (joins) beam_join(a, *reinterpret_cast<JoinSmem *>(smem), b);
@@ -830,17 +893,17 @@ __global__ void __launch_bounds__(BEAM_THREADS, MASK ? 2 : 4) beam_kernel(const 
 // ------------------------------------------------------------ host
 
 // Steps of a row, of a stretch, and the most pieces of a row.  As many
-// stretches as blocks fit on the GPU (those with a mask hold more registers).
+// stretches as blocks fit on the GPU.
 constexpr long long BEAM_SMS = 152;
 struct BeamSplit {
     int steps, span, pieces, stretches;
 };
-static BeamSplit beam_split(int rows, int V, int vec, bool mask)
+static BeamSplit beam_split(int rows, int V, int vec)
 {
     BeamSplit s;
     // (a row may begin inside its first vector)
     s.steps = ((V + vec - 1 + vec - 1) / vec + BEAM_STEP - 1) / BEAM_STEP;
-    const long long total = (long long)rows * s.steps, blocks = BEAM_SMS * (mask ? 2 : 4);
+    const long long total = (long long)rows * s.steps, blocks = BEAM_SMS * BEAM_BLOCKS;
     s.span = (int)((total + blocks - 1) / blocks);
     s.pieces = (s.steps + s.span - 1) / s.span + (s.steps % s.span != 0 || s.span == 0 ? 1 : 0);
     s.stretches = (int)((total + s.span - 1) / s.span);
@@ -849,8 +912,7 @@ static BeamSplit beam_split(int rows, int V, int vec, bool mask)
 
 static size_t beam_lists(int B, int W, int V, int vec)
 {
-    const size_t p = beam_split(B * W, V, vec, false).pieces, m = beam_split(B * W, V, vec, true).pieces;
-    return (size_t)B * W * (p > m ? p : m);
+    return (size_t)B * W * beam_split(B * W, V, vec).pieces;
 }
 
 size_t beam_workspace_bytes(int B, int W, int V, int k)
@@ -863,14 +925,15 @@ template <typename E>
 static cudaError_t run_beam(cudaStream_t st, const BeamArgs &a, int stretches)
 {
     const dim3 grid((unsigned)stretches);
-    return a.mask ? launch_k(beam_kernel<E, true>, grid, dim3(BEAM_THREADS), 0, st, a)
-                  : launch_k(beam_kernel<E, false>, grid, dim3(BEAM_THREADS), 0, st, a);
+    auto kernel = a.mask ? beam_kernel<E, true> : beam_kernel<E, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChunkSmem));
+    return e != cudaSuccess ? e : launch_k(kernel, grid, dim3(BEAM_THREADS), sizeof(ChunkSmem), st, a);
 }
 
 cudaError_t launch_beam_select(const DeviceState &ds, cudaStream_t st, const BeamCall &c, void *workspace)
 {
     const int vec = c.dtype == MX_F32 ? 4 : 8;
-    const BeamSplit split = beam_split(c.B * c.W, c.V, vec, c.mask != nullptr);
+    const BeamSplit split = beam_split(c.B * c.W, c.V, vec);
     BeamArgs a;
     a.logits = c.logits;
     a.row_stride = c.row_stride;
