@@ -35,6 +35,7 @@
 // both go slower ways to the same result.
 #include <cfloat>
 #include <cmath>
+#include <cstddef>
 
 #include "../../include/mx.h"
 #include "mx_common.cuh"
@@ -180,6 +181,26 @@ __device__ __forceinline__ int block_sum(int v, int *scratch)
     return s;
 }
 
+// How many of n numbers are larger than c, and how many equal it; v on a
+// 16-byte boundary.  (Four at a time without a branch: one by one with the order of
+// equal ones beside it, 100 took 4 us.)
+__device__ __forceinline__ int rank_of(const unsigned long long *v, int n, unsigned long long c, int &equal)
+{
+    int rank = 0, eq = 0, j = 0;
+#pragma unroll 2
+    for (; j + 4 <= n; j += 4) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(v + j), y = *reinterpret_cast<const ulonglong2 *>(v + j + 2);
+        rank += (x.x > c) + (x.y > c) + (y.x > c) + (y.y > c);
+        eq += (x.x == c) + (x.y == c) + (y.x == c) + (y.y == c);
+    }
+    for (; j < n; ++j) {
+        rank += v[j] > c;
+        eq += v[j] == c;
+    }
+    equal = eq;
+    return rank;
+}
+
 __device__ __forceinline__ float2 add2(float2 a, float2 b)
 {
     unsigned long long d;
@@ -276,7 +297,7 @@ struct JoinSmem {
     float2 part[BEAM_MAX_W];
     uint32_t warp_bound[BEAM_WARPS];
     float out_score[BEAM_MAX_K];
-    int out_parent[BEAM_MAX_K], out_token[BEAM_MAX_K], n_found;
+    int out_parent[BEAM_MAX_K], out_token[BEAM_MAX_K], n_found, n_kept;
 };
 
 // Within `off` of a candidate's key, in fp32; NaN: no candidate.
@@ -387,7 +408,7 @@ __device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b
         for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
         if (lane == 0) sm.part[w] = make_float2(top, t);
     }
-    if (tid == 0) sm.n_found = 0;
+    if (tid == 0) sm.n_found = sm.n_kept = 0;
     __syncthreads();
     if (tid < a.W) {
         const float2 p = sm.part[tid];
@@ -456,26 +477,52 @@ __device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b
             }
         }
     __syncthreads();
-    const int n = sm.n_found;
+    int n = sm.n_found;
     if (n <= BEAM_JOIN) {
+        // many: the bound again, from all of them (ranks cost the square of their number)
+        float atleast = least;
+        if (n > 2 * a.k) {
+            uint32_t low = 0u;
 #pragma unroll 1
-        for (int i = tid; i < n; i += BEAM_THREADS) sm.key[i] = key_exact(sm, sm.beam[i], sm.lt[i]);
-        __syncthreads();
+            for (int i = lane * BEAM_WARPS + warp; i < n; i += BEAM_THREADS) {
+                float off;
+                const float f = key_about(sm, sm.beam[i], sm.lt[i], off);
+                low = max(low, ordered((f - off) + 0.0f));
+            }
+            const int r = (a.k + BEAM_WARPS - 1) / BEAM_WARPS;
+            bound = warp_nth(low, r, [] { return 0u; });
+            if (lane == 0) sm.warp_bound[warp] = bound;
+            __syncthreads();
+            bound = __reduce_min_sync(0xFFFFFFFFu, sm.warp_bound[lane % BEAM_WARPS]);
+            if (bound != 0u) atleast = fmaxf(atleast, unordered(bound));
+        }
+        unsigned long long *order = sm.entry;
 #pragma unroll 1
         for (int i = tid; i < n; i += BEAM_THREADS) {
-            const unsigned long long ki = sm.key[i], li = sm.lt[i];
-            const int ri = sm.beam[i];
-            int rank = 0;
-#pragma unroll 2
-            for (int j = 0; j < n; ++j) {
-                const unsigned long long kj = sm.key[j];
-                rank += kj > ki;
-                if (kj == ki && j != i) rank += before(kj, sm.beam[j], sm.lt[j], ki, ri, li);
-            }
+            const unsigned long long l = sm.lt[i];
+            const int row = sm.beam[i];
+            float off;
+            const float f = key_about(sm, row, l, off);
+            if (f + off < atleast) continue;
+            const int at = atomicAdd(&sm.n_kept, 1);
+            sm.key[at] = key_exact(sm, row, l);
+            // the order of equal keys, in 58 bits: beam (6), logit (32), token (20)
+            order[at] = (unsigned long long)(BEAM_MAX_W - 1 - row) << 52 | (l >> 32) << 20 | ((uint32_t)l & (BEAM_MAX_V - 1));
+        }
+        __syncthreads();
+        n = sm.n_kept;
+#pragma unroll 1
+        for (int i = tid; i < n; i += BEAM_THREADS) {
+            const unsigned long long ki = sm.key[i], li = order[i];
+            int equal;
+            int rank = rank_of(sm.key, n, ki, equal);
+            if (equal > 1)  // (bf16 logits often are)
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) rank += (sm.key[j] == ki) & (order[j] > li);
             if (rank < a.k) {
                 sm.out_score[rank] = unordered((uint32_t)(ki >> 32));
-                sm.out_parent[rank] = b * a.W + ri;
-                sm.out_token[rank] = (int)(0xFFFFFFFFu - (uint32_t)li);
+                sm.out_parent[rank] = b * a.W + BEAM_MAX_W - 1 - (int)(li >> 52);
+                sm.out_token[rank] = BEAM_MAX_V - 1 - (int)((uint32_t)li & (BEAM_MAX_V - 1));
             }
         }
         for (int i = n + tid; i < a.k; i += BEAM_THREADS) {
@@ -546,6 +593,8 @@ struct ChunkSmem {
     unsigned long long found[BEAM_FOUND];
 };
 static_assert(sizeof(JoinSmem) <= sizeof(ChunkSmem), "the join's shared memory lies over the stretch's");
+static_assert(offsetof(ChunkSmem, found) % 16 == 0 && offsetof(JoinSmem, key) % 16 == 0, "rank_of");
+static_assert(BEAM_MAX_W == 64 && BEAM_MAX_V == 1 << 20, "the order of equal keys");
 static_assert(BEAM_QUEUE <= BEAM_THREADS, "a thread for each vector");
 static_assert(BEAM_BLOCKS * (sizeof(ChunkSmem) + 1024 + 256) <= 228 * 1024, "blocks of an SM");
 
@@ -845,8 +894,8 @@ __global__ void __launch_bounds__(BEAM_THREADS, BEAM_BLOCKS) beam_kernel(const _
             unsigned long long *best = a.best + list * a.kpad;
             for (int i = tid; i < n; i += BEAM_THREADS) {
                 const unsigned long long c = found[i];
-                int rank = 0;
-                for (int j = 0; j < n; ++j) rank += found[j] > c;
+                int equal;
+                const int rank = rank_of(found, n, c, equal);
                 if (rank < a.k) best[rank] = c;
             }
             for (int i = min(n, a.k) + tid; i < a.kpad; i += BEAM_THREADS) best[i] = 0ull;
@@ -870,7 +919,6 @@ __global__ void __launch_bounds__(BEAM_THREADS, BEAM_BLOCKS) beam_kernel(const _
     copy_wait<0>();
 
     // ---- this block's pieces are done: batch entries that are complete are joined
-    __threadfence();
     const int row0 = (int)((long long)blockIdx.x * a.span / a.steps), row1 = (int)((end - 1) / a.steps);
     for (int b = row0 / a.W; b <= row1 / a.W; ++b) {
         __syncthreads();
@@ -880,9 +928,11 @@ __global__ void __launch_bounds__(BEAM_THREADS, BEAM_BLOCKS) beam_kernel(const _
             for (int w = lane; w < a.W; w += 32) total += pieces_of(a, b * a.W + w);
             total = __reduce_add_sync(0xFFFFFFFFu, total);
             if (lane == 0) {
-                joins = atomicAdd(a.count + b, done) + done == total;
+                // (of what the block wrote before the barrier, and of what is read after the next)
+                int before;
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(before) : "l"(a.count + b), "r"(done) : "memory");
+                joins = before + done == total;
                 if (joins) a.count[b] = 0;
-                __threadfence();
             }
         }
         __syncthreads();
