@@ -201,22 +201,31 @@ __global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(I8MvArgs a)
     const int groups = (steps + a.parts * MV_GROUP - 1) / (a.parts * MV_GROUP);
     const int rounds = (tiles + per_cta - 1) / per_cta;
 
-    uint4 cur[MV_GROUP][2], nxt[MV_GROUP][2];
+    // Two buffers of loads, each refilled as soon as it is used, so that two
+    // groups are in flight while a warp waits; a third of the time went to
+    // waiting with one.  The loads run ahead over tile ends.
+    uint4 even[MV_GROUP][2], odd[MV_GROUP][2];
+    int load_round = blockIdx.x, load_q = 0;
     // step number i of group q: part + parts * (q * MV_GROUP + i)
-    auto load = [&](uint4 (&v)[MV_GROUP][2], int round, int q) {
-        const int tile = round * per_cta + sub;
+    auto load = [&](uint4 (&v)[MV_GROUP][2]) {
+        const int tile = load_round * per_cta + sub;
         const int n0 = 16 * tile + g, n1 = n0 + 8;
         const int8_t *w = a.w + 16 * t;
 #pragma unroll
         for (int i = 0; i < MV_GROUP; ++i) {
-            const int k = 64 * (part + a.parts * (q * MV_GROUP + i));
-            const bool in = round < rounds && k + 16 * t < a.K;
+            const int k = 64 * (part + a.parts * (load_q * MV_GROUP + i));
+            const bool in = load_round < rounds && k + 16 * t < a.K;
             v[i][0] = in && n0 < a.N ? ld_stream_v4(w + (size_t)n0 * a.K + k) : make_uint4(0u, 0u, 0u, 0u);
             v[i][1] = in && n1 < a.N ? ld_stream_v4(w + (size_t)n1 * a.K + k) : make_uint4(0u, 0u, 0u, 0u);
         }
+        if (++load_q == groups) {
+            load_q = 0;
+            load_round += gridDim.x;
+        }
     };
     pdl_trigger();
-    load(cur, blockIdx.x, 0);  // weights: before the tokens are there
+    load(even);  // weights: before the tokens are there
+    load(odd);
     pdl_wait();
     const int vecs = a.xpitch / 16;
     for (int i = threadIdx.x; i < 8 * NB * vecs; i += MV_THREADS) {
@@ -227,30 +236,30 @@ __global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(I8MvArgs a)
     }
     __syncthreads();
 
-    int flip = 0;
-    for (int round = blockIdx.x; round < rounds; round += gridDim.x) {
-        int acc[NB][4] = {};
-        for (int q = 0; q < groups; ++q) {
-            const bool more = q + 1 < groups;
-            load(nxt, more ? round : round + (int)gridDim.x, more ? q + 1 : 0);
+    int flip = 0, round = blockIdx.x, q = 0;
+    int acc[NB][4] = {};
+    auto step = [&](uint4 (&v)[MV_GROUP][2]) {
 #pragma unroll
-            for (int i = 0; i < MV_GROUP; ++i) {
-                const int k = min(64 * (part + a.parts * (q * MV_GROUP + i)), 64 * (steps - 1));  // (past the row: weights of zero)
+        for (int i = 0; i < MV_GROUP; ++i) {
+            const int k = min(64 * (part + a.parts * (q * MV_GROUP + i)), 64 * (steps - 1));  // (past the row: weights of zero)
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(xs + (size_t)(8 * b + g) * a.xpitch + k + 16 * t);
-                    mma_s8_16832(acc[b], cur[i][0].x, cur[i][1].x, cur[i][0].y, cur[i][1].y, x.x, x.y);
-                    mma_s8_16832(acc[b], cur[i][0].z, cur[i][1].z, cur[i][0].w, cur[i][1].w, x.z, x.w);
-                }
+            for (int b = 0; b < NB; ++b) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(xs + (size_t)(8 * b + g) * a.xpitch + k + 16 * t);
+                mma_s8_16832(acc[b], v[i][0].x, v[i][1].x, v[i][0].y, v[i][1].y, x.x, x.y);
+                mma_s8_16832(acc[b], v[i][0].z, v[i][1].z, v[i][0].w, v[i][1].w, x.z, x.w);
             }
-#pragma unroll
-            for (int i = 0; i < MV_GROUP; ++i) cur[i][0] = nxt[i][0], cur[i][1] = nxt[i][1];
         }
+        load(v);
+        if (++q < groups) return;
+        q = 0;
         // the parts' sums meet; outputs in rows of 16 channels
         int4 *r = red + (size_t)flip * MV_WARPS * NB * 32;
         flip ^= 1;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) r[(warp * NB + b) * 32 + lane] = make_int4(acc[b][0], acc[b][1], acc[b][2], acc[b][3]);
+        for (int b = 0; b < NB; ++b) {
+            r[(warp * NB + b) * 32 + lane] = make_int4(acc[b][0], acc[b][1], acc[b][2], acc[b][3]);
+            acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0;
+        }
         __syncthreads();
         const int *ri = reinterpret_cast<const int *>(r);
         for (int o = threadIdx.x; o < per_cta * NB * 128; o += MV_THREADS) {
@@ -260,10 +269,16 @@ __global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(I8MvArgs a)
             const int at = 4 * (4 * (row % 8) + c / 2) + 2 * (row / 8) + c % 2;
             int sum = 0;
             for (int p = 0; p < a.parts; ++p) sum += ri[((s * a.parts + p) * NB + b) * 128 + at];
-            const float v = __fmul_rn(__fmul_rn((float)sum, __ldcg(a.sx + m)), __ldg(a.sw + n));
-            if constexpr (sizeof(Y) == 4) static_cast<float *>(a.y)[(size_t)m * a.N + n] = v;
-            else static_cast<uint16_t *>(a.y)[(size_t)m * a.N + n] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
+            const float y = __fmul_rn(__fmul_rn((float)sum, __ldcg(a.sx + m)), __ldg(a.sw + n));
+            if constexpr (sizeof(Y) == 4) static_cast<float *>(a.y)[(size_t)m * a.N + n] = y;
+            else static_cast<uint16_t *>(a.y)[(size_t)m * a.N + n] = (uint16_t)f32x2_to_bf16x2(y, 0.0f);
         }
+        round += gridDim.x;
+    };
+    while (round < rounds) {
+        step(even);
+        if (round >= rounds) break;
+        step(odd);
     }
 }
 
