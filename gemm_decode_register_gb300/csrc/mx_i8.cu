@@ -164,8 +164,8 @@ struct I8MvArgs {
     const int8_t *w;
     const float *sw;
     void *y;
-    int M, N, K;
-    int tokens;  // of this launch: M rows from x on, at most 8 NB
+    int N, K;
+    int tokens;  // of this pass, at most 8 NB
     int parts;   // warps that share a row tile's K: 1, 2, 4, 8 or 16
     int xpitch;  // bytes of a staged token, an odd multiple of 64
 };
@@ -186,13 +186,15 @@ __device__ __forceinline__ void mma_s8_16832(int (&d)[4], uint32_t a0, uint32_t 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NB: groups of 8 tokens.  Y: float or uint16_t (bf16).
+// NB: groups of 8 tokens (places past the last token repeat it).  Y: float or uint16_t (bf16).
+// mma.sync does about 130 T 8-bit operations a second here (and no more of f16), what eight
+// tokens ask of the weights' stream: 8 through 128000 x 8192 take 154 us, 16 258.
 template <int NB, typename Y>
-__global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(I8MvArgs a)
+__global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(const __grid_constant__ I8MvArgs a)
 {
     extern __shared__ __align__(16) uint8_t smem[];
-    uint8_t *xs = smem;                                                            // [8 NB][xpitch]
-    int4 *red = reinterpret_cast<int4 *>(smem + (size_t)8 * NB * a.xpitch);        // [2][warps][NB][32]
+    uint8_t *xs = smem;                                                        // [tokens][xpitch]
+    int4 *red = reinterpret_cast<int4 *>(smem + (size_t)a.tokens * a.xpitch);  // [2][warps][NB][32]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int steps = (a.K + 63) / 64;             // of a row
     const int per_cta = MV_WARPS / a.parts;        // row tiles at a time
@@ -228,10 +230,10 @@ __global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(I8MvArgs a)
     load(odd);
     pdl_wait();
     const int vecs = a.xpitch / 16;
-    for (int i = threadIdx.x; i < 8 * NB * vecs; i += MV_THREADS) {
+    for (int i = threadIdx.x; i < a.tokens * vecs; i += MV_THREADS) {
         const int m = i / vecs, c = i - m * vecs;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (m < a.tokens && 16 * c < a.K) v = __ldcg(reinterpret_cast<const uint4 *>(a.x + (size_t)m * a.K) + c);
+        if (16 * c < a.K) v = __ldcg(reinterpret_cast<const uint4 *>(a.x + (size_t)m * a.K) + c);
         *reinterpret_cast<uint4 *>(xs + (size_t)m * a.xpitch + 16 * c) = v;
     }
     __syncthreads();
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(I8MvArgs a)
             const int k = min(64 * (part + a.parts * (q * MV_GROUP + i)), 64 * (steps - 1));  // (past the row: weights of zero)
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(xs + (size_t)(8 * b + g) * a.xpitch + k + 16 * t);
+                const uint4 x = *reinterpret_cast<const uint4 *>(xs + (size_t)min(8 * b + g, a.tokens - 1) * a.xpitch + k + 16 * t);
                 mma_s8_16832(acc[b], v[i][0].x, v[i][1].x, v[i][0].y, v[i][1].y, x.x, x.y);
                 mma_s8_16832(acc[b], v[i][0].z, v[i][1].z, v[i][0].w, v[i][1].w, x.z, x.w);
             }
@@ -284,55 +286,59 @@ __global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(I8MvArgs a)
 
 // ------------------------------------------------------------ host
 
-template <int NB, typename Y>
-static cudaError_t run_mv(const DeviceState &ds, cudaStream_t st, I8MvArgs a)
-{
-    const int smem = 8 * NB * a.xpitch + 2 * MV_WARPS * NB * 32 * 16;
-    if (smem > ds.max_smem_optin) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(i8_mv_kernel<NB, Y>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const int rounds = ((a.N + 15) / 16 + MV_WARPS / a.parts - 1) / (MV_WARPS / a.parts);
-    return launch_k(i8_mv_kernel<NB, Y>, dim3(rounds < ds.num_sms ? rounds : ds.num_sms), dim3(MV_THREADS), smem, st, a);
-}
-
 static int mv_pitch(int K)
 {
     const int p = (K + 63) / 64 * 64;
     return p % 128 == 0 ? p + 64 : p;  // two tokens' 64 bytes then fall into different banks
 }
 
+static int mv_smem(int tokens, int K) { return tokens * mv_pitch(K) + 2 * MV_WARPS * ((tokens + 7) / 8) * 512; }
+
+constexpr int MV_NB = 2;  // most groups of 8 tokens of a pass
+
 // Most tokens a pass can stage beside the sums' space.
 static int mv_pass_tokens(const DeviceState &ds, int K)
 {
-    for (int nb = 2; nb >= 1; --nb)
-        if (8 * nb * mv_pitch(K) + 2 * MV_WARPS * nb * 512 <= ds.max_smem_optin) return 8 * nb;
+    for (int m = 8 * MV_NB; m > 0; --m)
+        if (mv_smem(m, K) <= ds.max_smem_optin) return m;
     return 0;
 }
 
-static cudaError_t launch_i8_mv(const DeviceState &ds, cudaStream_t st, const int8_t *x, const float *sx, const int8_t *w,
-                                const float *sw, void *y, int ydtype, int M, int N, int K)
+template <int NB, typename Y>
+static cudaError_t run_mv(const DeviceState &ds, cudaStream_t st, const I8MvArgs &a)
 {
-    const int most = mv_pass_tokens(ds, K);
-    if (most == 0) return cudaErrorInvalidValue;
+    const int smem = mv_smem(a.tokens, a.K);
+    const cudaError_t e = cudaFuncSetAttribute(i8_mv_kernel<NB, Y>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int rounds = ((a.N + 15) / 16 + MV_WARPS / a.parts - 1) / (MV_WARPS / a.parts);
+    return launch_k(i8_mv_kernel<NB, Y>, dim3(rounds < ds.num_sms ? rounds : ds.num_sms), dim3(MV_THREADS), smem, st, a);
+}
+
+template <typename Y>
+static cudaError_t run_mv_pass(const DeviceState &ds, cudaStream_t st, const I8MvArgs &a)
+{
+    return a.tokens <= 8 ? run_mv<1, Y>(ds, st, a) : run_mv<2, Y>(ds, st, a);
+}
+
+static cudaError_t launch_i8_mv(const DeviceState &ds, cudaStream_t st, const int8_t *x, const float *sx, const int8_t *w,
+                                const float *sw, void *y, int ydtype, int M, int N, int K, int pass)
+{
     const size_t ye = ydtype == MX_F32 ? 4 : 2;
-    for (int m = 0; m < M; m += most) {
-        I8MvArgs a;
+    I8MvArgs a;
+    const int steps = (K + 63) / 64;
+    a.parts = 1;  // (each warp has two groups of loads of a tile or more)
+    while (a.parts < MV_WARPS && steps >= 2 * a.parts * MV_GROUP) a.parts *= 2;
+    for (int m = 0; m < M; m += pass) {
         a.x = x + (size_t)m * K;
         a.sx = sx + m;
         a.w = w;
         a.sw = sw;
         a.y = static_cast<char *>(y) + (size_t)m * N * ye;
-        a.M = M;
         a.N = N;
         a.K = K;
-        a.tokens = M - m < most ? M - m : most;
+        a.tokens = M - m < pass ? M - m : pass;
         a.xpitch = mv_pitch(K);
-        const int steps = (K + 63) / 64;
-        a.parts = 1;
-        while (a.parts < MV_WARPS && steps >= 2 * a.parts * MV_GROUP) a.parts *= 2;
-        cudaError_t e;
-        if (a.tokens <= 8) e = ydtype == MX_F32 ? run_mv<1, float>(ds, st, a) : run_mv<1, uint16_t>(ds, st, a);
-        else e = ydtype == MX_F32 ? run_mv<2, float>(ds, st, a) : run_mv<2, uint16_t>(ds, st, a);
+        const cudaError_t e = ydtype == MX_F32 ? run_mv_pass<float>(ds, st, a) : run_mv_pass<uint16_t>(ds, st, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -352,15 +358,24 @@ cudaError_t launch_i8_quantize(const DeviceState &, cudaStream_t st, const void 
                            : run_quantize<uint16_t, int8_t>(st, x, q, scales, M, K);
 }
 
-// Up to this many tokens the weights are streamed (again for every pass of
-// tokens), above they are multiplied in the GEMM's tiles.
-constexpr int I8_MV_TOKENS = 16;
-
 size_t i8_mm_workspace_bytes(int M, int K)
 {
     // codes (8-bit for the streaming kernel, f16 for the GEMM), then scales
     const size_t codes = ((size_t)M * K * 2 + 255) / 256 * 256;
     return codes + ((size_t)M * 4 + 255) / 256 * 256;
+}
+
+// Tokens of a streaming pass, or 0 for the GEMM: whichever takes less by these
+// estimates (us, measured on GB300).  A pass streams the weights, at 6.6 MB
+// per us for up to 8 tokens and 4.0 for up to 16, and takes about 5 beside.
+// The GEMM: see qmm_i8_estimate.
+static int i8_pass(const DeviceState &ds, int M, int N, int K)
+{
+    const int most = mv_pass_tokens(ds, K);
+    if (most == 0) return 0;
+    const int passes = (M + most - 1) / most, pass = (M + passes - 1) / passes;  // (equal passes)
+    const double stream = passes * ((double)N * K / (pass <= 8 ? 6.6e6 : 4.0e6) + 5.0);
+    return stream <= qmm_i8_estimate(ds, M, N, K) ? pass : 0;
 }
 
 cudaError_t launch_i8_mm(const DeviceState &ds, cudaStream_t st, const I8Call &c, void *workspace)
@@ -369,14 +384,14 @@ cudaError_t launch_i8_mm(const DeviceState &ds, cudaStream_t st, const I8Call &c
     float *own_sx = reinterpret_cast<float *>(static_cast<char *>(workspace) + codes);
     const float *sx = c.xdtype == MX_I8 ? c.sx : own_sx;
     cudaError_t e;
-    if (c.M <= I8_MV_TOKENS && mv_pass_tokens(ds, c.K) > 0) {
+    if (const int pass = i8_pass(ds, c.M, c.N, c.K)) {
         const int8_t *x = static_cast<const int8_t *>(c.x);
         if (c.xdtype != MX_I8) {
             e = launch_i8_quantize(ds, st, c.x, c.xdtype, static_cast<int8_t *>(workspace), own_sx, c.M, c.K);
             if (e != cudaSuccess) return e;
             x = static_cast<const int8_t *>(workspace);
         }
-        return launch_i8_mv(ds, st, x, sx, c.w, c.sw, c.y, c.ydtype, c.M, c.N, c.K);
+        return launch_i8_mv(ds, st, x, sx, c.w, c.sw, c.y, c.ydtype, c.M, c.N, c.K, pass);
     }
     uint16_t *h = static_cast<uint16_t *>(workspace);
     if (c.xdtype == MX_I8) {

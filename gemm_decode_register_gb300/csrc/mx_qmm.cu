@@ -35,11 +35,20 @@
 //   last warp   X: NACC 128 x 64 bf16 slabs per k-block by TMA (128-byte
 //               swizzle); both CTAs' slabs complete on CTA 0's barrier
 //
+// Few rows (QMM_FEW_ROWS; 8-bit integers): a tile of 256 X rows costs its MMAs
+// however few rows there are.  There the decoded weights are operand A (the
+// same 128 rows of each CTA, the same layout) and 128 X rows, 64 from each CTA,
+// operand B, of N = 128: a quarter of the MMA time and a half of the X slabs, below
+// the time that the weights take to arrive; the freed shared memory holds
+// twelve k-blocks of codes.  Tensor memory then has a weight row per lane and a
+// token per column.  (64 tokens through 128000 x 8192 466 -> 176 us.)
+//
 // Every mbarrier wait is bounded (about two seconds of %globaltimer); a wait
 // that gives up sets MX_DEVERR_TIMEOUT in the device error word, the CTA
 // drains what it has in flight, both CTAs of the pair write NaN to their Y
 // rows and return.
 #include <atomic>
+#include <cmath>
 
 #include "mx_decode_bf16.cuh"
 #include "mx_internal.h"
@@ -50,7 +59,7 @@ namespace mx {
 
 constexpr int QMM_BN = 256;                    // UMMA N: 128 weight rows from each CTA
 constexpr int QMM_BK = 64;                     // bf16 elements per 128-byte swizzle row
-constexpr int QMM_X_BYTES = 128 * QMM_BK * 2;  // a CTA's 128 rows of one 256-row X slab
+constexpr int QMM_FEW = 128;                   // rows of a tile of few rows (QMM_FEW_ROWS)
 constexpr int QMM_W_BYTES = 128 * QMM_BK * 2;  // a CTA's 128 decoded weight rows
 constexpr int QMM_SMEM_LIMIT = 232448;         // 227 KB of dynamic shared memory per CTA
 constexpr unsigned long long QMM_WAIT_NS = 2000000000ull;
@@ -65,22 +74,24 @@ constexpr int QMM_CTRL_WORDS = 5 + 16;
 //   C ring (SC slots): the packed codes (TMA) and block scales of a k-block.
 // A D slot is held from its decode through the hand-over to CTA 0 until the
 // MMA finishes; a C slot only until its codes are decoded.
-template <int FMT, int NACC, bool GROUPED = false>
+template <int FMT, int NACC, bool GROUPED = false, bool FEW = false>
 struct QmmGeo {
-    static constexpr int BM = 256 * NACC;  // output rows per pair tile
+    static constexpr int XROWS = FEW ? QMM_FEW / 2 : 128;     // X rows of a CTA and slab
+    static constexpr int BM = FEW ? QMM_FEW : 256 * NACC;     // output rows per pair tile
+    static constexpr int X_BYTES = XROWS * QMM_BK * 2;
     static constexpr int CODE_ROW = FMT == FMT_MXFP8 || FMT == FMT_I8 ? QMM_BK : QMM_BK / 2;  // code bytes per row per k-block
     static constexpr int C_BYTES = 128 * CODE_ROW;
     static constexpr int SPK = FMT == FMT_I8 ? 0 : FMT == FMT_NVFP4 ? 4 : 2;  // scale bytes per row per k-block
     static constexpr int SC_BYTES = 128 * SPK;
-    static constexpr int X_STAGE = NACC * QMM_X_BYTES;
+    static constexpr int X_STAGE = NACC * X_BYTES;
     // decoder groups: with 256-row tiles one group of 8 warps decoding a
     // k-block at a time cannot keep up with the MMAs (its warps are latency
     // bound), so two groups take alternate k-blocks; grouped tiles (up to 512
     // rows, often only 256 used) take two groups as well
     static constexpr int NG = (NACC == 1 || GROUPED) ? 2 : 1;
-    static constexpr int SX = NACC == 2 ? 4 : 8;  // 256-row tiles: X slabs land late under load, go deeper
+    static constexpr int SX = FEW ? 6 : NACC == 2 ? 4 : 8;  // 256-row tiles: X slabs land late under load, go deeper
     static constexpr int SD = NACC == 2 ? (NG == 2 ? 4 : 5) : 4;
-    static constexpr int SC_MAX = 4;  // codes ring depth cap
+    static constexpr int SC_MAX = FEW ? 12 : 4;  // codes ring depth cap (few rows: the weights' stream is the bound)
     static constexpr int THREADS = 96 + 256 * NG;  // codes producer, MMA, X producer, decoders
     static constexpr int SPF = 4;     // k-blocks of block scales the producer keeps in flight
     static constexpr int RESERVED = 1024 /*align*/ + 128 /*signal landing*/ + 512 /*barriers*/;
@@ -93,7 +104,7 @@ struct QmmGeo {
     static constexpr int OFF_SIG = OFF_S + SC * SC_BYTES;
     static constexpr int OFF_BAR = OFF_SIG + 128;
     static constexpr int SMEM = OFF_BAR + 512 + 1024;
-    static constexpr int TMEM_COLS = 256 * NACC;
+    static constexpr int TMEM_COLS = FEW ? QMM_FEW : 256 * NACC;
     static_assert(OFF_C % 1024 == 0 && OFF_S % 128 == 0 && OFF_SIG % 128 == 0, "ring alignment");
     static_assert(SC >= 2, "codes ring too shallow");
     // each ring slot is always used by the same decoder group (so a group
@@ -103,14 +114,17 @@ struct QmmGeo {
     static_assert(SMEM <= QMM_SMEM_LIMIT, "shared memory");
 };
 
+template <int FMT, int NACC, int MODE>
+using QmmShape = QmmGeo<FMT, NACC, MODE == 1 || MODE == 2, MODE == 3>;  // (grouped modes; few rows)
+
 // Instruction descriptor, kind::f16: A and B (K-major) bf16, or f16 for 8-bit
 // integers; fp32 D, M = 256 (the pair), N = 256.
-__host__ __device__ constexpr uint32_t qmm_idesc(bool f16)
+__host__ __device__ constexpr uint32_t qmm_idesc(bool f16, int n = QMM_BN)
 {
     return (1u << 4)                      // D format fp32
            | ((f16 ? 0u : 1u) << 7)       // A format f16 / bf16
            | ((f16 ? 0u : 1u) << 10)      // B format f16 / bf16
-           | ((QMM_BN >> 3) << 17)  // N / 8
+           | ((uint32_t)(n >> 3) << 17)  // N / 8
            | ((256 >> 4) << 24);    // M / 16
 }
 
@@ -144,6 +158,7 @@ __device__ __forceinline__ uint32_t scale_load_edge(const uint8_t *row, bool row
 // What a pair tile computes and where its rows go.
 constexpr int QMM_DENSE = 0;        // Y[M][N] = X W^T
 constexpr int QMM_GROUPED = 1;      // expert groups of sorted rows (up to 512); row i of group g -> Y[slot_of[r0 + i]]
+constexpr int QMM_FEW_ROWS = 3;     // as 0 for up to QMM_FEW rows (8-bit integers): the weights are operand A, see below
 constexpr int QMM_GROUPED_GLU = 2;  // as 1, but CTA 0 takes gate rows, CTA 1 up rows; h = SwiGLU -> H[r0 + i]
 
 struct QmmArgs {
@@ -228,10 +243,10 @@ __device__ __forceinline__ void store_row32_f32(float *dst, const uint32_t *v, i
 }
 
 template <int FMT, int NACC, int MODE>
-__global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS, 1) qmm_kernel(const __grid_constant__ CUtensorMap tmap_x,
+__global__ void __launch_bounds__(QmmShape<FMT, NACC, MODE>::THREADS, 1) qmm_kernel(const __grid_constant__ CUtensorMap tmap_x,
                                                              const __grid_constant__ CUtensorMap tmap_c, QmmArgs a)
 {
-    using QG = QmmGeo<FMT, NACC, MODE != QMM_DENSE>;
+    using QG = QmmShape<FMT, NACC, MODE>;
     constexpr int SX = QG::SX, SD = QG::SD, SC = QG::SC, SPK = QG::SPK;
     constexpr uint32_t SIG_BYTES = 8 * 16;  // one 16-byte signal per decoder warp of CTA 1
     extern __shared__ uint8_t smem_raw[];
@@ -264,7 +279,8 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
     // m0: first X row of the tile; n0: first output column; wrow: first of
     // this CTA's 128 weight rows (over all experts); rows: valid tile rows
     int m0, n0, wrow, rows, expert = 0;
-    if constexpr (MODE == QMM_DENSE) {
+    constexpr bool GROUPED = MODE == QMM_GROUPED || MODE == QMM_GROUPED_GLU;
+    if constexpr (!GROUPED) {
         const int m_tiles = (a.M + QG::BM - 1) / QG::BM;
         m0 = (cid % m_tiles) * QG::BM;
         n0 = (cid / m_tiles) * QMM_BN;
@@ -290,7 +306,7 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
     }
     // 256-row halves of the tile that hold rows: a grouped tile of at most 256
     // rows skips the second half's X slabs, MMAs and epilogue
-    const int nh = (MODE == QMM_DENSE || rows > 256) ? NACC : 1;
+    const int nh = (!GROUPED || rows > 256) ? NACC : 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < SX; ++s) {
@@ -329,7 +345,7 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_trigger();
-    if constexpr (MODE == QMM_DENSE) pdl_wait();  // X and Y may be used by the neighbouring kernels
+    if constexpr (!GROUPED) pdl_wait();  // X and Y may be used by the neighbouring kernels
 
     if (warp == 2 + 8 * QG::NG) {
         // ---------------- X producer: both CTAs' slabs complete on CTA 0's
@@ -341,12 +357,12 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
                 const int s = kb % SX;
                 if (kb >= SX && !mbar_wait(&empty_x[s], ((kb / SX) - 1) & 1, abort_flag, a.wait_ns)) break;
                 const uint32_t bar = fx0 + 8u * (uint32_t)s;
-                mbar_arrive_expect_tx_cluster(bar, (uint32_t)(nh * QMM_X_BYTES));
+                mbar_arrive_expect_tx_cluster(bar, (uint32_t)(nh * QG::X_BYTES));
 #pragma unroll
                 for (int h = 0; h < NACC; ++h)
                     if (h < nh)
-                        tma_load_2d_pair(xring + s * QG::X_STAGE + h * QMM_X_BYTES, &tmap_x, kb * QMM_BK,
-                                         m0 + 256 * h + 128 * (int)rank, bar);
+                        tma_load_2d_pair(xring + s * QG::X_STAGE + h * QG::X_BYTES, &tmap_x, kb * QMM_BK,
+                                         m0 + 256 * h + QG::XROWS * (int)rank, bar);
                 issued = kb + 1;
             }
             *x_issued = issued;
@@ -411,7 +427,7 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
             // ---------------- MMA issuer (CTA 0)
-            constexpr uint32_t idesc = qmm_idesc(FMT == FMT_I8);
+            constexpr uint32_t idesc = qmm_idesc(FMT == FMT_I8, MODE == QMM_FEW_ROWS ? QMM_FEW : QMM_BN);
             int taken = 0, ptaken = 0;
             for (int kb = 0; kb < KB; ++kb) {
                 const int sx = kb % SX, sd = kb % SD;
@@ -430,10 +446,12 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
                     const uint64_t bd = sw128_desc(da + kk * 32);
                     const uint32_t acc = (kb > 0 || kk > 0) ? 1u : 0u;
 #pragma unroll
-                    for (int h = 0; h < NACC; ++h)
-                        if (h < nh)
-                            umma2_bf16(tmem + h * QMM_BN, sw128_desc(xa + h * QMM_X_BYTES + kk * 32), bd, idesc,
-                                       acc);
+                    for (int h = 0; h < NACC; ++h) {
+                        if (h >= nh) continue;
+                        const uint64_t xd = sw128_desc(xa + h * QG::X_BYTES + kk * 32);
+                        if constexpr (MODE == QMM_FEW_ROWS) umma2_bf16(tmem, bd, xd, idesc, acc);
+                        else umma2_bf16(tmem + h * QMM_BN, xd, bd, idesc, acc);
+                    }
                 }
                 umma2_commit_both(&empty_x[sx]);
                 umma2_commit_both(&empty_d[sd]);
@@ -547,7 +565,32 @@ __global__ void __launch_bounds__(QmmGeo<FMT, NACC, MODE != QMM_DENSE>::THREADS,
             const size_t blocks = (size_t)(MODE == QMM_DENSE ? 1 : a.E) * a.N * (a.K / 16);
             g = load_f32_unaligned(a.scales + blocks + 4 * (size_t)expert);
         }
-        if constexpr (MODE == QMM_GROUPED_GLU) {
+        if constexpr (MODE == QMM_FEW_ROWS) {
+            // a lane's weight row, 32 tokens of each group of warps
+            static_assert(NCG * 32 == QMM_FEW, "a warp's columns");
+            const int n = wrow + 32 * quarter + lane, t0 = 32 * group;
+            if (t0 < rows) {  // warp-uniform
+                uint32_t v[32];
+                if (ok) {
+                    tmem_ld32(tmem + (uint32_t)t0 + ((uint32_t)(quarter * 32) << 16), v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0x7FC00000u;
+                }
+                const float sx = t0 + lane < rows ? __ldcg(a.xscale + m0 + t0 + lane) : 0.0f;
+                const float sw = n < a.N ? __ldg(a.wscale + n) : 0.0f;
+                float *yf = reinterpret_cast<float *>(a.Y) + (size_t)(m0 + t0) * a.N + n;
+                uint16_t *yh = a.Y + (size_t)(m0 + t0) * a.N + n;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float y = __fmul_rn(__fmul_rn(__uint_as_float(v[j]), __shfl_sync(0xFFFFFFFFu, sx, j)), sw);
+                    if (t0 + j < rows && n < a.N) {
+                        if (a.yf32) yf[(size_t)j * a.N] = y;
+                        else yh[(size_t)j * a.N] = (uint16_t)f32x2_to_bf16x2(y, 0.0f);
+                    }
+                }
+            }
+        } else if constexpr (MODE == QMM_GROUPED_GLU) {
             // in accumulator h, columns c (gate) and 128 + c (up) of a row hold
             // the same h column
             const int hw = a.N / 2;
@@ -666,7 +709,7 @@ template <int FMT, int NACC, int MODE>
 static cudaError_t run_qmm(const DeviceState &ds, cudaStream_t st, const CUtensorMap &xmap, const CUtensorMap &cmap,
                            const QmmArgs &a, int pairs)
 {
-    using QG = QmmGeo<FMT, NACC, MODE != QMM_DENSE>;
+    using QG = QmmShape<FMT, NACC, MODE>;
     if (QG::SMEM > ds.max_smem_optin) return cudaErrorInvalidValue;
     static int configured_dev[64] = {0};
     if (ds.device < 64 && !configured_dev[ds.device]) {
@@ -721,13 +764,13 @@ static cudaError_t run_qmm_fmt(const DeviceState &ds, cudaStream_t st, const CUt
 // `rows` read as zero.  Codes: [wrows][row bytes], boxes of one k-block's
 // bytes x 128 rows.
 static cudaError_t encode_maps(int fmt, const uint16_t *X, long long rows, const uint8_t *codes, long long wrows,
-                               int K, CUtensorMap &xmap, CUtensorMap &cmap)
+                               int K, CUtensorMap &xmap, CUtensorMap &cmap, int xrows = 128)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)QMM_BK, 128u};
+    const cuuint32_t box[2] = {(cuuint32_t)QMM_BK, (cuuint32_t)xrows};
     const cuuint32_t estr[2] = {1u, 1u};
     CUresult r = enc(&xmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(X), dims, strides, box,
                      estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -821,12 +864,24 @@ cudaError_t launch_qmm(const DeviceState &ds, cudaStream_t st, int fmt, const ui
     return run_qmm_fmt<FMT_NVFP4>(ds, st, xmap, cmap, a);
 }
 
+// Tiles of few rows, for up to two of them; above, 256-row tiles cost no more.
+static bool qmm_i8_few(int M) { return M <= QMM_FEW; }
+
+double qmm_i8_estimate(const DeviceState &ds, int M, int N, int K)
+{
+    const double slots = ds.num_sms / 2, tiles = (N + QMM_BN - 1) / QMM_BN, kb = (K + QMM_BK - 1) / QMM_BK;
+    if (qmm_i8_few(M)) return ceil(tiles / slots) * kb * 0.22 + 8.0;
+    const double r1 = ceil(tiles * ((M + 255) / 256) / slots), r2 = ceil(tiles * ((M + 511) / 512) / slots);
+    return fmin(r1 * 0.55, r2 * 0.8) * kb + 8.0;
+}
+
 cudaError_t launch_qmm_i8(const DeviceState &ds, cudaStream_t st, const uint8_t *w, const float *wscale,
                           const uint16_t *X, const float *xscale, void *Y, bool yf32, int M, int N, int K)
 {
     if (K <= 0 || K % 16 != 0) return cudaErrorInvalidValue;
     CUtensorMap xmap, cmap;
-    cudaError_t e = encode_maps(FMT_I8, X, M, w, N, K, xmap, cmap);
+    const bool few = qmm_i8_few(M);
+    cudaError_t e = encode_maps(FMT_I8, X, M, w, N, K, xmap, cmap, few ? QMM_FEW / 2 : 128);
     if (e != cudaSuccess) return e;
     QmmArgs a;
     a.scales = nullptr;
@@ -845,6 +900,9 @@ cudaError_t launch_qmm_i8(const DeviceState &ds, cudaStream_t st, const uint8_t 
     a.xscale = xscale;
     a.wscale = wscale;
     a.yf32 = yf32;
+    if (few)
+        return run_qmm<FMT_I8, 1, QMM_FEW_ROWS>(ds, st, xmap, cmap, a,
+                                                ((M + QMM_FEW - 1) / QMM_FEW) * ((N + QMM_BN - 1) / QMM_BN));
     return run_qmm_fmt<FMT_I8>(ds, st, xmap, cmap, a);
 }
 

@@ -66,7 +66,10 @@ size_t i8_mm_workspace_bytes(int M, int K);
 cudaError_t launch_i8_quantize(const DeviceState &ds, cudaStream_t st, const void *x, int dtype, int8_t *q, float *scales,
                                int M, int K);
 cudaError_t launch_i8_mm(const DeviceState &ds, cudaStream_t st, const I8Call &c, void *workspace);
-// mx_qmm.cu: X f16 integers, y = (X W^T) xscale wscale
+// mx_qmm.cu: X f16 integers, y = (X W^T) xscale wscale; its time in us, by
+// measurements on GB300 (for each 64 elements of K of a round of tiles, one tile
+// per pair of SMs)
+double qmm_i8_estimate(const DeviceState &ds, int M, int N, int K);
 cudaError_t launch_qmm_i8(const DeviceState &ds, cudaStream_t st, const uint8_t *w, const float *wscale,
                           const uint16_t *X, const float *xscale, void *Y, bool yf32, int M, int N, int K);
 

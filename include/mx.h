@@ -496,10 +496,10 @@ int mx_i8_quantize(const void *x, int dtype, int8_t *q, float *scales, int M, in
 /* y[m][n] = (sum_k xq[m][k] * w[n][k]) * x_scales[m] * w_scales[n],
  * w int8 [N][K], w_scales fp32 [N], y [M][N] bf16 or fp32 (ydtype).  x [M][K]:
  * int8 (xdtype MX_I8) with x_scales fp32 [M], or bf16 / fp32 (x_scales null),
- * quantised as by mx_i8_quantize on the way.  Up to 16 tokens (of K up
- * to about 25,000) stream the weights and sum in 32-bit integers; the rest goes to the tensor cores, where sums
- * are fp32: exact while they stay below 2^24 in magnitude, rounded to 24
- * bits above.  The scales are applied in fp32, then y is rounded once.
+ * quantised as by mx_i8_quantize on the way.  Few tokens stream the weights,
+ * in passes of up to 16; many go to the tensor cores' GEMM.  The streaming passes sum in
+ * 32-bit integers, the GEMM in fp32: exact while sums stay below 2^24 in
+ * magnitude, rounded to 24 bits above.  The scales are applied in fp32, then y is rounded once.
  * workspace: at least mx_i8_mm_workspace_size(M, K) bytes, 256-byte aligned,
  * overwritten; null (with workspace_bytes 0) where that is at most 16 MiB: the calling stream's
  * slot.  w and w_scales are weights: they are read as soon as the kernels start.
