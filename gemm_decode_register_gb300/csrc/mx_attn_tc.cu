@@ -512,17 +512,6 @@ __device__ __forceinline__ uint64_t desc64(uint32_t lo)
     return ((uint64_t)hi << 32) | lo;
 }
 
-// One lane of the warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "elect.sync _|p, 0xFFFFFFFF;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(p));
-    return p != 0;
-}
-
 #define MX_R32(r, o)                                                                                                  \
     "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]),  \
         "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]),            \

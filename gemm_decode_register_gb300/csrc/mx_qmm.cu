@@ -425,19 +425,24 @@ __global__ void __launch_bounds__(QmmShape<FMT, NACC, MODE>::THREADS, 1) qmm_ker
             for (int kb = (issued > SC ? issued - SC : 0); kb < issued; ++kb)
                 mbar_wait(&full_c[kb % SC], (kb / SC) & 1, abort_flag, a.drain_ns, false);
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
-            // ---------------- MMA issuer (CTA 0)
+        // ---------------- MMA issuer (CTA 0).  8-bit integers: the warp stays
+        // converged and one elected lane issues; a lane in a branch of its own
+        // takes some hundred cycles for an MMA, more than a tile of few rows has.
+        constexpr bool CONVERGED = FMT == FMT_I8;
+        if (rank == 0 && (CONVERGED || lane == 0)) {
+            const bool elected = !CONVERGED || elect_one();
+            auto all = [](bool ok) { return CONVERGED ? __all_sync(0xFFFFFFFFu, ok) != 0 : ok; };
             constexpr uint32_t idesc = qmm_idesc(FMT == FMT_I8, MODE == QMM_FEW_ROWS ? QMM_FEW : QMM_BN);
             int taken = 0, ptaken = 0;
             for (int kb = 0; kb < KB; ++kb) {
                 const int sx = kb % SX, sd = kb % SD;
-                if (!mbar_wait(&full_x[sx], (kb / SX) & 1, abort_flag, a.wait_ns)) break;
+                if (!all(mbar_wait(&full_x[sx], (kb / SX) & 1, abort_flag, a.wait_ns))) break;
                 taken = kb + 1;
-                if (!mbar_wait(&dec_full[sd], (kb / SD) & 1, abort_flag, a.wait_ns)) break;
-                if (!mbar_wait(&peer_full[sd], (kb / SD) & 1, abort_flag, a.wait_ns)) break;
+                if (!all(mbar_wait(&dec_full[sd], (kb / SD) & 1, abort_flag, a.wait_ns))) break;
+                if (!all(mbar_wait(&peer_full[sd], (kb / SD) & 1, abort_flag, a.wait_ns))) break;
                 ptaken = kb + 1;
                 // arm the slot's next use: its arrival, and the signal bytes to wait for
-                mbar_arrive_expect_tx(&peer_full[sd], SIG_BYTES);
+                if (elected) mbar_arrive_expect_tx(&peer_full[sd], SIG_BYTES);
                 tc_fence_after();
                 const uint32_t xa = smem_u32(xring + sx * QG::X_STAGE);
                 const uint32_t da = smem_u32(dring + sd * QMM_W_BYTES);
@@ -449,16 +454,21 @@ __global__ void __launch_bounds__(QmmShape<FMT, NACC, MODE>::THREADS, 1) qmm_ker
                     for (int h = 0; h < NACC; ++h) {
                         if (h >= nh) continue;
                         const uint64_t xd = sw128_desc(xa + h * QG::X_BYTES + kk * 32);
+                        if (!elected) continue;
                         if constexpr (MODE == QMM_FEW_ROWS) umma2_bf16(tmem, bd, xd, idesc, acc);
                         else umma2_bf16(tmem + h * QMM_BN, xd, bd, idesc, acc);
                     }
                 }
-                umma2_commit_both(&empty_x[sx]);
-                umma2_commit_both(&empty_d[sd]);
+                if (elected) {
+                    umma2_commit_both(&empty_x[sx]);
+                    umma2_commit_both(&empty_d[sd]);
+                }
             }
-            umma2_commit_both(acc_full);  // fires once every MMA issued so far has completed
-            *x_taken = taken;
-            *peer_taken = ptaken;
+            if (elected) {
+                umma2_commit_both(acc_full);  // fires once every MMA issued so far has completed
+                *x_taken = taken;
+                *peer_taken = ptaken;
+            }
         }
     } else {
         // ---------------- decoders (warps 2 ..): group grp (8 warps) takes
