@@ -7,7 +7,7 @@
 //
 // One launch.  The rows, laid end to end in steps of four
 // 16-byte vectors per thread, are cut into equal stretches, one for each
-// block that fits on the GPU; a block walks its own with the next three steps'
+// block that fits on the GPU; a block walks its own with the next two steps'
 // copies to shared memory in flight (cp.async; each thread reads back its own),
 // over row ends too.  Within a row the order of the keys is that
 // of the logits, so a row's part of a stretch (a piece) needs no more of its row
@@ -47,10 +47,13 @@ constexpr int BEAM_THREADS = 256;
 constexpr int BEAM_WARPS = BEAM_THREADS / 32;
 constexpr int BEAM_U = 4;                      // vectors of a thread and step
 constexpr int BEAM_STEP = BEAM_THREADS * BEAM_U;  // vectors of a step
-constexpr int BEAM_RING = 4;                      // steps in shared memory
+constexpr int BEAM_RING = 3;                      // steps in shared memory
 constexpr int BEAM_BLOCKS = 3;                    // blocks of an SM
-constexpr int BEAM_QUEUE = 256;   // vectors that reach a piece's bound
-constexpr int BEAM_FOUND = 512;   // elements that do
+// Vectors that reach a piece's bound, and elements that do.  Between two rises of
+// the bound some 4 k vectors come, more where bf16 logits are equal; too small
+// a queue sends pieces the slow way (256: one seed's 1024 beams 104 us, another's 775).
+constexpr int BEAM_QUEUE = 1024;
+constexpr int BEAM_FOUND = 768;
 constexpr int BEAM_JOIN = 1024;   // and a batch entry's
 constexpr int BEAM_ENTRIES = 4096;  // of the lists, in the join's shared memory
 
@@ -427,13 +430,20 @@ __device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b
     uint32_t bound = 0xFFFFFFFFu;
     if (warp < warps) {
         uint32_t low[4] = {0u, 0u, 0u, 0u};
-        if (mine < groups) {
-            const int l = mine % lists, row = sm.beam_of[l];
+        // (of several groups of a lane, the one with the best head)
+#pragma unroll 1
+        for (int q = mine; q < groups; q += 32 * warps) {
+            const int l = q % lists, row = sm.beam_of[l];
+            uint32_t v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float off;
-                const float f = key_about(sm, row, sm.entry[l * staged + 4 * (mine / lists) + i], off);
-                low[i] = f > -INFINITY ? ordered((f - off) + 0.0f) : 0u;
+                const float f = key_about(sm, row, sm.entry[l * staged + 4 * (q / lists) + i], off);
+                v[i] = f > -INFINITY ? ordered((f - off) + 0.0f) : 0u;
+            }
+            if (v[0] > low[0]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) low[i] = v[i];
             }
         }
         // (rounded down in fp32, the entries still descend)
@@ -448,7 +458,7 @@ __device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b
     if (lane == 0) sm.warp_bound[warp] = bound;
     __syncthreads();
     bound = __reduce_min_sync(0xFFFFFFFFu, sm.warp_bound[lane % BEAM_WARPS]);
-    const float least = bound == 0u ? -FLT_MAX : unordered(bound);
+    float least = bound == 0u ? -FLT_MAX : unordered(bound);
 
     // what may reach it, of the staged entries, and of those behind them where a
     // list's last staged one does (lists descend)
@@ -463,39 +473,49 @@ __device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b
         }
         return true;
     };
+    // the bound again, from what was stored (each thread's best of up to four)
+    auto raise = [&](int stored) {
+        uint32_t low = 0u;
 #pragma unroll 1
-    for (int e = tid; e < lists * staged; e += BEAM_THREADS) offer(sm.beam_of[e / staged], sm.entry[e]);
-    if (staged < a.kpad)
-#pragma unroll 1
-        for (int l = tid; l < lists; l += BEAM_THREADS) {
-            const int row = sm.beam_of[l];
+        for (int i = lane * BEAM_WARPS + warp; i < stored; i += BEAM_THREADS) {
             float off;
-            const float f = key_about(sm, row, sm.entry[l * staged + staged - 1], off);
-            if (!(f + off >= least)) continue;
-#pragma unroll 1
-            for (int e = staged; e < a.k && offer(row, __ldcg(best + (size_t)l * a.kpad + e)); ++e) {
-            }
+            const float f = key_about(sm, sm.beam[i], sm.lt[i], off);
+            low = max(low, ordered((f - off) + 0.0f));
         }
-    __syncthreads();
-    int n = sm.n_found;
-    if (n <= BEAM_JOIN) {
-        // many: the bound again, from all of them (ranks cost the square of their number)
-        float atleast = least;
-        if (n > 2 * a.k) {
-            uint32_t low = 0u;
+        low = warp_nth(low, (a.k + BEAM_WARPS - 1) / BEAM_WARPS, [] { return 0u; });
+        if (lane == 0) sm.warp_bound[warp] = low;
+        __syncthreads();
+        low = __reduce_min_sync(0xFFFFFFFFu, sm.warp_bound[lane % BEAM_WARPS]);
+        return low == 0u ? -FLT_MAX : unordered(low);
+    };
+    int n;
 #pragma unroll 1
-            for (int i = lane * BEAM_WARPS + warp; i < n; i += BEAM_THREADS) {
+    for (;;) {
+#pragma unroll 1
+        for (int e = tid; e < lists * staged; e += BEAM_THREADS) offer(sm.beam_of[e / staged], sm.entry[e]);
+        if (staged < a.kpad)
+#pragma unroll 1
+            for (int l = tid; l < lists; l += BEAM_THREADS) {
+                const int row = sm.beam_of[l];
                 float off;
-                const float f = key_about(sm, sm.beam[i], sm.lt[i], off);
-                low = max(low, ordered((f - off) + 0.0f));
+                const float f = key_about(sm, row, sm.entry[l * staged + staged - 1], off);
+                if (!(f + off >= least)) continue;
+#pragma unroll 1
+                for (int e = staged; e < a.k && offer(row, __ldcg(best + (size_t)l * a.kpad + e)); ++e) {
+                }
             }
-            const int r = (a.k + BEAM_WARPS - 1) / BEAM_WARPS;
-            bound = warp_nth(low, r, [] { return 0u; });
-            if (lane == 0) sm.warp_bound[warp] = bound;
-            __syncthreads();
-            bound = __reduce_min_sync(0xFFFFFFFFu, sm.warp_bound[lane % BEAM_WARPS]);
-            if (bound != 0u) atleast = fmaxf(atleast, unordered(bound));
-        }
+        __syncthreads();
+        n = sm.n_found;
+        if (n <= 2 * a.k) break;
+        // many: a better bound (ranks cost the square of their number); more than fit: again with that
+        const float better = raise(min(n, BEAM_JOIN));
+        const bool again = n > BEAM_JOIN && better > least;
+        least = fmaxf(least, better);
+        if (!again) break;
+        if (tid == 0) sm.n_found = 0;
+        __syncthreads();
+    }
+    if (n <= BEAM_JOIN) {
         unsigned long long *order = sm.entry;
 #pragma unroll 1
         for (int i = tid; i < n; i += BEAM_THREADS) {
@@ -503,7 +523,7 @@ __device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b
             const int row = sm.beam[i];
             float off;
             const float f = key_about(sm, row, l, off);
-            if (f + off < atleast) continue;
+            if (f + off < least) continue;
             const int at = atomicAdd(&sm.n_kept, 1);
             sm.key[at] = key_exact(sm, row, l);
             // the order of equal keys, in 58 bits: beam (6), logit (32), token (20)
@@ -595,7 +615,6 @@ struct ChunkSmem {
 static_assert(sizeof(JoinSmem) <= sizeof(ChunkSmem), "the join's shared memory lies over the stretch's");
 static_assert(offsetof(ChunkSmem, found) % 16 == 0 && offsetof(JoinSmem, key) % 16 == 0, "rank_of");
 static_assert(BEAM_MAX_W == 64 && BEAM_MAX_V == 1 << 20, "the order of equal keys");
-static_assert(BEAM_QUEUE <= BEAM_THREADS, "a thread for each vector");
 static_assert(BEAM_BLOCKS * (sizeof(ChunkSmem) + 1024 + 256) <= 228 * 1024, "blocks of an SM");
 
 // 16 bytes to shared memory.
@@ -712,6 +731,7 @@ __global__ void __launch_bounds__(BEAM_THREADS, BEAM_BLOCKS) beam_kernel(const _
     };
 
     float bound = -FLT_MAX;  // (-inf is no candidate)
+    bool lost = false;       // more reach it than there is room for
     // raises it to what k of the threads' values reach, of which the first
     // `have` threads have one: r lanes of each of their warps.  Two barriers.
     auto raise = [&](float v, int have) {
@@ -724,41 +744,10 @@ __global__ void __launch_bounds__(BEAM_THREADS, BEAM_BLOCKS) beam_kernel(const _
         if (n > ORD_NEG_INF) bound = fmaxf(bound, unordered(n));
         __syncthreads();
     };
-    // the queue's elements that reach the bound are found, a thread for each
-    // vector; later pushes go to the other counter.  One barrier.
-    auto drain = [&] {
-        const int n = min(n_queue[turn], BEAM_QUEUE);
-        if (warp * 32 < n) {
-            unsigned hits = 0u;
-            if (tid < n) {
-                const uint4 v = queue[tid];
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) hits |= (L::get(v, j) >= bound ? 1u : 0u) << j;
-            }
-            int o = __popc(hits);
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int before = __shfl_up_sync(0xFFFFFFFFu, o, d);
-                if (lane >= d) o += before;
-            }
-            int base = 0;
-            if (lane == 31) base = atomicAdd(&n_found, o);
-            o += __shfl_sync(0xFFFFFFFFu, base, 31) - __popc(hits);
-            for (; hits; hits &= hits - 1, ++o) {
-                const int j = __ffs((int)hits) - 1;
-                if (o < BEAM_FOUND) found[o] = logit_token(L::one(queue, tid * VEC + j), queue_at[tid] + j);
-            }
-        }
-        __syncthreads();
-        if (tid == 0) n_queue[turn] = 0;
-        turn ^= 1;
-    };
     // the bound from what is found so far, dealt out over the warps (each
-    // thread's larger of two); what no longer reaches it is dropped.  Nothing
-    // where little is found: that is ranked sooner than sifted.
-    auto sift = [&] {
-        const int n = n_found;
-        if (n <= BEAM_THREADS / 4) return;
+    // thread's largest of three); what no longer reaches it is dropped.  n: how
+    // much is found, as everyone has read it before a barrier of `raise`.
+    auto sift = [&](int n) {
         constexpr int F = BEAM_FOUND / BEAM_THREADS;
         unsigned long long mine[F];
         uint32_t v = 0u;
@@ -776,6 +765,45 @@ __global__ void __launch_bounds__(BEAM_THREADS, BEAM_BLOCKS) beam_kernel(const _
         for (int i = 0; i < F; ++i)
             if (mine[i] >= lo) found[atomicAdd(&n_found, 1)] = mine[i];
         __syncthreads();
+    };
+
+    // The queue's elements that reach the bound are found, a thread for each
+    // vector, and sifted; later pushes go to the other counter.  (The code of
+    // loops that run a few times is left rolled: it is fetched more than run.)
+    auto drain = [&] {
+        const int n = min(n_queue[turn], BEAM_QUEUE);
+        lost |= n_queue[turn] > BEAM_QUEUE;
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += BEAM_THREADS) {
+            const int i = i0 + tid;
+            unsigned hits = 0u;
+            if (i < n) {
+                const uint4 v = queue[i];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) hits |= (L::get(v, j) >= bound ? 1u : 0u) << j;
+            }
+            int o = __popc(hits);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int before = __shfl_up_sync(0xFFFFFFFFu, o, d);
+                if (lane >= d) o += before;
+            }
+            int base = 0;
+            if (lane == 31 && o > 0) base = atomicAdd(&n_found, o);
+            o += __shfl_sync(0xFFFFFFFFu, base, 31) - __popc(hits);
+            for (; hits; hits &= hits - 1, ++o) {
+                const int j = __ffs((int)hits) - 1;
+                if (o < BEAM_FOUND) found[o] = logit_token(L::one(queue, i * VEC + j), queue_at[i] + j);
+            }
+            __syncthreads();
+            const int f = n_found;
+            lost |= f > BEAM_FOUND;
+            if (lost) break;
+            if (f > BEAM_THREADS / 4) sift(f);  // (fewer are ranked sooner than sifted)
+            else __syncthreads();               // (everyone has read the count)
+        }
+        if (tid == 0) n_queue[turn] = 0;
+        turn ^= 1;
     };
 
     const long long end = min((long long)(blockIdx.x + 1) * a.span, (long long)a.B * a.W * a.steps);
@@ -804,7 +832,7 @@ __global__ void __launch_bounds__(BEAM_THREADS, BEAM_BLOCKS) beam_kernel(const _
     uint32_t bits[U];
     float ref = -INFINITY;
     float2 sum2 = make_float2(0.0f, 0.0f);
-    bool hot = true, lost = false;
+    bool hot = true;
     for (int i = 0; i < steps; ++i) {
         const bool row_ends = step + 1 == a.steps, last = row_ends || i + 1 == steps;  // of the piece
         fetch_next();
@@ -865,12 +893,9 @@ __global__ void __launch_bounds__(BEAM_THREADS, BEAM_BLOCKS) beam_kernel(const _
         }
         hot = __syncthreads_or(filling);  // (n_queue itself may have grown by another's next step)
         const int done = step - first + 1;
-        // (2, 8, 32, .. steps; for many candidates every power of two)
-        if (last || hot || ((done & (done - 1)) == 0 && (done & (a.k > 48 ? ~1 : 0x2AAAAAAA)) != 0)) {
-            lost |= n_queue[turn] > BEAM_QUEUE;
+        // (2, 8, 32, .. steps; for many candidates, whose first bounds are loose, 1, 2, 4, ..)
+        if (last || hot || ((done & (done - 1)) == 0 && (done & (a.k > 48 ? ~0 : 0x2AAAAAAA)) != 0)) {
             drain();
-            lost |= n_found > BEAM_FOUND;
-            if (!lost) sift();
         }
         if (last) {
             // ---- the piece ends

@@ -41,7 +41,9 @@
 // operand B, of N = 128: a quarter of the MMA time and a half of the X slabs, below
 // the time that the weights take to arrive; the freed shared memory holds
 // twelve k-blocks of codes.  Tensor memory then has a weight row per lane and a
-// token per column.  (64 tokens through 128000 x 8192 466 -> 176 us.)
+// token per column.  (64 tokens through 128000 x 8192: 367 us against 402 in a tile of 256 rows. A k-block
+// takes 0.43 us; a third group of decoders, eight slots of decoded
+// tiles, slots of two k-blocks of codes, or one commit instead of two left it there.)
 //
 // Every mbarrier wait is bounded (about two seconds of %globaltimer); a wait
 // that gives up sets MX_DEVERR_TIMEOUT in the device error word, the CTA
@@ -874,15 +876,15 @@ cudaError_t launch_qmm(const DeviceState &ds, cudaStream_t st, int fmt, const ui
     return run_qmm_fmt<FMT_NVFP4>(ds, st, xmap, cmap, a);
 }
 
-// Tiles of few rows, for up to two of them; above, 256-row tiles cost no more.
+// A tile of few rows where one is enough: two would take longer than one of 256 rows.
 static bool qmm_i8_few(int M) { return M <= QMM_FEW; }
 
 double qmm_i8_estimate(const DeviceState &ds, int M, int N, int K)
 {
     const double slots = ds.num_sms / 2, tiles = (N + QMM_BN - 1) / QMM_BN, kb = (K + QMM_BK - 1) / QMM_BK;
-    if (qmm_i8_few(M)) return ceil(tiles / slots) * kb * 0.22 + 8.0;
+    if (qmm_i8_few(M)) return ceil(tiles / slots) * kb * 0.43 + 8.0;
     const double r1 = ceil(tiles * ((M + 255) / 256) / slots), r2 = ceil(tiles * ((M + 511) / 512) / slots);
-    return fmin(r1 * 0.55, r2 * 0.8) * kb + 8.0;
+    return fmin(r1 * 0.48, r2 * 0.67) * kb + 8.0;
 }
 
 cudaError_t launch_qmm_i8(const DeviceState &ds, cudaStream_t st, const uint8_t *w, const float *wscale,
