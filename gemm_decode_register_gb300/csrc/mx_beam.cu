@@ -490,7 +490,7 @@ __device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b
     };
     int n;
 #pragma unroll 1
-    for (;;) {
+    for (int turn = 0;; ++turn) {
 #pragma unroll 1
         for (int e = tid; e < lists * staged; e += BEAM_THREADS) offer(sm.beam_of[e / staged], sm.entry[e]);
         if (staged < a.kpad)
@@ -509,7 +509,7 @@ __device__ __forceinline__ void beam_join(const BeamArgs &a, JoinSmem &sm, int b
         if (n <= 2 * a.k) break;
         // many: a better bound (ranks cost the square of their number); more than fit: again with that
         const float better = raise(min(n, BEAM_JOIN));
-        const bool again = n > BEAM_JOIN && better > least;
+        const bool again = n > BEAM_JOIN && better > least && turn < 8;
         least = fmaxf(least, better);
         if (!again) break;
         if (tid == 0) sm.n_found = 0;
