@@ -997,11 +997,12 @@ size_t beam_workspace_bytes(int B, int W, int V, int k)
 }
 
 template <typename E>
-static cudaError_t run_beam(cudaStream_t st, const BeamArgs &a, int stretches)
+static cudaError_t run_beam(const DeviceState &ds, cudaStream_t st, const BeamArgs &a, int stretches)
 {
     const dim3 grid((unsigned)stretches);
+    static unsigned char plain[64], masked[64];
     auto kernel = a.mask ? beam_kernel<E, true> : beam_kernel<E, false>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ChunkSmem));
+    const cudaError_t e = allow_smem(ds, kernel, (int)sizeof(ChunkSmem), a.mask ? masked : plain);
     return e != cudaSuccess ? e : launch_k(kernel, grid, dim3(BEAM_THREADS), sizeof(ChunkSmem), st, a);
 }
 
@@ -1034,7 +1035,7 @@ cudaError_t launch_beam_select(const DeviceState &ds, cudaStream_t st, const Bea
     a.count = ds.ws_count;
     a.best = static_cast<unsigned long long *>(workspace);
     a.sums = reinterpret_cast<float2 *>(a.best + lists * a.kpad);
-    return c.dtype == MX_F32 ? run_beam<float>(st, a, split.stretches) : run_beam<uint16_t>(st, a, split.stretches);
+    return c.dtype == MX_F32 ? run_beam<float>(ds, st, a, split.stretches) : run_beam<uint16_t>(ds, st, a, split.stretches);
 }
 
 }  // namespace mx

@@ -312,7 +312,8 @@ template <int NB, typename Y>
 static cudaError_t run_mv(const DeviceState &ds, cudaStream_t st, const I8MvArgs &a)
 {
     const int smem = mv_smem(a.tokens, a.K);
-    const cudaError_t e = cudaFuncSetAttribute(i8_mv_kernel<NB, Y>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static unsigned char done[64];
+    const cudaError_t e = allow_smem(ds, i8_mv_kernel<NB, Y>, ds.max_smem_optin, done);
     if (e != cudaSuccess) return e;
     const int rounds = ((a.N + 15) / 16 + MV_WARPS / a.parts - 1) / (MV_WARPS / a.parts);
     return launch_k(i8_mv_kernel<NB, Y>, dim3(rounds < ds.num_sms ? rounds : ds.num_sms), dim3(MV_THREADS), smem, st, a);

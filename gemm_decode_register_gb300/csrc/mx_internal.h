@@ -91,6 +91,17 @@ cudaError_t launch_moe_ffn_prefill(const DeviceState &ds, cudaStream_t st, int f
                                    const uint16_t *x, const int32_t *ids, const float *rw, float *out, int T, int E,
                                    int topk, int H, int I, void *workspace);
 
+// Let a kernel take up to `bytes` of dynamic shared memory, once per device (`done`: a
+// static of the caller, a byte for each device).
+template <typename Kernel>
+inline cudaError_t allow_smem(const DeviceState &ds, Kernel kernel, int bytes, unsigned char (&done)[64])
+{
+    if (ds.device >= 0 && ds.device < 64 && done[ds.device]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && ds.device >= 0 && ds.device < 64) done[ds.device] = 1;
+    return e;
+}
+
 // Test hook of the tensor-core kernels' bounded waits (mx_debug_qmm_stall).
 void set_qmm_stall(int stall_x, unsigned long long wait_ns);
 int qmm_stall(unsigned long long *wait_ns);  // its state: whether to stall, and the limit of a wait

@@ -745,10 +745,9 @@ cudaError_t launch_kv_remap(const DeviceState &ds, cudaStream_t st, const RemapC
     const int S = c.S_in > c.S_out ? c.S_in : c.S_out;
     const int pages = c.in_pages > c.out_pages ? c.in_pages : c.out_pages;
     const size_t smem = remap_smem(c.S_in, c.S_out);
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kv_remap_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    static unsigned char done[64];
+    const cudaError_t e = allow_smem(ds, kv_remap_kernel, (int)remap_smem(POOL_MAX_SLOTS, POOL_MAX_SLOTS), done);
+    if (e != cudaSuccess) return e;
     return run_cluster(st, kv_remap_kernel, pool_ctas(S, pages, c.pool.num_pages), smem, a);
 }
 

@@ -658,7 +658,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int | None = None
     if rows > 0:
         lib = load()
         stride = logits.stride(0) if rows > 1 else V
-        op = [t.data_ptr() for t in out]
+        a, b, c, d, e, f = out
+        op = (a.data_ptr(), b.data_ptr(), c.data_ptr(), d.data_ptr(), e.data_ptr(), f.data_ptr())
         wp, wn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
         _stream()
         s = lib.mx_beam_select(xp, dt, stride, sp, mp, ms, B, W, V, k, eos if eos >= 0 else -1, *op, wp, wn)
