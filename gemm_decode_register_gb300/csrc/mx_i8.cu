@@ -73,13 +73,15 @@ __device__ __forceinline__ void store8(uint16_t *p, const int (&c)[8])
 
 // One token per block: s = max |x| / 127, q = x / s to the nearest even
 // integer.  s = 0 (a row of zeros, or of values that small): q = 0.  A NaN or
-// an infinity in the row: s = NaN, q = 0.
+// an infinity in the row: s = NaN, q = 0.  early: whether dependents may start
+// at once; not when the codes may be the next call's weights, which its kernel
+// reads before it waits.
 template <typename In, typename Out>
 __global__ void __launch_bounds__(QI8_THREADS) i8_quantize_kernel(const In *__restrict__ x, Out *__restrict__ q,
-                                                                  float *__restrict__ scales, int K)
+                                                                  float *__restrict__ scales, int K, bool early)
 {
     __shared__ float wmax[QI8_THREADS / 32];
-    pdl_trigger();
+    if (early) pdl_trigger();
     pdl_wait();
     const size_t row = blockIdx.x;
     const In *xr = x + row * K;
@@ -136,6 +138,7 @@ __global__ void __launch_bounds__(QI8_THREADS) i8_quantize_kernel(const In *__re
         for (int j = 0; j < 8; ++j) c[j] = any ? code_of(v[j], s) : 0;
         store8(qr + 8 * i, c);
     }
+    if (!early) __threadfence();
 }
 
 // 8-bit integers as f16 integers, 16 at a time.
@@ -350,17 +353,17 @@ static cudaError_t launch_i8_mv(const DeviceState &ds, cudaStream_t st, const in
 }
 
 template <typename In, typename Out>
-static cudaError_t run_quantize(cudaStream_t st, const void *x, void *q, float *scales, int M, int K)
+static cudaError_t run_quantize(cudaStream_t st, const void *x, void *q, float *scales, int M, int K, bool early)
 {
     return launch_k(i8_quantize_kernel<In, Out>, dim3(M), dim3(QI8_THREADS), 0, st, static_cast<const In *>(x),
-                    static_cast<Out *>(q), scales, K);
+                    static_cast<Out *>(q), scales, K, early);
 }
 
 cudaError_t launch_i8_quantize(const DeviceState &, cudaStream_t st, const void *x, int dtype, int8_t *q, float *scales,
-                               int M, int K)
+                               int M, int K, bool early)
 {
-    return dtype == MX_F32 ? run_quantize<float, int8_t>(st, x, q, scales, M, K)
-                           : run_quantize<uint16_t, int8_t>(st, x, q, scales, M, K);
+    return dtype == MX_F32 ? run_quantize<float, int8_t>(st, x, q, scales, M, K, early)
+                           : run_quantize<uint16_t, int8_t>(st, x, q, scales, M, K, early);
 }
 
 size_t i8_mm_workspace_bytes(int M, int K)
@@ -392,7 +395,7 @@ cudaError_t launch_i8_mm(const DeviceState &ds, cudaStream_t st, const I8Call &c
     if (const int pass = i8_pass(ds, c.M, c.N, c.K)) {
         const int8_t *x = static_cast<const int8_t *>(c.x);
         if (c.xdtype != MX_I8) {
-            e = launch_i8_quantize(ds, st, c.x, c.xdtype, static_cast<int8_t *>(workspace), own_sx, c.M, c.K);
+            e = launch_i8_quantize(ds, st, c.x, c.xdtype, static_cast<int8_t *>(workspace), own_sx, c.M, c.K, true);
             if (e != cudaSuccess) return e;
             x = static_cast<const int8_t *>(workspace);
         }
@@ -404,8 +407,8 @@ cudaError_t launch_i8_mm(const DeviceState &ds, cudaStream_t st, const I8Call &c
         e = launch_k(i8_widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, st,
                      static_cast<const int8_t *>(c.x), h, n16);
     } else {
-        e = c.xdtype == MX_F32 ? run_quantize<float, uint16_t>(st, c.x, h, own_sx, c.M, c.K)
-                               : run_quantize<uint16_t, uint16_t>(st, c.x, h, own_sx, c.M, c.K);
+        e = c.xdtype == MX_F32 ? run_quantize<float, uint16_t>(st, c.x, h, own_sx, c.M, c.K, true)
+                               : run_quantize<uint16_t, uint16_t>(st, c.x, h, own_sx, c.M, c.K, true);
     }
     if (e != cudaSuccess) return e;
     return launch_qmm_i8(ds, st, reinterpret_cast<const uint8_t *>(c.w), c.sw, h, sx, c.y, c.ydtype == MX_F32, c.M, c.N, c.K);

@@ -64,7 +64,7 @@ struct I8Call {
 };
 size_t i8_mm_workspace_bytes(int M, int K);
 cudaError_t launch_i8_quantize(const DeviceState &ds, cudaStream_t st, const void *x, int dtype, int8_t *q, float *scales,
-                               int M, int K);
+                               int M, int K, bool early);
 cudaError_t launch_i8_mm(const DeviceState &ds, cudaStream_t st, const I8Call &c, void *workspace);
 // mx_qmm.cu: X f16 integers, y = (X W^T) xscale wscale; its time in us, by
 // measurements on GB300 (for each 64 elements of K of a round of tiles, one tile

@@ -199,7 +199,7 @@ extern "C" int mx_i8_quantize(const void *x, int dtype, int8_t *q, float *scales
     if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scales, 4)) return MX_EALIGN;
     DeviceState *ds = device_state();
     if (!ds) return MX_ECUDA;
-    return finish(launch_i8_quantize(*ds, current_stream(), x, dtype, q, scales, M, K));
+    return finish(launch_i8_quantize(*ds, current_stream(), x, dtype, q, scales, M, K, false));
 }
 
 extern "C" size_t mx_i8_mm_workspace_size(int M, int K)

@@ -490,7 +490,8 @@ int mx_kv_copy_pages(const mx_paged_kv *kv, int layers, const int32_t *copies, i
  * x[m][k] / scales[m] to the nearest integer, ties to even (quotients rounded
  * to fp32).  x [M][K] bf16 or fp32.  A row whose scale is 0 has codes 0; one
  * that holds a NaN or an infinity has a NaN scale and codes 0.  K a multiple of
- * 16; x and q 16-byte aligned. */
+ * 16; x and q 16-byte aligned.  (Weights may be quantised by it too, a row for each
+ * output channel, and used by the next call.) */
 int mx_i8_quantize(const void *x, int dtype, int8_t *q, float *scales, int M, int K);
 
 /* y[m][n] = (sum_k xq[m][k] * w[n][k]) * x_scales[m] * w_scales[n],

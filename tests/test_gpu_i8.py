@@ -127,6 +127,32 @@ def test_many_tokens(M, N, K, ydt):
     assert ops.device_error() == 0
 
 
+@pytest.mark.parametrize("M", [1, 8, 40])
+def test_weights_quantised_by_the_call_before(M):
+    """The product reads its weights as soon as it starts, so not before the quantisation that wrote them has ended."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    N, K = 9000, 4096
+    g = torch.Generator(device="cuda").manual_seed(M)
+    sources = [torch.randn((N, K), generator=g, device="cuda") for _ in range(4)]
+    x = torch.randn((M, K), generator=g, device="cuda").bfloat16()
+    xq, sx = ops.i8_quantize(x)
+    q, sw = torch.zeros((N, K), dtype=torch.int8, device="cuda"), torch.zeros(N, device="cuda")
+    ys = [[torch.empty((M, N), device="cuda") for _ in range(2)] for _ in sources]
+    torch.cuda.synchronize()
+    for w, (a, b) in zip(sources, ys):
+        ops.i8_quantize(w, q, sw)
+        ops.i8_mm(xq, q, sw, sx, out=a)
+        ops.i8_quantize(w.neg_(), q, sw)
+        ops.i8_mm(x, q, sw, out=b)
+    for w, (a, b) in zip(sources, ys):
+        wq, sw = ops.i8_quantize(w)
+        _check(torch, b, xq, sx, wq, sw, True)
+        _check(torch, a, xq, sx, -wq, sw, True)
+    assert ops.device_error() == 0
+
+
 def test_offsets_past_32_bits():
     """Weights of more than 4 GB: their last rows."""
     torch = need_gpu()
