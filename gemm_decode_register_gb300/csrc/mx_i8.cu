@@ -25,6 +25,7 @@
 
 #include "mx_common.cuh"
 #include "mx_serve.h"
+#include "mx_tc.cuh"
 
 namespace mx {
 
@@ -174,6 +175,7 @@ struct I8MvArgs {
     int N, K;
     int tokens;  // of this pass, at most 8 NB
     int parts;   // warps that share a row tile's K: 1, 2, 4, 8 or 16
+    int span;    // elements of K of a CTA: all, or the half of a pair's (a multiple of 64)
     int xpitch;  // bytes of a staged token, an odd multiple of 64
 };
 
@@ -196,14 +198,22 @@ __device__ __forceinline__ void mma_s8_16832(int (&d)[4], uint32_t a0, uint32_t 
 // NB: groups of 8 tokens (places past the last token repeat it).  Y: float or uint16_t (bf16).
 // mma.sync does about 130 T 8-bit operations a second here (and no more of f16), what eight
 // tokens ask of the weights' stream: 8 through 128000 x 8192 take 154 us, 16 258.
-template <int NB, typename Y>
+//
+// PAIR: where a CTA's shared memory has no room for the tokens, a cluster of two shares
+// each row tile, either half of K its own; the halves' sums meet through each
+// other's shared memory, and a pass more over the weights is saved (eight tokens
+// through 8192 x 28672 64 us, 107 in two passes; sixteen 113, 166 in three).
+template <int NB, typename Y, bool PAIR>
 __global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(const __grid_constant__ I8MvArgs a)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t *xs = smem;                                                        // [tokens][xpitch]
     int4 *red = reinterpret_cast<int4 *>(smem + (size_t)a.tokens * a.xpitch);  // [2][warps][NB][32]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int steps = (a.K + 63) / 64;             // of a row
+    const int steps = a.span / 64;                 // of a row
+    const int rank = PAIR ? (int)cluster_ctarank() : 0;
+    const int k0 = rank * a.span, ks = min(a.K - k0, a.span);  // this CTA's stretch of K
+    const int stride = PAIR ? gridDim.x / 2 : gridDim.x, start = PAIR ? blockIdx.x / 2 : blockIdx.x;
     const int per_cta = MV_WARPS / a.parts;        // row tiles at a time
     const int part = warp % a.parts, sub = warp / a.parts;
     const int tiles = (a.N + 15) / 16;
@@ -214,22 +224,22 @@ __global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(const __grid_const
     // groups are in flight while a warp waits (with one, eight tokens through
     // 128000 x 8192 took 186 us instead of 156).  The loads run ahead over tile ends.
     uint4 even[MV_GROUP][2], odd[MV_GROUP][2];
-    int load_round = blockIdx.x, load_q = 0;
+    int load_round = start, load_q = 0;
     // step number i of group q: part + parts * (q * MV_GROUP + i)
     auto load = [&](uint4 (&v)[MV_GROUP][2]) {
         const int tile = load_round * per_cta + sub;
         const int n0 = 16 * tile + g, n1 = n0 + 8;
-        const int8_t *w = a.w + 16 * t;
+        const int8_t *w = a.w + k0 + 16 * t;
 #pragma unroll
         for (int i = 0; i < MV_GROUP; ++i) {
             const int k = 64 * (part + a.parts * (load_q * MV_GROUP + i));
-            const bool in = load_round < rounds && k + 16 * t < a.K;
+            const bool in = load_round < rounds && k + 16 * t < ks;
             v[i][0] = in && n0 < a.N ? ld_stream_v4(w + (size_t)n0 * a.K + k) : make_uint4(0u, 0u, 0u, 0u);
             v[i][1] = in && n1 < a.N ? ld_stream_v4(w + (size_t)n1 * a.K + k) : make_uint4(0u, 0u, 0u, 0u);
         }
         if (++load_q == groups) {
             load_q = 0;
-            load_round += gridDim.x;
+            load_round += stride;
         }
     };
     pdl_trigger();
@@ -240,12 +250,12 @@ __global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(const __grid_const
     for (int i = threadIdx.x; i < a.tokens * vecs; i += MV_THREADS) {
         const int m = i / vecs, c = i - m * vecs;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (16 * c < a.K) v = __ldcg(reinterpret_cast<const uint4 *>(a.x + (size_t)m * a.K) + c);
+        if (16 * c < ks) v = __ldcg(reinterpret_cast<const uint4 *>(a.x + (size_t)m * a.K + k0) + c);
         *reinterpret_cast<uint4 *>(xs + (size_t)m * a.xpitch + 16 * c) = v;
     }
     __syncthreads();
 
-    int flip = 0, round = blockIdx.x, q = 0;
+    int flip = 0, round = start, q = 0;
     int acc[NB][4] = {};
     auto step = [&](uint4 (&v)[MV_GROUP][2]) {
 #pragma unroll
@@ -269,74 +279,87 @@ __global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(const __grid_const
             r[(warp * NB + b) * 32 + lane] = make_int4(acc[b][0], acc[b][1], acc[b][2], acc[b][3]);
             acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0;
         }
-        __syncthreads();
+        if constexpr (PAIR) cluster_sync_all();
+        else __syncthreads();
         const int *ri = reinterpret_cast<const int *>(r);
-        for (int o = threadIdx.x; o < per_cta * NB * 128; o += MV_THREADS) {
+        for (int o = threadIdx.x + rank * MV_THREADS; o < per_cta * NB * 128; o += (PAIR ? 2 : 1) * MV_THREADS) {
             const int row = o % 16, c = o / 16 % 8, b = o / 128 % NB, s = o / (128 * NB);
             const int m = 8 * b + c, n = 16 * (round * per_cta + s) + row;
             if (m >= a.tokens || n >= a.N) continue;
             const int at = 4 * (4 * (row % 8) + c / 2) + 2 * (row / 8) + c % 2;
             int sum = 0;
-            for (int p = 0; p < a.parts; ++p) sum += ri[((s * a.parts + p) * NB + b) * 128 + at];
+            for (int p = 0; p < a.parts; ++p) {
+                const int *v = ri + ((s * a.parts + p) * NB + b) * 128 + at;
+                sum += *v;
+                if constexpr (PAIR) sum += ld_cluster_s32(map_to_cta(smem_u32(v), rank ^ 1));
+            }
             const float y = __fmul_rn(__fmul_rn((float)sum, __ldcg(a.sx + m)), __ldg(a.sw + n));
             if constexpr (sizeof(Y) == 4) static_cast<float *>(a.y)[(size_t)m * a.N + n] = y;
             else static_cast<uint16_t *>(a.y)[(size_t)m * a.N + n] = (uint16_t)f32x2_to_bf16x2(y, 0.0f);
         }
-        round += gridDim.x;
+        round += stride;
     };
     while (round < rounds) {
         step(even);
         if (round >= rounds) break;
         step(odd);
     }
+    if constexpr (PAIR) cluster_sync_all();  // (the other CTA may still read this one's sums)
 }
 
 // ------------------------------------------------------------ host
 
-static int mv_pitch(int K)
-{
-    const int p = (K + 63) / 64 * 64;
-    return p % 128 == 0 ? p + 64 : p;  // two tokens' 64 bytes then fall into different banks
-}
+// Elements of K that a CTA takes: all, or half where a pair shares them.
+static int mv_span(int K, bool pair) { return ((pair ? (K + 1) / 2 : K) + 63) / 64 * 64; }
 
-static int mv_smem(int tokens, int K) { return tokens * mv_pitch(K) + 2 * MV_WARPS * ((tokens + 7) / 8) * 512; }
+static int mv_pitch(int span) { return span % 128 == 0 ? span + 64 : span; }  // two tokens' 64 bytes then fall into different banks
+
+static int mv_smem(int tokens, int span) { return tokens * mv_pitch(span) + 2 * MV_WARPS * ((tokens + 7) / 8) * 512; }
 
 constexpr int MV_NB = 2;  // most groups of 8 tokens of a pass
 
 // Most tokens a pass can stage beside the sums' space.
-static int mv_pass_tokens(const DeviceState &ds, int K)
+static int mv_pass_tokens(const DeviceState &ds, int span)
 {
     for (int m = 8 * MV_NB; m > 0; --m)
-        if (mv_smem(m, K) <= ds.max_smem_optin) return m;
+        if (mv_smem(m, span) <= ds.max_smem_optin) return m;
     return 0;
 }
 
-template <int NB, typename Y>
+struct I8Passes {
+    int tokens;  // of a pass; 0: not by passes
+    bool pair;
+};
+
+template <int NB, typename Y, bool PAIR>
 static cudaError_t run_mv(const DeviceState &ds, cudaStream_t st, const I8MvArgs &a)
 {
-    const int smem = mv_smem(a.tokens, a.K);
     static unsigned char done[64];
-    const cudaError_t e = allow_smem(ds, i8_mv_kernel<NB, Y>, ds.max_smem_optin, done);
+    const cudaError_t e = allow_smem(ds, i8_mv_kernel<NB, Y, PAIR>, ds.max_smem_optin, done);
     if (e != cudaSuccess) return e;
-    const int rounds = ((a.N + 15) / 16 + MV_WARPS / a.parts - 1) / (MV_WARPS / a.parts);
-    return launch_k(i8_mv_kernel<NB, Y>, dim3(rounds < ds.num_sms ? rounds : ds.num_sms), dim3(MV_THREADS), smem, st, a);
+    const int rounds = ((a.N + 15) / 16 + MV_WARPS / a.parts - 1) / (MV_WARPS / a.parts), most = ds.num_sms / (PAIR ? 2 : 1);
+    const int ctas = (rounds < most ? rounds : most) * (PAIR ? 2 : 1);
+    return launch_cluster_k(i8_mv_kernel<NB, Y, PAIR>, PAIR ? 2 : 1, dim3(ctas), dim3(MV_THREADS), mv_smem(a.tokens, a.span), st, a);
 }
 
 template <typename Y>
-static cudaError_t run_mv_pass(const DeviceState &ds, cudaStream_t st, const I8MvArgs &a)
+static cudaError_t run_mv_pass(const DeviceState &ds, cudaStream_t st, const I8MvArgs &a, bool pair)
 {
-    return a.tokens <= 8 ? run_mv<1, Y>(ds, st, a) : run_mv<2, Y>(ds, st, a);
+    if (pair) return a.tokens <= 8 ? run_mv<1, Y, true>(ds, st, a) : run_mv<2, Y, true>(ds, st, a);
+    return a.tokens <= 8 ? run_mv<1, Y, false>(ds, st, a) : run_mv<2, Y, false>(ds, st, a);
 }
 
 static cudaError_t launch_i8_mv(const DeviceState &ds, cudaStream_t st, const int8_t *x, const float *sx, const int8_t *w,
-                                const float *sw, void *y, int ydtype, int M, int N, int K, int pass)
+                                const float *sw, void *y, int ydtype, int M, int N, int K, I8Passes by)
 {
     const size_t ye = ydtype == MX_F32 ? 4 : 2;
     I8MvArgs a;
-    const int steps = (K + 63) / 64;
+    a.span = mv_span(K, by.pair);
+    a.xpitch = mv_pitch(a.span);
+    const int steps = a.span / 64;
     a.parts = 1;  // (each warp has two groups of loads of a tile or more)
     while (a.parts < MV_WARPS && steps >= 2 * a.parts * MV_GROUP) a.parts *= 2;
-    for (int m = 0; m < M; m += pass) {
+    for (int m = 0; m < M; m += by.tokens) {
         a.x = x + (size_t)m * K;
         a.sx = sx + m;
         a.w = w;
@@ -344,9 +367,8 @@ static cudaError_t launch_i8_mv(const DeviceState &ds, cudaStream_t st, const in
         a.y = static_cast<char *>(y) + (size_t)m * N * ye;
         a.N = N;
         a.K = K;
-        a.tokens = M - m < pass ? M - m : pass;
-        a.xpitch = mv_pitch(K);
-        const cudaError_t e = ydtype == MX_F32 ? run_mv_pass<float>(ds, st, a) : run_mv_pass<uint16_t>(ds, st, a);
+        a.tokens = M - m < by.tokens ? M - m : by.tokens;
+        const cudaError_t e = ydtype == MX_F32 ? run_mv_pass<float>(ds, st, a, by.pair) : run_mv_pass<uint16_t>(ds, st, a, by.pair);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -373,17 +395,27 @@ size_t i8_mm_workspace_bytes(int M, int K)
     return codes + ((size_t)M * 4 + 255) / 256 * 256;
 }
 
-// Tokens of a streaming pass, or 0 for the GEMM: whichever takes less by these
-// estimates (us, measured on GB300).  A pass streams the weights, at 6.6 MB
-// per us for up to 8 tokens and 4.0 for up to 16, and takes about 5 beside.
-// The GEMM: see qmm_i8_estimate.
-static int i8_pass(const DeviceState &ds, int M, int N, int K)
+// Passes of the streaming kernel, by single CTAs or pairs, or the GEMM: whichever
+// takes least by these estimates (us, measured on GB300).  A pass streams the
+// weights, at 6.6 MB per us for up to 8 tokens and 4.0 for up to 16, and takes
+// about 5 beside, a pair's 1 more.  The GEMM: see qmm_i8_estimate.
+static I8Passes i8_passes(const DeviceState &ds, int M, int N, int K)
 {
-    const int most = mv_pass_tokens(ds, K);
-    if (most == 0) return 0;
-    const int passes = (M + most - 1) / most, pass = (M + passes - 1) / passes;  // (equal passes)
-    const double stream = passes * ((double)N * K / (pass <= 8 ? 6.6e6 : 4.0e6) + 5.0);
-    return stream <= qmm_i8_estimate(ds, M, N, K) ? pass : 0;
+    I8Passes best = {0, false};
+    double least = qmm_i8_estimate(ds, M, N, K);
+    for (const bool pair : {false, true}) {
+        const int most = mv_pass_tokens(ds, mv_span(K, pair));
+        if (most == 0) continue;
+        const int passes = (M + most - 1) / most, tokens = (M + passes - 1) / passes;  // (equal passes)
+        // (crowded: loads in flight want room in what shared memory leaves of L1)
+        const bool crowded = mv_smem(tokens, mv_span(K, pair)) > 200 * 1024;
+        const double rate = tokens <= 8 ? (crowded ? 4.4e6 : 6.6e6) : (crowded ? 3.4e6 : 4.0e6);
+        const double us = passes * ((double)N * K / rate + (pair ? 6.0 : 5.0));
+        if (us > least || (pair && us == least)) continue;
+        least = us;
+        best = {tokens, pair};
+    }
+    return best;
 }
 
 cudaError_t launch_i8_mm(const DeviceState &ds, cudaStream_t st, const I8Call &c, void *workspace)
@@ -392,14 +424,15 @@ cudaError_t launch_i8_mm(const DeviceState &ds, cudaStream_t st, const I8Call &c
     float *own_sx = reinterpret_cast<float *>(static_cast<char *>(workspace) + codes);
     const float *sx = c.xdtype == MX_I8 ? c.sx : own_sx;
     cudaError_t e;
-    if (const int pass = i8_pass(ds, c.M, c.N, c.K)) {
+    const I8Passes by = i8_passes(ds, c.M, c.N, c.K);
+    if (by.tokens) {
         const int8_t *x = static_cast<const int8_t *>(c.x);
         if (c.xdtype != MX_I8) {
             e = launch_i8_quantize(ds, st, c.x, c.xdtype, static_cast<int8_t *>(workspace), own_sx, c.M, c.K, true);
             if (e != cudaSuccess) return e;
             x = static_cast<const int8_t *>(workspace);
         }
-        return launch_i8_mv(ds, st, x, sx, c.w, c.sw, c.y, c.ydtype, c.M, c.N, c.K, pass);
+        return launch_i8_mv(ds, st, x, sx, c.w, c.sw, c.y, c.ydtype, c.M, c.N, c.K, by);
     }
     uint16_t *h = static_cast<uint16_t *>(workspace);
     if (c.xdtype == MX_I8) {

@@ -711,26 +711,6 @@ __global__ void __launch_bounds__(COPY_THREADS, 4) kv_copy_kernel(const __grid_c
 
 // One cluster: a single CTA where it can take every entry in a few tasks per
 // warp, else the portable most.
-template <typename Args>
-static cudaError_t run_cluster(cudaStream_t st, void (*kernel)(const Args), int ctas, size_t smem, const Args &a)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(POOL_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
-}
-
 static int pool_ctas(long long S, long long pages, long long P)
 {
     return S * ((pages + 32 * RUN - 1) / (32 * RUN)) <= 2 * POOL_WARPS && P <= 64 * 1024 ? 1 : POOL_CLUSTER;
@@ -748,7 +728,8 @@ cudaError_t launch_kv_remap(const DeviceState &ds, cudaStream_t st, const RemapC
     static unsigned char done[64];
     const cudaError_t e = allow_smem(ds, kv_remap_kernel, (int)remap_smem(POOL_MAX_SLOTS, POOL_MAX_SLOTS), done);
     if (e != cudaSuccess) return e;
-    return run_cluster(st, kv_remap_kernel, pool_ctas(S, pages, c.pool.num_pages), smem, a);
+    const int ctas = pool_ctas(S, pages, c.pool.num_pages);
+    return launch_cluster_k(kv_remap_kernel, ctas, dim3(ctas), dim3(POOL_THREADS), smem, st, a);
 }
 
 cudaError_t launch_kv_compact(const DeviceState &ds, cudaStream_t st, const mx_page_pool &pool, int page_size,
@@ -765,7 +746,8 @@ cudaError_t launch_kv_compact(const DeviceState &ds, cudaStream_t st, const mx_p
     a.kv_len = kv_len;
     a.copies = copies;
     a.err = ds.err;
-    return run_cluster(st, kv_compact_kernel, pool_ctas(S, pages, pool.num_pages), 0, a);
+    const int ctas = pool_ctas(S, pages, pool.num_pages);
+    return launch_cluster_k(kv_compact_kernel, ctas, dim3(ctas), dim3(POOL_THREADS), 0, st, a);
 }
 
 // Widest unit that every address of a part is a multiple of.

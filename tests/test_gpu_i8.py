@@ -85,7 +85,9 @@ def test_quantize_edges():
 @pytest.mark.parametrize("M,N,K", [(1, 1, 16), (1, 17, 32), (2, 40, 48), (8, 100, 80), (9, 33, 1040), (16, 250, 8192),
                                    (1, 5000, 64), (3, 2500, 272), (7, 3001, 4096), (1, 10240, 8192), (4, 64, 25600),
                                    (5, 19, 131056), (8, 640, 28672), (3, 330, 40000), (12, 2440, 16384), (17, 5001, 2064),
-                                   (24, 999, 8192), (24, 70, 1008), (23, 20, 70000)])
+                                   (24, 999, 8192), (24, 70, 1008), (23, 20, 70000),
+                                   (8, 5003, 28672), (13, 200, 28672), (16, 2500, 28672), (6, 33, 40016), (7, 1300, 40016),
+                                   (4, 17, 100016), (14, 3000, 14336)])
 def test_few_tokens(M, N, K, ydt):
     torch = need_gpu()
     from gemm_decode_register_gb300 import ops
