@@ -31,7 +31,6 @@ namespace mx {
 
 // ------------------------------------------------------------ quantisation
 
-constexpr int QI8_THREADS = 256;
 constexpr int QI8_KEEP = 4;  // 8-element groups per thread kept in registers
 
 // Eight elements as fp32.
@@ -77,11 +76,11 @@ __device__ __forceinline__ void store8(uint16_t *p, const int (&c)[8])
 // an infinity in the row: s = NaN, q = 0.  early: whether dependents may start
 // at once; not when the codes may be the next call's weights, which its kernel
 // reads before it waits.
-template <typename In, typename Out>
-__global__ void __launch_bounds__(QI8_THREADS) i8_quantize_kernel(const In *__restrict__ x, Out *__restrict__ q,
-                                                                  float *__restrict__ scales, int K, bool early)
+template <typename In, typename Out, int THREADS>
+__global__ void __launch_bounds__(THREADS) i8_quantize_kernel(const In *__restrict__ x, Out *__restrict__ q,
+                                                              float *__restrict__ scales, int K, bool early)
 {
-    __shared__ float wmax[QI8_THREADS / 32];
+    __shared__ float wmax[THREADS / 32];
     if (early) pdl_trigger();
     pdl_wait();
     const size_t row = blockIdx.x;
@@ -93,7 +92,7 @@ __global__ void __launch_bounds__(QI8_THREADS) i8_quantize_kernel(const In *__re
     bool odd = false;  // a NaN (an infinity shows in the maximum)
 #pragma unroll
     for (int u = 0; u < QI8_KEEP; ++u) {
-        const int i = u * QI8_THREADS + (int)threadIdx.x;
+        const int i = u * THREADS + (int)threadIdx.x;
         if (i >= groups) break;
         load8(xr + 8 * i, keep[u]);
 #pragma unroll
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(QI8_THREADS) i8_quantize_kernel(const In *__re
             odd |= keep[u][j] != keep[u][j];
         }
     }
-    for (int i = QI8_KEEP * QI8_THREADS + (int)threadIdx.x; i < groups; i += QI8_THREADS) {
+    for (int i = QI8_KEEP * THREADS + (int)threadIdx.x; i < groups; i += THREADS) {
         float v[8];
         load8(xr + 8 * i, v);
 #pragma unroll
@@ -117,21 +116,21 @@ __global__ void __launch_bounds__(QI8_THREADS) i8_quantize_kernel(const In *__re
     __syncthreads();
     b = 0u;
 #pragma unroll
-    for (int w = 0; w < QI8_THREADS / 32; ++w) b = max(b, __float_as_uint(wmax[w]));
+    for (int w = 0; w < THREADS / 32; ++w) b = max(b, __float_as_uint(wmax[w]));
     const bool bad = b >= 0x7F800000u;
     const float s = bad ? NAN : __fdiv_rn(__uint_as_float(b), 127.0f);
     if (threadIdx.x == 0) scales[row] = s;
     const bool any = s > 0.0f;
 #pragma unroll
     for (int u = 0; u < QI8_KEEP; ++u) {
-        const int i = u * QI8_THREADS + (int)threadIdx.x;
+        const int i = u * THREADS + (int)threadIdx.x;
         if (i >= groups) break;
         int c[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) c[j] = any ? code_of(keep[u][j], s) : 0;
         store8(qr + 8 * i, c);
     }
-    for (int i = QI8_KEEP * QI8_THREADS + (int)threadIdx.x; i < groups; i += QI8_THREADS) {
+    for (int i = QI8_KEEP * THREADS + (int)threadIdx.x; i < groups; i += THREADS) {
         float v[8];
         int c[8];
         load8(xr + 8 * i, v);
@@ -374,18 +373,30 @@ static cudaError_t launch_i8_mv(const DeviceState &ds, cudaStream_t st, const in
     return cudaSuccess;
 }
 
-template <typename In, typename Out>
-static cudaError_t run_quantize(cudaStream_t st, const void *x, void *q, float *scales, int M, int K, bool early)
+template <typename In, typename Out, int THREADS>
+static cudaError_t run_quantize_with(cudaStream_t st, const void *x, void *q, float *scales, int M, int K, bool early)
 {
-    return launch_k(i8_quantize_kernel<In, Out>, dim3(M), dim3(QI8_THREADS), 0, st, static_cast<const In *>(x),
+    return launch_k(i8_quantize_kernel<In, Out, THREADS>, dim3(M), dim3(THREADS), 0, st, static_cast<const In *>(x),
                     static_cast<Out *>(q), scales, K, early);
 }
 
-cudaError_t launch_i8_quantize(const DeviceState &, cudaStream_t st, const void *x, int dtype, int8_t *q, float *scales,
+// More threads where a row's latency is what counts (no more rows than SMs) or
+// fewer would read the row twice: one of 8192 values takes 3.3 us by 1024 (by 256 the product
+// after it came 2 to 3 us later), one of 28672 5.4 (16).
+template <typename In, typename Out>
+static cudaError_t run_quantize(const DeviceState &ds, cudaStream_t st, const void *x, void *q, float *scales, int M, int K,
+                                bool early)
+{
+    return (M <= ds.num_sms && K > 2048) || K > QI8_KEEP * 256 * 8
+               ? run_quantize_with<In, Out, 1024>(st, x, q, scales, M, K, early)
+               : run_quantize_with<In, Out, 256>(st, x, q, scales, M, K, early);
+}
+
+cudaError_t launch_i8_quantize(const DeviceState &ds, cudaStream_t st, const void *x, int dtype, int8_t *q, float *scales,
                                int M, int K, bool early)
 {
-    return dtype == MX_F32 ? run_quantize<float, int8_t>(st, x, q, scales, M, K, early)
-                           : run_quantize<uint16_t, int8_t>(st, x, q, scales, M, K, early);
+    return dtype == MX_F32 ? run_quantize<float, int8_t>(ds, st, x, q, scales, M, K, early)
+                           : run_quantize<uint16_t, int8_t>(ds, st, x, q, scales, M, K, early);
 }
 
 size_t i8_mm_workspace_bytes(int M, int K)
@@ -440,8 +451,8 @@ cudaError_t launch_i8_mm(const DeviceState &ds, cudaStream_t st, const I8Call &c
         e = launch_k(i8_widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, st,
                      static_cast<const int8_t *>(c.x), h, n16);
     } else {
-        e = c.xdtype == MX_F32 ? run_quantize<float, uint16_t>(st, c.x, h, own_sx, c.M, c.K, true)
-                               : run_quantize<uint16_t, uint16_t>(st, c.x, h, own_sx, c.M, c.K, true);
+        e = c.xdtype == MX_F32 ? run_quantize<float, uint16_t>(ds, st, c.x, h, own_sx, c.M, c.K, true)
+                               : run_quantize<uint16_t, uint16_t>(ds, st, c.x, h, own_sx, c.M, c.K, true);
     }
     if (e != cudaSuccess) return e;
     return launch_qmm_i8(ds, st, reinterpret_cast<const uint8_t *>(c.w), c.sw, h, sx, c.y, c.ydtype == MX_F32, c.M, c.N, c.K);
