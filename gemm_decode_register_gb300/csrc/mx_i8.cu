@@ -51,23 +51,54 @@ __device__ __forceinline__ void load8(const float *p, float (&v)[8])
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-__device__ __forceinline__ int code_of(float x, float s) { return __float2int_rn(fminf(fmaxf(__fdiv_rn(x, s), -127.0f), 127.0f)); }
+// Adding it rounds a number of less than 2^22 to the nearest even integer, which the
+// sum's low bits then are: conversions run at an eighth of this rate.
+constexpr float INT_AT = 12582912.0f;  // 1.5 * 2^23
 
-__device__ __forceinline__ void store8(int8_t *p, const int (&c)[8])
+// x / s to the nearest integers, r = 1 / s.  x r is within 3 * 2^-24 of the
+// quotient (relative; 127 * that is 2.3e-5), so it has the same nearest integer unless
+// a tie is that near; then, and where r or the product is no number, the quotients
+// themselves decide.
+__device__ __forceinline__ void codes_of(const float (&x)[8], float s, float r, float (&c)[8])
 {
+    bool near = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float t = __fmul_rn(x[j], r);
+        c[j] = __fsub_rn(__fadd_rn(t, INT_AT), INT_AT);
+        near |= !(fabsf(t - c[j]) < 0.4999f);
+    }
+    if (near)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = rintf(fminf(fmaxf(__fdiv_rn(x[j], s), -127.0f), 127.0f));
+}
+
+// The larger of m and the magnitudes, as bits: these are in the order of the
+// values, infinities above them and a NaN above those.
+__device__ __forceinline__ uint32_t most_of(uint32_t m, const float (&x)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+    return m;
+}
+
+__device__ __forceinline__ void store8(int8_t *p, const float (&c)[8])
+{
+    uint32_t b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = __float_as_uint(__fadd_rn(c[j], INT_AT));
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        w[i] = (uint32_t)(c[4 * i] & 255) | (uint32_t)(c[4 * i + 1] & 255) << 8 | (uint32_t)(c[4 * i + 2] & 255) << 16 |
-               (uint32_t)c[4 * i + 3] << 24;
+        w[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040), __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
     *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 // f16 integers (bits), exact.
-__device__ __forceinline__ void store8(uint16_t *p, const int (&c)[8])
+__device__ __forceinline__ void store8(uint16_t *p, const float (&c)[8])
 {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = f32x2_to_f16x2((float)c[2 * i], (float)c[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) w[i] = f32x2_to_f16x2(c[2 * i], c[2 * i + 1]);
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -80,7 +111,7 @@ template <typename In, typename Out, int THREADS>
 __global__ void __launch_bounds__(THREADS) i8_quantize_kernel(const In *__restrict__ x, Out *__restrict__ q,
                                                               float *__restrict__ scales, int K, bool early)
 {
-    __shared__ float wmax[THREADS / 32];
+    __shared__ uint32_t wmax[THREADS / 32];
     if (early) pdl_trigger();
     pdl_wait();
     const size_t row = blockIdx.x;
@@ -88,55 +119,43 @@ __global__ void __launch_bounds__(THREADS) i8_quantize_kernel(const In *__restri
     Out *qr = q + row * K;
     const int groups = K / 8;
     float keep[QI8_KEEP][8];
-    float m = 0.0f;
-    bool odd = false;  // a NaN (an infinity shows in the maximum)
+    uint32_t m = 0u;
 #pragma unroll
     for (int u = 0; u < QI8_KEEP; ++u) {
         const int i = u * THREADS + (int)threadIdx.x;
         if (i >= groups) break;
         load8(xr + 8 * i, keep[u]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m = fmaxf(m, fabsf(keep[u][j]));
-            odd |= keep[u][j] != keep[u][j];
-        }
+        m = most_of(m, keep[u]);
     }
     for (int i = QI8_KEEP * THREADS + (int)threadIdx.x; i < groups; i += THREADS) {
         float v[8];
         load8(xr + 8 * i, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m = fmaxf(m, fabsf(v[j]));
-            odd |= v[j] != v[j];
-        }
+        m = most_of(m, v);
     }
-    // (non-negative floats are in the order of their bits; a NaN becomes the largest)
-    uint32_t b = __reduce_max_sync(0xFFFFFFFFu, odd ? 0x7FC00000u : __float_as_uint(m));
-    if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = __uint_as_float(b);
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
     __syncthreads();
-    b = 0u;
+    m = 0u;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) b = max(b, __float_as_uint(wmax[w]));
-    const bool bad = b >= 0x7F800000u;
-    const float s = bad ? NAN : __fdiv_rn(__uint_as_float(b), 127.0f);
+    for (int w = 0; w < THREADS / 32; ++w) m = max(m, wmax[w]);
+    const float s = m >= 0x7F800000u ? NAN : __fdiv_rn(__uint_as_float(m), 127.0f);
     if (threadIdx.x == 0) scales[row] = s;
-    const bool any = s > 0.0f;
+    const float r = __frcp_rn(s);
+    const auto write = [&](int i, const float (&v)[8]) {
+        float c[8] = {};
+        if (s > 0.0f) codes_of(v, s, r, c);
+        store8(qr + 8 * i, c);
+    };
 #pragma unroll
     for (int u = 0; u < QI8_KEEP; ++u) {
         const int i = u * THREADS + (int)threadIdx.x;
         if (i >= groups) break;
-        int c[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = any ? code_of(keep[u][j], s) : 0;
-        store8(qr + 8 * i, c);
+        write(i, keep[u]);
     }
     for (int i = QI8_KEEP * THREADS + (int)threadIdx.x; i < groups; i += THREADS) {
         float v[8];
-        int c[8];
         load8(xr + 8 * i, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = any ? code_of(v[j], s) : 0;
-        store8(qr + 8 * i, c);
+        write(i, v);
     }
     if (!early) __threadfence();
 }
@@ -381,8 +400,8 @@ static cudaError_t run_quantize_with(cudaStream_t st, const void *x, void *q, fl
 }
 
 // More threads where a row's latency is what counts (no more rows than SMs) or
-// fewer would read the row twice: one of 8192 values takes 3.3 us by 1024 (by 256 the product
-// after it came 2 to 3 us later), one of 28672 5.4 (16).
+// fewer would read the row twice: one of 8192 values takes 3.0 us by 1024 (by 256 the product
+// after it came 2 to 3 us later), one of 28672 4.6 (about 10).
 template <typename In, typename Out>
 static cudaError_t run_quantize(const DeviceState &ds, cudaStream_t st, const void *x, void *q, float *scales, int M, int K,
                                 bool early)

@@ -53,6 +53,26 @@ def test_quantize(dtype, M, K):
     assert np.array_equal(s.cpu().numpy(), ws) and np.array_equal(q.cpu().numpy(), wq)
 
 
+def test_quantize_next_to_halves():
+    """Values a place or two from half-way between codes."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    rng = np.random.default_rng(3)
+    x = np.zeros((40, 4096), np.float32)
+    for row in x:
+        top = np.float32(np.exp(rng.uniform(-80, 80)))
+        s = np.float32(top / np.float32(127))
+        row[:] = (rng.integers(-127, 127, 4096) + 0.5).astype(np.float32) * s
+        for _ in range(2):
+            up = rng.integers(-1, 2, 4096)
+            row[:] = np.where(up > 0, np.nextafter(row, np.float32(np.inf)), np.where(up < 0, np.nextafter(row, np.float32(-np.inf)), row))
+        row[7] = top
+    q, s = ops.i8_quantize(torch.from_numpy(x).cuda())
+    wq, ws = _codes(x)
+    assert np.array_equal(s.cpu().numpy(), ws) and np.array_equal(q.cpu().numpy(), wq)
+
+
 def test_quantize_edges():
     """Zeros, values whose scale is subnormal or vanishes, the largest, halves (to even), NaN and infinities."""
     torch = need_gpu()
