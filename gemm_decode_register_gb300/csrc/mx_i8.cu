@@ -2,7 +2,8 @@
 // output channel, sm_103a:
 //   y[m][n] = (sum_k xq[m][k] wq[n][k]) * sx[m] * sw[n].
 //
-// Quantisation (bound: HBM): a block per token, its row held in registers
+// Quantisation (bound: latency for few tokens, then instructions: 4096 rows of 8192
+// bf16 take 33 us, where HBM would allow 15): a block per token, its row held in registers
 // between the maximum and the rounding.
 //
 // Few tokens (bound: HBM, the weights once): mma.sync m16n8k32 on 8-bit
@@ -15,7 +16,8 @@
 // weights take 154-158 us for up to eight tokens, the measured copy's rate; 84 MB 16,
 // of 12.5, since 640 row tiles make five rounds of 152 SMs.  (Equal stretches
 // of K for each CTA, with the shared tiles' sums through global memory, took longer: 24
-// against 20 us, 167 against 156.)
+// against 20 us, 167 against 156; so do pairs of CTAs where single ones have the room, 25
+// against 19; quantising the tokens here too saves a launch, and 0.5 to 2 us are lost.)
 //
 // Many tokens: mx_qmm.cu's tensor-core GEMM.  sm_103a has no 8-bit integer
 // form of tcgen05.mma, and integers up to 2048 are exact in f16: tokens are
@@ -52,7 +54,7 @@ __device__ __forceinline__ void load8(const float *p, float (&v)[8])
 }
 
 // Adding it rounds a number of less than 2^22 to the nearest even integer, which the
-// sum's low bits then are: conversions run at an eighth of this rate.
+// sum's low bits then are (4096 rows of 16384 took 120 us by conversions, 105 by this).
 constexpr float INT_AT = 12582912.0f;  // 1.5 * 2^23
 
 // x / s to the nearest integers, r = 1 / s.  x r is within 3 * 2^-24 of the
@@ -220,7 +222,7 @@ __device__ __forceinline__ void mma_s8_16832(int (&d)[4], uint32_t a0, uint32_t 
 // PAIR: where a CTA's shared memory has no room for the tokens, a cluster of two shares
 // each row tile, either half of K its own; the halves' sums meet through each
 // other's shared memory, and a pass more over the weights is saved (eight tokens
-// through 8192 x 28672 64 us, 107 in two passes; sixteen 113, 166 in three).
+// through 8192 x 28672 48 us after their quantisation, 93 in two passes).
 template <int NB, typename Y, bool PAIR>
 __global__ void __launch_bounds__(MV_THREADS, 1) i8_mv_kernel(const __grid_constant__ I8MvArgs a)
 {
