@@ -662,8 +662,11 @@ __device__ __noinline__ void piece_exact(const E *x, const uint32_t *mask, int t
     __syncthreads();
     if (threadIdx.x == 0) *n_found = 0;
     __syncthreads();
+    // (k at most, unless another stream writes the logits meanwhile)
     each([&](unsigned long long v) {
-        if (v >= lo) found[atomicAdd(n_found, 1)] = v;
+        if (v < lo) return;
+        const int at = atomicAdd(n_found, 1);
+        if (at < BEAM_FOUND) found[at] = v;
     });
 }
 
@@ -915,7 +918,7 @@ __global__ void __launch_bounds__(BEAM_THREADS, BEAM_BLOCKS) beam_kernel(const _
                                      here.token0 + first * BEAM_STEP * VEC, min(a.V, here.token0 + (step + 1) * BEAM_STEP * VEC),
                                      a.V, a.k, (unsigned long long)ordered(bound + 0.0f) << 32, found, &n_found, scratch);
             __syncthreads();
-            const int n = n_found;
+            const int n = min(n_found, BEAM_FOUND);
             unsigned long long *best = a.best + list * a.kpad;
             for (int i = tid; i < n; i += BEAM_THREADS) {
                 const unsigned long long c = found[i];
