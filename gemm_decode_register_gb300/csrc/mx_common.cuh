@@ -230,8 +230,8 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
 // activations or writes outputs.  Weights (codes, block scales), MoE
 // expert ids and a paged batch's lengths and block table may be read before the
 // wait: the ABI requires them to be complete when a call is issued, and the
-// kernels of this library that write them (the page pool's, and the public
-// 8-bit quantisation) do not let their dependents start early.
+// kernels of this library that write them (the page pool's, and those of
+// mx_quantize and mx_i8_quantize) do not let their dependents start early.
 // Both are no-ops when the launch carries no programmatic dependency.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

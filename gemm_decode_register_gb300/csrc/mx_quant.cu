@@ -213,6 +213,8 @@ __device__ __forceinline__ uint32_t quant_block(const uint32_t (&w)[W], float g,
 
 // Each thread takes P consecutive blocks per step (P = 2 for NVFP4, so that
 // every thread, as for the MX formats, reads 64 contiguous bytes per step).
+// Dependents start when it has ended, not before: its codes may be the next
+// call's weights, which that kernel reads before it waits.
 template <int FMT>
 __global__ void quantize_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ codes,
                                 uint8_t *__restrict__ scales, long long nblocks, const unsigned *gbits)
@@ -221,7 +223,6 @@ __global__ void quantize_kernel(const uint16_t *__restrict__ x, uint8_t *__restr
     constexpr int W = B / 2;                                 // bf16 pairs per block
     constexpr int NC = FMT == FMT_MXFP8 ? B / 4 : B / 8;     // 32-bit code words per block
     constexpr int P = FMT == FMT_NVFP4 ? 2 : 1;              // blocks per thread and step
-    pdl_trigger();
     pdl_wait();
     float g = 1.0f, d6 = 6.0f;
     if constexpr (FMT == FMT_NVFP4) {
@@ -274,6 +275,7 @@ __global__ void quantize_kernel(const uint16_t *__restrict__ x, uint8_t *__restr
             *reinterpret_cast<uint2 *>(codes + b0 * 8) = make_uint2(c[0][0], c[0][1]);
         }
     }
+    __threadfence();
 }
 
 cudaError_t launch_quantize(const DeviceState &ds, cudaStream_t st, int fmt, const uint16_t *x, uint8_t *codes,

@@ -263,7 +263,8 @@ int mx_moe_ffn_prefill(int fmt, const void *gate_up_codes, const void *gate_up_s
  *     maximum goes through a word of the calling stream's workspace slot.
  *   A block holding a NaN or an infinity gets a NaN scale (0xFF / 0x7F) and
  *   zero codes; a zero result is stored as +0.
- * K a multiple of the block (else MX_EINVAL); x and codes 16-byte aligned. */
+ * K a multiple of the block (else MX_EINVAL); x and codes 16-byte aligned.
+ * (Weights may be quantised by it too, and used by the next call.) */
 int mx_quantize(int fmt, const void *x, void *codes, void *scales, int M, int K);
 
 /* ---- attention: rotary positions, paged key/value cache, attention over it
