@@ -196,6 +196,11 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
         lens[p] = len;
         children[p] = 0;
     }
+    // References of number i of the pages that are handed out: zero, or the
+    // stack is not in order.  CTA 0 fetches one for each thread before it is known
+    // how many there will be.
+    auto refs_of = [&](int page) { return (unsigned)page < (unsigned)P ? __ldcg(c.pool.refs + page) : 1; };
+    const int next_page = rank == 0 && count <= P && tid < count ? __ldcg(c.pool.free_pages + (count - 1 - tid)) : -1;
     for (int s = tid; s < c.S_out; s += POOL_THREADS) {
         Slot n;
         n.parent = __ldcg(c.parent + s);
@@ -275,6 +280,8 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
         }
         have_own = true;
     };
+
+    const int next_refs = refs_of(next_page);
 
     // ---- tally.  The partial page of each slot: CTA 0, a thread for each
     if (rank == 0)
@@ -357,6 +364,12 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
                 sh.handed = (int)n;
                 sh.copies = (int)(total / COPY);
             }
+            if (count <= P) {
+                const int n = (int)min(total & (COPY - 1), (unsigned long long)max(count, 0));
+                if (tid < n && next_refs != 0) bad |= DEVERR_BAD_PAGE;
+                for (int i = tid + POOL_THREADS; i < n; i += POOL_THREADS)
+                    if (refs_of(__ldcg(c.pool.free_pages + (count - 1 - i))) != 0) bad |= DEVERR_BAD_PAGE;
+            }
         }
         old_entries([&](int page, int d, bool) {
             if (d >= 0) return;
@@ -410,8 +423,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
             if (j >= end) continue;
             to[j] = page[i];
             if (j < start) continue;
-            if ((unsigned)page[i] < (unsigned)P) c.pool.refs[page[i]] = 1;
-            else set_device_error(a.err, DEVERR_BAD_PAGE);
+            c.pool.refs[page[i]] = 1;
             if (j == start && copy != 0)
                 reinterpret_cast<int4 *>(c.copies)[copy] = make_int4(__ldcg(from + j), page[i], n.kept % ps, 0);
         }

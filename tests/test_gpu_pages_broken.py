@@ -1,0 +1,37 @@
+"""Pools that are not in order: a step that would hand out a page that is in use, or none of the pool's, changes nothing."""
+import pytest
+
+from gpu_util import need_gpu
+from test_gpu_pages import Session, _clean, _i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("P,S,width,ps,deep", [(40, 6, 12, 4, 0), (40, 6, 12, 4, 5), (9000, 30, 260, 4, 2100), (70000, 40, 900, 2, 1023)])
+@pytest.mark.parametrize("bad", [-1, "P", 2 ** 31 - 1, -2 ** 31, "used"])
+def test_free_pages_that_cannot_be_handed_out(P, S, width, ps, deep, bad):
+    """Place `deep` of the pages that the step is to be handed holds a number outside the pool or a page that has references."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    t = Session(torch, P, S, width, ps)
+    add = [min(width * ps // 4, 9 + 7 * s) for s in range(S)]
+    assert t.step([-1] * S, None, add)
+    more = [width * ps // 3 if deep > 50 else ps] * S
+    need = sum(-(-(n + m) // ps) - -(-n // ps) for n, m in zip(t.lens, more))
+    count = int(t.pool.count)
+    assert deep < need <= count
+    at = count - 1 - deep
+    good = int(t.pool.free_pages[at])
+    t.pool.free_pages[at] = {"P": P, "used": t.rows[3][0]}.get(bad, bad)
+    old = [x.clone() for x in (t.tables[0], t.tables[1], t.pool.state)]
+    ident = _i32(torch, range(S))
+    n, copies = ops.kv_remap(t.pool, ps, t.tables[0], t.kv_len, ident, t.tables[1], _i32(torch, more))
+    assert ops.device_error() == 0x4
+    assert (n == -1).all() and copies[0].tolist() == [0, 0, 0, 0]
+    assert all(torch.equal(a, b) for a, b in zip(old, (t.tables[0], t.tables[1], t.pool.state))) and _clean(t.pool)
+    # a step that does not come to that place, and the whole one after it is put right
+    n, _ = ops.kv_remap(t.pool, ps, t.tables[0], t.kv_len, ident, t.tables[1], 0)
+    assert ops.device_error() == 0 and n.tolist() == t.lens
+    t.pool.free_pages[at] = good
+    assert t.step(list(range(S)), None, more)
