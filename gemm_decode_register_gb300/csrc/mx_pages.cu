@@ -544,39 +544,44 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_compact_kernel(const __gri
     if (threadIdx.x == 0) w.part[rank] = (int)total;
     if (fault) atomicOr(w.word, fault);
     cluster_phase();
-    fault = __ldcg(w.word);
-    if (fault) {
+    auto give_up = [&](int why) {
         for (int p = lo + lane; p < hi; p += 32) w.tally[p] = PageTally{0, 0};
         if (rank == 0 && threadIdx.x == 0) {
             reinterpret_cast<int4 *>(a.copies)[0] = make_int4(0, 0, 0, 0);
-            set_device_error(a.err, fault);
+            set_device_error(a.err, why);
         }
         cluster_phase();
         if (rank == 0 && threadIdx.x == 0) w.word[0] = 0;
-        return;
-    }
+    };
+    fault = __ldcg(w.word);
+    if (fault) return give_up(fault);
     int U;
     totals(0, U);
     cluster_phase();  // (the counts' places are used again)
 
     // ---- free places below U, pages to move from U on
-    auto kind = [&](int p) {  // 1: a free place, 2: a page to move
-        const int r = __ldcg(a.pool.refs + p);
+    auto kind = [&](int p) {  // 1: a free place, 2: a page to move; -1: it has more entries than references
+        const int r = __ldcg(a.pool.refs + p), users = tally_at(w.tally, p).users;
+        if (users > max(r, 0)) return -1;
         if (p < U) return r == 0 ? 1 : 0;
-        return r > 0 && tally_at(w.tally, p).users == r ? 2 : 0;
+        return r > 0 && users == r ? 2 : 0;
     };
     unsigned holes = 0, movers = 0;
     for (int p0 = lo; p0 < hi; p0 += 32) {
         const int k = p0 + lane < hi ? kind(p0 + lane) : 0;
         holes += __popc(__ballot_sync(0xFFFFFFFFu, k == 1));
         movers += __popc(__ballot_sync(0xFFFFFFFFu, k == 2));
+        if (k < 0) fault = DEVERR_BAD_PAGE;
     }
+    if (fault) atomicOr(w.word, fault);
     const unsigned long long at = __shfl_sync(0xFFFFFFFFu, range_sum(holes | ((unsigned long long)movers << 32), total), 0);
     if (threadIdx.x == 0) {
         w.part[rank] = (int)(uint32_t)total;
         w.part[POOL_CLUSTER + rank] = (int)(total >> 32);
     }
     cluster_phase();
+    fault = __ldcg(w.word);
+    if (fault) return give_up(fault);
     int all_holes, all_movers;
     int hole = totals(0, all_holes) + (int)(uint32_t)at, mover = totals(1, all_movers) + (int)(at >> 32);
     const int n = min(all_holes, all_movers);
@@ -585,7 +590,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_compact_kernel(const __gri
         const unsigned h = __ballot_sync(0xFFFFFFFFu, k == 1), m = __ballot_sync(0xFFFFFFFFu, k == 2);
         const unsigned below = (1u << lane) - 1u;
         const int i = k == 1 ? hole + __popc(h & below) : mover + __popc(m & below);
-        if (k != 0 && i < n) a.copies[4 * (size_t)(1 + i) + (k == 1 ? 1 : 0)] = p0 + lane;
+        if (k > 0 && i < n) a.copies[4 * (size_t)(1 + i) + (k == 1 ? 1 : 0)] = p0 + lane;
         hole += __popc(h);
         mover += __popc(m);
     }

@@ -469,7 +469,8 @@ int mx_kv_remap(const mx_page_pool *pool, int page_size, const int32_t *table_in
  * Tables and references follow; copies int32 [1 + num_pages/2][4] receives the moves
  * as above (whole pages), which must run before the cache is used.
  * free_pages becomes all pages without references, the lowest taken
- * first.  Faults (MX_DEVERR_BAD_PAGE) as for mx_kv_remap: nothing changes, n is 0. */
+ * first.  Faults (MX_DEVERR_BAD_PAGE) as for mx_kv_remap, a page that has more
+ * entries than references among them: nothing changes, n is 0. */
 int mx_kv_compact(const mx_page_pool *pool, int page_size, int32_t *table, int stride, int pages,
                   const int32_t *kv_len, int S, int32_t *copies);
 

@@ -1,4 +1,7 @@
-"""Pools that are not in order: a step that would hand out a page that is in use, or none of the pool's, changes nothing."""
+"""Pools that are not in order: a step that would hand out a page that is in use, or none of the pool's, and a compaction that
+would cover one, change nothing."""
+import random
+
 import pytest
 
 from gpu_util import need_gpu
@@ -35,3 +38,25 @@ def test_free_pages_that_cannot_be_handed_out(P, S, width, ps, deep, bad):
     assert ops.device_error() == 0 and n.tolist() == t.lens
     t.pool.free_pages[at] = good
     assert t.step(list(range(S)), None, more)
+
+
+@pytest.mark.parametrize("P,S,width,ps", [(60, 6, 12, 4), (70000, 90, 300, 2)])
+def test_pages_of_fewer_references_than_entries_are_not_covered(P, S, width, ps):
+    """A page in use whose references fell to nothing, or are fewer than its entries, is no free place."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    rng = random.Random(P)
+    t = Session(torch, P, S, width, ps)
+    assert t.step([-1] * S, None, [rng.randint(1, width * ps // 2) for _ in range(S)])
+    assert t.step([s // 2 * 2 if s % 3 else -1 for s in range(S)], None, 0)  # (free places, shared pages)
+    row = max(t.rows, key=len)
+    for page, refs in ((row[0], 0), (row[0], t.ref.refs[row[0]] - 1), (row[-1], 0)):
+        was = int(t.pool.refs[page])
+        t.pool.refs[page] = refs
+        old = [x.clone() for x in (t.tables[0], t.pool.state)]
+        copies = ops.kv_compact(t.pool, ps, t.tables[0], t.kv_len)
+        assert ops.device_error() == 0x4 and copies[0].tolist() == [0, 0, 0, 0]
+        assert torch.equal(old[0], t.tables[0]) and torch.equal(old[1], t.pool.state) and _clean(t.pool)
+        t.pool.refs[page] = was
+    t.compact()
