@@ -15,7 +15,7 @@
 //
 // These kernels write lengths and tables, which other kernels of the library
 // read before they wait for their predecessor; so they do not let their
-// dependents start early.
+// dependents start early, and fence what they wrote before they end.
 //
 // Copies (bound: HBM): an item is some heads of one page's half in one layer;
 // blocks walk the items, 16-byte vectors, eight in flight per thread.
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
                 set_device_error(a.err, fault);
             }
         }
-        cluster_sync_all();  // (no CTA leaves while another may report to it)
+        cluster_phase();  // (no CTA leaves while another may report to it; lengths are read early)
         return;
     }
     const uint32_t plan0 = map_to_cta(smem_u32(plan), 0);
