@@ -723,7 +723,9 @@ def kv_remap(pool: PagePool, page_size: int, table: torch.Tensor, kv_len: torch.
     op, os_, on, S_out = _table_of("table_out", table_out)
     size = (S_out,)
     lp = _whole("kv_len", kv_len, i32, (S_in,))
-    pp = _whole("parent", parent if parent.dim() == 1 else parent.reshape(-1), i32, size)
+    if parent.dim() != 1:
+        parent = parent.reshape(-1)  # (a copy where its rows lie apart: kept until the call is made)
+    pp = _whole("parent", parent, i32, size)
     kp = None if keep is None else _whole("keep", keep, i32, size)
     ap, each = (None, add) if isinstance(add, int) else (_whole("add", add, i32, size), 0)
     if kv_len_out is None:
