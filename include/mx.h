@@ -500,9 +500,11 @@ int mx_i8_quantize(const void *x, int dtype, int8_t *q, float *scales, int M, in
  * w int8 [N][K], w_scales fp32 [N], y [M][N] bf16 or fp32 (ydtype).  x [M][K]:
  * int8 (xdtype MX_I8) with x_scales fp32 [M], or bf16 / fp32 (x_scales null),
  * quantised as by mx_i8_quantize on the way.  Few tokens stream the weights,
- * in passes of up to 16; many go to the tensor cores' GEMM.  The streaming passes sum in
- * 32-bit integers, the GEMM in fp32: exact while sums stay below 2^24 in
- * magnitude, rounded to 24 bits above.  The scales are applied in fp32, then y is rounded once.
+ * in passes of up to 16; many go to the tensor cores' GEMM.  The streaming
+ * passes sum in 32-bit integers; the GEMM adds 16 products at a time to an
+ * fp32 sum: exact while it stays below 2^24 in magnitude; where it is larger
+ * each such step may lose its last place.  The sum is rounded to fp32,
+ * multiplied by x_scales, then by w_scales (fp32 each), then y is rounded once.
  * workspace: at least mx_i8_mm_workspace_size(M, K) bytes, 256-byte aligned,
  * overwritten; null (with workspace_bytes 0) where that is at most 16 MiB: the calling stream's
  * slot.  w and w_scales are weights: they are read as soon as the kernels start.
