@@ -3,8 +3,8 @@
 //   y[m][n] = (sum_k xq[m][k] wq[n][k]) * sx[m] * sw[n].
 //
 // Quantisation (bound: latency for few tokens, then instructions: 4096 rows of 8192
-// bf16 take 33 us, where HBM would allow 15): a block per token, its row held in registers
-// between the maximum and the rounding.
+// bf16 take 37 us, where HBM would allow 15; of 28672 100, of 53): a block per token, its row, or
+// as much as fits, held in registers between the maximum and the rounding.
 //
 // Few tokens (bound: HBM, the weights once): mma.sync m16n8k32 on 8-bit
 // integers, 32-bit sums, exact.  A warp's 16 weight rows come straight from
@@ -54,7 +54,8 @@ __device__ __forceinline__ void load8(const float *p, float (&v)[8])
 }
 
 // Adding it rounds a number of less than 2^22 to the nearest even integer, which the
-// sum's low bits then are (4096 rows of 16384 took 120 us by conversions, 105 by this).
+// sum's low bits then are (by 1024 threads each, 4096 rows of 16384 took 120 us by
+// conversions, 105 by this).
 constexpr float INT_AT = 12582912.0f;  // 1.5 * 2^23
 
 // x / s to the nearest integers, r = 1 / s.  x r is within 3 * 2^-24 of the
@@ -401,14 +402,19 @@ static cudaError_t run_quantize_with(cudaStream_t st, const void *x, void *q, fl
                     static_cast<Out *>(q), scales, K, early);
 }
 
-// More threads where a row's latency is what counts (no more rows than SMs) or
-// fewer would read the row twice: one of 8192 values takes 3.0 us by 1024 (by 256 the product
-// after it came 2 to 3 us later), one of 28672 4.6 (about 10).
+// Threads of a row, us by 256 / by 1024, of which an SM holds one block.
+//   No more rows than SMs: what counts is a row's latency.  8 of 1024 values 1.9 /
+// 2.5, of 4096 2.6 / 2.6, of 28672 8.6 / 5.0; 152 of 8192 5.3 / 4.2, of 16384 8.4 / 5.8.
+//   More: blocks that overlap (bf16: 153 of 16384 8.4 / 7.9, 256 9.3 / 9.3, 512 11.7 / 16.0;
+// 4096 of 4096 22 / 63, of 8192 37 / 74, of 16384 61 / 105, of 28672 101 / 155), also where 256
+// threads read twice what registers do not hold; up to rows of 128 KB, of
+// which four on every SM are still in L2 then (4096 of 32768 bf16 107 / 162, fp32 140 / 154, of
+// 49152 fp32 250 / 240, of 98304 535 / 439; 2048 of 65536 bf16 115 / 140, fp32 184 / 159).
 template <typename In, typename Out>
 static cudaError_t run_quantize(const DeviceState &ds, cudaStream_t st, const void *x, void *q, float *scales, int M, int K,
                                 bool early)
 {
-    return (M <= ds.num_sms && K > 2048) || K > QI8_KEEP * 256 * 8
+    return K > 2048 && (M <= ds.num_sms || K * (long long)sizeof(In) > 128 * 1024)
                ? run_quantize_with<In, Out, 1024>(st, x, q, scales, M, K, early)
                : run_quantize_with<In, Out, 256>(st, x, q, scales, M, K, early);
 }
