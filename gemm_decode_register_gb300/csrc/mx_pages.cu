@@ -27,7 +27,10 @@ namespace mx {
 
 constexpr int POOL_THREADS = 1024;
 constexpr int POOL_WARPS = POOL_THREADS / 32;
-constexpr int POOL_CLUSTER = 8;  // CTAs of a cluster, the portable most
+// CTAs of a cluster, the portable most.  (One CTA is no faster however little there
+// is: a step of one sequence 10.4 us by one and 10.1 by eight, of 4 14.9 and 14.5, of 32 of 2000 tokens 19.2 and
+// 15.9; a compaction of 4,000 pages 15 and 15, of 16,000 27 and 17.)
+constexpr int POOL_CLUSTER = 8;
 constexpr int RUN = 4;           // entries per lane of a warp's task: 128 of one table row,
 constexpr int GANG = 8;          // or 16 of each of eight neighbouring rows
 constexpr int NO_ENTRY = -0x7FFFFFFF - 1;
@@ -65,13 +68,6 @@ static PoolWork pool_work(const mx_page_pool &p)
     w.part = w.word + 4;
     w.freed = reinterpret_cast<uint32_t *>(w.part + 2 * POOL_CLUSTER);
     return w;
-}
-
-__device__ __forceinline__ uint32_t cluster_nctarank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
 }
 
 // Everything before it is visible to the whole cluster after it.
@@ -153,8 +149,8 @@ struct RemapShared {
 // (a 32-bit word of every CTA's shared memory)
 __device__ __forceinline__ void all_ctas_or(const void *word, int bits)
 {
-    const uint32_t n = cluster_nctarank(), here = smem_u32(word);
-    for (uint32_t r = 0; r < n; ++r)
+    const uint32_t here = smem_u32(word);
+    for (uint32_t r = 0; r < POOL_CLUSTER; ++r)
         asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(map_to_cta(here, r)), "r"(bits) : "memory");
 }
 
@@ -179,8 +175,8 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
     int *tails = lens + c.S_in + 3 * c.S_out;                   // [S_out] of CTA 0: page a growing slot writes in, or -1
     __shared__ RemapShared sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
-    const int rank = (int)cluster_ctarank(), ctas = (int)cluster_nctarank();
-    const int gw = warp * ctas + rank, nw = POOL_WARPS * ctas;
+    const int rank = (int)cluster_ctarank();
+    const int gw = warp * POOL_CLUSTER + rank, nw = POOL_WARPS * POOL_CLUSTER;
     const int ps = c.page_size, P = c.pool.num_pages;
     if (tid == 0) sh.fault = sh.late = 0;
     pdl_wait();
@@ -481,8 +477,8 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_compact_kernel(const __gri
     __shared__ int smax[32];
     __shared__ unsigned long long scan[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rank = (int)cluster_ctarank(), ctas = (int)cluster_nctarank();
-    const int gw = warp * ctas + rank, nw = POOL_WARPS * ctas;
+    const int rank = (int)cluster_ctarank();
+    const int gw = warp * POOL_CLUSTER + rank, nw = POOL_WARPS * POOL_CLUSTER;
     const int ps = a.page_size, P = a.pool.num_pages;
     // this warp's range of pages
     const int span = ((P + nw - 1) / nw + 31) / 32 * 32;
@@ -523,7 +519,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_compact_kernel(const __gri
     auto totals = [&](int slot, int &all) {
         int before = 0;
         all = 0;
-        for (int r = 0; r < ctas; ++r) {
+        for (int r = 0; r < POOL_CLUSTER; ++r) {
             const int v = __ldcg(w.part + slot * POOL_CLUSTER + r);
             if (r < rank) before += v;
             all += v;
@@ -726,27 +722,17 @@ __global__ void __launch_bounds__(COPY_THREADS, 4) kv_copy_kernel(const __grid_c
 
 // ------------------------------------------------------------ host
 
-// One cluster: a single CTA where it can take every entry in a few tasks per
-// warp, else the portable most.
-static int pool_ctas(long long S, long long pages, long long P)
-{
-    return S * ((pages + 32 * RUN - 1) / (32 * RUN)) <= 2 * POOL_WARPS && P <= 64 * 1024 ? 1 : POOL_CLUSTER;
-}
-
 cudaError_t launch_kv_remap(const DeviceState &ds, cudaStream_t st, const RemapCall &c)
 {
     RemapArgs a;
     a.c = c;
     a.w = pool_work(c.pool);
     a.err = ds.err;
-    const int S = c.S_in > c.S_out ? c.S_in : c.S_out;
-    const int pages = c.in_pages > c.out_pages ? c.in_pages : c.out_pages;
     const size_t smem = remap_smem(c.S_in, c.S_out);
     static unsigned char done[64];
     const cudaError_t e = allow_smem(ds, kv_remap_kernel, (int)remap_smem(POOL_MAX_SLOTS, POOL_MAX_SLOTS), done);
     if (e != cudaSuccess) return e;
-    const int ctas = pool_ctas(S, pages, c.pool.num_pages);
-    return launch_cluster_k(kv_remap_kernel, ctas, dim3(ctas), dim3(POOL_THREADS), smem, st, a);
+    return launch_cluster_k(kv_remap_kernel, POOL_CLUSTER, dim3(POOL_CLUSTER), dim3(POOL_THREADS), smem, st, a);
 }
 
 cudaError_t launch_kv_compact(const DeviceState &ds, cudaStream_t st, const mx_page_pool &pool, int page_size,
@@ -763,8 +749,7 @@ cudaError_t launch_kv_compact(const DeviceState &ds, cudaStream_t st, const mx_p
     a.kv_len = kv_len;
     a.copies = copies;
     a.err = ds.err;
-    const int ctas = pool_ctas(S, pages, pool.num_pages);
-    return launch_cluster_k(kv_compact_kernel, ctas, dim3(ctas), dim3(POOL_THREADS), 0, st, a);
+    return launch_cluster_k(kv_compact_kernel, POOL_CLUSTER, dim3(POOL_CLUSTER), dim3(POOL_THREADS), 0, st, a);
 }
 
 // Widest unit that every address of a part is a multiple of.
