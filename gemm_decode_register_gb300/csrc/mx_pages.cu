@@ -635,17 +635,18 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_compact_kernel(const __gri
 constexpr int COPY_THREADS = 256;
 
 // What is copied of a page in one half of the cache: rows (head, token) of
-// `row` bytes.  Data moves in 16-byte units, scales in `unit`s.
+// `row` bytes.  Data moves in 16-byte units (the cache's base and strides are
+// multiples of 16 bytes, a row is), scales in `scale_unit`s.
 struct CopyPart {
     long long page_stride, head_stride, token_stride;  // bytes
     int row;                                           // bytes
-    int unit;                                          // 16, 8, 4, 2 or 1
 };
 
 template <int LAYERS>
 struct CopyArgs {
     uint8_t *data[LAYERS][2], *scales[LAYERS][2];
     CopyPart d, s;  // s.row = 0: no scales
+    int scale_unit;  // bytes: 16, 8, 4, 2 or 1
     const int4 *copies;
     int max_copies, layers, num_pages, page_size, heads, group;  // group: heads of an item
     int *err;
@@ -676,9 +677,9 @@ __device__ __forceinline__ void copy_rows(const uint8_t *src, uint8_t *dst, cons
     }
 }
 
-__device__ __forceinline__ void copy_scales(const uint8_t *s, uint8_t *d, const CopyPart &p, int heads, int tokens)
+__device__ __forceinline__ void copy_scales(const uint8_t *s, uint8_t *d, const CopyPart &p, int unit, int heads, int tokens)
 {
-    switch (p.unit) {
+    switch (unit) {
     case 16: copy_rows<uint4, 1>(s, d, p, heads, tokens); break;
     case 8: copy_rows<uint2, 1>(s, d, p, heads, tokens); break;
     case 4: copy_rows<uint32_t, 2>(s, d, p, heads, tokens); break;
@@ -715,7 +716,7 @@ __global__ void __launch_bounds__(COPY_THREADS, 4) kv_copy_kernel(const __grid_c
         }
         if (a.s.row > 0) {
             uint8_t *base = a.scales[layer][half] + head * a.s.head_stride;
-            copy_scales(base + c.x * a.s.page_stride, base + c.y * a.s.page_stride, a.s, heads, tokens);
+            copy_scales(base + c.x * a.s.page_stride, base + c.y * a.s.page_stride, a.s, a.scale_unit, heads, tokens);
         }
     }
 }
@@ -778,12 +779,11 @@ static cudaError_t run_copy(const DeviceState &ds, cudaStream_t st, const mx_pag
     a.d.head_stride = kv->head_stride * e;
     a.d.token_stride = kv->token_stride * e;
     a.d.row = (int)(kv->D * e);
-    a.d.unit = 16;  // (the cache's base and strides are multiples of 16 bytes, a row is)
     a.s.page_stride = kv->scale_page_stride;
     a.s.head_stride = kv->scale_head_stride;
     a.s.token_stride = kv->scale_token_stride;
     a.s.row = mx8 ? kv->D / 32 : 0;
-    a.s.unit = copy_unit(bits | a.s.page_stride | a.s.head_stride | a.s.token_stride | a.s.row);
+    a.scale_unit = copy_unit(bits | a.s.page_stride | a.s.head_stride | a.s.token_stride | a.s.row);
     a.copies = reinterpret_cast<const int4 *>(copies);
     a.max_copies = max_copies;
     a.layers = layers;

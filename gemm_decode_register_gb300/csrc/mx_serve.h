@@ -12,7 +12,7 @@ constexpr int BEAM_MAX_W = 64;       // beams of a batch entry
 constexpr int BEAM_MAX_K = 128;      // candidates of a batch entry
 constexpr int BEAM_MAX_V = 1 << 20;  // vocabulary
 constexpr int BEAM_MAX_B = WS_COUNTERS;
-constexpr int BEAM_MAX_ROWS = 65535;  // B * W (a launch's second grid dimension)
+constexpr int BEAM_MAX_ROWS = 65535;  // B * W (all rows' steps are counted in an int)
 
 struct BeamCall {
     const void *logits;
