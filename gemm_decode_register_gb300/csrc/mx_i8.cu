@@ -2,9 +2,10 @@
 // output channel, sm_103a:
 //   y[m][n] = (sum_k xq[m][k] wq[n][k]) * sx[m] * sw[n].
 //
-// Quantisation (bound: latency for few tokens, then instructions: 4096 rows of 8192
-// bf16 take 37 us, where HBM would allow 15; of 28672 100, of 53): a block per token, its row, or
-// as much as fits, held in registers between the maximum and the rounding.
+// Quantisation (bound: latency; for many tokens a block's loads, barrier and stores
+// take turns: 4096 rows of 8192 bf16 take 37 us, where HBM would allow 15; of 28672 100, of
+// 53): a block per token, its row, or as much as fits, held in registers between
+// the maximum and the rounding.
 //
 // Few tokens (bound: HBM, the weights once): mma.sync m16n8k32 on 8-bit
 // integers, 32-bit sums, exact.  A warp's 16 weight rows come straight from

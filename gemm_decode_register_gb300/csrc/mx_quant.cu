@@ -214,7 +214,8 @@ __device__ __forceinline__ uint32_t quant_block(const uint32_t (&w)[W], float g,
 // Each thread takes P consecutive blocks per step (P = 2 for NVFP4, so that
 // every thread, as for the MX formats, reads 64 contiguous bytes per step).
 // Dependents start when it has ended, not before: its codes may be the next
-// call's weights, which that kernel reads before it waits.
+// call's weights, which that kernel reads before it waits.  (So calls back to back
+// do not overlap: 4096 x 8192 into MXFP4 15.0 us, 13.0 where they did.)
 template <int FMT>
 __global__ void quantize_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ codes,
                                 uint8_t *__restrict__ scales, long long nblocks, const unsigned *gbits)
