@@ -141,6 +141,7 @@ struct Slot {
 // What the CTAs of the cluster tell each other, in each one's shared memory.
 struct RemapShared {
     int fault, late;     // faults of the tally, of the decision (a word of its own: another CTA may be ahead)
+    int gained;          // pages freed, less those handed out
     int handed, copies;  // pages handed out, copies
     int smax[32];
     unsigned long long scan[32];
@@ -157,6 +158,13 @@ __device__ __forceinline__ void all_ctas_or(const void *word, int bits)
 // (the plan, of two words a slot, on an even word)
 static __host__ __device__ size_t remap_plan_at(int S_in, int S_out) { return (4 * (size_t)S_in + 4 * (size_t)S_out + 1) / 2 * 2; }
 static size_t remap_smem(int S_in, int S_out) { return sizeof(int) * (remap_plan_at(S_in, S_out) + 2 * (size_t)S_out); }
+
+__device__ __forceinline__ void all_ctas_add(const void *word, int n)
+{
+    const uint32_t here = smem_u32(word);
+    for (uint32_t r = 0; r < POOL_CLUSTER; ++r)
+        asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(map_to_cta(here, r)), "r"(n) : "memory");
+}
 
 // The first thing a step needs is every sequence's length and every slot's
 // parent: they are read once, into each CTA's shared memory.  A phase is then one
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
     const int rank = (int)cluster_ctarank();
     const int gw = warp * POOL_CLUSTER + rank, nw = POOL_WARPS * POOL_CLUSTER;
     const int ps = c.page_size, P = c.pool.num_pages;
-    if (tid == 0) sh.fault = sh.late = 0;
+    if (tid == 0) sh.fault = sh.late = sh.gained = 0;
     pdl_wait();
     cluster_sync_all();  // (before a CTA reports to the others)
 
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
     // without a user.  Not where a fault is known: lengths may not fit the tables.
     fault = *(volatile int *)&sh.fault;
     if (fault == 0) {
-        int bad = 0;
+        int bad = 0, gained = 0;
         if (rank == 0) {
             constexpr int PER = (POOL_MAX_SLOTS + POOL_THREADS - 1) / POOL_THREADS;
             constexpr unsigned long long COPY = 1ull << 40;  // pages below, copies above
@@ -357,6 +365,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
                 const unsigned long long n = total & (COPY - 1);
                 if (count < 0 || count > P) bad |= DEVERR_BAD_PAGE;
                 else if (n > (unsigned long long)count) bad |= DEVERR_NO_PAGE;
+                gained = -(int)n;
                 sh.handed = (int)n;
                 sh.copies = (int)(total / COPY);
             }
@@ -372,14 +381,21 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
             const PageTally t = tally_at(w.tally, page);
             const int left = __ldcg(c.pool.refs + page) + t.users;
             if (left < 0) bad |= DEVERR_BAD_PAGE;  // fewer references than entries
-            if (left == 0 && t.writer == 0) atomicOr(w.freed + (page >> 5), 1u << (page & 31));
+            if (left == 0 && t.writer == 0) {
+                const uint32_t bit = 1u << (page & 31);
+                gained += (atomicOr(w.freed + (page >> 5), bit) & bit) == 0u;
+            }
         });
         if (bad) all_ctas_or(&sh.late, bad);
+        gained = __reduce_add_sync(0xFFFFFFFFu, gained);
+        if (lane == 0 && gained != 0) all_ctas_add(&sh.gained, gained);
     }
     cluster_phase();
 
     // ---- all or nothing
     fault |= *(volatile int *)&sh.late;
+    // (more free pages than there are: the stack said so of pages in use)
+    if (fault == 0 && count + *(volatile int *)&sh.gained > P) fault = DEVERR_BAD_PAGE;
     if (fault) {
         old_entries([&](int page, int, bool) {
             if ((unsigned)page >= (unsigned)P) return;

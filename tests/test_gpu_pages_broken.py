@@ -60,3 +60,28 @@ def test_pages_of_fewer_references_than_entries_are_not_covered(P, S, width, ps)
         assert torch.equal(old[0], t.tables[0]) and torch.equal(old[1], t.pool.state) and _clean(t.pool)
         t.pool.refs[page] = was
     t.compact()
+
+
+@pytest.mark.parametrize("P,S,width,ps", [(40, 6, 12, 4), (70000, 90, 300, 2)])
+def test_more_free_pages_than_pages(P, S, width, ps):
+    """A count of free pages that leaves no room on the stack for those that a step releases."""
+    torch = need_gpu()
+    from gemm_decode_register_gb300 import ops
+
+    t = Session(torch, P, S, width, ps)
+    assert t.step([-1] * S, None, [1 + (5 * s) % (2 * ps) for s in range(S)])
+    count, used = int(t.pool.count), sum(len(r) for r in t.rows)
+    assert count + used == P and used > S
+    ends = [s if s != 1 else -1 for s in range(S)]  # (sequence 1 ends, the others grow by nothing)
+    released = len(t.rows[1])
+    for free, fits in ((P - released + 1, False), (P, False), (P - released, True)):
+        t.pool.count.fill_(free)
+        before = t.pool.state.clone()
+        old = [x.clone() for x in (t.tables[0], t.tables[1])]
+        n, copies = ops.kv_remap(t.pool, ps, t.tables[0], t.kv_len, _i32(torch, ends), t.tables[1], 0)
+        if fits:
+            assert ops.device_error() == 0 and int(t.pool.count) == P
+        else:
+            assert ops.device_error() == 0x4 and (n == -1).all() and copies[0].tolist() == [0, 0, 0, 0]
+            assert torch.equal(before, t.pool.state) and all(torch.equal(a, b) for a, b in zip(old, t.tables))
+        assert _clean(t.pool)
