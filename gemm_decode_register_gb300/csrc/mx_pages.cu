@@ -12,6 +12,9 @@
 // A page whose users stay as many needs no tally: neighbouring sequences that hold
 // the same page are counted together, so the prompt of a request's beams, or
 // a sequence that only grows, touches no counts.
+// Tables and the pool are read more than once.  Whoever writes them meanwhile (calls
+// on one pool must not overlap) gets wrong pages, but no access out of bounds:
+// a page is used as an index only where it is looked at again.
 //
 // These kernels write lengths and tables, which other kernels of the library
 // read before they wait for their predecessor; so they do not let their
@@ -141,7 +144,6 @@ struct Slot {
 // What the CTAs of the cluster tell each other, in each one's shared memory.
 struct RemapShared {
     int fault, late;     // faults of the tally, of the decision (a word of its own: another CTA may be ahead)
-    int gained;          // pages freed, less those handed out
     int handed, copies;  // pages handed out, copies
     int smax[32];
     unsigned long long scan[32];
@@ -158,13 +160,6 @@ __device__ __forceinline__ void all_ctas_or(const void *word, int bits)
 // (the plan, of two words a slot, on an even word)
 static __host__ __device__ size_t remap_plan_at(int S_in, int S_out) { return (4 * (size_t)S_in + 4 * (size_t)S_out + 1) / 2 * 2; }
 static size_t remap_smem(int S_in, int S_out) { return sizeof(int) * (remap_plan_at(S_in, S_out) + 2 * (size_t)S_out); }
-
-__device__ __forceinline__ void all_ctas_add(const void *word, int n)
-{
-    const uint32_t here = smem_u32(word);
-    for (uint32_t r = 0; r < POOL_CLUSTER; ++r)
-        asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(map_to_cta(here, r)), "r"(n) : "memory");
-}
 
 // The first thing a step needs is every sequence's length and every slot's
 // parent: they are read once, into each CTA's shared memory.  A phase is then one
@@ -186,7 +181,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
     const int rank = (int)cluster_ctarank();
     const int gw = warp * POOL_CLUSTER + rank, nw = POOL_WARPS * POOL_CLUSTER;
     const int ps = c.page_size, P = c.pool.num_pages;
-    if (tid == 0) sh.fault = sh.late = sh.gained = 0;
+    if (tid == 0) sh.fault = sh.late = 0;
     pdl_wait();
     cluster_sync_all();  // (before a CTA reports to the others)
 
@@ -326,7 +321,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
     // without a user.  Not where a fault is known: lengths may not fit the tables.
     fault = *(volatile int *)&sh.fault;
     if (fault == 0) {
-        int bad = 0, gained = 0;
+        int bad = 0;
         if (rank == 0) {
             constexpr int PER = (POOL_MAX_SLOTS + POOL_THREADS - 1) / POOL_THREADS;
             constexpr unsigned long long COPY = 1ull << 40;  // pages below, copies above
@@ -365,7 +360,6 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
                 const unsigned long long n = total & (COPY - 1);
                 if (count < 0 || count > P) bad |= DEVERR_BAD_PAGE;
                 else if (n > (unsigned long long)count) bad |= DEVERR_NO_PAGE;
-                gained = -(int)n;
                 sh.handed = (int)n;
                 sh.copies = (int)(total / COPY);
             }
@@ -377,25 +371,18 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
             }
         }
         old_entries([&](int page, int d, bool) {
-            if (d >= 0) return;
+            if (d >= 0 || (unsigned)page >= (unsigned)P) return;
             const PageTally t = tally_at(w.tally, page);
             const int left = __ldcg(c.pool.refs + page) + t.users;
             if (left < 0) bad |= DEVERR_BAD_PAGE;  // fewer references than entries
-            if (left == 0 && t.writer == 0) {
-                const uint32_t bit = 1u << (page & 31);
-                gained += (atomicOr(w.freed + (page >> 5), bit) & bit) == 0u;
-            }
+            if (left == 0 && t.writer == 0) atomicOr(w.freed + (page >> 5), 1u << (page & 31));
         });
         if (bad) all_ctas_or(&sh.late, bad);
-        gained = __reduce_add_sync(0xFFFFFFFFu, gained);
-        if (lane == 0 && gained != 0) all_ctas_add(&sh.gained, gained);
     }
     cluster_phase();
 
     // ---- all or nothing
     fault |= *(volatile int *)&sh.late;
-    // (more free pages than there are: the stack said so of pages in use)
-    if (fault == 0 && count + *(volatile int *)&sh.gained > P) fault = DEVERR_BAD_PAGE;
     if (fault) {
         old_entries([&](int page, int, bool) {
             if ((unsigned)page >= (unsigned)P) return;
@@ -426,8 +413,9 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
 #pragma unroll
         for (int i = 0; i < RUN; ++i) {
             const int j = j0 + 32 * i + lane;
+            const int place = count - 1 - first - (j - start);
             if (j < start) page[i] = __ldcg(from + j);
-            else if (j < end) page[i] = __ldcg(c.pool.free_pages + (count - 1 - first - (j - start)));
+            else if (j < end) page[i] = (unsigned)place < (unsigned)P ? __ldcg(c.pool.free_pages + place) : -1;
         }
 #pragma unroll
         for (int i = 0; i < RUN; ++i) {
@@ -435,14 +423,14 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
             if (j >= end) continue;
             to[j] = page[i];
             if (j < start) continue;
-            c.pool.refs[page[i]] = 1;
+            if ((unsigned)page[i] < (unsigned)P) c.pool.refs[page[i]] = 1;
             if (j == start && copy != 0)
                 reinterpret_cast<int4 *>(c.copies)[copy] = make_int4(__ldcg(from + j), page[i], n.kept % ps, 0);
         }
         if (j0 == 0 && lane == 0) c.kv_len_out[s] = n.tokens;
     }
     old_entries([&](int page, int d, bool special) {
-        if (d == 0 && !special) return;
+        if ((d == 0 && !special) || (unsigned)page >= (unsigned)P) return;
         // whoever comes first takes the tally
         const int refs = __ldcg(c.pool.refs + page);
         const unsigned long long v = atomicExch(reinterpret_cast<unsigned long long *>(w.tally + page), 0ull);
@@ -463,11 +451,14 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_remap_kernel(const __grid_
         unsigned long long total;
         int at = top + (int)block_prefix((unsigned)__popc(bits), sh.scan, total);
         if (bits) w.freed[i] = 0u;
-        for (; bits; bits &= bits - 1) c.pool.free_pages[at++] = 32 * i + __ffs((int)bits) - 1;
+        for (; bits && at < P; bits &= bits - 1) c.pool.free_pages[at++] = 32 * i + __ffs((int)bits) - 1;
         top += (int)total;
     }
     if (tid == 0) {
-        *c.pool.count = top;
+        // (the stack said so of pages in use.  Found here and not before anything is written, which
+        // would take a round trip to L2 more, 1 us of a step's 15)
+        if (top > P) set_device_error(a.err, DEVERR_BAD_PAGE);
+        *c.pool.count = min(top, P);
         reinterpret_cast<int4 *>(c.copies)[0] = make_int4(sh.copies, 0, 0, 0);
     }
 }
@@ -596,7 +587,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_compact_kernel(const __gri
     if (fault) return give_up(fault);
     int all_holes, all_movers;
     int hole = totals(0, all_holes) + (int)(uint32_t)at, mover = totals(1, all_movers) + (int)(at >> 32);
-    const int n = min(all_holes, all_movers);
+    const int n = min(min(all_holes, all_movers), P / 2);  // (P / 2: what the list holds)
     for (int p0 = lo; p0 < hi; p0 += 32) {
         const int k = p0 + lane < hi ? kind(p0 + lane) : 0;
         const unsigned h = __ballot_sync(0xFFFFFFFFu, k == 1), m = __ballot_sync(0xFFFFFFFFu, k == 2);
@@ -612,6 +603,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_compact_kernel(const __gri
     for (int i = gw * 32 + lane; i < n; i += nw * 32) {
         int4 *row = reinterpret_cast<int4 *>(a.copies) + 1 + i;
         const int2 v = __ldcg(reinterpret_cast<const int2 *>(row));
+        if ((unsigned)v.x >= (unsigned)P || (unsigned)v.y >= (unsigned)P) continue;
         *row = make_int4(v.x, v.y, ps, 0);
         w.tally[v.x].writer = v.y + 1;
         a.pool.refs[v.y] = __ldcg(a.pool.refs + v.x);
@@ -619,7 +611,7 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_compact_kernel(const __gri
     }
     cluster_phase();
     entries([&](int32_t *e, int page) {
-        const int to = tally_at(w.tally, page).writer;
+        const int to = (unsigned)page < (unsigned)P ? tally_at(w.tally, page).writer : 0;
         if (to > 0) *e = to - 1;
     });
     unsigned empty = 0;
@@ -636,7 +628,8 @@ __global__ void __launch_bounds__(POOL_THREADS, 1) kv_compact_kernel(const __gri
         const int p = p0 + lane;
         const bool e = p < hi && __ldcg(a.pool.refs + p) == 0;
         const unsigned m = __ballot_sync(0xFFFFFFFFu, e);
-        if (e) a.pool.free_pages[all - 1 - (below + __popc(m & ((1u << lane) - 1u)))] = p;
+        const int place = all - 1 - (below + __popc(m & ((1u << lane) - 1u)));
+        if (e && (unsigned)place < (unsigned)P) a.pool.free_pages[place] = p;
         if (p < hi) w.tally[p] = PageTally{0, 0};
         below += __popc(m);
     }

@@ -452,9 +452,10 @@ size_t mx_page_pool_work_size(int num_pages);
  * All or nothing: if the free pages do not suffice (MX_DEVERR_NO_PAGE), a
  * parent is not below S_in (MX_DEVERR_BAD_SLOT), or a length exceeds its
  * table row, a page number the pool, a page would lose more references than
- * it has, one that is to be handed out has any, or there would be more free
- * pages than pages (MX_DEVERR_BAD_PAGE), the pool and table_out stay as they
- * were, every kv_len_out is -1 and n is 0.
+ * it has, or one that is to be handed out has any (MX_DEVERR_BAD_PAGE), the
+ * pool and table_out stay as they were, every kv_len_out is -1 and n is 0.
+ * (Only a count so large that released pages do not fit the stack is found at
+ * the end of the step: those are lost to the pool, with MX_DEVERR_BAD_PAGE.)
  * Entries of table_out past a sequence's pages are left alone.  table_out and
  * kv_len_out must not overlap table_in and kv_len_in.  S_in, S_out <= 4096.
  * Reads nothing before the preceding kernel has ended, and lets no kernel

@@ -63,25 +63,24 @@ def test_pages_of_fewer_references_than_entries_are_not_covered(P, S, width, ps)
 
 
 @pytest.mark.parametrize("P,S,width,ps", [(40, 6, 12, 4), (70000, 90, 300, 2)])
-def test_more_free_pages_than_pages(P, S, width, ps):
-    """A count of free pages that leaves no room on the stack for those that a step releases."""
+@pytest.mark.parametrize("room", [2, 1, 0])
+def test_more_free_pages_than_pages(P, S, width, ps, room):
+    """A count of free pages that leaves less room on the stack than the three pages that a step releases: nothing is written
+    behind it."""
     torch = need_gpu()
     from gemm_decode_register_gb300 import ops
 
-    t = Session(torch, P, S, width, ps)
-    assert t.step([-1] * S, None, [1 + (5 * s) % (2 * ps) for s in range(S)])
-    count, used = int(t.pool.count), sum(len(r) for r in t.rows)
-    assert count + used == P and used > S
-    ends = [s if s != 1 else -1 for s in range(S)]  # (sequence 1 ends, the others grow by nothing)
-    released = len(t.rows[1])
-    for free, fits in ((P - released + 1, False), (P, False), (P - released, True)):
-        t.pool.count.fill_(free)
-        before = t.pool.state.clone()
-        old = [x.clone() for x in (t.tables[0], t.tables[1])]
-        n, copies = ops.kv_remap(t.pool, ps, t.tables[0], t.kv_len, _i32(torch, ends), t.tables[1], 0)
-        if fits:
-            assert ops.device_error() == 0 and int(t.pool.count) == P
-        else:
-            assert ops.device_error() == 0x4 and (n == -1).all() and copies[0].tolist() == [0, 0, 0, 0]
-            assert torch.equal(before, t.pool.state) and all(torch.equal(a, b) for a, b in zip(old, t.tables))
-        assert _clean(t.pool)
+    whole = torch.full((4 + 2 * P + 64,), -77, dtype=torch.int32, device="cuda")  # (the pool's numbers, and what lies behind)
+    state = whole[:4 + 2 * P]
+    state.copy_(ops.PagePool(P).state)
+    pool, tables = ops.PagePool(P, state=state), [torch.zeros((S, width), dtype=torch.int32, device="cuda") for _ in range(2)]
+    none, add = _i32(torch, [-1] * S), _i32(torch, [3 * ps if s == 1 else 1 for s in range(S)])
+    n, _ = ops.kv_remap(pool, ps, tables[1], torch.zeros_like(none), none, tables[0], add)
+    assert ops.device_error() == 0 and n.tolist() == add.tolist()
+    freed = sorted(tables[0][1, :3].tolist())
+    pool.count.fill_(P - room)
+    ends = _i32(torch, [s if s != 1 else -1 for s in range(S)])
+    n, _ = ops.kv_remap(pool, ps, tables[0], n, ends, tables[1], 0)
+    assert ops.device_error() == 0x4 and int(pool.count) == P
+    assert pool.free_pages[P - room:].tolist() == freed[:room] and (whole[4 + 2 * P:] == -77).all() and _clean(pool)
+    assert (pool.refs[torch.tensor(freed, device="cuda")] == 0).all()
